@@ -324,14 +324,16 @@ def _norm_rope_grad(dy, x, w, r, cos, sin, c):
 
 
 def _quantise(x, c):
-    """Codes and scales of x[..., d] in float32: each group divided by its largest magnitude."""
+    """Codes and scales of x[..., d] in float32: each group divided by its largest magnitude.
+    In 64 bits, where values next to a border between two codes keep their side."""
     q = QMAX[c["kind"]]
     groups = x.unflatten(-1, (-1, c["group"]))
     m = groups.abs().amax(-1, keepdim=True)
-    u = (groups * q / torch.where(m == 0, 1.0, m)).flatten(-2)
+    u = (groups.double() * q / torch.where(m == 0, 1.0, m)).flatten(-2)
     scales = (m / q)[..., 0]
     if c["kind"] == "e4m3":
-        return u.to(torch.float8_e4m3fn), scales
+        step = torch.ldexp(torch.ones_like(u), torch.frexp(u.abs().clamp_min(2.0 ** -6)).exponent - 4)
+        return ((u / step).round() * step).to(torch.float8_e4m3fn), scales
     codes = u.round().to(torch.int8)
     if c["kind"] == "int8":
         return codes, scales
