@@ -1,7 +1,8 @@
 /*
  * libnorm.h -- C ABI of libnorm: forward and backward passes of LayerNorm,
- * RMSNorm and BatchNorm (with fused residual add and activation) on one NVIDIA
- * GB300 GPU (sm_103a), computed by hand-written CUDA kernels.
+ * RMSNorm and BatchNorm (with fused residual add and activation), and the norms
+ * and position rotation of attention heads with a quantised key/value cache, on
+ * one NVIDIA GB300 GPU (sm_103a), computed by hand-written CUDA kernels.
  *
  * Sources for what each call computes (web articles on the attorch
  * normalization kernels):
@@ -107,7 +108,8 @@ typedef enum nrm_act {
 typedef enum nrm_op {
     NRM_OP_LAYERNORM_BWD = 1,
     NRM_OP_RMSNORM_BWD = 2,
-    NRM_OP_LAYERNORM_CF_BWD = 3 /* rows: n*l (unused), cols: c */
+    NRM_OP_LAYERNORM_CF_BWD = 3, /* rows: n*l (unused), cols: c */
+    NRM_OP_QK_NORM_BWD = 4       /* rows: tokens (unused), cols: d */
 } nrm_op;
 
 /* ------------------------------------------------------------------------ */
@@ -395,6 +397,187 @@ NRM_API nrm_status nrm_act_dropout_bwd(const void *dy, const void *x, void *dx, 
                                nrm_dtype dt, nrm_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Attention heads: norms with position rotation, quantised key/value cache  */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The operators of this section work on the heads of a projection.  The web
+ * articles have no counterpart; what each computes is stated here in full.
+ *
+ * Views.  q, k and v are [tokens, heads, d] views: element (t, h, i) lies at
+ * data + t*token_stride + h*head_stride + i (strides in elements), so the
+ * slices of one fused projection [tokens, (hq + 2*hk)*d] are taken as they
+ * are.  Strides are >= 0 and < 2^40.  Different (t, h) of an output must not
+ * overlap; an output may be its own input in place (same data and strides),
+ * where the entry point says so; any other overlap of outputs with inputs or
+ * one another is not supported.  1 <= d <= 256; tokens >= 0 (0 is a no-op);
+ * heads >= 1.
+ * 16-byte aligned pointers, strides that are multiples of 16 bytes, and d and
+ * rot that are multiples of 32 bytes of elements take the 128-bit path; the
+ * rest takes narrower accesses.
+ */
+typedef struct nrm_heads {
+    void *data;
+    int64_t heads;
+    int64_t token_stride; /* elements */
+    int64_t head_stride;  /* elements */
+} nrm_heads;
+
+typedef enum nrm_pairs {
+    NRM_PAIRS_HALF = 0,    /* pair p is elements (p, p + rot/2) */
+    NRM_PAIRS_ADJACENT = 1 /* pair p is elements (2p, 2p + 1) */
+} nrm_pairs;
+
+/*
+ * Rotation R by position, over one to four axes (a sequence; rows and columns
+ * of an image; time, height and width of a video).  Pair p < rot/2 of token t
+ * turns by the angle
+ *   a(t, p) = pos[axis[p]*pos_stride + t] * inv_freq[p]   (radians)
+ *   (u, v) -> (u*cos a - v*sin a, v*cos a + u*sin a)
+ * and elements i >= rot pass unchanged.  The product is taken modulo one turn
+ * in 64-bit fixed point, so far positions keep their angles: for frequencies up
+ * to 2 pi it is off by less than |pos| * 2^-52 + 2^-32 turns.
+ * pos: device int64 [axes][pos_stride >= tokens], any values.  inv_freq:
+ * device float32 [rot/2], finite.  axis: HOST bytes [rot/2], each below axes,
+ * read during the call; NULL when axes == 1.  rot even, 0 <= rot <= d; with
+ * rot == 0 nothing turns, and pos and inv_freq may be NULL.
+ */
+typedef struct nrm_rope {
+    const int64_t *pos;
+    int64_t pos_stride;
+    const float *inv_freq;
+    const uint8_t *axis;
+    int32_t rot;
+    int32_t axes;
+    nrm_pairs pairs;
+} nrm_rope;
+
+/*
+ * nrm_qk_norm_rope_fwd -- RMSNorm of every head of q and k, then the rotation,
+ * in one pass: for each row x (a token's head)
+ *   r = (sum_i x_i^2/d + eps)^(-1/2);  y = R(x*r*w)
+ * q, k: inputs in dt; k may be NULL (then k_out, wk, rstd_k are ignored).
+ * wq, wk: [d] in dt, one weight for all heads, each may be NULL (1).
+ * q_out, k_out: views with the heads of q and k; each may be its input in
+ * place.  rstd_q [tokens, hq], rstd_k [tokens, hk]: float32, dense, receive r;
+ * each may be NULL.  eps > 0.
+ */
+NRM_API nrm_status nrm_qk_norm_rope_fwd(const nrm_heads *q, const nrm_heads *k, const void *wq,
+                                const void *wk, const nrm_rope *rope, const nrm_heads *q_out,
+                                const nrm_heads *k_out, float *rstd_q, float *rstd_k,
+                                int64_t tokens, int64_t d, float eps, nrm_dtype dt,
+                                nrm_stream_t stream);
+
+/*
+ * nrm_qk_norm_rope_bwd -- its backward.  With g' = R^T(dy), g = g'*w and
+ * s = sum_i g_i*x_i over the row:
+ *   dx = r*g - x*r^3*s/d;  dw_i = sum over tokens and heads of g'_i*x_i*r
+ * dq_out, dk_out: the gradients of q_out, k_out; q, k, wq, wk, rope: those of
+ * the forward; rstd_q, rstd_k: as it wrote them.  dq, dk: output views (not
+ * in place).  dwq, dwk: [d] in dt, each may be NULL.  k (with dk_out, dk) may
+ * be NULL.  workspace: nrm_workspace_bytes(NRM_OP_QK_NORM_BWD, tokens, d, dt)
+ * bytes, 16-byte aligned, clobbered; may be NULL when dwq and dwk are NULL.
+ * With tokens == 0, dwq and dwk are set to 0.
+ */
+NRM_API nrm_status nrm_qk_norm_rope_bwd(const nrm_heads *dq_out, const nrm_heads *dk_out,
+                                const nrm_heads *q, const nrm_heads *k, const void *wq,
+                                const void *wk, const float *rstd_q, const float *rstd_k,
+                                const nrm_rope *rope, const nrm_heads *dq, const nrm_heads *dk,
+                                void *dwq, void *dwk, int64_t tokens, int64_t d, nrm_dtype dt,
+                                void *workspace, size_t workspace_bytes, nrm_stream_t stream);
+
+/*
+ * nrm_rope_fwd -- the rotation alone: q_out = R(q), k_out = R(k); in place is
+ * allowed, k may be NULL.  nrm_rope_bwd -- its backward, the turn the other
+ * way: dq = R^T(dq_out), dk = R^T(dk_out); the same rules.
+ */
+NRM_API nrm_status nrm_rope_fwd(const nrm_heads *q, const nrm_heads *k, const nrm_rope *rope,
+                        const nrm_heads *q_out, const nrm_heads *k_out, int64_t tokens, int64_t d,
+                        nrm_dtype dt, nrm_stream_t stream);
+NRM_API nrm_status nrm_rope_bwd(const nrm_heads *dq_out, const nrm_heads *dk_out, const nrm_rope *rope,
+                        const nrm_heads *dq, const nrm_heads *dk, int64_t tokens, int64_t d,
+                        nrm_dtype dt, nrm_stream_t stream);
+
+/* Stored forms of a cache, with the largest magnitude q of each. */
+typedef enum nrm_cache_kind {
+    NRM_CACHE_E4M3 = 0, /* one byte, 8-bit float with 4 exponent and 3 mantissa bits; q = 448 */
+    NRM_CACHE_INT8 = 1, /* one byte, -127..127; q = 127 */
+    NRM_CACHE_INT4 = 2  /* two elements to a byte, the even one in the low half, -7..7; q = 7 */
+} nrm_cache_kind;
+
+/*
+ * A paged, quantised key/value cache: pages * page_size slots of `heads` rows
+ * of d elements.  Each row is stored in groups of `group` consecutive elements
+ * (group divides d; even for INT4, whose d is even too).  A group is divided
+ * by its largest magnitude m, rounded to the form and kept with its scale:
+ *   scale = m/q;  code_i = round(x_i*q/m), ties to even;  value_i = code_i*scale
+ * A group whose m is below 2^-100 is stored as zeros (scale 0); one that holds
+ * a NaN or an infinity has the scale NaN and reads back as NaN.
+ * Slot s, head h starts at byte (s / page_size)*page_stride +
+ * (s % page_size)*slot_stride + h*head_stride of the codes, and its d/group
+ * scales at the like float of the scales: [pages, page, heads, d] and
+ * [pages, heads, page, d] are both such layouts.  k and v share the strides;
+ * either pair of pointers may be NULL in calls that do not touch it.
+ */
+typedef struct nrm_kv_cache {
+    void *k_codes;
+    float *k_scales;
+    void *v_codes;
+    float *v_scales;
+    int64_t pages;
+    int64_t page_size;
+    int64_t heads;
+    int64_t d;
+    int64_t group;
+    int64_t page_stride;       /* bytes */
+    int64_t slot_stride;       /* bytes */
+    int64_t head_stride;       /* bytes */
+    int64_t scale_page_stride; /* floats */
+    int64_t scale_slot_stride; /* floats */
+    int64_t scale_head_stride; /* floats */
+    nrm_cache_kind kind;
+} nrm_kv_cache;
+
+/*
+ * nrm_kv_cache_write -- quantises row (t, h) of k and v into slot slots[t] of
+ * the cache.  k, v: [tokens, cache->heads, cache->d] views in dt; either may
+ * be NULL.  slots: device int64 [tokens].  A slot of -1 skips its token (the
+ * padding of a batch); any other slot outside the cache is skipped too and
+ * reported by the next nrm_sync_status as NRM_ERR_INVALID_ARG.  The slots of
+ * one call must differ from one another, -1 apart: where two tokens name one
+ * slot, its rows may mix both (no other row is affected).
+ */
+NRM_API nrm_status nrm_kv_cache_write(const nrm_heads *k, const nrm_heads *v, const nrm_kv_cache *cache,
+                              const int64_t *slots, int64_t tokens, nrm_dtype dt,
+                              nrm_stream_t stream);
+
+/*
+ * nrm_kv_cache_read -- the values of slot slots[t] as row (t, h) of k_out and
+ * v_out (value_i above, in float32, rounded to dt); either view may be NULL.
+ * Slots may repeat.  The rows of a slot of -1 are left as they were, and so
+ * are those of a slot outside the cache, which is reported as above.
+ */
+NRM_API nrm_status nrm_kv_cache_read(const nrm_kv_cache *cache, const int64_t *slots,
+                             const nrm_heads *k_out, const nrm_heads *v_out, int64_t tokens,
+                             nrm_dtype dt, nrm_stream_t stream);
+
+/*
+ * nrm_qk_norm_rope_cache -- the step of a served model in one launch:
+ * nrm_qk_norm_rope_fwd of q and k (nrm_rope_fwd when norm == 0; wq, wk and eps
+ * are then ignored), and nrm_kv_cache_write of the resulting key, rounded to
+ * dt, and of v.  q_out: as there; may be q in place.  k_out: the key itself,
+ * or NULL when only the cache is wanted; may be k in place.  v: [tokens, hk,
+ * d]; cache->heads == hk.  A token whose slot is -1 gets q_out and k_out and
+ * leaves the cache alone.
+ */
+NRM_API nrm_status nrm_qk_norm_rope_cache(const nrm_heads *q, const nrm_heads *k, const nrm_heads *v,
+                                  const void *wq, const void *wk, const nrm_rope *rope,
+                                  const nrm_heads *q_out, const nrm_heads *k_out,
+                                  const nrm_kv_cache *cache, const int64_t *slots, int64_t tokens,
+                                  int64_t d, float eps, int norm, nrm_dtype dt,
+                                  nrm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Helpers                                                                   */
 /* ------------------------------------------------------------------------ */
 
@@ -412,8 +595,9 @@ NRM_API size_t nrm_batchnorm_workspace_bytes(int64_t n, int64_t c, int64_t l, nr
 NRM_API int64_t nrm_act_mask_words(int64_t n, int64_t c, int64_t l);
 
 /* Synchronises `stream`, then returns NRM_ERR_TIMEOUT if a kernel of this
- * library on the current device reported a timed-out wait since the last call
- * (and clears that report), NRM_ERR_CUDA if the stream reported an error, and
+ * library on the current device reported a timed-out wait since the last call,
+ * else NRM_ERR_INVALID_ARG if one met a cache slot outside its cache (and
+ * clears these reports), NRM_ERR_CUDA if the stream reported an error, and
  * NRM_OK otherwise. */
 NRM_API nrm_status nrm_sync_status(nrm_stream_t stream);
 

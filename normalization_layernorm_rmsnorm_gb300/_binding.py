@@ -20,7 +20,9 @@ NRM_F32, NRM_F16, NRM_BF16 = 0, 1, 2
 NRM_ACT_NONE, NRM_ACT_RELU, NRM_ACT_GELU, NRM_ACT_SILU, NRM_ACT_MISH = 0, 1, 2, 3, 4
 NRM_ACT_LEAKY_RELU, NRM_ACT_ELU, NRM_ACT_SIGMOID, NRM_ACT_CELU, NRM_ACT_SELU = 5, 6, 7, 8, 9
 NRM_ACT_RELU6, NRM_ACT_HARDTANH = 10, 11
-NRM_OP_LAYERNORM_BWD, NRM_OP_RMSNORM_BWD, NRM_OP_LAYERNORM_CF_BWD = 1, 2, 3
+NRM_OP_LAYERNORM_BWD, NRM_OP_RMSNORM_BWD, NRM_OP_LAYERNORM_CF_BWD, NRM_OP_QK_NORM_BWD = 1, 2, 3, 4
+NRM_PAIRS_HALF, NRM_PAIRS_ADJACENT = 0, 1
+NRM_CACHE_E4M3, NRM_CACHE_INT8, NRM_CACHE_INT4 = 0, 1, 2
 
 ACTS = {"none": NRM_ACT_NONE, "relu": NRM_ACT_RELU, "gelu": NRM_ACT_GELU, "silu": NRM_ACT_SILU,
         "mish": NRM_ACT_MISH, "leaky_relu": NRM_ACT_LEAKY_RELU, "elu": NRM_ACT_ELU,
@@ -33,6 +35,8 @@ EXPORTS = ("nrm_layernorm_fwd", "nrm_layernorm_bwd", "nrm_layernorm_bwd_noalloc"
            "nrm_rmsnorm_fwd", "nrm_rmsnorm_bwd", "nrm_layernorm_fwd_ex", "nrm_layernorm_bwd_ex",
            "nrm_rmsnorm_fwd_ex", "nrm_rmsnorm_bwd_ex",
            "nrm_batchnorm_fwd", "nrm_batchnorm_bwd", "nrm_act_dropout_fwd", "nrm_act_dropout_bwd",
+           "nrm_qk_norm_rope_fwd", "nrm_qk_norm_rope_bwd", "nrm_rope_fwd", "nrm_rope_bwd",
+           "nrm_kv_cache_write", "nrm_kv_cache_read", "nrm_qk_norm_rope_cache",
            "nrm_workspace_bytes",
            "nrm_batchnorm_workspace_bytes",
            "nrm_act_mask_words", "nrm_sync_status", "nrm_status_str",
@@ -50,6 +54,24 @@ _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _I = ctypes.c_int
 _lib = None
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("heads", _I64), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("pos", _P), ("pos_stride", _I64), ("inv_freq", _P), ("axis", ctypes.c_char_p), ("rot", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("pairs", _I)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P)] + [
+        (n, _I64) for n in ("pages", "page_size", "heads", "d", "group", "page_stride", "slot_stride", "head_stride",
+                            "scale_page_stride", "scale_slot_stride", "scale_head_stride")] + [("kind", _I)]
+
+
+_HP, _RP, _CP = (ctypes.POINTER(t) for t in (_Heads, _Rope, _Cache))
 
 
 def load(path: str | None = None):
@@ -81,6 +103,14 @@ def load(path: str | None = None):
                               _I, _F, _I, _P, ctypes.c_size_t, _P],
         "nrm_act_dropout_fwd": [_P, _P, _I64, _I, _F, _F, ctypes.c_uint32, _I, _P],
         "nrm_act_dropout_bwd": [_P, _P, _P, _I64, _I, _F, _F, ctypes.c_uint32, _I, _P],
+        "nrm_qk_norm_rope_fwd": [_HP, _HP, _P, _P, _RP, _HP, _HP, _P, _P, _I64, _I64, _F, _I, _P],
+        "nrm_qk_norm_rope_bwd": [_HP, _HP, _HP, _HP, _P, _P, _P, _P, _RP, _HP, _HP, _P, _P, _I64, _I64, _I, _P,
+                                 ctypes.c_size_t, _P],
+        "nrm_rope_fwd": [_HP, _HP, _RP, _HP, _HP, _I64, _I64, _I, _P],
+        "nrm_rope_bwd": [_HP, _HP, _RP, _HP, _HP, _I64, _I64, _I, _P],
+        "nrm_kv_cache_write": [_HP, _HP, _CP, _P, _I64, _I, _P],
+        "nrm_kv_cache_read": [_CP, _P, _HP, _HP, _I64, _I, _P],
+        "nrm_qk_norm_rope_cache": [_HP, _HP, _HP, _P, _P, _RP, _HP, _HP, _CP, _P, _I64, _I64, _F, _I, _I, _P],
         "nrm_workspace_bytes": [_I, _I64, _I64, _I],
         "nrm_batchnorm_workspace_bytes": [_I64, _I64, _I64, _I],
         "nrm_act_mask_words": [_I64, _I64, _I64],
@@ -308,6 +338,291 @@ def nrm_act_dropout_bwd(dy, x, dx, act, drop_p, seed, stream=None, act_param=0.0
                                       float(drop_p),
                                       int(seed) & 0xFFFFFFFF, _dtype_code(x), _stream(stream)),
            "nrm_act_dropout_bwd")
+
+
+# ---------------------------------------------------------------------------
+# attention heads: norms with position rotation, quantised key/value cache
+# ---------------------------------------------------------------------------
+# Views are [tokens, heads, d] or [batch, tokens, heads, d] tensors with
+# contiguous rows and any other strides that one token stride describes.
+
+_PAIRS = {"half": NRM_PAIRS_HALF, "pair": NRM_PAIRS_ADJACENT}
+
+
+def _heads_view(t, name, like=None, dtype=None):
+    """(C view, tokens, d) of a tensor of heads; `like`: a tensor whose shape it must have."""
+    shape, st = t.shape, t.stride()
+    if len(shape) == 4:
+        b, n, h, d = shape
+        ts = st[1] if n > 1 else st[0]
+        if b > 1 and n > 1 and st[0] != n * st[1]:
+            raise ValueError(f"{name}: batch and token dimensions must have one stride (strides {tuple(st)})")
+        tokens = b * n
+    elif len(shape) == 3:
+        tokens, h, d = shape
+        ts = st[0]
+    else:
+        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
+    if d > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if like is not None and shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {tuple(like.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    return _Heads(t.data_ptr(), h, ts, st[-2]), tokens, d
+
+
+def _dense(t, name, shape, dtype):
+    """data_ptr of a contiguous tensor of the given shape and dtype, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {shape} tensor, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _stat_ptr(t, name, tokens, heads):
+    """data_ptr of the saved statistics of tokens*heads rows, or None."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} is {t.dtype}, expected torch.float32")
+    if t.numel() != tokens * heads or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {tokens * heads} values, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on_device(*tensors):
+    """Every tensor lies on the current CUDA device, where the call launches."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"tensors must be on the current CUDA device ({dev}), got {t.device}")
+
+
+def _rope(pos, inv_freq, axis, pairs, tokens):
+    """The C description of a rotation, or None without one."""
+    import torch
+    if inv_freq is None:
+        return None
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous float32 vector")
+    n = inv_freq.shape[0]
+    if pos is None or pos.dtype != torch.int64:
+        raise TypeError("pos must be an int64 tensor")
+    if not pos.is_contiguous():
+        raise ValueError("pos must be contiguous")
+    axes = 1 if axis is None else pos.shape[0]
+    if pos.numel() != axes * tokens:
+        raise ValueError(f"pos has {pos.numel()} values, expected {axes} axes of {tokens} tokens")
+    if axis is not None:
+        axis = bytes(axis)
+        if len(axis) != n:
+            raise ValueError(f"axis has {len(axis)} entries, expected one for each of {n} pairs")
+    if pairs not in _PAIRS:
+        raise ValueError(f"pairs must be 'half' or 'pair', got {pairs!r}")
+    return _Rope(pos.data_ptr(), tokens, inv_freq.data_ptr(), axis, 2 * n, axes, _PAIRS[pairs])
+
+
+def rope_axis(sections, interleaved=False) -> bytes:
+    """The axis of each pair for nrm_*rope*: sections[a] pairs for axis a, one
+    section after another, or taken in turn while they last (interleaved)."""
+    if not interleaved:
+        return b"".join(bytes([a]) * n for a, n in enumerate(sections))
+    left, out = list(sections), bytearray()
+    while any(left):
+        for a, n in enumerate(left):
+            if n > 0:
+                out.append(a)
+                left[a] -= 1
+    return bytes(out)
+
+
+def qk_norm_workspace(q):
+    """A device workspace for nrm_qk_norm_rope_bwd on heads like q's."""
+    import torch
+    d = q.shape[-1]
+    nbytes = nrm_workspace_bytes(NRM_OP_QK_NORM_BWD, q.numel() // max(d, 1), d, _dtype_code(q))
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+
+
+def nrm_qk_norm_rope_fwd(q, k, wq, wk, pos, inv_freq, q_out, k_out, rstd_q, rstd_k, eps, stream=None, axis=None,
+                         pairs="half"):
+    """RMSNorm of every head of q and k and the rotation by position, in one pass.
+
+    q, k: [tokens, heads, d] views (k may be None); q_out, k_out may be q, k.
+    pos: int64 [tokens], or [axes, tokens] with `axis`, the axis of each pair
+    (rope_axis).  inv_freq: float32 [rot / 2] (None: no rotation).  pairs:
+    "half" turns elements (p, p + rot/2) together, "pair" (2p, 2p + 1)."""
+    dt = q.dtype
+    vq, tokens, d = _heads_view(q, "q")
+    vqo, _, _ = _heads_view(q_out, "q_out", q, dt)
+    vk = vko = None
+    if k is not None:
+        vk, vko = _key_views(k, "k", k_out, "k_out", tokens, d, dt)
+    pwq, pwk = _dense(wq, "wq", (d,), dt), _dense(wk, "wk", (d,), dt)
+    pr = _stat_ptr(rstd_q, "rstd_q", tokens, vq.heads), None if vk is None else _stat_ptr(rstd_k, "rstd_k", tokens, vk.heads)
+    rope = _rope(pos, inv_freq, axis, pairs, tokens)
+    _on_device(q, k, q_out, None if k is None else k_out, wq, wk, pos if rope else None, inv_freq, rstd_q, rstd_k)
+    _check(load().nrm_qk_norm_rope_fwd(vq, vk, pwq, pwk, rope, vqo, vko, *pr, tokens, d, eps, _dtype_code(q),
+                                       _stream(stream)),
+           "nrm_qk_norm_rope_fwd")
+
+
+def _key_views(k, name, k2, name2, tokens, d, dt):
+    vk, nk, dk = _heads_view(k, name, None, dt)
+    if nk != tokens or dk != d:
+        raise ValueError(f"{name} is {nk} tokens of {dk}, the queries {tokens} of {d}")
+    if k2 is None:
+        raise ValueError(f"{name2} must not be None")
+    return vk, _heads_view(k2, name2, k, dt)[0]
+
+
+def nrm_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, rstd_q, rstd_k, pos, inv_freq, dq, dk, dwq, dwk, workspace,
+                         stream=None, axis=None, pairs="half"):
+    """Backward of nrm_qk_norm_rope_fwd: dq, dk (views like q, k) and the weights'
+    gradients dwq, dwk (each may be None; workspace from qk_norm_workspace)."""
+    dt = q.dtype
+    vq, tokens, d = _heads_view(q, "q")
+    vdqo, vdq = _heads_view(dq_out, "dq_out", q, dt)[0], _heads_view(dq, "dq", q, dt)[0]
+    vk = vdko = vdk = None
+    if k is not None:
+        vk, vdko = _key_views(k, "k", dk_out, "dk_out", tokens, d, dt)
+        vdk = _key_views(k, "k", dk, "dk", tokens, d, dt)[1]
+    ptrs = [_dense(t, n, (d,), dt) for t, n in ((wq, "wq"), (wk, "wk"), (dwq, "dwq"), (dwk, "dwk"))]
+    pr = _stat_ptr(rstd_q, "rstd_q", tokens, vq.heads), None if vk is None else _stat_ptr(rstd_k, "rstd_k", tokens, vk.heads)
+    rope = _rope(pos, inv_freq, axis, pairs, tokens)
+    _on_device(q, k, dq_out, dq, *(() if k is None else (dk_out, dk)), wq, wk, dwq, dwk, rstd_q, rstd_k,
+               pos if rope else None, inv_freq, workspace)
+    _check(load().nrm_qk_norm_rope_bwd(vdqo, vdko, vq, vk, ptrs[0], ptrs[1], *pr, rope, vdq, vdk, ptrs[2], ptrs[3],
+                                       tokens, d, _dtype_code(q), _ptr(workspace), _ws(workspace), _stream(stream)),
+           "nrm_qk_norm_rope_bwd")
+
+
+def _rope_call(name, q, k, pos, inv_freq, q_out, k_out, stream, axis, pairs, names):
+    dt = q.dtype
+    vq, tokens, d = _heads_view(q, names[0])
+    vqo = _heads_view(q_out, names[2], q, dt)[0]
+    vk = vko = None
+    if k is not None:
+        vk, vko = _key_views(k, names[1], k_out, names[3], tokens, d, dt)
+    rope = _rope(pos, inv_freq, axis, pairs, tokens)
+    _on_device(q, k, q_out, None if k is None else k_out, pos if rope else None, inv_freq)
+    _check(getattr(load(), name)(vq, vk, rope, vqo, vko, tokens, d, _dtype_code(q), _stream(stream)), name)
+
+
+def nrm_rope_fwd(q, k, pos, inv_freq, q_out, k_out, stream=None, axis=None, pairs="half"):
+    """The rotation by position alone (arguments as nrm_qk_norm_rope_fwd); q_out, k_out may be q, k."""
+    _rope_call("nrm_rope_fwd", q, k, pos, inv_freq, q_out, k_out, stream, axis, pairs, ("q", "k", "q_out", "k_out"))
+
+
+def nrm_rope_bwd(dq_out, dk_out, pos, inv_freq, dq, dk, stream=None, axis=None, pairs="half"):
+    """Backward of nrm_rope_fwd: the turn the other way; dq, dk may be dq_out, dk_out."""
+    _rope_call("nrm_rope_bwd", dq_out, dk_out, pos, inv_freq, dq, dk, stream, axis, pairs,
+               ("dq_out", "dk_out", "dq", "dk"))
+
+
+class KvCache:
+    """A paged, quantised key/value cache (kv_cache): the tensors and their C description."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "heads", "d", "slots", "_c")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        import torch
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        codes, scales = (k_codes, k_scales) if k_codes is not None else (v_codes, v_scales)
+        if codes is None or scales is None:
+            raise ValueError("a cache needs codes and scales")
+        kinds = {torch.float8_e4m3fn: NRM_CACHE_E4M3, torch.int8: NRM_CACHE_INT8, torch.uint8: NRM_CACHE_INT4}
+        if codes.dtype not in kinds:
+            raise TypeError(f"codes are float8_e4m3fn, int8, or uint8 (two 4-bit values), got {codes.dtype}")
+        kind = kinds[codes.dtype]
+        if codes.dim() != 4 or scales.dim() != 4 or scales.dtype != torch.float32:
+            raise ValueError("codes are [pages, page, heads, d], scales float32 [pages, page, heads, d / group]")
+        pages, page, heads, d = codes.shape
+        if kind == NRM_CACHE_INT4:
+            d *= 2
+        if scales.shape[:3] != codes.shape[:3] or scales.shape[3] < 1 or d % scales.shape[3]:
+            raise ValueError(f"scales {tuple(scales.shape)} do not go with codes {tuple(codes.shape)}")
+        for t, like in ((k_codes, codes), (v_codes, codes), (k_scales, scales), (v_scales, scales)):
+            if t is None:
+                continue
+            if t.shape != like.shape or t.dtype != like.dtype or t.stride() != like.stride():
+                raise ValueError("keys and values must have one shape, dtype and strides")
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError("the rows of codes and scales must be contiguous")
+        if (k_codes is None) != (k_scales is None) or (v_codes is None) != (v_scales is None):
+            raise ValueError("codes and scales come together")
+        _on_device(k_codes, k_scales, v_codes, v_scales)
+        self.heads, self.d, self.slots = heads, d, pages * page
+        self._c = _Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, page, heads, d,
+                         d // scales.shape[3], *codes.stride()[:3], *scales.stride()[:3], kind)
+
+
+def kv_cache(k_codes, k_scales, v_codes=None, v_scales=None) -> KvCache:
+    """Describes the caller's cache tensors for the cache calls.
+
+    codes: [pages, page, heads, d] float8_e4m3fn or int8, or uint8
+    [pages, page, heads, d / 2] (two 4-bit values a byte); scales: float32
+    [pages, page, heads, d / group]; any strides but contiguous rows, the same
+    for keys and values.  The handle keeps the tensors alive; make a new one
+    when they are replaced."""
+    return KvCache(k_codes, k_scales, v_codes, v_scales)
+
+
+def _cache_views(cache, slots, k, v, names):
+    import torch
+    ref = k if k is not None else v
+    if ref is None:
+        raise ValueError(f"{names[0]} and {names[1]} must not both be None")
+    views = [None if t is None else _heads_view(t, n, ref, ref.dtype) for t, n in zip((k, v), names)]
+    _, tokens, d = views[0] or views[1]
+    if d != cache.d or ref.shape[-2] != cache.heads:
+        raise ValueError(f"rows are {ref.shape[-2]} heads of {d}, the cache's {cache.heads} of {cache.d}")
+    if slots.dtype != torch.int64 or slots.numel() != tokens or not slots.is_contiguous():
+        raise ValueError(f"slots must be {tokens} contiguous int64 values")
+    _on_device(k, v, slots, cache.k_codes if cache.k_codes is not None else cache.v_codes)
+    return [None if w is None else w[0] for w in views], tokens, _dtype_code(ref)
+
+
+def nrm_kv_cache_write(k, v, cache, slots, stream=None):
+    """Quantises row t of k and v ([tokens, heads, d]; either may be None) into
+    slot slots[t] of the cache; -1 skips a token."""
+    (vk, vv), tokens, code = _cache_views(cache, slots, k, v, ("k", "v"))
+    _check(load().nrm_kv_cache_write(vk, vv, cache._c, slots.data_ptr(), tokens, code, _stream(stream)),
+           "nrm_kv_cache_write")
+
+
+def nrm_kv_cache_read(cache, slots, k_out, v_out, stream=None):
+    """The values of slot slots[t] as row t of k_out and v_out (either may be
+    None); rows of slot -1 are left as they were."""
+    (vk, vv), tokens, code = _cache_views(cache, slots, k_out, v_out, ("k_out", "v_out"))
+    _check(load().nrm_kv_cache_read(cache._c, slots.data_ptr(), vk, vv, tokens, code, _stream(stream)),
+           "nrm_kv_cache_read")
+
+
+def nrm_qk_norm_rope_cache(q, k, v, wq, wk, pos, inv_freq, q_out, k_out, cache, slots, eps, stream=None, axis=None,
+                           pairs="half", norm=True):
+    """The step of a served model in one launch: nrm_qk_norm_rope_fwd (nrm_rope_fwd
+    with norm=False) of q and k, and the key and v quantised into the cache.
+    k_out may be None when only the cache is wanted."""
+    dt = q.dtype
+    vq, tokens, d = _heads_view(q, "q")
+    vqo = _heads_view(q_out, "q_out", q, dt)[0]
+    (vk, vv), nk, code = _cache_views(cache, slots, k, v, ("k", "v"))
+    if vk is None or vv is None or nk != tokens or d != cache.d or k.dtype != dt:
+        raise ValueError("k and v must be given, with the tokens, row length and dtype of q")
+    vko = None if k_out is None else _heads_view(k_out, "k_out", k, dt)[0]
+    pwq, pwk = _dense(wq, "wq", (d,), dt), _dense(wk, "wk", (d,), dt)
+    rope = _rope(pos, inv_freq, axis, pairs, tokens)
+    _on_device(q, q_out, k_out, wq, wk, pos if rope else None, inv_freq)
+    _check(load().nrm_qk_norm_rope_cache(vq, vk, vv, pwq, pwk, rope, vqo, vko, cache._c, slots.data_ptr(), tokens, d,
+                                         eps, int(bool(norm)), code, _stream(stream)),
+           "nrm_qk_norm_rope_cache")
 
 
 def nrm_act_mask_words(n: int, c: int, l: int) -> int:

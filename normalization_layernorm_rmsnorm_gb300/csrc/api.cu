@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "heads.h"
 #include "internal.h"
 
 // Set by a kernel whose bounded wait gave up; read and cleared by nrm_sync_status.
@@ -610,8 +611,11 @@ nrm_status nrm_batchnorm_bwd(const void* dy, const void* x, const void* residual
 }
 
 size_t nrm_workspace_bytes(nrm_op op, int64_t rows, int64_t cols, nrm_dtype dt) {
-    if (op != NRM_OP_LAYERNORM_BWD && op != NRM_OP_RMSNORM_BWD && op != NRM_OP_LAYERNORM_CF_BWD) return 0;
+    if (op != NRM_OP_LAYERNORM_BWD && op != NRM_OP_RMSNORM_BWD && op != NRM_OP_LAYERNORM_CF_BWD &&
+        op != NRM_OP_QK_NORM_BWD)
+        return 0;
     if (check_rows(rows, cols, dt) != NRM_OK) return 0;
+    if (op == NRM_OP_QK_NORM_BWD) return cols > kHeadMaxD ? 0 : row_ws_bytes(false, cols);  // q's and k's partial rows
     if (op == NRM_OP_LAYERNORM_CF_BWD && cols > kCfMaxChannels) return 0;
     return row_ws_bytes(true, cols);  // dw and db partial rows (RMSNorm's db: the optional bias)
 }
@@ -677,6 +681,8 @@ nrm_status nrm_sync_status(nrm_stream_t stream) {
         const unsigned int zero = 0;
         e = cudaMemcpyToSymbol(g_nrm_error_word, &zero, sizeof(zero));
         if (e != cudaSuccess) return cuda_status(e, "clearing the device error word");
+        if ((word & ~kErrCacheSlot) == 0)
+            return fail(NRM_ERR_INVALID_ARG, "a cache slot lay outside its cache (its token was skipped)");
         return fail(NRM_ERR_TIMEOUT, "a kernel's bounded wait gave up (code %u)", word);
     }
     return NRM_OK;
@@ -704,6 +710,6 @@ nrm_status nrm_test_expire_peer_waits(uint64_t limit_ns) {
     return NRM_OK;
 }
 
-int nrm_version(void) { return 100; }
+int nrm_version(void) { return 200; }
 
 }  // extern "C"
