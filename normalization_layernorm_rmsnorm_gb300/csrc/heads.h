@@ -15,6 +15,18 @@ constexpr int kHeadMaxAxes = 4;
 // cache (the low bits report waits that gave up).
 constexpr unsigned int kErrCacheSlot = 1u << 8;
 
+// Division of a row or slot number by a fixed divisor: a multiplication where
+// every dividend is below 2^32, else the 64-bit division.
+struct RowDiv {
+    int64_t d;
+    uint64_t m;
+    int small;
+};
+inline RowDiv make_row_div(int64_t d, int64_t below) {
+    const bool small = d < (int64_t(1) << 32) && below <= (int64_t(1) << 32);
+    return RowDiv{d, small ? make_fast_div(uint32_t(d)).m : 0, small};
+}
+
 // A [tokens, heads, d] view; strides in elements.
 struct HeadView {
     void* p;
@@ -38,7 +50,7 @@ struct CacheDev {
     uint8_t* codes[2];   // k, v
     float* scales[2];
     int64_t slots;       // pages * page_size
-    int64_t page_size;
+    RowDiv page;         // by page_size
     int64_t page_stride, slot_stride, head_stride;
     int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
     int group;
@@ -64,12 +76,13 @@ struct HeadArgs {
     unsigned int* err;
 };
 
-// `vec`: every pointer, stride, d, rot and group fits 128-bit accesses.
-template <typename T> nrm_status head_fwd(const HeadArgs& a, bool norm, bool cache, bool vec, cudaStream_t s);
-template <typename T> nrm_status head_bwd(const HeadArgs& a, bool vec, cudaStream_t s);
+// `vec`: the widest accesses (16 or 8 bytes) that every pointer, stride, d, rot
+// and group fits, or 0.
+template <typename T> nrm_status head_fwd(const HeadArgs& a, bool norm, bool cache, int vec, cudaStream_t s);
+template <typename T> nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s);
 // Cache rows of a.x[1], a.x[2] (written) or to a.y[0], a.y[1] (read), heads[1] each.
-template <typename T> nrm_status cache_write(const HeadArgs& a, bool vec, cudaStream_t s);
-template <typename T> nrm_status cache_read(const HeadArgs& a, bool vec, cudaStream_t s);
+template <typename T> nrm_status cache_write(const HeadArgs& a, int vec, cudaStream_t s);
+template <typename T> nrm_status cache_read(const HeadArgs& a, int vec, cudaStream_t s);
 
 // Upper bound of the backward's partial rows.
 int head_bwd_max_partials(const DevInfo& d);

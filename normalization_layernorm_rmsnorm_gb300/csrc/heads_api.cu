@@ -153,7 +153,7 @@ nrm_status set_cache(const nrm_kv_cache* c, bool keys, bool values, CacheDev* ou
     out->scales[0] = c->k_scales;
     out->scales[1] = c->v_scales;
     out->slots = c->pages * c->page_size;
-    out->page_size = c->page_size;
+    out->page = make_row_div(c->page_size, c->pages * c->page_size);
     out->page_stride = c->page_stride;
     out->slot_stride = c->slot_stride;
     out->head_stride = c->head_stride;
@@ -171,22 +171,28 @@ nrm_status check_slots(const int64_t* slots, int64_t tokens) {
     return NRM_OK;
 }
 
-// 128-bit accesses: the views, the weights, and rows of whole pairs of vectors.
-bool fits_vec(std::initializer_list<const nrm_heads*> views, std::initializer_list<const void*> ptrs, int64_t tokens,
-              int64_t d, const RopeDev& r, nrm_dtype dt) {
-    const int64_t v = 16 / int64_t(dsize(dt));
-    if (d % (2 * v) || r.rot % (2 * v)) return false;
-    for (const nrm_heads* h : views)
-        if (h && (!aligned(h->data, 16) || (tokens > 1 && h->token_stride % v) || (h->heads > 1 && h->head_stride % v)))
-            return false;
-    for (const void* p : ptrs)
-        if (!aligned(p, 16)) return false;
-    return true;
-}
-bool fits_vec_cache(const nrm_kv_cache* c, nrm_dtype dt) {
-    const int64_t v = 16 / int64_t(dsize(dt));
-    return c->group % v == 0 && aligned(c->k_codes, 16) && aligned(c->v_codes, 16) && c->page_stride % 16 == 0 &&
-           c->slot_stride % 16 == 0 && c->head_stride % 16 == 0;
+// The widest accesses (16 or 8 bytes; 0: single elements) that fit the views,
+// the weights, rows of whole pairs of vectors (at most 32 pairs), and, where
+// there is one, the cache's groups and rows of codes.
+int fits_vec(std::initializer_list<const nrm_heads*> views, std::initializer_list<const void*> ptrs, int64_t tokens,
+             int64_t d, const RopeDev& r, nrm_dtype dt, const nrm_kv_cache* c = nullptr) {
+    for (int bytes = 16; bytes >= 8; bytes /= 2) {
+        const int64_t v = bytes / int64_t(dsize(dt));
+        bool ok = d % (2 * v) == 0 && d / (2 * v) <= 32 && r.rot % (2 * v) == 0;
+        for (const nrm_heads* h : views)
+            if (h && (!aligned(h->data, size_t(bytes)) || (tokens > 1 && h->token_stride % v) ||
+                      (h->heads > 1 && h->head_stride % v)))
+                ok = false;
+        for (const void* p : ptrs) ok = ok && aligned(p, size_t(bytes));
+        if (c) {
+            const int64_t b = c->kind == NRM_CACHE_INT4 ? v / 2 : v;  // bytes of a vector's codes
+            ok = ok && c->group % v == 0 && aligned(c->k_codes, size_t(b)) && aligned(c->v_codes, size_t(b)) &&
+                 (c->pages == 1 || c->page_stride % b == 0) && (c->page_size == 1 || c->slot_stride % b == 0) &&
+                 (c->heads == 1 || c->head_stride % b == 0);
+        }
+        if (ok) return bytes;
+    }
+    return 0;
 }
 
 template <typename F>
@@ -278,7 +284,7 @@ nrm_status nrm_qk_norm_rope_fwd(const nrm_heads* q, const nrm_heads* k, const vo
         a.rstd[0] = rstd_q;
         a.rstd[1] = rstd_k;
         a.eps = eps;
-        const bool vec = fits_vec({q, k, q_out, k ? k_out : nullptr}, {wq, wk}, tokens, d, a.rope, dt);
+        const int vec = fits_vec({q, k, q_out, k ? k_out : nullptr}, {wq, wk}, tokens, d, a.rope, dt);
         return by_dtype(dt, [&](auto tag) {
             return head_fwd<decltype(tag)>(a, true, false, vec, reinterpret_cast<cudaStream_t>(stream));
         });
@@ -342,7 +348,7 @@ nrm_status nrm_qk_norm_rope_bwd(const nrm_heads* dq_out, const nrm_heads* dk_out
         a.heads[0] = int(q->heads);
         a.heads[1] = k ? int(k->heads) : 0;
         a.d = int(d);
-        const bool vec = fits_vec({q, k, dq_out, dk_out, dq, dk}, {wq, wk}, tokens, d, a.rope, dt);
+        const int vec = fits_vec({q, k, dq_out, dk_out, dq, dk}, {wq, wk}, tokens, d, a.rope, dt);
         return by_dtype(dt, [&](auto tag) {
             return head_bwd<decltype(tag)>(a, vec, reinterpret_cast<cudaStream_t>(stream));
         });
@@ -355,7 +361,7 @@ static nrm_status rope_only(const nrm_heads* q, const nrm_heads* k, const nrm_ro
     return entry([&]() -> nrm_status {
         HeadArgs a;
         NRM_TRY(set_fwd(q, k, rope, qo, ko, false, tokens, d, dt, inverse, &a));
-        const bool vec = fits_vec({q, k, qo, k ? ko : nullptr}, {}, tokens, d, a.rope, dt);
+        const int vec = fits_vec({q, k, qo, k ? ko : nullptr}, {}, tokens, d, a.rope, dt);
         return by_dtype(dt, [&](auto tag) {
             return head_fwd<decltype(tag)>(a, false, false, vec, reinterpret_cast<cudaStream_t>(stream));
         });
@@ -389,7 +395,7 @@ nrm_status nrm_kv_cache_write(const nrm_heads* k, const nrm_heads* v, const nrm_
         a.heads[1] = int(cache->heads);
         a.d = int(cache->d);
         a.slots = slots;
-        const bool vec = fits_vec({k, v}, {}, tokens, a.d, a.rope, dt) && fits_vec_cache(cache, dt);
+        const int vec = fits_vec({k, v}, {}, tokens, a.d, a.rope, dt, cache);
         return by_dtype(dt, [&](auto tag) {
             return cache_write<decltype(tag)>(a, vec, reinterpret_cast<cudaStream_t>(stream));
         });
@@ -414,7 +420,7 @@ nrm_status nrm_kv_cache_read(const nrm_kv_cache* cache, const int64_t* slots, co
         a.heads[1] = int(cache->heads);
         a.d = int(cache->d);
         a.slots = slots;
-        const bool vec = fits_vec({k_out, v_out}, {}, tokens, a.d, a.rope, dt) && fits_vec_cache(cache, dt);
+        const int vec = fits_vec({k_out, v_out}, {}, tokens, a.d, a.rope, dt, cache);
         return by_dtype(dt, [&](auto tag) {
             return cache_read<decltype(tag)>(a, vec, reinterpret_cast<cudaStream_t>(stream));
         });
@@ -448,8 +454,7 @@ nrm_status nrm_qk_norm_rope_cache(const nrm_heads* q, const nrm_heads* k, const 
         a.x[2] = view(v);
         a.heads[2] = int(v->heads);
         a.slots = slots;
-        const bool vec = fits_vec({q, k, v, q_out, k_out}, {a.w[0], a.w[1]}, tokens, d, a.rope, dt) &&
-                         fits_vec_cache(cache, dt);
+        const int vec = fits_vec({q, k, v, q_out, k_out}, {a.w[0], a.w[1]}, tokens, d, a.rope, dt, cache);
         return by_dtype(dt, [&](auto tag) {
             return head_fwd<decltype(tag)>(a, norm != 0, true, vec, reinterpret_cast<cudaStream_t>(stream));
         });
