@@ -11,8 +11,6 @@
 // fit no vector take a row per warp, element by element.
 #pragma once
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "heads.h"
 
@@ -125,6 +123,16 @@ __device__ __forceinline__ float group_scaled(float x, const GroupQ& g) {
         return g.r == 0.f ? 0.f : odd;
     }
 }
+// Of two elements, neither a NaN.
+template <typename T>
+__device__ __forceinline__ float2 group_scaled2(float2 x, const GroupQ& g) {
+    if constexpr (sizeof(T) == 2) {
+        const float2 n = __fmul2_rn(x, f2(g.q)), u0 = __fmul2_rn(n, f2(g.r));
+        return __ffma2_rn(__ffma2_rn(f2neg(u0), f2(g.m), n), f2(g.r), u0);
+    } else {
+        return make_float2(group_scaled<T>(x.x, g), group_scaled<T>(x.y, g));
+    }
+}
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -205,69 +213,113 @@ __device__ __forceinline__ void st_row(void* p, uint2 v) {
     asm volatile("st.global.v2.u32 [%0], {%1,%2};" :: "l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
 
+// The elements as pairs of floats, for the packed fp32 instructions (two elements
+// each, rounded as the scalar instruction would).
 template <typename T, int VE>
-__device__ __forceinline__ void raw_unpack(const Raw<T, VE>& r, float (&v)[VE]) {
+__device__ __forceinline__ void raw_unpack(const Raw<T, VE>& r, float2 (&v)[VE / 2]) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-    for (int i = 0; i < VE * int(sizeof(T)) / 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            v[i] = __uint_as_float(w[i]);
-        } else {
-            const float2 f = cvt2<T>(w[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
+    for (int i = 0; i < VE / 2; ++i) {
+        if constexpr (sizeof(T) == 4) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else v[i] = cvt2<T>(w[i]);
     }
 }
 template <typename T, int VE>
-__device__ __forceinline__ Raw<T, VE> raw_pack(const float (&v)[VE]) {
+__device__ __forceinline__ Raw<T, VE> raw_pack(const float2 (&v)[VE / 2]) {
     Raw<T, VE> r;
     uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-    for (int i = 0; i < VE * int(sizeof(T)) / 4; ++i) {
-        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
-        else w[i] = pack2<T>(make_float2(v[2 * i], v[2 * i + 1]));
+    for (int i = 0; i < VE / 2; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i] = __float_as_uint(v[i].x);
+            w[2 * i + 1] = __float_as_uint(v[i].y);
+        } else {
+            w[i] = pack2<T>(v[i]);
+        }
     }
     return r;
 }
 
-// The largest magnitude's bits.
-template <int VE>
-__device__ __forceinline__ uint32_t abs_max_bits(const float (&v)[VE]) {
-    uint32_t m = 0;
+// Largest magnitudes, compared as integers: of float32 its bits, of 16-bit types
+// two at once, in the halves of a word.
+template <typename T>
+__device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return max(a, b);
+    else return __vmaxu2(a, b);
+}
+template <typename T, int VE>
+__device__ __forceinline__ uint32_t raw_mag(const Raw<T, VE>& r) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+    constexpr uint32_t keep = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+    uint32_t m = w[0] & keep;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 1; i < VE * int(sizeof(T)) / 4; ++i) m = mag_max<T>(m, w[i] & keep);
     return m;
 }
+// The float32 bits of what such a word holds.
+template <typename T>
+__device__ __forceinline__ uint32_t mag_bits(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    else return __float_as_uint(Io<T>::load(typename Io<T>::bits_t(max(m & 0xffffu, m >> 16))));
+}
 
-// Codes of VE consecutive elements, stored at element e of the row.
+// Codes of VE consecutive elements, stored at element e of the row.  A whole
+// number comes out of the low bits of u + 1.5 * 2^23 (the sum rounds to nearest,
+// ties to even).
 template <typename T, int VE>
-__device__ __forceinline__ void store_codes(uint8_t* row, int e, const float (&v)[VE], const GroupQ& q, int kind) {
-    float u[VE];
+__device__ __forceinline__ void store_codes(uint8_t* row, int e, Raw<T, VE> x, const GroupQ& q, int kind) {
+    const uint32_t live = q.r != 0.f ? 0xffffffffu : 0u;  // no NaN reaches the arithmetic
+    uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) u[i] = group_scaled<T>(v[i], q);
-    if (kind == NRM_CACHE_INT4) {
-        uint32_t w = 0;
+    for (int i = 0; i < VE * int(sizeof(T)) / 4; ++i) xw[i] &= live;
+    float2 u[VE / 2];
+    raw_unpack<T, VE>(x, u);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) w |= (uint32_t(__float2int_rn(u[i])) & 0xfu) << (4 * i);
+    for (int i = 0; i < VE / 2; ++i) u[i] = group_scaled2<T>(u[i], q);
+    if (kind == NRM_CACHE_E4M3) {
+        uint32_t w[(VE + 3) / 4] = {};
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) w[i / 4] |= e4m3x2(u[i / 2].x, u[i / 2].y) << (8 * (i % 4));
+        uint8_t* at = row + e;
+        if constexpr (VE == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(at) = w[0];
+        else *reinterpret_cast<uint16_t*>(at) = uint16_t(w[0]);
+        return;
+    }
+    constexpr uint32_t magic = 0x4B400000u;  // 1.5 * 2^23
+    uint32_t b[VE];
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+        const float2 f = __fadd2_rn(u[i], f2(__uint_as_float(magic)));
+        b[2 * i] = __float_as_uint(f.x);
+        b[2 * i + 1] = __float_as_uint(f.y);
+    }
+    if (kind == NRM_CACHE_INT8) {
+        uint8_t* at = row + e;
+        if constexpr (VE == 2) {
+            *reinterpret_cast<uint16_t*>(at) = uint16_t(__byte_perm(b[0], b[1], 0x0040));
+        } else {
+            uint32_t w[VE / 4];
+#pragma unroll
+            for (int i = 0; i < VE / 4; ++i)
+                w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                                   __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
+            if constexpr (VE == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(at) = w[0];
+        }
+    } else {
+        // sum of code_i * 16^i: the constants come off at the end, and with 8 added to
+        // each code no digit borrows from the next
+        constexpr uint32_t ones = VE == 8 ? 0x11111111u : (VE == 4 ? 0x1111u : 0x11u);
+        uint32_t w = b[VE - 1];
+#pragma unroll
+        for (int i = VE - 2; i >= 0; --i) w = w * 16 + b[i];
+        w = (w - magic * ones + 8 * ones) ^ (8 * ones);
         uint8_t* at = row + (e >> 1);
         if constexpr (VE == 8) *reinterpret_cast<uint32_t*>(at) = w;
         else if constexpr (VE == 4) *reinterpret_cast<uint16_t*>(at) = uint16_t(w);
         else *at = uint8_t(w);
-        return;
     }
-    uint32_t w[(VE + 3) / 4] = {};
-    if (kind == NRM_CACHE_E4M3) {
-#pragma unroll
-        for (int i = 0; i < VE; i += 2) w[i / 4] |= e4m3x2(u[i], u[i + 1]) << (8 * (i % 4));
-    } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) w[i / 4] |= (uint32_t(__float2int_rn(u[i])) & 0xffu) << (8 * (i % 4));
-    }
-    uint8_t* at = row + e;
-    if constexpr (VE == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-    else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(at) = w[0];
-    else *reinterpret_cast<uint16_t*>(at) = uint16_t(w[0]);
 }
 
 // A lane's place in the vector kernels: which row of the warp's, which pair of
@@ -323,17 +375,22 @@ struct WarpTurns {
 
 // Turns a lane's two vectors by its VE pairs' angles.
 template <int VE>
-__device__ __forceinline__ void turn_vecs(float (&u)[VE], float (&v)[VE], const float (&c)[VE], const float (&s)[VE],
-                                          bool adjacent) {
+__device__ __forceinline__ void turn_vecs(float2 (&u)[VE / 2], float2 (&v)[VE / 2], const float2 (&c)[VE / 2],
+                                          const float2 (&s)[VE / 2], bool adjacent) {
+    constexpr int H = VE / 2;
     if (!adjacent) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) turn(u[i], v[i], make_float2(c[i], s[i]));
+        for (int i = 0; i < H; ++i) {
+            const float2 a = __ffma2_rn(u[i], c[i], f2neg(__fmul2_rn(v[i], s[i])));
+            v[i] = __ffma2_rn(v[i], c[i], __fmul2_rn(u[i], s[i]));
+            u[i] = a;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) turn(u[2 * i], u[2 * i + 1], make_float2(c[i], s[i]));
-#pragma unroll
-        for (int i = 0; i < VE / 2; ++i)
-            turn(v[2 * i], v[2 * i + 1], make_float2(c[VE / 2 + i], s[VE / 2 + i]));
+        for (int i = 0; i < VE; ++i) {
+            float2& x = i < H ? u[i % H] : v[i % H];
+            turn(x.x, x.y, i % 2 ? make_float2(c[i / 2].y, s[i / 2].y) : make_float2(c[i / 2].x, s[i / 2].x));
+        }
     }
 }
 
@@ -349,128 +406,138 @@ __device__ __forceinline__ float row_sum(float v, int lg) {
 constexpr int kHeadRows = 2;  // rows of a lane in flight
 
 // A warp takes (token, chunk) units; chunk c of 2^lchunk takes the token's row
-// steps c, c + 2^lchunk, ...  (a step: kHeadRows * (32 >> lg) rows).
+// steps c, c + 2^lchunk, ... (a step: kHeadRows * (32 >> lg) rows of one tensor).
 template <typename T, int VE, bool NORM, bool CACHE>
-__global__ void __launch_bounds__(kHeadWarps * 32)
+__global__ void __launch_bounds__(kHeadWarps * 32, CACHE ? 2 : 3)
 head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
+    constexpr int H = VE / 2;
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
     __shared__ uint32_t s_max[CACHE ? kHeadWarps : 1][CACHE ? 64 : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const LaneAt<VE> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
-    const int rows = 32 >> lg;
-    const int heads = a.heads[0] + a.heads[1] + (CACHE ? a.heads[2] : 0);
+    const int rows = 32 >> lg, lper = 5 - lg + (kHeadRows == 2 ? 1 : 0);  // 2^lper rows a step
     const int64_t units = a.tokens << lchunk;
     const float inv_d = 1.f / float(a.d);
+    const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
     for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = un >> lchunk;
-        int h0 = (int(un) & ((1 << lchunk) - 1)) * (rows * kHeadRows);
+        const int chunk = int(un) & ((1 << lchunk) - 1);
         const int64_t slot = CACHE ? cache_slot(a.cache, __ldg(a.slots + t), a.err) : -1;
         turns.make(a.rope, lane, t, s_cos[warp], s_sin[warp]);
-        float c[VE], s[VE];
+        float2 c[H], s[H];
         if (at.turns) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                c[i] = s_cos[warp][VE * at.j + i];
-                s[i] = s_sin[warp][VE * at.j + i];
+            for (int i = 0; i < H; ++i) {
+                c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
+                s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
             }
         }
-        for (; h0 < heads; h0 += (rows * kHeadRows) << lchunk) {
-            Raw<T, VE> x0[kHeadRows], x1[kHeadRows];
-            int which[kHeadRows], hd[kHeadRows];
+        int first = 0;  // the tensor's first step
+#pragma unroll 1
+        for (int which = 0; which < (CACHE ? 3 : 2); ++which) {
+            const int heads = a.heads[which], steps = (heads + (1 << lper) - 1) >> lper;
+            int st = (chunk - first) & ((1 << lchunk) - 1);
+            first += steps;
+            if (st >= steps) continue;
+            const HeadView xv = a.x[which], yv = which < 2 ? a.y[which] : HeadView{};
+            const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + at.b0;
+            T* y = reinterpret_cast<T*>(yv.p) + t * yv.ts + at.b0;
+            const int b01 = at.b1 - at.b0;
+            float2 w0[H], w1[H];
+            if (NORM && which < 2) {
 #pragma unroll
-            for (int k = 0; k < kHeadRows; ++k) {
-                const int hh = h0 + k * rows + at.sub;
-                which[k] = hh < a.heads[0] ? 0 : (hh < a.heads[0] + a.heads[1] ? 1 : 2);
-                hd[k] = hh - (which[k] > 0 ? a.heads[0] : 0) - (which[k] > 1 ? a.heads[1] : 0);
-                x0[k] = x1[k] = Raw<T, VE>{};
-                if (hh >= heads) which[k] = 3;  // no row
-                else if (at.on) {
-                    const HeadView v = a.x[which[k]];
-                    const T* x = reinterpret_cast<const T*>(v.p) + t * v.ts + hd[k] * v.hs;
-                    ld_row(x + at.b0, x0[k]);
-                    ld_row(x + at.b1, x1[k]);
+                for (int i = 0; i < H; ++i) w0[i] = w1[i] = f2(1.f);
+                const T* w = reinterpret_cast<const T*>(a.w[which]);
+                if (w && at.on) {
+                    raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
+                    raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
                 }
             }
+            float* rstd = NORM && which < 2 ? a.rstd[which] : nullptr;
+#pragma unroll 1
+            for (; st < steps; st += 1 << lchunk) {
+                Raw<T, VE> x0[kHeadRows], x1[kHeadRows];
+                const int h0 = (st << lper) + at.sub;
 #pragma unroll
-            for (int k = 0; k < kHeadRows; ++k) {
-                float u[VE], v[VE];
-                raw_unpack<T, VE>(x0[k], u);
-                raw_unpack<T, VE>(x1[k], v);
-                if (NORM) {
-                    float sum = 0.f;
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) sum = fmaf(u[i], u[i], fmaf(v[i], v[i], sum));
-                    const float r = rsqrtf(fmaf(row_sum(sum, lg), inv_d, a.eps));
-                    if (which[k] < 2) {
-                        if (at.j == 0 && a.rstd[which[k]]) a.rstd[which[k]][t * a.heads[which[k]] + hd[k]] = r;
-#pragma unroll
-                        for (int i = 0; i < VE; ++i) {
-                            u[i] = __fmul_rn(u[i], r);
-                            v[i] = __fmul_rn(v[i], r);
-                        }
-                        const T* w = reinterpret_cast<const T*>(a.w[which[k]]);
-                        if (w && at.on) {
-                            float w0[VE], w1[VE];
-                            raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
-                            raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
-#pragma unroll
-                            for (int i = 0; i < VE; ++i) {
-                                u[i] = __fmul_rn(u[i], w0[i]);
-                                v[i] = __fmul_rn(v[i], w1[i]);
-                            }
-                        }
+                for (int k = 0; k < kHeadRows; ++k) {
+                    const int h = h0 + k * rows;
+                    x0[k] = x1[k] = Raw<T, VE>{};
+                    if (h < heads && at.on) {
+                        const T* p = x + h * xv.hs;
+                        ld_row(p, x0[k]);
+                        ld_row(p + b01, x1[k]);
                     }
                 }
-                if (which[k] < 2) {
-                    if (at.turns) turn_vecs<VE>(u, v, c, s, a.rope.adjacent);
-                    x0[k] = raw_pack<T, VE>(u);
-                    x1[k] = raw_pack<T, VE>(v);
-                    const HeadView y = a.y[which[k]];
-                    if (at.on && y.p) {
-                        T* o = reinterpret_cast<T*>(y.p) + t * y.ts + hd[k] * y.hs;
-                        st_row(o + at.b0, x0[k]);
-                        st_row(o + at.b1, x1[k]);
-                    }
-                }
-                if constexpr (CACHE) {
-                    // uniform: the warp's rows of this step hold a key or a value, and the token has a slot
-                    if (slot < 0 || h0 + (k + 1) * rows <= a.heads[0]) continue;
-                    // the cache stores the key in the activations' type: what a separate write would read
-                    raw_unpack<T, VE>(x0[k], u);
-                    raw_unpack<T, VE>(x1[k], v);
-                    uint32_t m0 = at.on ? abs_max_bits<VE>(u) : 0, m1 = at.on ? abs_max_bits<VE>(v) : 0;
-                    const int group = a.cache.group;
-                    if (group == a.d) {
-                        m0 = max(m0, m1);
-                        for (int o = 1 << lg >> 1; o > 0; o >>= 1) m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                        m1 = m0;
-                    } else {
-                        // groups of whole vectors, which other lanes may hold: through shared memory
-                        uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
-                        if (at.on) {
-                            sm[at.b0 / VE] = m0;
-                            sm[at.b1 / VE] = m1;
-                        }
-                        __syncwarp();
-                        if (at.on) {
-                            const int n = group / VE, g0 = at.b0 / group * n, g1 = at.b1 / group * n;
-                            for (int i = 0; i < n; ++i) {
-                                m0 = max(m0, sm[g0 + i]);
-                                m1 = max(m1, sm[g1 + i]);
+#pragma unroll
+                for (int k = 0; k < kHeadRows; ++k) {
+                    const int h = h0 + k * rows;
+                    const bool row = h < heads;
+                    if (which < 2) {
+                        float2 u[H], v[H];
+                        raw_unpack<T, VE>(x0[k], u);
+                        raw_unpack<T, VE>(x1[k], v);
+                        if (NORM) {
+                            float2 sq = f2(0.f);
+#pragma unroll
+                            for (int i = 0; i < H; ++i) sq = __ffma2_rn(u[i], u[i], __ffma2_rn(v[i], v[i], sq));
+                            const float r = rsqrtf(fmaf(row_sum(sq.x + sq.y, lg), inv_d, a.eps));
+                            if (rstd && row && at.j == 0) rstd[t * heads + h] = r;
+#pragma unroll
+                            for (int i = 0; i < H; ++i) {
+                                u[i] = __fmul2_rn(__fmul2_rn(u[i], f2(r)), w0[i]);
+                                v[i] = __fmul2_rn(__fmul2_rn(v[i], f2(r)), w1[i]);
                             }
                         }
-                        __syncwarp();
+                        if (at.turns) turn_vecs<VE>(u, v, c, s, a.rope.adjacent);
+                        x0[k] = raw_pack<T, VE>(u);
+                        x1[k] = raw_pack<T, VE>(v);
+                        if (row && at.on && yv.p) {
+                            T* p = y + h * yv.hs;
+                            st_row(p, x0[k]);
+                            st_row(p + b01, x1[k]);
+                        }
                     }
-                    if (at.on && (which[k] == 1 || which[k] == 2)) {
-                        const CacheRow cr = cache_row(a.cache, slot, hd[k]);
-                        const GroupQ q0 = group_q(m0, a.cache.kind), q1 = group_q(m1, a.cache.kind);
-                        float* scales = a.cache.scales[which[k] - 1] + cr.scale;
-                        if (at.b0 % group == 0) scales[at.b0 / group] = q0.scale;
-                        if (at.b1 % group == 0) scales[at.b1 / group] = q1.scale;
-                        uint8_t* codes = a.cache.codes[which[k] - 1] + cr.code;
-                        store_codes<T, VE>(codes, at.b0, u, q0, a.cache.kind);
-                        store_codes<T, VE>(codes, at.b1, v, q1, a.cache.kind);
+                    if constexpr (CACHE) {
+                        // (both conditions are the warp's.)  The cache stores the key in the activations'
+                        // type: what a separate write would read.
+                        if (which == 0 || slot < 0) continue;
+                        uint32_t m0 = raw_mag<T, VE>(x0[k]), m1 = raw_mag<T, VE>(x1[k]);
+                        const int group = a.cache.group;
+                        if (group == a.d) {
+                            m0 = mag_max<T>(m0, m1);
+                            if (!at.on) m0 = 0;
+                            for (int o = 1 << lg >> 1; o > 0; o >>= 1)
+                                m0 = mag_max<T>(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                            m1 = m0;
+                        } else {
+                            // groups of whole vectors, which other lanes may hold: through shared memory
+                            uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
+                            const int n = group / VE;
+                            if (at.on) {
+                                sm[at.b0 / VE] = m0;
+                                sm[at.b1 / VE] = m1;
+                            }
+                            __syncwarp();
+                            if (at.on) {
+                                for (int i = 0; i < n; ++i) {
+                                    m0 = mag_max<T>(m0, sm[g0 * n + i]);
+                                    m1 = mag_max<T>(m1, sm[g1 * n + i]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        if (row && at.on) {
+                            const CacheRow cr = cache_row(a.cache, slot, h);
+                            const GroupQ q0 = group_q(mag_bits<T>(m0), a.cache.kind);
+                            const GroupQ q1 = group_q(mag_bits<T>(m1), a.cache.kind);
+                            float* scales = a.cache.scales[which - 1] + cr.scale;
+                            if (at.b0 == g0 * group) scales[g0] = q0.scale;
+                            if (at.b1 == g1 * group) scales[g1] = q1.scale;
+                            uint8_t* codes = a.cache.codes[which - 1] + cr.code;
+                            store_codes<T, VE>(codes, at.b0, x0[k], q0, a.cache.kind);
+                            store_codes<T, VE>(codes, at.b1, x1[k], q1, a.cache.kind);
+                        }
                     }
                 }
             }
@@ -484,8 +551,9 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
 template <typename T, int VE>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int nq) {
+    constexpr int H = VE / 2;
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
-    __shared__ float part[kHeadWarps][kHeadMaxD];
+    __shared__ __align__(16) float part[kHeadWarps][kHeadMaxD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int which = int(blockIdx.x) < nq ? 0 : 1;
     const int cta = int(blockIdx.x) - (which ? nq : 0);
@@ -497,11 +565,12 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const int64_t units = a.tokens << lchunk;
     const float inv_d = 1.f / float(a.d);
     const HeadView xv = a.x[which], gv = a.dy[which], dv = a.y[which];
-    float w0[VE], w1[VE], acc0[VE], acc1[VE];
+    const int b01 = at.b1 - at.b0;
+    float2 w0[H], w1[H], acc0[H], acc1[H];
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-        w0[i] = w1[i] = 1.f;
-        acc0[i] = acc1[i] = 0.f;
+    for (int i = 0; i < H; ++i) {
+        w0[i] = w1[i] = f2(1.f);
+        acc0[i] = acc1[i] = f2(0.f);
     }
     if (at.on && a.w[which]) {
         const T* w = reinterpret_cast<const T*>(a.w[which]);
@@ -511,67 +580,77 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     for (int64_t un = int64_t(cta) * kHeadWarps + warp; un < units; un += int64_t(ctas) * kHeadWarps) {
         const int64_t t = un >> lchunk;
         turns.make(a.rope, lane, t, s_cos[warp], s_sin[warp]);
-        float c[VE], s[VE];
+        float2 c[H], s[H];
         if (at.turns) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                c[i] = s_cos[warp][VE * at.j + i];
-                s[i] = s_sin[warp][VE * at.j + i];
+            for (int i = 0; i < H; ++i) {
+                c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
+                s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
             }
         }
-        for (int h = (int(un) & ((1 << lchunk) - 1)) * rows; h < heads; h += rows << lchunk) {
-            const int hd = h + at.sub;
-            const bool row = hd < heads, on = row && at.on;
+        const T* g = reinterpret_cast<const T*>(gv.p) + t * gv.ts + at.b0;
+        const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + at.b0;
+        T* dx = reinterpret_cast<T*>(dv.p) + t * dv.ts + at.b0;
+        const float* rstd = a.rstd[which] + t * heads;
+#pragma unroll 1
+        for (int h0 = (int(un) & ((1 << lchunk) - 1)) * rows; h0 < heads; h0 += rows << lchunk) {
+            const int h = h0 + at.sub;
+            const bool on = h < heads && at.on;
             Raw<T, VE> x0{}, x1{}, y0{}, y1{};
             float r = 0.f;
             if (on) {
-                const T* g = reinterpret_cast<const T*>(gv.p) + t * gv.ts + hd * gv.hs;
-                const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + hd * xv.hs;
-                ld_row(g + at.b0, y0);
-                ld_row(g + at.b1, y1);
-                ld_row(x + at.b0, x0);
-                ld_row(x + at.b1, x1);
-                r = __ldg(a.rstd[which] + t * heads + hd);
+                const T* pg = g + h * gv.hs;
+                const T* px = x + h * xv.hs;
+                ld_row(pg, y0);
+                ld_row(pg + b01, y1);
+                ld_row(px, x0);
+                ld_row(px + b01, x1);
+                r = __ldg(rstd + h);
             }
-            float u[VE], v[VE], gu[VE], gw[VE];
-            raw_unpack<T, VE>(x0, u);
-            raw_unpack<T, VE>(x1, v);
+            float2 u[H], v[H], gu[H], gw[H];
             raw_unpack<T, VE>(y0, gu);
             raw_unpack<T, VE>(y1, gw);
             if (at.turns) turn_vecs<VE>(gu, gw, c, s, a.rope.adjacent);
-            float sum = 0.f;
+            raw_unpack<T, VE>(x0, u);
+            raw_unpack<T, VE>(x1, v);
+            float2 sum = f2(0.f);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                acc0[i] = fmaf(gu[i], u[i] * r, acc0[i]);
-                acc1[i] = fmaf(gw[i], v[i] * r, acc1[i]);
-                gu[i] *= w0[i];
-                gw[i] *= w1[i];
-                sum = fmaf(gu[i], u[i], fmaf(gw[i], v[i], sum));
+            for (int i = 0; i < H; ++i) {
+                gu[i] = __fmul2_rn(gu[i], f2(r));
+                gw[i] = __fmul2_rn(gw[i], f2(r));
+                acc0[i] = __ffma2_rn(gu[i], u[i], acc0[i]);
+                acc1[i] = __ffma2_rn(gw[i], v[i], acc1[i]);
+                gu[i] = __fmul2_rn(gu[i], w0[i]);
+                gw[i] = __fmul2_rn(gw[i], w1[i]);
+                sum = __ffma2_rn(gu[i], u[i], __ffma2_rn(gw[i], v[i], sum));
             }
-            const float f = row_sum(sum, lg) * inv_d * r * r * r;
+            // dx = r g - x r^2 sum(r g x) / d, the terms r g at hand
+            const float f = -(row_sum(sum.x + sum.y, lg) * inv_d * r * r);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                gu[i] = fmaf(-u[i], f, gu[i] * r);
-                gw[i] = fmaf(-v[i], f, gw[i] * r);
+            for (int i = 0; i < H; ++i) {
+                gu[i] = __ffma2_rn(u[i], f2(f), gu[i]);
+                gw[i] = __ffma2_rn(v[i], f2(f), gw[i]);
             }
             if (on) {
-                T* o = reinterpret_cast<T*>(dv.p) + t * dv.ts + hd * dv.hs;
-                st_row(o + at.b0, raw_pack<T, VE>(gu));
-                st_row(o + at.b1, raw_pack<T, VE>(gw));
+                T* o = dx + h * dv.hs;
+                st_row(o, raw_pack<T, VE>(gu));
+                st_row(o + b01, raw_pack<T, VE>(gw));
             }
         }
     }
     if (a.ws == nullptr) return;
     // the warp's rows, then the CTA's warps, in a fixed order
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
+    for (int i = 0; i < H; ++i) {
         for (int o = 1 << lg; o < 32; o <<= 1) {
-            acc0[i] += __shfl_xor_sync(0xffffffffu, acc0[i], o);
-            acc1[i] += __shfl_xor_sync(0xffffffffu, acc1[i], o);
+            acc0[i].x += __shfl_xor_sync(0xffffffffu, acc0[i].x, o);
+            acc0[i].y += __shfl_xor_sync(0xffffffffu, acc0[i].y, o);
+            acc1[i].x += __shfl_xor_sync(0xffffffffu, acc1[i].x, o);
+            acc1[i].y += __shfl_xor_sync(0xffffffffu, acc1[i].y, o);
         }
         if (at.sub == 0 && at.on) {
-            part[warp][at.b0 + i] = acc0[i];
-            part[warp][at.b1 + i] = acc1[i];
+            *reinterpret_cast<float2*>(&part[warp][at.b0 + 2 * i]) = acc0[i];
+            *reinterpret_cast<float2*>(&part[warp][at.b1 + 2 * i]) = acc1[i];
         }
     }
     __syncthreads();
@@ -584,78 +663,104 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 }
 
 // ---------------------------------------------------------------------------
-// cache rows on vectors: 2^lg lanes a row, NV vectors of a row to a lane
+// cache rows on vectors
 // ---------------------------------------------------------------------------
-constexpr int kCacheRows = 4;  // rows of a lane in flight
+// 2^lg lanes hold a row, NV vectors each: lane j those at j and j + per.  A warp's
+// 32 >> lg row places are 2^lhp heads of each of its tokens; every lane goes over
+// its heads lhp, 2 lhp, ... of the keys and the values, kCacheHeads at a time.
+constexpr int kCacheHeads = 2;
+
+struct CacheLanes {
+    int lg;      // lanes of a row
+    int per;     // lanes of them that hold vectors
+    int lhp;     // heads of a token that the warp holds at once
+    int lchunk;  // a token's heads are split over 2^lchunk warps
+};
 
 template <typename T, int VE, int NV>
 __global__ void __launch_bounds__(kHeadWarps * 32)
-cache_write_vec_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads, int lg) {
+cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane >> lg, j = lane & ((1 << lg) - 1), rows = 32 >> lg;
-    const int which = a.x[1].p ? int(blockIdx.y) : 1;
-    const HeadView xv = a.x[1 + which];
-    const int64_t n = a.tokens * by_heads.d;
-    const int group = a.cache.group, kind = a.cache.kind;
-    const int gv = group / VE;                       // vectors of a group
+    const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp;
+    const bool on = j < cl.per;
+    const int heads = a.heads[1], group = a.cache.group, kind = a.cache.kind;
+    const int gv = group / VE;  // vectors of a group
     const bool whole = group == a.d, pow2 = (gv & (gv - 1)) == 0;
-    const int64_t step = int64_t(rows) * kCacheRows;
-    for (int64_t base = (int64_t(blockIdx.x) * kHeadWarps + warp) * step; base < n;
-         base += int64_t(gridDim.x) * kHeadWarps * step) {
-        Raw<T, VE> raw[kCacheRows][NV];
-        int64_t slot[kCacheRows];
-        int hd[kCacheRows];
+    const int source = (sub << cl.lg) + j / gv * gv;  // first lane of this lane's group
+    const int ltok = 5 - cl.lg - cl.lhp;              // tokens of a warp
+    int gi[NV];
+    bool leads[NV];
 #pragma unroll
-        for (int k = 0; k < kCacheRows; ++k) {
-            const int64_t i = base + k * rows + sub;
-            slot[k] = -1;
-            hd[k] = 0;
-            if (i < n) {
-                const int64_t t = row_div(i, by_heads);
-                hd[k] = int(i - t * by_heads.d);
-                slot[k] = __ldg(a.slots + t);
-                const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + hd[k] * xv.hs;
+    for (int v = 0; v < NV; ++v) {
+        gi[v] = (j + v * cl.per) * VE / group;
+        leads[v] = (j + v * cl.per) * VE == gi[v] * group;
+    }
+    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk;
+    for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
+        const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
+        int64_t slot = -1;
+        if (t < a.tokens) slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
+        const CacheRow cr = cache_row(a.cache, slot < 0 ? 0 : slot, 0);
+        const bool live = slot >= 0 && on;
+#pragma unroll 1
+        for (int h0 = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads); h0 < heads;
+             h0 += (hp * kCacheHeads) << cl.lchunk) {
+            Raw<T, VE> raw[2][kCacheHeads][NV];
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    raw[k][v] = Raw<T, VE>{};
-                    const int e = (j + 32 * v) * VE;
-                    if (e < a.d) ld_row(x + e, raw[k][v]);
+            for (int w = 0; w < 2; ++w) {
+                const HeadView xv = a.x[1 + w];
+                const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + j * VE;
+#pragma unroll
+                for (int k = 0; k < kCacheHeads; ++k) {
+                    const int h = h0 + k * hp + (sub & (hp - 1));
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        raw[w][k][v] = Raw<T, VE>{};
+                        if (xv.p && live && h < heads) ld_row(x + h * xv.hs + v * cl.per * VE, raw[w][k][v]);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < kCacheRows; ++k) {
-            slot[k] = cache_slot(a.cache, slot[k], a.err);
-            float x[NV][VE];
-            uint32_t m[NV];
+            for (int w = 0; w < 2; ++w) {
+                if (!a.x[1 + w].p) continue;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                raw_unpack<T, VE>(raw[k][v], x[v]);
-                m[v] = (j + 32 * v) * VE < a.d && slot[k] >= 0 ? abs_max_bits<VE>(x[v]) : 0;
-            }
-            if (whole) {
-                if constexpr (NV == 2) m[0] = max(m[0], m[1]);
-                for (int o = 1 << lg >> 1; o > 0; o >>= 1) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-                if constexpr (NV == 2) m[1] = m[0];
-            } else if (pow2) {
+                for (int k = 0; k < kCacheHeads; ++k) {
+                    const int h = h0 + k * hp + (sub & (hp - 1));
+                    uint32_t m[NV];
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    for (int o = gv >> 1; o > 0; o >>= 1) m[v] = max(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
-            } else {  // NV == 1
-                const int first = (sub << lg) + j / gv * gv;
-                uint32_t all = 0;
-                for (int i = 0; i < gv; ++i) all = max(all, __shfl_sync(0xffffffffu, m[0], (first + i) & 31));
-                m[0] = all;
-            }
-            if (slot[k] < 0) continue;
-            const CacheRow cr = cache_row(a.cache, slot[k], hd[k]);
+                    for (int v = 0; v < NV; ++v) m[v] = raw_mag<T, VE>(raw[w][k][v]);
+                    if (whole) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int e = (j + 32 * v) * VE;
-                if (e >= a.d) continue;
-                const GroupQ q = group_q(m[v], kind);
-                if (e % group == 0) a.cache.scales[which][cr.scale + e / group] = q.scale;
-                store_codes<T, VE>(a.cache.codes[which] + cr.code, e, x[v], q, kind);
+                        for (int v = 1; v < NV; ++v) m[0] = mag_max<T>(m[0], m[v]);
+                        for (int o = 1 << cl.lg >> 1; o > 0; o >>= 1)
+                            m[0] = mag_max<T>(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+#pragma unroll
+                        for (int v = 1; v < NV; ++v) m[v] = m[0];
+                    } else if (pow2) {
+                        for (int o = gv >> 1; o > 0; o >>= 1)
+#pragma unroll
+                            for (int v = 0; v < NV; ++v)
+                                m[v] = mag_max<T>(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) {
+                            uint32_t all = 0;
+                            for (int i = 0; i < gv; ++i)
+                                all = mag_max<T>(all, __shfl_sync(0xffffffffu, m[v], (source + i) & 31));
+                            m[v] = all;
+                        }
+                    }
+                    if (!live || h >= heads) continue;
+                    uint8_t* codes = a.cache.codes[w] + cr.code + h * a.cache.head_stride;
+                    float* scales = a.cache.scales[w] + cr.scale + h * a.cache.scale_head_stride;
+                    GroupQ q;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        if (v == 0 || !whole) q = group_q(mag_bits<T>(m[v]), kind);
+                        if (leads[v]) scales[gi[v]] = q.scale;
+                        store_codes<T, VE>(codes, (j + v * cl.per) * VE, raw[w][k][v], q, kind);
+                    }
+                }
             }
         }
     }
@@ -678,81 +783,94 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* row, int e, int kind)
     }
     return w;
 }
-// The numbers they are.  A whole number goes to float32 by way of its bits: with
-// its sign bit flipped it is the low end of the mantissa of 2^23 + code + half.
+// The values they stand for, code * scale.  A whole number goes to float32 by way
+// of its bits: with its sign bit flipped it takes a place in the mantissa of 2^23,
+// where it reads 2^23 + (code + half) * 16^i; the power goes into the scale.
 template <int VE>
-__device__ __forceinline__ void code_values(uint2 w, int kind, float (&v)[VE]) {
+__device__ __forceinline__ void code_values(uint2 w, int kind, float scale, float2 (&v)[VE / 2]) {
     if (kind == NRM_CACHE_E4M3) {
 #pragma unroll
-        for (int i = 0; i < VE; i += 2) {
-            const float2 f = e4m3x2_values((i < 4 ? w.x : w.y) >> (8 * (i % 4)));
-            v[i] = f.x;
-            v[i + 1] = f.y;
-        }
+        for (int i = 0; i < VE / 2; ++i)
+            v[i] = __fmul2_rn(e4m3x2_values((i < 2 ? w.x : w.y) >> (16 * (i % 2))), f2(scale));
     } else if (kind == NRM_CACHE_INT8) {
         const uint32_t x = w.x ^ 0x80808080u, y = w.y ^ 0x80808080u;
 #pragma unroll
-        for (int i = 0; i < VE; ++i)
-            v[i] = __uint_as_float(__byte_perm(i < 4 ? x : y, 0x4B000000u, 0x7650 + i % 4)) - 8388736.f;
+        for (int i = 0; i < VE; i += 2) {
+            const float2 f = make_float2(__uint_as_float(__byte_perm(i < 4 ? x : y, 0x4B000000u, 0x7650 + i % 4)),
+                                         __uint_as_float(__byte_perm(i < 4 ? x : y, 0x4B000000u, 0x7651 + i % 4)));
+            v[i / 2] = __fmul2_rn(__fadd2_rn(f, f2(-8388736.f)), f2(scale));  // - (2^23 + 128)
+        }
     } else {
         const uint32_t x = w.x ^ 0x88888888u;
+        const float2 down[2] = {make_float2(scale, scale * 0x1p-4f), make_float2(scale * 0x1p-8f, scale * 0x1p-12f)};
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[i] = __uint_as_float((x >> (4 * i) & 0xfu) | 0x4B000000u) - 8388616.f;
+        for (int i = 0; i < VE; i += 2) {
+            const uint32_t y = i < 4 ? x : x >> 16;
+            const int p = 4 * (i % 4);
+            const float2 f = make_float2(__uint_as_float((y & (0xfu << p)) | 0x4B000000u),
+                                         __uint_as_float((y & (0xf0u << p)) | 0x4B000000u));
+            const float2 off = i % 4 ? make_float2(-8390656.f, -8421376.f)   // - (2^23 + 8 * 16^2), 16^3
+                                     : make_float2(-8388616.f, -8388736.f);  // - (2^23 + 8), 16
+            v[i / 2] = __fmul2_rn(__fadd2_rn(f, off), down[i % 4 / 2]);
+        }
     }
 }
 
-template <typename T, int VE, int NV>
+template <typename T, int VE>
 __global__ void __launch_bounds__(kHeadWarps * 32)
-cache_read_vec_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads, int lg) {
+cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
+    constexpr int NV = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane >> lg, j = lane & ((1 << lg) - 1), rows = 32 >> lg;
-    const int which = a.y[0].p ? int(blockIdx.y) : 1;
-    const HeadView yv = a.y[which];
-    const int64_t n = a.tokens * by_heads.d;
-    const int group = a.cache.group, kind = a.cache.kind;
-    const int64_t step = int64_t(rows) * kCacheRows;
-    for (int64_t base = (int64_t(blockIdx.x) * kHeadWarps + warp) * step; base < n;
-         base += int64_t(gridDim.x) * kHeadWarps * step) {
-        int64_t tok[kCacheRows], slot[kCacheRows];
-        int hd[kCacheRows];
+    const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp;
+    const bool on = j < cl.per;
+    const int heads = a.heads[1], kind = a.cache.kind;
+    const int ltok = 5 - cl.lg - cl.lhp;  // tokens of a warp
+    int gi[NV];
 #pragma unroll
-        for (int k = 0; k < kCacheRows; ++k) {
-            const int64_t i = base + k * rows + sub;
-            slot[k] = -1;
-            if (i < n) {
-                tok[k] = row_div(i, by_heads);
-                hd[k] = int(i - tok[k] * by_heads.d);
-                slot[k] = __ldg(a.slots + tok[k]);
+    for (int v = 0; v < NV; ++v) gi[v] = (j + v * cl.per) * VE / a.cache.group;
+    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk;
+    for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
+        const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
+        int64_t slot = -1;
+        if (t < a.tokens) slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
+        if (slot < 0 || !on) continue;
+        const CacheRow cr = cache_row(a.cache, slot, 0);
+#pragma unroll 1
+        for (int h0 = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads) + (sub & (hp - 1)); h0 < heads;
+             h0 += (hp * kCacheHeads) << cl.lchunk) {
+            uint2 w[2][kCacheHeads][NV];
+            float sc[2][kCacheHeads][NV];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!a.y[i].p) continue;
+#pragma unroll
+                for (int k = 0; k < kCacheHeads; ++k) {
+                    const int h = h0 + k * hp;
+                    if (h >= heads) continue;
+                    const uint8_t* codes = a.cache.codes[i] + cr.code + h * a.cache.head_stride;
+                    const float* scales = a.cache.scales[i] + cr.scale + h * a.cache.scale_head_stride;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        w[i][k][v] = load_codes<VE>(codes, (j + v * cl.per) * VE, kind);
+                        sc[i][k][v] = __ldg(scales + gi[v]);
+                    }
+                }
             }
-        }
-        uint2 w[kCacheRows][NV];
-        float sc[kCacheRows][NV];
 #pragma unroll
-        for (int k = 0; k < kCacheRows; ++k) {
-            slot[k] = cache_slot(a.cache, slot[k], a.err);
-            if (slot[k] < 0) continue;
-            const CacheRow cr = cache_row(a.cache, slot[k], hd[k]);
+            for (int i = 0; i < 2; ++i) {
+                if (!a.y[i].p) continue;
+                T* y = reinterpret_cast<T*>(a.y[i].p) + t * a.y[i].ts + j * VE;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int e = (j + 32 * v) * VE;
-                if (e >= a.d) continue;
-                w[k][v] = load_codes<VE>(a.cache.codes[which] + cr.code, e, kind);
-                sc[k][v] = __ldg(a.cache.scales[which] + cr.scale + e / group);
-            }
-        }
+                for (int k = 0; k < kCacheHeads; ++k) {
+                    const int h = h0 + k * hp;
+                    if (h >= heads) continue;
 #pragma unroll
-        for (int k = 0; k < kCacheRows; ++k) {
-            if (slot[k] < 0) continue;
-            T* y = reinterpret_cast<T*>(yv.p) + tok[k] * yv.ts + hd[k] * yv.hs;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int e = (j + 32 * v) * VE;
-                if (e >= a.d) continue;
-                float x[VE];
-                code_values<VE>(w[k][v], kind, x);
-#pragma unroll
-                for (int i = 0; i < VE; ++i) x[i] *= sc[k][v];
-                st_row(y + e, raw_pack<T, VE>(x));
+                    for (int v = 0; v < NV; ++v) {
+                        float2 x[VE / 2];
+                        code_values<VE>(w[i][k][v], kind, sc[i][k][v], x);
+                        st_row(y + h * a.y[i].hs + v * cl.per * VE, raw_pack<T, VE>(x));
+                    }
+                }
             }
         }
     }
@@ -996,7 +1114,7 @@ head_dw_kernel(const float* __restrict__ ws, int d, int nq, int nk, T* dwq, T* d
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kHeadWarps * 32)
-cache_write_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads, int) {
+cache_write_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads) {
     __shared__ float stage[kHeadWarps][kHeadMaxD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int which = a.x[1].p ? int(blockIdx.y) : 1;
@@ -1019,7 +1137,7 @@ cache_write_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads, i
 
 template <typename T>
 __global__ void __launch_bounds__(kHeadWarps * 32)
-cache_read_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads, int) {
+cache_read_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int which = a.y[0].p ? int(blockIdx.y) : 1;
     const HeadView yv = a.y[which];
@@ -1072,8 +1190,10 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
     const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head forward kernel cannot be resident");
     int lg = row_lanes_log2(a.d / (2 * VE));
-    const int heads = a.heads[0] + a.heads[1] + (cache ? a.heads[2] : 0), per = (32 >> lg) * kHeadRows;
-    int lc = head_chunks_log2(a.tokens, (heads + per - 1) / per, d);
+    const int per = (32 >> lg) * kHeadRows;
+    int steps = 0;
+    for (int i = 0; i < (cache ? 3 : 2); ++i) steps += (a.heads[i] + per - 1) / per;
+    int lc = head_chunks_log2(a.tokens, steps, d);
     int64_t ctas = ((a.tokens << lc) + kHeadWarps - 1) / kHeadWarps;
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
@@ -1161,33 +1281,50 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
                       sargs, s);
 }
 
-// Launches a cache kernel over tokens * heads rows, `both`: of keys and of values.
-inline nrm_status cache_launch(const HeadArgs& a, const void* fn, int rows_per_warp, int lg, bool both,
-                               const DevInfo& d, cudaStream_t s) {
+// A row to each warp: any layout.
+template <typename T>
+nrm_status cache_launch_scalar(const HeadArgs& a, const void* fn, bool both, const DevInfo& d, cudaStream_t s) {
     const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "cache kernel cannot be resident");
-    const int64_t rows = a.tokens * a.heads[1], per = int64_t(rows_per_warp) * kHeadWarps;
-    int64_t ctas = (rows + per - 1) / per;
-    const int64_t cap = int64_t(occ) * d.sms;
-    if (ctas > cap) ctas = cap;
+    const int64_t rows = a.tokens * a.heads[1];
+    int64_t ctas = (rows + kHeadWarps - 1) / kHeadWarps;
+    if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
-    args.err = d.err;
     RowDiv by_heads = make_row_div(a.heads[1], rows);
-    void* kargs[] = {&args, &by_heads, &lg};
+    void* kargs[] = {&args, &by_heads};
     return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas), both ? 2 : 1), dim3(kHeadWarps * 32), kargs, 0, s),
                        "cache launch");
 }
 
-// The vector kernel of a row of d elements: one vector to a lane, or two where a
-// warp cannot hold the row else.  Two need groups that stay within 32 vectors.
-template <typename T, typename F>
-nrm_status cache_rows(const HeadArgs& a, int vec, F&& launch) {
-    const int ve = vec / int(sizeof(T)), gv = ve ? a.cache.group / ve : 0;
-    if (vec == 16 && a.d <= 32 * ve) return launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    if (vec == 8 && a.d <= 32 * ve) return launch(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-    if (vec == 16 && (a.cache.group == a.d || (gv & (gv - 1)) == 0))
-        return launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-    return launch(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+// `lanes` lanes of a row hold vectors.
+inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes, const DevInfo& d, cudaStream_t s) {
+    const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
+    if (occ <= 0) return fail(NRM_ERR_CUDA, "cache kernel cannot be resident");
+    CacheLanes cl{};
+    cl.lg = row_lanes_log2(lanes);
+    cl.per = lanes;
+    while (cl.lhp < 5 - cl.lg && (1 << cl.lhp) < a.heads[1]) ++cl.lhp;
+    const int ltok = 5 - cl.lg - cl.lhp, per = kCacheHeads << cl.lhp;
+    const int64_t blocks = (a.tokens + (1 << ltok) - 1) >> ltok;
+    cl.lchunk = head_chunks_log2(blocks, (a.heads[1] + per - 1) / per, d);
+    int64_t ctas = ((blocks << cl.lchunk) + kHeadWarps - 1) / kHeadWarps;
+    if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
+    HeadArgs args = a;
+    void* kargs[] = {&args, &cl};
+    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, 0, s), "cache launch");
+}
+
+// Two vectors of a row to a lane, where every group lies within the first ones,
+// within the second ones, or is the row (its magnitudes then meet by shuffles);
+// else one, where a warp holds the row.
+template <typename T, int BYTES>
+nrm_status cache_write_vec(const HeadArgs& a, const DevInfo& d, cudaStream_t s) {
+    constexpr int VE = BYTES / int(sizeof(T));
+    const int half = a.d / (2 * VE);
+    if (a.cache.group == a.d || half % (a.cache.group / VE) == 0)
+        return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 2>, half, d, s);
+    if (2 * half <= 32) return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 1>, 2 * half, d, s);
+    return cache_launch_scalar<T>(a, (const void*)&cache_write_scalar_kernel<T>, a.x[1].p && a.x[2].p, d, s);
 }
 
 template <typename T>
@@ -1195,17 +1332,11 @@ nrm_status cache_write(const HeadArgs& a, int vec, cudaStream_t s) {
     const DevInfo* d = dev_info();
     if (!d) return fail(NRM_ERR_CUDA, "no usable CUDA device");
     if (a.tokens == 0) return NRM_OK;
-    const bool both = a.x[1].p && a.x[2].p;
-    return cache_rows<T>(a, vec, [&](auto bytes, auto nv) {
-        if constexpr (bytes.value == 0) {
-            return cache_launch(a, (const void*)&cache_write_scalar_kernel<T>, 1, 5, both, *d, s);
-        } else {
-            constexpr int VE = bytes.value / int(sizeof(T));
-            const int lg = row_lanes_log2(a.d / VE);
-            return cache_launch(a, (const void*)&cache_write_vec_kernel<T, VE, nv.value>, (32 >> lg) * kCacheRows, lg,
-                                both, *d, s);
-        }
-    });
+    HeadArgs args = a;
+    args.err = d->err;
+    if (vec == 16) return cache_write_vec<T, 16>(args, *d, s);
+    if (vec == 8) return cache_write_vec<T, 8>(args, *d, s);
+    return cache_launch_scalar<T>(args, (const void*)&cache_write_scalar_kernel<T>, a.x[1].p && a.x[2].p, *d, s);
 }
 
 template <typename T>
@@ -1213,17 +1344,15 @@ nrm_status cache_read(const HeadArgs& a, int vec, cudaStream_t s) {
     const DevInfo* d = dev_info();
     if (!d) return fail(NRM_ERR_CUDA, "no usable CUDA device");
     if (a.tokens == 0) return NRM_OK;
-    const bool both = a.y[0].p && a.y[1].p;
-    return cache_rows<T>(a, vec, [&](auto bytes, auto nv) {
-        if constexpr (bytes.value == 0) {
-            return cache_launch(a, (const void*)&cache_read_scalar_kernel<T>, 1, 5, both, *d, s);
-        } else {
-            constexpr int VE = bytes.value / int(sizeof(T));
-            const int lg = row_lanes_log2(a.d / VE);
-            return cache_launch(a, (const void*)&cache_read_vec_kernel<T, VE, nv.value>, (32 >> lg) * kCacheRows, lg,
-                                both, *d, s);
-        }
-    });
+    HeadArgs args = a;
+    args.err = d->err;
+    if (vec) {
+        const int ve = vec / int(sizeof(T));
+        return cache_launch_vec(args, vec == 16 ? (const void*)&cache_read_vec_kernel<T, 16 / int(sizeof(T))>
+                                                : (const void*)&cache_read_vec_kernel<T, 8 / int(sizeof(T))>,
+                                a.d / (2 * ve), *d, s);
+    }
+    return cache_launch_scalar<T>(args, (const void*)&cache_read_scalar_kernel<T>, a.y[0].p && a.y[1].p, *d, s);
 }
 
 }  // namespace nrm
