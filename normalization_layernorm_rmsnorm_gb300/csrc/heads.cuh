@@ -356,15 +356,14 @@ struct WarpTurns {
             }
         }
     }
-    // cos[p], sin[p] of token t, for every pair.  Called by the whole warp.
-    __device__ __forceinline__ void make(const RopeDev& r, int lane, int64_t t, float* cos, float* sin) const {
+    // cos[p], sin[p] of a token at positions pos[axis], for every pair.  Called by the whole warp.
+    __device__ __forceinline__ void make(const RopeDev& r, int lane, const int64_t* pos, float* cos, float* sin) const {
         __syncwarp();
 #pragma unroll
         for (int s = 0; s < kHeadMaxPairs / 32; ++s) {
             const int p = lane + 32 * s;
             if (2 * p < r.rot) {
-                const int64_t pos = __ldg(r.pos + (axis >> (2 * s) & 3) * r.pos_stride + t);
-                const float2 cs = pair_turn(r, step[s], pos);
+                const float2 cs = pair_turn(r, step[s], pos[axis >> (2 * s) & 3]);
                 cos[p] = cs.x;
                 sin[p] = cs.y;
             }
@@ -401,168 +400,266 @@ __device__ __forceinline__ float row_sum(float v, int lg) {
 }
 
 // ---------------------------------------------------------------------------
+// asynchronous copies of a lane's own vectors
+// ---------------------------------------------------------------------------
+// A lane copies its vectors of the next steps to places in shared memory that no
+// other lane reads, kHeadStages - 1 steps ahead, so the bytes in flight do not
+// depend on registers or occupancy and no barrier is needed: the lane waits for
+// its own copies.
+constexpr int kHeadStages = 4;
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_addr(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(smem_addr(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of copies of this thread have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+// What a warp's lanes copy for a new token: its positions (one an axis), its cache slot.
+constexpr int kTokenSlot = kHeadMaxAxes;
+struct TokenWords {
+    int64_t w[kHeadMaxAxes + 1];
+};
+
+// ---------------------------------------------------------------------------
 // forward on vectors: norm, rotation, cache
 // ---------------------------------------------------------------------------
-constexpr int kHeadRows = 2;  // rows of a lane in flight
 
-// A warp takes (token, chunk) units; chunk c of 2^lchunk takes the token's row
-// steps c, c + 2^lchunk, ... (a step: kHeadRows * (32 >> lg) rows of one tensor).
+// A warp's way through its work: (token, chunk) units, of each the tensors q, k
+// (and v), of each the row steps chunk, chunk + 2^lchunk, ... of the token's
+// steps counted through all tensors.  A step is 32 >> lg rows.
+template <int TENSORS>
+struct StepWalk {
+    int64_t un;
+    int which, st, first;
+    bool fresh;  // the first step of a token
+    __device__ __forceinline__ void start(const HeadArgs& a, int64_t unit, int64_t units, int64_t stride, int lper,
+                                          int lchunk) {
+        un = unit;
+        enter(a, units, stride, lper, lchunk);
+    }
+    __device__ __forceinline__ bool live(int64_t units) const { return un < units; }
+    __device__ __forceinline__ void next(const HeadArgs& a, int64_t units, int64_t stride, int lper, int lchunk) {
+        fresh = false;
+        st += 1 << lchunk;
+        settle(a, units, stride, lper, lchunk);
+    }
+
+private:
+    __device__ __forceinline__ void enter(const HeadArgs& a, int64_t units, int64_t stride, int lper, int lchunk) {
+        which = first = 0;
+        st = int(un) & ((1 << lchunk) - 1);
+        fresh = true;
+        settle(a, units, stride, lper, lchunk);
+    }
+    __device__ __forceinline__ void settle(const HeadArgs& a, int64_t units, int64_t stride, int lper, int lchunk) {
+        while (un < units) {
+            const int steps = (a.heads[which] + (1 << lper) - 1) >> lper;
+            if (st < steps) return;
+            first += steps;
+            const int mask = (1 << lchunk) - 1;
+            if (++which == TENSORS) {
+                un += stride;
+                which = first = 0;
+                fresh = true;
+            }
+            st = (int(un) - first) & mask;
+        }
+    }
+};
+
+// Two vectors a step.
+template <typename T, int VE>
+constexpr size_t head_fwd_smem() {
+    return size_t(kHeadStages) * 2 * kHeadWarps * 32 * VE * sizeof(T);
+}
+
 template <typename T, int VE, bool NORM, bool CACHE>
-__global__ void __launch_bounds__(kHeadWarps * 32, CACHE ? 2 : 3)
+__global__ void __launch_bounds__(kHeadWarps * 32, 2)
 head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
-    constexpr int H = VE / 2;
+    constexpr int H = VE / 2, D = kHeadStages, TENSORS = CACHE ? 3 : 2, BYTES = VE * int(sizeof(T));
+    extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
+    __shared__ TokenWords s_tok[kHeadWarps][D];
     __shared__ uint32_t s_max[CACHE ? kHeadWarps : 1][CACHE ? 64 : 1];
+    Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][vector], blockDim.x apart
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const LaneAt<VE> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
-    const int rows = 32 >> lg, lper = 5 - lg + (kHeadRows == 2 ? 1 : 0);  // 2^lper rows a step
-    const int64_t units = a.tokens << lchunk;
+    const int lper = 5 - lg, b01 = at.b1 - at.b0;
+    const int64_t units = a.tokens << lchunk, stride = int64_t(gridDim.x) * kHeadWarps;
     const float inv_d = 1.f / float(a.d);
     const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
-    for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
-        const int64_t t = un >> lchunk;
-        const int chunk = int(un) & ((1 << lchunk) - 1);
-        const int64_t slot = CACHE ? cache_slot(a.cache, __ldg(a.slots + t), a.err) : -1;
-        turns.make(a.rope, lane, t, s_cos[warp], s_sin[warp]);
-        float2 c[H], s[H];
-        if (at.turns) {
+
+    StepWalk<TENSORS> in, cur;
+    in.start(a, int64_t(blockIdx.x) * kHeadWarps + warp, units, stride, lper, lchunk);
+    cur = in;
+    auto issue = [&](int stage) {
+        if (in.live(units)) {
+            const int64_t t = in.un >> lchunk;
+            const int h = (in.st << lper) + at.sub;
+            if (at.on && h < a.heads[in.which]) {
+                const HeadView v = a.x[in.which];
+                const T* p = reinterpret_cast<const T*>(v.p) + t * v.ts + h * v.hs + at.b0;
+                cp_async<BYTES>(ring + (2 * stage) * kHeadWarps * 32, p);
+                cp_async<BYTES>(ring + (2 * stage + 1) * kHeadWarps * 32, p + b01);
+            }
+            if (in.fresh) {
+                if (lane < a.rope.axes)
+                    cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
+                if (CACHE && lane == kTokenSlot) cp_async<8>(&s_tok[warp][stage].w[kTokenSlot], a.slots + t);
+            }
+            in.next(a, units, stride, lper, lchunk);
+        }
+        cp_async_commit();
+    };
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
-                s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
+    for (int i = 0; i < D - 1; ++i) issue(i);
+
+    float2 c[H], s[H], w0[H], w1[H];
+    int have = -1;  // the tensor whose weights are in registers
+    int64_t slot = -1;
+    for (int stage = 0; cur.live(units); stage = stage + 1 == D ? 0 : stage + 1) {
+        cp_async_wait<D - 2>();
+        const int64_t t = cur.un >> lchunk;
+        const int which = cur.which, heads = a.heads[which];
+        const int h = (cur.st << lper) + at.sub;
+        const bool row = h < heads, on = row && at.on;
+        Raw<T, VE> x0{}, x1{};
+        if (on) {
+            x0 = ring[(2 * stage) * kHeadWarps * 32];
+            x1 = ring[(2 * stage + 1) * kHeadWarps * 32];
+        }
+        if (cur.fresh) {
+            turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
+            if (at.turns) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
+                    s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
+                }
+            }
+            if (CACHE) slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
+            __syncwarp();
+        }
+        issue(stage == 0 ? D - 1 : stage - 1);
+        cur.next(a, units, stride, lper, lchunk);
+        if (which < 2) {
+            float2 u[H], v[H];
+            raw_unpack<T, VE>(x0, u);
+            raw_unpack<T, VE>(x1, v);
+            if (NORM) {
+                if (which != have) {
+                    have = which;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) w0[i] = w1[i] = f2(1.f);
+                    const T* w = reinterpret_cast<const T*>(a.w[which]);
+                    if (w && at.on) {
+                        raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
+                        raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
+                    }
+                }
+                float2 sq = f2(0.f);
+#pragma unroll
+                for (int i = 0; i < H; ++i) sq = __ffma2_rn(u[i], u[i], __ffma2_rn(v[i], v[i], sq));
+                const float r = rsqrtf(fmaf(row_sum(sq.x + sq.y, lg), inv_d, a.eps));
+                float* rstd = a.rstd[which];
+                if (rstd && row && at.j == 0) rstd[t * heads + h] = r;
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    u[i] = __fmul2_rn(__fmul2_rn(u[i], f2(r)), w0[i]);
+                    v[i] = __fmul2_rn(__fmul2_rn(v[i], f2(r)), w1[i]);
+                }
+            }
+            if (at.turns) turn_vecs<VE>(u, v, c, s, a.rope.adjacent);
+            x0 = raw_pack<T, VE>(u);
+            x1 = raw_pack<T, VE>(v);
+            const HeadView yv = a.y[which];
+            if (on && yv.p) {
+                T* p = reinterpret_cast<T*>(yv.p) + t * yv.ts + h * yv.hs + at.b0;
+                st_row(p, x0);
+                st_row(p + b01, x1);
             }
         }
-        int first = 0;  // the tensor's first step
-#pragma unroll 1
-        for (int which = 0; which < (CACHE ? 3 : 2); ++which) {
-            const int heads = a.heads[which], steps = (heads + (1 << lper) - 1) >> lper;
-            int st = (chunk - first) & ((1 << lchunk) - 1);
-            first += steps;
-            if (st >= steps) continue;
-            const HeadView xv = a.x[which], yv = which < 2 ? a.y[which] : HeadView{};
-            const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + at.b0;
-            T* y = reinterpret_cast<T*>(yv.p) + t * yv.ts + at.b0;
-            const int b01 = at.b1 - at.b0;
-            float2 w0[H], w1[H];
-            if (NORM && which < 2) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) w0[i] = w1[i] = f2(1.f);
-                const T* w = reinterpret_cast<const T*>(a.w[which]);
-                if (w && at.on) {
-                    raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
-                    raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
+        if constexpr (CACHE) {
+            // (both conditions are the warp's.)  The cache stores the key in the activations'
+            // type: what a separate write would read.
+            if (which == 0 || slot < 0) continue;
+            uint32_t m0 = raw_mag<T, VE>(x0), m1 = raw_mag<T, VE>(x1);
+            const int group = a.cache.group;
+            if (group == a.d) {
+                m0 = mag_max<T>(m0, m1);
+                if (!at.on) m0 = 0;
+                for (int o = 1 << lg >> 1; o > 0; o >>= 1) m0 = mag_max<T>(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                m1 = m0;
+            } else {
+                // groups of whole vectors, which other lanes may hold: through shared memory
+                uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
+                const int n = group / VE;
+                if (at.on) {
+                    sm[at.b0 / VE] = m0;
+                    sm[at.b1 / VE] = m1;
                 }
+                __syncwarp();
+                if (at.on) {
+                    for (int i = 0; i < n; ++i) {
+                        m0 = mag_max<T>(m0, sm[g0 * n + i]);
+                        m1 = mag_max<T>(m1, sm[g1 * n + i]);
+                    }
+                }
+                __syncwarp();
             }
-            float* rstd = NORM && which < 2 ? a.rstd[which] : nullptr;
-#pragma unroll 1
-            for (; st < steps; st += 1 << lchunk) {
-                Raw<T, VE> x0[kHeadRows], x1[kHeadRows];
-                const int h0 = (st << lper) + at.sub;
-#pragma unroll
-                for (int k = 0; k < kHeadRows; ++k) {
-                    const int h = h0 + k * rows;
-                    x0[k] = x1[k] = Raw<T, VE>{};
-                    if (h < heads && at.on) {
-                        const T* p = x + h * xv.hs;
-                        ld_row(p, x0[k]);
-                        ld_row(p + b01, x1[k]);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kHeadRows; ++k) {
-                    const int h = h0 + k * rows;
-                    const bool row = h < heads;
-                    if (which < 2) {
-                        float2 u[H], v[H];
-                        raw_unpack<T, VE>(x0[k], u);
-                        raw_unpack<T, VE>(x1[k], v);
-                        if (NORM) {
-                            float2 sq = f2(0.f);
-#pragma unroll
-                            for (int i = 0; i < H; ++i) sq = __ffma2_rn(u[i], u[i], __ffma2_rn(v[i], v[i], sq));
-                            const float r = rsqrtf(fmaf(row_sum(sq.x + sq.y, lg), inv_d, a.eps));
-                            if (rstd && row && at.j == 0) rstd[t * heads + h] = r;
-#pragma unroll
-                            for (int i = 0; i < H; ++i) {
-                                u[i] = __fmul2_rn(__fmul2_rn(u[i], f2(r)), w0[i]);
-                                v[i] = __fmul2_rn(__fmul2_rn(v[i], f2(r)), w1[i]);
-                            }
-                        }
-                        if (at.turns) turn_vecs<VE>(u, v, c, s, a.rope.adjacent);
-                        x0[k] = raw_pack<T, VE>(u);
-                        x1[k] = raw_pack<T, VE>(v);
-                        if (row && at.on && yv.p) {
-                            T* p = y + h * yv.hs;
-                            st_row(p, x0[k]);
-                            st_row(p + b01, x1[k]);
-                        }
-                    }
-                    if constexpr (CACHE) {
-                        // (both conditions are the warp's.)  The cache stores the key in the activations'
-                        // type: what a separate write would read.
-                        if (which == 0 || slot < 0) continue;
-                        uint32_t m0 = raw_mag<T, VE>(x0[k]), m1 = raw_mag<T, VE>(x1[k]);
-                        const int group = a.cache.group;
-                        if (group == a.d) {
-                            m0 = mag_max<T>(m0, m1);
-                            if (!at.on) m0 = 0;
-                            for (int o = 1 << lg >> 1; o > 0; o >>= 1)
-                                m0 = mag_max<T>(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                            m1 = m0;
-                        } else {
-                            // groups of whole vectors, which other lanes may hold: through shared memory
-                            uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
-                            const int n = group / VE;
-                            if (at.on) {
-                                sm[at.b0 / VE] = m0;
-                                sm[at.b1 / VE] = m1;
-                            }
-                            __syncwarp();
-                            if (at.on) {
-                                for (int i = 0; i < n; ++i) {
-                                    m0 = mag_max<T>(m0, sm[g0 * n + i]);
-                                    m1 = mag_max<T>(m1, sm[g1 * n + i]);
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        if (row && at.on) {
-                            const CacheRow cr = cache_row(a.cache, slot, h);
-                            const GroupQ q0 = group_q(mag_bits<T>(m0), a.cache.kind);
-                            const GroupQ q1 = group_q(mag_bits<T>(m1), a.cache.kind);
-                            float* scales = a.cache.scales[which - 1] + cr.scale;
-                            if (at.b0 == g0 * group) scales[g0] = q0.scale;
-                            if (at.b1 == g1 * group) scales[g1] = q1.scale;
-                            uint8_t* codes = a.cache.codes[which - 1] + cr.code;
-                            store_codes<T, VE>(codes, at.b0, x0[k], q0, a.cache.kind);
-                            store_codes<T, VE>(codes, at.b1, x1[k], q1, a.cache.kind);
-                        }
-                    }
-                }
+            if (on) {
+                const CacheRow cr = cache_row(a.cache, slot, h);
+                const GroupQ q0 = group_q(mag_bits<T>(m0), a.cache.kind);
+                const GroupQ q1 = group_q(mag_bits<T>(m1), a.cache.kind);
+                float* scales = a.cache.scales[which - 1] + cr.scale;
+                if (at.b0 == g0 * group) scales[g0] = q0.scale;
+                if (at.b1 == g1 * group) scales[g1] = q1.scale;
+                uint8_t* codes = a.cache.codes[which - 1] + cr.code;
+                store_codes<T, VE>(codes, at.b0, x0, q0, a.cache.kind);
+                store_codes<T, VE>(codes, at.b1, x1, q1, a.cache.kind);
             }
         }
     }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
 // backward on vectors
 // ---------------------------------------------------------------------------
+// A lane's copies of a step: two vectors each of dy and x, and the row's r.
 template <typename T, int VE>
-__global__ void __launch_bounds__(kHeadWarps * 32)
+constexpr size_t head_bwd_smem() {
+    return size_t(kHeadStages) * kHeadWarps * 32 * (4 * VE * sizeof(T) + 4);
+}
+
+template <typename T, int VE>
+__global__ void __launch_bounds__(kHeadWarps * 32, 2)
 head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int nq) {
-    constexpr int H = VE / 2;
+    constexpr int H = VE / 2, D = kHeadStages, BYTES = VE * int(sizeof(T)), N = kHeadWarps * 32;
+    extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
     __shared__ __align__(16) float part[kHeadWarps][kHeadMaxD];
+    __shared__ TokenWords s_tok[kHeadWarps][D];
+    Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][vector], N apart
+    float* ring_r = reinterpret_cast<float*>(dyn + size_t(D) * 4 * N * BYTES) + threadIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int which = int(blockIdx.x) < nq ? 0 : 1;
     const int cta = int(blockIdx.x) - (which ? nq : 0);
     const int ctas = which ? int(gridDim.x) - nq : nq;
     const LaneAt<VE> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
-    const int rows = 32 >> lg;
-    const int heads = a.heads[which];
-    const int64_t units = a.tokens << lchunk;
+    const int heads = a.heads[which], mask = (1 << lchunk) - 1;
+    const int hstep = (32 >> lg) << lchunk;  // heads from one of a unit's steps to its next
+    const int64_t units = a.tokens << lchunk, stride = int64_t(ctas) * kHeadWarps;
     const float inv_d = 1.f / float(a.d);
     const HeadView xv = a.x[which], gv = a.dy[which], dv = a.y[which];
     const int b01 = at.b1 - at.b0;
@@ -577,67 +674,103 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
         raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
         raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
     }
-    for (int64_t un = int64_t(cta) * kHeadWarps + warp; un < units; un += int64_t(ctas) * kHeadWarps) {
-        const int64_t t = un >> lchunk;
-        turns.make(a.rope, lane, t, s_cos[warp], s_sin[warp]);
-        float2 c[H], s[H];
-        if (at.turns) {
+    // the first head of unit un's first step; a unit without one is passed over
+    auto first_head = [&](int64_t un) { return (int(un) & mask) << (5 - lg); };
+    auto pass = [&](int64_t& un, int& h0) {
+        while (un < units && h0 >= heads) {
+            un += stride;
+            h0 = first_head(un);
+        }
+    };
+    int64_t in_un = int64_t(cta) * kHeadWarps + warp;
+    int in_h = first_head(in_un);
+    pass(in_un, in_h);
+    int64_t un = in_un;
+    int h0 = in_h;
+    auto issue = [&](int stage) {
+        if (in_un < units) {
+            const int64_t t = in_un >> lchunk;
+            const int h = in_h + at.sub;
+            if (at.on && h < heads) {
+                const T* pg = reinterpret_cast<const T*>(gv.p) + t * gv.ts + h * gv.hs + at.b0;
+                const T* px = reinterpret_cast<const T*>(xv.p) + t * xv.ts + h * xv.hs + at.b0;
+                Raw<T, VE>* to = ring + stage * 4 * N;
+                cp_async<BYTES>(to, pg);
+                cp_async<BYTES>(to + N, pg + b01);
+                cp_async<BYTES>(to + 2 * N, px);
+                cp_async<BYTES>(to + 3 * N, px + b01);
+                cp_async<4>(ring_r + stage * N, a.rstd[which] + t * heads + h);
+            }
+            if (in_h == first_head(in_un) && lane < a.rope.axes)
+                cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
+            in_h += hstep;
+            pass(in_un, in_h);
+        }
+        cp_async_commit();
+    };
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
-                s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
+    for (int i = 0; i < D - 1; ++i) issue(i);
+
+    float2 c[H], s[H];
+    for (int stage = 0; un < units; stage = stage + 1 == D ? 0 : stage + 1) {
+        cp_async_wait<D - 2>();
+        const int64_t t = un >> lchunk;
+        const int h = h0 + at.sub;
+        const bool on = h < heads && at.on;
+        Raw<T, VE> x0{}, x1{}, y0{}, y1{};
+        float r = 0.f;
+        if (on) {
+            const Raw<T, VE>* from = ring + stage * 4 * N;
+            y0 = from[0];
+            y1 = from[N];
+            x0 = from[2 * N];
+            x1 = from[3 * N];
+            r = ring_r[stage * N];
+        }
+        if (h0 == first_head(un)) {
+            turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
+            if (at.turns) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
+                    s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
+                }
             }
         }
-        const T* g = reinterpret_cast<const T*>(gv.p) + t * gv.ts + at.b0;
-        const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + at.b0;
-        T* dx = reinterpret_cast<T*>(dv.p) + t * dv.ts + at.b0;
-        const float* rstd = a.rstd[which] + t * heads;
-#pragma unroll 1
-        for (int h0 = (int(un) & ((1 << lchunk) - 1)) * rows; h0 < heads; h0 += rows << lchunk) {
-            const int h = h0 + at.sub;
-            const bool on = h < heads && at.on;
-            Raw<T, VE> x0{}, x1{}, y0{}, y1{};
-            float r = 0.f;
-            if (on) {
-                const T* pg = g + h * gv.hs;
-                const T* px = x + h * xv.hs;
-                ld_row(pg, y0);
-                ld_row(pg + b01, y1);
-                ld_row(px, x0);
-                ld_row(px + b01, x1);
-                r = __ldg(rstd + h);
-            }
-            float2 u[H], v[H], gu[H], gw[H];
-            raw_unpack<T, VE>(y0, gu);
-            raw_unpack<T, VE>(y1, gw);
-            if (at.turns) turn_vecs<VE>(gu, gw, c, s, a.rope.adjacent);
-            raw_unpack<T, VE>(x0, u);
-            raw_unpack<T, VE>(x1, v);
-            float2 sum = f2(0.f);
+        issue(stage == 0 ? D - 1 : stage - 1);
+        h0 += hstep;
+        pass(un, h0);
+        float2 u[H], v[H], gu[H], gw[H];
+        raw_unpack<T, VE>(y0, gu);
+        raw_unpack<T, VE>(y1, gw);
+        if (at.turns) turn_vecs<VE>(gu, gw, c, s, a.rope.adjacent);
+        raw_unpack<T, VE>(x0, u);
+        raw_unpack<T, VE>(x1, v);
+        float2 sum = f2(0.f);
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                gu[i] = __fmul2_rn(gu[i], f2(r));
-                gw[i] = __fmul2_rn(gw[i], f2(r));
-                acc0[i] = __ffma2_rn(gu[i], u[i], acc0[i]);
-                acc1[i] = __ffma2_rn(gw[i], v[i], acc1[i]);
-                gu[i] = __fmul2_rn(gu[i], w0[i]);
-                gw[i] = __fmul2_rn(gw[i], w1[i]);
-                sum = __ffma2_rn(gu[i], u[i], __ffma2_rn(gw[i], v[i], sum));
-            }
-            // dx = r g - x r^2 sum(r g x) / d, the terms r g at hand
-            const float f = -(row_sum(sum.x + sum.y, lg) * inv_d * r * r);
+        for (int i = 0; i < H; ++i) {
+            gu[i] = __fmul2_rn(gu[i], f2(r));
+            gw[i] = __fmul2_rn(gw[i], f2(r));
+            acc0[i] = __ffma2_rn(gu[i], u[i], acc0[i]);
+            acc1[i] = __ffma2_rn(gw[i], v[i], acc1[i]);
+            gu[i] = __fmul2_rn(gu[i], w0[i]);
+            gw[i] = __fmul2_rn(gw[i], w1[i]);
+            sum = __ffma2_rn(gu[i], u[i], __ffma2_rn(gw[i], v[i], sum));
+        }
+        // dx = r g - x r^2 sum(r g x) / d, the terms r g at hand
+        const float f = -(row_sum(sum.x + sum.y, lg) * inv_d * r * r);
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                gu[i] = __ffma2_rn(u[i], f2(f), gu[i]);
-                gw[i] = __ffma2_rn(v[i], f2(f), gw[i]);
-            }
-            if (on) {
-                T* o = dx + h * dv.hs;
-                st_row(o, raw_pack<T, VE>(gu));
-                st_row(o + b01, raw_pack<T, VE>(gw));
-            }
+        for (int i = 0; i < H; ++i) {
+            gu[i] = __ffma2_rn(u[i], f2(f), gu[i]);
+            gw[i] = __ffma2_rn(v[i], f2(f), gw[i]);
+        }
+        if (on) {
+            T* o = reinterpret_cast<T*>(dv.p) + t * dv.ts + h * dv.hs + at.b0;
+            st_row(o, raw_pack<T, VE>(gu));
+            st_row(o + b01, raw_pack<T, VE>(gw));
         }
     }
+    cp_async_wait<0>();
     if (a.ws == nullptr) return;
     // the warp's rows, then the CTA's warps, in a fixed order
 #pragma unroll
@@ -654,7 +787,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.d; i += kHeadWarps * 32) {
+    for (int i = threadIdx.x; i < a.d; i += N) {
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kHeadWarps; ++w) sum += part[w][i];
@@ -1187,10 +1320,12 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
                                    : (const void*)&head_fwd_vec_kernel<T, VE, true, false>)
                           : (cache ? (const void*)&head_fwd_vec_kernel<T, VE, false, true>
                                    : (const void*)&head_fwd_vec_kernel<T, VE, false, false>);
-    const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
+    const size_t smem = head_fwd_smem<T, VE>();
+    if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
+    const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head forward kernel cannot be resident");
     int lg = row_lanes_log2(a.d / (2 * VE));
-    const int per = (32 >> lg) * kHeadRows;
+    const int per = 32 >> lg;
     int steps = 0;
     for (int i = 0; i < (cache ? 3 : 2); ++i) steps += (a.heads[i] + per - 1) / per;
     int lc = head_chunks_log2(a.tokens, steps, d);
@@ -1198,9 +1333,10 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
     void* kargs[] = {&args, &lg, &lc};
-    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, 0, s),
+    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, smem, s),
                        "head forward launch");
 }
+
 template <typename T>
 nrm_status head_fwd_scalar(const HeadArgs& a, bool norm, bool cache, const DevInfo& d, cudaStream_t s) {
     const void* fn = norm ? (cache ? (const void*)&head_fwd_scalar_kernel<T, true, true>
@@ -1248,7 +1384,12 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
     const void* fn = vec == 16  ? (const void*)&head_bwd_vec_kernel<T, 16 / int(sizeof(T))>
                      : vec == 8 ? (const void*)&head_bwd_vec_kernel<T, 8 / int(sizeof(T))>
                                 : (const void*)&head_bwd_scalar_kernel<T>;
-    const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
+    const size_t smem = vec == 16  ? head_bwd_smem<T, 16 / int(sizeof(T))>()
+                        : vec == 8 ? head_bwd_smem<T, 8 / int(sizeof(T))>()
+                                   : 0;
+    if (smem)
+        if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
+    const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head backward kernel cannot be resident");
     int lg = vec ? row_lanes_log2(a.d * int(sizeof(T)) / (2 * vec)) : 5;
     const int per = vec ? 32 >> lg : kHeadWarps;
@@ -1269,7 +1410,7 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
     void* kargs_vec[] = {&args, &lg, &lc, &nq};
     void* kargs[] = {&args, &nq};
     nrm_status st = cuda_status(cudaLaunchKernel(fn, dim3(unsigned(nq + nk)), dim3(kHeadWarps * 32),
-                                                 vec ? kargs_vec : kargs, 0, s),
+                                                 vec ? kargs_vec : kargs, smem, s),
                                 "head backward launch");
     if (st != NRM_OK || a.ws == nullptr) return st;
     const float* ws = a.ws;
