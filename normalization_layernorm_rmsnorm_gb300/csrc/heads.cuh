@@ -54,8 +54,7 @@ __device__ __forceinline__ float2 pair_turn(const RopeDev& r, uint64_t step, int
     return make_float2(c, r.inverse ? -s : s);
 }
 
-// (u, v) turned by (cos, sin); the products' roundings are spelt out so that
-// every kernel that turns the same pair gets the same bits.
+// (u, v) turned by (cos, sin).
 __device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
     const float a = fmaf(u, cs.x, -__fmul_rn(v, cs.y));
     const float b = fmaf(v, cs.x, __fmul_rn(u, cs.y));
@@ -77,9 +76,21 @@ __device__ __forceinline__ float cache_qmax(int kind) {
 // representable.
 struct GroupQ {
     float scale;
-    float m, r;  // the scaled largest magnitude and its reciprocal; both 0 where every code is 0
+    float n, r;  // minus the scaled largest magnitude, and about its reciprocal; both 0 where every code is 0
     float q;     // the form's largest number, scaled like m
 };
+// m/q rounded to nearest, for the forms' q: Markstein's division by a known number
+// (checked against the division for every mantissa).
+__device__ __forceinline__ float over_qmax(float m, float q) {
+    const float r = q == 448.f ? 1.f / 448.f : (q == 127.f ? 1.f / 127.f : 1.f / 7.f);
+    const float s = __fmul_rn(m, r);
+    return fmaf(fmaf(-s, q, m), r, s);
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ GroupQ group_q(uint32_t m_bits, int kind) {
     GroupQ g{0.f, 0.f, 0.f, 0.f};
     const float m = __uint_as_float(m_bits);
@@ -88,17 +99,17 @@ __device__ __forceinline__ GroupQ group_q(uint32_t m_bits, int kind) {
     } else if (m >= 0x1p-100f) {  // else nothing but (almost) zeros
         const float q = cache_qmax(kind);
         const float p = m > 0x1p100f ? 0x1p-32f : (m < 0x1p-36f ? 0x1p64f : 1.f);
-        g.scale = __fdiv_rn(m, q);
-        g.m = m * p;
-        g.r = __frcp_rn(g.m);
+        g.scale = over_qmax(m, q);
+        g.n = -(m * p);
+        g.r = rcp_approx(m * p);
         g.q = q * p;
     }
     return g;
 }
 // x*q/m, such that the code nearest to it is the one nearest to the real
-// quotient, ties seen as ties: q0 = (x*q)*r is off by under 2 units in the last
-// place, and one step with its residual (Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990) mends it.
+// quotient, ties seen as ties: u0 = (x*q)*r is off by a few units in the last
+// place (r by one), and one step with its residual (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990) mends it.
 // 16-bit x: x*q is exact.  A quotient that is half way between codes has so few
 // bits that the residual and the sum come out exact; any other is further from
 // half way than the 2^-23 by which the result may be off (an 11-bit x and m and
@@ -111,12 +122,12 @@ __device__ __forceinline__ float group_scaled(float x, const GroupQ& g) {
     const float n = __fmul_rn(x, g.q);
     const float u0 = __fmul_rn(n, g.r);
     if constexpr (sizeof(T) == 2) {
-        const float u = fmaf(fmaf(-u0, g.m, n), g.r, u0);
+        const float u = fmaf(fmaf(u0, g.n, n), g.r, u0);
         return g.r == 0.f ? 0.f : u;  // (a NaN is no code)
     } else {
         const float lost = fmaf(x, g.q, -n);  // n + lost == x*q
-        const float u = fmaf(fmaf(-u0, g.m, n) + lost, g.r, u0);
-        const float left = fmaf(-u, g.m, n) + lost;
+        const float u = fmaf(fmaf(u0, g.n, n) + lost, g.r, u0);
+        const float left = fmaf(u, g.n, n) + lost;
         const int bits = __float_as_int(u);
         const bool off = left != 0.f && (bits & 1) == 0 && fabsf(u) >= 0x1p-24f;
         const float odd = off ? __int_as_float(bits + ((left > 0.f) == (u > 0.f) ? 1 : -1)) : u;
@@ -128,7 +139,7 @@ template <typename T>
 __device__ __forceinline__ float2 group_scaled2(float2 x, const GroupQ& g) {
     if constexpr (sizeof(T) == 2) {
         const float2 n = __fmul2_rn(x, f2(g.q)), u0 = __fmul2_rn(n, f2(g.r));
-        return __ffma2_rn(__ffma2_rn(f2neg(u0), f2(g.m), n), f2(g.r), u0);
+        return __ffma2_rn(__ffma2_rn(u0, f2(g.n), n), f2(g.r), u0);
     } else {
         return make_float2(group_scaled<T>(x.x, g), group_scaled<T>(x.y, g));
     }
@@ -372,41 +383,62 @@ struct WarpTurns {
     }
 };
 
-// Turns a lane's two vectors by its VE pairs' angles.
+// A lane's VE angles (the sines with both signs: a packed instruction has no negation).
 template <int VE>
-__device__ __forceinline__ void turn_vecs(float2 (&u)[VE / 2], float2 (&v)[VE / 2], const float2 (&c)[VE / 2],
-                                          const float2 (&s)[VE / 2], bool adjacent) {
-    constexpr int H = VE / 2;
-    if (!adjacent) {
+struct LaneTurns {
+    float2 c[VE / 2], s[VE / 2], n[VE / 2];
+    __device__ __forceinline__ void take(const float* cos, const float* sin) {
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const float2 a = __ffma2_rn(u[i], c[i], f2neg(__fmul2_rn(v[i], s[i])));
-            v[i] = __ffma2_rn(v[i], c[i], __fmul2_rn(u[i], s[i]));
-            u[i] = a;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            float2& x = i < H ? u[i % H] : v[i % H];
-            turn(x.x, x.y, i % 2 ? make_float2(c[i / 2].y, s[i / 2].y) : make_float2(c[i / 2].x, s[i / 2].x));
+        for (int i = 0; i < VE / 2; ++i) {
+            c[i] = *reinterpret_cast<const float2*>(cos + 2 * i);
+            s[i] = *reinterpret_cast<const float2*>(sin + 2 * i);
+            n[i] = f2neg(s[i]);
         }
     }
-}
+    // Turns the lane's two vectors.
+    __device__ __forceinline__ void turn(float2 (&u)[VE / 2], float2 (&v)[VE / 2], bool adjacent) const {
+        constexpr int H = VE / 2;
+        if (!adjacent) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float2 a = __ffma2_rn(v[i], n[i], __fmul2_rn(u[i], c[i]));
+                v[i] = __ffma2_rn(u[i], s[i], __fmul2_rn(v[i], c[i]));
+                u[i] = a;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                float2& x = i < H ? u[i % H] : v[i % H];
+                const float ci = i % 2 ? c[i / 2].y : c[i / 2].x, si = i % 2 ? s[i / 2].y : s[i / 2].x;
+                x = make_float2(fmaf(x.x, ci, -__fmul_rn(x.y, si)), fmaf(x.y, ci, __fmul_rn(x.x, si)));
+            }
+        }
+    }
+};
 
 // Sum over the 2^lg lanes of a row; every lane of it gets the same bits.
 __device__ __forceinline__ float row_sum(float v, int lg) {
-    for (int o = 1 << lg >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int i = 4; i >= 0; --i)
+        if (i < lg) v += __shfl_xor_sync(0xffffffffu, v, 1 << i);
     return v;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t row_mag(uint32_t m, int lg) {
+#pragma unroll
+    for (int i = 4; i >= 0; --i)
+        if (i < lg) m = mag_max<T>(m, __shfl_xor_sync(0xffffffffu, m, 1 << i));
+    return m;
 }
 
 // ---------------------------------------------------------------------------
 // asynchronous copies of a lane's own vectors
 // ---------------------------------------------------------------------------
 // A lane copies its vectors of the next steps to places in shared memory that no
-// other lane reads, kHeadStages - 1 steps ahead, so the bytes in flight do not
+// other lane reads, a step or more ahead, so the bytes in flight do not
 // depend on registers or occupancy and no barrier is needed: the lane waits for
 // its own copies.
-constexpr int kHeadStages = 4;
+constexpr int kHeadStages = 4;  // backward
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(void* dst, const void* src) {
@@ -434,128 +466,154 @@ struct TokenWords {
 
 // A warp's way through its work: (token, chunk) units, of each the tensors q, k
 // (and v), of each the row steps chunk, chunk + 2^lchunk, ... of the token's
-// steps counted through all tensors.  A step is 32 >> lg rows.
+// steps counted through all tensors.  A step is kHeadRows rows of a lane; the
+// common one, to the tensor's next step, adds to a head and (in the caller) to a
+// pointer.
 template <int TENSORS>
 struct StepWalk {
-    int64_t un;
-    int which, st, first;
-    bool fresh;  // the first step of a token
-    __device__ __forceinline__ void start(const HeadArgs& a, int64_t unit, int64_t units, int64_t stride, int lper,
-                                          int lchunk) {
+    int64_t un;          // unit
+    int which;           // tensor
+    int h0, heads;       // the step's first head; the tensor's heads
+    int first;           // steps of the token's earlier tensors
+    bool fresh, turned;  // the first step of a token; of a tensor (of a token)
+    int lper, lchunk;
+    int64_t units, stride;
+
+    __device__ __forceinline__ void start(const HeadArgs& a, int64_t unit) {
         un = unit;
-        enter(a, units, stride, lper, lchunk);
+        which = first = 0;
+        fresh = true;
+        settle(a);
     }
-    __device__ __forceinline__ bool live(int64_t units) const { return un < units; }
-    __device__ __forceinline__ void next(const HeadArgs& a, int64_t units, int64_t stride, int lper, int lchunk) {
-        fresh = false;
-        st += 1 << lchunk;
-        settle(a, units, stride, lper, lchunk);
+    __device__ __forceinline__ bool live() const { return un < units; }
+    __device__ __forceinline__ int64_t token() const { return un >> lchunk; }
+    __device__ __forceinline__ int head_step() const { return 1 << (lper + lchunk); }
+    // Moves to the next step: false where only the head moved, within the tensor.
+    __device__ __forceinline__ void next(const HeadArgs& a) {
+        h0 += head_step();
+        fresh = turned = false;
+        if (h0 < heads) return;
+        leave(a);
+        settle(a);
     }
 
 private:
-    __device__ __forceinline__ void enter(const HeadArgs& a, int64_t units, int64_t stride, int lper, int lchunk) {
-        which = first = 0;
-        st = int(un) & ((1 << lchunk) - 1);
-        fresh = true;
-        settle(a, units, stride, lper, lchunk);
+    __device__ __forceinline__ void leave(const HeadArgs& a) {
+        first += (heads + (1 << lper) - 1) >> lper;
+        if (++which == TENSORS) {
+            un += stride;
+            which = first = 0;
+            fresh = true;
+        }
     }
-    __device__ __forceinline__ void settle(const HeadArgs& a, int64_t units, int64_t stride, int lper, int lchunk) {
+    __device__ __forceinline__ void settle(const HeadArgs& a) {
+        turned = true;
         while (un < units) {
-            const int steps = (a.heads[which] + (1 << lper) - 1) >> lper;
-            if (st < steps) return;
-            first += steps;
-            const int mask = (1 << lchunk) - 1;
-            if (++which == TENSORS) {
-                un += stride;
-                which = first = 0;
-                fresh = true;
-            }
-            st = (int(un) - first) & mask;
+            heads = a.heads[which];
+            h0 = ((int(un) - first) & ((1 << lchunk) - 1)) << lper;
+            if (h0 < heads) return;
+            leave(a);
         }
     }
 };
 
-// Two vectors a step.
+constexpr int kHeadRows = 2;    // rows of a lane in a step
+constexpr int kHeadFwdStages = 3;
+
 template <typename T, int VE>
 constexpr size_t head_fwd_smem() {
-    return size_t(kHeadStages) * 2 * kHeadWarps * 32 * VE * sizeof(T);
+    return size_t(kHeadFwdStages) * 2 * kHeadRows * kHeadWarps * 32 * VE * sizeof(T);
 }
 
 template <typename T, int VE, bool NORM, bool CACHE>
 __global__ void __launch_bounds__(kHeadWarps * 32, 2)
 head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
-    constexpr int H = VE / 2, D = kHeadStages, TENSORS = CACHE ? 3 : 2, BYTES = VE * int(sizeof(T));
+    constexpr int H = VE / 2, D = kHeadFwdStages, R = kHeadRows, N = kHeadWarps * 32, BYTES = VE * int(sizeof(T));
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
     __shared__ TokenWords s_tok[kHeadWarps][D];
     __shared__ uint32_t s_max[CACHE ? kHeadWarps : 1][CACHE ? 64 : 1];
-    Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][vector], blockDim.x apart
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const LaneAt<VE> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
-    const int lper = 5 - lg, b01 = at.b1 - at.b0;
-    const int64_t units = a.tokens << lchunk, stride = int64_t(gridDim.x) * kHeadWarps;
+    const int rows = 32 >> lg, b01 = at.b1 - at.b0;
     const float inv_d = 1.f / float(a.d);
     const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
 
-    StepWalk<TENSORS> in, cur;
-    in.start(a, int64_t(blockIdx.x) * kHeadWarps + warp, units, stride, lper, lchunk);
-    cur = in;
+    StepWalk<CACHE ? 3 : 2> in;
+    in.lper = 5 - lg + (R == 2 ? 1 : 0);
+    in.lchunk = lchunk;
+    in.units = a.tokens << lchunk;
+    in.stride = int64_t(gridDim.x) * kHeadWarps;
+    in.start(a, int64_t(blockIdx.x) * kHeadWarps + warp);
+    StepWalk<CACHE ? 3 : 2> cur = in;
+
+    const T* px = nullptr;  // this lane's first vector of the step to copy
+    int64_t row_x = 0;      // from one of a lane's rows to its next
     auto issue = [&](int stage) {
-        if (in.live(units)) {
-            const int64_t t = in.un >> lchunk;
-            const int h = (in.st << lper) + at.sub;
-            if (at.on && h < a.heads[in.which]) {
+        if (in.live()) {
+            if (in.turned) {
                 const HeadView v = a.x[in.which];
-                const T* p = reinterpret_cast<const T*>(v.p) + t * v.ts + h * v.hs + at.b0;
-                cp_async<BYTES>(ring + (2 * stage) * kHeadWarps * 32, p);
-                cp_async<BYTES>(ring + (2 * stage + 1) * kHeadWarps * 32, p + b01);
+                px = reinterpret_cast<const T*>(v.p) + in.token() * v.ts + (in.h0 + at.sub) * v.hs + at.b0;
+                row_x = rows * v.hs;
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                if (at.on && in.h0 + at.sub + k * rows < in.heads) {
+                    const T* p = px + k * row_x;
+                    cp_async<BYTES>(ring + ((stage * R + k) * 2) * N, p);
+                    cp_async<BYTES>(ring + ((stage * R + k) * 2 + 1) * N, p + b01);
+                }
             }
             if (in.fresh) {
+                const int64_t t = in.token();
                 if (lane < a.rope.axes)
                     cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
                 if (CACHE && lane == kTokenSlot) cp_async<8>(&s_tok[warp][stage].w[kTokenSlot], a.slots + t);
             }
-            in.next(a, units, stride, lper, lchunk);
+            px += (R * row_x) << lchunk;
+            in.next(a);
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
 
-    float2 c[H], s[H], w0[H], w1[H];
+    LaneTurns<VE> tn;
+    float2 w0[H], w1[H];
     int have = -1;  // the tensor whose weights are in registers
-    int64_t slot = -1;
-    for (int stage = 0; cur.live(units); stage = stage + 1 == D ? 0 : stage + 1) {
+    T* py = nullptr;
+    float* pr = nullptr;
+    int64_t row_y = 0, slot = -1;
+    bool out = false;
+    for (int stage = 0; cur.live(); stage = stage + 1 == D ? 0 : stage + 1) {
         cp_async_wait<D - 2>();
-        const int64_t t = cur.un >> lchunk;
-        const int which = cur.which, heads = a.heads[which];
-        const int h = (cur.st << lper) + at.sub;
-        const bool row = h < heads, on = row && at.on;
-        Raw<T, VE> x0{}, x1{};
-        if (on) {
-            x0 = ring[(2 * stage) * kHeadWarps * 32];
-            x1 = ring[(2 * stage + 1) * kHeadWarps * 32];
+        const int which = cur.which, heads = cur.heads, h = cur.h0 + at.sub;
+        Raw<T, VE> x0[R], x1[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            x0[k] = x1[k] = Raw<T, VE>{};
+            if (at.on && h + k * rows < heads) {
+                x0[k] = ring[((stage * R + k) * 2) * N];
+                x1[k] = ring[((stage * R + k) * 2 + 1) * N];
+            }
         }
         if (cur.fresh) {
             turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
-            if (at.turns) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
-                    s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
-                }
-            }
+            if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
             if (CACHE) slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
             __syncwarp();
         }
         issue(stage == 0 ? D - 1 : stage - 1);
-        cur.next(a, units, stride, lper, lchunk);
-        if (which < 2) {
-            float2 u[H], v[H];
-            raw_unpack<T, VE>(x0, u);
-            raw_unpack<T, VE>(x1, v);
+        if (cur.turned && which < 2) {
+            const int64_t t = cur.token();
+            const HeadView v = a.y[which];
+            py = reinterpret_cast<T*>(v.p) + t * v.ts + h * v.hs + at.b0;
+            row_y = rows * v.hs;
+            out = v.p && at.on;
             if (NORM) {
+                pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
                 if (which != have) {
                     have = which;
 #pragma unroll
@@ -566,68 +624,95 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
                         raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
                     }
                 }
-                float2 sq = f2(0.f);
+            }
+        }
+        if (which < 2) {
+            float2 u[R][H], v[R][H];
 #pragma unroll
-                for (int i = 0; i < H; ++i) sq = __ffma2_rn(u[i], u[i], __ffma2_rn(v[i], v[i], sq));
-                const float r = rsqrtf(fmaf(row_sum(sq.x + sq.y, lg), inv_d, a.eps));
-                float* rstd = a.rstd[which];
-                if (rstd && row && at.j == 0) rstd[t * heads + h] = r;
+            for (int k = 0; k < R; ++k) {
+                raw_unpack<T, VE>(x0[k], u[k]);
+                raw_unpack<T, VE>(x1[k], v[k]);
+            }
+            if (NORM) {
+                float r[R];
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    u[i] = __fmul2_rn(__fmul2_rn(u[i], f2(r)), w0[i]);
-                    v[i] = __fmul2_rn(__fmul2_rn(v[i], f2(r)), w1[i]);
+                for (int k = 0; k < R; ++k) {
+                    float2 sq = f2(0.f);
+#pragma unroll
+                    for (int i = 0; i < H; ++i) sq = __ffma2_rn(u[k][i], u[k][i], __ffma2_rn(v[k][i], v[k][i], sq));
+                    r[k] = sq.x + sq.y;
+                }
+#pragma unroll
+                for (int k = 0; k < R; ++k) r[k] = rsqrtf(fmaf(row_sum(r[k], lg), inv_d, a.eps));
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    if (pr && h + k * rows < heads) pr[k * rows] = r[k];
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        u[k][i] = __fmul2_rn(__fmul2_rn(u[k][i], f2(r[k])), w0[i]);
+                        v[k][i] = __fmul2_rn(__fmul2_rn(v[k][i], f2(r[k])), w1[i]);
+                    }
                 }
             }
-            if (at.turns) turn_vecs<VE>(u, v, c, s, a.rope.adjacent);
-            x0 = raw_pack<T, VE>(u);
-            x1 = raw_pack<T, VE>(v);
-            const HeadView yv = a.y[which];
-            if (on && yv.p) {
-                T* p = reinterpret_cast<T*>(yv.p) + t * yv.ts + h * yv.hs + at.b0;
-                st_row(p, x0);
-                st_row(p + b01, x1);
+            if (at.turns) {
+#pragma unroll
+                for (int k = 0; k < R; ++k) tn.turn(u[k], v[k], a.rope.adjacent);
             }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                x0[k] = raw_pack<T, VE>(u[k]);
+                x1[k] = raw_pack<T, VE>(v[k]);
+                if (out && h + k * rows < heads) {
+                    T* p = py + k * row_y;
+                    st_row(p, x0[k]);
+                    st_row(p + b01, x1[k]);
+                }
+            }
+            py += (R * row_y) << lchunk;
+            if (NORM && pr) pr += cur.head_step();
         }
         if constexpr (CACHE) {
             // (both conditions are the warp's.)  The cache stores the key in the activations'
             // type: what a separate write would read.
-            if (which == 0 || slot < 0) continue;
-            uint32_t m0 = raw_mag<T, VE>(x0), m1 = raw_mag<T, VE>(x1);
-            const int group = a.cache.group;
-            if (group == a.d) {
-                m0 = mag_max<T>(m0, m1);
-                if (!at.on) m0 = 0;
-                for (int o = 1 << lg >> 1; o > 0; o >>= 1) m0 = mag_max<T>(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                m1 = m0;
-            } else {
-                // groups of whole vectors, which other lanes may hold: through shared memory
-                uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
-                const int n = group / VE;
-                if (at.on) {
-                    sm[at.b0 / VE] = m0;
-                    sm[at.b1 / VE] = m1;
-                }
-                __syncwarp();
-                if (at.on) {
-                    for (int i = 0; i < n; ++i) {
-                        m0 = mag_max<T>(m0, sm[g0 * n + i]);
-                        m1 = mag_max<T>(m1, sm[g1 * n + i]);
+            if (which > 0 && slot >= 0) {
+                const int group = a.cache.group;
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    uint32_t m0 = raw_mag<T, VE>(x0[k]), m1 = raw_mag<T, VE>(x1[k]);
+                    if (group == a.d) {
+                        m0 = m1 = row_mag<T>(at.on ? mag_max<T>(m0, m1) : 0u, lg);
+                    } else {
+                        // groups of whole vectors, which other lanes may hold: through shared memory
+                        uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
+                        const int n = group / VE;
+                        if (at.on) {
+                            sm[at.b0 / VE] = m0;
+                            sm[at.b1 / VE] = m1;
+                        }
+                        __syncwarp();
+                        if (at.on) {
+                            for (int i = 0; i < n; ++i) {
+                                m0 = mag_max<T>(m0, sm[g0 * n + i]);
+                                m1 = mag_max<T>(m1, sm[g1 * n + i]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (at.on && h + k * rows < heads) {
+                        const CacheRow cr = cache_row(a.cache, slot, h + k * rows);
+                        const GroupQ q0 = group_q(mag_bits<T>(m0), a.cache.kind);
+                        const GroupQ q1 = group_q(mag_bits<T>(m1), a.cache.kind);
+                        float* scales = a.cache.scales[which - 1] + cr.scale;
+                        if (at.b0 == g0 * group) scales[g0] = q0.scale;
+                        if (at.b1 == g1 * group) scales[g1] = q1.scale;
+                        uint8_t* codes = a.cache.codes[which - 1] + cr.code;
+                        store_codes<T, VE>(codes, at.b0, x0[k], q0, a.cache.kind);
+                        store_codes<T, VE>(codes, at.b1, x1[k], q1, a.cache.kind);
                     }
                 }
-                __syncwarp();
-            }
-            if (on) {
-                const CacheRow cr = cache_row(a.cache, slot, h);
-                const GroupQ q0 = group_q(mag_bits<T>(m0), a.cache.kind);
-                const GroupQ q1 = group_q(mag_bits<T>(m1), a.cache.kind);
-                float* scales = a.cache.scales[which - 1] + cr.scale;
-                if (at.b0 == g0 * group) scales[g0] = q0.scale;
-                if (at.b1 == g1 * group) scales[g1] = q1.scale;
-                uint8_t* codes = a.cache.codes[which - 1] + cr.code;
-                store_codes<T, VE>(codes, at.b0, x0, q0, a.cache.kind);
-                store_codes<T, VE>(codes, at.b1, x1, q1, a.cache.kind);
             }
         }
+        cur.next(a);
     }
     cp_async_wait<0>();
 }
@@ -651,7 +736,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     __shared__ TokenWords s_tok[kHeadWarps][D];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][vector], N apart
     float* ring_r = reinterpret_cast<float*>(dyn + size_t(D) * 4 * N * BYTES) + threadIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const int which = int(blockIdx.x) < nq ? 0 : 1;
     const int cta = int(blockIdx.x) - (which ? nq : 0);
     const int ctas = which ? int(gridDim.x) - nq : nq;
@@ -663,6 +748,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const float inv_d = 1.f / float(a.d);
     const HeadView xv = a.x[which], gv = a.dy[which], dv = a.y[which];
     const int b01 = at.b1 - at.b0;
+    const int64_t step_x = hstep * xv.hs, step_g = hstep * gv.hs, step_o = hstep * dv.hs;
     float2 w0[H], w1[H], acc0[H], acc1[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) {
@@ -676,47 +762,60 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     }
     // the first head of unit un's first step; a unit without one is passed over
     auto first_head = [&](int64_t un) { return (int(un) & mask) << (5 - lg); };
-    auto pass = [&](int64_t& un, int& h0) {
+    auto enter = [&](int64_t& un, int& h0) {
+        h0 = first_head(un);
         while (un < units && h0 >= heads) {
             un += stride;
             h0 = first_head(un);
         }
     };
     int64_t in_un = int64_t(cta) * kHeadWarps + warp;
-    int in_h = first_head(in_un);
-    pass(in_un, in_h);
+    int in_h;
+    enter(in_un, in_h);
     int64_t un = in_un;
     int h0 = in_h;
+    bool in_fresh = true, fresh = true;
+    const T *pg = nullptr, *px = nullptr;
+    const float* pr = nullptr;
+    T* po = nullptr;
     auto issue = [&](int stage) {
         if (in_un < units) {
-            const int64_t t = in_un >> lchunk;
-            const int h = in_h + at.sub;
-            if (at.on && h < heads) {
-                const T* pg = reinterpret_cast<const T*>(gv.p) + t * gv.ts + h * gv.hs + at.b0;
-                const T* px = reinterpret_cast<const T*>(xv.p) + t * xv.ts + h * xv.hs + at.b0;
+            if (in_fresh) {
+                const int64_t t = in_un >> lchunk;
+                const int h = in_h + at.sub;
+                pg = reinterpret_cast<const T*>(gv.p) + t * gv.ts + h * gv.hs + at.b0;
+                px = reinterpret_cast<const T*>(xv.p) + t * xv.ts + h * xv.hs + at.b0;
+                pr = a.rstd[which] + t * heads + h;
+                if (lane < a.rope.axes)
+                    cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
+            }
+            if (at.on && in_h + at.sub < heads) {
                 Raw<T, VE>* to = ring + stage * 4 * N;
                 cp_async<BYTES>(to, pg);
                 cp_async<BYTES>(to + N, pg + b01);
                 cp_async<BYTES>(to + 2 * N, px);
                 cp_async<BYTES>(to + 3 * N, px + b01);
-                cp_async<4>(ring_r + stage * N, a.rstd[which] + t * heads + h);
+                cp_async<4>(ring_r + stage * N, pr);
             }
-            if (in_h == first_head(in_un) && lane < a.rope.axes)
-                cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
+            pg += step_g;
+            px += step_x;
+            pr += hstep;
             in_h += hstep;
-            pass(in_un, in_h);
+            in_fresh = in_h >= heads;
+            if (in_fresh) {
+                in_un += stride;
+                enter(in_un, in_h);
+            }
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
 
-    float2 c[H], s[H];
+    LaneTurns<VE> tn;
     for (int stage = 0; un < units; stage = stage + 1 == D ? 0 : stage + 1) {
         cp_async_wait<D - 2>();
-        const int64_t t = un >> lchunk;
-        const int h = h0 + at.sub;
-        const bool on = h < heads && at.on;
+        const bool on = h0 + at.sub < heads && at.on;
         Raw<T, VE> x0{}, x1{}, y0{}, y1{};
         float r = 0.f;
         if (on) {
@@ -727,23 +826,16 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             x1 = from[3 * N];
             r = ring_r[stage * N];
         }
-        if (h0 == first_head(un)) {
+        if (fresh) {
             turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
-            if (at.turns) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    c[i] = *reinterpret_cast<const float2*>(&s_cos[warp][VE * at.j + 2 * i]);
-                    s[i] = *reinterpret_cast<const float2*>(&s_sin[warp][VE * at.j + 2 * i]);
-                }
-            }
+            if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
+            po = reinterpret_cast<T*>(dv.p) + (un >> lchunk) * dv.ts + (h0 + at.sub) * dv.hs + at.b0;
         }
         issue(stage == 0 ? D - 1 : stage - 1);
-        h0 += hstep;
-        pass(un, h0);
         float2 u[H], v[H], gu[H], gw[H];
         raw_unpack<T, VE>(y0, gu);
         raw_unpack<T, VE>(y1, gw);
-        if (at.turns) turn_vecs<VE>(gu, gw, c, s, a.rope.adjacent);
+        if (at.turns) tn.turn(gu, gw, a.rope.adjacent);
         raw_unpack<T, VE>(x0, u);
         raw_unpack<T, VE>(x1, v);
         float2 sum = f2(0.f);
@@ -765,9 +857,15 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             gw[i] = __ffma2_rn(v[i], f2(f), gw[i]);
         }
         if (on) {
-            T* o = reinterpret_cast<T*>(dv.p) + t * dv.ts + h * dv.hs + at.b0;
-            st_row(o, raw_pack<T, VE>(gu));
-            st_row(o + b01, raw_pack<T, VE>(gw));
+            st_row(po, raw_pack<T, VE>(gu));
+            st_row(po + b01, raw_pack<T, VE>(gw));
+        }
+        po += step_o;
+        h0 += hstep;
+        fresh = h0 >= heads;
+        if (fresh) {
+            un += stride;
+            enter(un, h0);
         }
     }
     cp_async_wait<0>();
@@ -865,8 +963,7 @@ cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
                     if (whole) {
 #pragma unroll
                         for (int v = 1; v < NV; ++v) m[0] = mag_max<T>(m[0], m[v]);
-                        for (int o = 1 << cl.lg >> 1; o > 0; o >>= 1)
-                            m[0] = mag_max<T>(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+                        m[0] = row_mag<T>(m[0], cl.lg);
 #pragma unroll
                         for (int v = 1; v < NV; ++v) m[v] = m[0];
                     } else if (pow2) {
@@ -1325,7 +1422,7 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
     const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head forward kernel cannot be resident");
     int lg = row_lanes_log2(a.d / (2 * VE));
-    const int per = 32 >> lg;
+    const int per = (32 >> lg) * kHeadRows;
     int steps = 0;
     for (int i = 0; i < (cache ? 3 : 2); ++i) steps += (a.heads[i] + per - 1) / per;
     int lc = head_chunks_log2(a.tokens, steps, d);
