@@ -11,6 +11,8 @@
 // fit no vector take a row per warp, element by element.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "heads.h"
 
@@ -65,15 +67,21 @@ __device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
 // ---------------------------------------------------------------------------
 // quantising a group by its largest magnitude
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float cache_qmax(int kind) {
-    return kind == NRM_CACHE_E4M3 ? 448.f : (kind == NRM_CACHE_INT8 ? 127.f : 7.f);
-}
+// A stored form: its largest number, and one over it.
+struct FormQ {
+    int kind;
+    float q, r;
+    __device__ __forceinline__ explicit FormQ(int k) : kind(k) {
+        q = k == NRM_CACHE_E4M3 ? 448.f : (k == NRM_CACHE_INT8 ? 127.f : 7.f);
+        r = k == NRM_CACHE_E4M3 ? 1.f / 448.f : (k == NRM_CACHE_INT8 ? 1.f / 127.f : 1.f / 7.f);
+    }
+};
 
 // A group's scale and what its codes need, from the bits of its largest
 // magnitude (compared as integers, so a NaN is the largest of all).  Groups
-// above 2^100 are divided by 2^32 and groups below 2^-36 multiplied by 2^64
-// (exactly, where it matters), so that products stay finite and residuals
-// representable.
+// above 2^100 are divided by 2^32, and of float32 groups those below 2^-36
+// multiplied by 2^64 (exactly, where it matters), so that products stay finite
+// and residuals representable.
 struct GroupQ {
     float scale;
     float n, r;  // minus the scaled largest magnitude, and about its reciprocal; both 0 where every code is 0
@@ -81,29 +89,25 @@ struct GroupQ {
 };
 // m/q rounded to nearest, for the forms' q: Markstein's division by a known number
 // (checked against the division for every mantissa).
-__device__ __forceinline__ float over_qmax(float m, float q) {
-    const float r = q == 448.f ? 1.f / 448.f : (q == 127.f ? 1.f / 127.f : 1.f / 7.f);
-    const float s = __fmul_rn(m, r);
-    return fmaf(fmaf(-s, q, m), r, s);
+__device__ __forceinline__ float over_qmax(float m, const FormQ& f) {
+    const float s = __fmul_rn(m, f.r);
+    return fmaf(fmaf(-s, f.q, m), f.r, s);
 }
 __device__ __forceinline__ float rcp_approx(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-__device__ __forceinline__ GroupQ group_q(uint32_t m_bits, int kind) {
-    GroupQ g{0.f, 0.f, 0.f, 0.f};
+template <typename T>
+__device__ __forceinline__ GroupQ group_q(uint32_t m_bits, const FormQ& f) {
     const float m = __uint_as_float(m_bits);
-    if (m_bits >= 0x7f800000u) {  // a NaN or an infinity: the group reads back as NaN
-        g.scale = __uint_as_float(0x7fffffffu);
-    } else if (m >= 0x1p-100f) {  // else nothing but (almost) zeros
-        const float q = cache_qmax(kind);
-        const float p = m > 0x1p100f ? 0x1p-32f : (m < 0x1p-36f ? 0x1p64f : 1.f);
-        g.scale = over_qmax(m, q);
-        g.n = -(m * p);
-        g.r = rcp_approx(m * p);
-        g.q = q * p;
-    }
+    float p = 1.f;
+    if constexpr (sizeof(T) == 4) p = m < 0x1p-36f ? 0x1p64f : p;
+    if constexpr (!std::is_same_v<T, __half>) p = m > 0x1p100f ? 0x1p-32f : p;
+    GroupQ g{over_qmax(m, f), -(m * p), rcp_approx(m * p), f.q * p};
+    // a NaN or an infinity (the group reads back as NaN), or nothing but (almost) zeros
+    const bool nan = m_bits >= 0x7f800000u;
+    if (nan || m < 0x1p-100f) g = GroupQ{nan ? __uint_as_float(0x7fffffffu) : 0.f, 0.f, 0.f, 0.f};
     return g;
 }
 // x*q/m, such that the code nearest to it is the one nearest to the real
@@ -186,10 +190,11 @@ __device__ __forceinline__ void quantise_row(const float* row, int d, const Cach
     const CacheRow at = cache_row(c, slot, head);
     uint8_t* codes = c.codes[which] + at.code;
     float* scales = c.scales[which] + at.scale;
+    const FormQ form(c.kind);
     for (int g0 = 0; g0 < d; g0 += c.group) {
         uint32_t m = 0;
         for (int i = lane; i < c.group; i += 32) m = max(m, __float_as_uint(row[g0 + i]) & 0x7fffffffu);
-        const GroupQ q = group_q(__reduce_max_sync(0xffffffffu, m), c.kind);
+        const GroupQ q = group_q<T>(__reduce_max_sync(0xffffffffu, m), form);
         if (lane == 0) scales[g0 / c.group] = q.scale;
         if (c.kind == NRM_CACHE_INT4) {
             for (int i = 2 * lane; i < c.group; i += 64)
@@ -251,6 +256,51 @@ __device__ __forceinline__ Raw<T, VE> raw_pack(const float2 (&v)[VE / 2]) {
     return r;
 }
 
+// A lane's two vectors as the first and the second elements of its VE pairs: the
+// two vectors, or (ADJ) the even and the odd elements of both.
+template <typename T, int VE, bool ADJ>
+__device__ __forceinline__ void pair_unpack(const Raw<T, VE>& r0, const Raw<T, VE>& r1, float2 (&u)[VE / 2],
+                                            float2 (&v)[VE / 2]) {
+    float2 a[VE / 2], b[VE / 2];
+    raw_unpack<T, VE>(r0, a);
+    raw_unpack<T, VE>(r1, b);
+#pragma unroll
+    for (int i = 0; i < VE / 2; ++i) {
+        if constexpr (!ADJ) {
+            u[i] = a[i];
+            v[i] = b[i];
+        } else {
+            const float2 x = 2 * i < VE / 2 ? a[2 * i % (VE / 2)] : b[2 * i % (VE / 2)];
+            const float2 y = 2 * i + 1 < VE / 2 ? a[(2 * i + 1) % (VE / 2)] : b[(2 * i + 1) % (VE / 2)];
+            u[i] = make_float2(x.x, y.x);
+            v[i] = make_float2(x.y, y.y);
+        }
+    }
+}
+template <typename T, int VE, bool ADJ>
+__device__ __forceinline__ void pair_pack(const float2 (&u)[VE / 2], const float2 (&v)[VE / 2], Raw<T, VE>& r0,
+                                          Raw<T, VE>& r1) {
+    if constexpr (!ADJ) {
+        r0 = raw_pack<T, VE>(u);
+        r1 = raw_pack<T, VE>(v);
+    } else {
+        float2 e[VE];  // the pairs in their order
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            e[2 * i] = make_float2(u[i].x, v[i].x);
+            e[2 * i + 1] = make_float2(u[i].y, v[i].y);
+        }
+        float2 a[VE / 2], b[VE / 2];
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            a[i] = e[i];
+            b[i] = e[VE / 2 + i];
+        }
+        r0 = raw_pack<T, VE>(a);
+        r1 = raw_pack<T, VE>(b);
+    }
+}
+
 // Largest magnitudes, compared as integers: of float32 its bits, of 16-bit types
 // two at once, in the halves of a word.
 template <typename T>
@@ -274,15 +324,12 @@ __device__ __forceinline__ uint32_t mag_bits(uint32_t m) {
     else return __float_as_uint(Io<T>::load(typename Io<T>::bits_t(max(m & 0xffffu, m >> 16))));
 }
 
-// Codes of VE consecutive elements, stored at element e of the row.  A whole
+// Codes of VE consecutive elements, stored at `at`.  A whole
 // number comes out of the low bits of u + 1.5 * 2^23 (the sum rounds to nearest,
 // ties to even).
 template <typename T, int VE>
-__device__ __forceinline__ void store_codes(uint8_t* row, int e, Raw<T, VE> x, const GroupQ& q, int kind) {
-    const uint32_t live = q.r != 0.f ? 0xffffffffu : 0u;  // no NaN reaches the arithmetic
-    uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-    for (int i = 0; i < VE * int(sizeof(T)) / 4; ++i) xw[i] &= live;
+__device__ __forceinline__ void store_codes(uint8_t* at, Raw<T, VE> x, const GroupQ& q, int kind) {
+    if (q.r == 0.f) x = Raw<T, VE>{};  // no NaN reaches the arithmetic
     float2 u[VE / 2];
     raw_unpack<T, VE>(x, u);
 #pragma unroll
@@ -291,7 +338,6 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int e, Raw<T, VE> x, c
         uint32_t w[(VE + 3) / 4] = {};
 #pragma unroll
         for (int i = 0; i < VE; i += 2) w[i / 4] |= e4m3x2(u[i / 2].x, u[i / 2].y) << (8 * (i % 4));
-        uint8_t* at = row + e;
         if constexpr (VE == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
         else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(at) = w[0];
         else *reinterpret_cast<uint16_t*>(at) = uint16_t(w[0]);
@@ -306,7 +352,6 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int e, Raw<T, VE> x, c
         b[2 * i + 1] = __float_as_uint(f.y);
     }
     if (kind == NRM_CACHE_INT8) {
-        uint8_t* at = row + e;
         if constexpr (VE == 2) {
             *reinterpret_cast<uint16_t*>(at) = uint16_t(__byte_perm(b[0], b[1], 0x0040));
         } else {
@@ -326,7 +371,6 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int e, Raw<T, VE> x, c
 #pragma unroll
         for (int i = VE - 2; i >= 0; --i) w = w * 16 + b[i];
         w = (w - magic * ones + 8 * ones) ^ (8 * ones);
-        uint8_t* at = row + (e >> 1);
         if constexpr (VE == 8) *reinterpret_cast<uint32_t*>(at) = w;
         else if constexpr (VE == 4) *reinterpret_cast<uint16_t*>(at) = uint16_t(w);
         else *at = uint8_t(w);
@@ -335,7 +379,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int e, Raw<T, VE> x, c
 
 // A lane's place in the vector kernels: which row of the warp's, which pair of
 // vectors of that row, and where they lie.  2^lg lanes hold a row.
-template <int VE>
+template <int VE, bool ADJ>
 struct LaneAt {
     int sub, j;      // row of the warp's 32 >> lg rows, pair of vectors of the row
     int b0, b1;      // first elements of the two vectors
@@ -345,7 +389,7 @@ struct LaneAt {
         j = lane & ((1 << lg) - 1);
         on = 2 * VE * j < d;
         turns = 2 * VE * j < r.rot;
-        const bool half = turns && !r.adjacent;
+        const bool half = turns && !ADJ;
         b0 = half ? VE * j : 2 * VE * j;
         b1 = half ? VE * j + (r.rot >> 1) : b0 + VE;
     }
@@ -395,23 +439,13 @@ struct LaneTurns {
             n[i] = f2neg(s[i]);
         }
     }
-    // Turns the lane's two vectors.
-    __device__ __forceinline__ void turn(float2 (&u)[VE / 2], float2 (&v)[VE / 2], bool adjacent) const {
-        constexpr int H = VE / 2;
-        if (!adjacent) {
+    // Turns the lane's pairs.
+    __device__ __forceinline__ void turn(float2 (&u)[VE / 2], float2 (&v)[VE / 2]) const {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                const float2 a = __ffma2_rn(v[i], n[i], __fmul2_rn(u[i], c[i]));
-                v[i] = __ffma2_rn(u[i], s[i], __fmul2_rn(v[i], c[i]));
-                u[i] = a;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                float2& x = i < H ? u[i % H] : v[i % H];
-                const float ci = i % 2 ? c[i / 2].y : c[i / 2].x, si = i % 2 ? s[i / 2].y : s[i / 2].x;
-                x = make_float2(fmaf(x.x, ci, -__fmul_rn(x.y, si)), fmaf(x.y, ci, __fmul_rn(x.x, si)));
-            }
+        for (int i = 0; i < VE / 2; ++i) {
+            const float2 a = __ffma2_rn(v[i], n[i], __fmul2_rn(u[i], c[i]));
+            v[i] = __ffma2_rn(u[i], s[i], __fmul2_rn(v[i], c[i]));
+            u[i] = a;
         }
     }
 };
@@ -525,9 +559,9 @@ constexpr size_t head_fwd_smem() {
     return size_t(kHeadFwdStages) * 2 * kHeadRows * kHeadWarps * 32 * VE * sizeof(T);
 }
 
-template <typename T, int VE, bool NORM, bool CACHE>
+template <typename T, int VE, bool ADJ, bool CACHE>
 __global__ void __launch_bounds__(kHeadWarps * 32, 2)
-head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
+head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int norm) {
     constexpr int H = VE / 2, D = kHeadFwdStages, R = kHeadRows, N = kHeadWarps * 32, BYTES = VE * int(sizeof(T));
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
@@ -535,12 +569,18 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
     __shared__ uint32_t s_max[CACHE ? kHeadWarps : 1][CACHE ? 64 : 1];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
-    const LaneAt<VE> at(lane, lg, a.d, a.rope);
+    const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
     const int rows = 32 >> lg, b01 = at.b1 - at.b0;
     const float inv_d = 1.f / float(a.d);
     const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
+    const FormQ form(CACHE ? a.cache.kind : 0);
+    const int packed = form.kind == NRM_CACHE_INT4;  // two elements to a byte
 
+    // lanes past the row copy nothing, and read zeros
+    if (!at.on)
+#pragma unroll
+        for (int i = 0; i < 2 * D * R; ++i) ring[i * N] = Raw<T, VE>{};
     StepWalk<CACHE ? 3 : 2> in;
     in.lper = 5 - lg + (R == 2 ? 1 : 0);
     in.lchunk = lchunk;
@@ -593,11 +633,9 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
         Raw<T, VE> x0[R], x1[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            x0[k] = x1[k] = Raw<T, VE>{};
-            if (at.on && h + k * rows < heads) {
-                x0[k] = ring[((stage * R + k) * 2) * N];
-                x1[k] = ring[((stage * R + k) * 2 + 1) * N];
-            }
+            // (of a row past the tensor's heads: what an earlier step left, used by no one)
+            x0[k] = ring[((stage * R + k) * 2) * N];
+            x1[k] = ring[((stage * R + k) * 2 + 1) * N];
         }
         if (cur.fresh) {
             turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
@@ -612,28 +650,24 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
             py = reinterpret_cast<T*>(v.p) + t * v.ts + h * v.hs + at.b0;
             row_y = rows * v.hs;
             out = v.p && at.on;
-            if (NORM) {
+            if (norm) {
                 pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
                 if (which != have) {
                     have = which;
 #pragma unroll
                     for (int i = 0; i < H; ++i) w0[i] = w1[i] = f2(1.f);
                     const T* w = reinterpret_cast<const T*>(a.w[which]);
-                    if (w && at.on) {
-                        raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
-                        raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
-                    }
+                    if (w && at.on)
+                        pair_unpack<T, VE, ADJ>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                                __ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
                 }
             }
         }
         if (which < 2) {
             float2 u[R][H], v[R][H];
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                raw_unpack<T, VE>(x0[k], u[k]);
-                raw_unpack<T, VE>(x1[k], v[k]);
-            }
-            if (NORM) {
+            for (int k = 0; k < R; ++k) pair_unpack<T, VE, ADJ>(x0[k], x1[k], u[k], v[k]);
+            if (norm) {
                 float r[R];
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
@@ -656,12 +690,11 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
             }
             if (at.turns) {
 #pragma unroll
-                for (int k = 0; k < R; ++k) tn.turn(u[k], v[k], a.rope.adjacent);
+                for (int k = 0; k < R; ++k) tn.turn(u[k], v[k]);
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                x0[k] = raw_pack<T, VE>(u[k]);
-                x1[k] = raw_pack<T, VE>(v[k]);
+                pair_pack<T, VE, ADJ>(u[k], v[k], x0[k], x1[k]);
                 if (out && h + k * rows < heads) {
                     T* p = py + k * row_y;
                     st_row(p, x0[k]);
@@ -669,7 +702,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
                 }
             }
             py += (R * row_y) << lchunk;
-            if (NORM && pr) pr += cur.head_step();
+            if (pr) pr += cur.head_step();
         }
         if constexpr (CACHE) {
             // (both conditions are the warp's.)  The cache stores the key in the activations'
@@ -700,14 +733,14 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk) {
                     }
                     if (at.on && h + k * rows < heads) {
                         const CacheRow cr = cache_row(a.cache, slot, h + k * rows);
-                        const GroupQ q0 = group_q(mag_bits<T>(m0), a.cache.kind);
-                        const GroupQ q1 = group_q(mag_bits<T>(m1), a.cache.kind);
+                        const GroupQ q0 = group_q<T>(mag_bits<T>(m0), form);
+                        const GroupQ q1 = group == a.d ? q0 : group_q<T>(mag_bits<T>(m1), form);
                         float* scales = a.cache.scales[which - 1] + cr.scale;
                         if (at.b0 == g0 * group) scales[g0] = q0.scale;
                         if (at.b1 == g1 * group) scales[g1] = q1.scale;
                         uint8_t* codes = a.cache.codes[which - 1] + cr.code;
-                        store_codes<T, VE>(codes, at.b0, x0[k], q0, a.cache.kind);
-                        store_codes<T, VE>(codes, at.b1, x1[k], q1, a.cache.kind);
+                        store_codes<T, VE>(codes + (at.b0 >> packed), x0[k], q0, form.kind);
+                        store_codes<T, VE>(codes + (at.b1 >> packed), x1[k], q1, form.kind);
                     }
                 }
             }
@@ -726,7 +759,7 @@ constexpr size_t head_bwd_smem() {
     return size_t(kHeadStages) * kHeadWarps * 32 * (4 * VE * sizeof(T) + 4);
 }
 
-template <typename T, int VE>
+template <typename T, int VE, bool ADJ>
 __global__ void __launch_bounds__(kHeadWarps * 32, 2)
 head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int nq) {
     constexpr int H = VE / 2, D = kHeadStages, BYTES = VE * int(sizeof(T)), N = kHeadWarps * 32;
@@ -740,7 +773,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const int which = int(blockIdx.x) < nq ? 0 : 1;
     const int cta = int(blockIdx.x) - (which ? nq : 0);
     const int ctas = which ? int(gridDim.x) - nq : nq;
-    const LaneAt<VE> at(lane, lg, a.d, a.rope);
+    const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
     const int heads = a.heads[which], mask = (1 << lchunk) - 1;
     const int hstep = (32 >> lg) << lchunk;  // heads from one of a unit's steps to its next
@@ -757,9 +790,13 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     }
     if (at.on && a.w[which]) {
         const T* w = reinterpret_cast<const T*>(a.w[which]);
-        raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)), w0);
-        raw_unpack<T, VE>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w1);
+        pair_unpack<T, VE, ADJ>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                __ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
     }
+    // lanes past the row copy nothing, and read zeros
+    if (!at.on)
+#pragma unroll
+        for (int i = 0; i < 4 * D; ++i) ring[i * N] = Raw<T, VE>{};
     // the first head of unit un's first step; a unit without one is passed over
     auto first_head = [&](int64_t un) { return (int(un) & mask) << (5 - lg); };
     auto enter = [&](int64_t& un, int& h0) {
@@ -815,17 +852,10 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     LaneTurns<VE> tn;
     for (int stage = 0; un < units; stage = stage + 1 == D ? 0 : stage + 1) {
         cp_async_wait<D - 2>();
-        const bool on = h0 + at.sub < heads && at.on;
-        Raw<T, VE> x0{}, x1{}, y0{}, y1{};
-        float r = 0.f;
-        if (on) {
-            const Raw<T, VE>* from = ring + stage * 4 * N;
-            y0 = from[0];
-            y1 = from[N];
-            x0 = from[2 * N];
-            x1 = from[3 * N];
-            r = ring_r[stage * N];
-        }
+        const bool row = h0 + at.sub < heads, on = row && at.on;
+        const Raw<T, VE>* from = ring + stage * 4 * N;
+        const Raw<T, VE> y0 = from[0], y1 = from[N], x0 = from[2 * N], x1 = from[3 * N];
+        const float r = on ? ring_r[stage * N] : 0.f;
         if (fresh) {
             turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
             if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
@@ -833,18 +863,18 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
         }
         issue(stage == 0 ? D - 1 : stage - 1);
         float2 u[H], v[H], gu[H], gw[H];
-        raw_unpack<T, VE>(y0, gu);
-        raw_unpack<T, VE>(y1, gw);
-        if (at.turns) tn.turn(gu, gw, a.rope.adjacent);
-        raw_unpack<T, VE>(x0, u);
-        raw_unpack<T, VE>(x1, v);
+        pair_unpack<T, VE, ADJ>(y0, y1, gu, gw);
+        if (at.turns) tn.turn(gu, gw);
+        pair_unpack<T, VE, ADJ>(x0, x1, u, v);
         float2 sum = f2(0.f);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             gu[i] = __fmul2_rn(gu[i], f2(r));
             gw[i] = __fmul2_rn(gw[i], f2(r));
-            acc0[i] = __ffma2_rn(gu[i], u[i], acc0[i]);
-            acc1[i] = __ffma2_rn(gw[i], v[i], acc1[i]);
+            if (row) {  // (what a row past the heads reads is an earlier step's)
+                acc0[i] = __ffma2_rn(gu[i], u[i], acc0[i]);
+                acc1[i] = __ffma2_rn(gw[i], v[i], acc1[i]);
+            }
             gu[i] = __fmul2_rn(gu[i], w0[i]);
             gw[i] = __fmul2_rn(gw[i], w1[i]);
             sum = __ffma2_rn(gu[i], u[i], __ffma2_rn(gw[i], v[i], sum));
@@ -857,8 +887,10 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             gw[i] = __ffma2_rn(v[i], f2(f), gw[i]);
         }
         if (on) {
-            st_row(po, raw_pack<T, VE>(gu));
-            st_row(po + b01, raw_pack<T, VE>(gw));
+            Raw<T, VE> o0, o1;
+            pair_pack<T, VE, ADJ>(gu, gw, o0, o1);
+            st_row(po, o0);
+            st_row(po + b01, o1);
         }
         po += step_o;
         h0 += hstep;
@@ -880,8 +912,11 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             acc1[i].y += __shfl_xor_sync(0xffffffffu, acc1[i].y, o);
         }
         if (at.sub == 0 && at.on) {
-            *reinterpret_cast<float2*>(&part[warp][at.b0 + 2 * i]) = acc0[i];
-            *reinterpret_cast<float2*>(&part[warp][at.b1 + 2 * i]) = acc1[i];
+            const int e = ADJ ? at.b0 + 4 * i : at.b0 + 2 * i, f = ADJ ? e + 1 : at.b1 + 2 * i, n = ADJ ? 2 : 1;
+            part[warp][e] = acc0[i].x;
+            part[warp][e + n] = acc0[i].y;
+            part[warp][f] = acc1[i].x;
+            part[warp][f + n] = acc1[i].y;
         }
     }
     __syncthreads();
@@ -899,7 +934,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 // 2^lg lanes hold a row, NV vectors each: lane j those at j and j + per.  A warp's
 // 32 >> lg row places are 2^lhp heads of each of its tokens; every lane goes over
 // its heads lhp, 2 lhp, ... of the keys and the values, kCacheHeads at a time.
-constexpr int kCacheHeads = 2;
+constexpr int kCacheHeads = 1;
 
 struct CacheLanes {
     int lg;      // lanes of a row
@@ -911,14 +946,17 @@ struct CacheLanes {
 template <typename T, int VE, int NV>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
+    const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
     const bool on = j < cl.per;
-    const int heads = a.heads[1], group = a.cache.group, kind = a.cache.kind;
-    const int gv = group / VE;  // vectors of a group
+    const int heads = a.heads[1], group = a.cache.group;
+    const FormQ form(a.cache.kind);
+    const int packed = form.kind == NRM_CACHE_INT4;  // two elements to a byte
+    const int gv = group / VE;                       // vectors of a group
     const bool whole = group == a.d, pow2 = (gv & (gv - 1)) == 0;
     const int source = (sub << cl.lg) + j / gv * gv;  // first lane of this lane's group
     const int ltok = 5 - cl.lg - cl.lhp;              // tokens of a warp
+    const int v_next = (cl.per * VE) >> packed;       // bytes from a lane's codes of one vector to its next
     int gi[NV];
     bool leads[NV];
 #pragma unroll
@@ -927,86 +965,94 @@ cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
         leads[v] = (j + v * cl.per) * VE == gi[v] * group;
     }
     const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk;
+    const int64_t next_c = hp * a.cache.head_stride, next_s = hp * a.cache.scale_head_stride;
     for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
         int64_t slot = -1;
         if (t < a.tokens) slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
-        const CacheRow cr = cache_row(a.cache, slot < 0 ? 0 : slot, 0);
         const bool live = slot >= 0 && on;
+        int h0 = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads);
+        const CacheRow cr = cache_row(a.cache, slot < 0 ? 0 : slot, h0 + hsub);
+        const T* px[2];
+        uint8_t* pc[2];
+        float* ps[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            px[w] = reinterpret_cast<const T*>(a.x[1 + w].p) + t * a.x[1 + w].ts + (h0 + hsub) * a.x[1 + w].hs + j * VE;
+            pc[w] = a.cache.codes[w] + cr.code + ((j * VE) >> packed);
+            ps[w] = a.cache.scales[w] + cr.scale;
+        }
 #pragma unroll 1
-        for (int h0 = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads); h0 < heads;
-             h0 += (hp * kCacheHeads) << cl.lchunk) {
+        for (; h0 < heads; h0 += (hp * kCacheHeads) << cl.lchunk) {
             Raw<T, VE> raw[2][kCacheHeads][NV];
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const HeadView xv = a.x[1 + w];
-                const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + j * VE;
 #pragma unroll
                 for (int k = 0; k < kCacheHeads; ++k) {
-                    const int h = h0 + k * hp + (sub & (hp - 1));
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         raw[w][k][v] = Raw<T, VE>{};
-                        if (xv.p && live && h < heads) ld_row(x + h * xv.hs + v * cl.per * VE, raw[w][k][v]);
+                        if (a.x[1 + w].p && live && h0 + k * hp + hsub < heads)
+                            ld_row(px[w] + k * hp * a.x[1 + w].hs + v * cl.per * VE, raw[w][k][v]);
                     }
                 }
             }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                if (!a.x[1 + w].p) continue;
+                if (a.x[1 + w].p) {
 #pragma unroll
-                for (int k = 0; k < kCacheHeads; ++k) {
-                    const int h = h0 + k * hp + (sub & (hp - 1));
-                    uint32_t m[NV];
+                    for (int k = 0; k < kCacheHeads; ++k) {
+                        uint32_t m[NV];
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) m[v] = raw_mag<T, VE>(raw[w][k][v]);
-                    if (whole) {
+                        for (int v = 0; v < NV; ++v) m[v] = raw_mag<T, VE>(raw[w][k][v]);
+                        if (whole) {
 #pragma unroll
-                        for (int v = 1; v < NV; ++v) m[0] = mag_max<T>(m[0], m[v]);
-                        m[0] = row_mag<T>(m[0], cl.lg);
+                            for (int v = 1; v < NV; ++v) m[0] = mag_max<T>(m[0], m[v]);
+                            m[0] = row_mag<T>(m[0], cl.lg);
+                        } else if (pow2) {
 #pragma unroll
-                        for (int v = 1; v < NV; ++v) m[v] = m[0];
-                    } else if (pow2) {
-                        for (int o = gv >> 1; o > 0; o >>= 1)
+                            for (int i = 4; i >= 0; --i)
+                                if (1 << i < gv)
 #pragma unroll
-                            for (int v = 0; v < NV; ++v)
-                                m[v] = mag_max<T>(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
-                    } else {
+                                    for (int v = 0; v < NV; ++v)
+                                        m[v] = mag_max<T>(m[v], __shfl_xor_sync(0xffffffffu, m[v], 1 << i));
+                        } else {
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) {
-                            uint32_t all = 0;
-                            for (int i = 0; i < gv; ++i)
-                                all = mag_max<T>(all, __shfl_sync(0xffffffffu, m[v], (source + i) & 31));
-                            m[v] = all;
+                            for (int v = 0; v < NV; ++v) {
+                                uint32_t all = 0;
+                                for (int i = 0; i < gv; ++i)
+                                    all = mag_max<T>(all, __shfl_sync(0xffffffffu, m[v], (source + i) & 31));
+                                m[v] = all;
+                            }
+                        }
+                        if (live && h0 + k * hp + hsub < heads) {
+                            GroupQ q;
+#pragma unroll
+                            for (int v = 0; v < NV; ++v) {
+                                if (v == 0 || !whole) q = group_q<T>(mag_bits<T>(m[v]), form);
+                                if (leads[v]) (ps[w] + k * next_s)[gi[v]] = q.scale;
+                                store_codes<T, VE>(pc[w] + k * next_c + v * v_next, raw[w][k][v], q, form.kind);
+                            }
                         }
                     }
-                    if (!live || h >= heads) continue;
-                    uint8_t* codes = a.cache.codes[w] + cr.code + h * a.cache.head_stride;
-                    float* scales = a.cache.scales[w] + cr.scale + h * a.cache.scale_head_stride;
-                    GroupQ q;
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        if (v == 0 || !whole) q = group_q(mag_bits<T>(m[v]), kind);
-                        if (leads[v]) scales[gi[v]] = q.scale;
-                        store_codes<T, VE>(codes, (j + v * cl.per) * VE, raw[w][k][v], q, kind);
-                    }
                 }
+                px[w] += (kCacheHeads * hp * a.x[1 + w].hs) << cl.lchunk;
+                pc[w] += (kCacheHeads * next_c) << cl.lchunk;
+                ps[w] += (kCacheHeads * next_s) << cl.lchunk;
             }
         }
     }
 }
 
-// The VE codes at element e of a row, as they lie in memory.
+// VE codes, as they lie in memory.
 template <int VE>
-__device__ __forceinline__ uint2 load_codes(const uint8_t* row, int e, int kind) {
+__device__ __forceinline__ uint2 load_codes(const uint8_t* at, int kind) {
     uint2 w{0u, 0u};
     if (kind == NRM_CACHE_INT4) {
-        const uint8_t* at = row + (e >> 1);
         if constexpr (VE == 8) w.x = __ldg(reinterpret_cast<const uint32_t*>(at));
         else if constexpr (VE == 4) w.x = __ldg(reinterpret_cast<const uint16_t*>(at));
         else w.x = __ldg(at);
     } else {
-        const uint8_t* at = row + e;
         if constexpr (VE == 8) w = __ldg(reinterpret_cast<const uint2*>(at));
         else if constexpr (VE == 4) w.x = __ldg(reinterpret_cast<const uint32_t*>(at));
         else w.x = __ldg(reinterpret_cast<const uint16_t*>(at));
@@ -1047,60 +1093,69 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
 }
 
 template <typename T, int VE>
-__global__ void __launch_bounds__(kHeadWarps * 32)
+__global__ void __launch_bounds__(kHeadWarps * 32, 5)
 cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     constexpr int NV = 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
+    const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
     const bool on = j < cl.per;
-    const int heads = a.heads[1], kind = a.cache.kind;
+    const int heads = a.heads[1], kind = a.cache.kind, packed = kind == NRM_CACHE_INT4;
     const int ltok = 5 - cl.lg - cl.lhp;  // tokens of a warp
+    const int v_next = (cl.per * VE) >> packed;
     int gi[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) gi[v] = (j + v * cl.per) * VE / a.cache.group;
     const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk;
+    const int64_t next_c = hp * a.cache.head_stride, next_s = hp * a.cache.scale_head_stride;
     for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
         int64_t slot = -1;
         if (t < a.tokens) slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
         if (slot < 0 || !on) continue;
-        const CacheRow cr = cache_row(a.cache, slot, 0);
+        int h = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads) + hsub;
+        const CacheRow cr = cache_row(a.cache, slot, h);
+        const uint8_t* pc[2];
+        const float* ps[2];
+        T* py[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            pc[i] = a.cache.codes[i] + cr.code + ((j * VE) >> packed);
+            ps[i] = a.cache.scales[i] + cr.scale;
+            py[i] = reinterpret_cast<T*>(a.y[i].p) + t * a.y[i].ts + h * a.y[i].hs + j * VE;
+        }
 #pragma unroll 1
-        for (int h0 = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads) + (sub & (hp - 1)); h0 < heads;
-             h0 += (hp * kCacheHeads) << cl.lchunk) {
+        for (; h < heads; h += (hp * kCacheHeads) << cl.lchunk) {
             uint2 w[2][kCacheHeads][NV];
             float sc[2][kCacheHeads][NV];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (!a.y[i].p) continue;
 #pragma unroll
                 for (int k = 0; k < kCacheHeads; ++k) {
-                    const int h = h0 + k * hp;
-                    if (h >= heads) continue;
-                    const uint8_t* codes = a.cache.codes[i] + cr.code + h * a.cache.head_stride;
-                    const float* scales = a.cache.scales[i] + cr.scale + h * a.cache.scale_head_stride;
+                    if (a.y[i].p && h + k * hp < heads) {
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        w[i][k][v] = load_codes<VE>(codes, (j + v * cl.per) * VE, kind);
-                        sc[i][k][v] = __ldg(scales + gi[v]);
+                        for (int v = 0; v < NV; ++v) {
+                            w[i][k][v] = load_codes<VE>(pc[i] + k * next_c + v * v_next, kind);
+                            sc[i][k][v] = __ldg(ps[i] + k * next_s + gi[v]);
+                        }
                     }
                 }
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (!a.y[i].p) continue;
-                T* y = reinterpret_cast<T*>(a.y[i].p) + t * a.y[i].ts + j * VE;
 #pragma unroll
                 for (int k = 0; k < kCacheHeads; ++k) {
-                    const int h = h0 + k * hp;
-                    if (h >= heads) continue;
+                    if (a.y[i].p && h + k * hp < heads) {
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        float2 x[VE / 2];
-                        code_values<VE>(w[i][k][v], kind, sc[i][k][v], x);
-                        st_row(y + h * a.y[i].hs + v * cl.per * VE, raw_pack<T, VE>(x));
+                        for (int v = 0; v < NV; ++v) {
+                            float2 x[VE / 2];
+                            code_values<VE>(w[i][k][v], kind, sc[i][k][v], x);
+                            st_row(py[i] + k * hp * a.y[i].hs + v * cl.per * VE, raw_pack<T, VE>(x));
+                        }
                     }
                 }
+                pc[i] += (kCacheHeads * next_c) << cl.lchunk;
+                ps[i] += (kCacheHeads * next_s) << cl.lchunk;
+                py[i] += (kCacheHeads * hp * a.y[i].hs) << cl.lchunk;
             }
         }
     }
@@ -1413,10 +1468,10 @@ inline int head_chunks_log2(int64_t tokens, int steps, const DevInfo& d) {
 
 template <typename T, int VE>
 nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo& d, cudaStream_t s) {
-    const void* fn = norm ? (cache ? (const void*)&head_fwd_vec_kernel<T, VE, true, true>
-                                   : (const void*)&head_fwd_vec_kernel<T, VE, true, false>)
-                          : (cache ? (const void*)&head_fwd_vec_kernel<T, VE, false, true>
-                                   : (const void*)&head_fwd_vec_kernel<T, VE, false, false>);
+    const void* fn = a.rope.adjacent ? (cache ? (const void*)&head_fwd_vec_kernel<T, VE, true, true>
+                                              : (const void*)&head_fwd_vec_kernel<T, VE, true, false>)
+                                     : (cache ? (const void*)&head_fwd_vec_kernel<T, VE, false, true>
+                                              : (const void*)&head_fwd_vec_kernel<T, VE, false, false>);
     const size_t smem = head_fwd_smem<T, VE>();
     if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
     const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
@@ -1429,7 +1484,8 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
     int64_t ctas = ((a.tokens << lc) + kHeadWarps - 1) / kHeadWarps;
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
-    void* kargs[] = {&args, &lg, &lc};
+    int with_norm = norm;
+    void* kargs[] = {&args, &lg, &lc, &with_norm};
     return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, smem, s),
                        "head forward launch");
 }
@@ -1478,12 +1534,14 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
                     return st;
         return NRM_OK;
     }
-    const void* fn = vec == 16  ? (const void*)&head_bwd_vec_kernel<T, 16 / int(sizeof(T))>
-                     : vec == 8 ? (const void*)&head_bwd_vec_kernel<T, 8 / int(sizeof(T))>
+    constexpr int V16 = 16 / int(sizeof(T)), V8 = V16 / 2;
+    const bool adj = a.rope.adjacent;
+    const void* fn = vec == 16  ? (adj ? (const void*)&head_bwd_vec_kernel<T, V16, true>
+                                       : (const void*)&head_bwd_vec_kernel<T, V16, false>)
+                     : vec == 8 ? (adj ? (const void*)&head_bwd_vec_kernel<T, V8, true>
+                                       : (const void*)&head_bwd_vec_kernel<T, V8, false>)
                                 : (const void*)&head_bwd_scalar_kernel<T>;
-    const size_t smem = vec == 16  ? head_bwd_smem<T, 16 / int(sizeof(T))>()
-                        : vec == 8 ? head_bwd_smem<T, 8 / int(sizeof(T))>()
-                                   : 0;
+    const size_t smem = vec == 16 ? head_bwd_smem<T, V16>() : (vec == 8 ? head_bwd_smem<T, V8>() : 0);
     if (smem)
         if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
     const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
