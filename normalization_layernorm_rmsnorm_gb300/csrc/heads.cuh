@@ -177,9 +177,16 @@ __device__ __forceinline__ int64_t cache_slot(const CacheDev& c, int64_t slot, u
     return -1;
 }
 __device__ __forceinline__ CacheRow cache_row(const CacheDev& c, int64_t slot, int head) {
-    const int64_t page = row_div(slot, c.page), at = slot - page * c.page.d;
-    return CacheRow{page * c.page_stride + at * c.slot_stride + head * c.head_stride,
-                    page * c.scale_page_stride + at * c.scale_slot_stride + head * c.scale_head_stride};
+    CacheRow r{head * c.head_stride, head * c.scale_head_stride};
+    if (!c.flat) {
+        const int64_t page = row_div(slot, c.page);
+        slot -= page * c.page.d;
+        r.code += page * c.page_stride;
+        r.scale += page * c.scale_page_stride;
+    }
+    r.code += slot * c.slot_stride;
+    r.scale += slot * c.scale_slot_stride;
+    return r;
 }
 
 // Quantises the d values of `row` (of T, as floats in shared memory, visible to
@@ -301,20 +308,27 @@ __device__ __forceinline__ void pair_pack(const float2 (&u)[VE / 2], const float
     }
 }
 
-// Largest magnitudes, compared as integers: of float32 its bits, of 16-bit types
-// two at once, in the halves of a word.
+// Largest magnitudes (a NaN is the largest of all): of float32 its bits, compared
+// as integers; of 16-bit types two at once, in the halves of a word.
 template <typename T>
 __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
-    if constexpr (sizeof(T) == 4) return max(a, b);
-    else return __vmaxu2(a, b);
+    if constexpr (sizeof(T) == 4) {
+        return max(a, b & 0x7fffffffu);
+    } else if constexpr (std::is_same_v<T, __half>) {
+        const __half2 m = __hmax2_nan(*reinterpret_cast<__half2*>(&a), __habs2(*reinterpret_cast<__half2*>(&b)));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+        const __nv_bfloat162 m =
+            __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
 }
 template <typename T, int VE>
 __device__ __forceinline__ uint32_t raw_mag(const Raw<T, VE>& r) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
-    constexpr uint32_t keep = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
-    uint32_t m = w[0] & keep;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 1; i < VE * int(sizeof(T)) / 4; ++i) m = mag_max<T>(m, w[i] & keep);
+    for (int i = 0; i < VE * int(sizeof(T)) / 4; ++i) m = mag_max<T>(m, w[i]);
     return m;
 }
 // The float32 bits of what such a word holds.
@@ -324,24 +338,21 @@ __device__ __forceinline__ uint32_t mag_bits(uint32_t m) {
     else return __float_as_uint(Io<T>::load(typename Io<T>::bits_t(max(m & 0xffffu, m >> 16))));
 }
 
-// Codes of VE consecutive elements, stored at `at`.  A whole
-// number comes out of the low bits of u + 1.5 * 2^23 (the sum rounds to nearest,
-// ties to even).
+// Codes of VE consecutive elements, in the low bytes of two words.  A whole number
+// comes out of the low bits of u + 1.5 * 2^23 (the sum rounds to nearest, ties to
+// even).
 template <typename T, int VE>
-__device__ __forceinline__ void store_codes(uint8_t* at, Raw<T, VE> x, const GroupQ& q, int kind) {
+__device__ __forceinline__ uint2 make_codes(Raw<T, VE> x, const GroupQ& q, int kind) {
     if (q.r == 0.f) x = Raw<T, VE>{};  // no NaN reaches the arithmetic
     float2 u[VE / 2];
     raw_unpack<T, VE>(x, u);
 #pragma unroll
     for (int i = 0; i < VE / 2; ++i) u[i] = group_scaled2<T>(u[i], q);
+    uint32_t w[2] = {0u, 0u};
     if (kind == NRM_CACHE_E4M3) {
-        uint32_t w[(VE + 3) / 4] = {};
 #pragma unroll
         for (int i = 0; i < VE; i += 2) w[i / 4] |= e4m3x2(u[i / 2].x, u[i / 2].y) << (8 * (i % 4));
-        if constexpr (VE == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-        else if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(at) = w[0];
-        else *reinterpret_cast<uint16_t*>(at) = uint16_t(w[0]);
-        return;
+        return make_uint2(w[0], w[1]);
     }
     constexpr uint32_t magic = 0x4B400000u;  // 1.5 * 2^23
     uint32_t b[VE];
@@ -352,28 +363,50 @@ __device__ __forceinline__ void store_codes(uint8_t* at, Raw<T, VE> x, const Gro
         b[2 * i + 1] = __float_as_uint(f.y);
     }
     if (kind == NRM_CACHE_INT8) {
-        if constexpr (VE == 2) {
-            *reinterpret_cast<uint16_t*>(at) = uint16_t(__byte_perm(b[0], b[1], 0x0040));
-        } else {
-            uint32_t w[VE / 4];
 #pragma unroll
-            for (int i = 0; i < VE / 4; ++i)
-                w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
-                                   __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
-            if constexpr (VE == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t*>(at) = w[0];
+        for (int i = 0; i < VE; i += 2) {
+            const uint32_t two = __byte_perm(b[i], b[i + 1], 0x0040);
+            w[i / 4] = i % 4 ? __byte_perm(w[i / 4], two, 0x5410) : two;
         }
+        if constexpr (VE == 2) w[0] &= 0xffffu;
     } else {
         // sum of code_i * 16^i: the constants come off at the end, and with 8 added to
         // each code no digit borrows from the next
         constexpr uint32_t ones = VE == 8 ? 0x11111111u : (VE == 4 ? 0x1111u : 0x11u);
-        uint32_t w = b[VE - 1];
+        uint32_t d = b[VE - 1];
 #pragma unroll
-        for (int i = VE - 2; i >= 0; --i) w = w * 16 + b[i];
-        w = (w - magic * ones + 8 * ones) ^ (8 * ones);
-        if constexpr (VE == 8) *reinterpret_cast<uint32_t*>(at) = w;
-        else if constexpr (VE == 4) *reinterpret_cast<uint16_t*>(at) = uint16_t(w);
-        else *at = uint8_t(w);
+        for (int i = VE - 2; i >= 0; --i) d = d * 16 + b[i];
+        w[0] = (d - magic * ones + 8 * ones) ^ (8 * ones);
+    }
+    return make_uint2(w[0], w[1]);
+}
+// Stores (loads) `bytes` of 1, 2, 4 or 8 bytes at an address aligned to them.
+__device__ __forceinline__ void st_bytes(uint8_t* at, uint2 w, int bytes) {
+    if (bytes == 8) *reinterpret_cast<uint2*>(at) = w;
+    else if (bytes == 4) *reinterpret_cast<uint32_t*>(at) = w.x;
+    else if (bytes == 2) *reinterpret_cast<uint16_t*>(at) = uint16_t(w.x);
+    else *at = uint8_t(w.x);
+}
+template <typename T, int VE>
+__device__ __forceinline__ void store_codes(uint8_t* at, Raw<T, VE> x, const GroupQ& q, int kind) {
+    const uint2 w = make_codes<T, VE>(x, q, kind);
+    if (kind == NRM_CACHE_INT4) st_bytes(at, w, VE / 2);
+    else st_bytes(at, w, VE);
+}
+// The codes of two neighbouring vectors.
+template <typename T, int VE>
+__device__ __forceinline__ void store_codes_twice(uint8_t* at, const Raw<T, VE> (&x)[2], const GroupQ& q, int kind) {
+    const uint2 a = make_codes<T, VE>(x[0], q, kind), b = make_codes<T, VE>(x[1], q, kind);
+    if (kind == NRM_CACHE_INT4) {
+        constexpr int bits = 4 * VE;
+        if constexpr (VE == 8) st_bytes(at, make_uint2(a.x, b.x), 8);
+        else st_bytes(at, make_uint2(a.x | b.x << (bits % 32), 0u), VE);
+    } else if constexpr (VE == 8) {
+        *reinterpret_cast<uint4*>(at) = make_uint4(a.x, a.y, b.x, b.y);
+    } else if constexpr (VE == 4) {
+        st_bytes(at, make_uint2(a.x, b.x), 8);
+    } else {
+        st_bytes(at, make_uint2(a.x | b.x << 16, 0u), 4);
     }
 }
 
@@ -576,6 +609,12 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
     const FormQ form(CACHE ? a.cache.kind : 0);
     const int packed = form.kind == NRM_CACHE_INT4;  // two elements to a byte
+    int meet_lanes = 0;  // lanes whose vectors are a group, where these are neighbours and a power of two
+    if (CACHE) {
+        const int gv = a.cache.group / VE, n = ADJ ? gv / 2 : gv;
+        const bool order = ADJ ? gv % 2 == 0 : (a.rope.rot == a.d && a.d / (2 * VE) % gv == 0);
+        if (order && (n & (n - 1)) == 0) meet_lanes = n;
+    }
 
     // lanes past the row copy nothing, and read zeros
     if (!at.on)
@@ -626,6 +665,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     T* py = nullptr;
     float* pr = nullptr;
     int64_t row_y = 0, slot = -1;
+    CacheRow cr{0, 0};
     bool out = false;
     for (int stage = 0; cur.live(); stage = stage + 1 == D ? 0 : stage + 1) {
         cp_async_wait<D - 2>();
@@ -640,7 +680,10 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
         if (cur.fresh) {
             turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
             if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
-            if (CACHE) slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
+            if (CACHE) {
+                slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
+                if (slot >= 0) cr = cache_row(a.cache, slot, 0);
+            }
             __syncwarp();
         }
         issue(stage == 0 ? D - 1 : stage - 1);
@@ -714,6 +757,16 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
                     uint32_t m0 = raw_mag<T, VE>(x0[k]), m1 = raw_mag<T, VE>(x1[k]);
                     if (group == a.d) {
                         m0 = m1 = row_mag<T>(at.on ? mag_max<T>(m0, m1) : 0u, lg);
+                    } else if (meet_lanes > 0) {
+                        // a group is one vector each of so many neighbouring lanes, or (ADJ) two
+                        if (ADJ) m0 = m1 = mag_max<T>(m0, m1);
+#pragma unroll
+                        for (int i = 4; i >= 0; --i)
+                            if (1 << i < meet_lanes) {
+                                m0 = mag_max<T>(m0, __shfl_xor_sync(0xffffffffu, m0, 1 << i));
+                                if (!ADJ) m1 = mag_max<T>(m1, __shfl_xor_sync(0xffffffffu, m1, 1 << i));
+                            }
+                        if (ADJ) m1 = m0;
                     } else {
                         // groups of whole vectors, which other lanes may hold: through shared memory
                         uint32_t* sm = s_max[warp] + at.sub * (a.d / VE);
@@ -732,13 +785,13 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
                         __syncwarp();
                     }
                     if (at.on && h + k * rows < heads) {
-                        const CacheRow cr = cache_row(a.cache, slot, h + k * rows);
+                        const int hk = h + k * rows;
                         const GroupQ q0 = group_q<T>(mag_bits<T>(m0), form);
                         const GroupQ q1 = group == a.d ? q0 : group_q<T>(mag_bits<T>(m1), form);
-                        float* scales = a.cache.scales[which - 1] + cr.scale;
+                        float* scales = a.cache.scales[which - 1] + cr.scale + hk * a.cache.scale_head_stride;
                         if (at.b0 == g0 * group) scales[g0] = q0.scale;
                         if (at.b1 == g1 * group) scales[g1] = q1.scale;
-                        uint8_t* codes = a.cache.codes[which - 1] + cr.code;
+                        uint8_t* codes = a.cache.codes[which - 1] + cr.code + hk * a.cache.head_stride;
                         store_codes<T, VE>(codes + (at.b0 >> packed), x0[k], q0, form.kind);
                         store_codes<T, VE>(codes + (at.b1 >> packed), x1[k], q1, form.kind);
                     }
@@ -931,114 +984,112 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 // ---------------------------------------------------------------------------
 // cache rows on vectors
 // ---------------------------------------------------------------------------
-// 2^lg lanes hold a row, NV vectors each: lane j those at j and j + per.  A warp's
-// 32 >> lg row places are 2^lhp heads of each of its tokens; every lane goes over
-// its heads lhp, 2 lhp, ... of the keys and the values, kCacheHeads at a time.
-constexpr int kCacheHeads = 1;
-
+// 2^lg lanes hold a row, one or two vectors each.  A warp's 32 >> lg row
+// places are 2^lhp heads of each of its tokens; every lane goes over its heads,
+// 2^lhp apart, a key and a value at a time.
 struct CacheLanes {
     int lg;      // lanes of a row
     int per;     // lanes of them that hold vectors
     int lhp;     // heads of a token that the warp holds at once
     int lchunk;  // a token's heads are split over 2^lchunk warps
+    int gl;      // writing: lanes of a group
+    int wide;    // writing: a lane's 32 bytes are aligned to them
 };
 
+// 32 bytes at once, where they are aligned (every lane then fills whole sectors).
+__device__ __forceinline__ void ld_row_wide(const void* p, uint4 (&r)[2]) {
+    asm volatile("ld.global.L1::no_allocate.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0].x), "=r"(r[0].y), "=r"(r[0].z), "=r"(r[0].w), "=r"(r[1].x), "=r"(r[1].y), "=r"(r[1].z),
+                   "=r"(r[1].w)
+                 : "l"(p) : "memory");
+}
+// A lane's vectors are neighbours: a group is then fewer lanes, and a lane makes
+// one scale for both.
 template <typename T, int VE, int NV>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
+    constexpr int E = NV * VE;  // elements of a lane
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
     const bool on = j < cl.per;
     const int heads = a.heads[1], group = a.cache.group;
     const FormQ form(a.cache.kind);
     const int packed = form.kind == NRM_CACHE_INT4;  // two elements to a byte
-    const int gv = group / VE;                       // vectors of a group
-    const bool whole = group == a.d, pow2 = (gv & (gv - 1)) == 0;
-    const int source = (sub << cl.lg) + j / gv * gv;  // first lane of this lane's group
-    const int ltok = 5 - cl.lg - cl.lhp;              // tokens of a warp
-    const int v_next = (cl.per * VE) >> packed;       // bytes from a lane's codes of one vector to its next
-    int gi[NV];
-    bool leads[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        gi[v] = (j + v * cl.per) * VE / group;
-        leads[v] = (j + v * cl.per) * VE == gi[v] * group;
-    }
-    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk;
-    const int64_t next_c = hp * a.cache.head_stride, next_s = hp * a.cache.scale_head_stride;
-    for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
+    const bool whole = group == a.d, pow2 = (cl.gl & (cl.gl - 1)) == 0;
+    const int source = (sub << cl.lg) + (whole ? 0 : j / cl.gl * cl.gl);  // first lane of this lane's group
+    const int gi = j * E / group;
+    const bool leads = j * E == gi * group;
+    const int ltok = 5 - cl.lg - cl.lhp;  // tokens of a warp
+    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, stride = int64_t(gridDim.x) * kHeadWarps;
+    // neither a token's slot nor its rows wait for one another: the slot was asked for a unit ago
+    auto ask = [&](int64_t un) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
-        int64_t slot = -1;
-        if (t < a.tokens) slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
-        const bool live = slot >= 0 && on;
-        int h0 = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads);
+        return un < units && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
+    };
+    int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp;
+    int64_t asked = ask(un);
+    for (; un < units; un += stride) {
+        const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
+        const int64_t slot = cache_slot(a.cache, asked, a.err);
+        asked = ask(un + stride);
+        const bool live = t < a.tokens && on;
+        int h0 = (int(un) & ((1 << cl.lchunk) - 1)) << cl.lhp;
         const CacheRow cr = cache_row(a.cache, slot < 0 ? 0 : slot, h0 + hsub);
         const T* px[2];
         uint8_t* pc[2];
         float* ps[2];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            px[w] = reinterpret_cast<const T*>(a.x[1 + w].p) + t * a.x[1 + w].ts + (h0 + hsub) * a.x[1 + w].hs + j * VE;
-            pc[w] = a.cache.codes[w] + cr.code + ((j * VE) >> packed);
-            ps[w] = a.cache.scales[w] + cr.scale;
+            px[w] = reinterpret_cast<const T*>(a.x[1 + w].p) + t * a.x[1 + w].ts + (h0 + hsub) * a.x[1 + w].hs + j * E;
+            pc[w] = a.cache.codes[w] + cr.code + ((j * E) >> packed);
+            ps[w] = a.cache.scales[w] + cr.scale + gi;
         }
 #pragma unroll 1
-        for (; h0 < heads; h0 += (hp * kCacheHeads) << cl.lchunk) {
-            Raw<T, VE> raw[2][kCacheHeads][NV];
+        for (; h0 < heads; h0 += hp << cl.lchunk) {
+            Raw<T, VE> raw[2][NV];
+            const bool here = live && h0 + hsub < heads;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
 #pragma unroll
-                for (int k = 0; k < kCacheHeads; ++k) {
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        raw[w][k][v] = Raw<T, VE>{};
-                        if (a.x[1 + w].p && live && h0 + k * hp + hsub < heads)
-                            ld_row(px[w] + k * hp * a.x[1 + w].hs + v * cl.per * VE, raw[w][k][v]);
+                for (int v = 0; v < NV; ++v) raw[w][v] = Raw<T, VE>{};
+                if (a.x[1 + w].p && here) {
+                    if constexpr (NV * VE * sizeof(T) == 32) {
+                        if (cl.wide) {
+                            ld_row_wide(px[w], raw[w]);
+                            continue;
+                        }
                     }
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) ld_row(px[w] + v * VE, raw[w][v]);
                 }
             }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 if (a.x[1 + w].p) {
+                    uint32_t m = raw_mag<T, VE>(raw[w][0]);
+                    if constexpr (NV == 2) m = mag_max<T>(m, raw_mag<T, VE>(raw[w][1]));
+                    if (whole) {
+                        m = row_mag<T>(m, cl.lg);
+                    } else if (pow2) {
 #pragma unroll
-                    for (int k = 0; k < kCacheHeads; ++k) {
-                        uint32_t m[NV];
-#pragma unroll
-                        for (int v = 0; v < NV; ++v) m[v] = raw_mag<T, VE>(raw[w][k][v]);
-                        if (whole) {
-#pragma unroll
-                            for (int v = 1; v < NV; ++v) m[0] = mag_max<T>(m[0], m[v]);
-                            m[0] = row_mag<T>(m[0], cl.lg);
-                        } else if (pow2) {
-#pragma unroll
-                            for (int i = 4; i >= 0; --i)
-                                if (1 << i < gv)
-#pragma unroll
-                                    for (int v = 0; v < NV; ++v)
-                                        m[v] = mag_max<T>(m[v], __shfl_xor_sync(0xffffffffu, m[v], 1 << i));
-                        } else {
-#pragma unroll
-                            for (int v = 0; v < NV; ++v) {
-                                uint32_t all = 0;
-                                for (int i = 0; i < gv; ++i)
-                                    all = mag_max<T>(all, __shfl_sync(0xffffffffu, m[v], (source + i) & 31));
-                                m[v] = all;
-                            }
-                        }
-                        if (live && h0 + k * hp + hsub < heads) {
-                            GroupQ q;
-#pragma unroll
-                            for (int v = 0; v < NV; ++v) {
-                                if (v == 0 || !whole) q = group_q<T>(mag_bits<T>(m[v]), form);
-                                if (leads[v]) (ps[w] + k * next_s)[gi[v]] = q.scale;
-                                store_codes<T, VE>(pc[w] + k * next_c + v * v_next, raw[w][k][v], q, form.kind);
-                            }
-                        }
+                        for (int i = 4; i >= 0; --i)
+                            if (1 << i < cl.gl) m = mag_max<T>(m, __shfl_xor_sync(0xffffffffu, m, 1 << i));
+                    } else {
+                        uint32_t all = 0;
+                        for (int i = 0; i < cl.gl; ++i)
+                            all = mag_max<T>(all, __shfl_sync(0xffffffffu, m, (source + i) & 31));
+                        m = all;
+                    }
+                    if (here && slot >= 0) {
+                        const GroupQ q = group_q<T>(mag_bits<T>(m), form);
+                        if (leads) *ps[w] = q.scale;
+                        if constexpr (NV == 2) store_codes_twice<T, VE>(pc[w], raw[w], q, form.kind);
+                        else store_codes<T, VE>(pc[w], raw[w][0], q, form.kind);
                     }
                 }
-                px[w] += (kCacheHeads * hp * a.x[1 + w].hs) << cl.lchunk;
-                pc[w] += (kCacheHeads * next_c) << cl.lchunk;
-                ps[w] += (kCacheHeads * next_s) << cl.lchunk;
+                px[w] += (hp * a.x[1 + w].hs) << cl.lchunk;
+                pc[w] += (hp * a.cache.head_stride) << cl.lchunk;
+                ps[w] += (hp * a.cache.scale_head_stride) << cl.lchunk;
             }
         }
     }
@@ -1092,6 +1143,9 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
     }
 }
 
+// A lane's two vectors are here those at j and j + per: each store of a warp then
+// covers whole lines (two neighbouring vectors a lane, stored 32 bytes at once,
+// were slower: 122 against 116 us for 131072 tokens of 8 heads of 128 in 4 bits).
 template <typename T, int VE>
 __global__ void __launch_bounds__(kHeadWarps * 32, 5)
 cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
@@ -1105,14 +1159,19 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     int gi[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) gi[v] = (j + v * cl.per) * VE / a.cache.group;
-    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk;
-    const int64_t next_c = hp * a.cache.head_stride, next_s = hp * a.cache.scale_head_stride;
-    for (int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp; un < units; un += int64_t(gridDim.x) * kHeadWarps) {
+    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, stride = int64_t(gridDim.x) * kHeadWarps;
+    auto ask = [&](int64_t un) {  // a token's slot, asked for a unit ahead
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
-        int64_t slot = -1;
-        if (t < a.tokens) slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
+        return un < units && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
+    };
+    int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp;
+    int64_t asked = ask(un);
+    for (; un < units; un += stride) {
+        const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
+        const int64_t slot = cache_slot(a.cache, asked, a.err);
+        asked = ask(un + stride);
         if (slot < 0 || !on) continue;
-        int h = (int(un) & ((1 << cl.lchunk) - 1)) * (hp * kCacheHeads) + hsub;
+        int h = ((int(un) & ((1 << cl.lchunk) - 1)) << cl.lhp) + hsub;
         const CacheRow cr = cache_row(a.cache, slot, h);
         const uint8_t* pc[2];
         const float* ps[2];
@@ -1124,38 +1183,32 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
             py[i] = reinterpret_cast<T*>(a.y[i].p) + t * a.y[i].ts + h * a.y[i].hs + j * VE;
         }
 #pragma unroll 1
-        for (; h < heads; h += (hp * kCacheHeads) << cl.lchunk) {
-            uint2 w[2][kCacheHeads][NV];
-            float sc[2][kCacheHeads][NV];
+        for (; h < heads; h += hp << cl.lchunk) {
+            uint2 w[2][NV];
+            float sc[2][NV];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                if (a.y[i].p) {
 #pragma unroll
-                for (int k = 0; k < kCacheHeads; ++k) {
-                    if (a.y[i].p && h + k * hp < heads) {
-#pragma unroll
-                        for (int v = 0; v < NV; ++v) {
-                            w[i][k][v] = load_codes<VE>(pc[i] + k * next_c + v * v_next, kind);
-                            sc[i][k][v] = __ldg(ps[i] + k * next_s + gi[v]);
-                        }
+                    for (int v = 0; v < NV; ++v) {
+                        w[i][v] = load_codes<VE>(pc[i] + v * v_next, kind);
+                        sc[i][v] = __ldg(ps[i] + gi[v]);
                     }
                 }
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                if (a.y[i].p) {
 #pragma unroll
-                for (int k = 0; k < kCacheHeads; ++k) {
-                    if (a.y[i].p && h + k * hp < heads) {
-#pragma unroll
-                        for (int v = 0; v < NV; ++v) {
-                            float2 x[VE / 2];
-                            code_values<VE>(w[i][k][v], kind, sc[i][k][v], x);
-                            st_row(py[i] + k * hp * a.y[i].hs + v * cl.per * VE, raw_pack<T, VE>(x));
-                        }
+                    for (int v = 0; v < NV; ++v) {
+                        float2 x[VE / 2];
+                        code_values<VE>(w[i][v], kind, sc[i][v], x);
+                        st_row(py[i] + v * cl.per * VE, raw_pack<T, VE>(x));
                     }
                 }
-                pc[i] += (kCacheHeads * next_c) << cl.lchunk;
-                ps[i] += (kCacheHeads * next_s) << cl.lchunk;
-                py[i] += (kCacheHeads * hp * a.y[i].hs) << cl.lchunk;
+                pc[i] += (hp * a.cache.head_stride) << cl.lchunk;
+                ps[i] += (hp * a.cache.scale_head_stride) << cl.lchunk;
+                py[i] += (hp * a.y[i].hs) << cl.lchunk;
             }
         }
     }
@@ -1592,17 +1645,20 @@ nrm_status cache_launch_scalar(const HeadArgs& a, const void* fn, bool both, con
                        "cache launch");
 }
 
-// `lanes` lanes of a row hold vectors.
-inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes, const DevInfo& d, cudaStream_t s) {
+// `lanes` lanes of a row hold vectors, `gl` of them a group.
+inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes, int gl, bool wide, const DevInfo& d,
+                                   cudaStream_t s) {
     const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "cache kernel cannot be resident");
     CacheLanes cl{};
     cl.lg = row_lanes_log2(lanes);
     cl.per = lanes;
+    cl.gl = gl;
+    cl.wide = wide;
     while (cl.lhp < 5 - cl.lg && (1 << cl.lhp) < a.heads[1]) ++cl.lhp;
-    const int ltok = 5 - cl.lg - cl.lhp, per = kCacheHeads << cl.lhp;
+    const int ltok = 5 - cl.lg - cl.lhp;
     const int64_t blocks = (a.tokens + (1 << ltok) - 1) >> ltok;
-    cl.lchunk = head_chunks_log2(blocks, (a.heads[1] + per - 1) / per, d);
+    cl.lchunk = head_chunks_log2(blocks, (a.heads[1] + (1 << cl.lhp) - 1) >> cl.lhp, d);
     int64_t ctas = ((blocks << cl.lchunk) + kHeadWarps - 1) / kHeadWarps;
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
@@ -1610,16 +1666,28 @@ inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes,
     return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, 0, s), "cache launch");
 }
 
-// Two vectors of a row to a lane, where every group lies within the first ones,
-// within the second ones, or is the row (its magnitudes then meet by shuffles);
-// else one, where a warp holds the row.
+// Whether rows start on 32 bytes in every given view.
+template <typename T>
+bool rows_on_32(const HeadView (&views)[2], int64_t tokens, int heads) {
+    constexpr int64_t n = 32 / int64_t(sizeof(T));
+    for (const HeadView& v : views)
+        if (v.p && (reinterpret_cast<uintptr_t>(v.p) % 32 || (tokens > 1 && v.ts % n) || (heads > 1 && v.hs % n)))
+            return false;
+    return true;
+}
+
+// Two vectors of a row to a lane, where every group is whole lanes; else one,
+// where a warp holds the row.
 template <typename T, int BYTES>
 nrm_status cache_write_vec(const HeadArgs& a, const DevInfo& d, cudaStream_t s) {
     constexpr int VE = BYTES / int(sizeof(T));
-    const int half = a.d / (2 * VE);
-    if (a.cache.group == a.d || half % (a.cache.group / VE) == 0)
-        return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 2>, half, d, s);
-    if (2 * half <= 32) return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 1>, 2 * half, d, s);
+    const int nvec = a.d / VE, gv = a.cache.group / VE;
+    const HeadView views[2] = {a.x[1], a.x[2]};
+    if (gv % 2 == 0)
+        return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 2>, nvec / 2, gv / 2,
+                                rows_on_32<T>(views, a.tokens, a.heads[1]), d, s);
+    if (nvec <= 32)
+        return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 1>, nvec, gv, false, d, s);
     return cache_launch_scalar<T>(a, (const void*)&cache_write_scalar_kernel<T>, a.x[1].p && a.x[2].p, d, s);
 }
 
@@ -1646,7 +1714,7 @@ nrm_status cache_read(const HeadArgs& a, int vec, cudaStream_t s) {
         const int ve = vec / int(sizeof(T));
         return cache_launch_vec(args, vec == 16 ? (const void*)&cache_read_vec_kernel<T, 16 / int(sizeof(T))>
                                                 : (const void*)&cache_read_vec_kernel<T, 8 / int(sizeof(T))>,
-                                a.d / (2 * ve), *d, s);
+                                a.d / (2 * ve), 0, false, *d, s);
     }
     return cache_launch_scalar<T>(args, (const void*)&cache_read_scalar_kernel<T>, a.y[0].p && a.y[1].p, *d, s);
 }

@@ -51,6 +51,7 @@ struct CacheDev {
     float* scales[2];
     int64_t slots;       // pages * page_size
     RowDiv page;         // by page_size
+    int flat;            // pages follow one another slot by slot: a slot's place needs no division
     int64_t page_stride, slot_stride, head_stride;
     int64_t scale_page_stride, scale_slot_stride, scale_head_stride;
     int group;

@@ -154,6 +154,8 @@ nrm_status set_cache(const nrm_kv_cache* c, bool keys, bool values, CacheDev* ou
     out->scales[1] = c->v_scales;
     out->slots = c->pages * c->page_size;
     out->page = make_row_div(c->page_size, c->pages * c->page_size);
+    out->flat = (c->pages == 1 || c->page_stride == c->page_size * c->slot_stride) &&
+                (c->pages == 1 || c->scale_page_stride == c->page_size * c->scale_slot_stride);
     out->page_stride = c->page_stride;
     out->slot_stride = c->slot_stride;
     out->head_stride = c->head_stride;
@@ -173,9 +175,10 @@ nrm_status check_slots(const int64_t* slots, int64_t tokens) {
 
 // The widest accesses (16 or 8 bytes; 0: single elements) that fit the views,
 // the weights, rows of whole pairs of vectors (at most 32 pairs), and, where
-// there is one, the cache's groups and rows of codes.
+// there is one, the cache's groups and rows of codes (`vectors` vectors' codes
+// are moved at once).
 int fits_vec(std::initializer_list<const nrm_heads*> views, std::initializer_list<const void*> ptrs, int64_t tokens,
-             int64_t d, const RopeDev& r, nrm_dtype dt, const nrm_kv_cache* c = nullptr) {
+             int64_t d, const RopeDev& r, nrm_dtype dt, const nrm_kv_cache* c = nullptr, int vectors = 1) {
     for (int bytes = 16; bytes >= 8; bytes /= 2) {
         const int64_t v = bytes / int64_t(dsize(dt));
         bool ok = d % (2 * v) == 0 && d / (2 * v) <= 32 && r.rot % (2 * v) == 0;
@@ -185,7 +188,8 @@ int fits_vec(std::initializer_list<const nrm_heads*> views, std::initializer_lis
                 ok = false;
         for (const void* p : ptrs) ok = ok && aligned(p, size_t(bytes));
         if (c) {
-            const int64_t b = c->kind == NRM_CACHE_INT4 ? v / 2 : v;  // bytes of a vector's codes
+            // bytes of the codes that a lane stores or loads at once
+            const int64_t b = vectors * (c->kind == NRM_CACHE_INT4 ? v / 2 : v);
             ok = ok && c->group % v == 0 && aligned(c->k_codes, size_t(b)) && aligned(c->v_codes, size_t(b)) &&
                  (c->pages == 1 || c->page_stride % b == 0) && (c->page_size == 1 || c->slot_stride % b == 0) &&
                  (c->heads == 1 || c->head_stride % b == 0);
@@ -395,7 +399,7 @@ nrm_status nrm_kv_cache_write(const nrm_heads* k, const nrm_heads* v, const nrm_
         a.heads[1] = int(cache->heads);
         a.d = int(cache->d);
         a.slots = slots;
-        const int vec = fits_vec({k, v}, {}, tokens, a.d, a.rope, dt, cache);
+        const int vec = fits_vec({k, v}, {}, tokens, a.d, a.rope, dt, cache, 2);
         return by_dtype(dt, [&](auto tag) {
             return cache_write<decltype(tag)>(a, vec, reinterpret_cast<cudaStream_t>(stream));
         });
