@@ -460,25 +460,63 @@ struct WarpTurns {
     }
 };
 
-// A lane's VE angles (the sines with both signs: a packed instruction has no negation).
+// A lane's VE angles.
 template <int VE>
 struct LaneTurns {
-    float2 c[VE / 2], s[VE / 2], n[VE / 2];
+    float2 c[VE / 2], s[VE / 2];
     __device__ __forceinline__ void take(const float* cos, const float* sin) {
 #pragma unroll
         for (int i = 0; i < VE / 2; ++i) {
             c[i] = *reinterpret_cast<const float2*>(cos + 2 * i);
             s[i] = *reinterpret_cast<const float2*>(sin + 2 * i);
-            n[i] = f2neg(s[i]);
         }
     }
-    // Turns the lane's pairs.
+    // Turns the lane's pairs.  (The packed instruction cannot negate: one product is scalar.)
     __device__ __forceinline__ void turn(float2 (&u)[VE / 2], float2 (&v)[VE / 2]) const {
 #pragma unroll
         for (int i = 0; i < VE / 2; ++i) {
-            const float2 a = __ffma2_rn(v[i], n[i], __fmul2_rn(u[i], c[i]));
-            v[i] = __ffma2_rn(u[i], s[i], __fmul2_rn(v[i], c[i]));
-            u[i] = a;
+            const float2 a = __fmul2_rn(u[i], c[i]);
+            const float2 b = __ffma2_rn(u[i], s[i], __fmul2_rn(v[i], c[i]));
+            u[i] = make_float2(fmaf(-v[i].x, s[i].x, a.x), fmaf(-v[i].y, s[i].y, a.y));
+            v[i] = b;
+        }
+    }
+};
+
+// The forward's row map of a lane: the weights w0, w1 of its pairs' two elements
+// and their turn in one, (u, v) -> (uu u + uv v, vu u + vv v), uu = w0 cos, uv =
+// -w1 sin, vu = w0 sin, vv = w1 cos.  Made once for a token's rows of a tensor,
+// and fewer registers than weights and angles.
+template <int VE>
+struct LaneMap {
+    float2 uu[VE / 2], uv[VE / 2], vu[VE / 2], vv[VE / 2];
+    // w0, w1 on entry in uu, vv.
+    __device__ __forceinline__ void turned(const float* cos, const float* sin) {
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+            const float2 c = *reinterpret_cast<const float2*>(cos + 2 * i);
+            const float2 s = *reinterpret_cast<const float2*>(sin + 2 * i);
+            uv[i] = __fmul2_rn(vv[i], f2neg(s));
+            vu[i] = __fmul2_rn(uu[i], s);
+            uu[i] = __fmul2_rn(uu[i], c);
+            vv[i] = __fmul2_rn(vv[i], c);
+        }
+    }
+    // (`turns`: elements past the rotated part are their own, whatever their partner holds)
+    __device__ __forceinline__ void apply(float2 (&u)[VE / 2], float2 (&v)[VE / 2], bool turns) const {
+        if (turns) {
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) {
+                const float2 a = __ffma2_rn(v[i], uv[i], __fmul2_rn(u[i], uu[i]));
+                v[i] = __ffma2_rn(u[i], vu[i], __fmul2_rn(v[i], vv[i]));
+                u[i] = a;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) {
+                u[i] = __fmul2_rn(u[i], uu[i]);
+                v[i] = __fmul2_rn(v[i], vv[i]);
+            }
         }
     }
 };
@@ -505,7 +543,7 @@ __device__ __forceinline__ uint32_t row_mag(uint32_t m, int lg) {
 // other lane reads, a step or more ahead, so the bytes in flight do not
 // depend on registers or occupancy and no barrier is needed: the lane waits for
 // its own copies.
-constexpr int kHeadStages = 4;  // backward
+constexpr int kHeadStages = 3;  // backward
 
 template <int BYTES>
 __device__ __forceinline__ void cp_async(void* dst, const void* src) {
@@ -659,9 +697,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
 
-    LaneTurns<VE> tn;
-    float2 w0[H], w1[H];
-    int have = -1;  // the tensor whose weights are in registers
+    LaneMap<VE> map;
     T* py = nullptr;
     float* pr = nullptr;
     int64_t row_y = 0, slot = -1;
@@ -679,7 +715,6 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
         }
         if (cur.fresh) {
             turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
-            if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
             if (CACHE) {
                 slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
                 if (slot >= 0) cr = cache_row(a.cache, slot, 0);
@@ -693,25 +728,25 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             py = reinterpret_cast<T*>(v.p) + t * v.ts + h * v.hs + at.b0;
             row_y = rows * v.hs;
             out = v.p && at.on;
+#pragma unroll
+            for (int i = 0; i < H; ++i) map.uu[i] = map.vv[i] = f2(1.f);
             if (norm) {
                 pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
-                if (which != have) {
-                    have = which;
-#pragma unroll
-                    for (int i = 0; i < H; ++i) w0[i] = w1[i] = f2(1.f);
-                    const T* w = reinterpret_cast<const T*>(a.w[which]);
-                    if (w && at.on)
-                        pair_unpack<T, VE, ADJ>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
-                                                __ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
-                }
+                const T* w = reinterpret_cast<const T*>(a.w[which]);
+                if (w && at.on)
+                    pair_unpack<T, VE, ADJ>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                            __ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), map.uu, map.vv);
             }
+            if (at.turns) map.turned(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
         }
         if (which < 2) {
             float2 u[R][H], v[R][H];
 #pragma unroll
             for (int k = 0; k < R; ++k) pair_unpack<T, VE, ADJ>(x0[k], x1[k], u[k], v[k]);
+            float r[R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) r[k] = 1.f;
             if (norm) {
-                float r[R];
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     float2 sq = f2(0.f);
@@ -722,18 +757,17 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 #pragma unroll
                 for (int k = 0; k < R; ++k) r[k] = rsqrtf(fmaf(row_sum(r[k], lg), inv_d, a.eps));
 #pragma unroll
-                for (int k = 0; k < R; ++k) {
+                for (int k = 0; k < R; ++k)
                     if (pr && h + k * rows < heads) pr[k * rows] = r[k];
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        u[k][i] = __fmul2_rn(__fmul2_rn(u[k][i], f2(r[k])), w0[i]);
-                        v[k][i] = __fmul2_rn(__fmul2_rn(v[k][i], f2(r[k])), w1[i]);
-                    }
-                }
             }
-            if (at.turns) {
 #pragma unroll
-                for (int k = 0; k < R; ++k) tn.turn(u[k], v[k]);
+            for (int k = 0; k < R; ++k) {
+                map.apply(u[k], v[k], at.turns);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    u[k][i] = __fmul2_rn(u[k][i], f2(r[k]));
+                    v[k][i] = __fmul2_rn(v[k][i], f2(r[k]));
+                }
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
