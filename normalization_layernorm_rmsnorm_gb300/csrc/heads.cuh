@@ -622,22 +622,23 @@ private:
     }
 };
 
-constexpr int kHeadRows = 2;    // rows of a lane in a step
-constexpr int kHeadFwdStages = 3;
+constexpr int kHeadRows = 2;      // rows of a lane in a step
+constexpr int kHeadFwdWarps = 4;  // warps of a CTA
+constexpr int kHeadFwdStages = 4;
 
 template <typename T, int VE>
 constexpr size_t head_fwd_smem() {
-    return size_t(kHeadFwdStages) * 2 * kHeadRows * kHeadWarps * 32 * VE * sizeof(T);
+    return size_t(kHeadFwdStages) * 2 * kHeadRows * kHeadFwdWarps * 32 * VE * sizeof(T);
 }
 
 template <typename T, int VE, bool ADJ, bool CACHE>
-__global__ void __launch_bounds__(kHeadWarps * 32, 2)
+__global__ void __launch_bounds__(kHeadFwdWarps * 32, 3)
 head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int norm) {
-    constexpr int H = VE / 2, D = kHeadFwdStages, R = kHeadRows, N = kHeadWarps * 32, BYTES = VE * int(sizeof(T));
+    constexpr int H = VE / 2, D = kHeadFwdStages, R = kHeadRows, N = kHeadFwdWarps * 32, BYTES = VE * int(sizeof(T));
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
-    __shared__ TokenWords s_tok[kHeadWarps][D];
-    __shared__ uint32_t s_max[CACHE ? kHeadWarps : 1][CACHE ? 64 : 1];
+    __shared__ __align__(16) float s_cos[kHeadFwdWarps][kHeadMaxPairs], s_sin[kHeadFwdWarps][kHeadMaxPairs];
+    __shared__ TokenWords s_tok[kHeadFwdWarps][D];
+    __shared__ uint32_t s_max[CACHE ? kHeadFwdWarps : 1][CACHE ? 64 : 1];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
@@ -662,8 +663,8 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     in.lper = 5 - lg + (R == 2 ? 1 : 0);
     in.lchunk = lchunk;
     in.units = a.tokens << lchunk;
-    in.stride = int64_t(gridDim.x) * kHeadWarps;
-    in.start(a, int64_t(blockIdx.x) * kHeadWarps + warp);
+    in.stride = int64_t(gridDim.x) * kHeadFwdWarps;
+    in.start(a, int64_t(blockIdx.x) * kHeadFwdWarps + warp);
     StepWalk<CACHE ? 3 : 2> cur = in;
 
     const T* px = nullptr;  // this lane's first vector of the step to copy
@@ -1545,11 +1546,11 @@ inline int row_lanes_log2(int n) {
     return lg;
 }
 
-// Chunks (as a power of two) that a token's `steps` row steps are split into:
-// one while tokens alone give every SM 16 warps, else as many as are needed.
-inline int head_chunks_log2(int64_t tokens, int steps, const DevInfo& d) {
+// Chunks (as a power of two) that a token's `steps` row steps are split into: one
+// while tokens alone give every SM `warps` warps, else as many as that takes.
+inline int head_chunks_log2(int64_t tokens, int steps, int warps, const DevInfo& d) {
     int lc = 0;
-    while ((1 << lc) < steps && (tokens << lc) < int64_t(16) * d.sms) ++lc;
+    while ((1 << lc) < steps && (tokens << lc) < int64_t(warps) * d.sms) ++lc;
     return lc;
 }
 
@@ -1561,19 +1562,19 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
                                               : (const void*)&head_fwd_vec_kernel<T, VE, false, false>);
     const size_t smem = head_fwd_smem<T, VE>();
     if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
-    const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
+    const int occ = cached_occupancy(fn, kHeadFwdWarps * 32, smem);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head forward kernel cannot be resident");
     int lg = row_lanes_log2(a.d / (2 * VE));
     const int per = (32 >> lg) * kHeadRows;
     int steps = 0;
     for (int i = 0; i < (cache ? 3 : 2); ++i) steps += (a.heads[i] + per - 1) / per;
-    int lc = head_chunks_log2(a.tokens, steps, d);
-    int64_t ctas = ((a.tokens << lc) + kHeadWarps - 1) / kHeadWarps;
+    int lc = head_chunks_log2(a.tokens, steps, 16, d);
+    int64_t ctas = ((a.tokens << lc) + kHeadFwdWarps - 1) / kHeadFwdWarps;
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
     int with_norm = norm;
     void* kargs[] = {&args, &lg, &lc, &with_norm};
-    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, smem, s),
+    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadFwdWarps * 32), kargs, smem, s),
                        "head forward launch");
 }
 
@@ -1636,7 +1637,7 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
     int lg = vec ? row_lanes_log2(a.d * int(sizeof(T)) / (2 * vec)) : 5;
     const int per = vec ? 32 >> lg : kHeadWarps;
     const int steps[2] = {(a.heads[0] + per - 1) / per, (a.heads[1] + per - 1) / per};
-    int lc = vec ? head_chunks_log2(a.tokens, steps[0] > steps[1] ? steps[0] : steps[1], *d) : 0;
+    int lc = vec ? head_chunks_log2(a.tokens, steps[0] > steps[1] ? steps[0] : steps[1], 8, *d) : 0;
     // CTAs go to q and k by what they cost: a token's row steps, and one more for its angles
     int64_t cap = int64_t(occ) * d->sms;
     if (cap > head_bwd_max_partials(*d)) cap = head_bwd_max_partials(*d);
@@ -1692,7 +1693,7 @@ inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes,
     while (cl.lhp < 5 - cl.lg && (1 << cl.lhp) < a.heads[1]) ++cl.lhp;
     const int ltok = 5 - cl.lg - cl.lhp;
     const int64_t blocks = (a.tokens + (1 << ltok) - 1) >> ltok;
-    cl.lchunk = head_chunks_log2(blocks, (a.heads[1] + (1 << cl.lhp) - 1) >> cl.lhp, d);
+    cl.lchunk = head_chunks_log2(blocks, (a.heads[1] + (1 << cl.lhp) - 1) >> cl.lhp, 16, d);
     int64_t ctas = ((blocks << cl.lchunk) + kHeadWarps - 1) / kHeadWarps;
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
