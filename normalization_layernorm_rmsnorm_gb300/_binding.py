@@ -15,6 +15,7 @@ import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libnorm.so")
+HEADS_PATH = os.path.join(_PKG, "_build", "_heads.so")
 
 NRM_OK, NRM_ERR_INVALID_ARG, NRM_ERR_UNSUPPORTED, NRM_ERR_WORKSPACE, NRM_ERR_CUDA, NRM_ERR_TIMEOUT = range(6)
 NRM_F32, NRM_F16, NRM_BF16 = 0, 1, 2
@@ -345,105 +346,26 @@ def nrm_act_dropout_bwd(dy, x, dx, act, drop_p, seed, stream=None, act_param=0.0
 # attention heads: norms with position rotation, quantised key/value cache
 # ---------------------------------------------------------------------------
 # Views are [tokens, heads, d] or [batch, tokens, heads, d] tensors with
-# contiguous rows and any other strides that one token stride describes.
-
-_PAIRS = {"half": NRM_PAIRS_HALF, "pair": NRM_PAIRS_ADJACENT}
-
+# contiguous rows and any other strides that one token stride describes.  Their
+# marshalling is compiled (csrc/heads_binding.cpp): from Python it took longer
+# than the kernels of small calls.
 
 @functools.lru_cache(maxsize=None)
-def _torch():
-    """torch, and what these calls take from it: dtypes' codes, the current device's getters."""
-    import torch
-    codes = {torch.float32: NRM_F32, torch.float16: NRM_F16, torch.bfloat16: NRM_BF16}
-    return torch, codes, torch.float32, torch.int64
+def _heads():
+    """The compiled marshalling of this section's calls."""
+    import importlib.machinery
+    import importlib.util
 
-
-def _code(t, name):
-    code = _torch()[1].get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return code
-
-
-def _heads_view(t, name, shape=None, dtype=None):
-    """(C view, tokens, d) of a tensor of heads; `shape`, `dtype`: what it must have."""
-    sh, st = t.shape, t.stride()
-    if shape is not None and sh != shape:
-        raise ValueError(f"{name} has shape {tuple(sh)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if len(st) == 3:
-        tokens, h, d = sh
-        ts, hs, one = st
-    elif len(st) == 4:
-        b, n, h, d = sh
-        sb, ts, hs, one = st
-        if n <= 1:
-            ts = sb
-        elif b > 1 and sb != n * ts:
-            raise ValueError(f"{name}: batch and token dimensions must have one stride (strides {tuple(st)})")
-        tokens = b * n
-    else:
-        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
-    if one != 1 and d > 1:
-        raise ValueError(f"{name}: rows must be contiguous")
-    return _Heads(t.data_ptr(), h, ts, hs), tokens, d
-
-
-def _dense(t, name, n, dtype):
-    """data_ptr of a contiguous vector of n values, or None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} values, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _stat_ptr(t, name, n):
-    """data_ptr of the saved statistics of n rows, or None."""
-    if t is None:
-        return None
-    if t.dtype is not _torch()[2]:
-        raise TypeError(f"{name} is {t.dtype}, expected torch.float32")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of {n} values, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _on_device(*tensors):
-    """Every tensor lies on the current CUDA device, where the call launches."""
-    cuda = _torch()[0].cuda
-    dev = cuda.current_device() if cuda.is_available() else None
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on the current CUDA device ({dev}), got {t.device}")
-
-
-def _rope(pos, inv_freq, axis, pairs, tokens):
-    """The C description of a rotation, or None without one."""
-    if inv_freq is None:
-        return None
-    _, _, float32, int64 = _torch()
-    if inv_freq.dtype is not float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise TypeError("inv_freq must be a contiguous float32 vector")
-    if pos is None or pos.dtype is not int64:
-        raise TypeError("pos must be an int64 tensor")
-    if not pos.is_contiguous():
-        raise ValueError("pos must be contiguous")
-    n = inv_freq.numel()
-    axes = 1 if axis is None else pos.shape[0]
-    if pos.numel() != axes * tokens:
-        raise ValueError(f"pos has {pos.numel()} values, expected {axes} axes of {tokens} tokens")
-    if axis is not None:
-        axis = bytes(axis)
-        if len(axis) != n:
-            raise ValueError(f"axis has {len(axis)} entries, expected one for each of {n} pairs")
-    kind = _PAIRS.get(pairs)
-    if kind is None:
-        raise ValueError(f"pairs must be 'half' or 'pair', got {pairs!r}")
-    return _Rope(pos.data_ptr(), tokens, inv_freq.data_ptr(), axis, 2 * n, axes, kind)
+    import torch  # noqa: F401  (the module uses its libraries)
+    load()
+    if not os.path.exists(HEADS_PATH):
+        raise ImportError(f"libnorm is not built ({HEADS_PATH} is missing); run "
+                          "`python -m normalization_layernorm_rmsnorm_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_heads", HEADS_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_heads", loader))
+    loader.exec_module(module)
+    module.set_error(NrmError)
+    return module
 
 
 def rope_axis(sections, interleaved=False) -> bytes:
@@ -476,83 +398,32 @@ def nrm_qk_norm_rope_fwd(q, k, wq, wk, pos, inv_freq, q_out, k_out, rstd_q, rstd
     pos: int64 [tokens], or [axes, tokens] with `axis`, the axis of each pair
     (rope_axis).  inv_freq: float32 [rot / 2] (None: no rotation).  pairs:
     "half" turns elements (p, p + rot/2) together, "pair" (2p, 2p + 1)."""
-    dt, sh = q.dtype, q.shape
-    vq, tokens, d = _heads_view(q, "q")
-    vqo = _heads_view(q_out, "q_out", sh, dt)[0]
-    vk = vko = prk = None
-    if k is not None:
-        vk, vko = _key_views(k, "k", k_out, "k_out", tokens, d, dt)
-        prk = _stat_ptr(rstd_k, "rstd_k", tokens * vk.heads)
-    pwq, pwk = _dense(wq, "wq", d, dt), _dense(wk, "wk", d, dt)
-    prq = _stat_ptr(rstd_q, "rstd_q", tokens * vq.heads)
-    rope = _rope(pos, inv_freq, axis, pairs, tokens)
-    _on_device(q, k, q_out, None if k is None else k_out, wq, wk, rope and pos, inv_freq, rstd_q, rstd_k)
-    _check(load().nrm_qk_norm_rope_fwd(vq, vk, pwq, pwk, rope, vqo, vko, prq, prk, tokens, d, eps, _code(q, "q"),
-                                       _stream(stream)),
-           "nrm_qk_norm_rope_fwd")
-
-
-def _key_views(k, name, k2, name2, tokens, d, dt):
-    vk, nk, dk = _heads_view(k, name, None, dt)
-    if nk != tokens or dk != d:
-        raise ValueError(f"{name} is {nk} tokens of {dk}, the queries {tokens} of {d}")
-    if k2 is None:
-        raise ValueError(f"{name2} must not be None")
-    return vk, _heads_view(k2, name2, k.shape, dt)[0]
+    _heads().qk_norm_rope_fwd(q, k, wq, wk, pos, inv_freq, q_out, k_out, rstd_q, rstd_k, eps, stream, axis, pairs)
 
 
 def nrm_qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, rstd_q, rstd_k, pos, inv_freq, dq, dk, dwq, dwk, workspace,
                          stream=None, axis=None, pairs="half"):
     """Backward of nrm_qk_norm_rope_fwd: dq, dk (views like q, k) and the weights'
     gradients dwq, dwk (each may be None; workspace from qk_norm_workspace)."""
-    dt, sh = q.dtype, q.shape
-    vq, tokens, d = _heads_view(q, "q")
-    vdqo, vdq = _heads_view(dq_out, "dq_out", sh, dt)[0], _heads_view(dq, "dq", sh, dt)[0]
-    vk = vdko = vdk = prk = None
-    if k is not None:
-        vk, vdko = _key_views(k, "k", dk_out, "dk_out", tokens, d, dt)
-        if dk is None:
-            raise ValueError("dk must not be None")
-        vdk = _heads_view(dk, "dk", k.shape, dt)[0]
-        prk = _stat_ptr(rstd_k, "rstd_k", tokens * vk.heads)
-    pwq, pwk = _dense(wq, "wq", d, dt), _dense(wk, "wk", d, dt)
-    pdwq, pdwk = _dense(dwq, "dwq", d, dt), _dense(dwk, "dwk", d, dt)
-    prq = _stat_ptr(rstd_q, "rstd_q", tokens * vq.heads)
-    rope = _rope(pos, inv_freq, axis, pairs, tokens)
-    _on_device(q, k, dq_out, dq, *(() if k is None else (dk_out, dk)), wq, wk, dwq, dwk, rstd_q, rstd_k,
-               rope and pos, inv_freq, workspace)
-    _check(load().nrm_qk_norm_rope_bwd(vdqo, vdko, vq, vk, pwq, pwk, prq, prk, rope, vdq, vdk, pdwq, pdwk, tokens, d,
-                                       _code(q, "q"), _ptr(workspace), _ws(workspace), _stream(stream)),
-           "nrm_qk_norm_rope_bwd")
-
-
-def _rope_call(name, q, k, pos, inv_freq, q_out, k_out, stream, axis, pairs, names):
-    dt = q.dtype
-    vq, tokens, d = _heads_view(q, names[0])
-    vqo = _heads_view(q_out, names[2], q.shape, dt)[0]
-    vk = vko = None
-    if k is not None:
-        vk, vko = _key_views(k, names[1], k_out, names[3], tokens, d, dt)
-    rope = _rope(pos, inv_freq, axis, pairs, tokens)
-    _on_device(q, k, q_out, None if k is None else k_out, rope and pos, inv_freq)
-    _check(getattr(load(), name)(vq, vk, rope, vqo, vko, tokens, d, _code(q, names[0]), _stream(stream)), name)
+    _heads().qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, rstd_q, rstd_k, pos, inv_freq, dq, dk, dwq, dwk, workspace,
+                              stream, axis, pairs)
 
 
 def nrm_rope_fwd(q, k, pos, inv_freq, q_out, k_out, stream=None, axis=None, pairs="half"):
     """The rotation by position alone (arguments as nrm_qk_norm_rope_fwd); q_out, k_out may be q, k."""
-    _rope_call("nrm_rope_fwd", q, k, pos, inv_freq, q_out, k_out, stream, axis, pairs, ("q", "k", "q_out", "k_out"))
+    _heads().rope_fwd(q, k, pos, inv_freq, q_out, k_out, stream, axis, pairs)
 
 
 def nrm_rope_bwd(dq_out, dk_out, pos, inv_freq, dq, dk, stream=None, axis=None, pairs="half"):
     """Backward of nrm_rope_fwd: the turn the other way; dq, dk may be dq_out, dk_out."""
-    _rope_call("nrm_rope_bwd", dq_out, dk_out, pos, inv_freq, dq, dk, stream, axis, pairs,
-               ("dq_out", "dk_out", "dq", "dk"))
+    _heads().rope_bwd(dq_out, dk_out, pos, inv_freq, dq, dk, stream, axis, pairs)
 
 
 class KvCache:
     """A paged, quantised key/value cache (kv_cache): the tensors and their C description."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "heads", "d", "slots", "held", "_c")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "heads", "d", "slots", "held", "address",
+                 "_c")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         import torch
@@ -580,10 +451,14 @@ class KvCache:
                 raise ValueError("the rows of codes and scales must be contiguous")
         if (k_codes is None) != (k_scales is None) or (v_codes is None) != (v_scales is None):
             raise ValueError("codes and scales come together")
-        _on_device(k_codes, k_scales, v_codes, v_scales)
+        dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+        for t in (k_codes, k_scales, v_codes, v_scales):
+            if t is not None and (not t.is_cuda or t.get_device() != dev):
+                raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
         self.heads, self.d, self.slots, self.held = heads, d, pages * page, codes
         self._c = _Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, page, heads, d,
                          d // scales.shape[3], *codes.stride()[:3], *scales.stride()[:3], kind)
+        self.address = ctypes.addressof(self._c)
 
 
 def kv_cache(k_codes, k_scales, v_codes=None, v_scales=None) -> KvCache:
@@ -597,48 +472,16 @@ def kv_cache(k_codes, k_scales, v_codes=None, v_scales=None) -> KvCache:
     return KvCache(k_codes, k_scales, v_codes, v_scales)
 
 
-def _cache_view(cache, t, name, tokens, dtype):
-    """The C view of rows that go to or come from the cache (None: none), their tokens and dtype."""
-    if t is None:
-        return None, tokens, dtype
-    v, n, d = _heads_view(t, name, None, dtype)
-    if d != cache.d or v.heads != cache.heads:
-        raise ValueError(f"{name}: rows are {v.heads} heads of {d}, the cache's {cache.heads} of {cache.d}")
-    if tokens is not None and n != tokens:
-        raise ValueError(f"{name} has {n} tokens, expected {tokens}")
-    return v, n, t.dtype
-
-
-def _slots_ptr(slots, tokens):
-    if slots.dtype is not _torch()[3] or slots.numel() != tokens or not slots.is_contiguous():
-        raise ValueError(f"slots must be {tokens} contiguous int64 values")
-    return slots.data_ptr()
-
-
-def _cache_call(name, cache, slots, k, v, names, stream):
-    vk, tokens, dt = _cache_view(cache, k, names[0], None, None)
-    vv, tokens, dt = _cache_view(cache, v, names[1], tokens, dt)
-    if tokens is None:
-        raise ValueError(f"{names[0]} and {names[1]} must not both be None")
-    ps = _slots_ptr(slots, tokens)
-    _on_device(k, v, slots, cache.held)
-    lib, code, stream = load(), _code(k if k is not None else v, names[0]), _stream(stream)
-    if name == "nrm_kv_cache_write":
-        _check(lib.nrm_kv_cache_write(vk, vv, cache._c, ps, tokens, code, stream), name)
-    else:
-        _check(lib.nrm_kv_cache_read(cache._c, ps, vk, vv, tokens, code, stream), name)
-
-
 def nrm_kv_cache_write(k, v, cache, slots, stream=None):
     """Quantises row t of k and v ([tokens, heads, d]; either may be None) into
     slot slots[t] of the cache; -1 skips a token."""
-    _cache_call("nrm_kv_cache_write", cache, slots, k, v, ("k", "v"), stream)
+    _heads().kv_cache_write(cache.address, cache.held, slots, k, v, stream)
 
 
 def nrm_kv_cache_read(cache, slots, k_out, v_out, stream=None):
     """The values of slot slots[t] as row t of k_out and v_out (either may be
     None); rows of slot -1 are left as they were."""
-    _cache_call("nrm_kv_cache_read", cache, slots, k_out, v_out, ("k_out", "v_out"), stream)
+    _heads().kv_cache_read(cache.address, cache.held, slots, k_out, v_out, stream)
 
 
 def nrm_qk_norm_rope_cache(q, k, v, wq, wk, pos, inv_freq, q_out, k_out, cache, slots, eps, stream=None, axis=None,
@@ -646,20 +489,8 @@ def nrm_qk_norm_rope_cache(q, k, v, wq, wk, pos, inv_freq, q_out, k_out, cache, 
     """The step of a served model in one launch: nrm_qk_norm_rope_fwd (nrm_rope_fwd
     with norm=False) of q and k, and the key and v quantised into the cache.
     k_out may be None when only the cache is wanted."""
-    dt = q.dtype
-    vq, tokens, d = _heads_view(q, "q")
-    vqo = _heads_view(q_out, "q_out", q.shape, dt)[0]
-    if k is None or v is None:
-        raise ValueError("k and v must not be None")
-    vk, vv = _cache_view(cache, k, "k", tokens, dt)[0], _cache_view(cache, v, "v", tokens, dt)[0]
-    vko = None if k_out is None else _heads_view(k_out, "k_out", k.shape, dt)[0]
-    pwq, pwk = _dense(wq, "wq", d, dt), _dense(wk, "wk", d, dt)
-    rope = _rope(pos, inv_freq, axis, pairs, tokens)
-    ps = _slots_ptr(slots, tokens)
-    _on_device(q, k, v, q_out, k_out, wq, wk, rope and pos, inv_freq, slots, cache.held)
-    _check(load().nrm_qk_norm_rope_cache(vq, vk, vv, pwq, pwk, rope, vqo, vko, cache._c, ps, tokens, d, eps,
-                                         1 if norm else 0, _code(q, "q"), _stream(stream)),
-           "nrm_qk_norm_rope_cache")
+    _heads().qk_norm_rope_cache(q, k, v, wq, wk, pos, inv_freq, q_out, k_out, cache.address, cache.held, slots, eps,
+                                stream, axis, pairs, norm)
 
 
 def nrm_act_mask_words(n: int, c: int, l: int) -> int:

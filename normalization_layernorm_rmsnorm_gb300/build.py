@@ -1,4 +1,5 @@
-"""Builds libnorm.so in-tree (``_build/``) with nvcc for sm_103a.
+"""Builds libnorm.so in-tree (``_build/``) with nvcc for sm_103a, and the Python
+extension that marshals the calls on attention heads (``_heads.so``) with g++.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  Rebuilds only what changed.
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libnorm.so")
+HEADS = os.path.join(BUILD, "_heads.so")  # the compiled marshalling (csrc/heads_binding.cpp)
 
 SOURCES = ["api.cu", "noalloc.cu", "dropout.cu",
            "rownorm_f32.cu", "rownorm_f16.cu", "rownorm_bf16.cu",
@@ -54,14 +56,45 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "heads_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "heads_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for heads_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = HEADS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-lnorm", "-L", libs, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HEADS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA source and link libnorm.so; returns its path."""
+    """Compile every source, link libnorm.so and the binding; returns libnorm.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     dep = _deps_mtime()
-    if not force and not verbose_ptxas and os.path.exists(LIB) and os.path.getmtime(LIB) >= dep:
+    made = [f for f in (LIB, HEADS) if os.path.exists(f) and os.path.getmtime(f) >= dep]
+    if not force and not verbose_ptxas and len(made) == 2:
         return LIB
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+        binding = pool.submit(_compile_binding)
         objs = list(pool.map(lambda s: _compile(s, extra), SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
@@ -69,6 +102,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     return LIB
 
 
