@@ -215,12 +215,19 @@ __device__ __forceinline__ void quantise_row(const float* row, int d, const Cach
 }
 
 // ---------------------------------------------------------------------------
-// vectors of VE elements (16 or 8 bytes)
+// vectors of VE elements (16 or 8 bytes, or 4 bytes of a 16-bit type)
 // ---------------------------------------------------------------------------
 template <int BYTES> struct RawBits;
 template <> struct RawBits<16> { using type = uint4; };
 template <> struct RawBits<8> { using type = uint2; };
+template <> struct RawBits<4> { using type = uint1; };
 template <typename T, int VE> using Raw = typename RawBits<VE * int(sizeof(T))>::type;
+
+template <typename R>
+__device__ __forceinline__ R ld_ro(const R* p) {
+    if constexpr (sizeof(R) == 4) return make_uint1(__ldg(reinterpret_cast<const uint32_t*>(p)));
+    else return __ldg(p);
+}
 
 // Loads of rows that this kernel may write in place: not through the read-only
 // path, and not kept in L1.
@@ -231,9 +238,16 @@ __device__ __forceinline__ void ld_row(const void* p, uint4& r) {
 __device__ __forceinline__ void ld_row(const void* p, uint2& r) {
     asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
 }
+__device__ __forceinline__ void ld_row(const void* p, uint1& r) {
+    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r.x) : "l"(p) : "memory");
+}
 __device__ __forceinline__ void st_row(void* p, uint4 v) { st_v4(p, v); }
 __device__ __forceinline__ void st_row(void* p, uint2 v) {
     asm volatile("st.global.v2.u32 [%0], {%1,%2};" :: "l"(p), "r"(v.x), "r"(v.y) : "memory");
+}
+
+__device__ __forceinline__ void st_row(void* p, uint1 v) {
+    asm volatile("st.global.u32 [%0], %1;" :: "l"(p), "r"(v.x) : "memory");
 }
 
 // The elements as pairs of floats, for the packed fp32 instructions (two elements
@@ -735,8 +749,8 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
                 pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
                 const T* w = reinterpret_cast<const T*>(a.w[which]);
                 if (w && at.on)
-                    pair_unpack<T, VE, ADJ>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
-                                            __ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), map.uu, map.vv);
+                    pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                            ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), map.uu, map.vv);
             }
             if (at.turns) map.turned(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
         }
@@ -878,8 +892,8 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     }
     if (at.on && a.w[which]) {
         const T* w = reinterpret_cast<const T*>(a.w[which]);
-        pair_unpack<T, VE, ADJ>(__ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
-                                __ldg(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
+        pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
     }
     // lanes past the row copy nothing, and read zeros
     if (!at.on)
@@ -1607,6 +1621,8 @@ nrm_status head_fwd(const HeadArgs& a, bool norm, bool cache, int vec, cudaStrea
     args.err = d->err;
     if (vec == 16) return head_fwd_vec<T, 16 / int(sizeof(T))>(args, norm, cache, *d, s);
     if (vec == 8) return head_fwd_vec<T, 8 / int(sizeof(T))>(args, norm, cache, *d, s);
+    if constexpr (sizeof(T) == 2)
+        if (vec == 4) return head_fwd_vec<T, 2>(args, norm, cache, *d, s);
     return head_fwd_scalar<T>(args, norm, cache, *d, s);
 }
 
@@ -1622,14 +1638,18 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
                     return st;
         return NRM_OK;
     }
-    constexpr int V16 = 16 / int(sizeof(T)), V8 = V16 / 2;
-    const bool adj = a.rope.adjacent;
-    const void* fn = vec == 16  ? (adj ? (const void*)&head_bwd_vec_kernel<T, V16, true>
-                                       : (const void*)&head_bwd_vec_kernel<T, V16, false>)
-                     : vec == 8 ? (adj ? (const void*)&head_bwd_vec_kernel<T, V8, true>
-                                       : (const void*)&head_bwd_vec_kernel<T, V8, false>)
-                                : (const void*)&head_bwd_scalar_kernel<T>;
-    const size_t smem = vec == 16 ? head_bwd_smem<T, V16>() : (vec == 8 ? head_bwd_smem<T, V8>() : 0);
+    const void* fn = (const void*)&head_bwd_scalar_kernel<T>;
+    size_t smem = 0;
+    auto take = [&](auto ve) {
+        constexpr int VE = decltype(ve)::value;
+        fn = a.rope.adjacent ? (const void*)&head_bwd_vec_kernel<T, VE, true>
+                             : (const void*)&head_bwd_vec_kernel<T, VE, false>;
+        smem = head_bwd_smem<T, VE>();
+    };
+    if (vec == 16) take(std::integral_constant<int, 16 / int(sizeof(T))>{});
+    if (vec == 8) take(std::integral_constant<int, 8 / int(sizeof(T))>{});
+    if constexpr (sizeof(T) == 2)
+        if (vec == 4) take(std::integral_constant<int, 2>{});
     if (smem)
         if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
     const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
@@ -1735,6 +1755,8 @@ nrm_status cache_write(const HeadArgs& a, int vec, cudaStream_t s) {
     args.err = d->err;
     if (vec == 16) return cache_write_vec<T, 16>(args, *d, s);
     if (vec == 8) return cache_write_vec<T, 8>(args, *d, s);
+    if constexpr (sizeof(T) == 2)
+        if (vec == 4) return cache_write_vec<T, 4>(args, *d, s);
     return cache_launch_scalar<T>(args, (const void*)&cache_write_scalar_kernel<T>, a.x[1].p && a.x[2].p, *d, s);
 }
 
@@ -1745,12 +1767,12 @@ nrm_status cache_read(const HeadArgs& a, int vec, cudaStream_t s) {
     if (a.tokens == 0) return NRM_OK;
     HeadArgs args = a;
     args.err = d->err;
-    if (vec) {
-        const int ve = vec / int(sizeof(T));
-        return cache_launch_vec(args, vec == 16 ? (const void*)&cache_read_vec_kernel<T, 16 / int(sizeof(T))>
-                                                : (const void*)&cache_read_vec_kernel<T, 8 / int(sizeof(T))>,
-                                a.d / (2 * ve), 0, false, *d, s);
-    }
+    const void* fn = nullptr;
+    if (vec == 16) fn = (const void*)&cache_read_vec_kernel<T, 16 / int(sizeof(T))>;
+    if (vec == 8) fn = (const void*)&cache_read_vec_kernel<T, 8 / int(sizeof(T))>;
+    if constexpr (sizeof(T) == 2)
+        if (vec == 4) fn = (const void*)&cache_read_vec_kernel<T, 2>;
+    if (fn) return cache_launch_vec(args, fn, a.d * int(sizeof(T)) / (2 * vec), 0, false, *d, s);
     return cache_launch_scalar<T>(args, (const void*)&cache_read_scalar_kernel<T>, a.y[0].p && a.y[1].p, *d, s);
 }
 

@@ -77,7 +77,7 @@ struct HeadArgs {
     unsigned int* err;
 };
 
-// `vec`: the widest accesses (16 or 8 bytes) that every pointer, stride, d, rot
+// `vec`: the widest accesses (16 or 8 bytes, 4 of a 16-bit type) that every pointer, stride, d, rot
 // and group fits, or 0.
 template <typename T> nrm_status head_fwd(const HeadArgs& a, bool norm, bool cache, int vec, cudaStream_t s);
 template <typename T> nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s);

@@ -173,13 +173,13 @@ nrm_status check_slots(const int64_t* slots, int64_t tokens) {
     return NRM_OK;
 }
 
-// The widest accesses (16 or 8 bytes; 0: single elements) that fit the views,
+// The widest accesses (16 or 8 bytes, 4 of a 16-bit type; 0: single elements) that fit the views,
 // the weights, rows of whole pairs of vectors (at most 32 pairs), and, where
 // there is one, the cache's groups and rows of codes (`vectors` vectors' codes
 // are moved at once).
 int fits_vec(std::initializer_list<const nrm_heads*> views, std::initializer_list<const void*> ptrs, int64_t tokens,
              int64_t d, const RopeDev& r, nrm_dtype dt, const nrm_kv_cache* c = nullptr, int vectors = 1) {
-    for (int bytes = 16; bytes >= 8; bytes /= 2) {
+    for (int bytes = 16; bytes >= 2 * int(dsize(dt)); bytes /= 2) {
         const int64_t v = bytes / int64_t(dsize(dt));
         bool ok = d % (2 * v) == 0 && d / (2 * v) <= 32 && r.rot % (2 * v) == 0;
         for (const nrm_heads* h : views)

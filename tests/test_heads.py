@@ -133,6 +133,10 @@ LAYOUTS = [
     ("bf16", 5, 2, 2, 72, 36, "half", 1, False, 4),
     ("f32", 12, 3, 1, 36, 36, "pair", 1, False, 2),
     ("bf16", 700, 9, 2, 128, 128, "half", 1, False, 0),
+    ("f16", 15, 3, 1, 72, 20, "pair", 3, False, 0),
+    ("bf16", 8, 2, 2, 128, 124, "half", 1, False, 2),
+    ("f16", 40, 12, 1, 40, 20, "half", 1, True, 0),
+    ("bf16", 2000, 3, 1, 64, 64, "pair", 2, False, 0),
 ]
 
 
@@ -405,6 +409,10 @@ CACHES = [
     ("f32", "int4", 6, 2, 256, 32, 16, "token", False, 0),
     ("bf16", "int8", 14, 3, 160, 32, 16, "token", True, 0),
     ("bf16", "int4", 14, 3, 24, 8, 16, "token", False, 0),
+    ("f16", "e4m3", 14, 3, 36, 12, 16, "token", False, 0),
+    ("bf16", "int8", 14, 2, 128, 4, 16, "head", False, 2),
+    ("f16", "int4", 14, 2, 128, 2, 16, "token", False, 2),
+    ("f16", "int4", 9, 2, 44, 44, 16, "token", False, 0),
 ]
 
 
@@ -569,6 +577,10 @@ SERVED = [
     ("bf16", 600, 2, 2, 128, 64, "half", 1, False, 0, "int4", 128, 64, "token"),
     ("f16", 5, 1, 1, 33, 32, "half", 1, False, 0, "int8", 3, 5, "token"),
     ("bf16", 6, 2, 2, 128, 96, "half", 1, False, 0, "e4m3", 8, 5, "token"),
+    ("f16", 6, 2, 2, 72, 36, "half", 1, False, 0, "int4", 12, 5, "token"),
+    ("bf16", 6, 3, 1, 64, 64, "pair", 1, False, 2, "int8", 2, 5, "head"),
+    ("f16", 3, 2, 2, 128, 128, "pair", 1, False, 0, "int8", 32, 5, "token"),
+    ("bf16", 3, 2, 2, 128, 128, "pair", 1, False, 0, "e4m3", 16, 5, "token"),
 ]
 
 
