@@ -477,6 +477,7 @@ NRM_API nrm_status nrm_qk_norm_rope_fwd(const nrm_heads *q, const nrm_heads *k, 
  * in place).  dwq, dwk: [d] in dt, each may be NULL.  k (with dk_out, dk) may
  * be NULL.  workspace: nrm_workspace_bytes(NRM_OP_QK_NORM_BWD, tokens, d, dt)
  * bytes, 16-byte aligned, clobbered; may be NULL when dwq and dwk are NULL.
+ * Calls that overlap on the GPU need separate workspaces.
  * With tokens == 0, dwq and dwk are set to 0.
  */
 NRM_API nrm_status nrm_qk_norm_rope_bwd(const nrm_heads *dq_out, const nrm_heads *dk_out,
@@ -517,7 +518,8 @@ typedef enum nrm_cache_kind {
  * (s % page_size)*slot_stride + h*head_stride of the codes, and its d/group
  * scales at the like float of the scales: [pages, page, heads, d] and
  * [pages, heads, page, d] are both such layouts.  k and v share the strides;
- * either pair of pointers may be NULL in calls that do not touch it.
+ * either pair of pointers may be NULL in calls that do not touch it.  A cache
+ * that is written keeps keys and values in memory of their own.
  */
 typedef struct nrm_kv_cache {
     void *k_codes;

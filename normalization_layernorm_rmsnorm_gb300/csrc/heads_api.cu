@@ -107,7 +107,7 @@ nrm_status set_rope(const nrm_rope* r, int64_t tokens, int64_t d, bool inverse, 
     return NRM_OK;
 }
 
-nrm_status set_cache(const nrm_kv_cache* c, bool keys, bool values, CacheDev* out) {
+nrm_status set_cache(const nrm_kv_cache* c, bool keys, bool values, bool written, CacheDev* out) {
     if (!c) return fail(NRM_ERR_INVALID_ARG, "cache must not be NULL");
     if (c->kind != NRM_CACHE_E4M3 && c->kind != NRM_CACHE_INT8 && c->kind != NRM_CACHE_INT4)
         return fail(NRM_ERR_INVALID_ARG, "unknown cache kind %d", int(c->kind));
@@ -145,6 +145,8 @@ nrm_status set_cache(const nrm_kv_cache* c, bool keys, bool values, CacheDev* ou
     }
     if (keys && (!c->k_codes || !c->k_scales)) return fail(NRM_ERR_INVALID_ARG, "the cache has no keys");
     if (values && (!c->v_codes || !c->v_scales)) return fail(NRM_ERR_INVALID_ARG, "the cache has no values");
+    if (written && keys && values && (c->k_codes == c->v_codes || c->k_scales == c->v_scales))
+        return fail(NRM_ERR_INVALID_ARG, "the cache's keys and values are the same memory");
     if (!aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
         return fail(NRM_ERR_INVALID_ARG, "the cache's scales must be aligned to 4 bytes");
     *out = CacheDev{};
@@ -386,7 +388,7 @@ nrm_status nrm_kv_cache_write(const nrm_heads* k, const nrm_heads* v, const nrm_
                               int64_t tokens, nrm_dtype dt, nrm_stream_t stream) {
     return entry([&]() -> nrm_status {
         HeadArgs a{};
-        NRM_TRY(set_cache(cache, k != nullptr, v != nullptr, &a.cache));
+        NRM_TRY(set_cache(cache, k != nullptr, v != nullptr, true, &a.cache));
         NRM_TRY(check_sizes(tokens, cache->d, dt));
         if (!k && !v) return fail(NRM_ERR_INVALID_ARG, "k and v must not both be NULL");
         const nrm_heads like{nullptr, cache->heads, 0, 0};
@@ -410,7 +412,7 @@ nrm_status nrm_kv_cache_read(const nrm_kv_cache* cache, const int64_t* slots, co
                              const nrm_heads* v_out, int64_t tokens, nrm_dtype dt, nrm_stream_t stream) {
     return entry([&]() -> nrm_status {
         HeadArgs a{};
-        NRM_TRY(set_cache(cache, k_out != nullptr, v_out != nullptr, &a.cache));
+        NRM_TRY(set_cache(cache, k_out != nullptr, v_out != nullptr, false, &a.cache));
         NRM_TRY(check_sizes(tokens, cache->d, dt));
         if (!k_out && !v_out) return fail(NRM_ERR_INVALID_ARG, "k_out and v_out must not both be NULL");
         const nrm_heads like{nullptr, cache->heads, 0, 0};
@@ -443,7 +445,7 @@ nrm_status nrm_qk_norm_rope_cache(const nrm_heads* q, const nrm_heads* k, const 
         NRM_TRY(check_view("v", v, k, tokens, d, dt, false));
         NRM_TRY(check_place("q_out", q_out, v, false, tokens));
         NRM_TRY(check_place("k_out", k_out, v, false, tokens));
-        NRM_TRY(set_cache(cache, true, true, &a.cache));
+        NRM_TRY(set_cache(cache, true, true, true, &a.cache));
         if (cache->heads != k->heads || cache->d != d)
             return fail(NRM_ERR_INVALID_ARG, "the cache has %lld heads of %lld, k %lld of %lld",
                         (long long)cache->heads, (long long)cache->d, (long long)k->heads, (long long)d);

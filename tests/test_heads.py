@@ -733,3 +733,104 @@ def test_refusals_leave_the_context_usable():
     with pytest.raises(ValueError, match="current CUDA device"):
         nrm.nrm_kv_cache_write(c.k, c.v, make_cache("int8", 2, 8, 1, 64, 64), torch.arange(10))
     nrm.nrm_sync_status()
+
+
+# ---------------------------------------------------------------------------
+# far offsets, other streams, first calls
+# ---------------------------------------------------------------------------
+
+def test_offsets_past_32_bits_in_a_long_cache():
+    # 2^22 pages of 16 slots, 1 head of 128 in one byte each: 8 GiB of codes, the slots asked for beyond
+    # 2^32 bytes and beyond 2^31
+    pages = 1 << 22
+    codes = torch.empty(pages, 16, 1, 128, dtype=torch.int8, device="cuda")
+    scales = torch.empty(pages, 16, 1, 1, device="cuda")
+    cache = nrm.kv_cache(codes, scales)
+    slots = torch.tensor([0, (1 << 24) + 3, (1 << 25) + 5, pages * 16 - 1, 77], device="cuda")
+    codes.view(-1, 128)[slots] = 0
+    c = Data("bf16", 5, 1, 1, 128, 0)
+    nrm.nrm_kv_cache_write(c.k, None, cache, slots)
+    near = make_cache("int8", 1, 5, 1, 128, 128)
+    nrm.nrm_kv_cache_write(c.k, None, near, torch.arange(5, device="cuda"))
+    assert torch.equal(codes.view(-1, 128)[slots], near.k_codes.view(5, 128))
+    assert torch.equal(scales.view(-1)[slots], near.k_scales.view(-1))
+    a, b = torch.empty_like(c.k), torch.empty_like(c.k)
+    nrm.nrm_kv_cache_read(cache, slots, a, None)
+    nrm.nrm_kv_cache_read(near, torch.arange(5, device="cuda"), b, None)
+    nrm.nrm_sync_status()
+    assert same(a, b)
+
+
+def test_offsets_past_32_bits_in_strided_views():
+    # tokens 2^30 + 64 elements apart in one buffer of 6 GiB, forward and backward
+    step = (1 << 30) + 64
+    buf = torch.empty(2 * step + 3 * 256, dtype=torch.bfloat16, device="cuda")
+    c = Data("bf16", 3, 2, 1, 128, 128)
+
+    def far(t):
+        v = buf.as_strided(t.shape, (step, 128, 1), 0)
+        v.copy_(t)
+        return v
+
+    rq, r2 = torch.empty(3, 2, device="cuda"), torch.empty(3, 2, device="cuda")
+    want, dq, dq2 = torch.empty_like(c.q), torch.empty_like(c.q), torch.empty_like(c.q)
+    nrm.nrm_qk_norm_rope_fwd(c.q, None, c.wq, None, c.pos, c.inv, want, None, rq, None, 1e-6)
+    nrm.nrm_qk_norm_rope_bwd(c.dqo, None, c.q, None, c.wq, None, rq, None, c.pos, c.inv, dq, None, None, None, None)
+    v = far(c.q)
+    nrm.nrm_qk_norm_rope_bwd(c.dqo, None, v, None, c.wq, None, rq, None, c.pos, c.inv, dq2, None, None, None, None)
+    nrm.nrm_qk_norm_rope_fwd(v, None, c.wq, None, c.pos, c.inv, v, None, r2, None, 1e-6)
+    nrm.nrm_sync_status()
+    assert same(v, want) and same(rq, r2) and same(dq, dq2)
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [Data("bf16", 3000, 8, 2, 128, 128, seed=i) for i in range(2)]
+    caches = [make_cache("int8", 50, 64, 2, 128, 64, seed=i) for i in range(2)]
+    slots = torch.randperm(3000, device="cuda")
+    out = [torch.empty_like(c.q) for c in cases]
+    back = [(torch.empty_like(c.k), torch.empty_like(c.v)) for c in cases]
+    want = []
+    for c, m, o, b in zip(cases, caches, out, back):
+        nrm.nrm_qk_norm_rope_cache(c.q, c.k, c.v, c.wq, c.wk, c.pos, c.inv, o, None, m, slots, 1e-6)
+        nrm.nrm_kv_cache_read(m, slots, *b)
+        want.append([o.clone(), b[0].clone(), b[1].clone()])
+        o.zero_(), b[0].zero_(), b[1].zero_()
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, c, m, o, b in zip(streams, cases, caches, out, back):
+            nrm.nrm_qk_norm_rope_cache(c.q, c.k, c.v, c.wq, c.wk, c.pos, c.inv, o, None, m, slots, 1e-6, stream=s)
+            with torch.cuda.stream(s):
+                nrm.nrm_kv_cache_read(m, slots, *b)
+    torch.cuda.synchronize()
+    for o, b, w in zip(out, back, want):
+        assert same(o, w[0]) and same(b[0], w[1]) and same(b[1], w[2])
+
+
+FIRST_CALL = """
+import torch, normalization_layernorm_rmsnorm_gb300 as nrm
+q = torch.randn(4, 2, 64, device="cuda"); w = torch.ones(64, device="cuda"); o = torch.empty_like(q)
+pos = torch.arange(4, device="cuda"); inv = torch.ones(32, device="cuda"); r = torch.empty(4, 2, device="cuda")
+dq, dw = torch.empty_like(q), torch.empty_like(w); ws = nrm.qk_norm_workspace(q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    nrm.nrm_qk_norm_rope_fwd(q, None, w, None, pos, inv, o, None, r, None, 1e-6)
+    nrm.nrm_qk_norm_rope_bwd(o, None, q, None, w, None, r, None, pos, inv, dq, None, dw, None, ws)
+g.replay(); torch.cuda.synchronize()
+a, b = o.clone(), dw.clone(); o.zero_(); dw.zero_()
+nrm.nrm_qk_norm_rope_fwd(q, None, w, None, pos, inv, o, None, r, None, 1e-6)
+nrm.nrm_qk_norm_rope_bwd(o, None, q, None, w, None, r, None, pos, inv, dq, None, dw, None, ws)
+nrm.nrm_sync_status()
+assert torch.equal(a, o) and torch.equal(b, dw)
+print("same")
+"""
+
+
+def test_a_first_call_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr

@@ -206,6 +206,9 @@ def fused(lib, q=None, k=None, v=None, qo=None, ko=None, c=None, slots=P, r=None
     (lambda L: write(L, c=C(k_codes=None)), 1),
     (lambda L: write(L, c=C(k_scales=P + 2)), 1),
     (lambda L: write(L, k=None), 1),
+    (lambda L: write(L, v=H(2 * P), c=C(v_codes=P)), 1),
+    (lambda L: write(L, v=H(2 * P), c=C(v_scales=P)), 1),
+    (lambda L: fused(L, c=C(v_codes=P)), 1),
     (lambda L: write(L, k=H(heads=3)), 1),
     (lambda L: write(L, slots=None), 1),
     (lambda L: write(L, slots=P + 4), 1),
