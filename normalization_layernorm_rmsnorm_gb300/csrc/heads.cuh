@@ -743,16 +743,16 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             py = reinterpret_cast<T*>(v.p) + t * v.ts + h * v.hs + at.b0;
             row_y = rows * v.hs;
             out = v.p && at.on;
+            if (norm) pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
+            if (norm || cur.fresh) {  // (without weights q and k share the map)
 #pragma unroll
-            for (int i = 0; i < H; ++i) map.uu[i] = map.vv[i] = f2(1.f);
-            if (norm) {
-                pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
+                for (int i = 0; i < H; ++i) map.uu[i] = map.vv[i] = f2(1.f);
                 const T* w = reinterpret_cast<const T*>(a.w[which]);
                 if (w && at.on)
                     pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
                                             ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), map.uu, map.vv);
+                if (at.turns) map.turned(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
             }
-            if (at.turns) map.turned(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
         }
         if (which < 2) {
             float2 u[R][H], v[R][H];
@@ -877,6 +877,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const int ctas = which ? int(gridDim.x) - nq : nq;
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
     const WarpTurns turns(a.rope, lane);
+    pdl_trigger();  // the column sums' CTAs start, and wait for this grid's end
     const int heads = a.heads[which], mask = (1 << lchunk) - 1;
     const int hstep = (32 >> lg) << lchunk;  // heads from one of a unit's steps to its next
     const int64_t units = a.tokens << lchunk, stride = int64_t(ctas) * kHeadWarps;
