@@ -71,7 +71,7 @@ __device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
 struct FormQ {
     int kind;
     float q, r;
-    __device__ __forceinline__ explicit FormQ(int k) : kind(k) {
+    __device__ __forceinline__ constexpr explicit FormQ(int k) : kind(k), q(0.f), r(0.f) {
         q = k == NRM_CACHE_E4M3 ? 448.f : (k == NRM_CACHE_INT8 ? 127.f : 7.f);
         r = k == NRM_CACHE_E4M3 ? 1.f / 448.f : (k == NRM_CACHE_INT8 ? 1.f / 127.f : 1.f / 7.f);
     }
@@ -1055,7 +1055,7 @@ __device__ __forceinline__ void ld_row_wide(const void* p, uint4 (&r)[2]) {
 }
 // A lane's vectors are neighbours: a group is then fewer lanes, and a lane makes
 // one scale for both.
-template <typename T, int VE, int NV>
+template <typename T, int VE, int NV, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     constexpr int E = NV * VE;  // elements of a lane
@@ -1063,8 +1063,8 @@ cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
     const bool on = j < cl.per;
     const int heads = a.heads[1], group = a.cache.group;
-    const FormQ form(a.cache.kind);
-    const int packed = form.kind == NRM_CACHE_INT4;  // two elements to a byte
+    constexpr FormQ form(KIND);
+    constexpr int packed = KIND == NRM_CACHE_INT4;  // two elements to a byte
     const bool whole = group == a.d, pow2 = (cl.gl & (cl.gl - 1)) == 0;
     const int source = (sub << cl.lg) + (whole ? 0 : j / cl.gl * cl.gl);  // first lane of this lane's group
     const int gi = j * E / group;
@@ -1196,14 +1196,15 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
 // A lane's two vectors are here those at j and j + per: each store of a warp then
 // covers whole lines (two neighbouring vectors a lane, stored 32 bytes at once,
 // were slower: 122 against 116 us for 131072 tokens of 8 heads of 128 in 4 bits).
-template <typename T, int VE>
+template <typename T, int VE, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32, 5)
 cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     constexpr int NV = 2;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
     const bool on = j < cl.per;
-    const int heads = a.heads[1], kind = a.cache.kind, packed = kind == NRM_CACHE_INT4;
+    const int heads = a.heads[1];
+    constexpr int kind = KIND, packed = kind == NRM_CACHE_INT4;  // two elements to a byte
     const int ltok = 5 - cl.lg - cl.lhp;  // tokens of a warp
     const int v_next = (cl.per * VE) >> packed;
     int gi[NV];
@@ -1732,18 +1733,31 @@ bool rows_on_32(const HeadView (&views)[2], int64_t tokens, int heads) {
     return true;
 }
 
+// The kernel of a stored form: f of the form as a constant.
+template <typename F>
+const void* cache_kind(int kind, F&& f) {
+    if (kind == NRM_CACHE_E4M3) return f(std::integral_constant<int, NRM_CACHE_E4M3>{});
+    if (kind == NRM_CACHE_INT8) return f(std::integral_constant<int, NRM_CACHE_INT8>{});
+    return f(std::integral_constant<int, NRM_CACHE_INT4>{});
+}
+
 // Two vectors of a row to a lane, where every group is whole lanes; else one,
 // where a warp holds the row.
 template <typename T, int BYTES>
 nrm_status cache_write_vec(const HeadArgs& a, const DevInfo& d, cudaStream_t s) {
     constexpr int VE = BYTES / int(sizeof(T));
     const int nvec = a.d / VE, gv = a.cache.group / VE;
+    auto by_kind = [&](auto f) { return cache_kind(a.cache.kind, f); };
     const HeadView views[2] = {a.x[1], a.x[2]};
     if (gv % 2 == 0)
-        return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 2>, nvec / 2, gv / 2,
+        return cache_launch_vec(a, by_kind([](auto kind) {
+                                    return (const void*)&cache_write_vec_kernel<T, VE, 2, decltype(kind)::value>;
+                                }), nvec / 2, gv / 2,
                                 rows_on_32<T>(views, a.tokens, a.heads[1]), d, s);
     if (nvec <= 32)
-        return cache_launch_vec(a, (const void*)&cache_write_vec_kernel<T, VE, 1>, nvec, gv, false, d, s);
+        return cache_launch_vec(a, by_kind([](auto kind) {
+                                    return (const void*)&cache_write_vec_kernel<T, VE, 1, decltype(kind)::value>;
+                                }), nvec, gv, false, d, s);
     return cache_launch_scalar<T>(a, (const void*)&cache_write_scalar_kernel<T>, a.x[1].p && a.x[2].p, d, s);
 }
 
@@ -1769,10 +1783,15 @@ nrm_status cache_read(const HeadArgs& a, int vec, cudaStream_t s) {
     HeadArgs args = a;
     args.err = d->err;
     const void* fn = nullptr;
-    if (vec == 16) fn = (const void*)&cache_read_vec_kernel<T, 16 / int(sizeof(T))>;
-    if (vec == 8) fn = (const void*)&cache_read_vec_kernel<T, 8 / int(sizeof(T))>;
+    auto take = [&](auto ve) {
+        fn = cache_kind(a.cache.kind, [](auto kind) {
+            return (const void*)&cache_read_vec_kernel<T, decltype(ve)::value, decltype(kind)::value>;
+        });
+    };
+    if (vec == 16) take(std::integral_constant<int, 16 / int(sizeof(T))>{});
+    if (vec == 8) take(std::integral_constant<int, 8 / int(sizeof(T))>{});
     if constexpr (sizeof(T) == 2)
-        if (vec == 4) fn = (const void*)&cache_read_vec_kernel<T, 2>;
+        if (vec == 4) take(std::integral_constant<int, 2>{});
     if (fn) return cache_launch_vec(args, fn, a.d * int(sizeof(T)) / (2 * vec), 0, false, *d, s);
     return cache_launch_scalar<T>(args, (const void*)&cache_read_scalar_kernel<T>, a.y[0].p && a.y[1].p, *d, s);
 }
