@@ -245,7 +245,6 @@ __device__ __forceinline__ void st_row(void* p, uint4 v) { st_v4(p, v); }
 __device__ __forceinline__ void st_row(void* p, uint2 v) {
     asm volatile("st.global.v2.u32 [%0], {%1,%2};" :: "l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
-
 __device__ __forceinline__ void st_row(void* p, uint1 v) {
     asm volatile("st.global.u32 [%0], %1;" :: "l"(p), "r"(v.x) : "memory");
 }
@@ -394,7 +393,7 @@ __device__ __forceinline__ uint2 make_codes(Raw<T, VE> x, const GroupQ& q, int k
     }
     return make_uint2(w[0], w[1]);
 }
-// Stores (loads) `bytes` of 1, 2, 4 or 8 bytes at an address aligned to them.
+// Stores 1, 2, 4 or 8 bytes at an address aligned to them.
 __device__ __forceinline__ void st_bytes(uint8_t* at, uint2 w, int bytes) {
     if (bytes == 8) *reinterpret_cast<uint2*>(at) = w;
     else if (bytes == 4) *reinterpret_cast<uint32_t*>(at) = w.x;
@@ -636,6 +635,22 @@ private:
     }
 };
 
+// For each row x of q and k: r = (mean(x^2) + eps)^-1/2, y = R(x r w) as one map of
+// pairs times r (without the norm r = 1 and the map is the rotation); rows of k and
+// v also go to the cache (below).
+//
+// Bound by bytes (a row is read and written once), and close behind by issue
+// slots: with the row arithmetic left out the kernel's copies alone take 50 us of
+// its 57 at bf16 16384 tokens of 32 + 8 heads of 128 (338 MB, 50 us at the copy
+// rate of 6.8 TB/s; 5.9 TB/s reached).  What was measured there, in us:
+//   one row a warp, scalar 259; vectors, a lane's rows loaded as they are needed 85;
+//   fp32 pairs and uniform steps 69; copies ahead, one row a step 72 (the rotation
+//   of 32760 tokens 77 -> 64); two rows a step 58; weights and angles in one map
+//   57, with 40 registers fewer.
+// Three CTAs of four warps at up to 168 registers: four CTAs (128 registers) 58,
+// two of eight warps 57, but the serving step 41 against 46 and 44.  Stages: 3, 4
+// and 5 give 68, 64 and 66 for the rotation of 32760 tokens.  Steps of four rows,
+// two at a time, took as many instructions and 57 to 58.
 constexpr int kHeadRows = 2;      // rows of a lane in a step
 constexpr int kHeadFwdWarps = 4;  // warps of a CTA
 constexpr int kHeadFwdStages = 4;
@@ -855,6 +870,16 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 // ---------------------------------------------------------------------------
 // backward on vectors
 // ---------------------------------------------------------------------------
+// For each row: g' = R^T dy, g = g' w, dx = r g - x r^2 sum(r g x)/d; dw_i sums
+// g'_i x_i r over tokens and heads.  A lane keeps the sums of its columns in
+// registers over all its rows, in float32; the CTA's rows then meet in a fixed
+// order and head_dw_kernel adds the CTAs' partial rows.  So that a lane's sums
+// belong to one weight, CTAs take q or k; a token's angles are made twice for that.
+//
+// Bound by bytes: bf16 16384 tokens of 32 + 8 heads of 128, 506 MB, 75 us at the
+// copy rate, 81 measured (6.2 TB/s).  Loads as they were needed 109, copies three
+// steps ahead 84, two steps ahead 81 (both of 128 registers, two CTAs).
+//
 // A lane's copies of a step: two vectors each of dy and x, and the row's r.
 template <typename T, int VE>
 constexpr size_t head_bwd_smem() {
@@ -1053,8 +1078,15 @@ __device__ __forceinline__ void ld_row_wide(const void* p, uint4 (&r)[2]) {
                    "=r"(r[1].w)
                  : "l"(p) : "memory");
 }
-// A lane's vectors are neighbours: a group is then fewer lanes, and a lane makes
-// one scale for both.
+// Writing.  A lane's vectors are neighbours: a group is then fewer lanes, and a
+// lane makes one scale for both.  The group's largest magnitude meets by shuffles.
+//
+// Bound by issue slots (about 240 instructions for four rows of 128: magnitudes,
+// a scale, four packed operations a pair of elements for codes that round like
+// the real quotient) and by bytes: 131072 tokens of 8 + 8 heads of 128, bf16 to
+// four bits in groups of 32, 713 MB, 105 us at the copy rate, 131 measured (5.4
+// TB/s).  One vector a lane, or two that are not neighbours, 160 to 215; copies
+// ahead as in the forward 186 (more instructions); the form at run time 141.
 template <typename T, int VE, int NV, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
@@ -1193,9 +1225,11 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
     }
 }
 
-// A lane's two vectors are here those at j and j + per: each store of a warp then
-// covers whole lines (two neighbouring vectors a lane, stored 32 bytes at once,
-// were slower: 122 against 116 us for 131072 tokens of 8 heads of 128 in 4 bits).
+// Reading: bound by bytes, 713 MB for the same 131072 tokens, 105 us at the copy
+// rate, 115 measured (6.2 TB/s).  A lane's two vectors are here those at j and j +
+// per: each store of a warp then covers whole lines (two neighbouring vectors a
+// lane, stored 32 bytes at once, took 122 against 116).  Five CTAs an SM; four and
+// six 113 and 125 here, 11.4 and 12.1 against 10.7 for 15250 tokens of 4 heads.
 template <typename T, int VE, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32, 5)
 cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
@@ -1454,6 +1488,7 @@ head_bwd_scalar_kernel(const __grid_constant__ HeadArgs a, int nq) {
     }
 }
 
+// (About 2.5 us, most of it launch and the first loads, under the backward's tail.)
 // dw of q (blockIdx.y 0) and of k (1): the column sums of their partial rows, in
 // a fixed order.  A column's rows are split over the 32 warps of a CTA; the
 // partial rows can be much larger than their sum, so both levels carry the
