@@ -441,37 +441,27 @@ struct LaneAt {
     }
 };
 
-// The angles of a warp's tokens: lane l makes those of pairs l, l + 32, ..., and
-// every lane then takes the VE pairs of its own vectors through shared memory.
-struct WarpTurns {
-    uint64_t step[kHeadMaxPairs / 32];
-    int axis;
-    __device__ __forceinline__ WarpTurns(const RopeDev& r, int lane) : axis(0) {
-#pragma unroll
-        for (int s = 0; s < kHeadMaxPairs / 32; ++s) {
-            const int p = lane + 32 * s;
-            step[s] = 0;
-            if (2 * p < r.rot) {
-                step[s] = turn_step(__ldg(r.inv_freq + p));
-                axis |= pair_axis(r, p) << (2 * s);
-            }
-        }
+// The turn of each pair per position, with the pair's axis in the low two bits
+// (an angle loses less than |pos| * 2^-62 turns by that).  Filled by the CTA's
+// threads; the caller's barrier makes them visible.
+__device__ __forceinline__ void fill_steps(const RopeDev& r, uint64_t* steps, int tid, int threads) {
+    for (int p = tid; 2 * p < r.rot; p += threads)
+        steps[p] = (turn_step(__ldg(r.inv_freq + p)) & ~uint64_t(3)) | uint64_t(pair_axis(r, p));
+}
+// cos[p], sin[p] of a token at positions pos[axis], for every pair: lane l makes
+// those of pairs l, l + 32, ..., and every lane then takes the VE pairs of its own
+// vectors from there.  Called by the whole warp.
+__device__ __forceinline__ void make_turns(const RopeDev& r, const uint64_t* steps, int lane, const int64_t* pos,
+                                           float* cos, float* sin) {
+    __syncwarp();
+    for (int p = lane; 2 * p < r.rot; p += 32) {
+        const uint64_t step = steps[p];
+        const float2 cs = pair_turn(r, step & ~uint64_t(3), pos[step & 3]);
+        cos[p] = cs.x;
+        sin[p] = cs.y;
     }
-    // cos[p], sin[p] of a token at positions pos[axis], for every pair.  Called by the whole warp.
-    __device__ __forceinline__ void make(const RopeDev& r, int lane, const int64_t* pos, float* cos, float* sin) const {
-        __syncwarp();
-#pragma unroll
-        for (int s = 0; s < kHeadMaxPairs / 32; ++s) {
-            const int p = lane + 32 * s;
-            if (2 * p < r.rot) {
-                const float2 cs = pair_turn(r, step[s], pos[axis >> (2 * s) & 3]);
-                cos[p] = cs.x;
-                sin[p] = cs.y;
-            }
-        }
-        __syncwarp();
-    }
-};
+    __syncwarp();
+}
 
 // A lane's VE angles.
 template <int VE>
@@ -641,19 +631,21 @@ private:
 //
 // Bound by bytes (a row is read and written once), and close behind by issue
 // slots: with the row arithmetic left out the kernel's copies alone take 50 us of
-// its 57 at bf16 16384 tokens of 32 + 8 heads of 128 (338 MB, 50 us at the copy
-// rate of 6.8 TB/s; 5.9 TB/s reached).  What was measured there, in us:
+// its 56 at bf16 16384 tokens of 32 + 8 heads of 128 (338 MB, 50 us at the copy
+// rate of 6.8 TB/s; 6.0 TB/s reached).  What was measured there, in us:
 //   one row a warp, scalar 259; vectors, a lane's rows loaded as they are needed 85;
 //   fp32 pairs and uniform steps 69; copies ahead, one row a step 72 (the rotation
-//   of 32760 tokens 77 -> 64); two rows a step 58; weights and angles in one map
-//   57, with 40 registers fewer.
-// Three CTAs of four warps at up to 168 registers: four CTAs (128 registers) 58,
-// two of eight warps 57, but the serving step 41 against 46 and 44.  Stages: 3, 4
-// and 5 give 68, 64 and 66 for the rotation of 32760 tokens.  Steps of four rows,
-// two at a time, took as many instructions and 57 to 58.
+//   of 32760 tokens 77 -> 64); two rows a step 58; weights and angles in one map,
+//   57, with 40 registers fewer; the turns per position in shared memory and three
+//   stages 56.
+// Three CTAs of four warps at up to 168 registers.  Four CTAs (128 registers) take
+// 61 here, 65 against 65 for the rotation of 32760 tokens and 42 against 41 for a
+// serving chunk, but 28.6 against 30.4 for heads of 64; two CTAs of eight warps 57,
+// and 44 for the chunk.  A fourth stage costs 57 here and gives the rotation 64.
+// Steps of four rows, two at a time, took as many instructions and 57 to 58.
 constexpr int kHeadRows = 2;      // rows of a lane in a step
 constexpr int kHeadFwdWarps = 4;  // warps of a CTA
-constexpr int kHeadFwdStages = 4;
+constexpr int kHeadFwdStages = 3;
 
 template <typename T, int VE>
 constexpr size_t head_fwd_smem() {
@@ -667,11 +659,13 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ __align__(16) float s_cos[kHeadFwdWarps][kHeadMaxPairs], s_sin[kHeadFwdWarps][kHeadMaxPairs];
     __shared__ TokenWords s_tok[kHeadFwdWarps][D];
+    __shared__ uint64_t s_step[kHeadMaxPairs];
     __shared__ uint32_t s_max[CACHE ? kHeadFwdWarps : 1][CACHE ? 64 : 1];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
-    const WarpTurns turns(a.rope, lane);
+    fill_steps(a.rope, s_step, threadIdx.x, N);
+    __syncthreads();
     const int rows = 32 >> lg, b01 = at.b1 - at.b0;
     const float inv_d = 1.f / float(a.d);
     const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
@@ -744,7 +738,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             x1[k] = ring[((stage * R + k) * 2 + 1) * N];
         }
         if (cur.fresh) {
-            turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
+            make_turns(a.rope, s_step, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
             if (CACHE) {
                 slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
                 if (slot >= 0) cr = cache_row(a.cache, slot, 0);
@@ -877,8 +871,9 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 // belong to one weight, CTAs take q or k; a token's angles are made twice for that.
 //
 // Bound by bytes: bf16 16384 tokens of 32 + 8 heads of 128, 506 MB, 75 us at the
-// copy rate, 81 measured (6.2 TB/s).  Loads as they were needed 109, copies three
-// steps ahead 84, two steps ahead 81 (both of 128 registers, two CTAs).
+// copy rate, 79 measured (6.4 TB/s).  Loads as they were needed 109, copies three
+// steps ahead 84, two steps ahead 79, one 92 (all two CTAs of eight warps; CTAs of
+// four warps, three or four an SM, 81 and 80).
 //
 // A lane's copies of a step: two vectors each of dy and x, and the row's r.
 template <typename T, int VE>
@@ -894,6 +889,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
     __shared__ __align__(16) float part[kHeadWarps][kHeadMaxD];
     __shared__ TokenWords s_tok[kHeadWarps][D];
+    __shared__ uint64_t s_step[kHeadMaxPairs];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][vector], N apart
     float* ring_r = reinterpret_cast<float*>(dyn + size_t(D) * 4 * N * BYTES) + threadIdx.x;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
@@ -901,7 +897,8 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const int cta = int(blockIdx.x) - (which ? nq : 0);
     const int ctas = which ? int(gridDim.x) - nq : nq;
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
-    const WarpTurns turns(a.rope, lane);
+    fill_steps(a.rope, s_step, threadIdx.x, N);
+    __syncthreads();
     pdl_trigger();  // the column sums' CTAs start, and wait for this grid's end
     const int heads = a.heads[which], mask = (1 << lchunk) - 1;
     const int hstep = (32 >> lg) << lchunk;  // heads from one of a unit's steps to its next
@@ -985,7 +982,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
         const Raw<T, VE> y0 = from[0], y1 = from[N], x0 = from[2 * N], x1 = from[3 * N];
         const float r = on ? ring_r[stage * N] : 0.f;
         if (fresh) {
-            turns.make(a.rope, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
+            make_turns(a.rope, s_step, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
             if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
             po = reinterpret_cast<T*>(dv.p) + (un >> lchunk) * dv.ts + (h0 + at.sub) * dv.hs + at.b0;
         }
