@@ -11,6 +11,7 @@
 // fit no vector take a row per warp, element by element.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -448,17 +449,26 @@ __device__ __forceinline__ void fill_steps(const RopeDev& r, uint64_t* steps, in
     for (int p = tid; 2 * p < r.rot; p += threads)
         steps[p] = (turn_step(__ldg(r.inv_freq + p)) & ~uint64_t(3)) | uint64_t(pair_axis(r, p));
 }
-// cos[p], sin[p] of a token at positions pos[axis], for every pair: lane l makes
-// those of pairs l, l + 32, ..., and every lane then takes the VE pairs of its own
-// vectors from there.  Called by the whole warp.
-__device__ __forceinline__ void make_turns(const RopeDev& r, const uint64_t* steps, int lane, const int64_t* pos,
+// What a warp copies for the tokens of a unit: positions (one an axis), cache slot.
+constexpr int kTokenSlot = kHeadMaxAxes;
+struct TokenWords {
+    int64_t w[kHeadMaxAxes + 1];
+};
+// cos[k * rot/2 + p], sin[...] of each token k at positions tok[k].w[axis], for
+// every pair p: lane l makes those of pairs l, l + 32, ..., and every lane then
+// takes the VE pairs of its own vectors from there.  Called by the whole warp.
+template <typename W>
+__device__ __forceinline__ void make_turns(const RopeDev& r, const uint64_t* steps, int lane, const W* tok, int tokens,
                                            float* cos, float* sin) {
     __syncwarp();
-    for (int p = lane; 2 * p < r.rot; p += 32) {
+    const int pairs = r.rot >> 1;
+    for (int p = lane; p < pairs; p += 32) {
         const uint64_t step = steps[p];
-        const float2 cs = pair_turn(r, step & ~uint64_t(3), pos[step & 3]);
-        cos[p] = cs.x;
-        sin[p] = cs.y;
+        for (int k = 0; k < tokens; ++k) {
+            const float2 cs = pair_turn(r, step & ~uint64_t(3), tok[k].w[step & 3]);
+            cos[k * pairs + p] = cs.x;
+            sin[k * pairs + p] = cs.y;
+        }
     }
     __syncwarp();
 }
@@ -562,29 +572,36 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
-// What a warp's lanes copy for a new token: its positions (one an axis), its cache slot.
-constexpr int kTokenSlot = kHeadMaxAxes;
-struct TokenWords {
-    int64_t w[kHeadMaxAxes + 1];
-};
+// Copies the positions of 2^ltok tokens from t0 on (those below `tokens`).
+template <bool MANY, typename W>
+__device__ __forceinline__ void copy_positions(const RopeDev& r, W* tok, int64_t t0, int ltok, int64_t tokens, int lane) {
+    static_assert(kHeadMaxAxes == 4, "four words a token");
+    if constexpr (!MANY) {
+        if (lane < r.axes) cp_async<8>(&tok[0].w[lane], r.pos + lane * r.pos_stride + t0);
+    } else {
+        for (int i = lane; i < 4 << ltok; i += 32)
+            if ((i & 3) < r.axes && t0 + (i >> 2) < tokens)
+                cp_async<8>(&tok[i >> 2].w[i & 3], r.pos + (i & 3) * r.pos_stride + t0 + (i >> 2));
+    }
+}
 
 // ---------------------------------------------------------------------------
 // forward on vectors: norm, rotation, cache
 // ---------------------------------------------------------------------------
 
-// A warp's way through its work: (token, chunk) units, of each the tensors q, k
-// (and v), of each the row steps chunk, chunk + 2^lchunk, ... of the token's
+// A warp's way through its work: (2^ltok tokens, chunk) units, of each the tensors
+// q, k (and v), of each the row steps chunk, chunk + 2^lchunk, ... of a token's
 // steps counted through all tensors.  A step is kHeadRows rows of a lane; the
 // common one, to the tensor's next step, adds to a head and (in the caller) to a
 // pointer.
-template <int TENSORS>
+template <int TENSORS, bool MANY>
 struct StepWalk {
     int64_t un;          // unit
     int which;           // tensor
     int h0, heads;       // the step's first head; the tensor's heads
     int first;           // steps of the token's earlier tensors
-    bool fresh, turned;  // the first step of a token; of a tensor (of a token)
-    int lper, lchunk;
+    bool fresh, turned;  // the first step of a unit; of a tensor (of a unit)
+    int lper, lchunk, ltok;  // log2 of: heads of a step, chunks, tokens of a unit
     int64_t units, stride;
 
     __device__ __forceinline__ void start(const HeadArgs& a, int64_t unit) {
@@ -594,7 +611,7 @@ struct StepWalk {
         settle(a);
     }
     __device__ __forceinline__ bool live() const { return un < units; }
-    __device__ __forceinline__ int64_t token() const { return un >> lchunk; }
+    __device__ __forceinline__ int64_t token() const { return MANY ? un >> lchunk << ltok : un >> lchunk; }  // the unit's first
     __device__ __forceinline__ int head_step() const { return 1 << (lper + lchunk); }
     // Moves to the next step: false where only the head moved, within the tensor.
     __device__ __forceinline__ void next(const HeadArgs& a) {
@@ -652,13 +669,15 @@ constexpr size_t head_fwd_smem() {
     return size_t(kHeadFwdStages) * 2 * kHeadRows * kHeadFwdWarps * 32 * VE * sizeof(T);
 }
 
-template <typename T, int VE, bool ADJ, bool CACHE>
+template <typename T, int VE, bool ADJ, bool CACHE, bool MANY>
 __global__ void __launch_bounds__(kHeadFwdWarps * 32, 3)
-head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int norm) {
+head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int lchunk, int norm) {
     constexpr int H = VE / 2, D = kHeadFwdStages, R = kHeadRows, N = kHeadFwdWarps * 32, BYTES = VE * int(sizeof(T));
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ __align__(16) float s_cos[kHeadFwdWarps][kHeadMaxPairs], s_sin[kHeadFwdWarps][kHeadMaxPairs];
-    __shared__ TokenWords s_tok[kHeadFwdWarps][D];
+    // (a warp's rows hold 32 * VE pairs, so its tokens have no more)
+    __shared__ __align__(16) float s_cos[kHeadFwdWarps][MANY ? 32 * VE : kHeadMaxPairs];
+    __shared__ __align__(16) float s_sin[kHeadFwdWarps][MANY ? 32 * VE : kHeadMaxPairs];
+    __shared__ TokenWords s_tok[kHeadFwdWarps][D][MANY ? 32 : 1];
     __shared__ uint64_t s_step[kHeadMaxPairs];
     __shared__ uint32_t s_max[CACHE ? kHeadFwdWarps : 1][CACHE ? 64 : 1];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
@@ -666,7 +685,10 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
     fill_steps(a.rope, s_step, threadIdx.x, N);
     __syncthreads();
-    const int rows = 32 >> lg, b01 = at.b1 - at.b0;
+    // the warp's rows are `rows` heads of each of its tokens
+    const int ltok = MANY ? ltokens : 0, lhp = 5 - lg - ltok, rows = 1 << lhp;
+    const int hsub = MANY ? at.sub & (rows - 1) : at.sub, tsub = MANY ? at.sub >> lhp : 0;
+    const int b01 = at.b1 - at.b0;
     const float inv_d = 1.f / float(a.d);
     const int g0 = CACHE ? at.b0 / a.cache.group : 0, g1 = CACHE ? at.b1 / a.cache.group : 0;
     const FormQ form(CACHE ? a.cache.kind : 0);
@@ -682,36 +704,38 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     if (!at.on)
 #pragma unroll
         for (int i = 0; i < 2 * D * R; ++i) ring[i * N] = Raw<T, VE>{};
-    StepWalk<CACHE ? 3 : 2> in;
-    in.lper = 5 - lg + (R == 2 ? 1 : 0);
+    StepWalk<CACHE ? 3 : 2, MANY> in;
+    in.lper = lhp + (R == 2 ? 1 : 0);
     in.lchunk = lchunk;
-    in.units = a.tokens << lchunk;
+    in.ltok = ltok;
+    in.units = (a.tokens + (1 << ltok) - 1) >> ltok << lchunk;
     in.stride = int64_t(gridDim.x) * kHeadFwdWarps;
     in.start(a, int64_t(blockIdx.x) * kHeadFwdWarps + warp);
-    StepWalk<CACHE ? 3 : 2> cur = in;
+    StepWalk<CACHE ? 3 : 2, MANY> cur = in;
 
     const T* px = nullptr;  // this lane's first vector of the step to copy
     int64_t row_x = 0;      // from one of a lane's rows to its next
     auto issue = [&](int stage) {
         if (in.live()) {
+            const int64_t t0 = in.token();
             if (in.turned) {
                 const HeadView v = a.x[in.which];
-                px = reinterpret_cast<const T*>(v.p) + in.token() * v.ts + (in.h0 + at.sub) * v.hs + at.b0;
+                px = reinterpret_cast<const T*>(v.p) + (t0 + tsub) * v.ts + (in.h0 + hsub) * v.hs + at.b0;
                 row_x = rows * v.hs;
             }
+            const int first = at.on && (!MANY || t0 + tsub < a.tokens) ? in.h0 + hsub : in.heads;  // this lane's first head
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                if (at.on && in.h0 + at.sub + k * rows < in.heads) {
+                if (first + k * rows < in.heads) {
                     const T* p = px + k * row_x;
                     cp_async<BYTES>(ring + ((stage * R + k) * 2) * N, p);
                     cp_async<BYTES>(ring + ((stage * R + k) * 2 + 1) * N, p + b01);
                 }
             }
             if (in.fresh) {
-                const int64_t t = in.token();
-                if (lane < a.rope.axes)
-                    cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
-                if (CACHE && lane == kTokenSlot) cp_async<8>(&s_tok[warp][stage].w[kTokenSlot], a.slots + t);
+                copy_positions<MANY>(a.rope, s_tok[warp][stage], t0, ltok, a.tokens, lane);
+                if (CACHE && lane < 1 << ltok && (!MANY || t0 + lane < a.tokens))
+                    cp_async<8>(&s_tok[warp][stage][lane].w[kTokenSlot], a.slots + t0 + lane);
             }
             px += (R * row_x) << lchunk;
             in.next(a);
@@ -729,7 +753,8 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     bool out = false;
     for (int stage = 0; cur.live(); stage = stage + 1 == D ? 0 : stage + 1) {
         cp_async_wait<D - 2>();
-        const int which = cur.which, heads = cur.heads, h = cur.h0 + at.sub;
+        const int which = cur.which, heads = cur.heads, h = cur.h0 + hsub;
+        const int64_t t = cur.token() + tsub;
         Raw<T, VE> x0[R], x1[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -738,21 +763,20 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             x1[k] = ring[((stage * R + k) * 2 + 1) * N];
         }
         if (cur.fresh) {
-            make_turns(a.rope, s_step, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
+            make_turns(a.rope, s_step, lane, s_tok[warp][stage], MANY ? 1 << ltok : 1, s_cos[warp], s_sin[warp]);
             if (CACHE) {
-                slot = cache_slot(a.cache, s_tok[warp][stage].w[kTokenSlot], a.err);
+                slot = !MANY || t < a.tokens ? cache_slot(a.cache, s_tok[warp][stage][tsub].w[kTokenSlot], a.err) : -1;
                 if (slot >= 0) cr = cache_row(a.cache, slot, 0);
             }
             __syncwarp();
         }
         issue(stage == 0 ? D - 1 : stage - 1);
         if (cur.turned && which < 2) {
-            const int64_t t = cur.token();
             const HeadView v = a.y[which];
             py = reinterpret_cast<T*>(v.p) + t * v.ts + h * v.hs + at.b0;
             row_y = rows * v.hs;
-            out = v.p && at.on;
-            if (norm) pr = at.j == 0 && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
+            out = v.p && at.on && (!MANY || t < a.tokens);
+            if (norm) pr = at.j == 0 && (!MANY || t < a.tokens) && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
             if (norm || cur.fresh) {  // (without weights q and k share the map)
 #pragma unroll
                 for (int i = 0; i < H; ++i) map.uu[i] = map.vv[i] = f2(1.f);
@@ -760,7 +784,8 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
                 if (w && at.on)
                     pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
                                             ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), map.uu, map.vv);
-                if (at.turns) map.turned(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
+                const int p = (MANY ? tsub * (a.rope.rot >> 1) : 0) + VE * at.j;
+                if (at.turns) map.turned(&s_cos[warp][p], &s_sin[warp][p]);
             }
         }
         if (which < 2) {
@@ -806,9 +831,9 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
             if (pr) pr += cur.head_step();
         }
         if constexpr (CACHE) {
-            // (both conditions are the warp's.)  The cache stores the key in the activations'
-            // type: what a separate write would read.
-            if (which > 0 && slot >= 0) {
+            // (the warp's condition.)  The cache stores the key in the activations' type: what a
+            // separate write would read.
+            if (which > 0) {
                 const int group = a.cache.group;
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
@@ -842,7 +867,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
                         }
                         __syncwarp();
                     }
-                    if (at.on && h + k * rows < heads) {
+                    if (slot >= 0 && at.on && h + k * rows < heads) {
                         const int hk = h + k * rows;
                         const GroupQ q0 = group_q<T>(mag_bits<T>(m0), form);
                         const GroupQ q1 = group == a.d ? q0 : group_q<T>(mag_bits<T>(m1), form);
@@ -881,28 +906,42 @@ constexpr size_t head_bwd_smem() {
     return size_t(kHeadStages) * kHeadWarps * 32 * (4 * VE * sizeof(T) + 4);
 }
 
-template <typename T, int VE, bool ADJ>
+// How the backward's work is laid out: CTAs [0, nq) take q, the others k.
+struct BwdPlan {
+    int lg, lchunk, nq;
+    int ltok[2];  // tokens of a warp's step, of q and of k
+};
+struct Positions {
+    int64_t w[kHeadMaxAxes];
+};
+
+template <typename T, int VE, bool ADJ, bool MANY>
 __global__ void __launch_bounds__(kHeadWarps * 32, 2)
-head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int nq) {
+head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ BwdPlan plan) {
     constexpr int H = VE / 2, D = kHeadStages, BYTES = VE * int(sizeof(T)), N = kHeadWarps * 32;
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxPairs], s_sin[kHeadWarps][kHeadMaxPairs];
-    __shared__ __align__(16) float part[kHeadWarps][kHeadMaxD];
-    __shared__ TokenWords s_tok[kHeadWarps][D];
+    // (a warp's rows hold 32 * VE pairs, so its tokens have no more)
+    __shared__ __align__(16) float s_cos[kHeadWarps][kHeadMaxD], s_sin[kHeadWarps][MANY ? 32 * VE : kHeadMaxPairs];
+    __shared__ Positions s_tok[kHeadWarps][D][MANY ? 32 : 1];
+    float(*part)[kHeadMaxD] = s_cos;  // at the end: a warp's sums, over its own cosines
     __shared__ uint64_t s_step[kHeadMaxPairs];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][vector], N apart
     float* ring_r = reinterpret_cast<float*>(dyn + size_t(D) * 4 * N * BYTES) + threadIdx.x;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
-    const int which = int(blockIdx.x) < nq ? 0 : 1;
-    const int cta = int(blockIdx.x) - (which ? nq : 0);
-    const int ctas = which ? int(gridDim.x) - nq : nq;
+    const int which = int(blockIdx.x) < plan.nq ? 0 : 1;
+    const int cta = int(blockIdx.x) - (which ? plan.nq : 0);
+    const int ctas = which ? int(gridDim.x) - plan.nq : plan.nq;
+    const int lg = plan.lg, lchunk = plan.lchunk, ltok = MANY ? plan.ltok[which] : 0;
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
     fill_steps(a.rope, s_step, threadIdx.x, N);
     __syncthreads();
     pdl_trigger();  // the column sums' CTAs start, and wait for this grid's end
     const int heads = a.heads[which], mask = (1 << lchunk) - 1;
-    const int hstep = (32 >> lg) << lchunk;  // heads from one of a unit's steps to its next
-    const int64_t units = a.tokens << lchunk, stride = int64_t(ctas) * kHeadWarps;
+    // the warp's rows are 2^lhp heads of each of its tokens
+    const int lhp = 5 - lg - ltok;
+    const int hsub = MANY ? at.sub & ((1 << lhp) - 1) : at.sub, tsub = MANY ? at.sub >> lhp : 0;
+    const int hstep = 1 << (lhp + lchunk);  // heads from one of a unit's steps to its next
+    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << lchunk, stride = int64_t(ctas) * kHeadWarps;
     const float inv_d = 1.f / float(a.d);
     const HeadView xv = a.x[which], gv = a.dy[which], dv = a.y[which];
     const int b01 = at.b1 - at.b0;
@@ -923,7 +962,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
 #pragma unroll
         for (int i = 0; i < 4 * D; ++i) ring[i * N] = Raw<T, VE>{};
     // the first head of unit un's first step; a unit without one is passed over
-    auto first_head = [&](int64_t un) { return (int(un) & mask) << (5 - lg); };
+    auto first_head = [&](int64_t un) { return (int(un) & mask) << lhp; };
     auto enter = [&](int64_t& un, int& h0) {
         h0 = first_head(un);
         while (un < units && h0 >= heads) {
@@ -942,16 +981,16 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     T* po = nullptr;
     auto issue = [&](int stage) {
         if (in_un < units) {
+            const int64_t t0 = in_un >> lchunk << ltok;
             if (in_fresh) {
-                const int64_t t = in_un >> lchunk;
-                const int h = in_h + at.sub;
+                const int64_t t = t0 + tsub;
+                const int h = in_h + hsub;
                 pg = reinterpret_cast<const T*>(gv.p) + t * gv.ts + h * gv.hs + at.b0;
                 px = reinterpret_cast<const T*>(xv.p) + t * xv.ts + h * xv.hs + at.b0;
                 pr = a.rstd[which] + t * heads + h;
-                if (lane < a.rope.axes)
-                    cp_async<8>(&s_tok[warp][stage].w[lane], a.rope.pos + lane * a.rope.pos_stride + t);
+                copy_positions<MANY>(a.rope, s_tok[warp][stage], t0, ltok, a.tokens, lane);
             }
-            if (at.on && in_h + at.sub < heads) {
+            if (at.on && in_h + hsub < heads && (!MANY || t0 + tsub < a.tokens)) {
                 Raw<T, VE>* to = ring + stage * 4 * N;
                 cp_async<BYTES>(to, pg);
                 cp_async<BYTES>(to + N, pg + b01);
@@ -977,14 +1016,16 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     LaneTurns<VE> tn;
     for (int stage = 0; un < units; stage = stage + 1 == D ? 0 : stage + 1) {
         cp_async_wait<D - 2>();
-        const bool row = h0 + at.sub < heads, on = row && at.on;
+        const int64_t t = (un >> lchunk << ltok) + tsub;
+        const bool row = h0 + hsub < heads && (!MANY || t < a.tokens), on = row && at.on;
         const Raw<T, VE>* from = ring + stage * 4 * N;
         const Raw<T, VE> y0 = from[0], y1 = from[N], x0 = from[2 * N], x1 = from[3 * N];
         const float r = on ? ring_r[stage * N] : 0.f;
         if (fresh) {
-            make_turns(a.rope, s_step, lane, s_tok[warp][stage].w, s_cos[warp], s_sin[warp]);
-            if (at.turns) tn.take(&s_cos[warp][VE * at.j], &s_sin[warp][VE * at.j]);
-            po = reinterpret_cast<T*>(dv.p) + (un >> lchunk) * dv.ts + (h0 + at.sub) * dv.hs + at.b0;
+            make_turns(a.rope, s_step, lane, s_tok[warp][stage], MANY ? 1 << ltok : 1, s_cos[warp], s_sin[warp]);
+            const int p = (MANY ? tsub * (a.rope.rot >> 1) : 0) + VE * at.j;
+            if (at.turns) tn.take(&s_cos[warp][p], &s_sin[warp][p]);
+            po = reinterpret_cast<T*>(dv.p) + t * dv.ts + (h0 + hsub) * dv.hs + at.b0;
         }
         issue(stage == 0 ? D - 1 : stage - 1);
         float2 u[H], v[H], gu[H], gw[H];
@@ -1027,6 +1068,7 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int lchunk, int 
     }
     cp_async_wait<0>();
     if (a.ws == nullptr) return;
+    __syncwarp();
     // the warp's rows, then the CTA's warps, in a fixed order
 #pragma unroll
     for (int i = 0; i < H; ++i) {
@@ -1602,26 +1644,44 @@ inline int head_chunks_log2(int64_t tokens, int steps, int warps, const DevInfo&
     return lc;
 }
 
+// Tokens (as a power of two) that share a warp's rows where a token's `heads` heads
+// leave some of the 32 >> lg free, and tokens are many enough to fill the SMs so
+// (f16, 21209 tokens of 1 + 1 heads of 64: 31 us with a token a warp).
+inline int head_tokens_log2(int64_t tokens, int heads, int lg, const DevInfo& d) {
+    int lt = 0;
+    while (lt < 5 - lg && heads <= (32 >> lg) >> (lt + 1) && tokens >> (lt + 1) >= int64_t(8) * d.sms) ++lt;
+    return lt;
+}
+
+// f of three conditions as constants.
+template <typename F>
+const void* pick3(bool a, bool b, bool c, F&& f) {
+    auto third = [&](auto x, auto y) { return c ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
+    auto second = [&](auto x) { return b ? third(x, std::true_type{}) : third(x, std::false_type{}); };
+    return a ? second(std::true_type{}) : second(std::false_type{});
+}
+
 template <typename T, int VE>
 nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo& d, cudaStream_t s) {
-    const void* fn = a.rope.adjacent ? (cache ? (const void*)&head_fwd_vec_kernel<T, VE, true, true>
-                                              : (const void*)&head_fwd_vec_kernel<T, VE, true, false>)
-                                     : (cache ? (const void*)&head_fwd_vec_kernel<T, VE, false, true>
-                                              : (const void*)&head_fwd_vec_kernel<T, VE, false, false>);
+    int lg = row_lanes_log2(a.d / (2 * VE));
+    int lt = head_tokens_log2(a.tokens, (std::max(a.heads[0], a.heads[1]) + kHeadRows - 1) / kHeadRows, lg, d);
+    const void* fn = pick3(a.rope.adjacent, cache, lt > 0, [](auto adj, auto with_cache, auto many) {
+        return (const void*)&head_fwd_vec_kernel<T, VE, adj.value, with_cache.value, many.value>;
+    });
     const size_t smem = head_fwd_smem<T, VE>();
     if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
     const int occ = cached_occupancy(fn, kHeadFwdWarps * 32, smem);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head forward kernel cannot be resident");
-    int lg = row_lanes_log2(a.d / (2 * VE));
-    const int per = (32 >> lg) * kHeadRows;
+    const int per = (32 >> lg >> lt) * kHeadRows;
     int steps = 0;
     for (int i = 0; i < (cache ? 3 : 2); ++i) steps += (a.heads[i] + per - 1) / per;
-    int lc = head_chunks_log2(a.tokens, steps, 16, d);
-    int64_t ctas = ((a.tokens << lc) + kHeadFwdWarps - 1) / kHeadFwdWarps;
+    const int64_t blocks = (a.tokens + (1 << lt) - 1) >> lt;
+    int lc = head_chunks_log2(blocks, steps, 16, d);
+    int64_t ctas = ((blocks << lc) + kHeadFwdWarps - 1) / kHeadFwdWarps;
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
     int with_norm = norm;
-    void* kargs[] = {&args, &lg, &lc, &with_norm};
+    void* kargs[] = {&args, &lg, &lt, &lc, &with_norm};
     return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadFwdWarps * 32), kargs, smem, s),
                        "head forward launch");
 }
@@ -1672,12 +1732,27 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
                     return st;
         return NRM_OK;
     }
+    BwdPlan plan{};
+    plan.lg = vec ? row_lanes_log2(a.d * int(sizeof(T)) / (2 * vec)) : 5;
+    // CTAs go to q and k by what they cost: a token's row steps, and one more for its angles
+    int steps[2];
+    int64_t blocks[2], units[2];
+    for (int i = 0; i < 2; ++i) {
+        plan.ltok[i] = vec ? head_tokens_log2(a.tokens, a.heads[i], plan.lg, *d) : 0;
+        const int per = vec ? 32 >> plan.lg >> plan.ltok[i] : kHeadWarps;
+        steps[i] = (a.heads[i] + per - 1) / per;
+        blocks[i] = (a.tokens + (1 << plan.ltok[i]) - 1) >> plan.ltok[i];
+    }
+    plan.lchunk = vec ? head_chunks_log2(a.tokens, std::max(steps[0], steps[1]), 8, *d) : 0;
+    for (int i = 0; i < 2; ++i)
+        units[i] = a.heads[i] == 0 ? 0 : (vec ? ((blocks[i] << plan.lchunk) + kHeadWarps - 1) / kHeadWarps : blocks[i]);
     const void* fn = (const void*)&head_bwd_scalar_kernel<T>;
     size_t smem = 0;
     auto take = [&](auto ve) {
         constexpr int VE = decltype(ve)::value;
-        fn = a.rope.adjacent ? (const void*)&head_bwd_vec_kernel<T, VE, true>
-                             : (const void*)&head_bwd_vec_kernel<T, VE, false>;
+        fn = pick3(a.rope.adjacent, plan.ltok[0] > 0 || plan.ltok[1] > 0, false, [](auto adj, auto many, auto) {
+            return (const void*)&head_bwd_vec_kernel<T, VE, adj.value, many.value>;
+        });
         smem = head_bwd_smem<T, VE>();
     };
     if (vec == 16) take(std::integral_constant<int, 16 / int(sizeof(T))>{});
@@ -1688,23 +1763,18 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
         if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
     const int occ = cached_occupancy(fn, kHeadWarps * 32, smem);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head backward kernel cannot be resident");
-    int lg = vec ? row_lanes_log2(a.d * int(sizeof(T)) / (2 * vec)) : 5;
-    const int per = vec ? 32 >> lg : kHeadWarps;
-    const int steps[2] = {(a.heads[0] + per - 1) / per, (a.heads[1] + per - 1) / per};
-    int lc = vec ? head_chunks_log2(a.tokens, steps[0] > steps[1] ? steps[0] : steps[1], 8, *d) : 0;
-    // CTAs go to q and k by what they cost: a token's row steps, and one more for its angles
     int64_t cap = int64_t(occ) * d->sms;
     if (cap > head_bwd_max_partials(*d)) cap = head_bwd_max_partials(*d);
-    const int64_t units = vec ? ((a.tokens << lc) + kHeadWarps - 1) / kHeadWarps : a.tokens;
     int64_t cq = cap, ck = 0;
     if (a.heads[1]) {
-        ck = cap * (steps[1] + 1) / (steps[0] + steps[1] + 2);
-        if (ck < 1) ck = 1;
+        const double cost[2] = {double(blocks[0]) * (steps[0] + 1), double(blocks[1]) * (steps[1] + 1)};
+        ck = std::min(std::max(int64_t(double(cap) * (cost[1] / (cost[0] + cost[1]))), int64_t(1)), cap - 1);
         cq = cap - ck;
     }
-    int nq = int(cq < units ? cq : units), nk = int(ck < units ? ck : units);
+    plan.nq = int(std::min(cq, units[0]));
+    int nq = plan.nq, nk = int(std::min(ck, units[1]));
     HeadArgs args = a;
-    void* kargs_vec[] = {&args, &lg, &lc, &nq};
+    void* kargs_vec[] = {&args, &plan};
     void* kargs[] = {&args, &nq};
     nrm_status st = cuda_status(cudaLaunchKernel(fn, dim3(unsigned(nq + nk)), dim3(kHeadWarps * 32),
                                                  vec ? kargs_vec : kargs, smem, s),

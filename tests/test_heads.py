@@ -137,6 +137,10 @@ LAYOUTS = [
     ("bf16", 8, 2, 2, 128, 124, "half", 1, False, 2),
     ("f16", 40, 12, 1, 40, 20, "half", 1, True, 0),
     ("bf16", 2000, 3, 1, 64, 64, "pair", 2, False, 0),
+    # few heads of many tokens: several tokens share a warp's rows
+    ("bf16", 20001, 1, 1, 16, 8, "half", 2, False, 0),
+    ("f16", 5003, 2, 1, 64, 64, "pair", 1, True, 0),
+    ("f32", 2503, 1, 2, 128, 64, "half", 3, False, 0),
 ]
 
 
@@ -581,6 +585,9 @@ SERVED = [
     ("bf16", 6, 3, 1, 64, 64, "pair", 1, False, 2, "int8", 2, 5, "head"),
     ("f16", 3, 2, 2, 128, 128, "pair", 1, False, 0, "int8", 32, 5, "token"),
     ("bf16", 3, 2, 2, 128, 128, "pair", 1, False, 0, "e4m3", 16, 5, "token"),
+    ("bf16", 5003, 2, 1, 64, 64, "half", 1, True, 0, "int8", 32, 64, "head"),
+    ("f16", 2601, 1, 1, 128, 128, "pair", 2, False, 0, "int4", 32, 64, "token"),
+    ("bf16", 10003, 1, 1, 64, 32, "half", 1, False, 0, "e4m3", 16, 64, "token"),
 ]
 
 
