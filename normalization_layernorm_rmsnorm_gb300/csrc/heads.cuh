@@ -20,7 +20,6 @@
 namespace nrm {
 
 constexpr int kHeadWarps = 8;                       // warps of a CTA
-constexpr int kHeadSlots = kHeadMaxPairs / 32;      // pair slots of a lane
 
 // ---------------------------------------------------------------------------
 // angles
@@ -1341,6 +1340,10 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
 // ---------------------------------------------------------------------------
 // any layout: a row per warp, two elements per slot
 // ---------------------------------------------------------------------------
+// Rows whose rotated halves start between vectors (rot/2 odd), unaligned views, odd
+// d.  Bound by latency and issue slots; a warp has 4 / S rows of S slots a lane
+// under way.  bf16, 6653 tokens of 24 + 12 heads of 40 with 10 rotated (38 MB): 55
+// us, one row at a time 64; about 250 instructions a row.
 
 // The elements of pair slot j (e1 == d: past the end of an odd row) and whether they turn.
 struct SlotAt {
@@ -1366,83 +1369,114 @@ __device__ __forceinline__ float round_to(float v) {
     return Io<T>::load(Io<T>::store(v));
 }
 
-template <typename T, bool NORM, bool CACHE>
+// The turns per position of a lane's slots, and the axes.
+template <int S>
+struct SlotSteps {
+    uint64_t step[S];
+    int axis;
+    __device__ __forceinline__ SlotSteps(const RopeDev& r, int lane) : axis(0) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            step[s] = 0;
+            if (2 * (lane + 32 * s) < r.rot) {
+                step[s] = turn_step(__ldg(r.inv_freq + lane + 32 * s));
+                axis |= pair_axis(r, lane + 32 * s) << (2 * s);
+            }
+        }
+    }
+    __device__ __forceinline__ void make(const RopeDev& r, int lane, int64_t t, float2 (&cs)[S]) const {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (2 * (lane + 32 * s) < r.rot)
+                cs[s] = pair_turn(r, step[s], __ldg(r.pos + (axis >> (2 * s) & 3) * r.pos_stride + t));
+    }
+};
+
+template <typename T, int S, bool CACHE>
 __global__ void __launch_bounds__(kHeadWarps * 32)
-head_fwd_scalar_kernel(const __grid_constant__ HeadArgs a) {
+head_fwd_scalar_kernel(const __grid_constant__ HeadArgs a, int norm) {
+    constexpr int R = 4 / S;  // rows of a warp under way
     __shared__ float stage[CACHE ? kHeadWarps : 1][CACHE ? kHeadMaxD : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = a.heads[0] + a.heads[1] + (CACHE ? a.heads[2] : 0);
     const int slots = (a.d + 1) >> 1;
+    const SlotSteps<S> steps(a.rope, lane);
+    SlotAt e[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) e[s] = slot_at(lane + 32 * s, a.d, a.rope);
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        float2 cs[kHeadSlots];
-#pragma unroll
-        for (int s = 0; s < kHeadSlots; ++s)
-            if (2 * (lane + 32 * s) < a.rope.rot)
-                cs[s] = pair_turn(a.rope, turn_step(__ldg(a.rope.inv_freq + lane + 32 * s)),
-                                  __ldg(a.rope.pos + pair_axis(a.rope, lane + 32 * s) * a.rope.pos_stride + t));
+        float2 cs[S];
+        steps.make(a.rope, lane, t, cs);
         const int64_t slot = CACHE ? cache_slot(a.cache, __ldg(a.slots + t), a.err) : -1;
-        for (int hh = warp + int(blockIdx.y) * kHeadWarps; hh < heads; hh += int(gridDim.y) * kHeadWarps) {
-            const int which = hh < a.heads[0] ? 0 : (hh < a.heads[0] + a.heads[1] ? 1 : 2);
-            const int h = hh - (which > 0 ? a.heads[0] : 0) - (which > 1 ? a.heads[1] : 0);
-            const HeadView xv = a.x[which];
-            const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + h * xv.hs;
-            float u[kHeadSlots], v[kHeadSlots];
-            float sum = 0.f;
+        const int apart = int(gridDim.y) * kHeadWarps;  // heads of a warp
+        for (int h0 = warp + int(blockIdx.y) * kHeadWarps; h0 < heads; h0 += apart * R) {
+            int which[R], hd[R];
+            float u[R][S], v[R][S];
 #pragma unroll
-            for (int s = 0; s < kHeadSlots; ++s) {
-                const int j = lane + 32 * s;
-                u[s] = v[s] = 0.f;
-                if (j < slots) {
-                    const SlotAt e = slot_at(j, a.d, a.rope);
-                    u[s] = ld_elem<T>(x, e.e0);
-                    if (e.e1 < a.d) v[s] = ld_elem<T>(x, e.e1);
-                    if (NORM) sum = fmaf(u[s], u[s], fmaf(v[s], v[s], sum));
+            for (int k = 0; k < R; ++k) {
+                const int hh = h0 + k * apart;
+                which[k] = hh < a.heads[0] ? 0 : (hh < a.heads[0] + a.heads[1] ? 1 : (hh < heads ? 2 : 3));
+                hd[k] = hh - (which[k] > 0 ? a.heads[0] : 0) - (which[k] > 1 ? a.heads[1] : 0);
+                const HeadView xv = a.x[which[k] < 3 ? which[k] : 0];
+                const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + hd[k] * xv.hs;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    u[k][s] = v[k][s] = 0.f;
+                    if (which[k] < 3 && lane + 32 * s < slots) {
+                        u[k][s] = ld_elem<T>(x, e[s].e0);
+                        if (e[s].e1 < a.d) v[k][s] = ld_elem<T>(x, e[s].e1);
+                    }
                 }
             }
-            if (which < 2) {
-                float r = 1.f;
-                if (NORM) {
-                    r = rsqrtf(warp_sum(sum) / float(a.d) + a.eps);
-                    if (lane == 0 && a.rstd[which]) a.rstd[which][t * a.heads[which] + h] = r;
-                }
 #pragma unroll
-                for (int s = 0; s < kHeadSlots; ++s) {
-                    const int j = lane + 32 * s;
-                    if (j < slots) {
-                        const SlotAt e = slot_at(j, a.d, a.rope);
-                        if (NORM) {
-                            u[s] = __fmul_rn(u[s], r);
-                            v[s] = __fmul_rn(v[s], r);
-                            if (a.w[which]) {
-                                u[s] = __fmul_rn(u[s], ld_elem<T>(a.w[which], e.e0));
-                                if (e.e1 < a.d) v[s] = __fmul_rn(v[s], ld_elem<T>(a.w[which], e.e1));
+            for (int k = 0; k < R; ++k) {
+                if (which[k] < 2) {
+                    float r = 1.f;
+                    if (norm) {
+                        float sum = 0.f;
+#pragma unroll
+                        for (int s = 0; s < S; ++s) sum = fmaf(u[k][s], u[k][s], fmaf(v[k][s], v[k][s], sum));
+                        r = rsqrtf(warp_sum(sum) / float(a.d) + a.eps);
+                        float* rstd = a.rstd[which[k]];
+                        if (lane == 0 && rstd) rstd[t * a.heads[which[k]] + hd[k]] = r;
+                    }
+                    const HeadView yv = a.y[which[k]];
+                    T* y = reinterpret_cast<T*>(yv.p) + t * yv.ts + hd[k] * yv.hs;
+                    const void* w = a.w[which[k]];
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        if (lane + 32 * s < slots) {
+                            const bool two = e[s].e1 < a.d;
+                            if (norm) {
+                                u[k][s] = __fmul_rn(u[k][s], r);
+                                v[k][s] = __fmul_rn(v[k][s], r);
+                                if (w) {
+                                    u[k][s] = __fmul_rn(u[k][s], ld_elem<T>(w, e[s].e0));
+                                    if (two) v[k][s] = __fmul_rn(v[k][s], ld_elem<T>(w, e[s].e1));
+                                }
+                            }
+                            if (e[s].turns) turn(u[k][s], v[k][s], cs[s]);
+                            if (yv.p) {
+                                st_elem<T>(y, e[s].e0, u[k][s]);
+                                if (two) st_elem<T>(y, e[s].e1, v[k][s]);
                             }
                         }
-                        if (e.turns) turn(u[s], v[s], cs[s]);
-                        const HeadView yv = a.y[which];
-                        if (yv.p) {
-                            T* y = reinterpret_cast<T*>(yv.p) + t * yv.ts + h * yv.hs;
-                            st_elem<T>(y, e.e0, u[s]);
-                            if (e.e1 < a.d) st_elem<T>(y, e.e1, v[s]);
+                    }
+                }
+                if (CACHE && which[k] > 0 && which[k] < 3 && slot >= 0) {
+                    // the cache stores the key in the activations' type: what a separate write would read
+                    float* row = stage[warp];
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        if (lane + 32 * s < slots) {
+                            row[e[s].e0] = round_to<T>(u[k][s]);
+                            if (e[s].e1 < a.d) row[e[s].e1] = round_to<T>(v[k][s]);
                         }
                     }
+                    __syncwarp();
+                    quantise_row<T>(row, a.d, a.cache, which[k] - 1, slot, hd[k], lane);
+                    __syncwarp();
                 }
-            }
-            if (CACHE && which > 0 && slot >= 0) {
-                // the cache stores the key in the activations' type: what a separate write would read
-                float* row = stage[warp];
-#pragma unroll
-                for (int s = 0; s < kHeadSlots; ++s) {
-                    const int j = lane + 32 * s;
-                    if (j < slots) {
-                        const SlotAt e = slot_at(j, a.d, a.rope);
-                        row[e.e0] = round_to<T>(u[s]);
-                        if (e.e1 < a.d) row[e.e1] = round_to<T>(v[s]);
-                    }
-                }
-                __syncwarp();
-                quantise_row<T>(row, a.d, a.cache, which - 1, slot, h, lane);
-                __syncwarp();
             }
         }
     }
@@ -1450,73 +1484,84 @@ head_fwd_scalar_kernel(const __grid_constant__ HeadArgs a) {
 
 // Backward.  CTAs [0, nq) take q, the others k, so that a thread's sums for dw
 // belong to one weight; each CTA writes its partial row [d].
-template <typename T>
+template <typename T, int S>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 head_bwd_scalar_kernel(const __grid_constant__ HeadArgs a, int nq) {
+    constexpr int R = 4 / S;  // rows of a warp under way
     __shared__ float part[kHeadWarps][kHeadMaxD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int which = int(blockIdx.x) < nq ? 0 : 1;
     const int cta = int(blockIdx.x) - (which ? nq : 0);
     const int ctas = which ? int(gridDim.x) - nq : nq;
-    const int slots = (a.d + 1) >> 1;
-    float acc_u[kHeadSlots] = {}, acc_v[kHeadSlots] = {};
+    const int slots = (a.d + 1) >> 1, heads = a.heads[which];
+    const SlotSteps<S> steps(a.rope, lane);
+    SlotAt e[S];
+    float w0[S], w1[S], acc_u[S], acc_v[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        e[s] = slot_at(lane + 32 * s, a.d, a.rope);
+        w0[s] = w1[s] = 1.f;
+        acc_u[s] = acc_v[s] = 0.f;
+        if (a.w[which] && lane + 32 * s < slots) {
+            w0[s] = ld_elem<T>(a.w[which], e[s].e0);
+            if (e[s].e1 < a.d) w1[s] = ld_elem<T>(a.w[which], e[s].e1);
+        }
+    }
     for (int64_t t = cta; t < a.tokens; t += ctas) {
-        float2 cs[kHeadSlots];
+        float2 cs[S];
+        steps.make(a.rope, lane, t, cs);
+        for (int h0 = warp; h0 < heads; h0 += kHeadWarps * R) {
+            float u[R][S], v[R][S], gu[R][S], gv[R][S], r[R];
 #pragma unroll
-        for (int s = 0; s < kHeadSlots; ++s)
-            if (2 * (lane + 32 * s) < a.rope.rot)
-                cs[s] = pair_turn(a.rope, turn_step(__ldg(a.rope.inv_freq + lane + 32 * s)),
-                                  __ldg(a.rope.pos + pair_axis(a.rope, lane + 32 * s) * a.rope.pos_stride + t));
-        for (int h = warp; h < a.heads[which]; h += kHeadWarps) {
-            const T* x = reinterpret_cast<const T*>(a.x[which].p) + t * a.x[which].ts + h * a.x[which].hs;
-            const T* dy = reinterpret_cast<const T*>(a.dy[which].p) + t * a.dy[which].ts + h * a.dy[which].hs;
-            T* dx = reinterpret_cast<T*>(a.y[which].p) + t * a.y[which].ts + h * a.y[which].hs;
-            const float r = a.rstd[which][t * a.heads[which] + h];
-            float u[kHeadSlots], v[kHeadSlots], gu[kHeadSlots], gv[kHeadSlots];
-            float sum = 0.f;
+            for (int k = 0; k < R; ++k) {
+                const int h = h0 + k * kHeadWarps;
+                const T* x = reinterpret_cast<const T*>(a.x[which].p) + t * a.x[which].ts + h * a.x[which].hs;
+                const T* dy = reinterpret_cast<const T*>(a.dy[which].p) + t * a.dy[which].ts + h * a.dy[which].hs;
+                r[k] = h < heads ? a.rstd[which][t * heads + h] : 0.f;
 #pragma unroll
-            for (int s = 0; s < kHeadSlots; ++s) {
-                const int j = lane + 32 * s;
-                u[s] = v[s] = gu[s] = gv[s] = 0.f;
-                if (j < slots) {
-                    const SlotAt e = slot_at(j, a.d, a.rope);
-                    const bool two = e.e1 < a.d;
-                    u[s] = ld_elem<T>(x, e.e0);
-                    gu[s] = ld_elem<T>(dy, e.e0);
-                    if (two) {
-                        v[s] = ld_elem<T>(x, e.e1);
-                        gv[s] = ld_elem<T>(dy, e.e1);
+                for (int s = 0; s < S; ++s) {
+                    u[k][s] = v[k][s] = gu[k][s] = gv[k][s] = 0.f;
+                    if (h < heads && lane + 32 * s < slots) {
+                        u[k][s] = ld_elem<T>(x, e[s].e0);
+                        gu[k][s] = ld_elem<T>(dy, e[s].e0);
+                        if (e[s].e1 < a.d) {
+                            v[k][s] = ld_elem<T>(x, e[s].e1);
+                            gv[k][s] = ld_elem<T>(dy, e[s].e1);
+                        }
                     }
-                    if (e.turns) turn(gu[s], gv[s], cs[s]);
-                    acc_u[s] = fmaf(gu[s], u[s] * r, acc_u[s]);
-                    acc_v[s] = fmaf(gv[s], v[s] * r, acc_v[s]);
-                    if (a.w[which]) {
-                        gu[s] *= ld_elem<T>(a.w[which], e.e0);
-                        if (two) gv[s] *= ld_elem<T>(a.w[which], e.e1);
-                    }
-                    sum = fmaf(gu[s], u[s], fmaf(gv[s], v[s], sum));
                 }
             }
-            const float f = warp_sum(sum) / float(a.d) * r * r * r;
 #pragma unroll
-            for (int s = 0; s < kHeadSlots; ++s) {
-                const int j = lane + 32 * s;
-                if (j < slots) {
-                    const SlotAt e = slot_at(j, a.d, a.rope);
-                    st_elem<T>(dx, e.e0, fmaf(-u[s], f, gu[s] * r));
-                    if (e.e1 < a.d) st_elem<T>(dx, e.e1, fmaf(-v[s], f, gv[s] * r));
+            for (int k = 0; k < R; ++k) {
+                float sum = 0.f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    if (e[s].turns) turn(gu[k][s], gv[k][s], cs[s]);
+                    acc_u[s] = fmaf(gu[k][s], u[k][s] * r[k], acc_u[s]);
+                    acc_v[s] = fmaf(gv[k][s], v[k][s] * r[k], acc_v[s]);
+                    gu[k][s] *= w0[s];
+                    gv[k][s] *= w1[s];
+                    sum = fmaf(gu[k][s], u[k][s], fmaf(gv[k][s], v[k][s], sum));
+                }
+                const float f = warp_sum(sum) / float(a.d) * r[k] * r[k] * r[k];
+                const int h = h0 + k * kHeadWarps;
+                T* dx = reinterpret_cast<T*>(a.y[which].p) + t * a.y[which].ts + h * a.y[which].hs;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    if (h < heads && lane + 32 * s < slots) {
+                        st_elem<T>(dx, e[s].e0, fmaf(-u[k][s], f, gu[k][s] * r[k]));
+                        if (e[s].e1 < a.d) st_elem<T>(dx, e[s].e1, fmaf(-v[k][s], f, gv[k][s] * r[k]));
+                    }
                 }
             }
         }
     }
     if (a.ws == nullptr) return;
 #pragma unroll
-    for (int s = 0; s < kHeadSlots; ++s) {
-        const int j = lane + 32 * s;
-        if (j < slots) {
-            const SlotAt e = slot_at(j, a.d, a.rope);
-            part[warp][e.e0] = acc_u[s];
-            if (e.e1 < a.d) part[warp][e.e1] = acc_v[s];
+    for (int s = 0; s < S; ++s) {
+        if (lane + 32 * s < slots) {
+            part[warp][e[s].e0] = acc_u[s];
+            if (e[s].e1 < a.d) part[warp][e[s].e1] = acc_v[s];
         }
     }
     __syncthreads();
@@ -1686,22 +1731,33 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
                        "head forward launch");
 }
 
+// f of the slots that a lane of a scalar kernel holds: 1, 2 or 4 for d up to 64, 128, 256.
+template <typename F>
+const void* pick_slots(int d, F&& f) {
+    if (d <= 64) return f(std::integral_constant<int, 1>{});
+    if (d <= 128) return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 4>{});
+}
+
 template <typename T>
 nrm_status head_fwd_scalar(const HeadArgs& a, bool norm, bool cache, const DevInfo& d, cudaStream_t s) {
-    const void* fn = norm ? (cache ? (const void*)&head_fwd_scalar_kernel<T, true, true>
-                                   : (const void*)&head_fwd_scalar_kernel<T, true, false>)
-                          : (cache ? (const void*)&head_fwd_scalar_kernel<T, false, true>
-                                   : (const void*)&head_fwd_scalar_kernel<T, false, false>);
+    int rows = 0;
+    const void* fn = pick_slots(a.d, [&](auto n) {
+        rows = 4 / n.value * kHeadWarps;
+        return cache ? (const void*)&head_fwd_scalar_kernel<T, n.value, true>
+                     : (const void*)&head_fwd_scalar_kernel<T, n.value, false>;
+    });
     const int occ = cached_occupancy(fn, kHeadWarps * 32, 0);
     if (occ <= 0) return fail(NRM_ERR_CUDA, "head forward kernel cannot be resident");
     const int64_t cap = int64_t(occ) * d.sms;
     const int heads = a.heads[0] + a.heads[1] + (cache ? a.heads[2] : 0);
     // few tokens: their heads are split over CTAs
     const int64_t gx = a.tokens < cap ? a.tokens : cap;
-    int64_t gy = (heads + kHeadWarps - 1) / kHeadWarps;
+    int64_t gy = (heads + rows - 1) / rows;
     if (gy > (cap + gx - 1) / gx) gy = (cap + gx - 1) / gx;
     HeadArgs args = a;
-    void* kargs[] = {&args};
+    int with_norm = norm;
+    void* kargs[] = {&args, &with_norm};
     return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(gx), unsigned(gy)), dim3(kHeadWarps * 32), kargs, 0, s),
                        "head forward launch");
 }
@@ -1746,7 +1802,7 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
     plan.lchunk = vec ? head_chunks_log2(a.tokens, std::max(steps[0], steps[1]), 8, *d) : 0;
     for (int i = 0; i < 2; ++i)
         units[i] = a.heads[i] == 0 ? 0 : (vec ? ((blocks[i] << plan.lchunk) + kHeadWarps - 1) / kHeadWarps : blocks[i]);
-    const void* fn = (const void*)&head_bwd_scalar_kernel<T>;
+    const void* fn = pick_slots(a.d, [](auto n) { return (const void*)&head_bwd_scalar_kernel<T, n.value>; });
     size_t smem = 0;
     auto take = [&](auto ve) {
         constexpr int VE = decltype(ve)::value;
