@@ -1572,11 +1572,11 @@ head_bwd_scalar_kernel(const __grid_constant__ HeadArgs a, int nq) {
     }
 }
 
-// (About 2.5 us, most of it launch and the first loads, under the backward's tail.)
 // dw of q (blockIdx.y 0) and of k (1): the column sums of their partial rows, in
 // a fixed order.  A column's rows are split over the 32 warps of a CTA; the
 // partial rows can be much larger than their sum, so both levels carry the
-// rounding error along (Neumaier's sum).
+// rounding error along (Neumaier's sum).  About 3 us after the backward, most of it
+// launch and the first loads; a tree of float pairs over the warps was no faster.
 constexpr int kHeadSumWarps = 32;
 struct CarriedSum {
     float s = 0.f, c = 0.f;
