@@ -460,7 +460,7 @@ typedef struct nrm_rope {
  * wq, wk: [d] in dt, one weight for all heads, each may be NULL (1).
  * q_out, k_out: views with the heads of q and k; each may be its input in
  * place.  rstd_q [tokens, hq], rstd_k [tokens, hk]: float32, dense, receive r;
- * each may be NULL.  eps > 0.
+ * each may be NULL; not one memory.  eps > 0.
  */
 NRM_API nrm_status nrm_qk_norm_rope_fwd(const nrm_heads *q, const nrm_heads *k, const void *wq,
                                 const void *wk, const nrm_rope *rope, const nrm_heads *q_out,
@@ -474,8 +474,9 @@ NRM_API nrm_status nrm_qk_norm_rope_fwd(const nrm_heads *q, const nrm_heads *k, 
  *   dx = r*g - x*r^3*s/d;  dw_i = sum over tokens and heads of g'_i*x_i*r
  * dq_out, dk_out: the gradients of q_out, k_out; q, k, wq, wk, rope: those of
  * the forward; rstd_q, rstd_k: as it wrote them.  dq, dk: output views (not
- * in place).  dwq, dwk: [d] in dt, each may be NULL.  k (with dk_out, dk) may
- * be NULL.  workspace: nrm_workspace_bytes(NRM_OP_QK_NORM_BWD, tokens, d, dt)
+ * in place).  dwq, dwk: [d] in dt, each may be NULL; where q and k share a
+ * weight they are its two parts, not one memory.  k may be NULL (then dk_out,
+ * wk, rstd_k, dk are ignored, and dwk is NULL).  workspace: nrm_workspace_bytes(NRM_OP_QK_NORM_BWD, tokens, d, dt)
  * bytes, 16-byte aligned, clobbered; may be NULL when dwq and dwk are NULL.
  * Calls that overlap on the GPU need separate workspaces.
  * With tokens == 0, dwq and dwk are set to 0.

@@ -283,8 +283,13 @@ nrm_status nrm_qk_norm_rope_fwd(const nrm_heads* q, const nrm_heads* k, const vo
         HeadArgs a;
         NRM_TRY(set_fwd(q, k, rope, q_out, k_out, false, tokens, d, dt, false, &a));
         NRM_TRY(check_eps(eps));
+        if (!k) {
+            wk = nullptr;
+            rstd_k = nullptr;
+        }
         NRM_TRY(check_stats({wq, wk}, dsize(dt)));
         NRM_TRY(check_stats({rstd_q, rstd_k}, 4));
+        if (rstd_q && rstd_q == rstd_k) return fail(NRM_ERR_INVALID_ARG, "rstd_q and rstd_k are the same memory");
         a.w[0] = wq;
         a.w[1] = wk;
         a.rstd[0] = rstd_q;
@@ -317,7 +322,10 @@ nrm_status nrm_qk_norm_rope_bwd(const nrm_heads* dq_out, const nrm_heads* dk_out
             return fail(NRM_ERR_INVALID_ARG, "dwk without k");
         } else {
             dk_out = dk = nullptr;
+            wk = nullptr;
+            rstd_k = nullptr;
         }
+        if (dwq && dwq == dwk) return fail(NRM_ERR_INVALID_ARG, "dwq and dwk are the same memory");
         for (const nrm_heads* in : {q, k, dq_out, dk_out}) {
             NRM_TRY(check_place("dq", dq, in, false, tokens));
             NRM_TRY(check_place("dk", dk, in, false, tokens));

@@ -220,7 +220,7 @@ void key_views(View& vk, View& v2, const at::Tensor& k, const char* name, PyObje
 PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* args, Py_ssize_t given) {
     return entry(args, given, 14, [](PyObject* const* o) {
         const at::Tensor &q = *tensor(o[0], "q"), *k = tensor(o[1], "k", true);
-        const at::Tensor *wq = tensor(o[2], "wq", true), *wk = tensor(o[3], "wk", true);
+        const at::Tensor *wq = tensor(o[2], "wq", true), *wk = k ? tensor(o[3], "wk", true) : nullptr;
         const at::Tensor *pos = tensor(o[4], "pos", true), *inv = tensor(o[5], "inv_freq", true);
         const at::Tensor &qo = *tensor(o[6], "q_out"), *ko = nullptr;
         const at::Tensor *rq = tensor(o[8], "rstd_q", true), *rk = k ? tensor(o[9], "rstd_k", true) : nullptr;
@@ -249,7 +249,7 @@ PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* args, Py_ssize_t given) {
 PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t given) {
     return entry(args, given, 18, [](PyObject* const* o) {
         const at::Tensor &dqo = *tensor(o[0], "dq_out"), &q = *tensor(o[2], "q"), *k = tensor(o[3], "k", true);
-        const at::Tensor *wq = tensor(o[4], "wq", true), *wk = tensor(o[5], "wk", true);
+        const at::Tensor *wq = tensor(o[4], "wq", true), *wk = k ? tensor(o[5], "wk", true) : nullptr;
         const at::Tensor *rq = tensor(o[6], "rstd_q", true), *rk = k ? tensor(o[7], "rstd_k", true) : nullptr;
         const at::Tensor *pos = tensor(o[8], "pos", true), *inv = tensor(o[9], "inv_freq", true);
         const at::Tensor &dq = *tensor(o[10], "dq"), *dko = nullptr, *dk = nullptr;

@@ -168,6 +168,7 @@ def fused(lib, q=None, k=None, v=None, qo=None, ko=None, c=None, slots=P, r=None
     (lambda L: fwd(L, k=H(2 * P), ko=H(3 * P)), 1),
     (lambda L: fwd(L, wq=P + 1), 1),
     (lambda L: fwd(L, rq=P + 2), 1),
+    (lambda L: L.nrm_qk_norm_rope_fwd(H(), H(2 * P), None, None, None, H(3 * P), H(4 * P), P, P, 8, 16, 1e-6, 0, None), 1),
     # rotations
     (lambda L: fwd(L, r=R(rot=15)), 1),
     (lambda L: fwd(L, r=R(rot=18)), 1),
@@ -188,6 +189,7 @@ def fused(lib, q=None, k=None, v=None, qo=None, ko=None, c=None, slots=P, r=None
     (lambda L: bwd(L, dq=H()), 1),
     (lambda L: bwd(L, dq=H(2 * P)), 1),
     (lambda L: bwd(L, dwk=P), 1),
+    (lambda L: bwd(L, k=H(4 * P), dko=H(5 * P), dk=H(6 * P), rk=P, dwq=P, dwk=P), 1),
     (lambda L: bwd(L, k=H(4 * P), dko=H(5 * P), dk=H(6 * P)), 1),
     (lambda L: bwd(L, k=H(4 * P), dko=H(5 * P), dk=H(3 * P), rk=P), 1),
     (lambda L: bwd(L, r=R(rot=17)), 1),
@@ -233,6 +235,16 @@ def fused(lib, q=None, k=None, v=None, qo=None, ko=None, c=None, slots=P, r=None
 def test_bad_arguments_are_refused_on_the_host(lib, call, expect):
     assert call(lib) == expect
     assert nrm.nrm_last_error_message() != ""
+
+
+def test_without_keys_their_arguments_are_ignored(lib):
+    # (no tokens: nothing is enqueued on a GPU)
+    odd = P + 1
+    assert lib.nrm_qk_norm_rope_fwd(H(), None, None, odd, None, H(3 * P), None, None, odd, 0, 16, 1e-6, 0, None) != 1
+    assert lib.nrm_qk_norm_rope_bwd(H(2 * P), None, H(), None, None, odd, P, odd, None, H(3 * P), None, None, None, 0, 16,
+                                    0, None, 0, None) != 1
+    with pytest.raises(ValueError, match="current CUDA device"):
+        nrm.nrm_qk_norm_rope_fwd(**_qk(wk=torch.ones(3), rstd_k=torch.ones(5)))
 
 
 def test_structures_match_the_header(tmp_path):
