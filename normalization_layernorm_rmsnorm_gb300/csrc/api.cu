@@ -164,10 +164,11 @@ int max_active_clusters(const void* fn, int cs, int block, size_t smem) {
     return n;
 }
 
-nrm_status launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t s) {
+nrm_status launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t s, size_t smem) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

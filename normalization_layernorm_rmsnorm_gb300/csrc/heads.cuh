@@ -21,6 +21,14 @@ namespace nrm {
 
 constexpr int kHeadWarps = 8;                       // warps of a CTA
 
+// Every kernel here is launched with its predecessor in the stream still running:
+// it sets up its indices, then waits for that kernel's end before it touches
+// memory, and lets its own successor be launched.
+__device__ __forceinline__ void pdl_next() {
+    pdl_wait();
+    pdl_trigger();
+}
+
 // ---------------------------------------------------------------------------
 // angles
 // ---------------------------------------------------------------------------
@@ -682,6 +690,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
+    pdl_next();
     fill_steps(a.rope, s_step, threadIdx.x, N);
     __syncthreads();
     // the warp's rows are `rows` heads of each of its tokens
@@ -932,9 +941,9 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ 
     const int ctas = which ? int(gridDim.x) - plan.nq : plan.nq;
     const int lg = plan.lg, lchunk = plan.lchunk, ltok = MANY ? plan.ltok[which] : 0;
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
+    pdl_next();
     fill_steps(a.rope, s_step, threadIdx.x, N);
     __syncthreads();
-    pdl_trigger();  // the column sums' CTAs start, and wait for this grid's end
     const int heads = a.heads[which], mask = (1 << lchunk) - 1;
     // the warp's rows are 2^lhp heads of each of its tokens
     const int lhp = 5 - lg - ltok;
@@ -1147,6 +1156,7 @@ cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
         return un < units && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
     };
     int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp;
+    pdl_next();
     int64_t asked = ask(un);
     for (; un < units; un += stride) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
@@ -1288,6 +1298,7 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
         return un < units && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
     };
     int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp;
+    pdl_next();
     int64_t asked = ask(un);
     for (; un < units; un += stride) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
@@ -1400,6 +1411,7 @@ head_fwd_scalar_kernel(const __grid_constant__ HeadArgs a, int norm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = a.heads[0] + a.heads[1] + (CACHE ? a.heads[2] : 0);
     const int slots = (a.d + 1) >> 1;
+    pdl_next();
     const SlotSteps<S> steps(a.rope, lane);
     SlotAt e[S];
 #pragma unroll
@@ -1494,6 +1506,7 @@ head_bwd_scalar_kernel(const __grid_constant__ HeadArgs a, int nq) {
     const int cta = int(blockIdx.x) - (which ? nq : 0);
     const int ctas = which ? int(gridDim.x) - nq : nq;
     const int slots = (a.d + 1) >> 1, heads = a.heads[which];
+    pdl_next();
     const SlotSteps<S> steps(a.rope, lane);
     SlotAt e[S];
     float w0[S], w1[S], acc_u[S], acc_v[S];
@@ -1589,7 +1602,7 @@ struct CarriedSum {
 template <typename T>
 __global__ void __launch_bounds__(kHeadSumWarps * 32)
 head_dw_kernel(const float* __restrict__ ws, int d, int nq, int nk, T* dwq, T* dwk) {
-    pdl_wait();
+    pdl_next();
     const int which = blockIdx.y;
     T* out = which ? dwk : dwq;
     if (out == nullptr) return;
@@ -1630,6 +1643,7 @@ cache_write_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads) {
     float* row = stage[warp];
     const int heads = a.heads[1];
     const int64_t rows = a.tokens * heads;
+    pdl_next();
     for (int64_t i = int64_t(blockIdx.x) * kHeadWarps + warp; i < rows; i += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = row_div(i, by_heads);
         const int h = int(i - t * heads);
@@ -1651,6 +1665,7 @@ cache_read_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads) {
     const HeadView yv = a.y[which];
     const int heads = a.heads[1];
     const int64_t rows = a.tokens * heads;
+    pdl_next();
     for (int64_t i = int64_t(blockIdx.x) * kHeadWarps + warp; i < rows; i += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = row_div(i, by_heads);
         const int h = int(i - t * heads);
@@ -1727,8 +1742,7 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
     HeadArgs args = a;
     int with_norm = norm;
     void* kargs[] = {&args, &lg, &lt, &lc, &with_norm};
-    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadFwdWarps * 32), kargs, smem, s),
-                       "head forward launch");
+    return launch_pdl(fn, dim3(unsigned(ctas)), dim3(kHeadFwdWarps * 32), kargs, s, smem);
 }
 
 // f of the slots that a lane of a scalar kernel holds: 1, 2 or 4 for d up to 64, 128, 256.
@@ -1758,8 +1772,7 @@ nrm_status head_fwd_scalar(const HeadArgs& a, bool norm, bool cache, const DevIn
     HeadArgs args = a;
     int with_norm = norm;
     void* kargs[] = {&args, &with_norm};
-    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(gx), unsigned(gy)), dim3(kHeadWarps * 32), kargs, 0, s),
-                       "head forward launch");
+    return launch_pdl(fn, dim3(unsigned(gx), unsigned(gy)), dim3(kHeadWarps * 32), kargs, s);
 }
 
 template <typename T>
@@ -1832,9 +1845,7 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
     HeadArgs args = a;
     void* kargs_vec[] = {&args, &plan};
     void* kargs[] = {&args, &nq};
-    nrm_status st = cuda_status(cudaLaunchKernel(fn, dim3(unsigned(nq + nk)), dim3(kHeadWarps * 32),
-                                                 vec ? kargs_vec : kargs, smem, s),
-                                "head backward launch");
+    nrm_status st = launch_pdl(fn, dim3(unsigned(nq + nk)), dim3(kHeadWarps * 32), vec ? kargs_vec : kargs, s, smem);
     if (st != NRM_OK || a.ws == nullptr) return st;
     const float* ws = a.ws;
     int dd = a.d;
@@ -1856,8 +1867,7 @@ nrm_status cache_launch_scalar(const HeadArgs& a, const void* fn, bool both, con
     HeadArgs args = a;
     RowDiv by_heads = make_row_div(a.heads[1], rows);
     void* kargs[] = {&args, &by_heads};
-    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas), both ? 2 : 1), dim3(kHeadWarps * 32), kargs, 0, s),
-                       "cache launch");
+    return launch_pdl(fn, dim3(unsigned(ctas), both ? 2 : 1), dim3(kHeadWarps * 32), kargs, s);
 }
 
 // `lanes` lanes of a row hold vectors, `gl` of them a group.
@@ -1878,7 +1888,7 @@ inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes,
     if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
     HeadArgs args = a;
     void* kargs[] = {&args, &cl};
-    return cuda_status(cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, 0, s), "cache launch");
+    return launch_pdl(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, s);
 }
 
 // Whether rows start on 32 bytes in every given view.

@@ -43,7 +43,7 @@ nrm_status prepare_kernel(const void* fn, size_t dyn_smem, bool nonportable_clus
 int max_active_clusters(const void* fn, int cs, int block, size_t smem);
 // Launch with programmatic stream serialisation (the kernel waits on its
 // predecessor with griddepcontrol.wait, so its launch overlaps the predecessor).
-nrm_status launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t s);
+nrm_status launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t s, size_t smem = 0);
 
 // Host copy of the device-side FastDiv.
 struct FastDivHost {
