@@ -690,9 +690,6 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
-    pdl_next();
-    fill_steps(a.rope, s_step, threadIdx.x, N);
-    __syncthreads();
     // the warp's rows are `rows` heads of each of its tokens
     const int ltok = MANY ? ltokens : 0, lhp = 5 - lg - ltok, rows = 1 << lhp;
     const int hsub = MANY ? at.sub & (rows - 1) : at.sub, tsub = MANY ? at.sub >> lhp : 0;
@@ -750,8 +747,11 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
         }
         cp_async_commit();
     };
+    pdl_next();
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
+    fill_steps(a.rope, s_step, threadIdx.x, N);
+    __syncthreads();
 
     LaneMap<VE> map;
     T* py = nullptr;
@@ -941,9 +941,6 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ 
     const int ctas = which ? int(gridDim.x) - plan.nq : plan.nq;
     const int lg = plan.lg, lchunk = plan.lchunk, ltok = MANY ? plan.ltok[which] : 0;
     const LaneAt<VE, ADJ> at(lane, lg, a.d, a.rope);
-    pdl_next();
-    fill_steps(a.rope, s_step, threadIdx.x, N);
-    __syncthreads();
     const int heads = a.heads[which], mask = (1 << lchunk) - 1;
     // the warp's rows are 2^lhp heads of each of its tokens
     const int lhp = 5 - lg - ltok;
@@ -959,11 +956,6 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ 
     for (int i = 0; i < H; ++i) {
         w0[i] = w1[i] = f2(1.f);
         acc0[i] = acc1[i] = f2(0.f);
-    }
-    if (at.on && a.w[which]) {
-        const T* w = reinterpret_cast<const T*>(a.w[which]);
-        pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
-                                ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
     }
     // lanes past the row copy nothing, and read zeros
     if (!at.on)
@@ -1018,8 +1010,16 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ 
         }
         cp_async_commit();
     };
+    pdl_next();
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
+    if (at.on && a.w[which]) {
+        const T* w = reinterpret_cast<const T*>(a.w[which]);
+        pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
+    }
+    fill_steps(a.rope, s_step, threadIdx.x, N);
+    __syncthreads();
 
     LaneTurns<VE> tn;
     for (int stage = 0; un < units; stage = stage + 1 == D ? 0 : stage + 1) {
