@@ -29,6 +29,29 @@ __device__ __forceinline__ void pdl_next() {
     pdl_trigger();
 }
 
+// Work in waves: as many CTAs as are resident at once, each warp taking `rounds`
+// units that lie a wave's warps apart, then the next wave's CTAs.  CTAs that stay
+// for all of a large problem drift apart, and what the GPU touches at one time
+// spreads over more and more of memory: the rotation of 400 MB, bf16, 12 + 12 heads
+// of 128, takes 140 us that way, 117 in waves of four or six rounds (118 at the copy
+// rate), 121 of eight and 127 of ten.  Where instructions bound (the norm of heads
+// of 64), a new wave's start costs 1 to 2% at six rounds, 4% at four.
+constexpr int kWaveRounds = 6;  // at most
+struct Waves {
+    int ctas, rounds;  // of a wave
+};
+template <int WARPS>
+struct WaveUnits {
+    int64_t first, end, stride;  // of this warp
+    __device__ __forceinline__ WaveUnits(const Waves& w, int64_t units, int warp) {
+        const int wave = int(blockIdx.x) < w.ctas ? 0 : int(blockIdx.x) / w.ctas;
+        stride = int64_t(w.ctas) * WARPS;
+        first = wave * w.rounds * stride;
+        end = min(units, first + w.rounds * stride);
+        first += (int(blockIdx.x) - wave * w.ctas) * WARPS + warp;
+    }
+};
+
 // ---------------------------------------------------------------------------
 // angles
 // ---------------------------------------------------------------------------
@@ -523,20 +546,25 @@ struct LaneMap {
         }
     }
     // (`turns`: elements past the rotated part are their own, whatever their partner holds)
-    __device__ __forceinline__ void apply(float2 (&u)[VE / 2], float2 (&v)[VE / 2], bool turns) const {
+    template <int R>
+    __device__ __forceinline__ void apply(float2 (&u)[R][VE / 2], float2 (&v)[R][VE / 2], bool turns) const {
         if (turns) {
 #pragma unroll
-            for (int i = 0; i < VE / 2; ++i) {
-                const float2 a = __ffma2_rn(v[i], uv[i], __fmul2_rn(u[i], uu[i]));
-                v[i] = __ffma2_rn(u[i], vu[i], __fmul2_rn(v[i], vv[i]));
-                u[i] = a;
-            }
+            for (int i = 0; i < VE / 2; ++i)
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const float2 a = __ffma2_rn(v[k][i], uv[i], __fmul2_rn(u[k][i], uu[i]));
+                    v[k][i] = __ffma2_rn(u[k][i], vu[i], __fmul2_rn(v[k][i], vv[i]));
+                    u[k][i] = a;
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < VE / 2; ++i) {
-                u[i] = __fmul2_rn(u[i], uu[i]);
-                v[i] = __fmul2_rn(v[i], vv[i]);
-            }
+            for (int i = 0; i < VE / 2; ++i)
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    u[k][i] = __fmul2_rn(u[k][i], uu[i]);
+                    v[k][i] = __fmul2_rn(v[k][i], vv[i]);
+                }
         }
     }
 };
@@ -655,18 +683,19 @@ private:
 //
 // Bound by bytes (a row is read and written once), and close behind by issue
 // slots: with the row arithmetic left out the kernel's copies alone take 50 us of
-// its 56 at bf16 16384 tokens of 32 + 8 heads of 128 (338 MB, 50 us at the copy
-// rate of 6.8 TB/s; 6.0 TB/s reached).  What was measured there, in us:
+// its 53 at bf16 16384 tokens of 32 + 8 heads of 128 (338 MB, 50 us at the copy
+// rate of 6.8 TB/s; 6.3 TB/s reached).  What was measured there, in us:
 //   one row a warp, scalar 259; vectors, a lane's rows loaded as they are needed 85;
 //   fp32 pairs and uniform steps 69; copies ahead, one row a step 72 (the rotation
 //   of 32760 tokens 77 -> 64); two rows a step 58; weights and angles in one map,
 //   57, with 40 registers fewer; the turns per position in shared memory and three
-//   stages 56.
-// Three CTAs of four warps at up to 168 registers.  Four CTAs (128 registers) take
-// 61 here, 65 against 65 for the rotation of 32760 tokens and 42 against 41 for a
-// serving chunk, but 28.6 against 30.4 for heads of 64; two CTAs of eight warps 57,
-// and 44 for the chunk.  A fourth stage costs 57 here and gives the rotation 64.
-// Steps of four rows, two at a time, took as many instructions and 57 to 58.
+//   stages 56; work in waves, weights in shared memory and the norm a template
+//   parameter 53 (the rotation of video tokens 66 -> 61, of 25216 image tokens of 12
+//   + 12 heads of 64 30 -> 26.5, at 116 registers in four CTAs an SM).
+// Three CTAs of four warps an SM at up to 168 registers (the rotation alone needs
+// fewer, and four fit).  Before the waves, the norm took 61 in four CTAs of 128
+// registers and 57 in two of eight warps; a serving chunk 42 and 44 against 41.  A
+// fourth stage 55; steps of four rows, two at a time, 57 to 58.
 constexpr int kHeadRows = 2;      // rows of a lane in a step
 constexpr int kHeadFwdWarps = 4;  // warps of a CTA
 constexpr int kHeadFwdStages = 3;
@@ -676,9 +705,9 @@ constexpr size_t head_fwd_smem() {
     return size_t(kHeadFwdStages) * 2 * kHeadRows * kHeadFwdWarps * 32 * VE * sizeof(T);
 }
 
-template <typename T, int VE, bool ADJ, bool CACHE, bool MANY>
+template <typename T, int VE, bool ADJ, bool CACHE, bool MANY, bool norm>
 __global__ void __launch_bounds__(kHeadFwdWarps * 32, 3)
-head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int lchunk, int norm) {
+head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int lchunk, Waves waves) {
     constexpr int H = VE / 2, D = kHeadFwdStages, R = kHeadRows, N = kHeadFwdWarps * 32, BYTES = VE * int(sizeof(T));
     extern __shared__ __align__(16) unsigned char dyn[];
     // (a warp's rows hold 32 * VE pairs, so its tokens have no more)
@@ -686,6 +715,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
     __shared__ __align__(16) float s_sin[kHeadFwdWarps][MANY ? 32 * VE : kHeadMaxPairs];
     __shared__ TokenWords s_tok[kHeadFwdWarps][D][MANY ? 32 : 1];
     __shared__ uint64_t s_step[kHeadMaxPairs];
+    __shared__ Raw<T, VE> s_w[2][norm ? kHeadMaxD / VE : 1];  // the weights
     __shared__ uint32_t s_max[CACHE ? kHeadFwdWarps : 1][CACHE ? 64 : 1];
     Raw<T, VE>* ring = reinterpret_cast<Raw<T, VE>*>(dyn) + threadIdx.x;  // [stage][row][vector], N apart
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
@@ -713,9 +743,10 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
     in.lper = lhp + (R == 2 ? 1 : 0);
     in.lchunk = lchunk;
     in.ltok = ltok;
-    in.units = (a.tokens + (1 << ltok) - 1) >> ltok << lchunk;
-    in.stride = int64_t(gridDim.x) * kHeadFwdWarps;
-    in.start(a, int64_t(blockIdx.x) * kHeadFwdWarps + warp);
+    const WaveUnits<kHeadFwdWarps> own(waves, (a.tokens + (1 << ltok) - 1) >> ltok << lchunk, warp);
+    in.units = own.end;
+    in.stride = own.stride;
+    in.start(a, own.first);
     StepWalk<CACHE ? 3 : 2, MANY> cur = in;
 
     const T* px = nullptr;  // this lane's first vector of the step to copy
@@ -751,8 +782,20 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
     fill_steps(a.rope, s_step, threadIdx.x, N);
+    if (norm) {
+        float2 ones[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) ones[i] = f2(1.f);
+        for (int i = threadIdx.x; i < 2 * kHeadMaxD / VE; i += N) {
+            const int which = i / (kHeadMaxD / VE), e = i % (kHeadMaxD / VE) * VE;
+            const T* w = reinterpret_cast<const T*>(a.w[which]);
+            s_w[which][e / VE] =
+                w && e < a.d ? ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + e)) : raw_pack<T, VE>(ones);
+        }
+    }
     __syncthreads();
 
+    const int w0 = at.on ? at.b0 / VE : 0, w1 = at.on ? at.b1 / VE : 0;
     LaneMap<VE> map;
     T* py = nullptr;
     float* pr = nullptr;
@@ -786,12 +829,12 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
             out = v.p && at.on && (!MANY || t < a.tokens);
             if (norm) pr = at.j == 0 && (!MANY || t < a.tokens) && a.rstd[which] ? a.rstd[which] + t * heads + h : nullptr;
             if (norm || cur.fresh) {  // (without weights q and k share the map)
+                if (norm) {
+                    pair_unpack<T, VE, ADJ>(s_w[which][w0], s_w[which][w1], map.uu, map.vv);
+                } else {
 #pragma unroll
-                for (int i = 0; i < H; ++i) map.uu[i] = map.vv[i] = f2(1.f);
-                const T* w = reinterpret_cast<const T*>(a.w[which]);
-                if (w && at.on)
-                    pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
-                                            ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), map.uu, map.vv);
+                    for (int i = 0; i < H; ++i) map.uu[i] = map.vv[i] = f2(1.f);
+                }
                 const int p = (MANY ? tsub * (a.rope.rot >> 1) : 0) + VE * at.j;
                 if (at.turns) map.turned(&s_cos[warp][p], &s_sin[warp][p]);
             }
@@ -817,14 +860,15 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
                 for (int k = 0; k < R; ++k)
                     if (pr && h + k * rows < heads) pr[k * rows] = r[k];
             }
+            map.apply(u, v, at.turns);
+            if (norm) {
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                map.apply(u[k], v[k], at.turns);
+                for (int i = 0; i < H; ++i)
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    u[k][i] = __fmul2_rn(u[k][i], f2(r[k]));
-                    v[k][i] = __fmul2_rn(v[k][i], f2(r[k]));
-                }
+                    for (int k = 0; k < R; ++k) {
+                        u[k][i] = __fmul2_rn(u[k][i], f2(r[k]));
+                        v[k][i] = __fmul2_rn(v[k][i], f2(r[k]));
+                    }
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
@@ -1131,12 +1175,12 @@ __device__ __forceinline__ void ld_row_wide(const void* p, uint4 (&r)[2]) {
 // Bound by issue slots (about 240 instructions for four rows of 128: magnitudes,
 // a scale, four packed operations a pair of elements for codes that round like
 // the real quotient) and by bytes: 131072 tokens of 8 + 8 heads of 128, bf16 to
-// four bits in groups of 32, 713 MB, 105 us at the copy rate, 131 measured (5.4
-// TB/s).  One vector a lane, or two that are not neighbours, 160 to 215; copies
+// four bits in groups of 32, 713 MB, 105 us at the copy rate, 123 measured (5.8
+// TB/s; CTAs that stay 129).  One vector a lane, or two that are not neighbours, 160 to 215; copies
 // ahead as in the forward 186 (more instructions); the form at run time 141.
 template <typename T, int VE, int NV, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32)
-cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
+cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves waves) {
     constexpr int E = NV * VE;  // elements of a lane
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
@@ -1149,19 +1193,19 @@ cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     const int gi = j * E / group;
     const bool leads = j * E == gi * group;
     const int ltok = 5 - cl.lg - cl.lhp;  // tokens of a warp
-    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, stride = int64_t(gridDim.x) * kHeadWarps;
+    const WaveUnits<kHeadWarps> own(waves, (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, warp);
     // neither a token's slot nor its rows wait for one another: the slot was asked for a unit ago
     auto ask = [&](int64_t un) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
-        return un < units && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
+        return un < own.end && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
     };
-    int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp;
+    int64_t un = own.first;
     pdl_next();
     int64_t asked = ask(un);
-    for (; un < units; un += stride) {
+    for (; un < own.end; un += own.stride) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
         const int64_t slot = cache_slot(a.cache, asked, a.err);
-        asked = ask(un + stride);
+        asked = ask(un + own.stride);
         const bool live = t < a.tokens && on;
         int h0 = (int(un) & ((1 << cl.lchunk) - 1)) << cl.lhp;
         const CacheRow cr = cache_row(a.cache, slot < 0 ? 0 : slot, h0 + hsub);
@@ -1274,13 +1318,13 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
 }
 
 // Reading: bound by bytes, 713 MB for the same 131072 tokens, 105 us at the copy
-// rate, 115 measured (6.2 TB/s).  A lane's two vectors are here those at j and j +
+// rate, 111 measured (6.4 TB/s; CTAs that stay 114).  A lane's two vectors are here those at j and j +
 // per: each store of a warp then covers whole lines (two neighbouring vectors a
 // lane, stored 32 bytes at once, took 122 against 116).  Five CTAs an SM; four and
 // six 113 and 125 here, 11.4 and 12.1 against 10.7 for 15250 tokens of 4 heads.
 template <typename T, int VE, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32, 5)
-cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
+cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves waves) {
     constexpr int NV = 2;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0);
     const int sub = lane >> cl.lg, j = lane & ((1 << cl.lg) - 1), hp = 1 << cl.lhp, hsub = sub & (hp - 1);
@@ -1292,18 +1336,18 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl) {
     int gi[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) gi[v] = (j + v * cl.per) * VE / a.cache.group;
-    const int64_t units = (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, stride = int64_t(gridDim.x) * kHeadWarps;
+    const WaveUnits<kHeadWarps> own(waves, (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, warp);
     auto ask = [&](int64_t un) {  // a token's slot, asked for a unit ahead
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
-        return un < units && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
+        return un < own.end && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
     };
-    int64_t un = int64_t(blockIdx.x) * kHeadWarps + warp;
+    int64_t un = own.first;
     pdl_next();
     int64_t asked = ask(un);
-    for (; un < units; un += stride) {
+    for (; un < own.end; un += own.stride) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
         const int64_t slot = cache_slot(a.cache, asked, a.err);
-        asked = ask(un + stride);
+        asked = ask(un + own.stride);
         if (slot < 0 || !on) continue;
         int h = ((int(un) & ((1 << cl.lchunk) - 1)) << cl.lhp) + hsub;
         const CacheRow cr = cache_row(a.cache, slot, h);
@@ -1704,6 +1748,16 @@ inline int head_chunks_log2(int64_t tokens, int steps, int warps, const DevInfo&
     return lc;
 }
 
+// The grid for `work` CTAs' worth of single units, of which `resident` run at once.
+inline int64_t make_waves(int64_t work, int64_t resident, Waves* w) {
+    w->ctas = int(std::min(work, resident));
+    const int64_t all = (work + w->ctas - 1) / w->ctas;  // rounds
+    const int64_t waves = std::min((all + kWaveRounds - 1) / kWaveRounds, int64_t(1) << 16);
+    w->rounds = int((all + waves - 1) / waves);
+    const int64_t full = work / (int64_t(w->ctas) * w->rounds);
+    return full * w->ctas + std::min(work - full * w->ctas * w->rounds, int64_t(w->ctas));
+}
+
 // Tokens (as a power of two) that share a warp's rows where a token's `heads` heads
 // leave some of the 32 >> lg free, and tokens are many enough to fill the SMs so
 // (f16, 21209 tokens of 1 + 1 heads of 64: 31 us with a token a warp).
@@ -1713,21 +1767,24 @@ inline int head_tokens_log2(int64_t tokens, int heads, int lg, const DevInfo& d)
     return lt;
 }
 
-// f of three conditions as constants.
+// f of the conditions as constants.
 template <typename F>
-const void* pick3(bool a, bool b, bool c, F&& f) {
-    auto third = [&](auto x, auto y) { return c ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
-    auto second = [&](auto x) { return b ? third(x, std::true_type{}) : third(x, std::false_type{}); };
-    return a ? second(std::true_type{}) : second(std::false_type{});
+const void* pick(F&& f) {
+    return f();
+}
+template <typename F, typename... More>
+const void* pick(F&& f, bool first, More... more) {
+    return first ? pick([&](auto... rest) { return f(std::true_type{}, rest...); }, more...)
+                 : pick([&](auto... rest) { return f(std::false_type{}, rest...); }, more...);
 }
 
 template <typename T, int VE>
 nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo& d, cudaStream_t s) {
     int lg = row_lanes_log2(a.d / (2 * VE));
     int lt = head_tokens_log2(a.tokens, (std::max(a.heads[0], a.heads[1]) + kHeadRows - 1) / kHeadRows, lg, d);
-    const void* fn = pick3(a.rope.adjacent, cache, lt > 0, [](auto adj, auto with_cache, auto many) {
-        return (const void*)&head_fwd_vec_kernel<T, VE, adj.value, with_cache.value, many.value>;
-    });
+    const void* fn = pick([](auto adj, auto with_cache, auto many, auto with_norm) {
+        return (const void*)&head_fwd_vec_kernel<T, VE, adj.value, with_cache.value, many.value, with_norm.value>;
+    }, bool(a.rope.adjacent), cache, lt > 0, norm);
     const size_t smem = head_fwd_smem<T, VE>();
     if (nrm_status st = prepare_kernel(fn, smem, false); st != NRM_OK) return st;
     const int occ = cached_occupancy(fn, kHeadFwdWarps * 32, smem);
@@ -1737,11 +1794,10 @@ nrm_status head_fwd_vec(const HeadArgs& a, bool norm, bool cache, const DevInfo&
     for (int i = 0; i < (cache ? 3 : 2); ++i) steps += (a.heads[i] + per - 1) / per;
     const int64_t blocks = (a.tokens + (1 << lt) - 1) >> lt;
     int lc = head_chunks_log2(blocks, steps, 16, d);
-    int64_t ctas = ((blocks << lc) + kHeadFwdWarps - 1) / kHeadFwdWarps;
-    if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
+    Waves waves{};
+    const int64_t ctas = make_waves(((blocks << lc) + kHeadFwdWarps - 1) / kHeadFwdWarps, int64_t(occ) * d.sms, &waves);
     HeadArgs args = a;
-    int with_norm = norm;
-    void* kargs[] = {&args, &lg, &lt, &lc, &with_norm};
+    void* kargs[] = {&args, &lg, &lt, &lc, &waves};
     return launch_pdl(fn, dim3(unsigned(ctas)), dim3(kHeadFwdWarps * 32), kargs, s, smem);
 }
 
@@ -1819,9 +1875,9 @@ nrm_status head_bwd(const HeadArgs& a, int vec, cudaStream_t s) {
     size_t smem = 0;
     auto take = [&](auto ve) {
         constexpr int VE = decltype(ve)::value;
-        fn = pick3(a.rope.adjacent, plan.ltok[0] > 0 || plan.ltok[1] > 0, false, [](auto adj, auto many, auto) {
+        fn = pick([](auto adj, auto many) {
             return (const void*)&head_bwd_vec_kernel<T, VE, adj.value, many.value>;
-        });
+        }, bool(a.rope.adjacent), plan.ltok[0] > 0 || plan.ltok[1] > 0);
         smem = head_bwd_smem<T, VE>();
     };
     if (vec == 16) take(std::integral_constant<int, 16 / int(sizeof(T))>{});
@@ -1884,10 +1940,10 @@ inline nrm_status cache_launch_vec(const HeadArgs& a, const void* fn, int lanes,
     const int ltok = 5 - cl.lg - cl.lhp;
     const int64_t blocks = (a.tokens + (1 << ltok) - 1) >> ltok;
     cl.lchunk = head_chunks_log2(blocks, (a.heads[1] + (1 << cl.lhp) - 1) >> cl.lhp, 16, d);
-    int64_t ctas = ((blocks << cl.lchunk) + kHeadWarps - 1) / kHeadWarps;
-    if (ctas > int64_t(occ) * d.sms) ctas = int64_t(occ) * d.sms;
+    Waves waves{};
+    const int64_t ctas = make_waves(((blocks << cl.lchunk) + kHeadWarps - 1) / kHeadWarps, int64_t(occ) * d.sms, &waves);
     HeadArgs args = a;
-    void* kargs[] = {&args, &cl};
+    void* kargs[] = {&args, &cl, &waves};
     return launch_pdl(fn, dim3(unsigned(ctas)), dim3(kHeadWarps * 32), kargs, s);
 }
 
