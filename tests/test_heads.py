@@ -841,3 +841,53 @@ def test_a_first_call_may_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_a_long_call_equals_its_pieces(norm):
+    # more tokens than the GPU holds at once several times over, against calls that it holds: a row's
+    # result does not depend on the call that it is part of, so the bits are the same
+    tokens, hq, hk, d, piece = 70_001, 12, 4, 64, 4_999
+    g = torch.Generator(device="cuda").manual_seed(5)
+    qkv = torch.randn(tokens, hq + 2 * hk, d, device="cuda", generator=g).bfloat16()
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+    wq, wk = (torch.randn(d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    pos = torch.randint(0, 1 << 40, (tokens,), device="cuda", generator=g)
+    inv = 0.5 ** torch.arange(d // 2, device="cuda").float()
+    slots = torch.randperm(16 * 4400, device="cuda", generator=g)[:tokens]
+
+    def run(step):
+        out = {"q": torch.zeros(tokens, hq, d, device="cuda", dtype=torch.bfloat16)}
+        for n in ("k", "k_fused", "k_back", "v_back"):
+            out[n] = torch.zeros(tokens, hk, d, device="cuda", dtype=torch.bfloat16)
+        out["q_fused"] = torch.zeros_like(out["q"])
+        codes = [torch.zeros(4400, 16, hk, d // 2, device="cuda", dtype=torch.uint8) for _ in range(4)]
+        scales = [torch.zeros(4400, 16, hk, 2, device="cuda") for _ in range(4)]
+        parts, fused = (nrm.kv_cache(codes[i], scales[i], codes[i + 1], scales[i + 1]) for i in (0, 2))
+        for t in range(0, tokens, step):
+            s = slice(t, t + step)
+            if norm:
+                nrm.nrm_qk_norm_rope_fwd(q[s], k[s], wq, wk, pos[s], inv, out["q"][s], out["k"][s], None, None, 1e-6)
+            else:
+                nrm.nrm_rope_fwd(q[s], k[s], pos[s], inv, out["q"][s], out["k"][s])
+            nrm.nrm_kv_cache_write(out["k"][s], v[s], parts, slots[s])
+            nrm.nrm_qk_norm_rope_cache(q[s], k[s], v[s], wq, wk, pos[s], inv, out["q_fused"][s], out["k_fused"][s], fused,
+                                       slots[s], 1e-6, norm=norm)
+            nrm.nrm_kv_cache_read(parts, slots[s], out["k_back"][s], out["v_back"][s])
+        nrm.nrm_sync_status()
+        out.update({f"codes{i}": c for i, c in enumerate(codes)})
+        out.update({f"scales{i}": c for i, c in enumerate(scales)})
+        return out
+
+    whole, pieces = run(tokens), run(piece)
+    for n, t in whole.items():
+        assert torch.equal(t, pieces[n]), n
+    assert torch.equal(whole["q"], whole["q_fused"]) and torch.equal(whole["k"], whole["k_fused"])
+    for i in range(2):
+        assert torch.equal(whole[f"codes{i}"], whole[f"codes{i + 2}"])
+        assert torch.equal(whole[f"scales{i}"], whole[f"scales{i + 2}"])
+    # and the last values: half a step of 4 bits off, then bf16's rounding (2^-8 of a value of at most 2 |x|)
+    x = v[-7:].double().cpu().numpy()
+    step = np.abs(x.reshape(7, hk, 2, 32)).max(-1, keepdims=True).repeat(32, -1).reshape(x.shape) / 7
+    got = whole["v_back"][-7:].double().cpu().numpy()
+    assert (np.abs(got - x) <= step * (0.5 + 1e-6) + np.abs(x) * 2.0 ** -7).all()
