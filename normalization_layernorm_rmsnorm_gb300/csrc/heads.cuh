@@ -948,9 +948,11 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
 // belong to one weight, CTAs take q or k; a token's angles are made twice for that.
 //
 // Bound by bytes: bf16 16384 tokens of 32 + 8 heads of 128, 506 MB, 75 us at the
-// copy rate, 79 measured (6.4 TB/s).  Loads as they were needed 109, copies three
-// steps ahead 84, two steps ahead 79, one 92 (all two CTAs of eight warps; CTAs of
-// four warps, three or four an SM, 81 and 80).
+// copy rate, 80 measured with the column sums (6.3 TB/s).  Loads as they were needed
+// 109, copies three steps ahead 84, two steps ahead 79 to 81, one 92 (all two CTAs of
+// eight warps; CTAs of four warps, three or four an SM, 81 and 80).  CTAs that stay:
+// two waves, as many as the partial rows allow, gain 6% at 400 MB of inputs and lose
+// 2 to 8% between 60 and 100 MB.
 //
 // A lane's copies of a step: two vectors each of dy and x, and the row's r.
 template <typename T, int VE>
@@ -1668,7 +1670,7 @@ head_dw_kernel(const float* __restrict__ ws, int d, int nq, int nk, T* dwq, T* d
 #pragma unroll 8
         for (int w = 0; w < kHeadSumWarps; ++w) {
             tot.add(part[w][0][lane]);
-            tot.add(part[w][1][lane]);
+            tot.c += part[w][1][lane];
         }
         st_elem<T>(out, col, tot.s + tot.c);
     }
