@@ -843,26 +843,27 @@ def test_a_first_call_may_be_captured():
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
 
 
-@pytest.mark.parametrize("norm", [True, False])
-def test_a_long_call_equals_its_pieces(norm):
+@pytest.mark.parametrize("norm,tokens,hq,hk,piece", [
+    (True, 70_001, 12, 4, 4_999), (False, 70_001, 12, 4, 4_999), (True, 200_003, 1, 1, 30_011)])
+def test_a_long_call_equals_its_pieces(norm, tokens, hq, hk, piece):
     # more tokens than the GPU holds at once several times over, against calls that it holds: a row's
     # result does not depend on the call that it is part of, so the bits are the same
-    tokens, hq, hk, d, piece = 70_001, 12, 4, 64, 4_999
+    d, pages = 64, tokens // 16 + 7
     g = torch.Generator(device="cuda").manual_seed(5)
     qkv = torch.randn(tokens, hq + 2 * hk, d, device="cuda", generator=g).bfloat16()
     q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
     wq, wk = (torch.randn(d, device="cuda", generator=g).bfloat16() for _ in range(2))
     pos = torch.randint(0, 1 << 40, (tokens,), device="cuda", generator=g)
     inv = 0.5 ** torch.arange(d // 2, device="cuda").float()
-    slots = torch.randperm(16 * 4400, device="cuda", generator=g)[:tokens]
+    slots = torch.randperm(16 * pages, device="cuda", generator=g)[:tokens]
 
     def run(step):
         out = {"q": torch.zeros(tokens, hq, d, device="cuda", dtype=torch.bfloat16)}
         for n in ("k", "k_fused", "k_back", "v_back"):
             out[n] = torch.zeros(tokens, hk, d, device="cuda", dtype=torch.bfloat16)
         out["q_fused"] = torch.zeros_like(out["q"])
-        codes = [torch.zeros(4400, 16, hk, d // 2, device="cuda", dtype=torch.uint8) for _ in range(4)]
-        scales = [torch.zeros(4400, 16, hk, 2, device="cuda") for _ in range(4)]
+        codes = [torch.zeros(pages, 16, hk, d // 2, device="cuda", dtype=torch.uint8) for _ in range(4)]
+        scales = [torch.zeros(pages, 16, hk, 2, device="cuda") for _ in range(4)]
         parts, fused = (nrm.kv_cache(codes[i], scales[i], codes[i + 1], scales[i + 1]) for i in (0, 2))
         for t in range(0, tokens, step):
             s = slice(t, t + step)
