@@ -892,3 +892,73 @@ def test_a_long_call_equals_its_pieces(norm, tokens, hq, hk, piece):
     step = np.abs(x.reshape(7, hk, 2, 32)).max(-1, keepdims=True).repeat(32, -1).reshape(x.shape) / 7
     got = whole["v_back"][-7:].double().cpu().numpy()
     assert (np.abs(got - x) <= step * (0.5 + 1e-6) + np.abs(x) * 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_follow_other_streams_copies_and_kernels(captured):
+    # each call is launched while its predecessor runs: what it waits for may be a copy, a fill, another
+    # stream's kernel, or two of them at once, and what follows it on another stream waits for it
+    tokens, heads, d = 3000, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(9)
+    inv = 0.9 ** torch.arange(d // 2, device="cuda").float()
+    pos = torch.arange(tokens, device="cuda")
+    w = torch.randn(d, device="cuda", generator=g).bfloat16()
+    src = [torch.empty(tokens, heads, d, device="cuda", dtype=torch.bfloat16) for _ in range(3)]
+    q, k, v, qo, ko, kb, vb, doubled = (torch.empty_like(src[0]) for _ in range(8))
+    slots = torch.empty(tokens, dtype=torch.int64, device="cuda")
+    order = torch.empty_like(slots)
+    codes = [torch.zeros(tokens // 8, 8, heads, d, device="cuda", dtype=torch.int8) for _ in range(2)]
+    scales = [torch.zeros(tokens // 8, 8, heads, 1, device="cuda") for _ in range(2)]
+    cache = nrm.kv_cache(codes[0], scales[0], codes[1], scales[1])
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        q.copy_(src[0])
+        two.wait_stream(one)
+        with torch.cuda.stream(two):
+            k.copy_(src[1])
+            k.mul_(2)
+            v.copy_(src[2])
+        q.mul_(2)
+        one.wait_stream(two)
+        nrm.nrm_qk_norm_rope_fwd(q, k, w, w, pos, inv, qo, ko, None, None, 1e-6)
+        two.wait_stream(one)
+        with torch.cuda.stream(two):
+            torch.mul(ko, 2, out=doubled)
+        slots.copy_(order)
+        nrm.nrm_kv_cache_write(ko, v, cache, slots)
+        kb.zero_()
+        vb.zero_()
+        nrm.nrm_kv_cache_read(cache, slots, kb, vb)
+        one.wait_stream(two)
+
+    torch.cuda.synchronize()
+    if captured:
+        for t in (*src, slots, order):
+            t.zero_()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=one):
+            work()
+    for i in range(20):
+        for t in src:
+            t.copy_(torch.randn(t.shape, device="cuda", generator=g).bfloat16())
+        order.copy_(torch.randperm(tokens, device="cuda", generator=g))
+        torch.cuda.synchronize()
+        if captured:
+            graph.replay()
+        else:
+            with torch.cuda.stream(one):
+                work()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (qo, ko, doubled, kb, vb)]
+        q2, k2 = 2 * src[0], 2 * src[1]
+        nrm.nrm_qk_norm_rope_fwd(q2, k2, w, w, pos, inv, qo, ko, None, None, 1e-6)
+        torch.cuda.synchronize()
+        nrm.nrm_kv_cache_write(ko, src[2], cache, order)
+        torch.cuda.synchronize()
+        nrm.nrm_kv_cache_read(cache, order, kb, vb)
+        torch.cuda.synchronize()
+        for a, b in zip(got, (qo, ko, 2 * ko, kb, vb)):
+            assert torch.equal(a, b), i
+    nrm.nrm_sync_status()
