@@ -646,9 +646,10 @@ struct StepWalk {
         settle(a);
     }
     __device__ __forceinline__ bool live() const { return un < units; }
-    __device__ __forceinline__ int64_t token() const { return MANY ? un >> lchunk << ltok : un >> lchunk; }  // the unit's first
+    // The unit's first token.
+    __device__ __forceinline__ int64_t token() const { return MANY ? un >> lchunk << ltok : un >> lchunk; }
     __device__ __forceinline__ int head_step() const { return 1 << (lper + lchunk); }
-    // Moves to the next step: false where only the head moved, within the tensor.
+    // Moves to the next step; `turned` stays false where only the head moved, within the tensor.
     __device__ __forceinline__ void next(const HeadArgs& a) {
         h0 += head_step();
         fresh = turned = false;
