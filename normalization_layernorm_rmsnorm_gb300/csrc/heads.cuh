@@ -29,6 +29,33 @@ __device__ __forceinline__ void pdl_next() {
     pdl_trigger();
 }
 
+// A load of what the predecessor may have written: weights, frequencies, positions,
+// slots, codes, scales.  The read-only path (__ldg, const __restrict__) wants memory
+// that nobody writes while the kernel lives, and here the predecessor still does;
+// the compiler may also move such loads to before the wait.  It was no faster:
+// a read of 131072 tokens from 4 bits takes 110 us either way.
+template <typename R>
+__device__ __forceinline__ R ld_after(const R* p) {
+    R r;
+    if constexpr (sizeof(R) == 1) {
+        uint32_t v;
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+        r = R(v);
+    } else if constexpr (sizeof(R) == 2) {
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(*reinterpret_cast<uint16_t*>(&r)) : "l"(p) : "memory");
+    } else if constexpr (sizeof(R) == 4) {
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(*reinterpret_cast<uint32_t*>(&r)) : "l"(p) : "memory");
+    } else if constexpr (std::is_integral_v<R>) {
+        asm volatile("ld.global.u64 %0, [%1];" : "=l"(r) : "l"(p) : "memory");
+    } else if constexpr (sizeof(R) == 8) {
+        asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
+    } else {
+        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    }
+    return r;
+}
+
 // Work in waves: as many CTAs as are resident at once, each warp taking `rounds`
 // units that lie a wave's warps apart, then the next wave's CTAs.  CTAs that stay
 // for all of a large problem drift apart, and what the GPU touches at one time
@@ -254,14 +281,7 @@ template <> struct RawBits<8> { using type = uint2; };
 template <> struct RawBits<4> { using type = uint1; };
 template <typename T, int VE> using Raw = typename RawBits<VE * int(sizeof(T))>::type;
 
-template <typename R>
-__device__ __forceinline__ R ld_ro(const R* p) {
-    if constexpr (sizeof(R) == 4) return make_uint1(__ldg(reinterpret_cast<const uint32_t*>(p)));
-    else return __ldg(p);
-}
-
-// Loads of rows that this kernel may write in place: not through the read-only
-// path, and not kept in L1.
+// Loads of rows, which this kernel may write in place: not kept in L1.
 __device__ __forceinline__ void ld_row(const void* p, uint4& r) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
@@ -477,7 +497,7 @@ struct LaneAt {
 // threads; the caller's barrier makes them visible.
 __device__ __forceinline__ void fill_steps(const RopeDev& r, uint64_t* steps, int tid, int threads) {
     for (int p = tid; 2 * p < r.rot; p += threads)
-        steps[p] = (turn_step(__ldg(r.inv_freq + p)) & ~uint64_t(3)) | uint64_t(pair_axis(r, p));
+        steps[p] = (turn_step(ld_after(r.inv_freq + p)) & ~uint64_t(3)) | uint64_t(pair_axis(r, p));
 }
 // What a warp copies for the tokens of a unit: positions (one an axis), cache slot.
 constexpr int kTokenSlot = kHeadMaxAxes;
@@ -791,7 +811,7 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
             const int which = i / (kHeadMaxD / VE), e = i % (kHeadMaxD / VE) * VE;
             const T* w = reinterpret_cast<const T*>(a.w[which]);
             s_w[which][e / VE] =
-                w && e < a.d ? ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + e)) : raw_pack<T, VE>(ones);
+                w && e < a.d ? ld_after(reinterpret_cast<const Raw<T, VE>*>(w + e)) : raw_pack<T, VE>(ones);
         }
     }
     __syncthreads();
@@ -1062,8 +1082,8 @@ head_bwd_vec_kernel(const __grid_constant__ HeadArgs a, const __grid_constant__ 
     for (int i = 0; i < D - 1; ++i) issue(i);
     if (at.on && a.w[which]) {
         const T* w = reinterpret_cast<const T*>(a.w[which]);
-        pair_unpack<T, VE, ADJ>(ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
-                                ld_ro(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
+        pair_unpack<T, VE, ADJ>(ld_after(reinterpret_cast<const Raw<T, VE>*>(w + at.b0)),
+                                ld_after(reinterpret_cast<const Raw<T, VE>*>(w + at.b1)), w0, w1);
     }
     fill_steps(a.rope, s_step, threadIdx.x, N);
     __syncthreads();
@@ -1200,7 +1220,7 @@ cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves 
     // neither a token's slot nor its rows wait for one another: the slot was asked for a unit ago
     auto ask = [&](int64_t un) {
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
-        return un < own.end && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
+        return un < own.end && t < a.tokens ? ld_after(a.slots + t) : int64_t(-1);
     };
     int64_t un = own.first;
     pdl_next();
@@ -1277,13 +1297,13 @@ template <int VE>
 __device__ __forceinline__ uint2 load_codes(const uint8_t* at, int kind) {
     uint2 w{0u, 0u};
     if (kind == NRM_CACHE_INT4) {
-        if constexpr (VE == 8) w.x = __ldg(reinterpret_cast<const uint32_t*>(at));
-        else if constexpr (VE == 4) w.x = __ldg(reinterpret_cast<const uint16_t*>(at));
-        else w.x = __ldg(at);
+        if constexpr (VE == 8) w.x = ld_after(reinterpret_cast<const uint32_t*>(at));
+        else if constexpr (VE == 4) w.x = ld_after(reinterpret_cast<const uint16_t*>(at));
+        else w.x = ld_after(at);
     } else {
-        if constexpr (VE == 8) w = __ldg(reinterpret_cast<const uint2*>(at));
-        else if constexpr (VE == 4) w.x = __ldg(reinterpret_cast<const uint32_t*>(at));
-        else w.x = __ldg(reinterpret_cast<const uint16_t*>(at));
+        if constexpr (VE == 8) w = ld_after(reinterpret_cast<const uint2*>(at));
+        else if constexpr (VE == 4) w.x = ld_after(reinterpret_cast<const uint32_t*>(at));
+        else w.x = ld_after(reinterpret_cast<const uint16_t*>(at));
     }
     return w;
 }
@@ -1342,7 +1362,7 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves w
     const WaveUnits<kHeadWarps> own(waves, (a.tokens + (1 << ltok) - 1) >> ltok << cl.lchunk, warp);
     auto ask = [&](int64_t un) {  // a token's slot, asked for a unit ahead
         const int64_t t = (un >> cl.lchunk << ltok) + (sub >> cl.lhp);
-        return un < own.end && t < a.tokens ? __ldg(a.slots + t) : int64_t(-1);
+        return un < own.end && t < a.tokens ? ld_after(a.slots + t) : int64_t(-1);
     };
     int64_t un = own.first;
     pdl_next();
@@ -1373,7 +1393,7 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves w
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         w[i][v] = load_codes<VE>(pc[i] + v * v_next, kind);
-                        sc[i][v] = __ldg(ps[i] + gi[v]);
+                        sc[i][v] = ld_after(ps[i] + gi[v]);
                     }
                 }
             }
@@ -1437,7 +1457,7 @@ struct SlotSteps {
         for (int s = 0; s < S; ++s) {
             step[s] = 0;
             if (2 * (lane + 32 * s) < r.rot) {
-                step[s] = turn_step(__ldg(r.inv_freq + lane + 32 * s));
+                step[s] = turn_step(ld_after(r.inv_freq + lane + 32 * s));
                 axis |= pair_axis(r, lane + 32 * s) << (2 * s);
             }
         }
@@ -1446,7 +1466,7 @@ struct SlotSteps {
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (2 * (lane + 32 * s) < r.rot)
-                cs[s] = pair_turn(r, step[s], __ldg(r.pos + (axis >> (2 * s) & 3) * r.pos_stride + t));
+                cs[s] = pair_turn(r, step[s], ld_after(r.pos + (axis >> (2 * s) & 3) * r.pos_stride + t));
     }
 };
 
@@ -1466,7 +1486,7 @@ head_fwd_scalar_kernel(const __grid_constant__ HeadArgs a, int norm) {
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         float2 cs[S];
         steps.make(a.rope, lane, t, cs);
-        const int64_t slot = CACHE ? cache_slot(a.cache, __ldg(a.slots + t), a.err) : -1;
+        const int64_t slot = CACHE ? cache_slot(a.cache, ld_after(a.slots + t), a.err) : -1;
         const int apart = int(gridDim.y) * kHeadWarps;  // heads of a warp
         for (int h0 = warp + int(blockIdx.y) * kHeadWarps; h0 < heads; h0 += apart * R) {
             int which[R], hd[R];
@@ -1648,7 +1668,7 @@ struct CarriedSum {
 };
 template <typename T>
 __global__ void __launch_bounds__(kHeadSumWarps * 32)
-head_dw_kernel(const float* __restrict__ ws, int d, int nq, int nk, T* dwq, T* dwk) {
+head_dw_kernel(const float* ws, int d, int nq, int nk, T* dwq, T* dwk) {
     pdl_next();
     const int which = blockIdx.y;
     T* out = which ? dwk : dwq;
@@ -1694,7 +1714,7 @@ cache_write_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads) {
     for (int64_t i = int64_t(blockIdx.x) * kHeadWarps + warp; i < rows; i += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = row_div(i, by_heads);
         const int h = int(i - t * heads);
-        const int64_t slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
+        const int64_t slot = cache_slot(a.cache, ld_after(a.slots + t), a.err);
         if (slot < 0) continue;
         const T* x = reinterpret_cast<const T*>(xv.p) + t * xv.ts + h * xv.hs;
         for (int e = lane; e < a.d; e += 32) row[e] = ld_elem<T>(x, e);
@@ -1716,7 +1736,7 @@ cache_read_scalar_kernel(const __grid_constant__ HeadArgs a, RowDiv by_heads) {
     for (int64_t i = int64_t(blockIdx.x) * kHeadWarps + warp; i < rows; i += int64_t(gridDim.x) * kHeadWarps) {
         const int64_t t = row_div(i, by_heads);
         const int h = int(i - t * heads);
-        const int64_t slot = cache_slot(a.cache, __ldg(a.slots + t), a.err);
+        const int64_t slot = cache_slot(a.cache, ld_after(a.slots + t), a.err);
         if (slot < 0) continue;
         const CacheRow at = cache_row(a.cache, slot, h);
         const uint8_t* codes = a.cache.codes[which] + at.code;
