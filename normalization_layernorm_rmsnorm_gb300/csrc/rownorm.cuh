@@ -503,13 +503,14 @@ struct NeumaierSum {
 
 // dw/db[col] = sum over the P partial rows, in a fixed order, rounded to T.
 // The partial rows can be much larger than their sum (dw of a column whose
-// per-row terms cancel), so the sum is compensated.
+// per-row terms cancel), so the sum is compensated.  (The partial rows are still
+// being written when this kernel is launched: no __restrict__, which would read
+// them through the read-only path.)
 constexpr int kColsumWarps = 32;  // partial rows are split over the warps: short dependent chains
 
 template <typename T>
 __global__ void __launch_bounds__(kColsumWarps * 32)
-row_colsum_kernel(const float* __restrict__ ws_dw, const float* __restrict__ ws_db, int P,
-                  int cols, T* dw, T* db) {
+row_colsum_kernel(const float* ws_dw, const float* ws_db, int P, int cols, T* dw, T* db) {
     pdl_wait();
     const float* ws = blockIdx.y == 0 ? ws_dw : ws_db;
     T* out = blockIdx.y == 0 ? dw : db;
@@ -543,8 +544,7 @@ constexpr int kColsumSerialMax = 64;
 constexpr int kColsumSerialBlock = 256;
 template <typename T>
 __global__ void __launch_bounds__(kColsumSerialBlock)
-row_colsum_serial_kernel(const float* __restrict__ ws_dw, const float* __restrict__ ws_db, int P, int cols, T* dw,
-                         T* db) {
+row_colsum_serial_kernel(const float* ws_dw, const float* ws_db, int P, int cols, T* dw, T* db) {
     pdl_wait();
     const float* ws = blockIdx.y == 0 ? ws_dw : ws_db;
     T* out = blockIdx.y == 0 ? dw : db;

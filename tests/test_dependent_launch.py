@@ -31,7 +31,7 @@ def kernels(text):
         yield text[m.start():start], text[start:i]
 
 
-@pytest.mark.parametrize("name", ["heads.cuh"])
+@pytest.mark.parametrize("name", ["heads.cuh", "rownorm.cuh"])
 def test_waiting_kernels_do_not_use_the_read_only_path(name):
     found = 0
     for signature, body in kernels(code(name)):
