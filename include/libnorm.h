@@ -436,7 +436,9 @@ typedef enum nrm_pairs {
  *   (u, v) -> (u*cos a - v*sin a, v*cos a + u*sin a)
  * and elements i >= rot pass unchanged.  The product is taken modulo one turn
  * in 64-bit fixed point, so far positions keep their angles: for frequencies up
- * to 2 pi it is off by less than |pos| * 2^-52 + 2^-32 turns.
+ * to 2 pi, the angle whose cosine and sine are taken is off by less than
+ * 2^-28 + 2^-32 + |pos| * 2^-61 turns (its float32 conversion, after whole
+ * quarter turns are taken off; the phase's 32 bits; the product).
  * pos: device int64 [axes][pos_stride >= tokens], any values.  inv_freq:
  * device float32 [rot/2], finite.  axis: HOST bytes [rot/2], each below axes,
  * read during the call; NULL when axes == 1.  rot even, 0 <= rot <= d; with

@@ -106,12 +106,19 @@ __device__ __forceinline__ int pair_axis(const RopeDev& r, int p) {
 }
 
 // cos and sin of a pair that turns by `step` per position, at position pos.  The
-// top 32 bits of the phase, read as signed, are the angle in 2^-31 half turns.
+// phase's top 32 bits, in 2^-32 turns, are taken off the nearest quarter turn before
+// they become a float32, which so is off by at most 2^-28 turns (of a whole half turn
+// it would be 2^-26: cosines off by 1.5 units in their last place more).  The quarter
+// turns then exchange and negate the two.
 __device__ __forceinline__ float2 pair_turn(const RopeDev& r, uint64_t step, int64_t pos) {
-    const uint64_t phase = uint64_t(pos) * step;
+    const uint32_t phase = uint32_t((uint64_t(pos) * step) >> 32);
+    const uint32_t quarters = (phase + 0x20000000u) >> 30;
     float s, c;
-    sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s, &c);
-    return make_float2(c, r.inverse ? -s : s);
+    sincospif(float(int32_t(phase - (quarters << 30))) * 0x1p-31f, &s, &c);
+    const float cos = quarters & 1u ? s : c, sin = quarters & 1u ? c : s;
+    const uint32_t neg_cos = (quarters + 1u) << 30, neg_sin = (quarters << 30) ^ (r.inverse ? 0x80000000u : 0u);
+    return make_float2(__uint_as_float(__float_as_uint(cos) ^ (neg_cos & 0x80000000u)),
+                       __uint_as_float(__float_as_uint(sin) ^ (neg_sin & 0x80000000u)));
 }
 
 // (u, v) turned by (cos, sin).
