@@ -1,5 +1,6 @@
 """Builds libnorm.so in-tree (``_build/``) with nvcc for sm_103a, and the Python
-extension that marshals the calls on attention heads (``_heads.so``) with g++.
+extension that marshals the calls on attention heads (``_heads.so``) with g++,
+where PyTorch's headers are (libnorm.so itself is plain C and needs none).
 
 Each translation unit is compiled in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  Rebuilds only what changed.
@@ -56,17 +57,30 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
-def _compile_binding() -> str:
+def _binding_includes() -> list[str] | None:
+    """Directories of the binding's headers; None where g++, PyTorch's headers (with
+    CUDA) or Python's are missing: then there is no binding to build."""
     import sysconfig
-
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+    for header in ("torch/csrc/autograd/python_variable.h", "c10/cuda/CUDAStream.h", "Python.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in dirs):
+            return None
+    return dirs if shutil.which("g++") else None
+
+
+def _compile_binding(includes: list[str]) -> str:
+    import torch
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "heads_binding.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
-           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
-           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "heads_binding.cpp"), "-o", obj]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *(x for d in [*includes, cuda] for x in ("-isystem", d)),
+           "-c", os.path.join(CSRC, "heads_binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for heads_binding.cpp:\n{r.stdout}\n{r.stderr}")
@@ -89,20 +103,25 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile every source, link libnorm.so and the binding; returns libnorm.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     dep = _deps_mtime()
-    made = [f for f in (LIB, HEADS) if os.path.exists(f) and os.path.getmtime(f) >= dep]
-    if not force and not verbose_ptxas and len(made) == 2:
-        return LIB
+
+    def stale(f):
+        return force or not os.path.exists(f) or os.path.getmtime(f) < dep
+
+    includes = _binding_includes()
+    lib, heads = verbose_ptxas or stale(LIB), includes is not None and stale(HEADS)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as pool:
-        binding = pool.submit(_compile_binding)
-        objs = list(pool.map(lambda s: _compile(s, extra), SOURCES))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding.result())
+        binding = pool.submit(_compile_binding, includes) if heads else None
+        objs = list(pool.map(lambda s: _compile(s, extra), SOURCES)) if lib else []
+    if lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB)
+    if binding:
+        _link_binding(binding.result())
     return LIB
 
 
