@@ -15,7 +15,6 @@ import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libnorm.so")
-HEADS_PATH = os.path.join(_PKG, "_build", "_heads.so")
 
 NRM_OK, NRM_ERR_INVALID_ARG, NRM_ERR_UNSUPPORTED, NRM_ERR_WORKSPACE, NRM_ERR_CUDA, NRM_ERR_TIMEOUT = range(6)
 NRM_F32, NRM_F16, NRM_BF16 = 0, 1, 2
@@ -356,12 +355,13 @@ def _heads():
     import importlib.machinery
     import importlib.util
 
-    import torch  # noqa: F401  (the module uses its libraries)
+    from .build import heads_path
     load()
-    if not os.path.exists(HEADS_PATH):
-        raise ImportError(f"libnorm is not built ({HEADS_PATH} is missing); run "
-                          "`python -m normalization_layernorm_rmsnorm_gb300.build`")
-    loader = importlib.machinery.ExtensionFileLoader("_heads", HEADS_PATH)
+    path = heads_path()  # (imports torch, whose libraries the module uses)
+    if not os.path.exists(path):
+        raise ImportError(f"libnorm's calls on heads are not built for this PyTorch and Python ({path} is missing); "
+                          "run `python -m normalization_layernorm_rmsnorm_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_heads", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_heads", loader))
     loader.exec_module(module)
     module.set_error(NrmError)

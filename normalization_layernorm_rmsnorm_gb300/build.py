@@ -1,6 +1,6 @@
 """Builds libnorm.so in-tree (``_build/``) with nvcc for sm_103a, and the Python
-extension that marshals the calls on attention heads (``_heads.so``) with g++,
-where PyTorch's headers are (libnorm.so itself is plain C and needs none).
+extension that marshals the calls on attention heads with g++, where PyTorch's
+headers are (libnorm.so itself is plain C and needs none).
 
 Each translation unit is compiled in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  Rebuilds only what changed.
@@ -21,7 +21,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libnorm.so")
-HEADS = os.path.join(BUILD, "_heads.so")  # the compiled marshalling (csrc/heads_binding.cpp)
 
 SOURCES = ["api.cu", "noalloc.cu", "dropout.cu",
            "rownorm_f32.cu", "rownorm_f16.cu", "rownorm_bf16.cu",
@@ -57,6 +56,16 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def heads_path() -> str:
+    """The compiled marshalling (csrc/heads_binding.cpp) for this PyTorch and Python.  It reads
+    PyTorch's objects, so one built for others must not be loaded: the name says which."""
+    import sysconfig
+
+    import torch
+    return os.path.join(BUILD, f"_heads.{sysconfig.get_config_var('SOABI')}.torch{torch.__version__}"
+                               f".abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}.so")
+
+
 def _binding_includes() -> list[str] | None:
     """Directories of the binding's headers; None where g++, PyTorch's headers (with
     CUDA) or Python's are missing: then there is no binding to build."""
@@ -90,13 +99,14 @@ def _compile_binding(includes: list[str]) -> str:
 def _link_binding(obj: str) -> None:
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = HEADS + f".tmp{os.getpid()}"
+    path = heads_path()
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-lnorm", "-L", libs, "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, HEADS)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -108,7 +118,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         return force or not os.path.exists(f) or os.path.getmtime(f) < dep
 
     includes = _binding_includes()
-    lib, heads = verbose_ptxas or stale(LIB), includes is not None and stale(HEADS)
+    lib, heads = verbose_ptxas or stale(LIB), includes is not None and stale(heads_path())
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as pool:
         binding = pool.submit(_compile_binding, includes) if heads else None

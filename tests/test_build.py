@@ -8,6 +8,7 @@ import types
 import pytest
 import torch
 
+from normalization_layernorm_rmsnorm_gb300 import _binding as B
 from normalization_layernorm_rmsnorm_gb300 import build as nbuild
 
 
@@ -28,11 +29,8 @@ def ran(monkeypatch, tmp_path):
         open(out, "w").write("made")
         return types.SimpleNamespace(returncode=0, stdout="", stderr="")
 
-    for name in ("BUILD", "LIB", "HEADS"):
-        if hasattr(nbuild, name):
-            old = getattr(nbuild, name)
-            monkeypatch.setattr(nbuild, name, str(tmp_path) + old[len(os.path.dirname(nbuild.LIB)):]
-                                if name != "BUILD" else str(tmp_path))
+    monkeypatch.setattr(nbuild, "BUILD", str(tmp_path))
+    monkeypatch.setattr(nbuild, "LIB", str(tmp_path / "libnorm.so"))
     monkeypatch.setattr(nbuild, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
     monkeypatch.setattr(nbuild, "subprocess", types.SimpleNamespace(run=run))
     return commands
@@ -78,3 +76,20 @@ def test_a_failure_of_the_binding_is_raised_after_libnorm_is_made(ran, monkeypat
     with pytest.raises(RuntimeError, match="g\\+\\+"):
         nbuild.build()
     assert os.path.exists(nbuild.LIB)
+
+
+@pytest.mark.parametrize("change", ["version", "abi", "python"])
+def test_the_binding_of_another_pytorch_or_python_is_neither_kept_nor_loaded(ran, monkeypatch, change):
+    nbuild.build()
+    del ran[:]
+    if change == "version":
+        monkeypatch.setattr(torch, "__version__", "2.0.0")
+    elif change == "abi":
+        monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    else:
+        import sysconfig
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-x86_64-linux-gnu")
+    with pytest.raises(ImportError, match="python -m normalization_layernorm_rmsnorm_gb300.build"):
+        B._heads.__wrapped__()
+    nbuild.build()
+    assert len(bindings(ran)) == 2 and len(ran) == 2
