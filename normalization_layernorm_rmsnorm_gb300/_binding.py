@@ -420,14 +420,25 @@ def nrm_rope_bwd(dq_out, dk_out, pos, inv_freq, dq, dk, stream=None, axis=None, 
 
 
 class KvCache:
-    """A paged, quantised key/value cache (kv_cache): the tensors and their C description."""
+    """A paged, quantised key/value cache (kv_cache): the tensors and their C description.
+
+    Its attributes cannot be set: the description holds the tensors' addresses, and a
+    tensor that was replaced here could be freed under it."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "heads", "d", "slots", "held", "address",
                  "_c")
 
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of a cache cannot be set: make a new one (kv_cache)")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of a cache cannot be deleted")
+
+    def __copy__(self):
+        return self
+
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         import torch
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         codes, scales = (k_codes, k_scales) if k_codes is not None else (v_codes, v_scales)
         if codes is None or scales is None:
             raise ValueError("a cache needs codes and scales")
@@ -455,10 +466,12 @@ class KvCache:
         for t in (k_codes, k_scales, v_codes, v_scales):
             if t is not None and (not t.is_cuda or t.get_device() != dev):
                 raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
-        self.heads, self.d, self.slots, self.held = heads, d, pages * page, codes
-        self._c = _Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, page, heads, d,
-                         d // scales.shape[3], *codes.stride()[:3], *scales.stride()[:3], kind)
-        self.address = ctypes.addressof(self._c)
+        c = _Cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, page, heads, d,
+                   d // scales.shape[3], *codes.stride()[:3], *scales.stride()[:3], kind)
+        for name, value in (("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales),
+                            ("heads", heads), ("d", d), ("slots", pages * page), ("held", codes),
+                            ("address", ctypes.addressof(c)), ("_c", c)):
+            object.__setattr__(self, name, value)
 
 
 def kv_cache(k_codes, k_scales, v_codes=None, v_scales=None) -> KvCache:
