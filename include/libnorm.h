@@ -481,7 +481,7 @@ NRM_API nrm_status nrm_qk_norm_rope_fwd(const nrm_heads *q, const nrm_heads *k, 
  * wk, rstd_k, dk are ignored, and dwk is NULL).  workspace: nrm_workspace_bytes(NRM_OP_QK_NORM_BWD, tokens, d, dt)
  * bytes, 16-byte aligned, clobbered; may be NULL when dwq and dwk are NULL.
  * Calls that overlap on the GPU need separate workspaces.
- * With tokens == 0, dwq and dwk are set to 0.
+ * tokens*d <= 2^40.  With tokens == 0, dwq and dwk are set to 0.
  */
 NRM_API nrm_status nrm_qk_norm_rope_bwd(const nrm_heads *dq_out, const nrm_heads *dk_out,
                                 const nrm_heads *q, const nrm_heads *k, const void *wq,

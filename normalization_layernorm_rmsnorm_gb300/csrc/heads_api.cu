@@ -309,6 +309,8 @@ nrm_status nrm_qk_norm_rope_bwd(const nrm_heads* dq_out, const nrm_heads* dk_out
                                 size_t workspace_bytes, nrm_stream_t stream) {
     return entry([&]() -> nrm_status {
         NRM_TRY(check_sizes(tokens, d, dt));
+        // beyond it nrm_workspace_bytes has no answer
+        if (tokens > kMaxRows / d) return fail(NRM_ERR_UNSUPPORTED, "tokens*d must be <= 2^40");
         NRM_TRY(check_view("q", q, nullptr, tokens, d, dt, false));
         NRM_TRY(check_view("dq_out", dq_out, q, tokens, d, dt, false));
         NRM_TRY(check_view("dq", dq, q, tokens, d, dt, true));
