@@ -493,7 +493,8 @@ NRM_API nrm_status nrm_qk_norm_rope_bwd(const nrm_heads *dq_out, const nrm_heads
 /*
  * nrm_rope_fwd -- the rotation alone: q_out = R(q), k_out = R(k); in place is
  * allowed, k may be NULL.  nrm_rope_bwd -- its backward, the turn the other
- * way: dq = R^T(dq_out), dk = R^T(dk_out); the same rules.
+ * way: dq = R^T(dq_out), dk = R^T(dk_out); the same rules.  A row's bits depend
+ * on the row and its position alone, not on pointers, strides or other rows.
  */
 NRM_API nrm_status nrm_rope_fwd(const nrm_heads *q, const nrm_heads *k, const nrm_rope *rope,
                         const nrm_heads *q_out, const nrm_heads *k_out, int64_t tokens, int64_t d,

@@ -121,10 +121,11 @@ __device__ __forceinline__ float2 pair_turn(const RopeDev& r, uint64_t step, int
                        __uint_as_float(__float_as_uint(sin) ^ (neg_sin & 0x80000000u)));
 }
 
-// (u, v) turned by (cos, sin).
+// (u, v) turned by (cos, sin), rounded as on vectors (LaneMap, LaneTurns): the
+// rotation's bits do not depend on how a row is accessed.
 __device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
-    const float a = fmaf(u, cs.x, -__fmul_rn(v, cs.y));
-    const float b = fmaf(v, cs.x, __fmul_rn(u, cs.y));
+    const float a = fmaf(-v, cs.y, __fmul_rn(u, cs.x));
+    const float b = fmaf(u, cs.y, __fmul_rn(v, cs.x));
     u = a;
     v = b;
 }
