@@ -66,6 +66,9 @@ def test_fuzz_rotation(case):
 def check_cache(cache, kind, group, slots, rows, back):
     """Codes and scales of `rows` (k, v) at `slots` are the reference's, and read back as their values."""
     live = slots >= 0
+    if not live.any():
+        assert not any(b.any() for b in back)
+        return
     for x, n, got in zip(rows, "kv", back):
         want_c, want_s = ref.quantise(H.f64(x[live]), kind, group)
         codes, scales = getattr(cache, n + "_codes"), getattr(cache, n + "_scales")
