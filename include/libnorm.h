@@ -574,7 +574,11 @@ NRM_API nrm_status nrm_kv_cache_read(const nrm_kv_cache *cache, const int64_t *s
  * dt, and of v.  q_out: as there; may be q in place.  k_out: the key itself,
  * or NULL when only the cache is wanted; may be k in place.  v: [tokens, hk,
  * d]; cache->heads == hk.  A token whose slot is -1 gets q_out and k_out and
- * leaves the cache alone.
+ * leaves the cache alone.  Where the norm is added up depends on how wide the
+ * accesses are, and these go by all of the call's views and the cache's groups and
+ * strides: where they are as wide as those of the separate calls, the bits are
+ * theirs too, else a normed row may differ from theirs in its last bit.  Without
+ * the norm the bits are always theirs.
  */
 NRM_API nrm_status nrm_qk_norm_rope_cache(const nrm_heads *q, const nrm_heads *k, const nrm_heads *v,
                                   const void *wq, const void *wk, const nrm_rope *rope,

@@ -59,9 +59,9 @@ __device__ __forceinline__ R ld_after(const R* p) {
 // Work in waves: as many CTAs as are resident at once, each warp taking `rounds`
 // units that lie a wave's warps apart, then the next wave's CTAs.  CTAs that stay
 // for all of a large problem drift apart, and what the GPU touches at one time
-// spreads over more and more of memory: the rotation of 400 MB, bf16, 12 + 12 heads
-// of 128, takes 140 us that way, 117 in waves of four or six rounds (118 at the copy
-// rate), 121 of eight and 127 of ten.  Where instructions bound (the norm of heads
+// spreads over more and more of memory: the rotation of 65536 tokens (bf16, 12 + 12
+// heads of 128: 400 MB read and 400 written) takes 140 us that way, 117 in waves of
+// four or six rounds (118 at the copy rate), 121 of eight and 127 of ten.  Where instructions bound (the norm of heads
 // of 64), a new wave's start costs 1 to 2% at six rounds, 4% at four.
 constexpr int kWaveRounds = 6;  // at most
 struct Waves {
@@ -1203,11 +1203,11 @@ __device__ __forceinline__ void ld_row_wide(const void* p, uint4 (&r)[2]) {
 // Writing.  A lane's vectors are neighbours: a group is then fewer lanes, and a
 // lane makes one scale for both.  The group's largest magnitude meets by shuffles.
 //
-// Bound by issue slots (about 240 instructions for four rows of 128: magnitudes,
+// Bound by issue slots (227 instructions for four rows of 128: magnitudes,
 // a scale, four packed operations a pair of elements for codes that round like
 // the real quotient) and by bytes: 131072 tokens of 8 + 8 heads of 128, bf16 to
-// four bits in groups of 32, 713 MB, 105 us at the copy rate, 123 measured (5.8
-// TB/s; CTAs that stay 129).  One vector a lane, or two that are not neighbours, 160 to 215; copies
+// four bits in groups of 32, 706 MB, 104 us at the copy rate, 124 measured (5.7
+// TB/s; CTAs that stay 129); to 8 bits, a scale a row, 815 MB, 120 and 124 to 127.  One vector a lane, or two that are not neighbours, 160 to 215; copies
 // ahead as in the forward 186 (more instructions); the form at run time 141.
 template <typename T, int VE, int NV, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32)
@@ -1348,8 +1348,8 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
     }
 }
 
-// Reading: bound by bytes, 713 MB for the same 131072 tokens, 105 us at the copy
-// rate, 111 measured (6.4 TB/s; CTAs that stay 114).  A lane's two vectors are here those at j and j +
+// Reading: bound by bytes, 706 MB for the same 131072 tokens, 104 us at the copy
+// rate, 110 measured (6.4 TB/s; CTAs that stay 114).  A lane's two vectors are here those at j and j +
 // per: each store of a warp then covers whole lines (two neighbouring vectors a
 // lane, stored 32 bytes at once, took 122 against 116).  Five CTAs an SM; four and
 // six 113 and 125 here, 11.4 and 12.1 against 10.7 for 15250 tokens of 4 heads.
@@ -1428,8 +1428,9 @@ cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves w
 // ---------------------------------------------------------------------------
 // Rows whose rotated halves start between vectors (rot/2 odd), unaligned views, odd
 // d.  Bound by latency and issue slots; a warp has 4 / S rows of S slots a lane
-// under way.  bf16, 6653 tokens of 24 + 12 heads of 40 with 10 rotated (38 MB): 55
-// us, one row at a time 64; about 250 instructions a row.
+// under way.  bf16, 6653 tokens of 24 + 12 heads of 40 with 10 rotated (38 MB, 5.8 us
+// at the copy rate): 55 us, one row at a time 64; backward 143.  About 250
+// instructions a row.
 
 // The elements of pair slot j (e1 == d: past the end of an odd row) and whether they turn.
 struct SlotAt {
@@ -1663,7 +1664,7 @@ head_bwd_scalar_kernel(const __grid_constant__ HeadArgs a, int nq) {
 // dw of q (blockIdx.y 0) and of k (1): the column sums of their partial rows, in
 // a fixed order.  A column's rows are split over the 32 warps of a CTA; the
 // partial rows can be much larger than their sum, so both levels carry the
-// rounding error along (Neumaier's sum).  About 3 us after the backward, most of it
+// rounding error along (Neumaier's sum).  2.5 us after the backward, most of it
 // launch and the first loads; a tree of float pairs over the warps was no faster.
 constexpr int kHeadSumWarps = 32;
 struct CarriedSum {
@@ -1791,7 +1792,7 @@ inline int64_t make_waves(int64_t work, int64_t resident, Waves* w) {
 
 // Tokens (as a power of two) that share a warp's rows where a token's `heads` heads
 // leave some of the 32 >> lg free, and tokens are many enough to fill the SMs so
-// (f16, 21209 tokens of 1 + 1 heads of 64: 31 us with a token a warp).
+// (f16, 21209 tokens of 1 + 1 heads of 64: 31 us with a token a warp, 9 so).
 inline int head_tokens_log2(int64_t tokens, int heads, int lg, const DevInfo& d) {
     int lt = 0;
     while (lt < 5 - lg && heads <= (32 >> lg) >> (lt + 1) && tokens >> (lt + 1) >= int64_t(8) * d.sms) ++lt;
