@@ -810,16 +810,26 @@ head_fwd_vec_kernel(const __grid_constant__ HeadArgs a, int lg, int ltokens, int
     pdl_next();
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
-    fill_steps(a.rope, s_step, threadIdx.x, N);
+    // (both loads are under way before either is waited for)
+    constexpr int W = 2 * kHeadMaxD / VE, PER = (W + N - 1) / N;
+    Raw<T, VE> wt[norm ? PER : 1];
     if (norm) {
         float2 ones[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) ones[i] = f2(1.f);
-        for (int i = threadIdx.x; i < 2 * kHeadMaxD / VE; i += N) {
-            const int which = i / (kHeadMaxD / VE), e = i % (kHeadMaxD / VE) * VE;
-            const T* w = reinterpret_cast<const T*>(a.w[which]);
-            s_w[which][e / VE] =
-                w && e < a.d ? ld_after(reinterpret_cast<const Raw<T, VE>*>(w + e)) : raw_pack<T, VE>(ones);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = threadIdx.x + k * N, which = i / (W / 2), e = i % (W / 2) * VE;
+            const T* w = i < W ? reinterpret_cast<const T*>(a.w[which]) : nullptr;
+            wt[k] = w && e < a.d ? ld_after(reinterpret_cast<const Raw<T, VE>*>(w + e)) : raw_pack<T, VE>(ones);
+        }
+    }
+    fill_steps(a.rope, s_step, threadIdx.x, N);
+    if (norm) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = threadIdx.x + k * N;
+            if (i < W) s_w[i / (W / 2)][i % (W / 2)] = wt[k];
         }
     }
     __syncthreads();
