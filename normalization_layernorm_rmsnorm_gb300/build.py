@@ -67,14 +67,17 @@ def heads_path() -> str:
 
 
 def _binding_includes() -> list[str] | None:
-    """Directories of the binding's headers; None where g++, PyTorch's headers (with
-    CUDA) or Python's are missing: then there is no binding to build."""
+    """Directories of the binding's headers; None where g++, PyTorch's headers and CUDA
+    library or Python's headers are missing: then there is no binding to build."""
     import sysconfig
     try:
         import torch
-    except ImportError:
+    except (ImportError, OSError):  # (its libraries may be missing)
         return None
-    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    home = os.path.dirname(torch.__file__)
+    if not os.path.exists(os.path.join(home, "lib", "libc10_cuda.so")):
+        return None
+    inc = os.path.join(home, "include")
     dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
     for header in ("torch/csrc/autograd/python_variable.h", "c10/cuda/CUDAStream.h", "Python.h"):
         if not any(os.path.exists(os.path.join(d, header)) for d in dirs):

@@ -54,6 +54,15 @@ def test_libnorm_needs_no_headers_of_pytorch(ran, monkeypatch, tmp_path):
     assert os.path.exists(nbuild.build()) and not bindings(ran)
 
 
+def test_libnorm_needs_no_cuda_in_pytorch(ran, monkeypatch, tmp_path):
+    # a PyTorch without CUDA has the headers, and no library to link
+    home = tmp_path / "torch"
+    home.mkdir()
+    (home / "include").symlink_to(os.path.join(os.path.dirname(torch.__file__), "include"))
+    monkeypatch.setattr(torch, "__file__", str(home / "__init__.py"))
+    assert os.path.exists(nbuild.build()) and not bindings(ran)
+
+
 def test_libnorm_needs_no_gxx(ran, monkeypatch):
     which = shutil.which
     monkeypatch.setattr(nbuild.shutil, "which", lambda c: None if c == "g++" else which(c))
