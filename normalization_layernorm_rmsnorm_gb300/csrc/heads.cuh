@@ -61,8 +61,9 @@ __device__ __forceinline__ R ld_after(const R* p) {
 // for all of a large problem drift apart, and what the GPU touches at one time
 // spreads over more and more of memory: the rotation of 65536 tokens (bf16, 12 + 12
 // heads of 128: 400 MB read and 400 written) takes 140 us that way, 117 in waves of
-// four or six rounds (118 at the copy rate), 121 of eight and 127 of ten.  Where instructions bound (the norm of heads
-// of 64), a new wave's start costs 1 to 2% at six rounds, 4% at four.
+// four or six rounds (118 at the copy rate), 121 of eight and 127 of ten.  Where
+// instructions bound (the norm of heads of 64), a new wave's start costs 1 to 2% at
+// six rounds, 4% at four.
 constexpr int kWaveRounds = 6;  // at most
 struct Waves {
     int ctas, rounds;  // of a wave
@@ -1217,8 +1218,9 @@ __device__ __forceinline__ void ld_row_wide(const void* p, uint4 (&r)[2]) {
 // a scale, four packed operations a pair of elements for codes that round like
 // the real quotient) and by bytes: 131072 tokens of 8 + 8 heads of 128, bf16 to
 // four bits in groups of 32, 706 MB, 104 us at the copy rate, 124 measured (5.7
-// TB/s; CTAs that stay 129); to 8 bits, a scale a row, 815 MB, 120 and 124 to 127.  One vector a lane, or two that are not neighbours, 160 to 215; copies
-// ahead as in the forward 186 (more instructions); the form at run time 141.
+// TB/s; CTAs that stay 129); to 8 bits, a scale a row, 815 MB, 120 and 124 to 127.
+// One vector a lane, or two that are not neighbours, 160 to 215; copies ahead as in
+// the forward 186 (more instructions); the form at run time 141.
 template <typename T, int VE, int NV, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32)
 cache_write_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves waves) {
@@ -1359,10 +1361,11 @@ __device__ __forceinline__ void code_values(uint2 w, int kind, float scale, floa
 }
 
 // Reading: bound by bytes, 706 MB for the same 131072 tokens, 104 us at the copy
-// rate, 110 measured (6.4 TB/s; CTAs that stay 114).  A lane's two vectors are here those at j and j +
-// per: each store of a warp then covers whole lines (two neighbouring vectors a
-// lane, stored 32 bytes at once, took 122 against 116).  Five CTAs an SM; four and
-// six 113 and 125 here, 11.4 and 12.1 against 10.7 for 15250 tokens of 4 heads.
+// rate, 110 measured (6.4 TB/s; CTAs that stay 114).  A lane's two vectors are here
+// those at j and j + per: each store of a warp then covers whole lines (two
+// neighbouring vectors a lane, stored 32 bytes at once, took 122 against 116).  Five
+// CTAs an SM; four and six 113 and 125 here, 11.4 and 12.1 against 10.7 for 15250
+// tokens of 4 heads.
 template <typename T, int VE, int KIND>
 __global__ void __launch_bounds__(kHeadWarps * 32, 5)
 cache_read_vec_kernel(const __grid_constant__ HeadArgs a, CacheLanes cl, Waves waves) {
