@@ -587,6 +587,151 @@ NRM_API nrm_status nrm_qk_norm_rope_cache(const nrm_heads *q, const nrm_heads *k
                                   int64_t d, float eps, int norm, nrm_dtype dt,
                                   nrm_stream_t stream);
 
+/*
+ * A paged sequence: position j of sequence s lies in the cache's slot
+ * table[s*stride + j/page_size]*page_size + j%page_size, and lengths[s]
+ * positions of it are written.  Entries behind the last position are not read.
+ * table: device int64, `sequences` rows of `width` page numbers, stride >=
+ * width.  lengths: device int64 [sequences], each in [0, width*page_size]; one
+ * outside it is taken as the nearer end.  A page outside the cache leaves its
+ * positions out.  Both are reported by the next nrm_sync_status as
+ * NRM_ERR_INVALID_ARG.  Sequences may share pages.
+ */
+typedef struct nrm_kv_pages {
+    const int64_t *table;
+    const int64_t *lengths;
+    int64_t sequences;
+    int64_t width;
+    int64_t stride; /* elements */
+} nrm_kv_pages;
+
+/* A float32 number for every position of every head of keys in a sequence:
+ * position j of head g of sequence s at data + s*sequence_stride +
+ * g*head_stride + j (strides in elements, >= 0, rows of `capacity` positions
+ * do not overlap).  A length above `capacity` counts as one out of range. */
+typedef struct nrm_kv_weights {
+    float *data;
+    int64_t capacity;
+    int64_t sequence_stride;
+    int64_t head_stride;
+} nrm_kv_weights;
+
+/*
+ * nrm_kv_cache_attention -- attention of one new token of each sequence over
+ * the cache, straight from its codes.  Query head h reads head g = h/(hq/hk)
+ * of the cache (hq a multiple of hk = cache->heads).  With n = lengths[s],
+ * over the positions max(0, n - window) <= j < n (all of them when window ==
+ * 0), and k_j, v_j the values that nrm_kv_cache_read would give in float32:
+ *   l_j = scale * sum_i q_i*k_ji;  lse = log sum_j exp l_j;
+ *   p_j = exp(l_j - lse);          out_i = sum_j p_j*v_ji
+ * Without a position (n == 0), out is 0 and lse -infinity.
+ * q, out: [sequences, hq, d] views in dt (not in place).  lse: float32
+ * [sequences, hq], dense; may be NULL.  weights: may be NULL, else the weight
+ * that each position received is added to what it holds,
+ *   weights[s, g, j] += sum over the heads h of g of p_j,
+ * and positions outside the window are left as they were.
+ * scale: finite.  workspace: nrm_kv_attention_workspace_bytes(...) bytes,
+ * 16-byte aligned, clobbered; calls that overlap on the GPU need separate ones.
+ * The sums are float32 over products that are exact, or of factors with 22
+ * bits, but for the p_j of bfloat16 outputs, rounded to 11 bits.
+ * 16-byte aligned rows of codes, with d and group multiples of 16, take the
+ * tensor cores; other layouts, 8-byte aligned ones apart, run element by element.
+ */
+NRM_API nrm_status nrm_kv_cache_attention(const nrm_heads *q, const nrm_kv_cache *cache,
+                                  const nrm_kv_pages *pages, const nrm_heads *out, float scale,
+                                  int64_t window, float *lse, const nrm_kv_weights *weights,
+                                  nrm_dtype dt, void *workspace, size_t workspace_bytes,
+                                  nrm_stream_t stream);
+
+/* Workspace bytes of nrm_kv_cache_attention on the current device for
+ * `sequences` sequences with `heads` query heads; with weights, `positions` is
+ * the smaller of width*page_size and the weights' capacity (a larger one
+ * suffices too), without them 0.  Returns 0 for bad arguments or when no CUDA
+ * device is usable. */
+NRM_API size_t nrm_kv_attention_workspace_bytes(int64_t sequences, int64_t heads, const nrm_kv_cache *cache,
+                                        int64_t positions);
+
+/*
+ * nrm_kv_cache_evict -- shortens sequences to `keep` positions by the weight
+ * that each position has received, head by head.  A sequence of n <= keep
+ * positions keeps them all.  Of a longer one, each head of the cache keeps
+ *   the first `first` positions, the last `recent` ones, and of those between,
+ *   the keep - first - recent with the largest weights (of equal ones the
+ *   earlier; a NaN counts as larger than any number, -0 as 0),
+ * in their order, and their rows of keys and values, codes and scales, are
+ * copied into the pages of new_table, where they are the positions 0, 1, ... of
+ * the shortened sequence.  Heads keep different positions, so a slot then holds
+ * keys of different tokens; rotation has been applied before a key is cached,
+ * so attention does not depend on the order.
+ * new_table: device int64 [sequences][new_stride >= new_width], new_width *
+ * page_size >= keep; its pages must not be among those that the call reads, nor
+ * occur twice.  new_lengths: device int64 [sequences], receives min(n, keep);
+ * not the memory of lengths.  kept: device int64 [sequences, hk, keep], dense,
+ * receives the positions that stay, ascending, and -1 behind the last.
+ * weights: as in nrm_kv_cache_attention (read).  new_weights: their values at
+ * the positions that stay, capacity >= keep; what lies behind the last is left
+ * as it was; may be NULL; not the memory of weights.
+ * 1 <= keep < 2^31; 0 <= first, recent; first + recent <= keep; sequences of
+ * fewer than 2^32 positions.
+ */
+NRM_API nrm_status nrm_kv_cache_evict(const nrm_kv_cache *cache, const nrm_kv_pages *pages,
+                              const nrm_kv_weights *weights, const int64_t *new_table,
+                              int64_t new_width, int64_t new_stride, int64_t *new_lengths,
+                              const nrm_kv_weights *new_weights, int64_t *kept, int64_t keep,
+                              int64_t first, int64_t recent, nrm_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Between two blocks of a residual stream                                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * nrm_block_norm_fwd -- the RMSNorm after a block, its gate and residual scale,
+ * the residual add and the RMSNorm before the next block, in one pass over
+ * rows of `cols`:
+ *   n = f*r1*w_post, r1 = (sum f^2/cols + eps)^(-1/2)   (n = f when post == 0)
+ *   y = x + alpha*gate*n, rounded to dt
+ *   h = y*r2*w_pre,  r2 = (sum y^2/cols + eps)^(-1/2)
+ * x: the stream before the block; f: the block's output; y: the stream after
+ * it; all [rows, cols] dense, in dt.  gate: [gates, cols] in dt, row r takes
+ * row r/(rows/gates) (gates divides rows; 1: one for all rows); NULL with
+ * gates == 0: 1.  w_post, w_pre: [cols] in dt, each may be NULL (1).  h may be
+ * NULL: the stream alone.  rstd_post, rstd_pre: float32 [rows], receive r1 and
+ * r2; each may be NULL; not one memory.  y may be x and h may be f (in place);
+ * no other overlap.  alpha: finite.  eps > 0.
+ */
+NRM_API nrm_status nrm_block_norm_fwd(const void *x, const void *f, const void *gate, const void *w_post,
+                              const void *w_pre, void *y, void *h, float *rstd_post, float *rstd_pre,
+                              int64_t rows, int64_t cols, int64_t gates, float alpha, float eps,
+                              int post, nrm_dtype dt, nrm_stream_t stream);
+
+/*
+ * nrm_block_norm_bwd -- its backward.  With G = dh*w_pre (r2, y and the sums
+ * over a row as above):
+ *   dx = dy + r2*G - y*r2^3*sum(G*y)/cols        (the gradient of y, and of x)
+ *   dn = alpha*gate*dx;  dgate = sum over the gate row's rows of alpha*dx*n
+ *   df = r1*g - f*r1^3*sum(g*f)/cols, g = dn*w_post     (df = dn when post == 0)
+ *   dw_post = sum over rows of dn*f*r1;  dw_pre = sum over rows of dh*y*r2
+ * dh: the gradient of h; NULL where the forward had no h (then w_pre and
+ * rstd_pre are ignored, and dw_pre is NULL).  dy: the gradient of y that the
+ * stream brings back; may be NULL (0); not both NULL.  f, y, gate, w_post,
+ * w_pre, rstd_*: those of the forward.  dx, df: [rows, cols], not in place.
+ * dgate: [gates, cols] in dt; dw_post, dw_pre: [cols] in dt; each may be NULL,
+ * and dgate is without a gate, dw_post with post == 0.  workspace:
+ * nrm_block_norm_workspace_bytes(...) bytes, 16-byte aligned, clobbered; may be
+ * NULL when dgate, dw_post and dw_pre are.  Calls that overlap on the GPU need
+ * separate workspaces.  With rows == 0 the gradients of the weights are 0.
+ */
+NRM_API nrm_status nrm_block_norm_bwd(const void *dh, const void *dy, const void *f, const void *y,
+                              const void *gate, const void *w_post, const void *w_pre,
+                              const float *rstd_post, const float *rstd_pre, void *dx, void *df,
+                              void *dgate, void *dw_post, void *dw_pre, int64_t rows, int64_t cols,
+                              int64_t gates, float alpha, int post, nrm_dtype dt, void *workspace,
+                              size_t workspace_bytes, nrm_stream_t stream);
+
+/* Workspace bytes of nrm_block_norm_bwd on the current device.  Returns 0 for
+ * bad arguments or when no CUDA device is usable. */
+NRM_API size_t nrm_block_norm_workspace_bytes(int64_t rows, int64_t cols, int64_t gates, nrm_dtype dt);
+
 /* ------------------------------------------------------------------------ */
 /* Helpers                                                                   */
 /* ------------------------------------------------------------------------ */

@@ -38,6 +38,8 @@ EXPORTS = ("nrm_layernorm_fwd", "nrm_layernorm_bwd", "nrm_layernorm_bwd_noalloc"
            "nrm_batchnorm_fwd", "nrm_batchnorm_bwd", "nrm_act_dropout_fwd", "nrm_act_dropout_bwd",
            "nrm_qk_norm_rope_fwd", "nrm_qk_norm_rope_bwd", "nrm_rope_fwd", "nrm_rope_bwd",
            "nrm_kv_cache_write", "nrm_kv_cache_read", "nrm_qk_norm_rope_cache",
+           "nrm_kv_cache_attention", "nrm_kv_attention_workspace_bytes", "nrm_kv_cache_evict",
+           "nrm_block_norm_fwd", "nrm_block_norm_bwd", "nrm_block_norm_workspace_bytes",
            "nrm_workspace_bytes",
            "nrm_batchnorm_workspace_bytes",
            "nrm_act_mask_words", "nrm_sync_status", "nrm_status_str",
@@ -72,7 +74,15 @@ class _Cache(ctypes.Structure):
                             "scale_page_stride", "scale_slot_stride", "scale_head_stride")] + [("kind", _I)]
 
 
-_HP, _RP, _CP = (ctypes.POINTER(t) for t in (_Heads, _Rope, _Cache))
+class _Pages(ctypes.Structure):
+    _fields_ = [("table", _P), ("lengths", _P), ("sequences", _I64), ("width", _I64), ("stride", _I64)]
+
+
+class _Weights(ctypes.Structure):
+    _fields_ = [("data", _P), ("capacity", _I64), ("sequence_stride", _I64), ("head_stride", _I64)]
+
+
+_HP, _RP, _CP, _PP, _WP = (ctypes.POINTER(t) for t in (_Heads, _Rope, _Cache, _Pages, _Weights))
 
 
 def load(path: str | None = None):
@@ -112,6 +122,13 @@ def load(path: str | None = None):
         "nrm_kv_cache_write": [_HP, _HP, _CP, _P, _I64, _I, _P],
         "nrm_kv_cache_read": [_CP, _P, _HP, _HP, _I64, _I, _P],
         "nrm_qk_norm_rope_cache": [_HP, _HP, _HP, _P, _P, _RP, _HP, _HP, _CP, _P, _I64, _I64, _F, _I, _I, _P],
+        "nrm_kv_cache_attention": [_HP, _CP, _PP, _HP, _F, _I64, _P, _WP, _I, _P, ctypes.c_size_t, _P],
+        "nrm_kv_attention_workspace_bytes": [_I64, _I64, _CP, _I64],
+        "nrm_kv_cache_evict": [_CP, _PP, _WP, _P, _I64, _I64, _P, _WP, _P, _I64, _I64, _I64, _P],
+        "nrm_block_norm_fwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _F, _I, _I, _P],
+        "nrm_block_norm_bwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _F, _I, _I, _P,
+                               ctypes.c_size_t, _P],
+        "nrm_block_norm_workspace_bytes": [_I64, _I64, _I64, _I],
         "nrm_workspace_bytes": [_I, _I64, _I64, _I],
         "nrm_batchnorm_workspace_bytes": [_I64, _I64, _I64, _I],
         "nrm_act_mask_words": [_I64, _I64, _I64],
@@ -126,6 +143,8 @@ def load(path: str | None = None):
         f.argtypes = args
         f.restype = _I
     lib.nrm_workspace_bytes.restype = ctypes.c_size_t
+    lib.nrm_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.nrm_block_norm_workspace_bytes.restype = ctypes.c_size_t
     lib.nrm_batchnorm_workspace_bytes.restype = ctypes.c_size_t
     lib.nrm_act_mask_words.restype = ctypes.c_int64
     lib.nrm_status_str.restype = ctypes.c_char_p
@@ -504,6 +523,80 @@ def nrm_qk_norm_rope_cache(q, k, v, wq, wk, pos, inv_freq, q_out, k_out, cache, 
     k_out may be None when only the cache is wanted."""
     _heads().qk_norm_rope_cache(q, k, v, wq, wk, pos, inv_freq, q_out, k_out, cache.address, cache.held, slots, eps,
                                 stream, axis, pairs, norm)
+
+
+# ---------------------------------------------------------------------------
+# whole cached sequences: attention of a new token, eviction by weight
+# ---------------------------------------------------------------------------
+
+def kv_attention_workspace(q, cache, table, weights=False):
+    """A device workspace for nrm_kv_cache_attention on queries like q ([sequences,
+    heads, d]) with page tables like table; weights: for calls with weights."""
+    import torch
+    positions = table.shape[1] * (cache.slots // cache.held.shape[0]) if weights else 0
+    nbytes = int(load().nrm_kv_attention_workspace_bytes(table.shape[0], q.shape[-2], ctypes.byref(cache._c), positions))
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+
+
+def nrm_kv_cache_attention(q, cache, table, lengths, out, scale, workspace, stream=None, window=0, lse=None, weights=None):
+    """Attention of one new token of each sequence over the cache, straight from its codes.
+
+    q, out: [sequences, heads, d] views, heads a multiple of the cache's.  table:
+    int64 [sequences, pages], the pages of each sequence in order; lengths: int64
+    [sequences], its written positions (the new token's own among them, once it
+    is written).  window: the last positions that count (0: all).  lse: float32
+    [sequences, heads] receives log sum exp.  weights: float32 [sequences,
+    cache.heads, positions]; each position's attention weight, summed over the
+    heads that share it, is added to it (what nrm_kv_cache_evict goes by)."""
+    _heads().kv_cache_attention(q, cache.address, cache.held, table, lengths, out, scale, workspace, stream, window, lse,
+                                weights)
+
+
+def nrm_kv_cache_evict(cache, table, lengths, weights, new_table, new_lengths, new_weights, kept, stream=None, first=0,
+                       recent=0):
+    """Shortens sequences to keep = kept.shape[2] positions by weight, head by head:
+    the first `first`, the last `recent` and the largest weights between them
+    stay, in order, and their rows are copied to the pages of new_table.
+
+    kept: int64 [sequences, cache.heads, keep] receives the positions that stay
+    (-1 behind the last); new_lengths: int64 [sequences]; new_weights: float32
+    [sequences, cache.heads, >= keep] or None.  The pages of new_table must not be
+    among those that are read."""
+    _heads().kv_cache_evict(cache.address, cache.held, table, lengths, weights, new_table, new_lengths, new_weights, kept,
+                            stream, first, recent)
+
+
+# ---------------------------------------------------------------------------
+# between two blocks of a residual stream
+# ---------------------------------------------------------------------------
+
+def block_norm_workspace(x, gate=None):
+    """A device workspace for nrm_block_norm_bwd on rows like x's."""
+    import torch
+    rows, cols = _rows_cols(x)
+    gates = 0 if gate is None or cols == 0 else gate.numel() // cols
+    nbytes = int(load().nrm_block_norm_workspace_bytes(rows, cols, gates, _dtype_code(x)))
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+
+
+def nrm_block_norm_fwd(x, f, gate, w_post, w_pre, y, h, rstd_post, rstd_pre, alpha, eps, stream=None, post=True):
+    """The RMSNorm after a block, gate, residual scale and add, and the RMSNorm
+    before the next block: y = x + alpha * gate * norm(f) * w_post (the norm is
+    left out with post=False), h = norm(y) * w_pre.
+
+    x, f, y, h: [..., cols], contiguous; h may be None; y may be x, h may be f.
+    gate: None, [cols], or [gates, cols], each row for rows / gates rows of x.
+    Weights and statistics (float32, one a row) may be None."""
+    _heads().block_norm_fwd(x, f, gate, w_post, w_pre, y, h, rstd_post, rstd_pre, alpha, eps, stream, post)
+
+
+def nrm_block_norm_bwd(dh, dy, f, y, gate, w_post, w_pre, rstd_post, rstd_pre, dx, df, dgate, dw_post, dw_pre, workspace,
+                       alpha, stream=None, post=True):
+    """Backward of nrm_block_norm_fwd: dx, df and the gradients of gate and weights
+    (each may be None; workspace from block_norm_workspace).  dh is None where the
+    forward had no h, dy (the stream's own gradient) where there is none."""
+    _heads().block_norm_bwd(dh, dy, f, y, gate, w_post, w_pre, rstd_post, rstd_pre, dx, df, dgate, dw_post, dw_pre,
+                            workspace, alpha, stream, post)
 
 
 def nrm_act_mask_words(n: int, c: int, l: int) -> int:

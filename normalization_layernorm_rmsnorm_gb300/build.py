@@ -25,7 +25,9 @@ LIB = os.path.join(BUILD, "libnorm.so")
 SOURCES = ["api.cu", "noalloc.cu", "dropout.cu",
            "rownorm_f32.cu", "rownorm_f16.cu", "rownorm_bf16.cu",
            "batchnorm_f32.cu", "batchnorm_f16.cu", "batchnorm_bf16.cu",
-           "heads_api.cu", "heads_f32.cu", "heads_f16.cu", "heads_bf16.cu"]
+           "heads_api.cu", "heads_f32.cu", "heads_f16.cu", "heads_bf16.cu",
+           "kvattn_api.cu", "kvattn_f32.cu", "kvattn_f16.cu", "kvattn_bf16.cu", "kvevict.cu",
+           "blocknorm_api.cu", "blocknorm_f32.cu", "blocknorm_f16.cu", "blocknorm_bf16.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",

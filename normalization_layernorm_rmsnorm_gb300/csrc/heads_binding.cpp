@@ -1,5 +1,5 @@
-// heads_binding.cpp -- argument marshalling of the operators on attention heads,
-// compiled: these calls take up to fifteen tensors with strides, and a served
+// heads_binding.cpp -- argument marshalling of the operators on attention heads, on
+// the cached sequences and between the blocks of a residual stream, compiled: these calls take up to fifteen tensors with strides, and a served
 // model makes them for single tokens, where reading the tensors' shapes from
 // Python takes several times as long as the kernels.  Each function checks its
 // tensors (types, shapes, the current device), then calls the C entry point of
@@ -395,6 +395,206 @@ PyObject* qk_norm_rope_cache(PyObject*, PyObject* const* args, Py_ssize_t given)
     });
 }
 
+// Page tables [sequences, width] with contiguous rows, and a length for each.
+int64_t table_stride(const at::Tensor& t, const char* name, int64_t sequences) {
+    if (t.scalar_type() != at::kLong || t.dim() != 2)
+        raise(PyExc_ValueError, std::string(name) + " must be int64 [sequences, pages]");
+    if (t.size(0) != sequences)
+        raise(PyExc_ValueError, std::string(name) + " has " + std::to_string(t.size(0)) + " sequences, expected " +
+                                    std::to_string(sequences));
+    if (t.size(1) > 1 && t.stride(1) != 1) raise(PyExc_ValueError, std::string(name) + ": rows must be contiguous");
+    return t.size(0) > 1 ? t.stride(0) : t.size(1);
+}
+struct Pages {
+    nrm_kv_pages c{};
+    Pages(const at::Tensor& table, const at::Tensor& lengths, int64_t sequences) {
+        c.stride = table_stride(table, "table", sequences);
+        c.table = table.data_ptr<int64_t>();
+        c.width = table.size(1);
+        c.sequences = sequences;
+        c.lengths = static_cast<const int64_t*>(dense<true>(&lengths, "lengths", sequences, at::kLong));
+    }
+};
+
+// [sequences, heads, positions] with contiguous rows, or none.
+struct Weights {
+    nrm_kv_weights c{};
+    const nrm_kv_weights* ptr = nullptr;
+    Weights(const at::Tensor* t, const char* name, int64_t sequences, int64_t heads) {
+        if (!t) return;
+        if (t->scalar_type() != at::kFloat || t->dim() != 3)
+            raise(PyExc_ValueError, std::string(name) + " must be float32 [sequences, heads, positions]");
+        if (t->size(0) != sequences || t->size(1) != heads)
+            raise(PyExc_ValueError, std::string(name) + " has shape " + shape_text(t->sizes()) + ", expected " +
+                                        std::to_string(sequences) + " sequences of " + std::to_string(heads) + " heads");
+        if (t->size(2) > 1 && t->stride(2) != 1)
+            raise(PyExc_ValueError, std::string(name) + ": rows must be contiguous");
+        c = nrm_kv_weights{t->data_ptr<float>(), t->size(2), t->stride(0), t->stride(1)};
+        ptr = &c;
+    }
+};
+
+int64_t whole(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (PyErr_Occurred()) throw Raised{};
+    return v;
+}
+
+// (q, cache address, cache tensor, table, lengths, out, scale, workspace, stream, window, lse, weights)
+PyObject* kv_cache_attention(PyObject*, PyObject* const* args, Py_ssize_t given) {
+    return entry(args, given, 12, [](PyObject* const* o) {
+        const at::Tensor& q = *tensor(o[0], "q");
+        const Cache cache(o[1], o[2]);
+        const at::Tensor &table = *tensor(o[3], "table"), &lengths = *tensor(o[4], "lengths"), &out = *tensor(o[5], "out");
+        const at::Tensor *ws = tensor(o[7], "workspace", true), *lse = tensor(o[10], "lse", true);
+        const at::Tensor* weights = tensor(o[11], "weights", true);
+        View vq, vo;
+        vq.set(q, "q");
+        vo.set(out, "out", &q, &q);
+        if (vq.d != cache.c->d)
+            raise(PyExc_ValueError, "q has rows of " + std::to_string(vq.d) + ", the cache of " + std::to_string(cache.c->d));
+        const nrm_dtype dt = dtype_of(q, "q");
+        const Pages pages(table, lengths, vq.tokens);
+        const Weights w(weights, "weights", vq.tokens, cache.c->heads);
+        auto* pl = static_cast<float*>(dense<false>(lse, "lse", vq.tokens * vq.c.heads, at::kFloat));
+        if (ws && !ws->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+        const float scale = number(o[6]);
+        const int64_t window = whole(o[9]);
+        on_device({&q, &out, &table, &lengths, ws, lse, weights, cache.held});
+        const nrm_stream_t s = stream_of(o[8]);
+        call("nrm_kv_cache_attention", [&] {
+            return nrm_kv_cache_attention(vq.ptr, cache.c, &pages.c, vo.ptr, scale, window, pl, w.ptr, dt,
+                                          ws ? ws->data_ptr() : nullptr, ws ? size_t(ws->nbytes()) : 0, s);
+        });
+    });
+}
+
+// (cache address, cache tensor, table, lengths, weights, new_table, new_lengths, new_weights, kept, stream, first, recent)
+PyObject* kv_cache_evict(PyObject*, PyObject* const* args, Py_ssize_t given) {
+    return entry(args, given, 12, [](PyObject* const* o) {
+        const Cache cache(o[0], o[1]);
+        const at::Tensor &table = *tensor(o[2], "table"), &lengths = *tensor(o[3], "lengths");
+        const at::Tensor &weights = *tensor(o[4], "weights"), &new_table = *tensor(o[5], "new_table");
+        const at::Tensor &new_lengths = *tensor(o[6], "new_lengths"), *new_weights = tensor(o[7], "new_weights", true);
+        const at::Tensor& kept = *tensor(o[8], "kept");
+        if (table.dim() != 2) raise(PyExc_ValueError, "table must be int64 [sequences, pages]");
+        const int64_t sequences = table.size(0), heads = cache.c->heads;
+        const Pages pages(table, lengths, sequences);
+        const int64_t new_stride = table_stride(new_table, "new_table", sequences);
+        const Weights w(&weights, "weights", sequences, heads), nw(new_weights, "new_weights", sequences, heads);
+        auto* pl = static_cast<int64_t*>(dense<true>(&new_lengths, "new_lengths", sequences, at::kLong));
+        if (kept.dim() != 3) raise(PyExc_ValueError, "kept must be int64 [sequences, heads, keep]");
+        const int64_t keep = kept.size(2);
+        if (kept.size(0) != sequences || kept.size(1) != heads)
+            raise(PyExc_ValueError, "kept has shape " + shape_text(kept.sizes()) + ", expected " +
+                                        std::to_string(sequences) + " sequences of " + std::to_string(heads) + " heads");
+        auto* pk = static_cast<int64_t*>(dense<false>(&kept, "kept", sequences * heads * keep, at::kLong));
+        const int64_t first = whole(o[10]), recent = whole(o[11]);
+        on_device({&table, &lengths, &weights, &new_table, &new_lengths, new_weights, &kept, cache.held});
+        const nrm_stream_t s = stream_of(o[9]);
+        call("nrm_kv_cache_evict", [&] {
+            return nrm_kv_cache_evict(cache.c, &pages.c, w.ptr, new_table.data_ptr<int64_t>(), new_table.size(1),
+                                      new_stride, pl, nw.ptr, pk, keep, first, recent, s);
+        });
+    });
+}
+
+// Dense tensors of one shape [..., cols] and type.
+struct Rows {
+    int64_t rows, cols;
+    at::ScalarType type;
+    at::IntArrayRef shape;
+    nrm_dtype dt;
+    Rows(const at::Tensor& t, const char* name) : type(t.scalar_type()), shape(t.sizes()), dt(dtype_of(t, name)) {
+        if (t.dim() < 1 || t.size(-1) < 1) raise(PyExc_ValueError, std::string(name) + " must be [..., cols]");
+        cols = t.size(-1);
+        rows = t.numel() / cols;
+    }
+    void* at(const at::Tensor* t, const char* name) const {
+        if (!t) return nullptr;
+        if (t->sizes() != shape)
+            raise(PyExc_ValueError, std::string(name) + " has shape " + shape_text(t->sizes()) + ", expected " +
+                                        shape_text(shape));
+        return dense<false>(t, name, rows * cols, type);
+    }
+    void* param(const at::Tensor* t, const char* name) const { return dense<true>(t, name, cols, type); }
+    // [gates, cols], or [cols] for one gate row
+    void* gate(const at::Tensor* t, const char* name, int64_t* gates) const {
+        *gates = 0;
+        if (!t) return nullptr;
+        if (t->dim() < 1 || t->size(-1) != cols)
+            raise(PyExc_ValueError, std::string(name) + " must be [gates, " + std::to_string(cols) + "], got " +
+                                        shape_text(t->sizes()));
+        *gates = t->numel() / cols;
+        return dense<false>(t, name, t->numel(), type);
+    }
+};
+
+// (x, f, gate, w_post, w_pre, y, h, rstd_post, rstd_pre, alpha, eps, stream, post)
+PyObject* block_norm_fwd(PyObject*, PyObject* const* args, Py_ssize_t given) {
+    return entry(args, given, 13, [](PyObject* const* o) {
+        const at::Tensor &x = *tensor(o[0], "x"), &f = *tensor(o[1], "f"), *gate = tensor(o[2], "gate", true);
+        const int post = PyObject_IsTrue(o[12]);
+        if (post < 0) throw Raised{};
+        const at::Tensor *w1 = post ? tensor(o[3], "w_post", true) : nullptr, &y = *tensor(o[5], "y");
+        const at::Tensor *h = tensor(o[6], "h", true), *w2 = h ? tensor(o[4], "w_pre", true) : nullptr;
+        const at::Tensor* r1 = post ? tensor(o[7], "rstd_post", true) : nullptr;
+        const at::Tensor* r2 = h ? tensor(o[8], "rstd_pre", true) : nullptr;
+        const Rows rows(x, "x");
+        const void *px = rows.at(&x, "x"), *pf = rows.at(&f, "f"), *pw1 = rows.param(w1, "w_post");
+        const void* pw2 = rows.param(w2, "w_pre");
+        int64_t gates;
+        const void* pg = rows.gate(gate, "gate", &gates);
+        void *py = rows.at(&y, "y"), *ph = rows.at(h, "h");
+        auto* p1 = static_cast<float*>(dense<false>(r1, "rstd_post", rows.rows, at::kFloat));
+        auto* p2 = static_cast<float*>(dense<false>(r2, "rstd_pre", rows.rows, at::kFloat));
+        on_device({&x, &f, gate, w1, w2, &y, h, r1, r2});
+        const float alpha = number(o[9]), eps = number(o[10]);
+        const nrm_stream_t s = stream_of(o[11]);
+        call("nrm_block_norm_fwd", [&] {
+            return nrm_block_norm_fwd(px, pf, pg, pw1, pw2, py, ph, p1, p2, rows.rows, rows.cols, gates, alpha, eps, post,
+                                      rows.dt, s);
+        });
+    });
+}
+
+// (dh, dy, f, y, gate, w_post, w_pre, rstd_post, rstd_pre, dx, df, dgate, dw_post, dw_pre, workspace, alpha, stream, post)
+PyObject* block_norm_bwd(PyObject*, PyObject* const* args, Py_ssize_t given) {
+    return entry(args, given, 18, [](PyObject* const* o) {
+        const int post = PyObject_IsTrue(o[17]);
+        if (post < 0) throw Raised{};
+        const at::Tensor *dh = tensor(o[0], "dh", true), *dy = tensor(o[1], "dy", true), &f = *tensor(o[2], "f");
+        const at::Tensor *y = tensor(o[3], "y", !dh), *gate = tensor(o[4], "gate", true);
+        const at::Tensor *w1 = post ? tensor(o[5], "w_post", true) : nullptr, *w2 = dh ? tensor(o[6], "w_pre", true) : nullptr;
+        const at::Tensor* r1 = post ? tensor(o[7], "rstd_post") : nullptr;
+        const at::Tensor* r2 = dh ? tensor(o[8], "rstd_pre") : nullptr;
+        const at::Tensor &dx = *tensor(o[9], "dx"), &df = *tensor(o[10], "df");
+        const at::Tensor *dgate = tensor(o[11], "dgate", true), *dw1 = tensor(o[12], "dw_post", true);
+        const at::Tensor *dw2 = tensor(o[13], "dw_pre", true), *ws = tensor(o[14], "workspace", true);
+        const Rows rows(f, "f");
+        const void *pdh = rows.at(dh, "dh"), *pdy = rows.at(dy, "dy"), *pf = rows.at(&f, "f"), *py = rows.at(y, "y");
+        const void *pw1 = rows.param(w1, "w_post"), *pw2 = rows.param(w2, "w_pre");
+        int64_t gates, dgates;
+        const void* pg = rows.gate(gate, "gate", &gates);
+        void* pdg = rows.gate(dgate, "dgate", &dgates);
+        if (dgate && dgates != gates)
+            raise(PyExc_ValueError, "dgate has " + std::to_string(dgates) + " rows, expected " + std::to_string(gates));
+        void *pdx = rows.at(&dx, "dx"), *pdf = rows.at(&df, "df");
+        void *pdw1 = rows.param(dw1, "dw_post"), *pdw2 = rows.param(dw2, "dw_pre");
+        const auto* p1 = static_cast<const float*>(dense<false>(r1, "rstd_post", rows.rows, at::kFloat));
+        const auto* p2 = static_cast<const float*>(dense<false>(r2, "rstd_pre", rows.rows, at::kFloat));
+        if (ws && !ws->is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+        on_device({dh, dy, &f, y, gate, w1, w2, r1, r2, &dx, &df, dgate, dw1, dw2, ws});
+        const float alpha = number(o[15]);
+        const nrm_stream_t s = stream_of(o[16]);
+        call("nrm_block_norm_bwd", [&] {
+            return nrm_block_norm_bwd(pdh, pdy, pf, py, pg, pw1, pw2, p1, p2, pdx, pdf, pdg, pdw1, pdw2, rows.rows,
+                                      rows.cols, gates, alpha, post, rows.dt, ws ? ws->data_ptr() : nullptr,
+                                      ws ? size_t(ws->nbytes()) : 0, s);
+        });
+    });
+}
+
 // (NrmError)
 PyObject* set_error(PyObject*, PyObject* type) {
     Py_INCREF(type);
@@ -415,6 +615,10 @@ PyMethodDef g_methods[] = {
     method<kv_cache_write>("kv_cache_write"),
     method<kv_cache_read>("kv_cache_read"),
     method<qk_norm_rope_cache>("qk_norm_rope_cache"),
+    method<kv_cache_attention>("kv_cache_attention"),
+    method<kv_cache_evict>("kv_cache_evict"),
+    method<block_norm_fwd>("block_norm_fwd"),
+    method<block_norm_bwd>("block_norm_bwd"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

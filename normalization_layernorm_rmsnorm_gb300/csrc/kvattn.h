@@ -1,0 +1,78 @@
+// kvattn.h -- host-side declarations of the calls that work on whole cached
+// sequences: attention of one new token over the paged cache, and eviction from
+// it by weight; shared by their C ABI (kvattn_api.cu) and the kernel
+// translation units (kvattn_<dtype>.cu, kvevict.cu).
+#pragma once
+
+#include "heads.h"
+
+namespace nrm {
+
+// Sequences of one launch: their tile counts lie in a CTA's shared memory.  A
+// call with more is cut into launches.
+constexpr int kAttnSequences = 1024;
+constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
+constexpr int kAttnWarps = 8;        // warps of a CTA, each a worker of its own
+constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
+
+// The positions of the sequences, cut into tiles: tiles of sequence s, for each
+// of its `pairs` (a head of the cache with a chunk of its query heads), are
+// dealt to the workers in equal contiguous shares.
+struct AttnArgs {
+    HeadView q, out;          // ts: from sequence to sequence
+    CacheDev cache;
+    const int64_t* table;
+    int64_t table_stride;
+    const int64_t* lengths;
+    int sequences;            // of this launch
+    int hq, hk;
+    int shared;               // query heads of a head of the cache: hq / hk
+    int heads;                // query heads of a pair, at most
+    int chunks;               // pairs of a head of the cache
+    int d;
+    int64_t cap;              // positions that a sequence may have
+    int64_t window;           // 0: all
+    float scale_log2;         // scale * log2(e)
+    float* lse;               // [sequences, hq] (nullable)
+    float* weights;           // (nullable)
+    int64_t weight_ts, weight_hs;
+    // workspace
+    int64_t* prefix;          // [sequences + 1] tiles before each sequence
+    float* lse2;              // [sequences, hq], base 2
+    float* part;              // [workers][2] partial results
+    float* logits;            // [sequences, hq, logit_stride], base 2 (with weights)
+    int64_t logit_stride;
+    int workers;
+    int min_tiles;            // of a worker that is used, but for the last
+    unsigned int* err;
+};
+
+// Floats of one partial result: maximum, sum and accumulator of each head.
+__host__ __device__ inline int64_t attn_part_floats(int heads, int d) { return int64_t(heads) * (d + 2); }
+
+// `vec`: the rows' codes are whole aligned vectors of that many bytes (16 or 8)
+// and d and the group are multiples of 16; else 0.
+template <typename T> nrm_status kv_attention(const AttnArgs& a, int vec, cudaStream_t s);
+
+struct EvictArgs {
+    CacheDev cache;
+    const int64_t* table;
+    int64_t table_stride;
+    const int64_t* lengths;
+    const int64_t* new_table;
+    int64_t new_stride;
+    int64_t* new_lengths;
+    const float* weights;
+    int64_t weight_ts, weight_hs;
+    float* new_weights;       // (nullable)
+    int64_t new_ts, new_hs;
+    int64_t* kept;
+    int64_t sequences;
+    int heads, d;
+    int64_t cap;
+    int64_t keep, first, recent;
+    unsigned int* err;
+};
+nrm_status kv_evict(const EvictArgs& a, cudaStream_t s);
+
+}  // namespace nrm
