@@ -26,7 +26,8 @@ SOURCES = ["api.cu", "noalloc.cu", "dropout.cu",
            "rownorm_f32.cu", "rownorm_f16.cu", "rownorm_bf16.cu",
            "batchnorm_f32.cu", "batchnorm_f16.cu", "batchnorm_bf16.cu",
            "heads_api.cu", "heads_f32.cu", "heads_f16.cu", "heads_bf16.cu",
-           "kvattn_api.cu", "kvattn_f32.cu", "kvattn_f16.cu", "kvattn_bf16.cu", "kvevict.cu",
+           *(f"kvattn_{t}_{k}.cu" for t in ("f32", "f16", "bf16") for k in ("e4m3", "int8", "int4")),
+           "kvattn_api.cu", "kvattn.cu", "kvevict.cu",
            "blocknorm_api.cu", "blocknorm_f32.cu", "blocknorm_f16.cu", "blocknorm_bf16.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

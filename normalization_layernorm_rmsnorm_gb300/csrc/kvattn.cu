@@ -1,0 +1,44 @@
+// kvattn.cu -- attention over the cache: the kernel for any layout, the joining of
+// pieces, the weights, and the choice between the kernels.
+#include "kvattn.cuh"
+
+namespace nrm {
+
+template <typename T>
+nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
+    AttnArgs a = args;
+    const DevInfo* dev = dev_info();
+    if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
+    a.err = dev->err;
+    a.workers = dev->sms * kAttnWarps;
+    a.min_tiles = 1;
+    void* p[] = {&a};
+    nrm_status st;
+    if (vec) {
+        a.vec = vec;
+        st = a.cache.kind == NRM_CACHE_E4M3   ? attn_mma<T, NRM_CACHE_E4M3>(a, dev, s)
+             : a.cache.kind == NRM_CACHE_INT8 ? attn_mma<T, NRM_CACHE_INT8>(a, dev, s)
+                                              : attn_mma<T, NRM_CACHE_INT4>(a, dev, s);
+    } else {
+        a.heads = a.shared < kAttnScalarHeads ? a.shared : kAttnScalarHeads;
+        a.chunks = (a.shared + a.heads - 1) / a.heads;
+        st = launch_pdl(reinterpret_cast<const void*>(&attn_scalar_kernel<T>), dim3(unsigned(dev->sms)),
+                        dim3(kAttnThreads), p, s);
+    }
+    if (st != NRM_OK) return st;
+    // sequences of one tile are never cut
+    if (a.cap > kAttnTile && (a.window == 0 || a.window > kAttnTile)) {
+        st = launch_pdl(reinterpret_cast<const void*>(&attn_join_kernel<T>), dim3(unsigned(a.sequences * a.hq)),
+                        dim3(kAttnThreads), p, s);
+        if (st != NRM_OK) return st;
+    }
+    if (!a.weights) return NRM_OK;
+    return launch_pdl(reinterpret_cast<const void*>(&attn_weights_kernel<T>), dim3(unsigned(dev->sms)),
+                      dim3(kAttnThreads), p, s);
+}
+
+template nrm_status kv_attention<float>(const AttnArgs&, int, cudaStream_t);
+template nrm_status kv_attention<__half>(const AttnArgs&, int, cudaStream_t);
+template nrm_status kv_attention<__nv_bfloat16>(const AttnArgs&, int, cudaStream_t);
+
+}  // namespace nrm

@@ -266,20 +266,20 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
             if (h >= p.heads) break;
             const float scale = p.whole ? (sum[h] == 0.f ? 0.f : 1.f / sum[h]) : 1.f;
             bits* row = static_cast<bits*>(a.out.p) + p.s * a.out.ts + (p.q0 + h) * a.out.hs;
-            float* part = a.part + p.part + int64_t(h) * (a.d + 2);
+            float* part = a.part + p.part + h * attn_part_row(a.d);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int i = lane + 32 * e;
                 if (i >= a.d) break;
                 if (p.whole) row[i] = Io<T>::store(acc[h][e] * scale);
-                else part[2 + i] = acc[h][e];
+                else part[i] = acc[h][e];
             }
             if (lane == 0) {
                 if (p.whole) {
                     attn_write_lse(a, p.s, p.q0 + h, m[h], sum[h]);
                 } else {
-                    part[0] = m[h];
-                    part[1] = sum[h];
+                    part[a.d] = m[h];
+                    part[a.d + 1] = sum[h];
                 }
             }
         }
@@ -308,11 +308,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(const AttnArgs 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the first worker's piece is the beginning of its last pair, the others' the end of their first
     auto part = [&](int64_t w) {
-        return a.part + (w * 2 + (w == w0)) * attn_part_floats(a.heads, a.d) + int64_t(h) * (a.d + 2);
+        return a.part + (w * 2 + (w == w0)) * attn_part_floats(a.heads, a.d) + h * attn_part_row(a.d);
     };
     float top = -INFINITY;
     for (int64_t w = w0 + lane; w <= w1; w += 32) {
-        const float m = ld_after(part(w));
+        const float m = ld_after(part(w) + a.d);
         top = fmaxf(top, m);
     }
 #pragma unroll
@@ -321,11 +321,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(const AttnArgs 
     float acc[E] = {}, sum = 0.f;
     for (int64_t w = w0 + warp; w <= w1; w += kAttnWarps) {
         const float* from = part(w);
-        const float f = exp2_approx(ld_after(from) - base);
-        sum = fmaf(ld_after(from + 1), f, sum);
+        const float f = exp2_approx(ld_after(from + a.d) - base);
+        sum = fmaf(ld_after(from + a.d + 1), f, sum);
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            if (lane + 32 * e < a.d) acc[e] = fmaf(ld_after(from + 2 + lane + 32 * e), f, acc[e]);
+            if (lane + 32 * e < a.d) acc[e] = fmaf(ld_after(from + lane + 32 * e), f, acc[e]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -381,35 +381,6 @@ __global__ void __launch_bounds__(kAttnThreads) attn_weights_kernel(const AttnAr
         }
         t += tile1 - tile0;
     }
-}
-
-// ---------------------------------------------------------------------------
-// launches
-// ---------------------------------------------------------------------------
-template <typename T>
-nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
-    AttnArgs a = args;
-    const DevInfo* dev = dev_info();
-    if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
-    a.err = dev->err;
-    (void)vec;
-    a.heads = a.shared < kAttnScalarHeads ? a.shared : kAttnScalarHeads;
-    a.chunks = (a.shared + a.heads - 1) / a.heads;
-    a.workers = dev->sms * kAttnWarps;
-    a.min_tiles = 1;
-    void* p[] = {&a};
-    nrm_status st = launch_pdl(reinterpret_cast<const void*>(&attn_scalar_kernel<T>), dim3(unsigned(dev->sms)),
-                               dim3(kAttnThreads), p, s);
-    if (st != NRM_OK) return st;
-    // sequences of one tile are never cut
-    if (a.cap > kAttnTile && (a.window == 0 || a.window > kAttnTile)) {
-        st = launch_pdl(reinterpret_cast<const void*>(&attn_join_kernel<T>), dim3(unsigned(a.sequences * a.hq)),
-                        dim3(kAttnThreads), p, s);
-        if (st != NRM_OK) return st;
-    }
-    if (!a.weights) return NRM_OK;
-    return launch_pdl(reinterpret_cast<const void*>(&attn_weights_kernel<T>), dim3(unsigned(dev->sms)),
-                      dim3(kAttnThreads), p, s);
 }
 
 }  // namespace nrm

@@ -44,15 +44,22 @@ struct AttnArgs {
     int64_t logit_stride;
     int workers;
     int min_tiles;            // of a worker that is used, but for the last
+    // on matrix instructions
+    int row_bytes, vec;       // of a row of codes, copied in vectors of 16 or 8 bytes
+    int k_pitch, v_pitch;     // of a row in shared memory
+    int q_vec, out_vec;       // queries and outputs are aligned to 16 bytes
     unsigned int* err;
 };
 
-// Floats of one partial result: maximum, sum and accumulator of each head.
-__host__ __device__ inline int64_t attn_part_floats(int heads, int d) { return int64_t(heads) * (d + 2); }
+// Floats of one partial result: accumulator, maximum and sum of each head, in whole 16 bytes.
+__host__ __device__ inline int64_t attn_part_row(int d) { return (int64_t(d) + 2 + 3) / 4 * 4; }
+__host__ __device__ inline int64_t attn_part_floats(int heads, int d) { return heads * attn_part_row(d); }
 
 // `vec`: the rows' codes are whole aligned vectors of that many bytes (16 or 8)
 // and d and the group are multiples of 16; else 0.
 template <typename T> nrm_status kv_attention(const AttnArgs& a, int vec, cudaStream_t s);
+// The part of it on matrix instructions (sets a's pairs), for one stored form.
+template <typename T, int KIND> nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s);
 
 struct EvictArgs {
     CacheDev cache;

@@ -153,6 +153,12 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
                     (cache->heads == 1 || cache->head_stride % b == 0))
                     vec = int(b);
         const int64_t es = int64_t(dsize(dt));
+        auto whole = [&](const nrm_heads* v) {
+            return aligned(v->data, 16) && (sequences == 1 || v->token_stride * es % 16 == 0) &&
+                   (v->heads == 1 || v->head_stride * es % 16 == 0);
+        };
+        a.q_vec = whole(q);
+        a.out_vec = whole(out);
         for (int64_t s0 = 0; s0 < sequences; s0 += kAttnSequences) {
             AttnArgs b = a;
             b.sequences = int(sequences - s0 < kAttnSequences ? sequences - s0 : kAttnSequences);

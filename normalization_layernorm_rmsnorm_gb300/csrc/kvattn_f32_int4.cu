@@ -1,0 +1,3 @@
+// kvattn_f32_int4.cu -- attention over the cache on matrix instructions, float queries, codes in int4
+#include "kvattn_mma.cuh"
+template nrm_status nrm::attn_mma<float, NRM_CACHE_INT4>(nrm::AttnArgs&, const nrm::DevInfo*, cudaStream_t);

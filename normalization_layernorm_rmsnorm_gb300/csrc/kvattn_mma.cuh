@@ -1,0 +1,586 @@
+// kvattn_mma.cuh -- the attention over the cache on matrix instructions.
+//
+// Both products are m16n8k16 with fp16 factors and fp32 sums, the query heads of
+// a pair as the eight columns: logits = codes of 16 keys [16 x d] * queries [d x
+// 8], and out^T = codes of 16 values [d x 16] * weights [16 x 8].  A code is
+// exact in fp16 in every stored form; the keys' scales multiply the logits, the
+// values' the weights.  Queries are scaled by a power of two to at most 2^15:
+// those of 16 bits then are exact, of float32 ones the rest is a second factor
+// (22 bits).  A weight p <= 1 times its value's scale, with the largest scale seen
+// brought to 2^14, keeps 11 bits down to 2^-28 of that; where the output has
+// them (fp16, float32), the rest is a second factor too.  The order of the d
+// elements in a product is free, so a lane takes its keys' elements as they lie
+// in 8 (or 4) neighbours, and its values' in 4 (or 2).
+//
+// The column's heads are the lanes' pairs in both results, so the running
+// maximum, the rescaling and the sum need nothing from other lanes but the
+// maximum over the 16 positions; the weights change from rows to columns by a
+// transposing exchange of 8x8 matrices.
+//
+// Codes and scales are copied asynchronously into the warp's own ring in shared
+// memory, 16 positions to a stage; warps share nothing and the loop holds no
+// barrier of the CTA.  The row of a page is found by the lane of its position, a
+// tile ahead.  Rows are padded so that the fragments' reads have no conflicts.
+#pragma once
+
+#include "kvattn.cuh"
+
+namespace nrm {
+
+// n bytes, and zeros for the rest.
+__device__ __forceinline__ void cp_async_8_or_0(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_4_or_0(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transposes an 8x8 matrix of 16-bit elements spread over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// Shared memory at byte `at` of the CTA's ring.
+template <typename R>
+__device__ __forceinline__ R& in_ring(uint32_t at) {
+    extern __shared__ __align__(128) unsigned char attn_ring[];
+    return *reinterpret_cast<R*>(attn_ring + at);
+}
+template <int BYTES>
+__device__ __forceinline__ uint32_t lds(uint32_t at) {
+    if constexpr (BYTES == 4) return in_ring<const uint32_t>(at);
+    else if constexpr (BYTES == 2) return in_ring<const uint16_t>(at);
+    else return in_ring<const uint8_t>(at);
+}
+
+// Codes as pairs of fp16.
+__device__ __forceinline__ uint32_t add_half2(uint32_t v, uint32_t bias) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(bias));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_halves(uint32_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(v)));
+    return h;
+}
+// Four 8-bit codes: bytes (0, 1) and (2, 3).  int8: the byte above 1024 in fp16, taken off again.
+template <int KIND>
+__device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    if constexpr (KIND == NRM_CACHE_E4M3) {
+        lo = e4m3x2_halves(v);
+        hi = e4m3x2_halves(v >> 16);
+    } else {
+        v ^= 0x80808080u;
+        lo = add_half2(__byte_perm(v, 0x64646464u, 0x4140), 0xe480e480u);  // - 1152
+        hi = add_half2(__byte_perm(v, 0x64646464u, 0x4342), 0xe480e480u);
+    }
+}
+// The 4-bit codes at the low ends of both halves (already turned by 8).
+__device__ __forceinline__ uint32_t codes4(uint32_t v) {
+    return add_half2((v & 0x000f000fu) | 0x64006400u, 0xe408e408u);  // - 1032
+}
+
+// What a kernel is made for: the stored form, elements of a unit of a row (every group is whole units of 32, or of
+// 16), the longest rows, and eights of heads.
+template <int KIND_, int UNIT_, int DMAX_, int NT_>
+struct AttnForm {
+    static constexpr int KIND = KIND_, UNIT = UNIT_, DMAX = DMAX_, NT = NT_;
+    static constexpr int UNITS = DMAX / UNIT, STEPS = UNIT / 16, TILES = UNIT / 16;
+    static constexpr int KP = UNIT / 4, VP = UNIT / 8;  // elements of a lane's piece of a unit
+    static constexpr int BITS = KIND == NRM_CACHE_INT4 ? 4 : 8;
+    // stages of 16 positions that fit beside one another (at most 6: the copies run less than 3 tiles ahead)
+    static constexpr int STAGES = DMAX == 128 ? (BITS == 4 ? 6 : 5) : (BITS == 4 ? 5 : 3);
+};
+
+// A warp's shared memory: stages (keys, values, scales of both), then for two tiles the rows' places.
+struct AttnSmem {
+    uint32_t stage, bytes;     // of the first stage; of one
+    uint32_t places;           // [2][32] code offsets, [2][32] scale offsets, then which positions of 4 tiles are there
+};
+__host__ __device__ inline uint32_t attn_stage_bytes(int k_pitch, int v_pitch, int groups) {
+    return uint32_t(16 * (k_pitch + v_pitch) + 2 * 16 * groups * 4 + 15) / 16 * 16;
+}
+constexpr uint32_t kAttnPlaces = 2 * 32 * 8 * 2 + 16;
+
+template <typename T, typename F>
+__device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiece& p, const AttnSmem& sm, int groups) {
+    using bits = typename Io<T>::bits_t;
+    constexpr int NT = F::NT, QT = sizeof(T) == 4 ? 2 : 1, WT = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
+    constexpr int KSTEPS = F::DMAX / 16, S = F::STAGES;
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
+    const int units = a.d / F::UNIT, group_units = a.cache.group / F::UNIT;
+
+    // ---- the copies: 16 positions to a stage ----
+    const int64_t j0 = p.lo + p.tile0 * kAttnTile;
+    const int64_t positions = min(p.n, p.lo + p.tile1 * kAttnTile) - j0;
+    const int subs = int((positions + 15) / 16);
+    const int chunks = a.row_bytes / a.vec, copies = 16 * chunks;
+    const int row_step = 32 / chunks, chunk_step = 32 - row_step * chunks;
+    const int first_row = lane / chunks, first_chunk = lane - first_row * chunks;
+    const uint32_t v_at = 16 * a.k_pitch, s_at = v_at + 16 * a.v_pitch;
+    const int64_t pages = a.cache.slots / a.cache.page.d;
+    const uint32_t ring = smem_addr(&in_ring<unsigned char>(0));
+    int64_t page = 0, in_page = 0;
+    auto look_up = [&](int tile) {  // this lane's position of a tile (in_page -1: there is none)
+        const int64_t j = j0 + int64_t(tile) * kAttnTile + lane;
+        in_page = -1;
+        if (j - j0 < positions) {
+            const int64_t entry = row_div(j, a.cache.page);
+            in_page = j - entry * a.cache.page.d;
+            page = ld_after(a.table + p.s * a.table_stride + entry);
+        }
+    };
+    auto issue = [&](int sub) {
+        const int tile = sub >> 1, odd = tile & 1, half = sub & 1;
+        const uint32_t code_places = sm.places + odd * 256, scale_places = sm.places + 512 + odd * 256;
+        if (half == 0) {
+            const bool ok = in_page >= 0 && page >= 0 && page < pages;
+            if (in_page >= 0 && !ok) atomicOr(a.err, kErrCacheSlot);
+            const uint32_t m = __ballot_sync(0xffffffffu, ok);
+            CacheRow r{0, 0};
+            if (ok) r = cache_row(a.cache, page * a.cache.page.d + in_page, p.head);
+            in_ring<int64_t>(code_places + lane * 8) = r.code;
+            in_ring<int64_t>(scale_places + lane * 8) = r.scale;
+            if (lane == 0) in_ring<uint32_t>(sm.places + 1024 + (tile & 3) * 4) = m;
+            __syncwarp();
+            look_up(tile + 1);
+        }
+        const uint32_t there = in_ring<const uint32_t>(sm.places + 1024 + (tile & 3) * 4) >> (16 * half);
+        const uint32_t to = ring + sm.stage + uint32_t(sub % S) * sm.bytes;
+        int row = first_row, chunk = first_chunk;
+        for (int i = lane; i < copies; i += 32) {
+            const int64_t at = in_ring<const int64_t>(code_places + (16 * half + row) * 8) + chunk * a.vec;
+            const int n = there >> row & 1 ? a.vec : 0;
+            const uint32_t k = to + row * a.k_pitch + chunk * a.vec, v = to + v_at + row * a.v_pitch + chunk * a.vec;
+            if (a.vec == 16) {
+                cp_async_16_or_0(k, a.cache.codes[0] + at, n);
+                cp_async_16_or_0(v, a.cache.codes[1] + at, n);
+            } else {
+                cp_async_8_or_0(k, a.cache.codes[0] + at, n);
+                cp_async_8_or_0(v, a.cache.codes[1] + at, n);
+            }
+            row += row_step;
+            chunk += chunk_step;
+            if (chunk >= chunks) {
+                chunk -= chunks;
+                ++row;
+            }
+        }
+        // scales: keys' by the lower half of the warp, values' by the upper, [group][position]
+        const int sr = lane & 15, which = lane >> 4;
+        const float* from = a.cache.scales[which] + in_ring<const int64_t>(scale_places + (16 * half + sr) * 8);
+        const int n = there >> sr & 1 ? 4 : 0;
+        for (int g = 0; g < groups; ++g) cp_async_4_or_0(to + s_at + ((which * groups + g) * 16 + sr) * 4, from + g, n);
+    };
+    look_up(0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (i < subs) issue(i);
+        cp_async_commit();
+    }
+
+    // ---- the queries, while the first copies are under way ----
+    uint32_t q[KSTEPS][NT][QT][2];
+    float factor[NT][2];  // of the logits of this lane's two heads
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int h = nt * 8 + gid;
+        const bits* row = static_cast<const bits*>(a.q.p) + p.s * a.q.ts + (p.q0 + h) * a.q.hs;
+        float x[F::UNITS][F::KP], most = 0.f;
+#pragma unroll
+        for (int u = 0; u < F::UNITS; ++u) {
+            const int at = u * F::UNIT + tid * F::KP;
+            const bool there = h < p.heads && u < units;
+            if (there && a.q_vec) {
+                constexpr int B = F::KP * int(sizeof(T));  // 8, 16 or 32 bytes
+                uint32_t w[B / 4];
+#pragma unroll
+                for (int b = 0; b < B; b += 16) {
+                    if constexpr (B >= 16) {
+                        const uint4 v = ld_after(reinterpret_cast<const uint4*>(row + at) + b / 16);
+                        w[b / 4] = v.x, w[b / 4 + 1] = v.y, w[b / 4 + 2] = v.z, w[b / 4 + 3] = v.w;
+                    } else {
+                        const uint2 v = ld_after(reinterpret_cast<const uint2*>(row + at));
+                        w[0] = v.x, w[1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < F::KP; ++i)
+                    x[u][i] = sizeof(T) == 4 ? __uint_as_float(w[i % (B / 4)])
+                                             : Io<T>::load(typename Io<T>::bits_t(w[i / 2 % (B / 4)] >> (16 * (i & 1))));
+            } else {
+#pragma unroll
+                for (int i = 0; i < F::KP; ++i) x[u][i] = there ? Io<T>::load(ld_after(row + at + i)) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < F::KP; ++i) most = fmaxf(most, fabsf(x[u][i]));
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // 2^e > most (an infinity or a row of tiny numbers stays what it is, nearly)
+        const int e = max(-100, min(127, int(__float_as_uint(most) >> 23) - 126));
+        const float up = __uint_as_float(uint32_t(127 + 15 - e) << 23);
+        const float down = __uint_as_float(uint32_t(127 + e) << 23) * 0x1p-15f * a.scale_log2;
+        factor[nt][0] = __shfl_sync(0xffffffffu, down, tid * 8);
+        factor[nt][1] = __shfl_sync(0xffffffffu, down, tid * 8 + 4);
+#pragma unroll
+        for (int ks = 0; ks < KSTEPS; ++ks) {
+            const int u = ks / F::STEPS, part = ks % F::STEPS;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                // the elements that a fragment of codes pairs
+                const int i0 = F::BITS == 8 ? part * 4 + b * 2 : part * 2 + b;
+                const int i1 = F::BITS == 8 ? i0 + 1 : i0 + F::KP / 2;
+                const float lo = x[u][i0] * up, hi = x[u][i1] * up;
+                q[ks][nt][0][b] = half2_bits(lo, hi);
+                if constexpr (QT == 2) {
+                    const float2 r = half2_floats(q[ks][nt][0][b]);
+                    q[ks][nt][QT - 1][b] = half2_bits(lo - r.x, hi - r.y);
+                }
+            }
+        }
+    }
+
+    // ---- the running softmax ----
+    float acc[F::UNITS][F::TILES][NT][4], m[NT][2], sum[NT][2];
+    int top[F::UNITS];  // the values' largest scale so far is at most 2^top
+#pragma unroll
+    for (int u = 0; u < F::UNITS; ++u) {
+        top[u] = -1000;
+#pragma unroll
+        for (int t = 0; t < F::TILES; ++t)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[u][t][nt][i] = 0.f;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, sum[nt][0] = sum[nt][1] = 0.f;
+
+    for (int sub = 0; sub < subs; ++sub) {
+        if (sub + S - 1 < subs) issue(sub + S - 1);
+        cp_async_commit();
+        cp_async_wait<S - 1>();
+        __syncwarp();
+        const uint32_t there = in_ring<const uint32_t>(sm.places + 1024 + (sub >> 1 & 3) * 4) >> (16 * (sub & 1));
+        const uint32_t at = sm.stage + uint32_t(sub % S) * sm.bytes;
+        const uint32_t k_at = at + gid * a.k_pitch + tid * (F::KP * F::BITS / 8);
+        const uint32_t scales = at + s_at + gid * 4;
+
+        // logits of positions gid and gid + 8
+        float l[NT][4], c[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[nt][i] = c[nt][i] = 0.f;
+        int left = group_units, g = 0;
+#pragma unroll
+        for (int u = 0; u < F::UNITS; ++u) {
+            if (u >= units) break;
+            uint32_t f[F::STEPS][4];
+            const uint32_t from = k_at + u * (F::UNIT * F::BITS / 8);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t row = from + r * 8 * a.k_pitch;
+                if constexpr (F::BITS == 8 && F::STEPS == 2) {
+                    const uint2 w = in_ring<const uint2>(row);
+                    codes8<F::KIND>(w.x, f[0][r], f[0][2 + r]);
+                    codes8<F::KIND>(w.y, f[F::STEPS - 1][r], f[F::STEPS - 1][2 + r]);
+                } else if constexpr (F::BITS == 8) {
+                    codes8<F::KIND>(lds<4>(row), f[0][r], f[0][2 + r]);
+                } else if constexpr (F::STEPS == 2) {
+                    const uint32_t w = lds<4>(row) ^ 0x88888888u;  // elements (0, 4), (1, 5), (2, 6), (3, 7)
+                    f[0][r] = codes4(w);
+                    f[0][2 + r] = codes4(w >> 4);
+                    f[F::STEPS - 1][r] = codes4(w >> 8);
+                    f[F::STEPS - 1][2 + r] = codes4(w >> 12);
+                } else {
+                    uint32_t w = lds<2>(row) ^ 0x8888u;  // elements (0, 2), (1, 3)
+                    w |= w << 8;
+                    f[0][r] = codes4(w);
+                    f[0][2 + r] = codes4(w >> 4);
+                }
+            }
+#pragma unroll
+            for (int st = 0; st < F::STEPS; ++st)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int t = 0; t < QT; ++t)
+                        mma16816(c[nt], f[st], q[u * F::STEPS + st][nt][t][0], q[u * F::STEPS + st][nt][t][1]);
+            if (--left == 0) {
+                const float s0 = in_ring<const float>(scales + g * 64), s1 = in_ring<const float>(scales + g * 64 + 32);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    l[nt][0] = fmaf(c[nt][0], s0, l[nt][0]);
+                    l[nt][1] = fmaf(c[nt][1], s0, l[nt][1]);
+                    l[nt][2] = fmaf(c[nt][2], s1, l[nt][2]);
+                    l[nt][3] = fmaf(c[nt][3], s1, l[nt][3]);
+                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+                }
+                left = group_units;
+                ++g;
+            }
+        }
+        const bool ok0 = there >> gid & 1, ok1 = there >> (gid + 8) & 1;
+        float grow[NT][2];
+        bool grows = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[nt][i] = ok0 ? l[nt][i] * factor[nt][i] : -INFINITY;
+                l[nt][2 + i] = ok1 ? l[nt][2 + i] * factor[nt][i] : -INFINITY;
+            }
+            if (a.logits) {
+                const int64_t j = j0 + int64_t(sub) * 16 + gid;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int h = nt * 8 + tid * 2 + (i & 1);
+                    const int64_t at_j = j + (i >> 1) * 8;
+                    if (h < p.heads && at_j - j0 < positions)
+                        a.logits[(int64_t(p.s) * a.hq + p.q0 + h) * a.logit_stride + at_j] = l[nt][i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float most = fmaxf(l[nt][i], l[nt][2 + i]);
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
+                most = fmaxf(m[nt][i], most);
+                const float base = finite_max(most);
+                grow[nt][i] = exp2_approx(m[nt][i] - base);
+                grows |= most > m[nt][i];
+                m[nt][i] = most;
+                l[nt][i] = exp2_approx(l[nt][i] - base);
+                l[nt][2 + i] = exp2_approx(l[nt][2 + i] - base);
+                sum[nt][i] = fmaf(sum[nt][i], grow[nt][i], l[nt][i] + l[nt][2 + i]);
+            }
+        }
+        if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+            for (int u = 0; u < F::UNITS; ++u)
+#pragma unroll
+                for (int t = 0; t < F::TILES; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[u][t][nt][i] *= grow[nt][i & 1];
+        }
+
+        // the values, a group's weights after another
+        const uint32_t v_from = at + v_at + tid * 2 * a.v_pitch + gid * F::VP * F::BITS / 8;
+        uint32_t w[NT][WT][2];
+        left = 0;
+        g = 0;
+        float raise = 1.f;
+        int now = 0;
+#pragma unroll
+        for (int u = 0; u < F::UNITS; ++u) {
+            if (u >= units) break;
+            if (left == 0) {
+                const uint32_t of_group = scales + (groups + g) * 64;
+                const float s0 = in_ring<const float>(of_group), s1 = in_ring<const float>(of_group + 32);
+                const uint32_t b0 = __float_as_uint(s0), b1 = __float_as_uint(s1);
+                const uint32_t most = __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
+                now = max(top[u], most == 0u ? -1000 : max(int(most >> 23), 1) - 126);
+                raise = now > top[u] && top[u] > -1000 ? exp2f(float(top[u] - now)) : 1.f;
+                // in two steps: the power itself may be none of float32's
+                const int up = now == -1000 ? 0 : 14 - now, half_up = up / 2;
+                const float up0 = __uint_as_float(uint32_t(127 + half_up) << 23);
+                const float up1 = __uint_as_float(uint32_t(127 + up - half_up) << 23);
+                const float t0 = s0 * up0 * up1, t1 = s1 * up0 * up1;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float x[4] = {l[nt][0] * t0, l[nt][1] * t0, l[nt][2] * t1, l[nt][3] * t1};
+                    uint32_t lo = half2_bits(x[0], x[1]), hi = half2_bits(x[2], x[3]);
+                    w[nt][0][0] = transpose8(lo);
+                    w[nt][0][1] = transpose8(hi);
+                    if constexpr (WT == 2) {
+                        const float2 r0 = half2_floats(lo), r1 = half2_floats(hi);
+                        w[nt][WT - 1][0] = transpose8(half2_bits(x[0] - r0.x, x[1] - r0.y));
+                        w[nt][WT - 1][1] = transpose8(half2_bits(x[2] - r1.x, x[3] - r1.y));
+                    }
+                }
+                left = group_units;
+                ++g;
+            }
+            --left;
+            top[u] = now;
+            if (raise != 1.f) {
+#pragma unroll
+                for (int t = 0; t < F::TILES; ++t)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[u][t][nt][i] *= raise;
+            }
+            // elements of this lane's piece as pairs of positions (2 tid, 2 tid + 1) and 8 further
+            uint32_t f[F::TILES][4];
+            const uint32_t from = v_from + u * (F::UNIT * F::BITS / 8);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t row = from + r * 8 * a.v_pitch;
+                const uint32_t x = lds<F::VP * F::BITS / 8>(row), y = lds<F::VP * F::BITS / 8>(row + a.v_pitch);
+                if constexpr (F::BITS == 8 && F::TILES == 2) {
+                    codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
+                    codes8<F::KIND>(__byte_perm(x, y, 0x7362), f[F::TILES - 1][2 * r], f[F::TILES - 1][2 * r + 1]);
+                } else if constexpr (F::BITS == 8) {
+                    codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
+                } else if constexpr (F::TILES == 2) {
+                    const uint32_t b = (x | y << 16) ^ 0x88888888u;
+                    f[0][2 * r] = codes4(b);
+                    f[0][2 * r + 1] = codes4(b >> 4);
+                    f[F::TILES - 1][2 * r] = codes4(b >> 8);
+                    f[F::TILES - 1][2 * r + 1] = codes4(b >> 12);
+                } else {
+                    const uint32_t b = (x | y << 16) ^ 0x00880088u;
+                    f[0][2 * r] = codes4(b);
+                    f[0][2 * r + 1] = codes4(b >> 4);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < F::TILES; ++t)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < WT; ++k) mma16816(acc[u][t][nt], f[t], w[nt][k][0], w[nt][k][1]);
+        }
+        __syncwarp();
+    }
+
+    // ---- what the piece comes to ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float s = sum[nt][i];
+            s += __shfl_xor_sync(0xffffffffu, s, 4);
+            s += __shfl_xor_sync(0xffffffffu, s, 8);
+            s += __shfl_xor_sync(0xffffffffu, s, 16);
+            const int h = nt * 8 + tid * 2 + i;
+            if (h >= p.heads) continue;
+            const float scale = p.whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f;
+            bits* row = static_cast<bits*>(a.out.p) + p.s * a.out.ts + (p.q0 + h) * a.out.hs;
+            float* part = a.part + p.part + h * attn_part_row(a.d);
+#pragma unroll
+            for (int u = 0; u < F::UNITS; ++u) {
+                if (u >= units) break;
+                const int down = top[u] == -1000 ? 0 : top[u] - 14, half_down = down / 2;
+                const float d0 = __uint_as_float(uint32_t(127 + half_down) << 23) * scale;
+                const float d1 = __uint_as_float(uint32_t(127 + down - half_down) << 23);
+                const int at = u * F::UNIT + gid * F::VP;
+                float v[F::VP];
+#pragma unroll
+                for (int t = 0; t < F::TILES; ++t) {
+                    v[2 * t] = acc[u][t][nt][i] * d0 * d1;
+                    v[2 * t + 1] = acc[u][t][nt][2 + i] * d0 * d1;
+                }
+                if (!p.whole) {
+                    if constexpr (F::VP == 4) *reinterpret_cast<float4*>(part + at) = make_float4(v[0], v[1], v[F::VP - 2], v[F::VP - 1]);
+                    else *reinterpret_cast<float2*>(part + at) = make_float2(v[0], v[1]);
+                } else if (a.out_vec) {
+                    if constexpr (sizeof(T) == 4) {
+                        if constexpr (F::VP == 4)
+                            *reinterpret_cast<float4*>(row + at) = make_float4(v[0], v[1], v[F::VP - 2], v[F::VP - 1]);
+                        else *reinterpret_cast<float2*>(row + at) = make_float2(v[0], v[1]);
+                    } else {
+                        uint32_t w0 = pack2<T>(make_float2(v[0], v[1]));
+                        if constexpr (F::VP == 4)
+                            *reinterpret_cast<uint2*>(row + at) =
+                                make_uint2(w0, pack2<T>(make_float2(v[F::VP - 2], v[F::VP - 1])));
+                        else *reinterpret_cast<uint32_t*>(row + at) = w0;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < F::VP; ++k) row[at + k] = Io<T>::store(v[k]);
+                }
+            }
+            if (gid == 0) {
+                if (p.whole) {
+                    attn_write_lse(a, p.s, p.q0 + h, m[nt][i], s);
+                } else {
+                    part[a.d] = m[nt][i];
+                    part[a.d + 1] = s;
+                }
+            }
+        }
+    cp_async_wait<0>();
+    __syncwarp();
+}
+
+template <typename T, typename F>
+__global__ void __launch_bounds__(kAttnThreads, 1) attn_mma_kernel(const AttnArgs a) {
+    __shared__ int64_t pre[kAttnSequences + 1], sums[kAttnWarps];
+    pdl_next();
+    attn_prefix(a, pre, sums);
+    if (blockIdx.x == 0)
+        for (int s = int(threadIdx.x); s <= a.sequences; s += kAttnThreads) a.prefix[s] = pre[s];
+    attn_empty<T>(a, pre);
+    const int groups = a.d / a.cache.group, warp = threadIdx.x >> 5;
+    AttnSmem sm;
+    sm.bytes = attn_stage_bytes(a.k_pitch, a.v_pitch, groups);
+    sm.stage = uint32_t(warp) * (F::STAGES * sm.bytes + kAttnPlaces);
+    sm.places = sm.stage + F::STAGES * sm.bytes;
+    if (warp >= a.workers / int(gridDim.x)) return;
+    attn_pieces(a, pre, int64_t(warp) * gridDim.x + blockIdx.x,
+                [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
+}
+
+template <typename T, typename F>
+nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
+    const void* fn = reinterpret_cast<const void*>(&attn_mma_kernel<T, F>);
+    const size_t warp = F::STAGES * attn_stage_bytes(a.k_pitch, a.v_pitch, a.d / a.cache.group) + kAttnPlaces;
+    // as many workers to an SM as have room for their rings beside the lengths (rows of 256 bytes: 7; 16 scales: 6)
+    const size_t room = size_t(dev->max_smem_optin) - (kAttnSequences + 1 + kAttnWarps) * 8 - 64;
+    const int warps = int(std::min<size_t>(kAttnWarps, room / warp));
+    a.workers = dev->sms * warps;
+    const size_t smem = warps * warp;
+    nrm_status st = prepare_kernel(fn, smem, false);
+    if (st != NRM_OK) return st;
+    void* p[] = {&a};
+    return launch_pdl(fn, dim3(unsigned(dev->sms)), dim3(kAttnThreads), p, s, smem);
+}
+
+// One translation unit for each storage type and stored form.
+template <typename T, int KIND>
+nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
+    const bool wide = a.d % 32 == 0 && a.cache.group % 32 == 0;
+    a.row_bytes = KIND == NRM_CACHE_INT4 ? a.d / 2 : a.d;
+    // rows 32 bytes (8 bits: a key's fragment is 8 bytes a lane, 4 rows at a time) or 16 bytes (else) off a multiple of
+    // 64 or 32 apart: the fragments' reads then meet no bank twice
+    const int k_unit = KIND != NRM_CACHE_INT4 && wide ? 32 : 16;
+    a.k_pitch = (a.row_bytes + k_unit - 1) / k_unit * k_unit;
+    if (a.k_pitch / k_unit % 2 == 0) a.k_pitch += k_unit;
+    a.v_pitch = (a.row_bytes + 15) / 16 * 16;
+    if (a.v_pitch / 16 % 2 == 0) a.v_pitch += 16;
+    const int nt = a.d <= 128 && a.shared > 8 ? 2 : 1;
+    a.heads = a.shared < 8 * nt ? a.shared : 8 * nt;
+    a.chunks = (a.shared + a.heads - 1) / a.heads;
+    if (a.d > 128)
+        return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 256, 1>>(a, dev, s)
+                    : attn_mma_launch<T, AttnForm<KIND, 16, 256, 1>>(a, dev, s);
+    if (nt == 2)
+        return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 128, 2>>(a, dev, s)
+                    : attn_mma_launch<T, AttnForm<KIND, 16, 128, 2>>(a, dev, s);
+    return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 128, 1>>(a, dev, s)
+                : attn_mma_launch<T, AttnForm<KIND, 16, 128, 1>>(a, dev, s);
+}
+
+}  // namespace nrm
