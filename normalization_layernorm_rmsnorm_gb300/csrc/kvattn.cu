@@ -10,7 +10,6 @@ nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
     const DevInfo* dev = dev_info();
     if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
     a.err = dev->err;
-    a.workers = dev->sms * kAttnWarps;
     a.min_tiles = 1;
     void* p[] = {&a};
     nrm_status st;
@@ -20,20 +19,22 @@ nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
              : a.cache.kind == NRM_CACHE_INT8 ? attn_mma<T, NRM_CACHE_INT8>(a, dev, s)
                                               : attn_mma<T, NRM_CACHE_INT4>(a, dev, s);
     } else {
-        a.heads = a.shared < kAttnScalarHeads ? a.shared : kAttnScalarHeads;
-        a.chunks = (a.shared + a.heads - 1) / a.heads;
+        attn_chunks(a, kAttnScalarHeads);
+        a.workers = dev->sms * (kAttnThreads / 32);
         st = launch_pdl(reinterpret_cast<const void*>(&attn_scalar_kernel<T>), dim3(unsigned(dev->sms)),
                         dim3(kAttnThreads), p, s);
     }
     if (st != NRM_OK) return st;
     // sequences of one tile are never cut
     if (a.cap > kAttnTile && (a.window == 0 || a.window > kAttnTile)) {
-        st = launch_pdl(reinterpret_cast<const void*>(&attn_join_kernel<T>), dim3(unsigned(a.sequences * a.hq)),
-                        dim3(kAttnThreads), p, s);
+        // a CTA for each head where there are too few pairs to fill the GPU
+        const int pairs = a.sequences * a.hk * a.chunks;
+        st = launch_pdl(reinterpret_cast<const void*>(&attn_join_kernel<T>),
+                        dim3(unsigned(pairs), pairs < dev->sms ? unsigned(a.heads) : 1u), dim3(32 * kJoinWarps), p, s);
         if (st != NRM_OK) return st;
     }
     if (!a.weights) return NRM_OK;
-    return launch_pdl(reinterpret_cast<const void*>(&attn_weights_kernel<T>), dim3(unsigned(dev->sms)),
+    return launch_pdl(reinterpret_cast<const void*>(&attn_weights_kernel<T>), dim3(unsigned(4 * dev->sms)),
                       dim3(kAttnThreads), p, s);
 }
 

@@ -23,7 +23,8 @@
 
 namespace nrm {
 
-constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnThreads = 256;    // of a CTA of the kernel for any layout and of the one for the weights
+constexpr int kJoinWarps = 16;
 
 __device__ __forceinline__ float exp2_approx(float v) {
     float r;
@@ -33,66 +34,74 @@ __device__ __forceinline__ float exp2_approx(float v) {
 // What a maximum is subtracted as: an empty one (all logits -infinity) as 0.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
-// The positions of sequence s that count: [lo, n).
-struct AttnSpan {
-    int64_t lo, n;
+// The sequences' tiles, in shared memory.
+struct AttnTable {
+    int64_t n[kAttnSequences];        // positions
+    int pre[kAttnSequences + 1];      // tiles before each sequence
+    int sums[32];
 };
-__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int s) {
-    int64_t n = ld_after(a.lengths + s);
-    if (n < 0 || n > a.cap) {
-        atomicOr(a.err, kErrCacheSlot);
-        n = n < 0 ? 0 : a.cap;
-    }
-    return AttnSpan{a.window > 0 && n > a.window ? n - a.window : 0, n};
+__device__ __forceinline__ int attn_tiles(const AttnArgs& a, int64_t n) {
+    const int64_t seen = a.window > 0 && n > a.window ? a.window : n;
+    return int((seen + kAttnTile - 1) / kAttnTile);
 }
 
-// Tiles before each sequence, in shared memory; all threads of the CTA.
-__device__ __forceinline__ void attn_prefix(const AttnArgs& a, int64_t* pre, int64_t* sums) {
-    constexpr int per = kAttnSequences / kAttnThreads;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t tiles[per], total = 0;
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-        const int s = int(threadIdx.x) * per + i;
-        tiles[i] = 0;
+// All threads of the CTA; CTA 0 writes the tiles to the workspace, for the kernels that follow.
+__device__ __forceinline__ void attn_table(const AttnArgs& a, AttnTable& t) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = int(blockDim.x) >> 5;
+    int before = 0;
+    for (int s0 = 0; s0 < a.sequences; s0 += int(blockDim.x)) {
+        const int s = s0 + int(threadIdx.x);
+        int tiles = 0;
         if (s < a.sequences) {
-            const AttnSpan p = attn_span(a, s);
-            tiles[i] = (p.n - p.lo + kAttnTile - 1) / kAttnTile;
+            int64_t n = ld_after(a.lengths + s);
+            if (n < 0 || n > a.cap) {
+                atomicOr(a.err, kErrCacheSlot);
+                n = n < 0 ? 0 : a.cap;
+            }
+            t.n[s] = n;
+            tiles = attn_tiles(a, n);
         }
-        total += tiles[i];
-    }
-    int64_t run = total;
+        int run = tiles;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += up;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += up;
+        }
+        if (lane == 31) t.sums[warp] = run;
+        __syncthreads();
+        const int w = lane < warps ? t.sums[lane] : 0;
+        run += before + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+        before += __reduce_add_sync(0xffffffffu, w);
+        if (s < a.sequences) {
+            t.pre[s + 1] = run;
+            if (blockIdx.x == 0) a.prefix[s + 1] = run;
+        }
+        if (s == 0) {
+            t.pre[0] = 0;
+            if (blockIdx.x == 0) a.prefix[0] = 0;
+        }
+        __syncthreads();
     }
-    if (lane == 31) sums[warp] = run;
-    __syncthreads();
-    int64_t before = run - total;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-#pragma unroll
-    for (int i = 0; i < per; ++i) {
-        const int s = int(threadIdx.x) * per + i;
-        if (s < a.sequences) pre[s] = before;
-        before += tiles[i];
-        if (s == a.sequences - 1) pre[a.sequences] = before;
-    }
-    __syncthreads();
 }
 
-// Workers that get a share of `total` tiles, and where shares begin.
-__device__ __forceinline__ int64_t attn_used(const AttnArgs& a, int64_t total) {
-    const int64_t w = (total + a.min_tiles - 1) / a.min_tiles;
-    return w < a.workers ? w : a.workers;
-}
-__device__ __forceinline__ int64_t attn_begin(int64_t total, int64_t used, int64_t w) { return total * w / used; }
-// The worker whose share holds tile t.
-__device__ __forceinline__ int64_t attn_owner(int64_t total, int64_t used, int64_t t) {
-    return ((t + 1) * used - 1) / total;
-}
+// Workers that get a share of `total` tiles, and their shares: the first `more` have one tile more.
+struct AttnShares {
+    int used, each, more;
+    __device__ __forceinline__ AttnShares(const AttnArgs& a, int total) {
+        const int w = (total + a.min_tiles - 1) / a.min_tiles;
+        used = max(1, min(w, a.workers));
+        each = total / used;
+        more = total - each * used;
+    }
+    __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
+    // the worker whose share holds tile t
+    __device__ __forceinline__ int owner(int t) const {
+        const int longer = more * (each + 1);
+        return t < longer ? t / (each + 1) : more + (t - longer) / each;
+    }
+};
 // The sequence that tile `t` of the sequences' tiles (not their pairs') belongs to.
-__device__ __forceinline__ int attn_sequence(const int64_t* pre, int sequences, int64_t t) {
+__device__ __forceinline__ int attn_sequence(const int* pre, int sequences, int t) {
     int lo = 0, hi = sequences - 1;  // the last s with pre[s] <= t
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -105,55 +114,62 @@ __device__ __forceinline__ int attn_sequence(const int64_t* pre, int sequences, 
 // A worker's piece of one pair: tiles [tile0, tile1) of sequence s.
 struct AttnPiece {
     int s, head, q0, heads;  // head of the cache; query heads q0 .. q0 + heads - 1
-    int64_t lo, n;           // positions that count
-    int64_t tile0, tile1;
+    int pair;
+    int tile0, tile1;
     bool whole;              // all of the pair
-    int64_t part;            // else: where its partial result goes
+    int64_t lo, n;           // positions that count
+    int64_t part;            // where its partial result goes, if it is not whole
 };
 
-// Calls f(piece) for each piece of worker w's share.  `pre`: shared memory.
+// Calls f(piece) for each piece of worker w's share.
 template <typename F>
-__device__ __forceinline__ void attn_pieces(const AttnArgs& a, const int64_t* pre, int64_t w, F&& f) {
+__device__ __forceinline__ void attn_pieces(const AttnArgs& a, const AttnTable& table, int w, F&& f) {
     const int pairs = a.hk * a.chunks;
-    const int64_t total = pre[a.sequences] * pairs, used = attn_used(a, total);
-    if (w >= used) return;
-    int64_t t = attn_begin(total, used, w);
-    const int64_t end = attn_begin(total, used, w + 1);
-    int s = attn_sequence(pre, a.sequences, t / pairs);
+    const int total = table.pre[a.sequences] * pairs;
+    const AttnShares shares(a, total);
+    if (w >= shares.used) return;
+    int t = shares.begin(w);
+    const int end = shares.begin(w + 1);
+    if (t >= end) return;
+    int s = attn_sequence(table.pre, a.sequences, t / pairs);
     while (t < end) {
-        while (pre[s + 1] * pairs <= t) ++s;  // (sequences without tiles are passed over)
-        const int64_t tiles = pre[s + 1] - pre[s], at = t - pre[s] * pairs;
-        const int pair = int(at / tiles);
+        while (table.pre[s + 1] * pairs <= t) ++s;  // (sequences without tiles are passed over)
+        const int tiles = table.pre[s + 1] - table.pre[s], at = t - table.pre[s] * pairs;
         AttnPiece p;
         p.s = s;
-        p.head = pair / a.chunks;
-        const int chunk = pair - p.head * a.chunks;
+        p.pair = at / tiles;
+        p.head = p.pair / a.chunks;
+        const int chunk = p.pair - p.head * a.chunks;
         p.q0 = p.head * a.shared + chunk * a.heads;
         p.heads = min(a.heads, a.shared - chunk * a.heads);
-        const AttnSpan span = attn_span(a, s);
-        p.lo = span.lo;
-        p.n = span.n;
-        p.tile0 = at - pair * tiles;
+        p.n = table.n[s];
+        p.lo = a.window > 0 && p.n > a.window ? p.n - a.window : 0;
+        p.tile0 = at - p.pair * tiles;
         p.tile1 = min(tiles, p.tile0 + (end - t));
         p.whole = p.tile0 == 0 && p.tile1 == tiles;
         // its first pair's end, or its last pair's beginning
-        p.part = (w * 2 + (p.tile0 == 0 ? 1 : 0)) * attn_part_floats(a.heads, a.d);
+        p.part = (int64_t(w) * 2 + (p.tile0 == 0 ? 1 : 0)) * attn_part_floats(a.heads, a.d);
         f(p);
         t += p.tile1 - p.tile0;
     }
 }
 
+// A position's logits of a pair.
+__device__ __forceinline__ float* attn_logits(const AttnArgs& a, int s, int pair, int64_t j) {
+    return a.logits + ((int64_t(s) * a.hk * a.chunks + pair) * a.logit_stride + j) * a.logit_heads;
+}
+
 // Sequences without a position: out is 0, lse -infinity.
 template <typename T>
-__device__ __forceinline__ void attn_empty(const AttnArgs& a, const int64_t* pre) {
+__device__ __forceinline__ void attn_empty(const AttnArgs& a, const AttnTable& table) {
     for (int s = int(blockIdx.x); s < a.sequences; s += int(gridDim.x)) {
-        if (pre[s + 1] != pre[s]) continue;
+        if (table.pre[s + 1] != table.pre[s]) continue;
         typename Io<T>::bits_t* out = static_cast<typename Io<T>::bits_t*>(a.out.p) + s * a.out.ts;
-        for (int i = int(threadIdx.x); i < a.hq * a.d; i += kAttnThreads) {
+        for (int i = int(threadIdx.x); i < a.hq * a.d; i += int(blockDim.x)) {
             const int h = i / a.d;
             out[h * a.out.hs + (i - h * a.d)] = Io<T>::store(0.f);
         }
-        for (int h = int(threadIdx.x); h < a.hq; h += kAttnThreads)
+        for (int h = int(threadIdx.x); h < a.hq; h += int(blockDim.x))
             if (a.lse) a.lse[int64_t(s) * a.hq + h] = -INFINITY;
     }
 }
@@ -179,8 +195,6 @@ __device__ __forceinline__ void attn_write_lse(const AttnArgs& a, int s, int h, 
 // ---------------------------------------------------------------------------
 // any layout: a lane holds every 32nd element of a row
 // ---------------------------------------------------------------------------
-constexpr int kAttnScalarHeads = 4;  // query heads of a worker
-
 __device__ __forceinline__ float code_value(const uint8_t* codes, int i, int kind) {
     if (kind == NRM_CACHE_INT4) {
         const uint32_t b = ld_after(codes + (i >> 1));
@@ -194,14 +208,12 @@ template <typename T>
 __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArgs a) {
     using bits = typename Io<T>::bits_t;
     constexpr int E = kHeadMaxD / 32, H = kAttnScalarHeads;
-    __shared__ int64_t pre[kAttnSequences + 1], sums[kAttnWarps];
+    __shared__ AttnTable table;
     pdl_next();
-    attn_prefix(a, pre, sums);
-    if (blockIdx.x == 0)
-        for (int s = int(threadIdx.x); s <= a.sequences; s += kAttnThreads) a.prefix[s] = pre[s];
-    attn_empty<T>(a, pre);
+    attn_table(a, table);
+    attn_empty<T>(a, table);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    attn_pieces(a, pre, int64_t(warp) * gridDim.x + blockIdx.x, [&](const AttnPiece& p) {
+    attn_pieces(a, table, warp * int(gridDim.x) + int(blockIdx.x), [&](const AttnPiece& p) {
         float q[H][E], acc[H][E], m[H], sum[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -215,8 +227,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
                 acc[h][e] = 0.f;
             }
         }
-        const int64_t j1 = min(p.n, p.lo + p.tile1 * kAttnTile);
-        for (int64_t j = p.lo + p.tile0 * kAttnTile; j < j1; ++j) {
+        const int64_t j1 = min(p.n, p.lo + int64_t(p.tile1) * kAttnTile);
+        for (int64_t j = p.lo + int64_t(p.tile0) * kAttnTile; j < j1; ++j) {
             const int64_t slot = attn_slot(a, p.s, j);
             float l[H];
             if (slot >= 0) {
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
                 float mine = l[0];
 #pragma unroll
                 for (int h = 1; h < H; ++h) mine = lane == h ? l[h] : mine;
-                a.logits[(int64_t(p.s) * a.hq + p.q0 + lane) * a.logit_stride + j] = mine;
+                attn_logits(a, p.s, p.pair, j)[lane] = mine;
             }
         }
 #pragma unroll
@@ -287,63 +299,95 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
 }
 
 // ---------------------------------------------------------------------------
-// joining the pieces of a pair: a CTA for each query head
+// joining the pieces of a pair: a CTA for each pair (blockIdx.x), or, where pairs
+// are few and so have many pieces, for each of its heads (blockIdx.y).  Its warps
+// share the heads, and the warps of a head its pieces.
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs a) {
     using bits = typename Io<T>::bits_t;
-    constexpr int E = kHeadMaxD / 32;
-    __shared__ float joined[kAttnWarps][kHeadMaxD], sums[kAttnWarps];
+    constexpr int E = kHeadMaxD / 128, AHEAD = 4;
+    __shared__ float4 joined[kJoinWarps][kHeadMaxD / 4];
+    __shared__ float sums[kJoinWarps];
     pdl_next();
-    const int s = int(blockIdx.x) / a.hq, hq = int(blockIdx.x) - s * a.hq;
-    const int head = hq / a.shared, in_head = hq - head * a.shared;
-    const int chunk = in_head / a.heads, h = in_head - chunk * a.heads;
-    const int pairs = a.hk * a.chunks, pair = head * a.chunks + chunk;
-    const int64_t before = ld_after(a.prefix + s), tiles = ld_after(a.prefix + s + 1) - before;
-    const int64_t total = ld_after(a.prefix + a.sequences) * pairs;
-    if (tiles == 0) return;
-    const int64_t used = attn_used(a, total), t0 = before * pairs + pair * tiles;
-    const int64_t w0 = attn_owner(total, used, t0), w1 = attn_owner(total, used, t0 + tiles - 1);
+    const int pairs = a.hk * a.chunks;
+    const int s = int(blockIdx.x) / pairs, pair = int(blockIdx.x) - s * pairs;
+    const int before = ld_after(a.prefix + s), tiles = ld_after(a.prefix + s + 1) - before;
+    if (tiles <= 1) return;
+    const int t0 = before * pairs + pair * tiles;
+    const AttnShares shares(a, ld_after(a.prefix + a.sequences) * pairs);
+    const int w0 = shares.owner(t0), w1 = shares.owner(t0 + tiles - 1);
     if (w0 == w1) return;  // written by that worker
+    const int head = pair / a.chunks, chunk = pair - head * a.chunks;
+    const int heads = min(a.heads, a.shared - chunk * a.heads), q0 = head * a.shared + chunk * a.heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // the first worker's piece is the beginning of its last pair, the others' the end of their first
-    auto part = [&](int64_t w) {
-        return a.part + (w * 2 + (w == w0)) * attn_part_floats(a.heads, a.d) + h * attn_part_row(a.d);
-    };
-    float top = -INFINITY;
-    for (int64_t w = w0 + lane; w <= w1; w += 32) {
-        const float m = ld_after(part(w) + a.d);
-        top = fmaxf(top, m);
+    // heads of this CTA, in rounds of as many as have warps of their own
+    const int mine = gridDim.y > 1 ? 1 : heads, at_once = min(mine, kJoinWarps), each = kJoinWarps / at_once;
+    const int group = warp / each, in_group = warp - group * each;
+    for (int h0 = 0; h0 < mine; h0 += at_once) {
+        const int h = gridDim.y > 1 ? int(blockIdx.y) : h0 + group;
+        const bool there = group < at_once && h0 + group < mine && h < heads;
+        // the first worker's piece is the beginning of its last pair, the others' the end of their first
+        auto part = [&](int w) {
+            return a.part + (int64_t(w) * 2 + (w == w0)) * attn_part_floats(a.heads, a.d) + h * attn_part_row(a.d);
+        };
+        float top = -INFINITY, sum = 0.f;
+        float4 acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there) {
+            for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, ld_after(part(w) + a.d));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float base = finite_max(top);
+            for (int w = w0 + in_group; w <= w1; w += AHEAD * each) {
+                float f[AHEAD], l[AHEAD];
+                uint4 v[AHEAD][E];
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const bool in = w + k * each <= w1;
+                    const float* from = part(in ? w + k * each : w);
+                    f[k] = in ? ld_after(from + a.d) : -INFINITY;
+                    l[k] = ld_after(from + a.d + 1);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (lane * 4 + 128 * e < a.d) v[k][e] = ld_after(reinterpret_cast<const uint4*>(from) + lane + 32 * e);
+                }
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    if (w + k * each > w1) break;
+                    f[k] = exp2_approx(f[k] - base);
+                    sum = fmaf(l[k], f[k], sum);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        if (lane * 4 + 128 * e >= a.d) break;
+                        acc[e].x = fmaf(__uint_as_float(v[k][e].x), f[k], acc[e].x);
+                        acc[e].y = fmaf(__uint_as_float(v[k][e].y), f[k], acc[e].y);
+                        acc[e].z = fmaf(__uint_as_float(v[k][e].z), f[k], acc[e].z);
+                        acc[e].w = fmaf(__uint_as_float(v[k][e].w), f[k], acc[e].w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (lane * 4 + 128 * e < a.d) joined[warp][lane + 32 * e] = acc[e];
+            if (lane == 0) sums[warp] = sum;
+        }
+        __syncthreads();
+        if (there) {
+            float all = 0.f;
+            for (int k = 0; k < each; ++k) all += sums[group * each + k];
+            const float scale = all == 0.f ? 0.f : 1.f / all;
+            bits* row = static_cast<bits*>(a.out.p) + s * a.out.ts + (q0 + h) * a.out.hs;
+            for (int i = in_group * 32 + lane; i < a.d; i += each * 32) {
+                float v = 0.f;
+                for (int k = 0; k < each; ++k) v += reinterpret_cast<const float*>(joined[group * each + k])[i];
+                row[i] = Io<T>::store(v * scale);
+            }
+            if (in_group == 0 && lane == 0) attn_write_lse(a, s, q0 + h, top, all);
+        }
+        __syncthreads();
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = finite_max(top);
-    float acc[E] = {}, sum = 0.f;
-    for (int64_t w = w0 + warp; w <= w1; w += kAttnWarps) {
-        const float* from = part(w);
-        const float f = exp2_approx(ld_after(from + a.d) - base);
-        sum = fmaf(ld_after(from + a.d + 1), f, sum);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (lane + 32 * e < a.d) acc[e] = fmaf(ld_after(from + lane + 32 * e), f, acc[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (lane + 32 * e < a.d) joined[warp][lane + 32 * e] = acc[e];
-    if (lane == 0) sums[warp] = sum;
-    __syncthreads();
-    float all = 0.f;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) all += sums[w];
-    const float scale = all == 0.f ? 0.f : 1.f / all;
-    bits* row = static_cast<bits*>(a.out.p) + s * a.out.ts + hq * a.out.hs;
-    for (int i = int(threadIdx.x); i < a.d; i += kAttnThreads) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) v += joined[w][i];
-        row[i] = Io<T>::store(v * scale);
-    }
-    if (threadIdx.x == 0) attn_write_lse(a, s, hq, top, all);
 }
 
 // ---------------------------------------------------------------------------
@@ -351,33 +395,53 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(const AttnArgs 
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kAttnThreads) attn_weights_kernel(const AttnArgs a) {
-    __shared__ int64_t pre[kAttnSequences + 1];
+    constexpr int AHEAD = 4;
+    __shared__ int pre[kAttnSequences + 1];
     pdl_next();
     for (int s = int(threadIdx.x); s <= a.sequences; s += kAttnThreads) pre[s] = ld_after(a.prefix + s);
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    const int64_t total = pre[a.sequences] * a.hk, warps = int64_t(gridDim.x) * kAttnWarps;
-    const int64_t w = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-    int64_t t = total * w / warps;
-    const int64_t end = total * (w + 1) / warps;
+    const int total = pre[a.sequences] * a.hk, warps = int(gridDim.x) * (kAttnThreads / 32);
+    const int w = int(threadIdx.x >> 5) * int(gridDim.x) + int(blockIdx.x);
+    const int each = total / warps, more = total - each * warps;
+    int t = w * each + min(w, more);
+    const int end = t + each + (w < more);
     if (t >= end) return;
     int s = attn_sequence(pre, a.sequences, t / a.hk);
     while (t < end) {
         while (pre[s + 1] * a.hk <= t) ++s;
-        const int64_t tiles = pre[s + 1] - pre[s], at = t - pre[s] * a.hk;
-        const int head = int(at / tiles);
-        const int64_t tile0 = at - head * tiles, tile1 = min(tiles, tile0 + (end - t));
-        const AttnSpan span = attn_span(a, s);
-        const float* lse2 = a.lse2 + int64_t(s) * a.hq + head * a.shared;
-        const float* logits = a.logits + (int64_t(s) * a.hq + head * a.shared) * a.logit_stride;
+        const int tiles = pre[s + 1] - pre[s], at = t - pre[s] * a.hk;
+        const int head = at / tiles;
+        const int tile0 = at - head * tiles, tile1 = min(tiles, tile0 + (end - t));
+        const int64_t n = max(int64_t(0), min(a.cap, ld_after(a.lengths + s)));
+        const int64_t lo = a.window > 0 && n > a.window ? n - a.window : 0;
+        const int64_t j1 = min(n, lo + int64_t(tile1) * kAttnTile);
         float* out = a.weights + s * a.weight_ts + head * a.weight_hs;
-        for (int64_t j = span.lo + tile0 * kAttnTile + lane; j < min(span.n, span.lo + tile1 * kAttnTile); j += 32) {
-            float sum = 0.f;
-            for (int h = 0; h < a.shared; ++h) {
-                const float l = ld_after(logits + h * a.logit_stride + j);
-                sum += l == -INFINITY ? 0.f : exp2_approx(l - ld_after(lse2 + h));
+        for (int64_t j = lo + int64_t(tile0) * kAttnTile + lane; j < j1; j += 32 * AHEAD) {
+            float sum[AHEAD] = {};
+            for (int c = 0; c < a.chunks; ++c) {
+                const float* lse2 = a.lse2 + int64_t(s) * a.hq + head * a.shared + c * a.heads;
+                const int heads = min(a.heads, a.shared - c * a.heads);
+                const float* logits = attn_logits(a, s, head * a.chunks + c, j);
+                for (int h = 0; h < heads; h += 2) {
+                    const float l0 = ld_after(lse2 + h), l1 = h + 1 < heads ? ld_after(lse2 + h + 1) : 0.f;
+                    uint2 v[AHEAD];
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k)
+                        if (j + 32 * k < j1)
+                            v[k] = ld_after(reinterpret_cast<const uint2*>(logits + int64_t(32 * k) * a.logit_heads + h));
+#pragma unroll
+                    for (int k = 0; k < AHEAD; ++k) {
+                        if (j + 32 * k >= j1) break;
+                        const float x = __uint_as_float(v[k].x), y = __uint_as_float(v[k].y);
+                        sum[k] += x == -INFINITY ? 0.f : exp2_approx(x - l0);
+                        if (h + 1 < heads) sum[k] += y == -INFINITY ? 0.f : exp2_approx(y - l1);
+                    }
+                }
             }
-            out[j] += sum;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (j + 32 * k < j1) out[j + 32 * k] += sum[k];
         }
         t += tile1 - tile0;
     }

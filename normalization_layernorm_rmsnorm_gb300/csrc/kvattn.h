@@ -12,8 +12,9 @@ namespace nrm {
 // call with more is cut into launches.
 constexpr int kAttnSequences = 1024;
 constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
-constexpr int kAttnWarps = 8;        // warps of a CTA, each a worker of its own
+constexpr int kAttnWarps = 12;       // warps of a CTA at most, each a worker of its own
 constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
+constexpr int64_t kAttnTiles = int64_t(1) << 31;  // of all pairs of a launch, fewer than this
 
 // The positions of the sequences, cut into tiles: tiles of sequence s, for each
 // of its `pairs` (a head of the cache with a chunk of its query heads), are
@@ -29,6 +30,7 @@ struct AttnArgs {
     int shared;               // query heads of a head of the cache: hq / hk
     int heads;                // query heads of a pair, at most
     int chunks;               // pairs of a head of the cache
+    int logit_heads;          // heads, made even
     int d;
     int64_t cap;              // positions that a sequence may have
     int64_t window;           // 0: all
@@ -37,10 +39,10 @@ struct AttnArgs {
     float* weights;           // (nullable)
     int64_t weight_ts, weight_hs;
     // workspace
-    int64_t* prefix;          // [sequences + 1] tiles before each sequence
+    int* prefix;              // [sequences + 1] tiles before each sequence
     float* lse2;              // [sequences, hq], base 2
     float* part;              // [workers][2] partial results
-    float* logits;            // [sequences, hq, logit_stride], base 2 (with weights)
+    float* logits;            // [sequences, pairs, logit_stride, logit_heads], base 2 (with weights)
     int64_t logit_stride;
     int workers;
     int min_tiles;            // of a worker that is used, but for the last
@@ -48,12 +50,25 @@ struct AttnArgs {
     int row_bytes, vec;       // of a row of codes, copied in vectors of 16 or 8 bytes
     int k_pitch, v_pitch;     // of a row in shared memory
     int q_vec, out_vec;       // queries and outputs are aligned to 16 bytes
+    int scale_vec;            // a row's scales are whole aligned 16 bytes
+    int64_t pages;
     unsigned int* err;
 };
 
+// The query heads of a head of the cache in chunks of at most `most`, as even as they come.
+inline void attn_chunks(AttnArgs& a, int most) {
+    a.chunks = (a.shared + most - 1) / most;
+    a.heads = (a.shared + a.chunks - 1) / a.chunks;
+    a.logit_heads = (a.heads + 1) / 2 * 2;
+}
 // Floats of one partial result: accumulator, maximum and sum of each head, in whole 16 bytes.
 __host__ __device__ inline int64_t attn_part_row(int d) { return (int64_t(d) + 2 + 3) / 4 * 4; }
 __host__ __device__ inline int64_t attn_part_floats(int heads, int d) { return heads * attn_part_row(d); }
+
+// Pairs of a sequence, and floats of a position's logits, at most.
+constexpr int kAttnScalarHeads = 4;  // query heads of a worker of the kernel for any layout
+inline int64_t attn_most_pairs(int64_t hq, int64_t hk) { return hk * ((hq / hk + kAttnScalarHeads - 1) / kAttnScalarHeads); }
+inline int64_t attn_most_logits(int64_t hq, int64_t hk) { return hq + 2 * attn_most_pairs(hq, hk); }
 
 // `vec`: the rows' codes are whole aligned vectors of that many bytes (16 or 8)
 // and d and the group are multiples of 16; else 0.

@@ -64,13 +64,14 @@ struct AttnWorkspace {
 bool attn_workspace(int64_t sequences, int64_t hq, int64_t hk, int64_t d, int64_t positions, int sms, AttnWorkspace* w) {
     const int64_t n = sequences < kAttnSequences ? sequences : kAttnSequences;
     const int64_t heads = hq / hk < kAttnHeads ? hq / hk : kAttnHeads;
-    w->logit_stride = (positions + 3) / 4 * 4;
-    if (n * hq > 0 && w->logit_stride > kMaxWorkspace / (n * hq * 4)) return false;
+    const int64_t logits = n * attn_most_logits(hq, hk);
+    w->logit_stride = positions;
+    if (logits > 0 && positions > kMaxWorkspace / (logits * 4)) return false;
     w->at[0] = 0;
-    w->at[1] = round16((n + 1) * 8);
+    w->at[1] = round16((n + 1) * 4);
     w->at[2] = w->at[1] + round16(n * hq * 4);
     w->at[3] = w->at[2] + round16(int64_t(sms) * kAttnWarps * 2 * attn_part_floats(int(heads), int(d)) * 4);
-    w->at[4] = w->at[3] + n * hq * w->logit_stride * 4;
+    w->at[4] = w->at[3] + logits * positions * 4;
     return true;
 }
 
@@ -113,6 +114,10 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
         if (window < 0) return fail(NRM_ERR_INVALID_ARG, "window must be >= 0");
         NRM_TRY(check_stats({lse}, 4));
         if (sequences == 0) return NRM_OK;
+        // the tiles of a launch are counted in 32 bits
+        const int64_t tiles = (a.cap / kAttnTile + 1) * attn_most_pairs(q->heads, cache->heads);
+        if (a.cap / kAttnTile >= kAttnTiles || tiles >= kAttnTiles)
+            return fail(NRM_ERR_UNSUPPORTED, "positions*heads of a sequence must be < 2^36");
         const DevInfo* dev = dev_info();
         if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
         AttnWorkspace w;
@@ -124,7 +129,7 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
             return fail(NRM_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", workspace_bytes,
                         size_t(w.at[4]));
         char* ws = static_cast<char*>(workspace);
-        a.prefix = reinterpret_cast<int64_t*>(ws + w.at[0]);
+        a.prefix = reinterpret_cast<int*>(ws + w.at[0]);
         a.lse2 = reinterpret_cast<float*>(ws + w.at[1]);
         a.part = reinterpret_cast<float*>(ws + w.at[2]);
         a.logits = weights ? reinterpret_cast<float*>(ws + w.at[3]) : nullptr;
@@ -159,9 +164,14 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
         };
         a.q_vec = whole(q);
         a.out_vec = whole(out);
-        for (int64_t s0 = 0; s0 < sequences; s0 += kAttnSequences) {
+        a.scale_vec = cache->d / cache->group % 4 == 0 && aligned(cache->k_scales, 16) && aligned(cache->v_scales, 16) &&
+                      (cache->pages == 1 || cache->scale_page_stride % 4 == 0) &&
+                      (cache->page_size == 1 || cache->scale_slot_stride % 4 == 0) &&
+                      (cache->heads == 1 || cache->scale_head_stride % 4 == 0);
+        const int64_t most = std::min<int64_t>(kAttnSequences, (kAttnTiles - 1) / tiles);
+        for (int64_t s0 = 0; s0 < sequences; s0 += most) {
             AttnArgs b = a;
-            b.sequences = int(sequences - s0 < kAttnSequences ? sequences - s0 : kAttnSequences);
+            b.sequences = int(std::min(sequences - s0, most));
             b.table = pages->table + s0 * a.table_stride;
             b.lengths = pages->lengths + s0;
             b.q.p = static_cast<char*>(a.q.p) + s0 * a.q.ts * es;

@@ -6,21 +6,25 @@
 // exact in fp16 in every stored form; the keys' scales multiply the logits, the
 // values' the weights.  Queries are scaled by a power of two to at most 2^15:
 // those of 16 bits then are exact, of float32 ones the rest is a second factor
-// (22 bits).  A weight p <= 1 times its value's scale, with the largest scale seen
-// brought to 2^14, keeps 11 bits down to 2^-28 of that; where the output has
-// them (fp16, float32), the rest is a second factor too.  The order of the d
-// elements in a product is free, so a lane takes its keys' elements as they lie
-// in 8 (or 4) neighbours, and its values' in 4 (or 2).
+// (22 bits).  A weight is p*2^8 times its value's scale, the largest scale seen
+// brought below 2^6, all in fp16: 11 bits down to 2^-28 of the largest; where
+// the output has more (fp16, float32), p, the scale and their product each have a
+// second factor too.  The order of the d elements in a product is free, so a lane
+// takes its keys' elements as they lie in 8 (or 4) neighbours, and its values' in
+// 4 (or 2).
 //
-// The column's heads are the lanes' pairs in both results, so the running
+// The columns' heads are the lanes' pairs in both results, so the running
 // maximum, the rescaling and the sum need nothing from other lanes but the
-// maximum over the 16 positions; the weights change from rows to columns by a
-// transposing exchange of 8x8 matrices.
+// maximum over the positions; p changes from rows to columns by a transposing
+// exchange of 8x8 matrices.
 //
 // Codes and scales are copied asynchronously into the warp's own ring in shared
-// memory, 16 positions to a stage; warps share nothing and the loop holds no
+// memory, a tile of 32 positions to a stage; warps share nothing and the loop holds no
 // barrier of the CTA.  The row of a page is found by the lane of its position, a
 // tile ahead.  Rows are padded so that the fragments' reads have no conflicts.
+// (Bulk copies of single rows are no way to move them: one takes an SM about ten
+// cycles, 1.8 TB/s with rows of 64 bytes and 3.7 with 128, against 3.5 and 6.2 by
+// 16-byte copies that eight lanes make of a row.)
 #pragma once
 
 #include "kvattn.cuh"
@@ -90,9 +94,14 @@ __device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
         hi = add_half2(__byte_perm(v, 0x64646464u, 0x4342), 0xe480e480u);
     }
 }
-// The 4-bit codes at the low ends of both halves (already turned by 8).
+// The 4-bit codes at the low ends of both halves (already turned by 8), and those above them (16 times as large).
 __device__ __forceinline__ uint32_t codes4(uint32_t v) {
     return add_half2((v & 0x000f000fu) | 0x64006400u, 0xe408e408u);  // - 1032
+}
+__device__ __forceinline__ uint32_t codes4_next(uint32_t v) {
+    uint32_t r;  // / 16 - 72
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
+    return r;
 }
 
 // What a kernel is made for: the stored form, elements of a unit of a row (every group is whole units of 32, or of
@@ -103,19 +112,33 @@ struct AttnForm {
     static constexpr int UNITS = DMAX / UNIT, STEPS = UNIT / 16, TILES = UNIT / 16;
     static constexpr int KP = UNIT / 4, VP = UNIT / 8;  // elements of a lane's piece of a unit
     static constexpr int BITS = KIND == NRM_CACHE_INT4 ? 4 : 8;
-    // stages of 16 positions that fit beside one another (at most 6: the copies run less than 3 tiles ahead)
-    static constexpr int STAGES = DMAX == 128 ? (BITS == 4 ? 6 : 5) : (BITS == 4 ? 5 : 3);
+    static constexpr int WARPS = DMAX == 128 && NT == 1 ? 12 : 8;  // by the registers that a thread needs
+    static constexpr int STAGES = BITS == 4 && DMAX == 128 ? 3 : 2;
 };
 
-// A warp's shared memory: stages (keys, values, scales of both), then for two tiles the rows' places.
+// A warp's shared memory: stages (keys, values, scales of both), then the places of two tiles' rows, which positions
+// of the stages are there, and the values' scales in fp16.
 struct AttnSmem {
     uint32_t stage, bytes;     // of the first stage; of one
-    uint32_t places;           // [2][32] code offsets, [2][32] scale offsets, then which positions of 4 tiles are there
+    uint32_t places;           // [2][32] code offsets
+    uint32_t there;            // [stages]
+    uint32_t half_scales;      // [factors][groups][32]
 };
 __host__ __device__ inline uint32_t attn_stage_bytes(int k_pitch, int v_pitch, int groups) {
-    return uint32_t(16 * (k_pitch + v_pitch) + 2 * 16 * groups * 4 + 15) / 16 * 16;
+    return uint32_t(32 * (k_pitch + v_pitch) + 2 * 32 * groups * 4);
 }
-constexpr uint32_t kAttnPlaces = 2 * 32 * 8 * 2 + 16;
+constexpr uint32_t kAttnPlaces = 2 * 32 * 8, kAttnThere = 16;
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 
 template <typename T, typename F>
 __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiece& p, const AttnSmem& sm, int groups) {
@@ -125,72 +148,97 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
     const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
     const int units = a.d / F::UNIT, group_units = a.cache.group / F::UNIT;
 
-    // ---- the copies: 16 positions to a stage ----
-    const int64_t j0 = p.lo + p.tile0 * kAttnTile;
-    const int64_t positions = min(p.n, p.lo + p.tile1 * kAttnTile) - j0;
-    const int subs = int((positions + 15) / 16);
-    const int chunks = a.row_bytes / a.vec, copies = 16 * chunks;
+    // ---- the copies: a tile to a stage ----
+    const int64_t j0 = p.lo + int64_t(p.tile0) * kAttnTile;
+    const int64_t j1 = min(p.n, p.lo + int64_t(p.tile1) * kAttnTile);
+    const int tiles = p.tile1 - p.tile0;
+    const int chunks = a.row_bytes / a.vec;
     const int row_step = 32 / chunks, chunk_step = 32 - row_step * chunks;
     const int first_row = lane / chunks, first_chunk = lane - first_row * chunks;
-    const uint32_t v_at = 16 * a.k_pitch, s_at = v_at + 16 * a.v_pitch;
-    const int64_t pages = a.cache.slots / a.cache.page.d;
+    const uint32_t v_at = 32 * a.k_pitch, s_at = v_at + 32 * a.v_pitch;
     const uint32_t ring = smem_addr(&in_ring<unsigned char>(0));
+    const int64_t* const table = a.table + p.s * a.table_stride;
     int64_t page = 0, in_page = 0;
-    auto look_up = [&](int tile) {  // this lane's position of a tile (in_page -1: there is none)
-        const int64_t j = j0 + int64_t(tile) * kAttnTile + lane;
+    auto look_up = [&](int64_t j) {  // this lane's position of a tile (in_page -1: there is none)
+        j += lane;
         in_page = -1;
-        if (j - j0 < positions) {
+        if (j < j1) {
             const int64_t entry = row_div(j, a.cache.page);
             in_page = j - entry * a.cache.page.d;
-            page = ld_after(a.table + p.s * a.table_stride + entry);
+            page = ld_after(table + entry);
         }
     };
-    auto issue = [&](int sub) {
-        const int tile = sub >> 1, odd = tile & 1, half = sub & 1;
-        const uint32_t code_places = sm.places + odd * 256, scale_places = sm.places + 512 + odd * 256;
-        if (half == 0) {
-            const bool ok = in_page >= 0 && page >= 0 && page < pages;
-            if (in_page >= 0 && !ok) atomicOr(a.err, kErrCacheSlot);
-            const uint32_t m = __ballot_sync(0xffffffffu, ok);
-            CacheRow r{0, 0};
-            if (ok) r = cache_row(a.cache, page * a.cache.page.d + in_page, p.head);
-            in_ring<int64_t>(code_places + lane * 8) = r.code;
-            in_ring<int64_t>(scale_places + lane * 8) = r.scale;
-            if (lane == 0) in_ring<uint32_t>(sm.places + 1024 + (tile & 3) * 4) = m;
-            __syncwarp();
-            look_up(tile + 1);
+    auto issue = [&](int tile, int stage) {
+        const uint32_t places = sm.places + (tile & 1) * 256;
+        const bool ok = in_page >= 0 && uint64_t(page) < uint64_t(a.pages);
+        if (in_page >= 0 && !ok) atomicOr(a.err, kErrCacheSlot);
+        const uint32_t m = __ballot_sync(0xffffffffu, ok);
+        int64_t code = 0, scale = 0;
+        if (ok) {
+            code = page * a.cache.page_stride + in_page * a.cache.slot_stride + p.head * a.cache.head_stride;
+            scale = page * a.cache.scale_page_stride + in_page * a.cache.scale_slot_stride + p.head * a.cache.scale_head_stride;
         }
-        const uint32_t there = in_ring<const uint32_t>(sm.places + 1024 + (tile & 3) * 4) >> (16 * half);
-        const uint32_t to = ring + sm.stage + uint32_t(sub % S) * sm.bytes;
+        in_ring<int64_t>(places + lane * 8) = code;
+        if (lane == 0) in_ring<uint32_t>(sm.there + stage * 4) = m;
+        __syncwarp();
+        const uint32_t to = ring + sm.stage + uint32_t(stage) * sm.bytes;
         int row = first_row, chunk = first_chunk;
-        for (int i = lane; i < copies; i += 32) {
-            const int64_t at = in_ring<const int64_t>(code_places + (16 * half + row) * 8) + chunk * a.vec;
-            const int n = there >> row & 1 ? a.vec : 0;
-            const uint32_t k = to + row * a.k_pitch + chunk * a.vec, v = to + v_at + row * a.v_pitch + chunk * a.vec;
-            if (a.vec == 16) {
-                cp_async_16_or_0(k, a.cache.codes[0] + at, n);
-                cp_async_16_or_0(v, a.cache.codes[1] + at, n);
-            } else {
-                cp_async_8_or_0(k, a.cache.codes[0] + at, n);
-                cp_async_8_or_0(v, a.cache.codes[1] + at, n);
+        uint32_t from = places + row * 8, k = to + row * a.k_pitch + chunk * a.vec, v = to + v_at + row * a.v_pitch + chunk * a.vec;
+        if (a.vec == 16 && chunk_step == 0 && m == 0xffffffffu) {
+            // a lane's vectors are one column of the rows: eight lanes of neighbours copy a row of 128 bytes
+            const unsigned char *kc = a.cache.codes[0] + chunk * 16, *vc = a.cache.codes[1] + chunk * 16;
+#pragma unroll 4
+            for (int i = 0; i < chunks; ++i) {
+                const int64_t at = in_ring<const int64_t>(from);
+                cp_async_16_or_0(k, kc + at, 16);
+                cp_async_16_or_0(v, vc + at, 16);
+                from += row_step * 8;
+                k += row_step * a.k_pitch;
+                v += row_step * a.v_pitch;
             }
-            row += row_step;
-            chunk += chunk_step;
-            if (chunk >= chunks) {
-                chunk -= chunks;
-                ++row;
+        } else {
+            for (int i = 0; i < chunks; ++i) {
+                const int64_t at = in_ring<const int64_t>(places + row * 8) + chunk * a.vec;
+                const int n = m >> row & 1 ? a.vec : 0;
+                k = to + row * a.k_pitch + chunk * a.vec;
+                v = to + v_at + row * a.v_pitch + chunk * a.vec;
+                if (a.vec == 16) {
+                    cp_async_16_or_0(k, a.cache.codes[0] + at, n);
+                    cp_async_16_or_0(v, a.cache.codes[1] + at, n);
+                } else {
+                    cp_async_8_or_0(k, a.cache.codes[0] + at, n);
+                    cp_async_8_or_0(v, a.cache.codes[1] + at, n);
+                }
+                row += row_step;
+                chunk += chunk_step;
+                if (chunk >= chunks) {
+                    chunk -= chunks;
+                    ++row;
+                }
             }
         }
-        // scales: keys' by the lower half of the warp, values' by the upper, [group][position]
-        const int sr = lane & 15, which = lane >> 4;
-        const float* from = a.cache.scales[which] + in_ring<const int64_t>(scale_places + (16 * half + sr) * 8);
-        const int n = there >> sr & 1 ? 4 : 0;
-        for (int g = 0; g < groups; ++g) cp_async_4_or_0(to + s_at + ((which * groups + g) * 16 + sr) * 4, from + g, n);
+        // this lane's position's scales, [position][group]
+        const uint32_t ks = to + s_at + lane * groups * 4, vs = ks + 32 * groups * 4;
+        const float *kf = a.cache.scales[0] + scale, *vf = a.cache.scales[1] + scale;
+        if (a.scale_vec) {
+            for (int g = 0; g < groups; g += 4) {
+                cp_async_16_or_0(ks + g * 4, kf + g, ok ? 16 : 0);
+                cp_async_16_or_0(vs + g * 4, vf + g, ok ? 16 : 0);
+            }
+        } else {
+            for (int g = 0; g < groups; ++g) {
+                cp_async_4_or_0(ks + g * 4, kf + g, ok ? 4 : 0);
+                cp_async_4_or_0(vs + g * 4, vf + g, ok ? 4 : 0);
+            }
+        }
     };
-    look_up(0);
+    look_up(j0);
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
-        if (i < subs) issue(i);
+        if (i < tiles) {
+            issue(i, i);
+            look_up(j0 + (i + 1) * kAttnTile);
+        }
         cp_async_commit();
     }
 
@@ -258,7 +306,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 
     // ---- the running softmax ----
     float acc[F::UNITS][F::TILES][NT][4], m[NT][2], sum[NT][2];
-    int top[F::UNITS];  // the values' largest scale so far is at most 2^top
+    int top[F::UNITS];  // the values' largest scale so far is below 2^top
 #pragma unroll
     for (int u = 0; u < F::UNITS; ++u) {
         top[u] = -1000;
@@ -272,94 +320,169 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, sum[nt][0] = sum[nt][1] = 0.f;
 
-    for (int sub = 0; sub < subs; ++sub) {
-        if (sub + S - 1 < subs) issue(sub + S - 1);
+    int stage = 0;
+    for (int tile = 0; tile < tiles; ++tile) {
+        if (tile + S - 1 < tiles) {
+            issue(tile + S - 1, stage == 0 ? S - 1 : stage - 1);
+            look_up(j0 + int64_t(tile + S) * kAttnTile);
+        }
         cp_async_commit();
         cp_async_wait<S - 1>();
         __syncwarp();
-        const uint32_t there = in_ring<const uint32_t>(sm.places + 1024 + (sub >> 1 & 3) * 4) >> (16 * (sub & 1));
-        const uint32_t at = sm.stage + uint32_t(sub % S) * sm.bytes;
-        const uint32_t k_at = at + gid * a.k_pitch + tid * (F::KP * F::BITS / 8);
-        const uint32_t scales = at + s_at + gid * 4;
+        const uint32_t there = in_ring<const uint32_t>(sm.there + stage * 4);
+        const uint32_t at = sm.stage + uint32_t(stage) * sm.bytes;
 
-        // logits of positions gid and gid + 8
-        float l[NT][4], c[NT][4];
+        // the values' scales in fp16, this lane's position's; seldom one is larger than all before it
+        {
+            const uint32_t mine = at + s_at + (32 + lane) * groups * 4;
+            bool larger = false;
+            int left = 0, g = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < F::UNITS; ++u) {
+                if (u >= units) break;
+                if (left == 0) {
+                    larger |= in_ring<const float>(mine + g * 4) >= (top[u] < -126 ? -1.f : __uint_as_float(uint32_t(127 + top[u]) << 23));
+                    left = group_units;
+                    ++g;
+                }
+                --left;
+            }
+            if (__any_sync(0xffffffffu, larger)) {
+                left = g = 0;
+                float raise = 1.f;
+                int now = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l[nt][i] = c[nt][i] = 0.f;
-        int left = group_units, g = 0;
+                for (int u = 0; u < F::UNITS; ++u) {
+                    if (u >= units) break;
+                    if (left == 0) {
+                        const uint32_t b = in_ring<const uint32_t>(mine + g * 4);
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
+                        now = min(127, max(max(top[u], -100), int(most >> 23) - 126));
+                        raise = exp2f(float(max(top[u] - now, -126)));
+                        left = group_units;
+                        ++g;
+                    }
+                    --left;
+                    top[u] = now;
 #pragma unroll
-        for (int u = 0; u < F::UNITS; ++u) {
-            if (u >= units) break;
-            uint32_t f[F::STEPS][4];
-            const uint32_t from = k_at + u * (F::UNIT * F::BITS / 8);
+                    for (int t = 0; t < F::TILES; ++t)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t row = from + r * 8 * a.k_pitch;
-                if constexpr (F::BITS == 8 && F::STEPS == 2) {
-                    const uint2 w = in_ring<const uint2>(row);
-                    codes8<F::KIND>(w.x, f[0][r], f[0][2 + r]);
-                    codes8<F::KIND>(w.y, f[F::STEPS - 1][r], f[F::STEPS - 1][2 + r]);
-                } else if constexpr (F::BITS == 8) {
-                    codes8<F::KIND>(lds<4>(row), f[0][r], f[0][2 + r]);
-                } else if constexpr (F::STEPS == 2) {
-                    const uint32_t w = lds<4>(row) ^ 0x88888888u;  // elements (0, 4), (1, 5), (2, 6), (3, 7)
-                    f[0][r] = codes4(w);
-                    f[0][2 + r] = codes4(w >> 4);
-                    f[F::STEPS - 1][r] = codes4(w >> 8);
-                    f[F::STEPS - 1][2 + r] = codes4(w >> 12);
-                } else {
-                    uint32_t w = lds<2>(row) ^ 0x8888u;  // elements (0, 2), (1, 3)
-                    w |= w << 8;
-                    f[0][r] = codes4(w);
-                    f[0][2 + r] = codes4(w >> 4);
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[u][t][nt][i] *= raise;
                 }
             }
+            left = g = 0;
 #pragma unroll
-            for (int st = 0; st < F::STEPS; ++st)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int t = 0; t < QT; ++t)
-                        mma16816(c[nt], f[st], q[u * F::STEPS + st][nt][t][0], q[u * F::STEPS + st][nt][t][1]);
-            if (--left == 0) {
-                const float s0 = in_ring<const float>(scales + g * 64), s1 = in_ring<const float>(scales + g * 64 + 32);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    l[nt][0] = fmaf(c[nt][0], s0, l[nt][0]);
-                    l[nt][1] = fmaf(c[nt][1], s0, l[nt][1]);
-                    l[nt][2] = fmaf(c[nt][2], s1, l[nt][2]);
-                    l[nt][3] = fmaf(c[nt][3], s1, l[nt][3]);
-                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+            for (int u = 0; u < F::UNITS; ++u) {
+                if (u >= units) break;
+                if (left == 0) {
+                    const float s = in_ring<const float>(mine + g * 4) * __uint_as_float(uint32_t(127 + 6 - top[u]) << 23);
+                    const __half hi = __float2half_rn(s);
+                    in_ring<__half>(sm.half_scales + (g * 32 + lane) * 2) = hi;
+                    if constexpr (WT == 2)
+                        in_ring<__half>(sm.half_scales + ((groups + g) * 32 + lane) * 2) = __float2half_rn(s - __half2float(hi));
+                    left = group_units;
+                    ++g;
                 }
-                left = group_units;
-                ++g;
+                --left;
+            }
+            __syncwarp();
+        }
+
+        // logits of positions gid, gid + 8, gid + 16 and gid + 24: [half of the tile][head, head + 1, 8 further]
+        float l[2][NT][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t k_at = at + (16 * half + gid) * a.k_pitch + tid * (F::KP * F::BITS / 8);
+            const uint32_t scales = at + s_at + (16 * half + gid) * groups * 4;
+            float c[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l[half][nt][i] = c[nt][i] = 0.f;
+            int left = group_units, g = 0;
+#pragma unroll
+            for (int u = 0; u < F::UNITS; ++u) {
+                if (u >= units) break;
+                uint32_t f[F::STEPS][4];
+                const uint32_t from = k_at + u * (F::UNIT * F::BITS / 8);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t row = from + r * 8 * a.k_pitch;
+                    if constexpr (F::BITS == 8 && F::STEPS == 2) {
+                        const uint2 w = in_ring<const uint2>(row);
+                        codes8<F::KIND>(w.x, f[0][r], f[0][2 + r]);
+                        codes8<F::KIND>(w.y, f[F::STEPS - 1][r], f[F::STEPS - 1][2 + r]);
+                    } else if constexpr (F::BITS == 8) {
+                        codes8<F::KIND>(lds<4>(row), f[0][r], f[0][2 + r]);
+                    } else if constexpr (F::STEPS == 2) {
+                        const uint32_t w = lds<4>(row) ^ 0x88888888u;  // elements (0, 4), (1, 5), (2, 6), (3, 7)
+                        f[0][r] = codes4(w);
+                        f[0][2 + r] = codes4_next(w);
+                        f[F::STEPS - 1][r] = codes4(w >> 8);
+                        f[F::STEPS - 1][2 + r] = codes4_next(w >> 8);
+                    } else {
+                        uint32_t w = lds<2>(row) ^ 0x8888u;  // elements (0, 2), (1, 3)
+                        w |= w << 8;
+                        f[0][r] = codes4(w);
+                        f[0][2 + r] = codes4_next(w);
+                    }
+                }
+#pragma unroll
+                for (int st = 0; st < F::STEPS; ++st)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int t = 0; t < QT; ++t)
+                            mma16816(c[nt], f[st], q[u * F::STEPS + st][nt][t][0], q[u * F::STEPS + st][nt][t][1]);
+                if (--left == 0) {
+                    const float s0 = in_ring<const float>(scales + g * 4);
+                    const float s1 = in_ring<const float>(scales + (8 * groups + g) * 4);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        l[half][nt][0] = fmaf(c[nt][0], s0, l[half][nt][0]);
+                        l[half][nt][1] = fmaf(c[nt][1], s0, l[half][nt][1]);
+                        l[half][nt][2] = fmaf(c[nt][2], s1, l[half][nt][2]);
+                        l[half][nt][3] = fmaf(c[nt][3], s1, l[half][nt][3]);
+                        c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+                    }
+                    left = group_units;
+                    ++g;
+                }
             }
         }
-        const bool ok0 = there >> gid & 1, ok1 = there >> (gid + 8) & 1;
         float grow[NT][2];
+        uint32_t w[2][NT][WT][2];  // p as columns
         bool grows = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[nt][i] = ok0 ? l[nt][i] * factor[nt][i] : -INFINITY;
-                l[nt][2 + i] = ok1 ? l[nt][2 + i] * factor[nt][i] : -INFINITY;
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l[half][nt][i] *= factor[nt][i & 1];
+            if (there != 0xffffffffu) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!(there >> (16 * half + 8 * (i >> 1) + gid) & 1)) l[half][nt][i] = -INFINITY;
             }
             if (a.logits) {
-                const int64_t j = j0 + int64_t(sub) * 16 + gid;
+                const int h = nt * 8 + tid * 2;
+                const int64_t j = j0 + int64_t(tile) * kAttnTile + gid;
+                float* to = attn_logits(a, p.s, p.pair, j) + h;
+                if (h < a.logit_heads) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int h = nt * 8 + tid * 2 + (i & 1);
-                    const int64_t at_j = j + (i >> 1) * 8;
-                    if (h < p.heads && at_j - j0 < positions)
-                        a.logits[(int64_t(p.s) * a.hq + p.q0 + h) * a.logit_stride + at_j] = l[nt][i];
+                    for (int k = 0; k < 4; ++k)
+                        if (j + 8 * k < j1)
+                            *reinterpret_cast<float2*>(to + 8 * k * a.logit_heads) =
+                                make_float2(l[k >> 1][nt][(k & 1) * 2], l[k >> 1][nt][(k & 1) * 2 + 1]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float most = fmaxf(l[nt][i], l[nt][2 + i]);
+                float most = fmaxf(fmaxf(l[0][nt][i], l[0][nt][2 + i]), fmaxf(l[1][nt][i], l[1][nt][2 + i]));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 4));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
@@ -368,10 +491,27 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 grow[nt][i] = exp2_approx(m[nt][i] - base);
                 grows |= most > m[nt][i];
                 m[nt][i] = most;
-                l[nt][i] = exp2_approx(l[nt][i] - base);
-                l[nt][2 + i] = exp2_approx(l[nt][2 + i] - base);
-                sum[nt][i] = fmaf(sum[nt][i], grow[nt][i], l[nt][i] + l[nt][2 + i]);
+                float add = 0.f;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    l[half][nt][i] = exp2_approx(l[half][nt][i] - base);
+                    l[half][nt][2 + i] = exp2_approx(l[half][nt][2 + i] - base);
+                    add += l[half][nt][i] + l[half][nt][2 + i];
+                }
+                sum[nt][i] = fmaf(sum[nt][i], grow[nt][i], add);
             }
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float x = l[half][nt][2 * r] * 0x1p8f, y = l[half][nt][2 * r + 1] * 0x1p8f;
+                    const uint32_t hi = half2_bits(x, y);
+                    w[half][nt][0][r] = transpose8(hi);
+                    if constexpr (WT == 2) {
+                        const float2 f = half2_floats(hi);
+                        w[half][nt][WT - 1][r] = transpose8(half2_bits(x - f.x, y - f.y));
+                    }
+                }
         }
         if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
@@ -384,87 +524,69 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                         for (int i = 0; i < 4; ++i) acc[u][t][nt][i] *= grow[nt][i & 1];
         }
 
-        // the values, a group's weights after another
-        const uint32_t v_from = at + v_at + tid * 2 * a.v_pitch + gid * F::VP * F::BITS / 8;
-        uint32_t w[NT][WT][2];
-        left = 0;
-        g = 0;
-        float raise = 1.f;
-        int now = 0;
+        // the values, half a tile after the other
 #pragma unroll
-        for (int u = 0; u < F::UNITS; ++u) {
-            if (u >= units) break;
-            if (left == 0) {
-                const uint32_t of_group = scales + (groups + g) * 64;
-                const float s0 = in_ring<const float>(of_group), s1 = in_ring<const float>(of_group + 32);
-                const uint32_t b0 = __float_as_uint(s0), b1 = __float_as_uint(s1);
-                const uint32_t most = __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
-                now = max(top[u], most == 0u ? -1000 : max(int(most >> 23), 1) - 126);
-                raise = now > top[u] && top[u] > -1000 ? exp2f(float(top[u] - now)) : 1.f;
-                // in two steps: the power itself may be none of float32's
-                const int up = now == -1000 ? 0 : 14 - now, half_up = up / 2;
-                const float up0 = __uint_as_float(uint32_t(127 + half_up) << 23);
-                const float up1 = __uint_as_float(uint32_t(127 + up - half_up) << 23);
-                const float t0 = s0 * up0 * up1, t1 = s1 * up0 * up1;
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t v_from = at + v_at + (16 * half + tid * 2) * a.v_pitch + gid * F::VP * F::BITS / 8;
+            uint32_t b[NT][WT][2];
+            int left = 0, g = 0;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float x[4] = {l[nt][0] * t0, l[nt][1] * t0, l[nt][2] * t1, l[nt][3] * t1};
-                    uint32_t lo = half2_bits(x[0], x[1]), hi = half2_bits(x[2], x[3]);
-                    w[nt][0][0] = transpose8(lo);
-                    w[nt][0][1] = transpose8(hi);
-                    if constexpr (WT == 2) {
-                        const float2 r0 = half2_floats(lo), r1 = half2_floats(hi);
-                        w[nt][WT - 1][0] = transpose8(half2_bits(x[0] - r0.x, x[1] - r0.y));
-                        w[nt][WT - 1][1] = transpose8(half2_bits(x[2] - r1.x, x[3] - r1.y));
+            for (int u = 0; u < F::UNITS; ++u) {
+                if (u >= units) break;
+                if (left == 0) {
+                    // p times the scales of positions 2 tid and 2 tid + 1, and of 8 further
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t of = sm.half_scales + (g * 32 + 16 * half + 8 * r + 2 * tid) * 2;
+                        const uint32_t hi = in_ring<const uint32_t>(of);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) b[nt][0][r] = mul_half2(w[half][nt][0][r], hi);
+                        if constexpr (WT == 2) {
+                            // what the product lost, and the products with the second factors
+                            const uint32_t lo = in_ring<const uint32_t>(of + groups * 64);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t lost = fma_half2(w[half][nt][0][r], hi, b[nt][0][r] ^ 0x80008000u);
+                                b[nt][WT - 1][r] = fma_half2(w[half][nt][0][r], lo, fma_half2(w[half][nt][WT - 1][r], hi, lost));
+                            }
+                        }
+                    }
+                    left = group_units;
+                    ++g;
+                }
+                --left;
+                // elements of this lane's piece as pairs of positions (2 tid, 2 tid + 1) and 8 further
+                uint32_t f[F::TILES][4];
+                const uint32_t from = v_from + u * (F::UNIT * F::BITS / 8);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t row = from + r * 8 * a.v_pitch;
+                    const uint32_t x = lds<F::VP * F::BITS / 8>(row), y = lds<F::VP * F::BITS / 8>(row + a.v_pitch);
+                    if constexpr (F::BITS == 8) {
+                        codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
+                        if constexpr (F::TILES == 2)
+                            codes8<F::KIND>(__byte_perm(x, y, 0x7362), f[F::TILES - 1][2 * r], f[F::TILES - 1][2 * r + 1]);
+                    } else {
+                        const uint32_t v = __byte_perm(x, y, 0x5410) ^ (F::TILES == 2 ? 0x88888888u : 0x00880088u);
+                        f[0][2 * r] = codes4(v);
+                        f[0][2 * r + 1] = codes4_next(v);
+                        if constexpr (F::TILES == 2) {
+                            f[F::TILES - 1][2 * r] = codes4(v >> 8);
+                            f[F::TILES - 1][2 * r + 1] = codes4_next(v >> 8);
+                        }
                     }
                 }
-                left = group_units;
-                ++g;
-            }
-            --left;
-            top[u] = now;
-            if (raise != 1.f) {
 #pragma unroll
                 for (int t = 0; t < F::TILES; ++t)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[u][t][nt][i] *= raise;
+                        for (int k = 0; k < WT; ++k) mma16816(acc[u][t][nt], f[t], b[nt][k][0], b[nt][k][1]);
             }
-            // elements of this lane's piece as pairs of positions (2 tid, 2 tid + 1) and 8 further
-            uint32_t f[F::TILES][4];
-            const uint32_t from = v_from + u * (F::UNIT * F::BITS / 8);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t row = from + r * 8 * a.v_pitch;
-                const uint32_t x = lds<F::VP * F::BITS / 8>(row), y = lds<F::VP * F::BITS / 8>(row + a.v_pitch);
-                if constexpr (F::BITS == 8 && F::TILES == 2) {
-                    codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
-                    codes8<F::KIND>(__byte_perm(x, y, 0x7362), f[F::TILES - 1][2 * r], f[F::TILES - 1][2 * r + 1]);
-                } else if constexpr (F::BITS == 8) {
-                    codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
-                } else if constexpr (F::TILES == 2) {
-                    const uint32_t b = (x | y << 16) ^ 0x88888888u;
-                    f[0][2 * r] = codes4(b);
-                    f[0][2 * r + 1] = codes4(b >> 4);
-                    f[F::TILES - 1][2 * r] = codes4(b >> 8);
-                    f[F::TILES - 1][2 * r + 1] = codes4(b >> 12);
-                } else {
-                    const uint32_t b = (x | y << 16) ^ 0x00880088u;
-                    f[0][2 * r] = codes4(b);
-                    f[0][2 * r + 1] = codes4(b >> 4);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < F::TILES; ++t)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < WT; ++k) mma16816(acc[u][t][nt], f[t], w[nt][k][0], w[nt][k][1]);
         }
         __syncwarp();
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
-
     // ---- what the piece comes to ----
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -482,15 +604,13 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (u >= units) break;
-                const int down = top[u] == -1000 ? 0 : top[u] - 14, half_down = down / 2;
-                const float d0 = __uint_as_float(uint32_t(127 + half_down) << 23) * scale;
-                const float d1 = __uint_as_float(uint32_t(127 + down - half_down) << 23);
+                const float d0 = __uint_as_float(uint32_t(127 + top[u]) << 23) * scale;
                 const int at = u * F::UNIT + gid * F::VP;
                 float v[F::VP];
 #pragma unroll
                 for (int t = 0; t < F::TILES; ++t) {
-                    v[2 * t] = acc[u][t][nt][i] * d0 * d1;
-                    v[2 * t + 1] = acc[u][t][nt][2 + i] * d0 * d1;
+                    v[2 * t] = acc[u][t][nt][i] * 0x1p-14f * d0;
+                    v[2 * t + 1] = acc[u][t][nt][2 + i] * 0x1p-14f * d0;
                 }
                 if (!p.whole) {
                     if constexpr (F::VP == 4) *reinterpret_cast<float4*>(part + at) = make_float4(v[0], v[1], v[F::VP - 2], v[F::VP - 1]);
@@ -526,36 +646,41 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 }
 
 template <typename T, typename F>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_mma_kernel(const AttnArgs a) {
-    __shared__ int64_t pre[kAttnSequences + 1], sums[kAttnWarps];
+__host__ __device__ constexpr uint32_t attn_warp_bytes(uint32_t stage, int groups) {
+    return F::STAGES * stage + kAttnPlaces + kAttnThere + (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * groups * 64;
+}
+
+template <typename T, typename F>
+__global__ void __launch_bounds__(32 * F::WARPS, 1) attn_mma_kernel(const AttnArgs a) {
+    __shared__ AttnTable table;
     pdl_next();
-    attn_prefix(a, pre, sums);
-    if (blockIdx.x == 0)
-        for (int s = int(threadIdx.x); s <= a.sequences; s += kAttnThreads) a.prefix[s] = pre[s];
-    attn_empty<T>(a, pre);
+    attn_table(a, table);
+    attn_empty<T>(a, table);
     const int groups = a.d / a.cache.group, warp = threadIdx.x >> 5;
     AttnSmem sm;
     sm.bytes = attn_stage_bytes(a.k_pitch, a.v_pitch, groups);
-    sm.stage = uint32_t(warp) * (F::STAGES * sm.bytes + kAttnPlaces);
+    sm.stage = uint32_t(warp) * attn_warp_bytes<T, F>(sm.bytes, groups);
     sm.places = sm.stage + F::STAGES * sm.bytes;
-    if (warp >= a.workers / int(gridDim.x)) return;
-    attn_pieces(a, pre, int64_t(warp) * gridDim.x + blockIdx.x,
+    sm.there = sm.places + kAttnPlaces;
+    sm.half_scales = sm.there + kAttnThere;
+    attn_pieces(a, table, warp * int(gridDim.x) + int(blockIdx.x),
                 [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
 }
 
 template <typename T, typename F>
 nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&attn_mma_kernel<T, F>);
-    const size_t warp = F::STAGES * attn_stage_bytes(a.k_pitch, a.v_pitch, a.d / a.cache.group) + kAttnPlaces;
-    // as many workers to an SM as have room for their rings beside the lengths (rows of 256 bytes: 7; 16 scales: 6)
-    const size_t room = size_t(dev->max_smem_optin) - (kAttnSequences + 1 + kAttnWarps) * 8 - 64;
-    const int warps = int(std::min<size_t>(kAttnWarps, room / warp));
+    const int groups = a.d / a.cache.group;
+    const size_t warp = attn_warp_bytes<T, F>(attn_stage_bytes(a.k_pitch, a.v_pitch, groups), groups);
+    // as many workers to an SM as have room for their rings beside the table
+    const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 64;
+    const int warps = int(std::min<size_t>(F::WARPS, room / warp));
     a.workers = dev->sms * warps;
     const size_t smem = warps * warp;
     nrm_status st = prepare_kernel(fn, smem, false);
     if (st != NRM_OK) return st;
     void* p[] = {&a};
-    return launch_pdl(fn, dim3(unsigned(dev->sms)), dim3(kAttnThreads), p, s, smem);
+    return launch_pdl(fn, dim3(unsigned(dev->sms)), dim3(unsigned(32 * warps)), p, s, smem);
 }
 
 // One translation unit for each storage type and stored form.
@@ -571,8 +696,8 @@ nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     a.v_pitch = (a.row_bytes + 15) / 16 * 16;
     if (a.v_pitch / 16 % 2 == 0) a.v_pitch += 16;
     const int nt = a.d <= 128 && a.shared > 8 ? 2 : 1;
-    a.heads = a.shared < 8 * nt ? a.shared : 8 * nt;
-    a.chunks = (a.shared + a.heads - 1) / a.heads;
+    attn_chunks(a, 8 * nt);
+    a.pages = a.cache.slots / a.cache.page.d;
     if (a.d > 128)
         return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 256, 1>>(a, dev, s)
                     : attn_mma_launch<T, AttnForm<KIND, 16, 256, 1>>(a, dev, s);
