@@ -31,6 +31,9 @@
 
 namespace nrm {
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
 // n bytes, and zeros for the rest.
 __device__ __forceinline__ void cp_async_8_or_0(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
@@ -104,16 +107,19 @@ __device__ __forceinline__ uint32_t codes4_next(uint32_t v) {
     return r;
 }
 
-// What a kernel is made for: the stored form, elements of a unit of a row (every group is whole units of 32, or of
-// 16), the longest rows, and eights of heads.
-template <int KIND_, int UNIT_, int DMAX_, int NT_>
+// What a kernel is made for: the stored form, rows of UNITS units of 32 or 16 elements (every group is whole units;
+// EXACT: of no fewer), and eights of heads.  With the count known the products of a tile are one block of
+// instructions, which the loops' ends would cut in pieces too short to fill the waits.
+template <int KIND_, int UNIT_, int UNITS_, int NT_, bool EXACT_ = true>
 struct AttnForm {
-    static constexpr int KIND = KIND_, UNIT = UNIT_, DMAX = DMAX_, NT = NT_;
-    static constexpr int UNITS = DMAX / UNIT, STEPS = UNIT / 16, TILES = UNIT / 16;
+    static constexpr int KIND = KIND_, UNIT = UNIT_, UNITS = UNITS_, NT = NT_, DMAX = UNIT * UNITS;
+    static constexpr bool EXACT = EXACT_;
+    static constexpr int STEPS = UNIT / 16, TILES = UNIT / 16;
     static constexpr int KP = UNIT / 4, VP = UNIT / 8;  // elements of a lane's piece of a unit
     static constexpr int BITS = KIND == NRM_CACHE_INT4 ? 4 : 8;
-    static constexpr int WARPS = DMAX == 128 && NT == 1 ? 12 : 8;  // by the registers that a thread needs
-    static constexpr int STAGES = BITS == 4 && DMAX == 128 ? 3 : 2;
+    static constexpr int WARPS = DMAX <= 128 && NT == 1 ? 12 : 8;  // by the registers that a thread needs
+    static constexpr int STAGES = BITS == 4 && DMAX <= 128 ? 3 : 2;
+    static constexpr int CHUNKS = DMAX * BITS / 8 % 16 == 0 ? DMAX * BITS / 8 / 16 : 0;  // 16-byte vectors of a row
 };
 
 // A warp's shared memory: stages (keys, values, scales of both), then the places of two tiles' rows, which positions
@@ -122,7 +128,7 @@ struct AttnSmem {
     uint32_t stage, bytes;     // of the first stage; of one
     uint32_t places;           // [2][32] code offsets
     uint32_t there;            // [stages]
-    uint32_t half_scales;      // [factors][groups][32]
+    uint32_t half_scales;      // [factors][units][32]
 };
 __host__ __device__ inline uint32_t attn_stage_bytes(int k_pitch, int v_pitch, int groups) {
     return uint32_t(32 * (k_pitch + v_pitch) + 2 * 32 * groups * 4);
@@ -146,7 +152,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
     constexpr int NT = F::NT, QT = sizeof(T) == 4 ? 2 : 1, WT = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
     constexpr int KSTEPS = F::DMAX / 16, S = F::STAGES;
     const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
-    const int units = a.d / F::UNIT, group_units = a.cache.group / F::UNIT;
+    const int units = F::EXACT ? F::UNITS : a.d / F::UNIT;
+    int of_unit[F::UNITS];  // a unit's scale in its row's, in bytes
+#pragma unroll
+    for (int u = 0; u < F::UNITS; ++u) of_unit[u] = u * F::UNIT / a.cache.group * 4;
 
     // ---- the copies: a tile to a stage ----
     const int64_t j0 = p.lo + int64_t(p.tile0) * kAttnTile;
@@ -183,25 +192,22 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         __syncwarp();
         const uint32_t to = ring + sm.stage + uint32_t(stage) * sm.bytes;
         int row = first_row, chunk = first_chunk;
-        uint32_t from = places + row * 8, k = to + row * a.k_pitch + chunk * a.vec, v = to + v_at + row * a.v_pitch + chunk * a.vec;
-        if (a.vec == 16 && chunk_step == 0 && m == 0xffffffffu) {
-            // a lane's vectors are one column of the rows: eight lanes of neighbours copy a row of 128 bytes
-            const unsigned char *kc = a.cache.codes[0] + chunk * 16, *vc = a.cache.codes[1] + chunk * 16;
-#pragma unroll 4
-            for (int i = 0; i < chunks; ++i) {
-                const int64_t at = in_ring<const int64_t>(from);
-                cp_async_16_or_0(k, kc + at, 16);
-                cp_async_16_or_0(v, vc + at, 16);
-                from += row_step * 8;
-                k += row_step * a.k_pitch;
-                v += row_step * a.v_pitch;
+        if (F::EXACT && F::CHUNKS > 0 && a.vec == 16 && m == 0xffffffffu) {
+            // neighbouring lanes copy neighbouring vectors of a row
+            constexpr int C = F::CHUNKS > 0 ? F::CHUNKS : 1;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
+                const int64_t at = in_ring<const int64_t>(places + r * 8) + c * 16;
+                cp_async_16(to + r * a.k_pitch + c * 16, a.cache.codes[0] + at);
+                cp_async_16(to + v_at + r * a.v_pitch + c * 16, a.cache.codes[1] + at);
             }
         } else {
+#pragma unroll 1
             for (int i = 0; i < chunks; ++i) {
                 const int64_t at = in_ring<const int64_t>(places + row * 8) + chunk * a.vec;
                 const int n = m >> row & 1 ? a.vec : 0;
-                k = to + row * a.k_pitch + chunk * a.vec;
-                v = to + v_at + row * a.v_pitch + chunk * a.vec;
+                const uint32_t k = to + row * a.k_pitch + chunk * a.vec, v = to + v_at + row * a.v_pitch + chunk * a.vec;
                 if (a.vec == 16) {
                     cp_async_16_or_0(k, a.cache.codes[0] + at, n);
                     cp_async_16_or_0(v, a.cache.codes[1] + at, n);
@@ -253,7 +259,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
         for (int u = 0; u < F::UNITS; ++u) {
             const int at = u * F::UNIT + tid * F::KP;
-            const bool there = h < p.heads && u < units;
+            const bool there = h < p.heads && (F::EXACT || u < units);
             if (there && a.q_vec) {
                 constexpr int B = F::KP * int(sizeof(T));  // 8, 16 or 32 bytes
                 uint32_t w[B / 4];
@@ -335,34 +341,22 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         // the values' scales in fp16, this lane's position's; seldom one is larger than all before it
         {
             const uint32_t mine = at + s_at + (32 + lane) * groups * 4;
+            float mine_of[F::UNITS];
             bool larger = false;
-            int left = 0, g = 0;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
-                if (u >= units) break;
-                if (left == 0) {
-                    larger |= in_ring<const float>(mine + g * 4) >= (top[u] < -126 ? -1.f : __uint_as_float(uint32_t(127 + top[u]) << 23));
-                    left = group_units;
-                    ++g;
-                }
-                --left;
+                if (!F::EXACT && u >= units) break;
+                mine_of[u] = in_ring<const float>(mine + of_unit[u]);
+                larger |= mine_of[u] >= (top[u] < -126 ? -1.f : __uint_as_float(uint32_t(127 + top[u]) << 23));
             }
             if (__any_sync(0xffffffffu, larger)) {
-                left = g = 0;
-                float raise = 1.f;
-                int now = 0;
 #pragma unroll
                 for (int u = 0; u < F::UNITS; ++u) {
-                    if (u >= units) break;
-                    if (left == 0) {
-                        const uint32_t b = in_ring<const uint32_t>(mine + g * 4);
-                        const uint32_t most = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
-                        now = min(127, max(max(top[u], -100), int(most >> 23) - 126));
-                        raise = exp2f(float(max(top[u] - now, -126)));
-                        left = group_units;
-                        ++g;
-                    }
-                    --left;
+                    if (!F::EXACT && u >= units) break;
+                    const uint32_t b = __float_as_uint(mine_of[u]);
+                    const uint32_t most = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
+                    const int now = min(127, max(max(top[u], -100), int(most >> 23) - 126));
+                    const float raise = exp2f(float(max(top[u] - now, -126)));
                     top[u] = now;
 #pragma unroll
                     for (int t = 0; t < F::TILES; ++t)
@@ -372,20 +366,14 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                             for (int i = 0; i < 4; ++i) acc[u][t][nt][i] *= raise;
                 }
             }
-            left = g = 0;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
-                if (u >= units) break;
-                if (left == 0) {
-                    const float s = in_ring<const float>(mine + g * 4) * __uint_as_float(uint32_t(127 + 6 - top[u]) << 23);
-                    const __half hi = __float2half_rn(s);
-                    in_ring<__half>(sm.half_scales + (g * 32 + lane) * 2) = hi;
-                    if constexpr (WT == 2)
-                        in_ring<__half>(sm.half_scales + ((groups + g) * 32 + lane) * 2) = __float2half_rn(s - __half2float(hi));
-                    left = group_units;
-                    ++g;
-                }
-                --left;
+                if (!F::EXACT && u >= units) break;
+                const float s = mine_of[u] * __uint_as_float(uint32_t(127 + 6 - top[u]) << 23);
+                const __half hi = __float2half_rn(s);
+                in_ring<__half>(sm.half_scales + (u * 32 + lane) * 2) = hi;
+                if constexpr (WT == 2)
+                    in_ring<__half>(sm.half_scales + ((F::UNITS + u) * 32 + lane) * 2) = __float2half_rn(s - __half2float(hi));
             }
             __syncwarp();
         }
@@ -393,20 +381,12 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         // logits of positions gid, gid + 8, gid + 16 and gid + 24: [half of the tile][head, head + 1, 8 further]
         float l[2][NT][4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const uint32_t k_at = at + (16 * half + gid) * a.k_pitch + tid * (F::KP * F::BITS / 8);
-            const uint32_t scales = at + s_at + (16 * half + gid) * groups * 4;
-            float c[NT][4];
+        for (int u = 0; u < F::UNITS; ++u) {
+            if (!F::EXACT && u >= units) break;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) l[half][nt][i] = c[nt][i] = 0.f;
-            int left = group_units, g = 0;
-#pragma unroll
-            for (int u = 0; u < F::UNITS; ++u) {
-                if (u >= units) break;
+            for (int half = 0; half < 2; ++half) {
                 uint32_t f[F::STEPS][4];
-                const uint32_t from = k_at + u * (F::UNIT * F::BITS / 8);
+                const uint32_t from = at + (16 * half + gid) * a.k_pitch + tid * (F::KP * F::BITS / 8) + u * (F::UNIT * F::BITS / 8);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t row = from + r * 8 * a.k_pitch;
@@ -429,26 +409,19 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                         f[0][2 + r] = codes4_next(w);
                     }
                 }
+                const uint32_t scales = at + s_at + (16 * half + gid) * groups * 4 + of_unit[u];
+                const float s0 = in_ring<const float>(scales), s1 = in_ring<const float>(scales + 32 * groups);
 #pragma unroll
-                for (int st = 0; st < F::STEPS; ++st)
+                for (int nt = 0; nt < NT; ++nt) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int st = 0; st < F::STEPS; ++st)
 #pragma unroll
                         for (int t = 0; t < QT; ++t)
-                            mma16816(c[nt], f[st], q[u * F::STEPS + st][nt][t][0], q[u * F::STEPS + st][nt][t][1]);
-                if (--left == 0) {
-                    const float s0 = in_ring<const float>(scales + g * 4);
-                    const float s1 = in_ring<const float>(scales + (8 * groups + g) * 4);
+                            mma16816(c, f[st], q[u * F::STEPS + st][nt][t][0], q[u * F::STEPS + st][nt][t][1]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        l[half][nt][0] = fmaf(c[nt][0], s0, l[half][nt][0]);
-                        l[half][nt][1] = fmaf(c[nt][1], s0, l[half][nt][1]);
-                        l[half][nt][2] = fmaf(c[nt][2], s1, l[half][nt][2]);
-                        l[half][nt][3] = fmaf(c[nt][3], s1, l[half][nt][3]);
-                        c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-                    }
-                    left = group_units;
-                    ++g;
+                    for (int i = 0; i < 4; ++i)
+                        l[half][nt][i] = u == 0 ? c[i] * (i < 2 ? s0 : s1) : fmaf(c[i], i < 2 ? s0 : s1, l[half][nt][i]);
                 }
             }
         }
@@ -528,33 +501,27 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const uint32_t v_from = at + v_at + (16 * half + tid * 2) * a.v_pitch + gid * F::VP * F::BITS / 8;
-            uint32_t b[NT][WT][2];
-            int left = 0, g = 0;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
-                if (u >= units) break;
-                if (left == 0) {
-                    // p times the scales of positions 2 tid and 2 tid + 1, and of 8 further
+                if (!F::EXACT && u >= units) break;
+                // p times the scales of positions 2 tid and 2 tid + 1, and of 8 further
+                uint32_t b[NT][WT][2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t of = sm.half_scales + (g * 32 + 16 * half + 8 * r + 2 * tid) * 2;
-                        const uint32_t hi = in_ring<const uint32_t>(of);
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t of = sm.half_scales + (u * 32 + 16 * half + 8 * r + 2 * tid) * 2;
+                    const uint32_t hi = in_ring<const uint32_t>(of);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) b[nt][0][r] = mul_half2(w[half][nt][0][r], hi);
-                        if constexpr (WT == 2) {
-                            // what the product lost, and the products with the second factors
-                            const uint32_t lo = in_ring<const uint32_t>(of + groups * 64);
+                    for (int nt = 0; nt < NT; ++nt) b[nt][0][r] = mul_half2(w[half][nt][0][r], hi);
+                    if constexpr (WT == 2) {
+                        // what the product lost, and the products with the second factors
+                        const uint32_t lo = in_ring<const uint32_t>(of + F::UNITS * 64);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint32_t lost = fma_half2(w[half][nt][0][r], hi, b[nt][0][r] ^ 0x80008000u);
-                                b[nt][WT - 1][r] = fma_half2(w[half][nt][0][r], lo, fma_half2(w[half][nt][WT - 1][r], hi, lost));
-                            }
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t lost = fma_half2(w[half][nt][0][r], hi, b[nt][0][r] ^ 0x80008000u);
+                            b[nt][WT - 1][r] = fma_half2(w[half][nt][0][r], lo, fma_half2(w[half][nt][WT - 1][r], hi, lost));
                         }
                     }
-                    left = group_units;
-                    ++g;
                 }
-                --left;
                 // elements of this lane's piece as pairs of positions (2 tid, 2 tid + 1) and 8 further
                 uint32_t f[F::TILES][4];
                 const uint32_t from = v_from + u * (F::UNIT * F::BITS / 8);
@@ -603,7 +570,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             float* part = a.part + p.part + h * attn_part_row(a.d);
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
-                if (u >= units) break;
+                if (!F::EXACT && u >= units) break;
                 const float d0 = __uint_as_float(uint32_t(127 + top[u]) << 23) * scale;
                 const int at = u * F::UNIT + gid * F::VP;
                 float v[F::VP];
@@ -646,8 +613,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 }
 
 template <typename T, typename F>
-__host__ __device__ constexpr uint32_t attn_warp_bytes(uint32_t stage, int groups) {
-    return F::STAGES * stage + kAttnPlaces + kAttnThere + (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * groups * 64;
+__host__ __device__ constexpr uint32_t attn_warp_bytes(uint32_t stage) {
+    return F::STAGES * stage + kAttnPlaces + kAttnThere + (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * F::UNITS * 64;
 }
 
 template <typename T, typename F>
@@ -659,7 +626,7 @@ __global__ void __launch_bounds__(32 * F::WARPS, 1) attn_mma_kernel(const AttnAr
     const int groups = a.d / a.cache.group, warp = threadIdx.x >> 5;
     AttnSmem sm;
     sm.bytes = attn_stage_bytes(a.k_pitch, a.v_pitch, groups);
-    sm.stage = uint32_t(warp) * attn_warp_bytes<T, F>(sm.bytes, groups);
+    sm.stage = uint32_t(warp) * attn_warp_bytes<T, F>(sm.bytes);
     sm.places = sm.stage + F::STAGES * sm.bytes;
     sm.there = sm.places + kAttnPlaces;
     sm.half_scales = sm.there + kAttnThere;
@@ -671,7 +638,7 @@ template <typename T, typename F>
 nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&attn_mma_kernel<T, F>);
     const int groups = a.d / a.cache.group;
-    const size_t warp = attn_warp_bytes<T, F>(attn_stage_bytes(a.k_pitch, a.v_pitch, groups), groups);
+    const size_t warp = attn_warp_bytes<T, F>(attn_stage_bytes(a.k_pitch, a.v_pitch, groups));
     // as many workers to an SM as have room for their rings beside the table
     const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 64;
     const int warps = int(std::min<size_t>(F::WARPS, room / warp));
@@ -698,14 +665,23 @@ nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const int nt = a.d <= 128 && a.shared > 8 ? 2 : 1;
     attn_chunks(a, 8 * nt);
     a.pages = a.cache.slots / a.cache.page.d;
-    if (a.d > 128)
-        return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 256, 1>>(a, dev, s)
-                    : attn_mma_launch<T, AttnForm<KIND, 16, 256, 1>>(a, dev, s);
-    if (nt == 2)
-        return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 128, 2>>(a, dev, s)
-                    : attn_mma_launch<T, AttnForm<KIND, 16, 128, 2>>(a, dev, s);
-    return wide ? attn_mma_launch<T, AttnForm<KIND, 32, 128, 1>>(a, dev, s)
-                : attn_mma_launch<T, AttnForm<KIND, 16, 128, 1>>(a, dev, s);
+    // rows of the usual lengths have kernels of their own; of others, one for all
+    const int units = a.d / (wide ? 32 : 16);
+    switch (wide ? units : 100 + units) {
+    case 2: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 32, 2, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 32, 2, 1>>(a, dev, s);
+    case 3: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 32, 3, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 32, 3, 1>>(a, dev, s);
+    case 4: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 32, 4, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 32, 4, 1>>(a, dev, s);
+    case 5: return attn_mma_launch<T, AttnForm<KIND, 32, 5, 1>>(a, dev, s);
+    case 8: return attn_mma_launch<T, AttnForm<KIND, 32, 8, 1>>(a, dev, s);
+    case 104: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 16, 4, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 16, 4, 1>>(a, dev, s);
+    case 105: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 16, 5, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 16, 5, 1>>(a, dev, s);
+    case 106: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 16, 6, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 16, 6, 1>>(a, dev, s);
+    case 110: return attn_mma_launch<T, AttnForm<KIND, 16, 10, 1>>(a, dev, s);
+    default: break;
+    }
+    attn_chunks(a, 8);
+    a.v_pitch = a.k_pitch = (a.row_bytes + 15) / 16 % 2 ? (a.row_bytes + 15) / 16 * 16 : (a.row_bytes + 31) / 16 * 16;
+    return attn_mma_launch<T, AttnForm<KIND, 16, 16, 1, false>>(a, dev, s);
 }
 
 }  // namespace nrm
