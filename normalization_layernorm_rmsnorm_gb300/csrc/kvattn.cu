@@ -21,16 +21,18 @@ nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
     } else {
         attn_chunks(a, kAttnScalarHeads);
         a.workers = dev->sms * (kAttnThreads / 32);
+        attn_snap(a);
         st = launch_pdl(reinterpret_cast<const void*>(&attn_scalar_kernel<T>), dim3(unsigned(dev->sms)),
                         dim3(kAttnThreads), p, s);
     }
     if (st != NRM_OK) return st;
-    // sequences of one tile are never cut
-    if (a.cap > kAttnTile && (a.window == 0 || a.window > kAttnTile)) {
+    // unless no sequence can be cut
+    if (attn_most_tiles(a) > a.snap) {
         // a CTA for each head where there are too few pairs to fill the GPU
         const int pairs = a.sequences * a.hk * a.chunks;
+        const bool few = pairs < dev->sms;
         st = launch_pdl(reinterpret_cast<const void*>(&attn_join_kernel<T>),
-                        dim3(unsigned(pairs), pairs < dev->sms ? unsigned(a.heads) : 1u), dim3(32 * kJoinWarps), p, s);
+                        dim3(unsigned(pairs), few ? unsigned(a.heads) : 1u), dim3(few ? 32 * kJoinWarps : 128), p, s);
         if (st != NRM_OK) return st;
     }
     if (!a.weights) return NRM_OK;

@@ -128,10 +128,17 @@ __device__ __forceinline__ void attn_pieces(const AttnArgs& a, const AttnTable& 
     const int total = table.pre[a.sequences] * pairs;
     const AttnShares shares(a, total);
     if (w >= shares.used) return;
-    int t = shares.begin(w);
-    const int end = shares.begin(w + 1);
+    // a share's end, moved to the beginning of the pair that it would cut where that is short
+    auto edge = [&](int t, int& s) {
+        s = attn_sequence(table.pre, a.sequences, t / pairs);
+        while (t < total && table.pre[s + 1] * pairs <= t) ++s;
+        const int tiles = table.pre[s + 1] - table.pre[s], at = t - table.pre[s] * pairs;
+        return t < total && tiles <= a.snap ? t - at % tiles : t;
+    };
+    int s, s_end;
+    int t = edge(shares.begin(w), s);
+    const int end = edge(shares.begin(w + 1), s_end);
     if (t >= end) return;
-    int s = attn_sequence(table.pre, a.sequences, t / pairs);
     while (t < end) {
         while (table.pre[s + 1] * pairs <= t) ++s;  // (sequences without tiles are passed over)
         const int tiles = table.pre[s + 1] - table.pre[s], at = t - table.pre[s] * pairs;
@@ -309,11 +316,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
     constexpr int E = kHeadMaxD / 128, AHEAD = 4;
     __shared__ float4 joined[kJoinWarps][kHeadMaxD / 4];
     __shared__ float sums[kJoinWarps];
+    const int warps = int(blockDim.x) >> 5;
     pdl_next();
     const int pairs = a.hk * a.chunks;
     const int s = int(blockIdx.x) / pairs, pair = int(blockIdx.x) - s * pairs;
     const int before = ld_after(a.prefix + s), tiles = ld_after(a.prefix + s + 1) - before;
-    if (tiles <= 1) return;
+    if (tiles <= a.snap) return;
     const int t0 = before * pairs + pair * tiles;
     const AttnShares shares(a, ld_after(a.prefix + a.sequences) * pairs);
     const int w0 = shares.owner(t0), w1 = shares.owner(t0 + tiles - 1);
@@ -322,7 +330,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
     const int heads = min(a.heads, a.shared - chunk * a.heads), q0 = head * a.shared + chunk * a.heads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // heads of this CTA, in rounds of as many as have warps of their own
-    const int mine = gridDim.y > 1 ? 1 : heads, at_once = min(mine, kJoinWarps), each = kJoinWarps / at_once;
+    const int mine = gridDim.y > 1 ? 1 : heads, at_once = min(mine, warps), each = warps / at_once;
     const int group = warp / each, in_group = warp - group * each;
     for (int h0 = 0; h0 < mine; h0 += at_once) {
         const int h = gridDim.y > 1 ? int(blockIdx.y) : h0 + group;

@@ -48,7 +48,7 @@ struct AttnArgs {
     int min_tiles;            // of a worker that is used, but for the last
     // on matrix instructions
     int row_bytes, vec;       // of a row of codes, copied in vectors of 16 or 8 bytes
-    int k_pitch, v_pitch;     // of a row in shared memory
+    int snap;                 // pairs of at most so many tiles are not cut
     int q_vec, out_vec;       // queries and outputs are aligned to 16 bytes
     int scale_vec;            // a row's scales are whole aligned 16 bytes
     int64_t pages;
@@ -60,6 +60,17 @@ inline void attn_chunks(AttnArgs& a, int most) {
     a.chunks = (a.shared + most - 1) / most;
     a.heads = (a.shared + a.chunks - 1) / a.chunks;
     a.logit_heads = (a.heads + 1) / 2 * 2;
+}
+// Tiles of a sequence, at most.
+inline int attn_most_tiles(const AttnArgs& a) {
+    const int64_t seen = a.window > 0 && a.window < a.cap ? a.window : a.cap;
+    return int((seen + kAttnTile - 1) / kAttnTile);
+}
+// Where there are pairs for half of the workers, short ones are left whole: a worker then takes up to 8 tiles where it
+// would have taken 1, but nothing has to be joined.  (250 sequences of 60 positions: cut, the joining took as long as
+// the rest.)  Otherwise those of one tile, which cannot be cut.
+inline void attn_snap(AttnArgs& a) {
+    a.snap = 2 * int64_t(a.sequences) * a.hk * a.chunks >= a.workers ? 8 : 1;
 }
 // Floats of one partial result: accumulator, maximum and sum of each head, in whole 16 bytes.
 __host__ __device__ inline int64_t attn_part_row(int d) { return (int64_t(d) + 2 + 3) / 4 * 4; }

@@ -3,8 +3,9 @@
 // Both products are m16n8k16 with fp16 factors and fp32 sums, the query heads of
 // a pair as the eight columns: logits = codes of 16 keys [16 x d] * queries [d x
 // 8], and out^T = codes of 16 values [d x 16] * weights [16 x 8].  A code is
-// exact in fp16 in every stored form; the keys' scales multiply the logits, the
-// values' the weights.  Queries are scaled by a power of two to at most 2^15:
+// exact in fp16 in every stored form (an integer is taken with a bias, which one more
+// product takes off again, as one of fp16's smallest numbers, so that it costs no
+// conversion); the keys' scales multiply the logits, the values' the weights.  Queries are scaled by a power of two to at most 2^15:
 // those of 16 bits then are exact, of float32 ones the rest is a second factor
 // (22 bits).  A weight is p*2^8 times its value's scale, the largest scale seen
 // brought below 2^6, all in fp16: 11 bits down to 2^-28 of the largest; where
@@ -31,9 +32,6 @@
 
 namespace nrm {
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
 // n bytes, and zeros for the rest.
 __device__ __forceinline__ void cp_async_8_or_0(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
@@ -75,17 +73,12 @@ __device__ __forceinline__ uint32_t lds(uint32_t at) {
 }
 
 // Codes as pairs of fp16.
-__device__ __forceinline__ uint32_t add_half2(uint32_t v, uint32_t bias) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(bias));
-    return r;
-}
 __device__ __forceinline__ uint32_t e4m3x2_halves(uint32_t v) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(v)));
     return h;
 }
-// Four 8-bit codes: bytes (0, 1) and (2, 3).  int8: the byte above 1024 in fp16, taken off again.
+// Four 8-bit codes: bytes (0, 1) and (2, 3).  Integers: the byte plus 128, as fp16's smallest numbers (2^-24 of it).
 template <int KIND>
 __device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
     if constexpr (KIND == NRM_CACHE_E4M3) {
@@ -93,19 +86,13 @@ __device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
         hi = e4m3x2_halves(v >> 16);
     } else {
         v ^= 0x80808080u;
-        lo = add_half2(__byte_perm(v, 0x64646464u, 0x4140), 0xe480e480u);  // - 1152
-        hi = add_half2(__byte_perm(v, 0x64646464u, 0x4342), 0xe480e480u);
+        lo = __byte_perm(v, 0, 0x4140);
+        hi = __byte_perm(v, 0, 0x4342);
     }
 }
-// The 4-bit codes at the low ends of both halves (already turned by 8), and those above them (16 times as large).
-__device__ __forceinline__ uint32_t codes4(uint32_t v) {
-    return add_half2((v & 0x000f000fu) | 0x64006400u, 0xe408e408u);  // - 1032
-}
-__device__ __forceinline__ uint32_t codes4_next(uint32_t v) {
-    uint32_t r;  // / 16 - 72
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
-    return r;
-}
+// The 4-bit codes (plus 8) at the low ends of both halves, 2^-24 of them, and those above, 2^-20 of them.
+__device__ __forceinline__ uint32_t codes4(uint32_t v) { return v & 0x000f000fu; }
+__device__ __forceinline__ uint32_t codes4_next(uint32_t v) { return v & 0x00f000f0u; }
 
 // What a kernel is made for: the stored form, rows of UNITS units of 32 or 16 elements (every group is whole units;
 // EXACT: of no fewer), and eights of heads.  With the count known the products of a tile are one block of
@@ -119,21 +106,37 @@ struct AttnForm {
     static constexpr int BITS = KIND == NRM_CACHE_INT4 ? 4 : 8;
     static constexpr int WARPS = DMAX <= 128 && NT == 1 ? 12 : 8;  // by the registers that a thread needs
     static constexpr int STAGES = BITS == 4 && DMAX <= 128 ? 3 : 2;
-    static constexpr int CHUNKS = DMAX * BITS / 8 % 16 == 0 ? DMAX * BITS / 8 / 16 : 0;  // 16-byte vectors of a row
+    static constexpr int ROW = DMAX * BITS / 8;
+    static constexpr int CHUNKS = ROW % 16 == 0 ? ROW / 16 : 0;  // 16-byte vectors of a row
+    // rows in shared memory: an odd number of 32 bytes (a key's fragment of 8 bytes a lane, 4 rows at a time) or of 16
+    // (else) apart, the fragments' reads meet no bank twice
+    static constexpr int K_UNIT = BITS == 8 && UNIT == 32 ? 32 : 16;
+    static constexpr int K_PITCH = ((ROW + K_UNIT - 1) / K_UNIT | 1) * K_UNIT, V_PITCH = ((ROW + 15) / 16 | 1) * 16;
+    static constexpr uint32_t V_AT = 32 * K_PITCH, S_AT = V_AT + 32 * V_PITCH;
+    // the integers' codes are taken as they lie, plus BIAS, as fp16's smallest numbers: 2^-24 of the value
+    static constexpr int BIAS = KIND == NRM_CACHE_INT4 ? 8 : KIND == NRM_CACHE_INT8 ? 128 : 0;
 };
 
 // A warp's shared memory: stages (keys, values, scales of both), then the places of two tiles' rows, which positions
-// of the stages are there, and the values' scales in fp16.
+// of the stages are there, and a tile's scales of each unit, the values' in fp16.
 struct AttnSmem {
     uint32_t stage, bytes;     // of the first stage; of one
     uint32_t places;           // [2][32] code offsets
     uint32_t there;            // [stages]
-    uint32_t half_scales;      // [factors][units][32]
+    uint32_t k_scales;         // [units][32]
+    uint32_t v_scales;         // [factors][units][32]
+    uint32_t bias;             // [units][heads]: what the codes' bias adds to a unit's products, negative
 };
-__host__ __device__ inline uint32_t attn_stage_bytes(int k_pitch, int v_pitch, int groups) {
-    return uint32_t(32 * (k_pitch + v_pitch) + 2 * 32 * groups * 4);
-}
 constexpr uint32_t kAttnPlaces = 2 * 32 * 8, kAttnThere = 16;
+template <typename F>
+__host__ __device__ constexpr uint32_t attn_stage_bytes(int groups) {
+    return F::S_AT + 2 * 32 * groups * 4;
+}
+template <typename T, typename F>
+__host__ __device__ constexpr uint32_t attn_warp_bytes(uint32_t stage) {
+    return F::STAGES * stage + kAttnPlaces + kAttnThere + F::UNITS * 128 +
+           (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * F::UNITS * 64 + (F::BIAS ? F::UNITS * F::NT * 32 : 0);
+}
 
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -164,7 +167,6 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
     const int chunks = a.row_bytes / a.vec;
     const int row_step = 32 / chunks, chunk_step = 32 - row_step * chunks;
     const int first_row = lane / chunks, first_chunk = lane - first_row * chunks;
-    const uint32_t v_at = 32 * a.k_pitch, s_at = v_at + 32 * a.v_pitch;
     const uint32_t ring = smem_addr(&in_ring<unsigned char>(0));
     const int64_t* const table = a.table + p.s * a.table_stride;
     int64_t page = 0, in_page = 0;
@@ -192,22 +194,23 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         __syncwarp();
         const uint32_t to = ring + sm.stage + uint32_t(stage) * sm.bytes;
         int row = first_row, chunk = first_chunk;
-        if (F::EXACT && F::CHUNKS > 0 && a.vec == 16 && m == 0xffffffffu) {
-            // neighbouring lanes copy neighbouring vectors of a row
+        if (F::EXACT && F::CHUNKS > 0 && a.vec == 16) {
+            // neighbouring lanes copy neighbouring vectors of a row; one that is not there becomes zeros
             constexpr int C = F::CHUNKS > 0 ? F::CHUNKS : 1;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
                 const int64_t at = in_ring<const int64_t>(places + r * 8) + c * 16;
-                cp_async_16(to + r * a.k_pitch + c * 16, a.cache.codes[0] + at);
-                cp_async_16(to + v_at + r * a.v_pitch + c * 16, a.cache.codes[1] + at);
+                const int n = int(m >> r << 4) & 16;
+                cp_async_16_or_0(to + r * F::K_PITCH + c * 16, a.cache.codes[0] + at, n);
+                cp_async_16_or_0(to + F::V_AT + r * F::V_PITCH + c * 16, a.cache.codes[1] + at, n);
             }
         } else {
 #pragma unroll 1
             for (int i = 0; i < chunks; ++i) {
                 const int64_t at = in_ring<const int64_t>(places + row * 8) + chunk * a.vec;
                 const int n = m >> row & 1 ? a.vec : 0;
-                const uint32_t k = to + row * a.k_pitch + chunk * a.vec, v = to + v_at + row * a.v_pitch + chunk * a.vec;
+                const uint32_t k = to + row * F::K_PITCH + chunk * a.vec, v = to + F::V_AT + row * F::V_PITCH + chunk * a.vec;
                 if (a.vec == 16) {
                     cp_async_16_or_0(k, a.cache.codes[0] + at, n);
                     cp_async_16_or_0(v, a.cache.codes[1] + at, n);
@@ -224,7 +227,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             }
         }
         // this lane's position's scales, [position][group]
-        const uint32_t ks = to + s_at + lane * groups * 4, vs = ks + 32 * groups * 4;
+        const uint32_t ks = to + F::S_AT + lane * groups * 4, vs = ks + 32 * groups * 4;
         const float *kf = a.cache.scales[0] + scale, *vf = a.cache.scales[1] + scale;
         if (a.scale_vec) {
             for (int g = 0; g < groups; g += 4) {
@@ -255,7 +258,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
     for (int nt = 0; nt < NT; ++nt) {
         const int h = nt * 8 + gid;
         const bits* row = static_cast<const bits*>(a.q.p) + p.s * a.q.ts + (p.q0 + h) * a.q.hs;
-        float x[F::UNITS][F::KP], most = 0.f;
+        float x[F::UNITS][F::KP], off[F::UNITS], most = 0.f;
 #pragma unroll
         for (int u = 0; u < F::UNITS; ++u) {
             const int at = u * F::UNIT + tid * F::KP;
@@ -287,9 +290,9 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
         // 2^e > most (an infinity or a row of tiny numbers stays what it is, nearly)
-        const int e = max(-100, min(127, int(__float_as_uint(most) >> 23) - 126));
+        const int e = max(-100, min(F::BIAS ? 118 : 127, int(__float_as_uint(most) >> 23) - 126));
         const float up = __uint_as_float(uint32_t(127 + 15 - e) << 23);
-        const float down = __uint_as_float(uint32_t(127 + e) << 23) * 0x1p-15f * a.scale_log2;
+        const float down = __uint_as_float(uint32_t(127 + e) << 23) * (F::BIAS ? 0x1p9f : 0x1p-15f) * a.scale_log2;
         factor[nt][0] = __shfl_sync(0xffffffffu, down, tid * 8);
         factor[nt][1] = __shfl_sync(0xffffffffu, down, tid * 8 + 4);
 #pragma unroll
@@ -300,12 +303,29 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 // the elements that a fragment of codes pairs
                 const int i0 = F::BITS == 8 ? part * 4 + b * 2 : part * 2 + b;
                 const int i1 = F::BITS == 8 ? i0 + 1 : i0 + F::KP / 2;
-                const float lo = x[u][i0] * up, hi = x[u][i1] * up;
+                // the codes of the second pair of four lie 16 times as large
+                const float by = F::BITS == 4 && b == 1 ? up * 0x1p-4f : up;
+                const float lo = x[u][i0] * by, hi = x[u][i1] * by;
                 q[ks][nt][0][b] = half2_bits(lo, hi);
+                float2 r = half2_floats(q[ks][nt][0][b]);
                 if constexpr (QT == 2) {
-                    const float2 r = half2_floats(q[ks][nt][0][b]);
                     q[ks][nt][QT - 1][b] = half2_bits(lo - r.x, hi - r.y);
+                    const float2 r2 = half2_floats(q[ks][nt][QT - 1][b]);
+                    r.x += r2.x, r.y += r2.y;
                 }
+                if constexpr (F::BIAS != 0) {
+                    constexpr float of = -F::BIAS * 0x1p-24f;
+                    if (b == 0 && part == 0) off[u] = 0.f;
+                    off[u] = fmaf(F::BITS == 4 && b == 1 ? 16.f * of : of, r.x + r.y, off[u]);
+                }
+            }
+        }
+        if constexpr (F::BIAS != 0) {
+#pragma unroll
+            for (int u = 0; u < F::UNITS; ++u) {
+                off[u] += __shfl_xor_sync(0xffffffffu, off[u], 1);
+                off[u] += __shfl_xor_sync(0xffffffffu, off[u], 2);
+                if (tid == 0) in_ring<float>(sm.bias + ((u * NT + nt) * 8 + gid) * 4) = off[u];
             }
         }
     }
@@ -338,9 +358,9 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         const uint32_t there = in_ring<const uint32_t>(sm.there + stage * 4);
         const uint32_t at = sm.stage + uint32_t(stage) * sm.bytes;
 
-        // the values' scales in fp16, this lane's position's; seldom one is larger than all before it
+        // the scales of this lane's position, of each unit, the values' in fp16; seldom one is larger than all before it
         {
-            const uint32_t mine = at + s_at + (32 + lane) * groups * 4;
+            const uint32_t mine = at + F::S_AT + (32 + lane) * groups * 4;
             float mine_of[F::UNITS];
             bool larger = false;
 #pragma unroll
@@ -371,9 +391,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 if (!F::EXACT && u >= units) break;
                 const float s = mine_of[u] * __uint_as_float(uint32_t(127 + 6 - top[u]) << 23);
                 const __half hi = __float2half_rn(s);
-                in_ring<__half>(sm.half_scales + (u * 32 + lane) * 2) = hi;
+                in_ring<__half>(sm.v_scales + (u * 32 + lane) * 2) = hi;
                 if constexpr (WT == 2)
-                    in_ring<__half>(sm.half_scales + ((F::UNITS + u) * 32 + lane) * 2) = __float2half_rn(s - __half2float(hi));
+                    in_ring<__half>(sm.v_scales + ((F::UNITS + u) * 32 + lane) * 2) = __float2half_rn(s - __half2float(hi));
+                in_ring<float>(sm.k_scales + (u * 32 + lane) * 4) = in_ring<const float>(mine - 32 * groups * 4 + of_unit[u]);
             }
             __syncwarp();
         }
@@ -386,10 +407,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t f[F::STEPS][4];
-                const uint32_t from = at + (16 * half + gid) * a.k_pitch + tid * (F::KP * F::BITS / 8) + u * (F::UNIT * F::BITS / 8);
+                const uint32_t from = at + (16 * half + gid) * F::K_PITCH + tid * (F::KP * F::BITS / 8) + u * (F::UNIT * F::BITS / 8);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t row = from + r * 8 * a.k_pitch;
+                    const uint32_t row = from + r * 8 * F::K_PITCH;
                     if constexpr (F::BITS == 8 && F::STEPS == 2) {
                         const uint2 w = in_ring<const uint2>(row);
                         codes8<F::KIND>(w.x, f[0][r], f[0][2 + r]);
@@ -409,11 +430,16 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                         f[0][2 + r] = codes4_next(w);
                     }
                 }
-                const uint32_t scales = at + s_at + (16 * half + gid) * groups * 4 + of_unit[u];
-                const float s0 = in_ring<const float>(scales), s1 = in_ring<const float>(scales + 32 * groups);
+                const uint32_t scales = sm.k_scales + (u * 32 + 16 * half + gid) * 4;
+                const float s0 = in_ring<const float>(scales), s1 = in_ring<const float>(scales + 32);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (F::BIAS != 0) {
+                        const float2 less = in_ring<const float2>(sm.bias + ((u * NT + nt) * 8 + tid * 2) * 4);
+                        c[0] = c[2] = less.x;
+                        c[1] = c[3] = less.y;
+                    }
 #pragma unroll
                     for (int st = 0; st < F::STEPS; ++st)
 #pragma unroll
@@ -460,8 +486,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
                 most = fmaxf(m[nt][i], most);
-                const float base = finite_max(most);
-                grow[nt][i] = exp2_approx(m[nt][i] - base);
+                const float base = finite_max(most) - 8.f;  // p * 2^8, and so the sum
+                grow[nt][i] = exp2_approx(m[nt][i] - base - 8.f);
                 grows |= most > m[nt][i];
                 m[nt][i] = most;
                 float add = 0.f;
@@ -477,7 +503,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float x = l[half][nt][2 * r] * 0x1p8f, y = l[half][nt][2 * r + 1] * 0x1p8f;
+                    const float x = l[half][nt][2 * r], y = l[half][nt][2 * r + 1];
                     const uint32_t hi = half2_bits(x, y);
                     w[half][nt][0][r] = transpose8(hi);
                     if constexpr (WT == 2) {
@@ -500,7 +526,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         // the values, half a tile after the other
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint32_t v_from = at + v_at + (16 * half + tid * 2) * a.v_pitch + gid * F::VP * F::BITS / 8;
+            const uint32_t v_from = at + F::V_AT + (16 * half + tid * 2) * F::V_PITCH + gid * F::VP * F::BITS / 8;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
@@ -508,7 +534,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 uint32_t b[NT][WT][2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t of = sm.half_scales + (u * 32 + 16 * half + 8 * r + 2 * tid) * 2;
+                    const uint32_t of = sm.v_scales + (u * 32 + 16 * half + 8 * r + 2 * tid) * 2;
                     const uint32_t hi = in_ring<const uint32_t>(of);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) b[nt][0][r] = mul_half2(w[half][nt][0][r], hi);
@@ -527,8 +553,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 const uint32_t from = v_from + u * (F::UNIT * F::BITS / 8);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t row = from + r * 8 * a.v_pitch;
-                    const uint32_t x = lds<F::VP * F::BITS / 8>(row), y = lds<F::VP * F::BITS / 8>(row + a.v_pitch);
+                    const uint32_t row = from + r * 8 * F::V_PITCH;
+                    const uint32_t x = lds<F::VP * F::BITS / 8>(row), y = lds<F::VP * F::BITS / 8>(row + F::V_PITCH);
                     if constexpr (F::BITS == 8) {
                         codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
                         if constexpr (F::TILES == 2)
@@ -548,7 +574,15 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int k = 0; k < WT; ++k) mma16816(acc[u][t][nt], f[t], b[nt][k][0], b[nt][k][1]);
+                        for (int k = 0; k < WT; ++k) {
+                            mma16816(acc[u][t][nt], f[t], b[nt][k][0], b[nt][k][1]);
+                            if constexpr (F::BIAS != 0) {
+                                // less the bias (0x8008: -8 * 2^-24)
+                                constexpr uint32_t once = F::BITS == 4 ? 0x80088008u : 0x80808080u, next = 0x80808080u;
+                                const uint32_t less[4] = {once, next, once, next};
+                                mma16816(acc[u][t][nt], less, b[nt][k][0], b[nt][k][1]);
+                            }
+                        }
             }
         }
         __syncwarp();
@@ -563,6 +597,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             s += __shfl_xor_sync(0xffffffffu, s, 4);
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
+            s *= 0x1p-8f;
             const int h = nt * 8 + tid * 2 + i;
             if (h >= p.heads) continue;
             const float scale = p.whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f;
@@ -576,8 +611,9 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 float v[F::VP];
 #pragma unroll
                 for (int t = 0; t < F::TILES; ++t) {
-                    v[2 * t] = acc[u][t][nt][i] * 0x1p-14f * d0;
-                    v[2 * t + 1] = acc[u][t][nt][2 + i] * 0x1p-14f * d0;
+                    constexpr float once = F::BIAS ? 0x1p10f : 0x1p-14f, next = F::BITS == 4 ? 0x1p6f : once;
+                    v[2 * t] = acc[u][t][nt][i] * once * d0;
+                    v[2 * t + 1] = acc[u][t][nt][2 + i] * next * d0;
                 }
                 if (!p.whole) {
                     if constexpr (F::VP == 4) *reinterpret_cast<float4*>(part + at) = make_float4(v[0], v[1], v[F::VP - 2], v[F::VP - 1]);
@@ -613,11 +649,6 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 }
 
 template <typename T, typename F>
-__host__ __device__ constexpr uint32_t attn_warp_bytes(uint32_t stage) {
-    return F::STAGES * stage + kAttnPlaces + kAttnThere + (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * F::UNITS * 64;
-}
-
-template <typename T, typename F>
 __global__ void __launch_bounds__(32 * F::WARPS, 1) attn_mma_kernel(const AttnArgs a) {
     __shared__ AttnTable table;
     pdl_next();
@@ -625,11 +656,13 @@ __global__ void __launch_bounds__(32 * F::WARPS, 1) attn_mma_kernel(const AttnAr
     attn_empty<T>(a, table);
     const int groups = a.d / a.cache.group, warp = threadIdx.x >> 5;
     AttnSmem sm;
-    sm.bytes = attn_stage_bytes(a.k_pitch, a.v_pitch, groups);
+    sm.bytes = attn_stage_bytes<F>(groups);
     sm.stage = uint32_t(warp) * attn_warp_bytes<T, F>(sm.bytes);
     sm.places = sm.stage + F::STAGES * sm.bytes;
     sm.there = sm.places + kAttnPlaces;
-    sm.half_scales = sm.there + kAttnThere;
+    sm.k_scales = sm.there + kAttnThere;
+    sm.v_scales = sm.k_scales + F::UNITS * 128;
+    sm.bias = sm.v_scales + (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * F::UNITS * 64;
     attn_pieces(a, table, warp * int(gridDim.x) + int(blockIdx.x),
                 [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
 }
@@ -638,11 +671,12 @@ template <typename T, typename F>
 nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&attn_mma_kernel<T, F>);
     const int groups = a.d / a.cache.group;
-    const size_t warp = attn_warp_bytes<T, F>(attn_stage_bytes(a.k_pitch, a.v_pitch, groups));
+    const size_t warp = attn_warp_bytes<T, F>(attn_stage_bytes<F>(groups));
     // as many workers to an SM as have room for their rings beside the table
     const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 64;
     const int warps = int(std::min<size_t>(F::WARPS, room / warp));
     a.workers = dev->sms * warps;
+    attn_snap(a);
     const size_t smem = warps * warp;
     nrm_status st = prepare_kernel(fn, smem, false);
     if (st != NRM_OK) return st;
@@ -655,13 +689,6 @@ template <typename T, int KIND>
 nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const bool wide = a.d % 32 == 0 && a.cache.group % 32 == 0;
     a.row_bytes = KIND == NRM_CACHE_INT4 ? a.d / 2 : a.d;
-    // rows 32 bytes (8 bits: a key's fragment is 8 bytes a lane, 4 rows at a time) or 16 bytes (else) off a multiple of
-    // 64 or 32 apart: the fragments' reads then meet no bank twice
-    const int k_unit = KIND != NRM_CACHE_INT4 && wide ? 32 : 16;
-    a.k_pitch = (a.row_bytes + k_unit - 1) / k_unit * k_unit;
-    if (a.k_pitch / k_unit % 2 == 0) a.k_pitch += k_unit;
-    a.v_pitch = (a.row_bytes + 15) / 16 * 16;
-    if (a.v_pitch / 16 % 2 == 0) a.v_pitch += 16;
     const int nt = a.d <= 128 && a.shared > 8 ? 2 : 1;
     attn_chunks(a, 8 * nt);
     a.pages = a.cache.slots / a.cache.page.d;
@@ -680,7 +707,6 @@ nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     default: break;
     }
     attn_chunks(a, 8);
-    a.v_pitch = a.k_pitch = (a.row_bytes + 15) / 16 % 2 ? (a.row_bytes + 15) / 16 * 16 : (a.row_bytes + 31) / 16 * 16;
     return attn_mma_launch<T, AttnForm<KIND, 16, 16, 1, false>>(a, dev, s);
 }
 
