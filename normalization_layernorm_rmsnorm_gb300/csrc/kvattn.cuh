@@ -2,16 +2,19 @@
 // quantised key/value cache.
 //
 // The work is every position of every head of the cache once, so it is bound by
-// the bytes of the codes.  Sequences are cut into tiles of 32 positions, and all
-// tiles of all sequences and heads are dealt to the warps of the GPU in equal
-// contiguous shares: a worker's share may end inside a sequence and begin inside
+// the bytes of the codes.  Sequences are cut into tiles of 32 positions, all tiles
+// of all sequences are dealt out in equal contiguous shares, and the workers (the
+// warps of the GPU) take a share for one pair each (a head of the cache and the
+// query heads that read it).  A share may end inside a sequence and begin inside
 // another, so short and long sequences of one batch load the GPU evenly, and the
-// cut is made on the device, from the lengths that lie there.  Each worker runs
-// the softmax with a running maximum and sum over its tiles of a pair (a head of
-// the cache and the query heads that read it).  A pair that lies in one worker's
-// share is written at once; of the others, each worker leaves its maximum, sum
-// and accumulator in the workspace (it holds at most two such pieces: its first
-// pair's end and its last pair's beginning), and a second kernel joins them.
+// cut is made on the device, from the lengths that lie there.  The workers of one
+// share are neighbours, so that the heads of a slot, which lie side by side, are
+// read at one time (one head after the other, 131072 positions in 4 bits read 1.7
+// times their bytes).  Each worker runs the softmax with a running maximum and sum
+// over its tiles of a sequence.  A sequence that lies in one share is written at
+// once; of the others, each worker leaves its maximum, sum and accumulator in the
+// workspace (it holds at most two such pieces: its first sequence's end and its
+// last one's beginning), and a second kernel joins them.
 // With weights, the logits lie in the workspace and a third kernel adds each
 // position's weight once its sequence's sum is known.
 #pragma once
@@ -84,23 +87,24 @@ __device__ __forceinline__ void attn_table(const AttnArgs& a, AttnTable& t) {
     }
 }
 
-// Workers that get a share of `total` tiles, and their shares: the first `more` have one tile more.
+// The shares of all sequences' tiles: the first `more` have one tile more.  Where there are more pairs than workers,
+// one share.
 struct AttnShares {
     int used, each, more;
     __device__ __forceinline__ AttnShares(const AttnArgs& a, int total) {
         const int w = (total + a.min_tiles - 1) / a.min_tiles;
-        used = max(1, min(w, a.workers));
+        used = max(1, min(w, a.workers / (a.hk * a.chunks)));
         each = total / used;
         more = total - each * used;
     }
-    __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
-    // the worker whose share holds tile t
+    __device__ __forceinline__ int begin(int r) const { return r * each + min(r, more); }
+    // the share that holds tile t
     __device__ __forceinline__ int owner(int t) const {
         const int longer = more * (each + 1);
         return t < longer ? t / (each + 1) : more + (t - longer) / each;
     }
 };
-// The sequence that tile `t` of the sequences' tiles (not their pairs') belongs to.
+// The sequence that tile t belongs to.
 __device__ __forceinline__ int attn_sequence(const int* pre, int sequences, int t) {
     int lo = 0, hi = sequences - 1;  // the last s with pre[s] <= t
     while (lo < hi) {
@@ -111,53 +115,63 @@ __device__ __forceinline__ int attn_sequence(const int* pre, int sequences, int 
     return lo;
 }
 
-// A worker's piece of one pair: tiles [tile0, tile1) of sequence s.
+// A worker's piece of a sequence: tiles [tile0, tile1) of sequence s, for one pair.
 struct AttnPiece {
     int s, head, q0, heads;  // head of the cache; query heads q0 .. q0 + heads - 1
     int pair;
     int tile0, tile1;
-    bool whole;              // all of the pair
+    bool whole;              // all of the sequence
     int64_t lo, n;           // positions that count
     int64_t part;            // where its partial result goes, if it is not whole
 };
+// The place of the partial result of share r for a pair: its first sequence's end (0) or its last one's beginning (1).
+__device__ __forceinline__ int64_t attn_part(const AttnArgs& a, int r, int pair, int which) {
+    return ((int64_t(r) * a.hk * a.chunks + pair) * 2 + which) * attn_part_floats(a.heads, a.d);
+}
 
-// Calls f(piece) for each piece of worker w's share.
+// Calls f(piece) for each piece of this warp's share.
 template <typename F>
-__device__ __forceinline__ void attn_pieces(const AttnArgs& a, const AttnTable& table, int w, F&& f) {
+__device__ __forceinline__ void attn_pieces(const AttnArgs& a, const AttnTable& table, F&& f) {
     const int pairs = a.hk * a.chunks;
-    const int total = table.pre[a.sequences] * pairs;
+    const int total = table.pre[a.sequences];
+    if (total == 0) return;
     const AttnShares shares(a, total);
-    if (w >= shares.used) return;
-    // a share's end, moved to the beginning of the pair that it would cut where that is short
-    auto edge = [&](int t, int& s) {
-        s = attn_sequence(table.pre, a.sequences, t / pairs);
-        while (t < total && table.pre[s + 1] * pairs <= t) ++s;
-        const int tiles = table.pre[s + 1] - table.pre[s], at = t - table.pre[s] * pairs;
-        return t < total && tiles <= a.snap ? t - at % tiles : t;
-    };
-    int s, s_end;
-    int t = edge(shares.begin(w), s);
-    const int end = edge(shares.begin(w + 1), s_end);
-    if (t >= end) return;
-    while (t < end) {
-        while (table.pre[s + 1] * pairs <= t) ++s;  // (sequences without tiles are passed over)
-        const int tiles = table.pre[s + 1] - table.pre[s], at = t - table.pre[s] * pairs;
-        AttnPiece p;
-        p.s = s;
-        p.pair = at / tiles;
-        p.head = p.pair / a.chunks;
-        const int chunk = p.pair - p.head * a.chunks;
-        p.q0 = p.head * a.shared + chunk * a.heads;
-        p.heads = min(a.heads, a.shared - chunk * a.heads);
-        p.n = table.n[s];
-        p.lo = a.window > 0 && p.n > a.window ? p.n - a.window : 0;
-        p.tile0 = at - p.pair * tiles;
-        p.tile1 = min(tiles, p.tile0 + (end - t));
-        p.whole = p.tile0 == 0 && p.tile1 == tiles;
-        // its first pair's end, or its last pair's beginning
-        p.part = (int64_t(w) * 2 + (p.tile0 == 0 ? 1 : 0)) * attn_part_floats(a.heads, a.d);
-        f(p);
-        t += p.tile1 - p.tile0;
+    // as few warps of a CTA as the work takes, so that it fills the GPU
+    const int warps = int(blockDim.x) >> 5, warp = int(threadIdx.x) >> 5;
+    const int64_t work = int64_t(shares.used) * pairs;
+    const int used_warps = int(min(int64_t(warps), (work + gridDim.x - 1) / gridDim.x));
+    if (warp >= used_warps) return;
+    // (more pairs than workers: a worker takes several)
+    for (int64_t w = int(blockIdx.x) * used_warps + warp; w < work; w += int64_t(gridDim.x) * used_warps) {
+        const int r = int(w / pairs), pair = int(w - int64_t(r) * pairs);
+        // a share's end, moved to the beginning of the sequence that it would cut where that is short
+        auto edge = [&](int t, int& s) {
+            s = attn_sequence(table.pre, a.sequences, min(t, total - 1));
+            const int first = table.pre[s];
+            return t < total && table.pre[s + 1] - first <= a.snap ? first : t;
+        };
+        int s, s_end;
+        int t = edge(shares.begin(r), s);
+        const int end = edge(shares.begin(r + 1), s_end);
+        const int head = pair / a.chunks, chunk = pair - head * a.chunks;
+        while (t < end) {
+            while (table.pre[s + 1] <= t) ++s;  // (sequences without tiles are passed over)
+            const int first = table.pre[s], tiles = table.pre[s + 1] - first;
+            AttnPiece p;
+            p.s = s;
+            p.pair = pair;
+            p.head = head;
+            p.q0 = head * a.shared + chunk * a.heads;
+            p.heads = min(a.heads, a.shared - chunk * a.heads);
+            p.n = table.n[s];
+            p.lo = a.window > 0 && p.n > a.window ? p.n - a.window : 0;
+            p.tile0 = t - first;
+            p.tile1 = min(tiles, p.tile0 + (end - t));
+            p.whole = p.tile0 == 0 && p.tile1 == tiles;
+            p.part = attn_part(a, r, pair, p.tile0 == 0);
+            f(p);
+            t += p.tile1 - p.tile0;
+        }
     }
 }
 
@@ -219,8 +233,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
     pdl_next();
     attn_table(a, table);
     attn_empty<T>(a, table);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    attn_pieces(a, table, warp * int(gridDim.x) + int(blockIdx.x), [&](const AttnPiece& p) {
+    const int lane = threadIdx.x & 31;
+    attn_pieces(a, table, [&](const AttnPiece& p) {
         float q[H][E], acc[H][E], m[H], sum[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
 }
 
 // ---------------------------------------------------------------------------
-// joining the pieces of a pair: a CTA for each pair (blockIdx.x), or, where pairs
+// joining the pieces of a sequence: a CTA for each pair (blockIdx.x), or, where pairs
 // are few and so have many pieces, for each of its heads (blockIdx.y).  Its warps
 // share the heads, and the warps of a head its pieces.
 // ---------------------------------------------------------------------------
@@ -322,9 +336,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
     const int s = int(blockIdx.x) / pairs, pair = int(blockIdx.x) - s * pairs;
     const int before = ld_after(a.prefix + s), tiles = ld_after(a.prefix + s + 1) - before;
     if (tiles <= a.snap) return;
-    const int t0 = before * pairs + pair * tiles;
-    const AttnShares shares(a, ld_after(a.prefix + a.sequences) * pairs);
-    const int w0 = shares.owner(t0), w1 = shares.owner(t0 + tiles - 1);
+    const AttnShares shares(a, ld_after(a.prefix + a.sequences));
+    const int w0 = shares.owner(before), w1 = shares.owner(before + tiles - 1);
     if (w0 == w1) return;  // written by that worker
     const int head = pair / a.chunks, chunk = pair - head * a.chunks;
     const int heads = min(a.heads, a.shared - chunk * a.heads), q0 = head * a.shared + chunk * a.heads;
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
         const bool there = group < at_once && h0 + group < mine && h < heads;
         // the first worker's piece is the beginning of its last pair, the others' the end of their first
         auto part = [&](int w) {
-            return a.part + (int64_t(w) * 2 + (w == w0)) * attn_part_floats(a.heads, a.d) + h * attn_part_row(a.d);
+            return a.part + attn_part(a, w, pair, w == w0) + h * attn_part_row(a.d);
         };
         float top = -INFINITY, sum = 0.f;
         float4 acc[E];

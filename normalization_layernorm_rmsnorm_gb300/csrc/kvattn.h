@@ -12,13 +12,11 @@ namespace nrm {
 // call with more is cut into launches.
 constexpr int kAttnSequences = 1024;
 constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
-constexpr int kAttnWarps = 12;       // warps of a CTA at most, each a worker of its own
+constexpr int kAttnWarps = 16;       // warps of a CTA at most, each a worker of its own
 constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
 constexpr int64_t kAttnTiles = int64_t(1) << 31;  // of all pairs of a launch, fewer than this
 
-// The positions of the sequences, cut into tiles: tiles of sequence s, for each
-// of its `pairs` (a head of the cache with a chunk of its query heads), are
-// dealt to the workers in equal contiguous shares.
+// Pairs: a head of the cache with a chunk of the query heads that read it.
 struct AttnArgs {
     HeadView q, out;          // ts: from sequence to sequence
     CacheDev cache;

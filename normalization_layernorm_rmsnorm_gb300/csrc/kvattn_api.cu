@@ -70,7 +70,9 @@ bool attn_workspace(int64_t sequences, int64_t hq, int64_t hk, int64_t d, int64_
     w->at[0] = 0;
     w->at[1] = round16((n + 1) * 4);
     w->at[2] = w->at[1] + round16(n * hq * 4);
-    w->at[3] = w->at[2] + round16(int64_t(sms) * kAttnWarps * 2 * attn_part_floats(int(heads), int(d)) * 4);
+    // shares times pairs: no more than workers, or pairs where they are more
+    const int64_t parts = std::max<int64_t>(int64_t(sms) * kAttnWarps, attn_most_pairs(hq, hk));
+    w->at[3] = w->at[2] + round16(parts * 2 * attn_part_floats(int(heads), int(d)) * 4);
     w->at[4] = w->at[3] + logits * positions * 4;
     return true;
 }

@@ -20,9 +20,11 @@
 // exchange of 8x8 matrices.
 //
 // Codes and scales are copied asynchronously into the warp's own ring in shared
-// memory, a tile of 32 positions to a stage; warps share nothing and the loop holds no
-// barrier of the CTA.  The row of a page is found by the lane of its position, a
-// tile ahead.  Rows are padded so that the fragments' reads have no conflicts.
+// memory, a tile of 32 positions at a time: its keys while the values before them are
+// worked on, and its values while the keys are; warps share nothing and the loop
+// holds no barrier of the CTA.  (Two whole stages leave room for 10 warps, whose
+// waits then show.)  The row of a page is found by the lane of its position, a tile
+// ahead.  Rows are padded so that the fragments' reads have no conflicts.
 // (Bulk copies of single rows are no way to move them: one takes an SM about ten
 // cycles, 1.8 TB/s with rows of 64 bytes and 3.7 with 128, against 3.5 and 6.2 by
 // 16-byte copies that eight lanes make of a row.)
@@ -104,8 +106,6 @@ struct AttnForm {
     static constexpr int STEPS = UNIT / 16, TILES = UNIT / 16;
     static constexpr int KP = UNIT / 4, VP = UNIT / 8;  // elements of a lane's piece of a unit
     static constexpr int BITS = KIND == NRM_CACHE_INT4 ? 4 : 8;
-    static constexpr int WARPS = DMAX <= 128 && NT == 1 ? 12 : 8;  // by the registers that a thread needs
-    static constexpr int STAGES = BITS == 4 && DMAX <= 128 ? 3 : 2;
     static constexpr int ROW = DMAX * BITS / 8;
     static constexpr int CHUNKS = ROW % 16 == 0 ? ROW / 16 : 0;  // 16-byte vectors of a row
     // rows in shared memory: an odd number of 32 bytes (a key's fragment of 8 bytes a lane, 4 rows at a time) or of 16
@@ -117,25 +117,26 @@ struct AttnForm {
     static constexpr int BIAS = KIND == NRM_CACHE_INT4 ? 8 : KIND == NRM_CACHE_INT8 ? 128 : 0;
 };
 
-// A warp's shared memory: stages (keys, values, scales of both), then the places of two tiles' rows, which positions
-// of the stages are there, and a tile's scales of each unit, the values' in fp16.
+// A warp's shared memory: a tile's keys, values and scales of both, the places of a tile's rows, and its scales of each
+// unit, the values' in fp16.
 struct AttnSmem {
-    uint32_t stage, bytes;     // of the first stage; of one
-    uint32_t places;           // [2][32] code offsets
-    uint32_t there;            // [stages]
+    uint32_t codes;            // keys, values
+    uint32_t scales;           // [keys, values][32][groups]
+    uint32_t places;           // [32] code offsets
     uint32_t k_scales;         // [units][32]
     uint32_t v_scales;         // [factors][units][32]
     uint32_t bias;             // [units][heads]: what the codes' bias adds to a unit's products, negative
 };
-constexpr uint32_t kAttnPlaces = 2 * 32 * 8, kAttnThere = 16;
-template <typename F>
-__host__ __device__ constexpr uint32_t attn_stage_bytes(int groups) {
-    return F::S_AT + 2 * 32 * groups * 4;
-}
+constexpr uint32_t kAttnPlaces = 32 * 8;
+// Warps of a CTA, by the registers that a thread needs.
 template <typename T, typename F>
-__host__ __device__ constexpr uint32_t attn_warp_bytes(uint32_t stage) {
-    return F::STAGES * stage + kAttnPlaces + kAttnThere + F::UNITS * 128 +
-           (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * F::UNITS * 64 + (F::BIAS ? F::UNITS * F::NT * 32 : 0);
+constexpr int attn_warps = F::DMAX > 128 || F::NT > 1 ? 8 : sizeof(T) == 4 ? 12 : 16;
+template <typename T>
+constexpr int kAttnFactors = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;  // of p
+template <typename T, typename F>
+__host__ __device__ constexpr uint32_t attn_warp_bytes(int groups) {
+    return F::S_AT + 2 * 32 * groups * 4 + kAttnPlaces + F::UNITS * 128 + kAttnFactors<T> * F::UNITS * 64 +
+           (F::BIAS ? F::UNITS * F::NT * 32 : 0);
 }
 
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
@@ -152,21 +153,18 @@ __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c
 template <typename T, typename F>
 __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiece& p, const AttnSmem& sm, int groups) {
     using bits = typename Io<T>::bits_t;
-    constexpr int NT = F::NT, QT = sizeof(T) == 4 ? 2 : 1, WT = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
-    constexpr int KSTEPS = F::DMAX / 16, S = F::STAGES;
+    constexpr int NT = F::NT, QT = sizeof(T) == 4 ? 2 : 1, WT = kAttnFactors<T>;
+    constexpr int KSTEPS = F::DMAX / 16;
     const int lane = threadIdx.x & 31, gid = lane >> 2, tid = lane & 3;
     const int units = F::EXACT ? F::UNITS : a.d / F::UNIT;
     int of_unit[F::UNITS];  // a unit's scale in its row's, in bytes
 #pragma unroll
     for (int u = 0; u < F::UNITS; ++u) of_unit[u] = u * F::UNIT / a.cache.group * 4;
 
-    // ---- the copies: a tile to a stage ----
+    // ---- the copies ----
     const int64_t j0 = p.lo + int64_t(p.tile0) * kAttnTile;
     const int64_t j1 = min(p.n, p.lo + int64_t(p.tile1) * kAttnTile);
     const int tiles = p.tile1 - p.tile0;
-    const int chunks = a.row_bytes / a.vec;
-    const int row_step = 32 / chunks, chunk_step = 32 - row_step * chunks;
-    const int first_row = lane / chunks, first_chunk = lane - first_row * chunks;
     const uint32_t ring = smem_addr(&in_ring<unsigned char>(0));
     const int64_t* const table = a.table + p.s * a.table_stride;
     int64_t page = 0, in_page = 0;
@@ -179,45 +177,29 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             page = ld_after(table + entry);
         }
     };
-    auto issue = [&](int tile, int stage) {
-        const uint32_t places = sm.places + (tile & 1) * 256;
-        const bool ok = in_page >= 0 && uint64_t(page) < uint64_t(a.pages);
-        if (in_page >= 0 && !ok) atomicOr(a.err, kErrCacheSlot);
-        const uint32_t m = __ballot_sync(0xffffffffu, ok);
-        int64_t code = 0, scale = 0;
-        if (ok) {
-            code = page * a.cache.page_stride + in_page * a.cache.slot_stride + p.head * a.cache.head_stride;
-            scale = page * a.cache.scale_page_stride + in_page * a.cache.scale_slot_stride + p.head * a.cache.scale_head_stride;
-        }
-        in_ring<int64_t>(places + lane * 8) = code;
-        if (lane == 0) in_ring<uint32_t>(sm.there + stage * 4) = m;
-        __syncwarp();
-        const uint32_t to = ring + sm.stage + uint32_t(stage) * sm.bytes;
-        int row = first_row, chunk = first_chunk;
+    // the rows of keys (0) or values (1) at the places in shared memory; one that is not there becomes zeros
+    auto copy_rows = [&](auto which, uint32_t m) {
+        constexpr int W = decltype(which)::value, PITCH = W ? F::V_PITCH : F::K_PITCH;
+        const uint32_t to = ring + sm.codes + (W ? F::V_AT : 0);
+        const uint8_t* codes = a.cache.codes[W];
         if (F::EXACT && F::CHUNKS > 0 && a.vec == 16) {
-            // neighbouring lanes copy neighbouring vectors of a row; one that is not there becomes zeros
+            // neighbouring lanes copy neighbouring vectors of a row
             constexpr int C = F::CHUNKS > 0 ? F::CHUNKS : 1;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
-                const int64_t at = in_ring<const int64_t>(places + r * 8) + c * 16;
-                const int n = int(m >> r << 4) & 16;
-                cp_async_16_or_0(to + r * F::K_PITCH + c * 16, a.cache.codes[0] + at, n);
-                cp_async_16_or_0(to + F::V_AT + r * F::V_PITCH + c * 16, a.cache.codes[1] + at, n);
+                cp_async_16_or_0(to + r * PITCH + c * 16, codes + in_ring<const int64_t>(sm.places + r * 8) + c * 16,
+                                 int(m >> r << 4) & 16);
             }
         } else {
+            const int chunks = a.row_bytes / a.vec, row_step = 32 / chunks, chunk_step = 32 - row_step * chunks;
+            int row = lane / chunks, chunk = lane - row * chunks;
 #pragma unroll 1
             for (int i = 0; i < chunks; ++i) {
-                const int64_t at = in_ring<const int64_t>(places + row * 8) + chunk * a.vec;
+                const int64_t at = in_ring<const int64_t>(sm.places + row * 8) + chunk * a.vec;
                 const int n = m >> row & 1 ? a.vec : 0;
-                const uint32_t k = to + row * F::K_PITCH + chunk * a.vec, v = to + F::V_AT + row * F::V_PITCH + chunk * a.vec;
-                if (a.vec == 16) {
-                    cp_async_16_or_0(k, a.cache.codes[0] + at, n);
-                    cp_async_16_or_0(v, a.cache.codes[1] + at, n);
-                } else {
-                    cp_async_8_or_0(k, a.cache.codes[0] + at, n);
-                    cp_async_8_or_0(v, a.cache.codes[1] + at, n);
-                }
+                if (a.vec == 16) cp_async_16_or_0(to + row * PITCH + chunk * 16, codes + at, n);
+                else cp_async_8_or_0(to + row * PITCH + chunk * 8, codes + at, n);
                 row += row_step;
                 chunk += chunk_step;
                 if (chunk >= chunks) {
@@ -226,30 +208,43 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 }
             }
         }
-        // this lane's position's scales, [position][group]
-        const uint32_t ks = to + F::S_AT + lane * groups * 4, vs = ks + 32 * groups * 4;
+    };
+    // the places of the tile that was looked up, its keys and the scales of both; which positions are there
+    auto issue_keys = [&]() -> uint32_t {
+        const bool ok = in_page >= 0 && uint64_t(page) < uint64_t(a.pages);
+        if (in_page >= 0 && !ok) atomicOr(a.err, kErrCacheSlot);
+        const uint32_t m = __ballot_sync(0xffffffffu, ok);
+        int64_t code = 0, scale = 0;
+        if (ok) {
+            code = page * a.cache.page_stride + in_page * a.cache.slot_stride + p.head * a.cache.head_stride;
+            scale = page * a.cache.scale_page_stride + in_page * a.cache.scale_slot_stride + p.head * a.cache.scale_head_stride;
+        }
+        in_ring<int64_t>(sm.places + lane * 8) = code;
+        __syncwarp();
+        copy_rows(std::integral_constant<int, 0>{}, m);
+        const uint32_t ks = ring + sm.scales + lane * groups * 4, vs = ks + 32 * groups * 4;
         const float *kf = a.cache.scales[0] + scale, *vf = a.cache.scales[1] + scale;
         if (a.scale_vec) {
+#pragma unroll 1
             for (int g = 0; g < groups; g += 4) {
                 cp_async_16_or_0(ks + g * 4, kf + g, ok ? 16 : 0);
                 cp_async_16_or_0(vs + g * 4, vf + g, ok ? 16 : 0);
             }
         } else {
+#pragma unroll 1
             for (int g = 0; g < groups; ++g) {
                 cp_async_4_or_0(ks + g * 4, kf + g, ok ? 4 : 0);
                 cp_async_4_or_0(vs + g * 4, vf + g, ok ? 4 : 0);
             }
         }
+        return m;
     };
     look_up(j0);
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        if (i < tiles) {
-            issue(i, i);
-            look_up(j0 + (i + 1) * kAttnTile);
-        }
-        cp_async_commit();
-    }
+    uint32_t there = issue_keys(), next_there = 0;
+    cp_async_commit();
+    copy_rows(std::integral_constant<int, 1>{}, there);
+    cp_async_commit();
+    look_up(j0 + kAttnTile);
 
     // ---- the queries, while the first copies are under way ----
     uint32_t q[KSTEPS][NT][QT][2];
@@ -346,21 +341,13 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, sum[nt][0] = sum[nt][1] = 0.f;
 
-    int stage = 0;
     for (int tile = 0; tile < tiles; ++tile) {
-        if (tile + S - 1 < tiles) {
-            issue(tile + S - 1, stage == 0 ? S - 1 : stage - 1);
-            look_up(j0 + int64_t(tile + S) * kAttnTile);
-        }
-        cp_async_commit();
-        cp_async_wait<S - 1>();
+        cp_async_wait<1>();  // the keys and the scales
         __syncwarp();
-        const uint32_t there = in_ring<const uint32_t>(sm.there + stage * 4);
-        const uint32_t at = sm.stage + uint32_t(stage) * sm.bytes;
 
         // the scales of this lane's position, of each unit, the values' in fp16; seldom one is larger than all before it
         {
-            const uint32_t mine = at + F::S_AT + (32 + lane) * groups * 4;
+            const uint32_t mine = sm.scales + (32 + lane) * groups * 4;
             float mine_of[F::UNITS];
             bool larger = false;
 #pragma unroll
@@ -407,7 +394,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t f[F::STEPS][4];
-                const uint32_t from = at + (16 * half + gid) * F::K_PITCH + tid * (F::KP * F::BITS / 8) + u * (F::UNIT * F::BITS / 8);
+                const uint32_t from = sm.codes + (16 * half + gid) * F::K_PITCH + tid * (F::KP * F::BITS / 8) + u * (F::UNIT * F::BITS / 8);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t row = from + r * 8 * F::K_PITCH;
@@ -451,6 +438,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 }
             }
         }
+        __syncwarp();
+        if (tile + 1 < tiles) next_there = issue_keys();
+        cp_async_commit();
+
         float grow[NT][2];
         uint32_t w[2][NT][WT][2];  // p as columns
         bool grows = false;
@@ -524,9 +515,11 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         }
 
         // the values, half a tile after the other
+        cp_async_wait<1>();
+        __syncwarp();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint32_t v_from = at + F::V_AT + (16 * half + tid * 2) * F::V_PITCH + gid * F::VP * F::BITS / 8;
+            const uint32_t v_from = sm.codes + F::V_AT + (16 * half + tid * 2) * F::V_PITCH + gid * F::VP * F::BITS / 8;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
@@ -586,7 +579,12 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             }
         }
         __syncwarp();
-        stage = stage == S - 1 ? 0 : stage + 1;
+        there = next_there;
+        if (tile + 1 < tiles) {
+            copy_rows(std::integral_constant<int, 1>{}, there);
+            look_up(j0 + int64_t(tile + 2) * kAttnTile);
+        }
+        cp_async_commit();
     }
     // ---- what the piece comes to ----
 #pragma unroll
@@ -649,32 +647,30 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 }
 
 template <typename T, typename F>
-__global__ void __launch_bounds__(32 * F::WARPS, 1) attn_mma_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * attn_warps<T, F>, 1) attn_mma_kernel(const AttnArgs a) {
     __shared__ AttnTable table;
     pdl_next();
     attn_table(a, table);
     attn_empty<T>(a, table);
     const int groups = a.d / a.cache.group, warp = threadIdx.x >> 5;
     AttnSmem sm;
-    sm.bytes = attn_stage_bytes<F>(groups);
-    sm.stage = uint32_t(warp) * attn_warp_bytes<T, F>(sm.bytes);
-    sm.places = sm.stage + F::STAGES * sm.bytes;
-    sm.there = sm.places + kAttnPlaces;
-    sm.k_scales = sm.there + kAttnThere;
+    sm.codes = uint32_t(warp) * attn_warp_bytes<T, F>(groups);
+    sm.scales = sm.codes + F::S_AT;
+    sm.places = sm.scales + 2 * 32 * groups * 4;
+    sm.k_scales = sm.places + kAttnPlaces;
     sm.v_scales = sm.k_scales + F::UNITS * 128;
-    sm.bias = sm.v_scales + (std::is_same_v<T, __nv_bfloat16> ? 1 : 2) * F::UNITS * 64;
-    attn_pieces(a, table, warp * int(gridDim.x) + int(blockIdx.x),
-                [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
+    sm.bias = sm.v_scales + kAttnFactors<T> * F::UNITS * 64;
+    attn_pieces(a, table, [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
 }
 
 template <typename T, typename F>
 nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&attn_mma_kernel<T, F>);
     const int groups = a.d / a.cache.group;
-    const size_t warp = attn_warp_bytes<T, F>(attn_stage_bytes<F>(groups));
+    const size_t warp = attn_warp_bytes<T, F>(groups);
     // as many workers to an SM as have room for their rings beside the table
     const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 64;
-    const int warps = int(std::min<size_t>(F::WARPS, room / warp));
+    const int warps = int(std::min<size_t>(attn_warps<T, F>, room / warp));
     a.workers = dev->sms * warps;
     attn_snap(a);
     const size_t smem = warps * warp;
