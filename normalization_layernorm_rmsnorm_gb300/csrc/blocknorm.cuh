@@ -174,6 +174,376 @@ __global__ void __launch_bounds__(kBlockThreads) block_cols_kernel(const BlockAr
 }
 
 // ---------------------------------------------------------------------------
+// whole 16-byte vectors, forward: a row in the registers of a warp, or of a CTA
+// ---------------------------------------------------------------------------
+// Every input is read once and every output written once; the stored stream is
+// kept as its rounded bits for the second norm.  ROWS rows to a CTA (a warp each)
+// or one.  Bound by bytes; the weights and the gate come from L1.
+constexpr int kBlockRowWarps = 4;  // rows of a CTA where a warp takes one
+
+template <typename T, int VPT, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fwd_vec_kernel(const BlockArgs a) {
+    constexpr int VE = kVec<T>, H = VE / 2;
+    __shared__ float sums[2][16];
+    pdl_next();
+    const int threads = WARP_ROW ? 32 : int(blockDim.x), t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t r = WARP_ROW ? int64_t(blockIdx.x) * kBlockRowWarps + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP_ROW && r >= a.rows) return;
+    const int nvec = a.cols / VE;
+    const int64_t at = r * nvec, gate_at = a.gates ? row_div(r, a.per_gate) * nvec : 0;
+    const float inv = 1.f / float(a.cols);
+    auto row_sum = [&](float v, int which) {
+        v = warp_sum(v);
+        if constexpr (WARP_ROW) return v;
+        if ((threadIdx.x & 31) == 0) sums[which][threadIdx.x >> 5] = v;
+        __syncthreads();
+        float all = 0.f;
+        for (int w = 0; w < int(blockDim.x >> 5); ++w) all += sums[which][w];
+        return all;
+    };
+    auto vec = [&](const void* p, int64_t i) { return ld_after(static_cast<const uint4*>(p) + i); };
+    uint4 fr[VPT], xr[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+        if (j * threads + t < nvec) fr[j] = vec(a.f, at + j * threads + t);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+        if (j * threads + t < nvec) xr[j] = vec(a.x, at + j * threads + t);
+    float r1 = 1.f;
+    if (a.post) {
+        float2 s = f2(0.f);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (j * threads + t >= nvec) break;
+            float2 f[H];
+            unpack2<T>(fr[j], f);
+#pragma unroll
+            for (int h = 0; h < H; ++h) s = __ffma2_rn(f[h], f[h], s);
+        }
+        r1 = rsqrtf(row_sum(s.x + s.y, 0) * inv + a.eps);
+        if (a.rstd_post && t == 0) a.rstd_post[r] = r1;
+    }
+    float2 s = f2(0.f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = j * threads + t;
+        if (i >= nvec) break;
+        float2 f[H], x[H], w[H], g[H], o[H];
+        unpack2<T>(fr[j], f);
+        unpack2<T>(xr[j], x);
+        if (a.post) {
+            if (a.w_post) unpack2<T>(vec(a.w_post, i), w);
+#pragma unroll
+            for (int h = 0; h < H; ++h) f[h] = a.w_post ? __fmul2_rn(__fmul2_rn(f[h], f2(r1)), w[h]) : __fmul2_rn(f[h], f2(r1));
+        }
+        if (a.gates) unpack2<T>(vec(a.gate, gate_at + i), g);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            o[h] = __ffma2_rn(a.gates ? __fmul2_rn(g[h], f2(a.alpha)) : f2(a.alpha), f[h], x[h]);
+        xr[j] = pack2x<T>(o);
+        st_v4(static_cast<uint4*>(a.y) + at + i, xr[j]);
+        unpack2<T>(xr[j], o);
+#pragma unroll
+        for (int h = 0; h < H; ++h) s = __ffma2_rn(o[h], o[h], s);
+    }
+    if (!a.h) return;
+    const float r2 = rsqrtf(row_sum(s.x + s.y, 1) * inv + a.eps);
+    if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = j * threads + t;
+        if (i >= nvec) break;
+        float2 y[H], w[H];
+        unpack2<T>(xr[j], y);
+        if (a.w_pre) unpack2<T>(vec(a.w_pre, i), w);
+#pragma unroll
+        for (int h = 0; h < H; ++h) y[h] = a.w_pre ? __fmul2_rn(__fmul2_rn(y[h], f2(r2)), w[h]) : __fmul2_rn(y[h], f2(r2));
+        st_v4(static_cast<uint4*>(a.h) + at + i, pack2x<T>(y));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// whole 16-byte vectors, backward: rows through a ring in shared memory
+// ---------------------------------------------------------------------------
+// A CTA stays for its chunk of rows.  One bulk copy for each of dh, dy, f and y
+// brings the next rows into a slot of the ring (a few slots ahead: enough bytes in
+// flight for the memory without a register each), and groups of threads take a
+// row of the slot each, a thread the same VPT vectors of every row, so that the
+// columns' sums stay in its registers.  A row's elements are read from the slot
+// once and kept as their bits through its two sums (sum(G*y), then sum(g*f),
+// which needs the first); after the first the slot is free.  A slot does not
+// reach over the end of a gate's row; there the groups' sums of its gradient are
+// added, in their order.
+constexpr int kBlockConsumers = 512;
+constexpr int kBlockSlots = 8;                       // at most
+constexpr uint64_t kBlockWaitNs = 2000000000ull;     // bounded waits: 2 s
+constexpr int kBlockBar = 1;                         // the groups' named barriers
+
+struct BlockRing {
+    int groups, threads;     // groups of threads to a CTA; threads of a group, whole warps
+    int slots;
+    uint32_t tensor_bytes;   // of a tensor's rows in a slot
+    uint32_t slot_bytes;
+    uint32_t ring_at;        // after the weights
+};
+
+// The chunk's rows, slot by slot: f(first row, rows, whether a gate's row ends with them).
+struct BlockWalk {
+    int64_t r, end, gate_end;
+    int count;
+    __device__ __forceinline__ BlockWalk(const BlockArgs& a, bool by_gate) : r(chunk_begin(a, blockIdx.x)), end(chunk_begin(a, blockIdx.x + 1)) {
+        gate_end = by_gate ? (row_div(r, a.per_gate) + 1) * a.per_gate.d : end;
+        count = 0;
+    }
+    __device__ __forceinline__ bool next(const BlockArgs& a, const BlockRing& g) {
+        r += count;
+        if (r >= end) return false;
+        if (r == gate_end) gate_end += a.per_gate.d;
+        count = int(min(int64_t(g.groups), min(end, gate_end) - r));
+        return true;
+    }
+};
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(const BlockArgs a, const BlockRing g) {
+    constexpr int VE = kVec<T>, H = VE / 2;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(8) uint64_t full[kBlockSlots], empty[kBlockSlots];
+    __shared__ float sums[2][2][kBlockConsumers / 32];
+    __shared__ int s_bad;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = int(threadIdx.x) / g.threads, t = int(threadIdx.x) - group * g.threads, warps = g.threads >> 5;
+    const int nvec = a.cols / VE;
+    if (threadIdx.x == 0) {
+        s_bad = 0;
+        for (int i = 0; i < g.slots; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], g.groups);
+        }
+        mbar_init_fence();
+    }
+    pdl_next();
+    uint4* const weights = reinterpret_cast<uint4*>(smem);  // w_pre, w_post
+    for (int i = int(threadIdx.x); i < 2 * nvec; i += int(blockDim.x)) {
+        const void* w = i < nvec ? a.w_pre : a.w_post;
+        float2 one[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) one[h] = f2(1.f);
+        weights[i] = w ? ld_after(static_cast<const uint4*>(w) + (i < nvec ? i : i - nvec)) : pack2x<T>(one);
+    }
+    __syncthreads();
+
+    const bool by_row = a.gates > 0 && a.per_gate.d == 1;  // a gate of its own for every row: its gradient is written as it is made
+    const bool by_gate = a.gates > 0 && !by_row && a.dgate;
+    const int64_t row_bytes = int64_t(a.cols) * int64_t(sizeof(T));
+    const uint64_t pol = l2_evict_first();
+    bool bad = false;
+    // thread 0 asks for the rows, slots ahead
+    BlockWalk ahead(a, by_gate);
+    int asked = 0;
+    auto ask = [&]() {
+        if (!ahead.next(a, g)) return;
+        const int slot = asked % g.slots;
+        if (asked >= g.slots && !mbar_wait_bounded(&empty[slot], uint32_t(asked / g.slots - 1) & 1u, kBlockWaitNs)) {
+            bad = true;
+            ahead.r = ahead.end;  // no more copies
+            ahead.count = 0;
+            return;
+        }
+        const uint32_t bytes = uint32_t(ahead.count * row_bytes);
+        unsigned char* to = smem + g.ring_at + size_t(slot) * g.slot_bytes;
+        const void* from[4] = {a.dh, a.dy, a.f, a.dh ? a.y : nullptr};
+        const int tensors = (a.dh ? 2 : 0) + (a.dy ? 1 : 0) + 1;
+        mbar_arrive_expect_tx(&full[slot], bytes * tensors);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (from[k])
+                bulk_g2s(to + k * g.tensor_bytes, static_cast<const unsigned char*>(from[k]) + ahead.r * row_bytes, bytes,
+                         &full[slot], pol);
+        ++asked;
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < g.slots; ++i) ask();
+
+    float2 sum_pre[VPT][H], sum_post[VPT][H], sum_gate[VPT][H];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int h = 0; h < H; ++h) sum_pre[j][h] = sum_post[j][h] = sum_gate[j][h] = f2(0.f);
+    int phase = 0;
+    auto row_sum = [&](float v, int which) {
+        v = warp_sum(v);
+        if (warps == 1) return v;
+        if (lane == 0) sums[which][phase][warp] = v;
+        named_barrier(kBlockBar + group, g.threads);
+        float all = 0.f;
+        for (int w = 0; w < warps; ++w) all += sums[which][phase][group * warps + w];
+        return all;
+    };
+    const float inv = 1.f / float(a.cols);
+    const bool consumer = group < g.groups;
+    // the groups' sums of the gradient of a row of the gate (kind 4: that row itself, in T) or of a weight, to `out`
+    auto flush = [&](float2 (&acc)[VPT][H], float* out, void* out_t) {
+        // (the ring may be in use: its own place, before the ring)
+        float* place = reinterpret_cast<float*>(smem + 2 * size_t(nvec) * 16);
+        if (g.groups == 1) {
+            if (consumer) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    const int i = j * g.threads + t;
+                    if (i >= nvec) break;
+                    if (out_t) st_v4(static_cast<uint4*>(out_t) + i, pack2x<T>(acc[j]));
+                    else
+#pragma unroll
+                        for (int h = 0; h < H; ++h) reinterpret_cast<float2*>(out)[i * H + h] = acc[j][h];
+                }
+            }
+        } else {
+            for (int k = 0; k < g.groups; ++k) {
+                if (group == k && consumer) {
+#pragma unroll
+                    for (int j = 0; j < VPT; ++j) {
+                        const int i = j * g.threads + t;
+                        if (i >= nvec) break;
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            float2* p = reinterpret_cast<float2*>(place) + h * nvec + i;
+                            *p = k == 0 ? acc[j][h] : __fadd2_rn(*p, acc[j][h]);
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+            for (int i = int(threadIdx.x); i < nvec; i += int(blockDim.x)) {
+                float2 v[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) v[h] = reinterpret_cast<float2*>(place)[h * nvec + i];
+                if (out_t) st_v4(static_cast<uint4*>(out_t) + i, pack2x<T>(v));
+                else
+#pragma unroll
+                    for (int h = 0; h < H; ++h) reinterpret_cast<float2*>(out)[i * H + h] = v[h];
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int h = 0; h < H; ++h) acc[j][h] = f2(0.f);
+    };
+
+    BlockWalk walk(a, by_gate);
+    int64_t first = walk.r;  // of the gate's row's rows in this chunk
+    for (int q = 0; walk.next(a, g); ++q) {
+        const int slot = q % g.slots;
+        if (group < walk.count) {
+            if (!bad && !mbar_wait_bounded(&full[slot], uint32_t(q / g.slots) & 1u, kBlockWaitNs)) bad = true;
+            const unsigned char* from = smem + g.ring_at + size_t(slot) * g.slot_bytes + group * row_bytes;
+            const int64_t r = walk.r + group, gate_at = a.gates ? row_div(r, a.per_gate) * nvec : 0;
+            const float r1 = a.post ? ld_after(a.rstd_post + r) : 1.f, r2 = a.dh ? ld_after(a.rstd_pre + r) : 0.f;
+            uint4 dhr[VPT], dyr[VPT], fr[VPT], yr[VPT], gr[VPT];
+            float2 s = f2(0.f);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = j * g.threads + t;
+                if (i >= nvec) break;
+                const uint4* at = reinterpret_cast<const uint4*>(from) + i;
+                const uint32_t step = g.tensor_bytes / 16;
+                if (a.gates) gr[j] = ld_after(static_cast<const uint4*>(a.gate) + gate_at + i);
+                dyr[j] = a.dy ? at[step] : make_uint4(0, 0, 0, 0);
+                fr[j] = at[2 * step];
+                if (a.dh) {
+                    dhr[j] = at[0];
+                    yr[j] = at[3 * step];
+                    float2 dh[H], y[H], w[H];
+                    unpack2<T>(dhr[j], dh);
+                    unpack2<T>(yr[j], y);
+                    unpack2<T>(weights[i], w);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) s = __ffma2_rn(__fmul2_rn(dh[h], w[h]), y[h], s);
+                }
+            }
+            float c2 = 0.f;
+            if (a.dh) c2 = r2 * r2 * r2 * (row_sum(s.x + s.y, 0) * inv);
+            else if (warps > 1) named_barrier(kBlockBar + group, g.threads);
+            else __syncwarp();
+            if (t == 0) mbar_arrive(&empty[slot]);  // (every thread of the group has read its part)
+            if (threadIdx.x == 0 && q > 0) ask();
+            s = f2(0.f);
+            float2 back[VPT][H];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = j * g.threads + t;
+                if (i >= nvec) break;
+                float2 d[H], f[H], gate[H], w[H];
+                unpack2<T>(dyr[j], d);
+                unpack2<T>(fr[j], f);
+                if (a.dh) {
+                    float2 dh[H], y[H];
+                    unpack2<T>(dhr[j], dh);
+                    unpack2<T>(yr[j], y);
+                    unpack2<T>(weights[i], w);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        d[h] = __fadd2_rn(d[h], __ffma2_rn(f2(r2), __fmul2_rn(dh[h], w[h]), __fmul2_rn(y[h], f2(-c2))));
+                        sum_pre[j][h] = __ffma2_rn(dh[h], __fmul2_rn(y[h], f2(r2)), sum_pre[j][h]);
+                    }
+                }
+                st_v4(static_cast<uint4*>(a.dx) + r * nvec + i, pack2x<T>(d));
+                unpack2<T>(weights[nvec + i], w);
+                if (a.gates) unpack2<T>(gr[j], gate);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const float2 ad = __fmul2_rn(d[h], f2(a.alpha)), dn = a.gates ? __fmul2_rn(ad, gate[h]) : ad;
+                    const float2 unit = a.post ? __fmul2_rn(f[h], f2(r1)) : f[h];
+                    const float2 n = a.post ? __fmul2_rn(unit, w[h]) : unit;
+                    if (by_row) gate[h] = __fmul2_rn(ad, n);
+                    else sum_gate[j][h] = __ffma2_rn(ad, n, sum_gate[j][h]);
+                    sum_post[j][h] = __ffma2_rn(dn, unit, sum_post[j][h]);
+                    back[j][h] = a.post ? __fmul2_rn(dn, w[h]) : dn;
+                    s = __ffma2_rn(back[j][h], f[h], s);
+                }
+                if (by_row && a.dgate) st_v4(static_cast<uint4*>(a.dgate) + gate_at + i, pack2x<T>(gate));
+            }
+            float c1 = 0.f;
+            if (a.post) c1 = r1 * r1 * r1 * (row_sum(s.x + s.y, 1) * inv);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = j * g.threads + t;
+                if (i >= nvec) break;
+                if (a.post) {
+                    float2 f[H];
+                    unpack2<T>(fr[j], f);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) back[j][h] = __ffma2_rn(f2(r1), back[j][h], __fmul2_rn(f[h], f2(-c1)));
+                }
+                st_v4(static_cast<uint4*>(a.df) + r * nvec + i, pack2x<T>(back[j]));
+            }
+            phase ^= 1;
+        } else if (consumer) {
+            if (t == 0) mbar_arrive(&empty[slot]);  // no row of this slot is this group's
+        }
+        if (by_gate && (walk.r + walk.count == walk.gate_end || walk.r + walk.count == walk.end)) {
+            const int64_t row = row_div(walk.r, a.per_gate);
+            const bool begins = first == row * a.per_gate.d, ends = walk.r + walk.count == walk.gate_end;
+            flush(sum_gate, part_row(a, begins ? 3 : 2, blockIdx.x),
+                  begins && ends ? static_cast<uint4*>(a.dgate) + row * nvec : nullptr);
+            first = walk.r + walk.count;
+        }
+    }
+    __syncthreads();
+    if (a.dw_post) flush(sum_post, part_row(a, 0, blockIdx.x), nullptr);
+    if (a.dw_pre) flush(sum_pre, part_row(a, 1, blockIdx.x), nullptr);
+    if (bad) s_bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0 && s_bad) {
+        atomicOr(a.err, kErrTimeoutStage);
+        // no copy may be under way when the CTA ends
+        for (int i = 0; i < g.slots && i < asked; ++i)
+            (void)mbar_wait_bounded(&full[i], uint32_t((asked - 1 - i) / g.slots) & 1u, kBlockWaitNs);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the chunks' partial rows added, each column in a fixed order with the rounding
 // errors carried (the partial rows can be much larger than their sum).  blockIdx.y
 // 0 and 1: dw_post, dw_pre; the others the rows of the gate that several chunks
@@ -234,17 +604,48 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
+template <typename T, int VPT>
+nrm_status block_fwd_vec(BlockArgs& a, int warps, cudaStream_t s) {
+    void* p[] = {&a};
+    if (warps == 0)
+        return launch_pdl(reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, true>),
+                          dim3(unsigned((a.rows + kBlockRowWarps - 1) / kBlockRowWarps)), dim3(32 * kBlockRowWarps), p, s);
+    return launch_pdl(reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, false>), dim3(unsigned(a.rows)),
+                      dim3(unsigned(32 * warps)), p, s);
+}
+
 template <typename T>
 nrm_status block_norm_fwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     BlockArgs a = args;
     const DevInfo* dev = dev_info();
     if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
     a.err = dev->err;
-    (void)vec;
     if (a.rows == 0) return NRM_OK;
+    const int nvec = a.cols / kVec<T>;
+    if (vec && nvec <= 2048 && a.rows < (int64_t(1) << 31)) {
+        // a warp to a row of up to 4 vectors a lane, where rows are many; else as few warps as give a thread 2 (long
+        // rows 4), and where there are no more rows than SMs, 1
+        if (nvec <= 128 && a.rows > dev->sms) {
+            const int v = (nvec + 31) / 32;
+            return v <= 1 ? block_fwd_vec<T, 1>(a, 0, s) : v == 2 ? block_fwd_vec<T, 2>(a, 0, s) : block_fwd_vec<T, 4>(a, 0, s);
+        }
+        const int v = a.rows <= dev->sms && nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+        const int warps = (nvec + 32 * v - 1) / (32 * v);
+        return v == 1 ? block_fwd_vec<T, 1>(a, warps, s) : v == 2 ? block_fwd_vec<T, 2>(a, warps, s) : block_fwd_vec<T, 4>(a, warps, s);
+    }
     void* p[] = {&a};
     return launch_pdl(reinterpret_cast<const void*>(&block_fwd_scalar_kernel<T>),
                       dim3(unsigned(std::min<int64_t>(a.rows, int64_t(dev->sms) * 64))), dim3(kBlockThreads), p, s);
+}
+
+template <typename T, int VPT>
+nrm_status block_bwd_ring(BlockArgs& a, BlockRing& g, size_t smem, cudaStream_t s) {
+    const void* fn = reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, VPT>);
+    nrm_status st = prepare_kernel(fn, smem, false);
+    if (st != NRM_OK) return st;
+    void* p[] = {&a, &g};
+    const int threads = (g.groups * g.threads + 31) / 32 * 32;
+    return launch_pdl(fn, dim3(unsigned(a.chunks)), dim3(unsigned(threads)), p, s, smem);
 }
 
 template <typename T>
@@ -253,7 +654,6 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     const DevInfo* dev = dev_info();
     if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
     a.err = dev->err;
-    (void)vec;
     if (a.rows == 0) {
         const size_t row = size_t(a.cols) * sizeof(T);
         for (auto& o : {std::make_pair(a.dw_post, int64_t(1)), std::make_pair(a.dw_pre, int64_t(1)),
@@ -265,14 +665,39 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
         return NRM_OK;
     }
     void* p[] = {&a};
-    nrm_status st = launch_pdl(reinterpret_cast<const void*>(&block_bwd_scalar_kernel<T>),
-                               dim3(unsigned(std::min<int64_t>(a.rows, int64_t(dev->sms) * 64))), dim3(kBlockThreads),
-                               p, s);
-    if (st != NRM_OK || (!a.dgate && !a.dw_post && !a.dw_pre)) return st;
-    st = launch_pdl(reinterpret_cast<const void*>(&block_cols_kernel<T>),
-                    dim3(unsigned((a.cols + kBlockThreads - 1) / kBlockThreads), unsigned(a.chunks)),
-                    dim3(kBlockThreads), p, s);
-    if (st != NRM_OK) return st;
+    nrm_status st;
+    bool sums = a.dgate || a.dw_post || a.dw_pre;
+    const int nvec = a.cols / kVec<T>;
+    BlockRing g{};
+    if (vec && nvec <= 2 * kBlockConsumers) {
+        const int vpt = nvec > kBlockConsumers ? 2 : 1;
+        g.threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
+        g.groups = std::min(kBlockConsumers / g.threads, 14);  // (named barriers)
+        const uint32_t row = uint32_t(a.cols) * uint32_t(sizeof(T));
+        g.tensor_bytes = uint32_t(g.groups) * row;
+        g.slot_bytes = 4 * g.tensor_bytes;
+        // the weights, and the place where the groups' sums are added
+        g.ring_at = (uint32_t(nvec) * 32 + (g.groups > 1 ? uint32_t(a.cols) * 4 : 0) + 127) / 128 * 128;
+        const int room = (dev->max_smem_optin - 1024 - int(g.ring_at)) / int(g.slot_bytes);
+        g.slots = std::min(room, kBlockSlots);
+        if (g.slots >= 2) {
+            a.chunks = std::min<int64_t>(dev->sms, (a.rows + g.groups - 1) / g.groups);
+            const size_t smem = g.ring_at + size_t(g.slots) * g.slot_bytes;
+            st = vpt == 1 ? block_bwd_ring<T, 1>(a, g, smem, s) : block_bwd_ring<T, 2>(a, g, smem, s);
+            // a gate for every row is done with
+            if (a.gates > 0 && a.per_gate.d == 1) a.dgate = nullptr;
+            sums = a.dgate || a.dw_post || a.dw_pre;
+        }
+    }
+    if (g.slots < 2) {
+        st = launch_pdl(reinterpret_cast<const void*>(&block_bwd_scalar_kernel<T>),
+                        dim3(unsigned(std::min<int64_t>(a.rows, int64_t(dev->sms) * 64))), dim3(kBlockThreads), p, s);
+        if (st != NRM_OK || !sums) return st;
+        st = launch_pdl(reinterpret_cast<const void*>(&block_cols_kernel<T>),
+                        dim3(unsigned((a.cols + kBlockThreads - 1) / kBlockThreads), unsigned(a.chunks)),
+                        dim3(kBlockThreads), p, s);
+    }
+    if (st != NRM_OK || !sums) return st;
     int by_chunk = a.gates > a.chunks;
     const int64_t gate_rows = a.dgate ? (by_chunk ? a.chunks - 1 : a.gates) : 0;
     void* q[] = {&a, &by_chunk};
