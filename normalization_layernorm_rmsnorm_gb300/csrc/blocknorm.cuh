@@ -28,6 +28,15 @@ __device__ __forceinline__ float cta_sum(float v, float* sums) {
     return t;
 }
 
+// Sum of the warps' numbers in `sums` (at most 16), the same bits in every lane of every warp.
+__device__ __forceinline__ float warps_sum(const float* sums, int warps) {
+    const int lane = threadIdx.x & 31;
+    float v = (lane & 15) < warps ? sums[lane & 15] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // Element i of a weight (1 where there is none).
 template <typename T>
 __device__ __forceinline__ float weight_at(const void* w, int64_t i) {
@@ -197,9 +206,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fw
         if constexpr (WARP_ROW) return v;
         if ((threadIdx.x & 31) == 0) sums[which][threadIdx.x >> 5] = v;
         __syncthreads();
-        float all = 0.f;
-        for (int w = 0; w < int(blockDim.x >> 5); ++w) all += sums[which][w];
-        return all;
+        return warps_sum(sums[which], int(blockDim.x >> 5));
     };
     auto vec = [&](const void* p, int64_t i) { return ld_after(static_cast<const uint4*>(p) + i); };
     uint4 fr[VPT], xr[VPT];
@@ -340,15 +347,20 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     bool bad = false;
     // thread 0 asks for the rows, slots ahead
     BlockWalk ahead(a, by_gate);
-    int asked = 0;
+    int asked = 0, ask_slot = 0;
+    uint32_t ask_round = 0;
     auto ask = [&]() {
         if (!ahead.next(a, g)) return;
-        const int slot = asked % g.slots;
-        if (asked >= g.slots && !mbar_wait_bounded(&empty[slot], uint32_t(asked / g.slots - 1) & 1u, kBlockWaitNs)) {
+        const int slot = ask_slot;
+        if (ask_round > 0 && !mbar_wait_bounded(&empty[slot], (ask_round - 1) & 1u, kBlockWaitNs)) {
             bad = true;
             ahead.r = ahead.end;  // no more copies
             ahead.count = 0;
             return;
+        }
+        if (++ask_slot == g.slots) {
+            ask_slot = 0;
+            ++ask_round;
         }
         const uint32_t bytes = uint32_t(ahead.count * row_bytes);
         unsigned char* to = smem + g.ring_at + size_t(slot) * g.slot_bytes;
@@ -376,9 +388,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
         if (warps == 1) return v;
         if (lane == 0) sums[which][phase][warp] = v;
         named_barrier(kBlockBar + group, g.threads);
-        float all = 0.f;
-        for (int w = 0; w < warps; ++w) all += sums[which][phase][group * warps + w];
-        return all;
+        return warps_sum(&sums[which][phase][group * warps], warps);
     };
     const float inv = 1.f / float(a.cols);
     const bool consumer = group < g.groups;
@@ -433,10 +443,15 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 
     BlockWalk walk(a, by_gate);
     int64_t first = walk.r;  // of the gate's row's rows in this chunk
-    for (int q = 0; walk.next(a, g); ++q) {
-        const int slot = q % g.slots;
+    int slot = -1;
+    uint32_t round = 0;
+    for (bool begun = false; walk.next(a, g); begun = true) {
+        if (++slot == g.slots) {
+            slot = 0;
+            ++round;
+        }
         if (group < walk.count) {
-            if (!bad && !mbar_wait_bounded(&full[slot], uint32_t(q / g.slots) & 1u, kBlockWaitNs)) bad = true;
+            if (!bad && !mbar_wait_bounded(&full[slot], round & 1u, kBlockWaitNs)) bad = true;
             const unsigned char* from = smem + g.ring_at + size_t(slot) * g.slot_bytes + group * row_bytes;
             const int64_t r = walk.r + group, gate_at = a.gates ? row_div(r, a.per_gate) * nvec : 0;
             const float r1 = a.post ? ld_after(a.rstd_post + r) : 1.f, r2 = a.dh ? ld_after(a.rstd_pre + r) : 0.f;
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             else if (warps > 1) named_barrier(kBlockBar + group, g.threads);
             else __syncwarp();
             if (t == 0) mbar_arrive(&empty[slot]);  // (every thread of the group has read its part)
-            if (threadIdx.x == 0 && q > 0) ask();
+            if (threadIdx.x == 0 && begun) ask();
             s = f2(0.f);
             float2 back[VPT][H];
 #pragma unroll
@@ -548,22 +563,27 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 // errors carried (the partial rows can be much larger than their sum).  blockIdx.y
 // 0 and 1: dw_post, dw_pre; the others the rows of the gate that several chunks
 // hold: each of its rows, or, where there are more of them than chunks, the row
-// that goes on from one chunk into the next.
+// that goes on from one chunk into the next.  The warps of a CTA share a sum's
+// partial rows; where the gate's rows are many, and so each has few, a warp takes
+// a row of its own (`by_warp`).
 // ---------------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const BlockArgs a, int by_chunk) {
+__global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const BlockArgs a, int by_chunk, int by_warp) {
     __shared__ float part[kBlockSumWarps][2][33];
     pdl_next();
     void* out;
     int64_t c0 = 0, c1 = a.chunks - 1, row = 0;
     int kind = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool alone = by_warp && blockIdx.y >= 2;
     if (blockIdx.y < 2) {
         kind = int(blockIdx.y);
         out = kind == 0 ? a.dw_post : a.dw_pre;
     } else {
         kind = 2;
         out = a.dgate;
-        row = int64_t(blockIdx.y) - 2;
+        row = alone ? (int64_t(blockIdx.y) - 2) * kBlockSumWarps + warp : int64_t(blockIdx.y) - 2;
+        if (row >= (by_chunk ? a.chunks - 1 : a.gates)) return;
         if (by_chunk) {
             const int64_t c = row, r0 = chunk_begin(a, c + 1);
             row = row_div(r0, a.per_gate);
@@ -574,7 +594,6 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
         if (c0 == c1) return;  // written by that chunk
     }
     if (!out) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = int(blockIdx.x) * 32 + lane;
     // Neumaier's sum
     float s = 0.f, e = 0.f;
@@ -585,8 +604,12 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
     };
     if (col < a.cols) {
 #pragma unroll 4
-        for (int64_t c = c0 + warp; c <= c1; c += kBlockSumWarps)
+        for (int64_t c = alone ? c0 : c0 + warp; c <= c1; c += alone ? 1 : kBlockSumWarps)
             add(ld_after(part_row(a, kind == 2 && c == c0 ? 3 : kind, c) + col));
+    }
+    if (alone) {
+        if (col < a.cols) put<T>(out, row * a.cols + col, s + e);
+        return;
     }
     part[warp][0][lane] = s;
     part[warp][1][lane] = e;
@@ -699,8 +722,10 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     }
     if (st != NRM_OK || !sums) return st;
     int by_chunk = a.gates > a.chunks;
-    const int64_t gate_rows = a.dgate ? (by_chunk ? a.chunks - 1 : a.gates) : 0;
-    void* q[] = {&a, &by_chunk};
+    int64_t gate_rows = a.dgate ? (by_chunk ? a.chunks - 1 : a.gates) : 0;
+    int by_warp = gate_rows > 4;
+    if (by_warp) gate_rows = (gate_rows + kBlockSumWarps - 1) / kBlockSumWarps;
+    void* q[] = {&a, &by_chunk, &by_warp};
     return launch_pdl(reinterpret_cast<const void*>(&block_sum_kernel<T>),
                       dim3(unsigned((a.cols + 31) / 32), unsigned(2 + gate_rows)), dim3(kBlockSumWarps * 32), q, s);
 }
