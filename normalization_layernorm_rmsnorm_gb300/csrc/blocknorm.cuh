@@ -186,86 +186,121 @@ __global__ void __launch_bounds__(kBlockThreads) block_cols_kernel(const BlockAr
 // whole 16-byte vectors, forward: a row in the registers of a warp, or of a CTA
 // ---------------------------------------------------------------------------
 // Every input is read once and every output written once; the stored stream is
-// kept as its rounded bits for the second norm.  ROWS rows to a CTA (a warp each)
-// or one.  Bound by bytes; the weights and the gate come from L1.
+// kept as its rounded bits for the second norm.  A warp or a CTA takes `per`
+// neighbouring rows, so that its columns of the weights and the gate stay in
+// registers, and asks for the next row before it has done with one.  Bound by bytes.
 constexpr int kBlockRowWarps = 4;  // rows of a CTA where a warp takes one
 
 template <typename T, int VPT, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fwd_vec_kernel(const BlockArgs a) {
+__global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fwd_vec_kernel(const BlockArgs a, int per) {
     constexpr int VE = kVec<T>, H = VE / 2;
-    __shared__ float sums[2][16];
+    __shared__ float sums[2][2][16];
     pdl_next();
     const int threads = WARP_ROW ? 32 : int(blockDim.x), t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t r = WARP_ROW ? int64_t(blockIdx.x) * kBlockRowWarps + (threadIdx.x >> 5) : blockIdx.x;
-    if (WARP_ROW && r >= a.rows) return;
+    int64_t r = (WARP_ROW ? int64_t(blockIdx.x) * kBlockRowWarps + (threadIdx.x >> 5) : int64_t(blockIdx.x)) * per;
+    const int64_t end = min(a.rows, r + per);
+    if (r >= end) return;
     const int nvec = a.cols / VE;
-    const int64_t at = r * nvec, gate_at = a.gates ? row_div(r, a.per_gate) * nvec : 0;
     const float inv = 1.f / float(a.cols);
+    int phase = 0;
     auto row_sum = [&](float v, int which) {
         v = warp_sum(v);
         if constexpr (WARP_ROW) return v;
-        if ((threadIdx.x & 31) == 0) sums[which][threadIdx.x >> 5] = v;
+        if ((threadIdx.x & 31) == 0) sums[which][phase][threadIdx.x >> 5] = v;
         __syncthreads();
-        return warps_sum(sums[which], int(blockDim.x >> 5));
+        return warps_sum(sums[which][phase], int(blockDim.x >> 5));
     };
     auto vec = [&](const void* p, int64_t i) { return ld_after(static_cast<const uint4*>(p) + i); };
-    uint4 fr[VPT], xr[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-        if (j * threads + t < nvec) fr[j] = vec(a.f, at + j * threads + t);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-        if (j * threads + t < nvec) xr[j] = vec(a.x, at + j * threads + t);
-    float r1 = 1.f;
-    if (a.post) {
-        float2 s = f2(0.f);
+    auto in_row = [&](int j) { return j * threads + t < nvec; };
+    // this thread's columns of alpha * gate * w_post and of w_pre
+    float2 scale[VPT][H], w_pre[VPT][H];
+    auto load_scale = [&](int64_t gate_row) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (j * threads + t >= nvec) break;
-            float2 f[H];
-            unpack2<T>(fr[j], f);
+            float2 v[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) s = __ffma2_rn(f[h], f[h], s);
+            for (int h = 0; h < H; ++h) scale[j][h] = f2(a.alpha);
+            if (!in_row(j)) continue;
+            if (a.gates) {
+                unpack2<T>(vec(a.gate, gate_row * nvec + j * threads + t), v);
+#pragma unroll
+                for (int h = 0; h < H; ++h) scale[j][h] = __fmul2_rn(scale[j][h], v[h]);
+            }
+            if (a.w_post) {
+                unpack2<T>(vec(a.w_post, j * threads + t), v);
+#pragma unroll
+                for (int h = 0; h < H; ++h) scale[j][h] = __fmul2_rn(scale[j][h], v[h]);
+            }
         }
-        r1 = rsqrtf(row_sum(s.x + s.y, 0) * inv + a.eps);
-        if (a.rstd_post && t == 0) a.rstd_post[r] = r1;
-    }
-    float2 s = f2(0.f);
+    };
+    uint4 fr[VPT], xr[VPT];
+    auto load_row = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (in_row(j)) fr[j] = vec(a.f, row * nvec + j * threads + t);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (in_row(j)) xr[j] = vec(a.x, row * nvec + j * threads + t);
+    };
+    load_row(r);
+    int64_t gate_row = a.gates ? row_div(r, a.per_gate) : 0, gate_end = a.gates ? (gate_row + 1) * a.per_gate.d : end;
+    load_scale(gate_row);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int i = j * threads + t;
-        if (i >= nvec) break;
-        float2 f[H], x[H], w[H], g[H], o[H];
-        unpack2<T>(fr[j], f);
-        unpack2<T>(xr[j], x);
+#pragma unroll
+        for (int h = 0; h < H; ++h) w_pre[j][h] = f2(1.f);
+        if (a.h && a.w_pre && in_row(j)) unpack2<T>(vec(a.w_pre, j * threads + t), w_pre[j]);
+    }
+    for (; r < end; ++r) {
+        if (r == gate_end) {
+            gate_end += a.per_gate.d;
+            load_scale(++gate_row);
+        }
+        const int64_t at = r * nvec + t;
+        float r1 = 1.f;
         if (a.post) {
-            if (a.w_post) unpack2<T>(vec(a.w_post, i), w);
+            float2 s = f2(0.f);
 #pragma unroll
-            for (int h = 0; h < H; ++h) f[h] = a.w_post ? __fmul2_rn(__fmul2_rn(f[h], f2(r1)), w[h]) : __fmul2_rn(f[h], f2(r1));
+            for (int j = 0; j < VPT; ++j) {
+                if (!in_row(j)) break;
+                float2 f[H];
+                unpack2<T>(fr[j], f);
+#pragma unroll
+                for (int h = 0; h < H; ++h) s = __ffma2_rn(f[h], f[h], s);
+            }
+            r1 = rsqrtf(row_sum(s.x + s.y, 0) * inv + a.eps);
+            if (a.rstd_post && t == 0) a.rstd_post[r] = r1;
         }
-        if (a.gates) unpack2<T>(vec(a.gate, gate_at + i), g);
+        float2 s = f2(0.f);
+        uint4 yr[VPT];
 #pragma unroll
-        for (int h = 0; h < H; ++h)
-            o[h] = __ffma2_rn(a.gates ? __fmul2_rn(g[h], f2(a.alpha)) : f2(a.alpha), f[h], x[h]);
-        xr[j] = pack2x<T>(o);
-        st_v4(static_cast<uint4*>(a.y) + at + i, xr[j]);
-        unpack2<T>(xr[j], o);
+        for (int j = 0; j < VPT; ++j) {
+            if (!in_row(j)) break;
+            float2 f[H], x[H];
+            unpack2<T>(fr[j], f);
+            unpack2<T>(xr[j], x);
 #pragma unroll
-        for (int h = 0; h < H; ++h) s = __ffma2_rn(o[h], o[h], s);
-    }
-    if (!a.h) return;
-    const float r2 = rsqrtf(row_sum(s.x + s.y, 1) * inv + a.eps);
-    if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
+            for (int h = 0; h < H; ++h) x[h] = __ffma2_rn(__fmul2_rn(f[h], f2(r1)), scale[j][h], x[h]);
+            yr[j] = pack2x<T>(x);
+            st_v4(static_cast<uint4*>(a.y) + at + j * threads, yr[j]);
+            if constexpr (sizeof(T) == 2) unpack2<T>(yr[j], x);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int i = j * threads + t;
-        if (i >= nvec) break;
-        float2 y[H], w[H];
-        unpack2<T>(xr[j], y);
-        if (a.w_pre) unpack2<T>(vec(a.w_pre, i), w);
+            for (int h = 0; h < H; ++h) s = __ffma2_rn(x[h], x[h], s);
+        }
+        if (r + 1 < end) load_row(r + 1);
+        if (!a.h) continue;
+        const float r2 = rsqrtf(row_sum(s.x + s.y, 1) * inv + a.eps);
+        if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
 #pragma unroll
-        for (int h = 0; h < H; ++h) y[h] = a.w_pre ? __fmul2_rn(__fmul2_rn(y[h], f2(r2)), w[h]) : __fmul2_rn(y[h], f2(r2));
-        st_v4(static_cast<uint4*>(a.h) + at + i, pack2x<T>(y));
+        for (int j = 0; j < VPT; ++j) {
+            if (!in_row(j)) break;
+            float2 y[H];
+            unpack2<T>(yr[j], y);
+#pragma unroll
+            for (int h = 0; h < H; ++h) y[h] = __fmul2_rn(__fmul2_rn(y[h], f2(r2)), w_pre[j][h]);
+            st_v4(static_cast<uint4*>(a.h) + at + j * threads, pack2x<T>(y));
+        }
+        phase ^= 1;
     }
 }
 
@@ -341,7 +376,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     __syncthreads();
 
     const bool by_row = a.gates > 0 && a.per_gate.d == 1;  // a gate of its own for every row: its gradient is written as it is made
-    const bool by_gate = a.gates > 0 && !by_row && a.dgate;
+    const bool by_gate = a.gates > 0 && !by_row && (a.gates > 1 || a.dgate);
     const int64_t row_bytes = int64_t(a.cols) * int64_t(sizeof(T));
     const uint64_t pol = l2_evict_first();
     bool bad = false;
@@ -377,11 +412,48 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     if (threadIdx.x == 0)
         for (int i = 0; i < g.slots; ++i) ask();
 
-    float2 sum_pre[VPT][H], sum_post[VPT][H], sum_gate[VPT][H];
+    // Over rows with one gate (and over all without), the sums of dgate and dw_post are this one's, times alpha*w_post
+    // and alpha*gate: sum_unit = sum of dx*f*r1.
+    float2 sum_pre[VPT][H], sum_post[VPT][H], sum_unit[VPT][H];
+    float2 scale[VPT][H];  // alpha * gate * w_post
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int h = 0; h < H; ++h) sum_pre[j][h] = sum_post[j][h] = sum_gate[j][h] = f2(0.f);
+        for (int h = 0; h < H; ++h) sum_pre[j][h] = sum_post[j][h] = sum_unit[j][h] = f2(0.f);
+    auto load_scale = [&](int64_t gate_row, bool with_weight, float2 (&to)[VPT][H]) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = j * g.threads + t;
+#pragma unroll
+            for (int h = 0; h < H; ++h) to[j][h] = f2(a.alpha);
+            if (i >= nvec) break;
+            float2 v[H];
+            if (with_weight) {
+                unpack2<T>(weights[nvec + i], v);
+#pragma unroll
+                for (int h = 0; h < H; ++h) to[j][h] = __fmul2_rn(to[j][h], v[h]);
+            }
+            if (a.gates && gate_row >= 0) {
+                unpack2<T>(ld_after(static_cast<const uint4*>(a.gate) + gate_row * nvec + i), v);
+#pragma unroll
+                for (int h = 0; h < H; ++h) to[j][h] = __fmul2_rn(to[j][h], v[h]);
+            }
+        }
+    };
+    // the rows of one gate are done: their share of dw_post, and sum_unit as the gradient of the gate
+    auto close_gate = [&](int64_t gate_row) {
+        float2 by[VPT][H];
+        load_scale(gate_row, false, by);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int h = 0; h < H; ++h) sum_post[j][h] = __ffma2_rn(sum_unit[j][h], by[j][h], sum_post[j][h]);
+        load_scale(-1, true, by);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int h = 0; h < H; ++h) sum_unit[j][h] = __fmul2_rn(sum_unit[j][h], by[j][h]);
+    };
     int phase = 0;
     auto row_sum = [&](float v, int which) {
         v = warp_sum(v);
@@ -391,26 +463,29 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
         return warps_sum(&sums[which][phase][group * warps], warps);
     };
     const float inv = 1.f / float(a.cols);
-    const bool consumer = group < g.groups;
-    // the groups' sums of the gradient of a row of the gate (kind 4: that row itself, in T) or of a weight, to `out`
+    auto clear = [&](float2 (&acc)[VPT][H]) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int h = 0; h < H; ++h) acc[j][h] = f2(0.f);
+    };
+    // the groups' sums of a gradient, added in their order, to a partial row `out` or, whole, to `out_t`
     auto flush = [&](float2 (&acc)[VPT][H], float* out, void* out_t) {
         // (the ring may be in use: its own place, before the ring)
         float* place = reinterpret_cast<float*>(smem + 2 * size_t(nvec) * 16);
         if (g.groups == 1) {
-            if (consumer) {
 #pragma unroll
-                for (int j = 0; j < VPT; ++j) {
-                    const int i = j * g.threads + t;
-                    if (i >= nvec) break;
-                    if (out_t) st_v4(static_cast<uint4*>(out_t) + i, pack2x<T>(acc[j]));
-                    else
+            for (int j = 0; j < VPT; ++j) {
+                const int i = j * g.threads + t;
+                if (i >= nvec) break;
+                if (out_t) st_v4(static_cast<uint4*>(out_t) + i, pack2x<T>(acc[j]));
+                else
 #pragma unroll
-                        for (int h = 0; h < H; ++h) reinterpret_cast<float2*>(out)[i * H + h] = acc[j][h];
-                }
+                    for (int h = 0; h < H; ++h) reinterpret_cast<float2*>(out)[i * H + h] = acc[j][h];
             }
         } else {
             for (int k = 0; k < g.groups; ++k) {
-                if (group == k && consumer) {
+                if (group == k) {
 #pragma unroll
                     for (int j = 0; j < VPT; ++j) {
                         const int i = j * g.threads + t;
@@ -435,14 +510,13 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             }
             __syncthreads();
         }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int h = 0; h < H; ++h) acc[j][h] = f2(0.f);
+        clear(acc);
     };
 
     BlockWalk walk(a, by_gate);
     int64_t first = walk.r;  // of the gate's row's rows in this chunk
+    int64_t gate_row = a.gates ? row_div(first, a.per_gate) : 0;
+    if (!by_row) load_scale(gate_row, true, scale);
     int slot = -1;
     uint32_t round = 0;
     for (bool begun = false; walk.next(a, g); begun = true) {
@@ -450,31 +524,35 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             slot = 0;
             ++round;
         }
+        if (by_gate && walk.r == first && begun) load_scale(gate_row, true, scale);
         if (group < walk.count) {
             if (!bad && !mbar_wait_bounded(&full[slot], round & 1u, kBlockWaitNs)) bad = true;
-            const unsigned char* from = smem + g.ring_at + size_t(slot) * g.slot_bytes + group * row_bytes;
-            const int64_t r = walk.r + group, gate_at = a.gates ? row_div(r, a.per_gate) * nvec : 0;
+            const uint4* const from =
+                reinterpret_cast<const uint4*>(smem + g.ring_at + size_t(slot) * g.slot_bytes + group * row_bytes) + t;
+            const uint32_t step = g.tensor_bytes / 16;
+            const int64_t r = walk.r + group, at = r * nvec + t;
             const float r1 = a.post ? ld_after(a.rstd_post + r) : 1.f, r2 = a.dh ? ld_after(a.rstd_pre + r) : 0.f;
-            uint4 dhr[VPT], dyr[VPT], fr[VPT], yr[VPT], gr[VPT];
-            float2 s = f2(0.f);
+            if (by_row) load_scale(r, true, scale);
+            uint4 dyr[VPT], fr[VPT], yr[VPT];
+            float2 big[VPT][H], s = f2(0.f);  // dh*w_pre
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads + t;
-                if (i >= nvec) break;
-                const uint4* at = reinterpret_cast<const uint4*>(from) + i;
-                const uint32_t step = g.tensor_bytes / 16;
-                if (a.gates) gr[j] = ld_after(static_cast<const uint4*>(a.gate) + gate_at + i);
-                dyr[j] = a.dy ? at[step] : make_uint4(0, 0, 0, 0);
-                fr[j] = at[2 * step];
+                const int i = j * g.threads;
+                if (i + t >= nvec) break;
+                if (a.dy) dyr[j] = from[step + i];
+                fr[j] = from[2 * step + i];
                 if (a.dh) {
-                    dhr[j] = at[0];
-                    yr[j] = at[3 * step];
+                    yr[j] = from[3 * step + i];
                     float2 dh[H], y[H], w[H];
-                    unpack2<T>(dhr[j], dh);
+                    unpack2<T>(from[i], dh);
                     unpack2<T>(yr[j], y);
-                    unpack2<T>(weights[i], w);
+                    unpack2<T>(weights[i + t], w);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) s = __ffma2_rn(__fmul2_rn(dh[h], w[h]), y[h], s);
+                    for (int h = 0; h < H; ++h) {
+                        big[j][h] = __fmul2_rn(dh[h], w[h]);
+                        s = __ffma2_rn(big[j][h], y[h], s);
+                        sum_pre[j][h] = __ffma2_rn(dh[h], __fmul2_rn(y[h], f2(r2)), sum_pre[j][h]);
+                    }
                 }
             }
             float c2 = 0.f;
@@ -487,64 +565,66 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             float2 back[VPT][H];
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads + t;
-                if (i >= nvec) break;
-                float2 d[H], f[H], gate[H], w[H];
-                unpack2<T>(dyr[j], d);
+                const int i = j * g.threads;
+                if (i + t >= nvec) break;
+                float2 d[H], f[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) d[h] = f2(0.f);
+                if (a.dy) unpack2<T>(dyr[j], d);
                 unpack2<T>(fr[j], f);
                 if (a.dh) {
-                    float2 dh[H], y[H];
-                    unpack2<T>(dhr[j], dh);
+                    float2 y[H];
                     unpack2<T>(yr[j], y);
-                    unpack2<T>(weights[i], w);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        d[h] = __fadd2_rn(d[h], __ffma2_rn(f2(r2), __fmul2_rn(dh[h], w[h]), __fmul2_rn(y[h], f2(-c2))));
-                        sum_pre[j][h] = __ffma2_rn(dh[h], __fmul2_rn(y[h], f2(r2)), sum_pre[j][h]);
-                    }
+                    for (int h = 0; h < H; ++h)
+                        d[h] = __ffma2_rn(y[h], f2(-c2), __ffma2_rn(f2(r2), big[j][h], d[h]));
                 }
-                st_v4(static_cast<uint4*>(a.dx) + r * nvec + i, pack2x<T>(d));
-                unpack2<T>(weights[nvec + i], w);
-                if (a.gates) unpack2<T>(gr[j], gate);
+                st_v4(static_cast<uint4*>(a.dx) + at + i, pack2x<T>(d));
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    const float2 ad = __fmul2_rn(d[h], f2(a.alpha)), dn = a.gates ? __fmul2_rn(ad, gate[h]) : ad;
-                    const float2 unit = a.post ? __fmul2_rn(f[h], f2(r1)) : f[h];
-                    const float2 n = a.post ? __fmul2_rn(unit, w[h]) : unit;
-                    if (by_row) gate[h] = __fmul2_rn(ad, n);
-                    else sum_gate[j][h] = __ffma2_rn(ad, n, sum_gate[j][h]);
-                    sum_post[j][h] = __ffma2_rn(dn, unit, sum_post[j][h]);
-                    back[j][h] = a.post ? __fmul2_rn(dn, w[h]) : dn;
+                    back[j][h] = __fmul2_rn(d[h], scale[j][h]);
                     s = __ffma2_rn(back[j][h], f[h], s);
+                    const float2 unit = __fmul2_rn(f[h], f2(r1));
+                    sum_unit[j][h] = by_row ? __fmul2_rn(d[h], unit) : __ffma2_rn(d[h], unit, sum_unit[j][h]);
                 }
-                if (by_row && a.dgate) st_v4(static_cast<uint4*>(a.dgate) + gate_at + i, pack2x<T>(gate));
+            }
+            if (by_row) {
+                close_gate(r);
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if (j * g.threads + t < nvec && a.dgate)
+                        st_v4(static_cast<uint4*>(a.dgate) + at + j * g.threads, pack2x<T>(sum_unit[j]));
             }
             float c1 = 0.f;
             if (a.post) c1 = r1 * r1 * r1 * (row_sum(s.x + s.y, 1) * inv);
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads + t;
-                if (i >= nvec) break;
+                const int i = j * g.threads;
+                if (i + t >= nvec) break;
                 if (a.post) {
                     float2 f[H];
                     unpack2<T>(fr[j], f);
 #pragma unroll
                     for (int h = 0; h < H; ++h) back[j][h] = __ffma2_rn(f2(r1), back[j][h], __fmul2_rn(f[h], f2(-c1)));
                 }
-                st_v4(static_cast<uint4*>(a.df) + r * nvec + i, pack2x<T>(back[j]));
+                st_v4(static_cast<uint4*>(a.df) + at + i, pack2x<T>(back[j]));
             }
             phase ^= 1;
-        } else if (consumer) {
+        } else {
             if (t == 0) mbar_arrive(&empty[slot]);  // no row of this slot is this group's
         }
         if (by_gate && (walk.r + walk.count == walk.gate_end || walk.r + walk.count == walk.end)) {
-            const int64_t row = row_div(walk.r, a.per_gate);
-            const bool begins = first == row * a.per_gate.d, ends = walk.r + walk.count == walk.gate_end;
-            flush(sum_gate, part_row(a, begins ? 3 : 2, blockIdx.x),
-                  begins && ends ? static_cast<uint4*>(a.dgate) + row * nvec : nullptr);
+            const bool begins = first == gate_row * a.per_gate.d, ends = walk.r + walk.count == walk.gate_end;
+            close_gate(gate_row);
+            if (a.dgate)
+                flush(sum_unit, part_row(a, begins ? 3 : 2, blockIdx.x),
+                      begins && ends ? static_cast<uint4*>(a.dgate) + gate_row * nvec : nullptr);
+            else clear(sum_unit);
             first = walk.r + walk.count;
+            ++gate_row;
         }
     }
+    if (!by_gate && !by_row) close_gate(gate_row);
     __syncthreads();
     if (a.dw_post) flush(sum_post, part_row(a, 0, blockIdx.x), nullptr);
     if (a.dw_pre) flush(sum_pre, part_row(a, 1, blockIdx.x), nullptr);
@@ -628,13 +708,16 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
 // launches
 // ---------------------------------------------------------------------------
 template <typename T, int VPT>
-nrm_status block_fwd_vec(BlockArgs& a, int warps, cudaStream_t s) {
-    void* p[] = {&a};
-    if (warps == 0)
-        return launch_pdl(reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, true>),
-                          dim3(unsigned((a.rows + kBlockRowWarps - 1) / kBlockRowWarps)), dim3(32 * kBlockRowWarps), p, s);
-    return launch_pdl(reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, false>), dim3(unsigned(a.rows)),
-                      dim3(unsigned(32 * warps)), p, s);
+nrm_status block_fwd_vec(BlockArgs& a, int warps, const DevInfo* dev, cudaStream_t s) {
+    const void* fn = warps == 0 ? reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, true>)
+                                : reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, false>);
+    const int block = warps == 0 ? 32 * kBlockRowWarps : 32 * warps, at_once = warps == 0 ? kBlockRowWarps : 1;
+    // rows to a CTA or warp: as many as leave the GPU two rounds of CTAs, at most 16
+    const int64_t resident = int64_t(dev->sms) * std::max(1, cached_occupancy(fn, block, 0)) * at_once;
+    int per = int(std::max<int64_t>(1, std::min<int64_t>(16, a.rows / (2 * resident))));
+    void* p[] = {&a, &per};
+    const int64_t each = int64_t(per) * at_once;
+    return launch_pdl(fn, dim3(unsigned((a.rows + each - 1) / each)), dim3(unsigned(block)), p, s);
 }
 
 template <typename T>
@@ -650,11 +733,11 @@ nrm_status block_norm_fwd(const BlockArgs& args, bool vec, cudaStream_t s) {
         // rows 4), and where there are no more rows than SMs, 1
         if (nvec <= 128 && a.rows > dev->sms) {
             const int v = (nvec + 31) / 32;
-            return v <= 1 ? block_fwd_vec<T, 1>(a, 0, s) : v == 2 ? block_fwd_vec<T, 2>(a, 0, s) : block_fwd_vec<T, 4>(a, 0, s);
+            return v <= 1 ? block_fwd_vec<T, 1>(a, 0, dev, s) : v == 2 ? block_fwd_vec<T, 2>(a, 0, dev, s) : block_fwd_vec<T, 4>(a, 0, dev, s);
         }
         const int v = a.rows <= dev->sms && nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
         const int warps = (nvec + 32 * v - 1) / (32 * v);
-        return v == 1 ? block_fwd_vec<T, 1>(a, warps, s) : v == 2 ? block_fwd_vec<T, 2>(a, warps, s) : block_fwd_vec<T, 4>(a, warps, s);
+        return v == 1 ? block_fwd_vec<T, 1>(a, warps, dev, s) : v == 2 ? block_fwd_vec<T, 2>(a, warps, dev, s) : block_fwd_vec<T, 4>(a, warps, dev, s);
     }
     void* p[] = {&a};
     return launch_pdl(reinterpret_cast<const void*>(&block_fwd_scalar_kernel<T>),
