@@ -183,35 +183,43 @@ __global__ void __launch_bounds__(kBlockThreads) block_cols_kernel(const BlockAr
 }
 
 // ---------------------------------------------------------------------------
-// whole 16-byte vectors, forward: a row in the registers of a warp, or of a CTA
+// whole 16-byte vectors, forward: a row in the registers of a CTA
 // ---------------------------------------------------------------------------
 // Every input is read once and every output written once; the stored stream is
-// kept as its rounded bits for the second norm.  A warp or a CTA takes `per`
-// neighbouring rows, so that its columns of the weights and the gate stay in
-// registers, and asks for the next row before it has done with one.  Bound by bytes.
-constexpr int kBlockRowWarps = 4;  // rows of a CTA where a warp takes one
-
-template <typename T, int VPT, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fwd_vec_kernel(const BlockArgs a, int per) {
+// kept as its rounded bits for the second norm.  A CTA takes `per` neighbouring
+// rows, one at a time, so that its columns of the weights and the gate stay in
+// registers, and asks for a row DEPTH rows before it is needed.  Bound by bytes.
+template <typename T, int VPT, int DEPTH>
+__global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) block_fwd_vec_kernel(const BlockArgs a, int per) {
     constexpr int VE = kVec<T>, H = VE / 2;
     __shared__ float sums[2][2][16];
     pdl_next();
-    const int threads = WARP_ROW ? 32 : int(blockDim.x), t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
-    int64_t r = (WARP_ROW ? int64_t(blockIdx.x) * kBlockRowWarps + (threadIdx.x >> 5) : int64_t(blockIdx.x)) * per;
-    const int64_t end = min(a.rows, r + per);
-    if (r >= end) return;
+    const int threads = int(blockDim.x), t = threadIdx.x, warps = threads >> 5;
+    const int64_t first = int64_t(blockIdx.x) * per, end = min(a.rows, first + per);
     const int nvec = a.cols / VE;
     const float inv = 1.f / float(a.cols);
     int phase = 0;
     auto row_sum = [&](float v, int which) {
         v = warp_sum(v);
-        if constexpr (WARP_ROW) return v;
-        if ((threadIdx.x & 31) == 0) sums[which][phase][threadIdx.x >> 5] = v;
+        if (warps == 1) return v;
+        if ((t & 31) == 0) sums[which][phase][t >> 5] = v;
         __syncthreads();
-        return warps_sum(sums[which][phase], int(blockDim.x >> 5));
+        return warps_sum(sums[which][phase], warps);
     };
     auto vec = [&](const void* p, int64_t i) { return ld_after(static_cast<const uint4*>(p) + i); };
     auto in_row = [&](int j) { return j * threads + t < nvec; };
+    uint4 fr[DEPTH][VPT], xr[DEPTH][VPT];
+    auto load_row = [&](int d, int64_t row) {
+        if (row >= end) return;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (in_row(j)) fr[d][j] = vec(a.f, row * nvec + j * threads + t);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (in_row(j)) xr[d][j] = vec(a.x, row * nvec + j * threads + t);
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load_row(d, first + d);
     // this thread's columns of alpha * gate * w_post and of w_pre
     float2 scale[VPT][H], w_pre[VPT][H];
     auto load_scale = [&](int64_t gate_row) {
@@ -233,17 +241,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fw
             }
         }
     };
-    uint4 fr[VPT], xr[VPT];
-    auto load_row = [&](int64_t row) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (in_row(j)) fr[j] = vec(a.f, row * nvec + j * threads + t);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (in_row(j)) xr[j] = vec(a.x, row * nvec + j * threads + t);
-    };
-    load_row(r);
-    int64_t gate_row = a.gates ? row_div(r, a.per_gate) : 0, gate_end = a.gates ? (gate_row + 1) * a.per_gate.d : end;
+    int64_t gate_row = a.gates ? row_div(first, a.per_gate) : 0, gate_end = a.gates ? (gate_row + 1) * a.per_gate.d : end;
     load_scale(gate_row);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -251,56 +249,62 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kBlockRowWarps : 512) block_fw
         for (int h = 0; h < H; ++h) w_pre[j][h] = f2(1.f);
         if (a.h && a.w_pre && in_row(j)) unpack2<T>(vec(a.w_pre, j * threads + t), w_pre[j]);
     }
-    for (; r < end; ++r) {
-        if (r == gate_end) {
-            gate_end += a.per_gate.d;
-            load_scale(++gate_row);
-        }
-        const int64_t at = r * nvec + t;
-        float r1 = 1.f;
-        if (a.post) {
+    for (int64_t r0 = first; r0 < end; r0 += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int64_t r = r0 + d;
+            if (r >= end) break;
+            if (r == gate_end) {
+                gate_end += a.per_gate.d;
+                load_scale(++gate_row);
+            }
+            const int64_t at = r * nvec + t;
+            float r1 = 1.f;
+            if (a.post) {
+                float2 s = f2(0.f);
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    if (!in_row(j)) break;
+                    float2 f[H];
+                    unpack2<T>(fr[d][j], f);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) s = __ffma2_rn(f[h], f[h], s);
+                }
+                r1 = rsqrtf(row_sum(s.x + s.y, 0) * inv + a.eps);
+                if (a.rstd_post && t == 0) a.rstd_post[r] = r1;
+            }
             float2 s = f2(0.f);
+            uint4 yr[VPT];
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (!in_row(j)) break;
-                float2 f[H];
-                unpack2<T>(fr[j], f);
+                float2 f[H], x[H];
+                unpack2<T>(fr[d][j], f);
+                unpack2<T>(xr[d][j], x);
 #pragma unroll
-                for (int h = 0; h < H; ++h) s = __ffma2_rn(f[h], f[h], s);
+                for (int h = 0; h < H; ++h) x[h] = __ffma2_rn(__fmul2_rn(f[h], f2(r1)), scale[j][h], x[h]);
+                yr[j] = pack2x<T>(x);
+                st_v4(static_cast<uint4*>(a.y) + at + j * threads, yr[j]);
+                if constexpr (sizeof(T) == 2) unpack2<T>(yr[j], x);
+#pragma unroll
+                for (int h = 0; h < H; ++h) s = __ffma2_rn(x[h], x[h], s);
             }
-            r1 = rsqrtf(row_sum(s.x + s.y, 0) * inv + a.eps);
-            if (a.rstd_post && t == 0) a.rstd_post[r] = r1;
+            load_row(d, r + DEPTH);
+            if (a.h) {
+                const float r2 = rsqrtf(row_sum(s.x + s.y, 1) * inv + a.eps);
+                if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    if (!in_row(j)) break;
+                    float2 y[H];
+                    unpack2<T>(yr[j], y);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) y[h] = __fmul2_rn(__fmul2_rn(y[h], f2(r2)), w_pre[j][h]);
+                    st_v4(static_cast<uint4*>(a.h) + at + j * threads, pack2x<T>(y));
+                }
+            }
+            phase ^= 1;
         }
-        float2 s = f2(0.f);
-        uint4 yr[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (!in_row(j)) break;
-            float2 f[H], x[H];
-            unpack2<T>(fr[j], f);
-            unpack2<T>(xr[j], x);
-#pragma unroll
-            for (int h = 0; h < H; ++h) x[h] = __ffma2_rn(__fmul2_rn(f[h], f2(r1)), scale[j][h], x[h]);
-            yr[j] = pack2x<T>(x);
-            st_v4(static_cast<uint4*>(a.y) + at + j * threads, yr[j]);
-            if constexpr (sizeof(T) == 2) unpack2<T>(yr[j], x);
-#pragma unroll
-            for (int h = 0; h < H; ++h) s = __ffma2_rn(x[h], x[h], s);
-        }
-        if (r + 1 < end) load_row(r + 1);
-        if (!a.h) continue;
-        const float r2 = rsqrtf(row_sum(s.x + s.y, 1) * inv + a.eps);
-        if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (!in_row(j)) break;
-            float2 y[H];
-            unpack2<T>(yr[j], y);
-#pragma unroll
-            for (int h = 0; h < H; ++h) y[h] = __fmul2_rn(__fmul2_rn(y[h], f2(r2)), w_pre[j][h]);
-            st_v4(static_cast<uint4*>(a.h) + at + j * threads, pack2x<T>(y));
-        }
-        phase ^= 1;
     }
 }
 
@@ -323,6 +327,7 @@ constexpr int kBlockBar = 1;                         // the groups' named barrie
 
 struct BlockRing {
     int groups, threads;     // groups of threads to a CTA; threads of a group, whole warps
+    int rows;                // of a slot: groups times the rows that a group takes at once
     int slots;
     uint32_t tensor_bytes;   // of a tensor's rows in a slot
     uint32_t slot_bytes;
@@ -341,19 +346,73 @@ struct BlockWalk {
         r += count;
         if (r >= end) return false;
         if (r == gate_end) gate_end += a.per_gate.d;
-        count = int(min(int64_t(g.groups), min(end, gate_end) - r));
+        count = int(min(int64_t(g.rows), min(end, gate_end) - r));
         return true;
     }
 };
 
-template <typename T, int VPT>
+// What thread 0 asks for, slot by slot: the next rows of up to four tensors.
+struct BlockAsk {
+    BlockWalk walk;
+    const void* from[4];
+    int asked = 0, slot = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ BlockAsk(const BlockArgs& a, bool by_gate, const void* t0, const void* t1, const void* t2, const void* t3)
+        : walk(a, by_gate), from{t0, t1, t2, t3} {}
+    // false: the slot's last rows were not done with in time
+    __device__ __forceinline__ bool next(const BlockArgs& a, const BlockRing& g, unsigned char* smem, uint64_t* full, uint64_t* empty,
+                                         int64_t row_bytes, uint64_t pol) {
+        if (!walk.next(a, g)) return true;
+        if (round > 0 && !mbar_wait_bounded(&empty[slot], (round - 1) & 1u, kBlockWaitNs)) {
+            walk.r = walk.end;  // no more copies
+            walk.count = 0;
+            return false;
+        }
+        const uint32_t bytes = uint32_t(walk.count * row_bytes);
+        unsigned char* to = smem + g.ring_at + size_t(slot) * g.slot_bytes;
+        mbar_arrive_expect_tx(&full[slot], bytes * ((from[0] != nullptr) + (from[1] != nullptr) + (from[2] != nullptr) + (from[3] != nullptr)));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (from[k])
+                bulk_g2s(to + k * g.tensor_bytes, static_cast<const unsigned char*>(from[k]) + walk.r * row_bytes, bytes, &full[slot],
+                         pol);
+        ++asked;
+        if (++slot == g.slots) {
+            slot = 0;
+            ++round;
+        }
+        return true;
+    }
+    // no copy may be under way when the CTA ends
+    __device__ __forceinline__ void settle(const BlockRing& g, uint64_t* full) const {
+        for (int i = 0; i < g.slots && i < asked; ++i)
+            (void)mbar_wait_bounded(&full[i], uint32_t((asked - 1 - i) / g.slots) & 1u, kBlockWaitNs);
+    }
+};
+
+// The sums of R numbers each over a group's threads.
+template <int R>
+__device__ __forceinline__ void group_sums(float (&v)[R], float* place, int group, int warps, int threads) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = warp_sum(v[k]);
+    if (warps == 1) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) place[k * 16 + warp] = v[k];
+    }
+    named_barrier(kBlockBar + group, threads);
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = warps_sum(place + k * 16 + group * warps, warps);
+}
+
+template <typename T, int VPT, int ROWS>
 __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(const BlockArgs a, const BlockRing g) {
     constexpr int VE = kVec<T>, H = VE / 2;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t full[kBlockSlots], empty[kBlockSlots];
-    __shared__ float sums[2][2][kBlockConsumers / 32];
+    __shared__ float sums[2][2][ROWS * 16];
     __shared__ int s_bad;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = int(threadIdx.x) / g.threads, t = int(threadIdx.x) - group * g.threads, warps = g.threads >> 5;
     const int nvec = a.cols / VE;
     if (threadIdx.x == 0) {
@@ -380,37 +439,9 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     const int64_t row_bytes = int64_t(a.cols) * int64_t(sizeof(T));
     const uint64_t pol = l2_evict_first();
     bool bad = false;
-    // thread 0 asks for the rows, slots ahead
-    BlockWalk ahead(a, by_gate);
-    int asked = 0, ask_slot = 0;
-    uint32_t ask_round = 0;
-    auto ask = [&]() {
-        if (!ahead.next(a, g)) return;
-        const int slot = ask_slot;
-        if (ask_round > 0 && !mbar_wait_bounded(&empty[slot], (ask_round - 1) & 1u, kBlockWaitNs)) {
-            bad = true;
-            ahead.r = ahead.end;  // no more copies
-            ahead.count = 0;
-            return;
-        }
-        if (++ask_slot == g.slots) {
-            ask_slot = 0;
-            ++ask_round;
-        }
-        const uint32_t bytes = uint32_t(ahead.count * row_bytes);
-        unsigned char* to = smem + g.ring_at + size_t(slot) * g.slot_bytes;
-        const void* from[4] = {a.dh, a.dy, a.f, a.dh ? a.y : nullptr};
-        const int tensors = (a.dh ? 2 : 0) + (a.dy ? 1 : 0) + 1;
-        mbar_arrive_expect_tx(&full[slot], bytes * tensors);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (from[k])
-                bulk_g2s(to + k * g.tensor_bytes, static_cast<const unsigned char*>(from[k]) + ahead.r * row_bytes, bytes,
-                         &full[slot], pol);
-        ++asked;
-    };
+    BlockAsk ask(a, by_gate, a.dh, a.dy, a.f, a.dh ? a.y : nullptr);
     if (threadIdx.x == 0)
-        for (int i = 0; i < g.slots; ++i) ask();
+        for (int i = 0; i < g.slots; ++i) ask.next(a, g, smem, full, empty, row_bytes, pol);
 
     // Over rows with one gate (and over all without), the sums of dgate and dw_post are this one's, times alpha*w_post
     // and alpha*gate: sum_unit = sum of dx*f*r1.
@@ -455,13 +486,6 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             for (int h = 0; h < H; ++h) sum_unit[j][h] = __fmul2_rn(sum_unit[j][h], by[j][h]);
     };
     int phase = 0;
-    auto row_sum = [&](float v, int which) {
-        v = warp_sum(v);
-        if (warps == 1) return v;
-        if (lane == 0) sums[which][phase][warp] = v;
-        named_barrier(kBlockBar + group, g.threads);
-        return warps_sum(&sums[which][phase][group * warps], warps);
-    };
     const float inv = 1.f / float(a.cols);
     auto clear = [&](float2 (&acc)[VPT][H]) {
 #pragma unroll
@@ -525,68 +549,84 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             ++round;
         }
         if (by_gate && walk.r == first && begun) load_scale(gate_row, true, scale);
-        if (group < walk.count) {
-            if (!bad && !mbar_wait_bounded(&full[slot], round & 1u, kBlockWaitNs)) bad = true;
+        const int mine = walk.count - group * ROWS;  // rows of this group, if not all
+        // (a group without one waits too: it must not be rounds ahead when it says that it is done with the slot)
+        if (!bad && !mbar_wait_bounded(&full[slot], round & 1u, kBlockWaitNs)) bad = true;
+        if (mine > 0) {
             const uint4* const from =
-                reinterpret_cast<const uint4*>(smem + g.ring_at + size_t(slot) * g.slot_bytes + group * row_bytes) + t;
+                reinterpret_cast<const uint4*>(smem + g.ring_at + size_t(slot) * g.slot_bytes + group * ROWS * row_bytes) + t;
             const uint32_t step = g.tensor_bytes / 16;
-            const int64_t r = walk.r + group, at = r * nvec + t;
-            const float r1 = a.post ? ld_after(a.rstd_post + r) : 1.f, r2 = a.dh ? ld_after(a.rstd_pre + r) : 0.f;
-            if (by_row) load_scale(r, true, scale);
-            uint4 dyr[VPT], fr[VPT], yr[VPT];
-            float2 big[VPT][H], s = f2(0.f);  // dh*w_pre
+            const int64_t r = walk.r + group * ROWS, at = r * nvec + t;
+            if (by_row) load_scale(r, true, scale);  // (one row at once)
+            uint4 dyr[ROWS][VPT], fr[ROWS][VPT], yr[ROWS][VPT];
+            float2 big[ROWS][VPT][H];  // dh*w_pre, then dx*scale
+            float r1[ROWS], r2[ROWS], s[ROWS];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads;
-                if (i + t >= nvec) break;
-                if (a.dy) dyr[j] = from[step + i];
-                fr[j] = from[2 * step + i];
-                if (a.dh) {
-                    yr[j] = from[3 * step + i];
-                    float2 dh[H], y[H], w[H];
-                    unpack2<T>(from[i], dh);
-                    unpack2<T>(yr[j], y);
-                    unpack2<T>(weights[i + t], w);
+            for (int k = 0; k < ROWS; ++k) {
+                // a row behind the last: statistics of 0, so that whatever its slot holds adds nothing
+                r1[k] = k >= mine ? 0.f : a.post ? ld_after(a.rstd_post + r + k) : 1.f;
+                r2[k] = k < mine && a.dh ? ld_after(a.rstd_pre + r + k) : 0.f;
+            }
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        big[j][h] = __fmul2_rn(dh[h], w[h]);
-                        s = __ffma2_rn(big[j][h], y[h], s);
-                        sum_pre[j][h] = __ffma2_rn(dh[h], __fmul2_rn(y[h], f2(r2)), sum_pre[j][h]);
+            for (int k = 0; k < ROWS; ++k) {
+                float2 sum = f2(0.f);
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    const int i = j * g.threads;
+                    if (i + t >= nvec || k >= mine) break;
+                    if (a.dy) dyr[k][j] = from[step + k * nvec + i];
+                    fr[k][j] = from[2 * step + k * nvec + i];
+                    if (a.dh) {
+                        yr[k][j] = from[3 * step + k * nvec + i];
+                        float2 dh[H], y[H], w[H];
+                        unpack2<T>(from[k * nvec + i], dh);
+                        unpack2<T>(yr[k][j], y);
+                        unpack2<T>(weights[i + t], w);
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            big[k][j][h] = __fmul2_rn(dh[h], w[h]);
+                            sum = __ffma2_rn(big[k][j][h], y[h], sum);
+                            sum_pre[j][h] = __ffma2_rn(dh[h], __fmul2_rn(y[h], f2(r2[k])), sum_pre[j][h]);
+                        }
                     }
                 }
+                s[k] = sum.x + sum.y;
             }
-            float c2 = 0.f;
-            if (a.dh) c2 = r2 * r2 * r2 * (row_sum(s.x + s.y, 0) * inv);
+            if (a.dh) group_sums<ROWS>(s, sums[0][phase], group, warps, g.threads);
             else if (warps > 1) named_barrier(kBlockBar + group, g.threads);
             else __syncwarp();
             if (t == 0) mbar_arrive(&empty[slot]);  // (every thread of the group has read its part)
-            if (threadIdx.x == 0 && begun) ask();
-            s = f2(0.f);
-            float2 back[VPT][H];
+            if (threadIdx.x == 0 && begun && !ask.next(a, g, smem, full, empty, row_bytes, pol)) bad = true;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads;
-                if (i + t >= nvec) break;
-                float2 d[H], f[H];
+            for (int k = 0; k < ROWS; ++k) {
+                const float c2 = r2[k] * r2[k] * r2[k] * (s[k] * inv);
+                float2 sum = f2(0.f);
 #pragma unroll
-                for (int h = 0; h < H; ++h) d[h] = f2(0.f);
-                if (a.dy) unpack2<T>(dyr[j], d);
-                unpack2<T>(fr[j], f);
-                if (a.dh) {
-                    float2 y[H];
-                    unpack2<T>(yr[j], y);
+                for (int j = 0; j < VPT; ++j) {
+                    const int i = j * g.threads;
+                    if (i + t >= nvec || k >= mine) break;
+                    float2 d[H], f[H];
 #pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        d[h] = __ffma2_rn(y[h], f2(-c2), __ffma2_rn(f2(r2), big[j][h], d[h]));
+                    for (int h = 0; h < H; ++h) d[h] = f2(0.f);
+                    if (a.dy) unpack2<T>(dyr[k][j], d);
+                    unpack2<T>(fr[k][j], f);
+                    if (a.dh) {
+                        float2 y[H];
+                        unpack2<T>(yr[k][j], y);
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            d[h] = __ffma2_rn(y[h], f2(-c2), __ffma2_rn(f2(r2[k]), big[k][j][h], d[h]));
+                    }
+                    st_v4(static_cast<uint4*>(a.dx) + at + k * nvec + i, pack2x<T>(d));
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        big[k][j][h] = __fmul2_rn(d[h], scale[j][h]);
+                        sum = __ffma2_rn(big[k][j][h], f[h], sum);
+                        const float2 unit = __fmul2_rn(f[h], f2(r1[k]));
+                        sum_unit[j][h] = by_row ? __fmul2_rn(d[h], unit) : __ffma2_rn(d[h], unit, sum_unit[j][h]);
+                    }
                 }
-                st_v4(static_cast<uint4*>(a.dx) + at + i, pack2x<T>(d));
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    back[j][h] = __fmul2_rn(d[h], scale[j][h]);
-                    s = __ffma2_rn(back[j][h], f[h], s);
-                    const float2 unit = __fmul2_rn(f[h], f2(r1));
-                    sum_unit[j][h] = by_row ? __fmul2_rn(d[h], unit) : __ffma2_rn(d[h], unit, sum_unit[j][h]);
-                }
+                s[k] = sum.x + sum.y;
             }
             if (by_row) {
                 close_gate(r);
@@ -595,19 +635,23 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                     if (j * g.threads + t < nvec && a.dgate)
                         st_v4(static_cast<uint4*>(a.dgate) + at + j * g.threads, pack2x<T>(sum_unit[j]));
             }
-            float c1 = 0.f;
-            if (a.post) c1 = r1 * r1 * r1 * (row_sum(s.x + s.y, 1) * inv);
+            if (a.post) group_sums<ROWS>(s, sums[1][phase], group, warps, g.threads);
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads;
-                if (i + t >= nvec) break;
-                if (a.post) {
-                    float2 f[H];
-                    unpack2<T>(fr[j], f);
+            for (int k = 0; k < ROWS; ++k) {
+                const float c1 = r1[k] * r1[k] * r1[k] * (s[k] * inv);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) back[j][h] = __ffma2_rn(f2(r1), back[j][h], __fmul2_rn(f[h], f2(-c1)));
+                for (int j = 0; j < VPT; ++j) {
+                    const int i = j * g.threads;
+                    if (i + t >= nvec || k >= mine) break;
+                    if (a.post) {
+                        float2 f[H];
+                        unpack2<T>(fr[k][j], f);
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+                            big[k][j][h] = __ffma2_rn(f2(r1[k]), big[k][j][h], __fmul2_rn(f[h], f2(-c1)));
+                    }
+                    st_v4(static_cast<uint4*>(a.df) + at + k * nvec + i, pack2x<T>(big[k][j]));
                 }
-                st_v4(static_cast<uint4*>(a.df) + at + i, pack2x<T>(back[j]));
             }
             phase ^= 1;
         } else {
@@ -632,9 +676,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     __syncthreads();
     if (threadIdx.x == 0 && s_bad) {
         atomicOr(a.err, kErrTimeoutStage);
-        // no copy may be under way when the CTA ends
-        for (int i = 0; i < g.slots && i < asked; ++i)
-            (void)mbar_wait_bounded(&full[i], uint32_t((asked - 1 - i) / g.slots) & 1u, kBlockWaitNs);
+        ask.settle(g, full);
     }
 }
 
@@ -707,17 +749,35 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-template <typename T, int VPT>
-nrm_status block_fwd_vec(BlockArgs& a, int warps, const DevInfo* dev, cudaStream_t s) {
-    const void* fn = warps == 0 ? reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, true>)
-                                : reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, false>);
-    const int block = warps == 0 ? 32 * kBlockRowWarps : 32 * warps, at_once = warps == 0 ? kBlockRowWarps : 1;
-    // rows to a CTA or warp: as many as leave the GPU two rounds of CTAs, at most 16
-    const int64_t resident = int64_t(dev->sms) * std::max(1, cached_occupancy(fn, block, 0)) * at_once;
+// The ring for `tensors` tensors, groups taking `rows` rows at once, behind `before` bytes; false: no room for two slots.
+inline bool block_ring(BlockArgs& a, BlockRing& g, const DevInfo* dev, int nvec, int vpt, int rows, int tensors, uint32_t before) {
+    g.threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
+    g.groups = std::min(kBlockConsumers / g.threads, 14);  // (named barriers)
+    g.rows = g.groups * rows;
+    g.tensor_bytes = uint32_t(g.rows) * uint32_t(nvec) * 16;
+    g.slot_bytes = uint32_t(tensors) * g.tensor_bytes;
+    g.ring_at = (before + 127) / 128 * 128;
+    g.slots = std::min((dev->max_smem_optin - 2048 - int(g.ring_at)) / int(g.slot_bytes), kBlockSlots);
+    return g.slots >= 2;
+}
+inline nrm_status block_ring_launch(const void* fn, BlockArgs& a, BlockRing& g, const DevInfo* dev, cudaStream_t s) {
+    a.chunks = std::min<int64_t>(dev->sms, (a.rows + g.rows - 1) / g.rows);
+    const size_t smem = g.ring_at + size_t(g.slots) * g.slot_bytes;
+    nrm_status st = prepare_kernel(fn, smem, false);
+    if (st != NRM_OK) return st;
+    void* p[] = {&a, &g};
+    return launch_pdl(fn, dim3(unsigned(a.chunks)), dim3(unsigned(g.groups * g.threads)), p, s, smem);
+}
+
+template <typename T, int VPT, int DEPTH>
+nrm_status block_fwd_vec(BlockArgs& a, const DevInfo* dev, cudaStream_t s) {
+    const void* fn = reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, DEPTH>);
+    const int nvec = a.cols / kVec<T>, block = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
+    // rows to a CTA: as many as leave the GPU two rounds of CTAs, at most 16
+    const int64_t resident = int64_t(dev->sms) * std::max(1, cached_occupancy(fn, block, 0));
     int per = int(std::max<int64_t>(1, std::min<int64_t>(16, a.rows / (2 * resident))));
     void* p[] = {&a, &per};
-    const int64_t each = int64_t(per) * at_once;
-    return launch_pdl(fn, dim3(unsigned((a.rows + each - 1) / each)), dim3(unsigned(block)), p, s);
+    return launch_pdl(fn, dim3(unsigned((a.rows + per - 1) / per)), dim3(unsigned(block)), p, s);
 }
 
 template <typename T>
@@ -729,29 +789,12 @@ nrm_status block_norm_fwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     if (a.rows == 0) return NRM_OK;
     const int nvec = a.cols / kVec<T>;
     if (vec && nvec <= 2048 && a.rows < (int64_t(1) << 31)) {
-        // a warp to a row of up to 4 vectors a lane, where rows are many; else as few warps as give a thread 2 (long
-        // rows 4), and where there are no more rows than SMs, 1
-        if (nvec <= 128 && a.rows > dev->sms) {
-            const int v = (nvec + 31) / 32;
-            return v <= 1 ? block_fwd_vec<T, 1>(a, 0, dev, s) : v == 2 ? block_fwd_vec<T, 2>(a, 0, dev, s) : block_fwd_vec<T, 4>(a, 0, dev, s);
-        }
-        const int v = a.rows <= dev->sms && nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-        const int warps = (nvec + 32 * v - 1) / (32 * v);
-        return v == 1 ? block_fwd_vec<T, 1>(a, warps, dev, s) : v == 2 ? block_fwd_vec<T, 2>(a, warps, dev, s) : block_fwd_vec<T, 4>(a, warps, dev, s);
+        if (nvec <= 512) return block_fwd_vec<T, 1, 3>(a, dev, s);
+        return nvec <= 1024 ? block_fwd_vec<T, 2, 2>(a, dev, s) : block_fwd_vec<T, 4, 1>(a, dev, s);
     }
     void* p[] = {&a};
     return launch_pdl(reinterpret_cast<const void*>(&block_fwd_scalar_kernel<T>),
                       dim3(unsigned(std::min<int64_t>(a.rows, int64_t(dev->sms) * 64))), dim3(kBlockThreads), p, s);
-}
-
-template <typename T, int VPT>
-nrm_status block_bwd_ring(BlockArgs& a, BlockRing& g, size_t smem, cudaStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, VPT>);
-    nrm_status st = prepare_kernel(fn, smem, false);
-    if (st != NRM_OK) return st;
-    void* p[] = {&a, &g};
-    const int threads = (g.groups * g.threads + 31) / 32 * 32;
-    return launch_pdl(fn, dim3(unsigned(a.chunks)), dim3(unsigned(threads)), p, s, smem);
 }
 
 template <typename T>
@@ -774,28 +817,29 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     nrm_status st;
     bool sums = a.dgate || a.dw_post || a.dw_pre;
     const int nvec = a.cols / kVec<T>;
-    BlockRing g{};
+    bool ringed = false;
     if (vec && nvec <= 2 * kBlockConsumers) {
+        BlockRing g{};
+        const bool by_row = a.gates > 0 && a.per_gate.d == 1;
         const int vpt = nvec > kBlockConsumers ? 2 : 1;
-        g.threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
-        g.groups = std::min(kBlockConsumers / g.threads, 14);  // (named barriers)
-        const uint32_t row = uint32_t(a.cols) * uint32_t(sizeof(T));
-        g.tensor_bytes = uint32_t(g.groups) * row;
-        g.slot_bytes = 4 * g.tensor_bytes;
         // the weights, and the place where the groups' sums are added
-        g.ring_at = (uint32_t(nvec) * 32 + (g.groups > 1 ? uint32_t(a.cols) * 4 : 0) + 127) / 128 * 128;
-        const int room = (dev->max_smem_optin - 1024 - int(g.ring_at)) / int(g.slot_bytes);
-        g.slots = std::min(room, kBlockSlots);
-        if (g.slots >= 2) {
-            a.chunks = std::min<int64_t>(dev->sms, (a.rows + g.groups - 1) / g.groups);
-            const size_t smem = g.ring_at + size_t(g.slots) * g.slot_bytes;
-            st = vpt == 1 ? block_bwd_ring<T, 1>(a, g, smem, s) : block_bwd_ring<T, 2>(a, g, smem, s);
-            // a gate for every row is done with
-            if (a.gates > 0 && a.per_gate.d == 1) a.dgate = nullptr;
+        const uint32_t before = uint32_t(nvec) * 32 + uint32_t(a.cols) * 4;
+        // two rows of a group at once, for their waits to overlap, where the registers allow
+        if (vpt == 1 && !by_row && block_ring(a, g, dev, nvec, 1, 2, 4, before)) {
+            ringed = true;
+            st = block_ring_launch(reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2>), a, g, dev, s);
+        } else if (block_ring(a, g, dev, nvec, vpt, 1, 4, before)) {
+            ringed = true;
+            st = block_ring_launch(vpt == 1 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1>)
+                                            : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1>),
+                                   a, g, dev, s);
+        }
+        if (ringed) {
+            if (by_row) a.dgate = nullptr;  // done with
             sums = a.dgate || a.dw_post || a.dw_pre;
         }
     }
-    if (g.slots < 2) {
+    if (!ringed) {
         st = launch_pdl(reinterpret_cast<const void*>(&block_bwd_scalar_kernel<T>),
                         dim3(unsigned(std::min<int64_t>(a.rows, int64_t(dev->sms) * 64))), dim3(kBlockThreads), p, s);
         if (st != NRM_OK || !sums) return st;
