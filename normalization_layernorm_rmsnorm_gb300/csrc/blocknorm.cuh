@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(kBlockThreads) block_cols_kernel(const BlockAr
 // kept as its rounded bits for the second norm.  A CTA takes `per` neighbouring
 // rows, one at a time, so that its columns of the weights and the gate stay in
 // registers, and asks for a row DEPTH rows before it is needed.  Bound by bytes.
-template <typename T, int VPT, int DEPTH>
-__global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) block_fwd_vec_kernel(const BlockArgs a, int per) {
+// FAST: both norms, and rows of whole vectors for every thread: nothing then parts the loops' instructions.
+template <typename T, int VPT, int DEPTH, int MOST, int CTAS, bool FAST>
+__global__ void __launch_bounds__(MOST, CTAS) block_fwd_vec_kernel(const BlockArgs a, int per) {
     constexpr int VE = kVec<T>, H = VE / 2;
     __shared__ float sums[2][2][16];
     pdl_next();
@@ -207,7 +208,8 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) block_fwd_vec_kernel(co
         return warps_sum(sums[which][phase], warps);
     };
     auto vec = [&](const void* p, int64_t i) { return ld_after(static_cast<const uint4*>(p) + i); };
-    auto in_row = [&](int j) { return j * threads + t < nvec; };
+    auto in_row = [&](int j) { return FAST || j * threads + t < nvec; };
+    const bool post = FAST || a.post, pre = FAST || a.h;
     uint4 fr[DEPTH][VPT], xr[DEPTH][VPT];
     auto load_row = [&](int d, int64_t row) {
         if (row >= end) return;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) block_fwd_vec_kernel(co
     for (int j = 0; j < VPT; ++j) {
 #pragma unroll
         for (int h = 0; h < H; ++h) w_pre[j][h] = f2(1.f);
-        if (a.h && a.w_pre && in_row(j)) unpack2<T>(vec(a.w_pre, j * threads + t), w_pre[j]);
+        if (pre && a.w_pre && in_row(j)) unpack2<T>(vec(a.w_pre, j * threads + t), w_pre[j]);
     }
     for (int64_t r0 = first; r0 < end; r0 += DEPTH) {
 #pragma unroll
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) block_fwd_vec_kernel(co
             }
             const int64_t at = r * nvec + t;
             float r1 = 1.f;
-            if (a.post) {
+            if (post) {
                 float2 s = f2(0.f);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) block_fwd_vec_kernel(co
                 for (int h = 0; h < H; ++h) s = __ffma2_rn(x[h], x[h], s);
             }
             load_row(d, r + DEPTH);
-            if (a.h) {
+            if (pre) {
                 const float r2 = rsqrtf(row_sum(s.x + s.y, 1) * inv + a.eps);
                 if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
 #pragma unroll
@@ -406,7 +408,8 @@ __device__ __forceinline__ void group_sums(float (&v)[R], float* place, int grou
     for (int k = 0; k < R; ++k) v[k] = warps_sum(place + k * 16 + group * warps, warps);
 }
 
-template <typename T, int VPT, int ROWS>
+// FAST: everything is there, with one gate for many rows or none, and rows of whole vectors for every thread.
+template <typename T, int VPT, int ROWS, bool FAST>
 __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(const BlockArgs a, const BlockRing g) {
     constexpr int VE = kVec<T>, H = VE / 2;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -434,7 +437,8 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     }
     __syncthreads();
 
-    const bool by_row = a.gates > 0 && a.per_gate.d == 1;  // a gate of its own for every row: its gradient is written as it is made
+    const bool has_dh = FAST || a.dh, has_dy = FAST || a.dy, post = FAST || a.post;
+    const bool by_row = !FAST && a.gates > 0 && a.per_gate.d == 1;  // a gate of its own for every row: its gradient is written as it is made
     const bool by_gate = a.gates > 0 && !by_row && (a.gates > 1 || a.dgate);
     const int64_t row_bytes = int64_t(a.cols) * int64_t(sizeof(T));
     const uint64_t pol = l2_evict_first();
@@ -553,6 +557,8 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
         // (a group without one waits too: it must not be rounds ahead when it says that it is done with the slot)
         if (!bad && !mbar_wait_bounded(&full[slot], round & 1u, kBlockWaitNs)) bad = true;
         if (mine > 0) {
+            auto rows = [&](auto full_rows) {
+            constexpr bool FULL = decltype(full_rows)::value;  // all ROWS of them
             const uint4* const from =
                 reinterpret_cast<const uint4*>(smem + g.ring_at + size_t(slot) * g.slot_bytes + group * ROWS * row_bytes) + t;
             const uint32_t step = g.tensor_bytes / 16;
@@ -564,8 +570,8 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
                 // a row behind the last: statistics of 0, so that whatever its slot holds adds nothing
-                r1[k] = k >= mine ? 0.f : a.post ? ld_after(a.rstd_post + r + k) : 1.f;
-                r2[k] = k < mine && a.dh ? ld_after(a.rstd_pre + r + k) : 0.f;
+                r1[k] = !(FULL || k < mine) ? 0.f : post ? ld_after(a.rstd_post + r + k) : 1.f;
+                r2[k] = k < mine && has_dh ? ld_after(a.rstd_pre + r + k) : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
@@ -573,10 +579,10 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     const int i = j * g.threads;
-                    if (i + t >= nvec || k >= mine) break;
-                    if (a.dy) dyr[k][j] = from[step + k * nvec + i];
+                    if ((!FAST && i + t >= nvec) || !(FULL || k < mine)) break;
+                    if (has_dy) dyr[k][j] = from[step + k * nvec + i];
                     fr[k][j] = from[2 * step + k * nvec + i];
-                    if (a.dh) {
+                    if (has_dh) {
                         yr[k][j] = from[3 * step + k * nvec + i];
                         float2 dh[H], y[H], w[H];
                         unpack2<T>(from[k * nvec + i], dh);
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 }
                 s[k] = sum.x + sum.y;
             }
-            if (a.dh) group_sums<ROWS>(s, sums[0][phase], group, warps, g.threads);
+            if (has_dh) group_sums<ROWS>(s, sums[0][phase], group, warps, g.threads);
             else if (warps > 1) named_barrier(kBlockBar + group, g.threads);
             else __syncwarp();
             if (t == 0) mbar_arrive(&empty[slot]);  // (every thread of the group has read its part)
@@ -604,13 +610,13 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     const int i = j * g.threads;
-                    if (i + t >= nvec || k >= mine) break;
+                    if ((!FAST && i + t >= nvec) || !(FULL || k < mine)) break;
                     float2 d[H], f[H];
 #pragma unroll
                     for (int h = 0; h < H; ++h) d[h] = f2(0.f);
-                    if (a.dy) unpack2<T>(dyr[k][j], d);
+                    if (has_dy) unpack2<T>(dyr[k][j], d);
                     unpack2<T>(fr[k][j], f);
-                    if (a.dh) {
+                    if (has_dh) {
                         float2 y[H];
                         unpack2<T>(yr[k][j], y);
 #pragma unroll
@@ -635,15 +641,15 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                     if (j * g.threads + t < nvec && a.dgate)
                         st_v4(static_cast<uint4*>(a.dgate) + at + j * g.threads, pack2x<T>(sum_unit[j]));
             }
-            if (a.post) group_sums<ROWS>(s, sums[1][phase], group, warps, g.threads);
+            if (post) group_sums<ROWS>(s, sums[1][phase], group, warps, g.threads);
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
                 const float c1 = r1[k] * r1[k] * r1[k] * (s[k] * inv);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     const int i = j * g.threads;
-                    if (i + t >= nvec || k >= mine) break;
-                    if (a.post) {
+                    if ((!FAST && i + t >= nvec) || !(FULL || k < mine)) break;
+                    if (post) {
                         float2 f[H];
                         unpack2<T>(fr[k][j], f);
 #pragma unroll
@@ -653,6 +659,9 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                     st_v4(static_cast<uint4*>(a.df) + at + k * nvec + i, pack2x<T>(big[k][j]));
                 }
             }
+            };
+            if (mine >= ROWS) rows(std::true_type{});
+            else rows(std::false_type{});
             phase ^= 1;
         } else {
             if (t == 0) mbar_arrive(&empty[slot]);  // no row of this slot is this group's
@@ -769,13 +778,16 @@ inline nrm_status block_ring_launch(const void* fn, BlockArgs& a, BlockRing& g, 
     return launch_pdl(fn, dim3(unsigned(a.chunks)), dim3(unsigned(g.groups * g.threads)), p, s, smem);
 }
 
-template <typename T, int VPT, int DEPTH>
+template <typename T, int VPT, int DEPTH, int MOST, int CTAS>
 nrm_status block_fwd_vec(BlockArgs& a, const DevInfo* dev, cudaStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, DEPTH>);
     const int nvec = a.cols / kVec<T>, block = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
-    // rows to a CTA: as many as leave the GPU two rounds of CTAs, at most 16
+    const void* fn = nvec == VPT * block && a.post && a.h
+                         ? reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, DEPTH, MOST, CTAS, true>)
+                         : reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, DEPTH, MOST, CTAS, false>);
+    // rows to a CTA: about 16, such that the CTAs come to whole waves (a wave of 3.4 costs as much as one of 4)
     const int64_t resident = int64_t(dev->sms) * std::max(1, cached_occupancy(fn, block, 0));
-    int per = int(std::max<int64_t>(1, std::min<int64_t>(16, a.rows / (2 * resident))));
+    const int64_t waves = (a.rows + 16 * resident - 1) / (16 * resident);
+    int per = int((a.rows + waves * resident - 1) / (waves * resident));
     void* p[] = {&a, &per};
     return launch_pdl(fn, dim3(unsigned((a.rows + per - 1) / per)), dim3(unsigned(block)), p, s);
 }
@@ -789,8 +801,19 @@ nrm_status block_norm_fwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     if (a.rows == 0) return NRM_OK;
     const int nvec = a.cols / kVec<T>;
     if (vec && nvec <= 2048 && a.rows < (int64_t(1) << 31)) {
-        if (nvec <= 512) return block_fwd_vec<T, 1, 3>(a, dev, s);
-        return nvec <= 1024 ? block_fwd_vec<T, 2, 2>(a, dev, s) : block_fwd_vec<T, 4, 1>(a, dev, s);
+        // few rows: all the threads that there are vectors for
+        if (nvec <= 512 && a.rows <= 2 * dev->sms) return block_fwd_vec<T, 1, 1, 512, 2>(a, dev, s);
+        // a warp to a row of up to 4 vectors a lane, without a barrier; longer rows 2 vectors a thread (what a row costs
+        // beside its vectors, 217 of 296 instructions of a warp with one, is then shared by two), the longest 4
+        switch ((nvec + 31) / 32) {
+        case 1: return block_fwd_vec<T, 1, 3, 32, 28>(a, dev, s);
+        case 2: return block_fwd_vec<T, 2, 3, 32, 16>(a, dev, s);
+        case 3: return block_fwd_vec<T, 3, 3, 32, 12>(a, dev, s);
+        case 4: return block_fwd_vec<T, 4, 2, 32, 12>(a, dev, s);
+        default: break;
+        }
+        if (nvec <= 512) return block_fwd_vec<T, 2, 3, 256, 2>(a, dev, s);
+        return nvec <= 1024 ? block_fwd_vec<T, 2, 2, 512, 1>(a, dev, s) : block_fwd_vec<T, 4, 1, 512, 1>(a, dev, s);
     }
     void* p[] = {&a};
     return launch_pdl(reinterpret_cast<const void*>(&block_fwd_scalar_kernel<T>),
@@ -827,11 +850,14 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
         // two rows of a group at once, for their waits to overlap, where the registers allow
         if (vpt == 1 && !by_row && block_ring(a, g, dev, nvec, 1, 2, 4, before)) {
             ringed = true;
-            st = block_ring_launch(reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2>), a, g, dev, s);
+            const bool fast = nvec == g.threads && a.dh && a.dy && a.post;
+            st = block_ring_launch(fast ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, true>)
+                                        : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false>),
+                                   a, g, dev, s);
         } else if (block_ring(a, g, dev, nvec, vpt, 1, 4, before)) {
             ringed = true;
-            st = block_ring_launch(vpt == 1 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1>)
-                                            : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1>),
+            st = block_ring_launch(vpt == 1 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false>)
+                                            : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false>),
                                    a, g, dev, s);
         }
         if (ringed) {
