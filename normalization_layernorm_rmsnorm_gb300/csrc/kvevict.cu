@@ -21,9 +21,10 @@ namespace {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictTurn = 4 * kEvictThreads;  // positions that its threads take at once
 constexpr int kEvictBins = 2048;
 constexpr int kEvictCluster = 8;         // CTAs of a cluster, at most
-constexpr int kEvictPart = 2048;         // positions that are worth a CTA more
+constexpr int kEvictPart = 8192;         // positions that are worth a CTA more
 constexpr int kEvictHeld = 45 * 1024;    // weights that a CTA's shared memory holds
 constexpr int kCopyThreads = 256;
 constexpr int kCopyAhead = 4;            // rows of a lane under way
@@ -65,8 +66,9 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t a) {
 }
 
 __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const EvictArgs a, int ctas, int held) {
-    extern __shared__ uint32_t keys[];  // [held]
-    __shared__ uint32_t counts[2][kEvictBins], sums[32], found[2], share[2];
+    extern __shared__ __align__(16) uint32_t keys[];  // [held]
+    __shared__ __align__(16) uint32_t counts[2][kEvictBins];
+    __shared__ uint32_t sums[32], found[2], share[2];
     pdl_next();
     const int64_t which = blockIdx.x / ctas, s = which / a.heads;
     const int part = int(blockIdx.x % ctas), head = int(which - s * a.heads);
@@ -78,35 +80,42 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
     if (head == 0 && part == 0 && threadIdx.x == 0) a.new_lengths[s] = n < a.keep ? n : a.keep;
     const float* weights = a.weights + s * a.weight_ts + head * a.weight_hs;
     int64_t* kept = a.kept + which * a.keep;
-    float* out = a.new_weights ? a.new_weights + s * a.new_ts + head * a.new_hs : nullptr;
     if (n <= a.keep) {
-        for (int64_t i = int64_t(part) * kEvictThreads + threadIdx.x; i < a.keep; i += int64_t(ctas) * kEvictThreads) {
+        for (int64_t i = int64_t(part) * kEvictThreads + threadIdx.x; i < a.keep; i += int64_t(ctas) * kEvictThreads)
             kept[i] = i < n ? i : -1;
-            if (out && i < n) out[i] = ld_after(weights + i);
-        }
         return;
     }
     auto cluster_sync = [&]() {
         if (ctas > 1) cluster_sync_all();
         else __syncthreads();
     };
-    // this CTA's positions, rounded to the warps' strides
-    const int64_t each = ((n + ctas - 1) / ctas + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
+    // this CTA's positions, whole turns of its threads
+    const int64_t each = ((n + ctas - 1) / ctas + kEvictTurn - 1) / kEvictTurn * kEvictTurn;
     const int64_t first = min(n, part * each), last = min(n, first + each), lo = a.first, hi = n - a.recent;
     const bool holds = last - first <= held;
     if (holds) {
         const int count = int(last - first);
-        for (int i = threadIdx.x; i < count; i += 4 * kEvictThreads) {
-            float w[4];
+        constexpr int AHEAD = 16;
+        for (int i = threadIdx.x; i < count; i += AHEAD * kEvictThreads) {
+            float w[AHEAD];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < AHEAD; ++k)
                 if (i + k * kEvictThreads < count) w[k] = ld_after(weights + first + i + k * kEvictThreads);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < AHEAD; ++k)
                 if (i + k * kEvictThreads < count) keys[i + k * kEvictThreads] = weight_key(w[k]);
         }
     }
-    auto key = [&](int64_t i) { return holds ? keys[i - first] : weight_key(ld_after(weights + i)); };
+    // four neighbouring positions, those below `last`
+    auto four = [&](int64_t i, uint32_t (&k)[4]) {
+        if (holds) {
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + (i - first));  // (what lies behind `last` is not used)
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[j] = i + j < last ? weight_key(ld_after(weights + i + j)) : 0;
+        }
+    };
     // the border among the positions between: of those with its key, the first `want` stay
     uint32_t want = uint32_t(a.keep - a.first - a.recent), border = 0;
     const bool any = want > 0;
@@ -118,23 +127,28 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         uint32_t* mine = counts[round & 1];
         for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads) mine[i] = 0;
         __syncthreads();
-        for (int64_t i = max(first, lo) + threadIdx.x; i < min(last, hi); i += kEvictThreads) {
-            const uint32_t k = key(i);
-            if (round == 0 || k >> (shift + bits) == border >> (shift + bits))
-                atomicAdd(&mine[k >> shift & ((1u << bits) - 1)], 1u);
+        const int64_t from = max(first, lo), to = min(last, hi);
+        for (int64_t i = first + 4 * int(threadIdx.x); i < to; i += kEvictTurn) {
+            uint32_t k[4];
+            four(i, k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j >= from && i + j < to && (round == 0 || k[j] >> (shift + bits) == border >> (shift + bits)))
+                    atomicAdd(&mine[k[j] >> shift & ((1u << bits) - 1)], 1u);
         }
         cluster_sync();
-        // thread t has the digits 4 t to 4 t + 3 from the largest down
-        uint32_t c[4], sum = 0, all;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int digit = kEvictBins - 1 - (int(threadIdx.x) * 4 + j);
-            c[j] = 0;
-            if (ctas == 1) c[j] = mine[digit];
-            else
-                for (int r = 0; r < ctas; ++r) c[j] += ld_dsmem_u32(dsmem_addr(&mine[digit], uint32_t(r)));
-            sum += c[j];
+        // thread t has the digits 4 t to 4 t + 3 from the largest down (16 bytes of each CTA's counts)
+        uint32_t c[4] = {}, all;
+        const uint32_t* digits = &mine[kEvictBins - 4 - int(threadIdx.x) * 4];
+#pragma unroll 8
+        for (int r = 0; r < ctas; ++r) {
+            const float4 v = ctas == 1 ? *reinterpret_cast<const float4*>(digits) : ld_dsmem_f4(dsmem_addr(digits, uint32_t(r)));
+            c[0] += __float_as_uint(v.w);
+            c[1] += __float_as_uint(v.z);
+            c[2] += __float_as_uint(v.y);
+            c[3] += __float_as_uint(v.x);
         }
+        const uint32_t sum = c[0] + c[1] + c[2] + c[3];
         static_assert(kEvictBins == 4 * kEvictThreads, "four digits to a thread");
         uint32_t before = cta_before(sum, sums, &all);
 #pragma unroll
@@ -150,18 +164,25 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         want = found[1];
         __syncthreads();
     }
-    // how many of this CTA's positions stay for sure, and how many lie on the border
-    auto stays = [&](int64_t i, bool& tie) {
-        const bool between = i >= lo && i < hi;
-        const uint32_t k = between && any ? key(i) : 0;
-        tie = between && any && k == border;
-        return !between || (any && k > border);
+    // of four positions, which stay for sure and which lie on the border: a bit each, and their counts
+    auto stay = [&](int64_t i, uint32_t& sure, uint32_t& tie) {
+        sure = tie = 0;
+        if (i >= last) return;
+        uint32_t k[4];
+        four(i, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i + j >= last) break;
+            const bool between = i + j >= lo && i + j < hi;
+            sure |= uint32_t(!between || (any && k[j] > border)) << j;
+            tie |= uint32_t(between && any && k[j] == border) << j;
+        }
     };
-    uint32_t above = 0, ties = 0;
-    for (int64_t i = first + threadIdx.x; i < last; i += kEvictThreads) {
-        bool tie;
-        above += stays(i, tie);
-        ties += tie;
+    uint32_t above = 0, ties = 0, sure, tie;
+    for (int64_t i = first + 4 * int(threadIdx.x); i < last; i += kEvictTurn) {
+        stay(i, sure, tie);
+        above += __popc(sure);
+        ties += __popc(tie);
     }
     uint32_t all_above, all_ties;
     cta_before(above, sums, &all_above);
@@ -177,20 +198,21 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         tied += ld_dsmem_u32(dsmem_addr(&share[1], uint32_t(r)));
     }
     taken += min(tied, want);  // of the ties before this CTA's, those that stay
-    // in order: each round takes the next positions, one to a thread
-    for (int64_t i0 = first; i0 < last; i0 += kEvictThreads) {
-        const int64_t i = i0 + threadIdx.x;
-        bool tie = false, sure = false;
-        if (i < last) sure = stays(i, tie);
-        // both counts in one sum: a round has at most 512 of each
+    // in order: each turn takes the next positions, four to a thread
+    for (int64_t i0 = first; i0 < last; i0 += kEvictTurn) {
+        const int64_t i = i0 + 4 * int(threadIdx.x);
+        stay(i, sure, tie);
+        // both counts in one sum: a turn has at most 2048 of each
         uint32_t all;
-        const uint32_t before = cta_before(uint32_t(sure) | uint32_t(tie) << 16, sums, &all);
-        const uint32_t tie_at = tied + (before >> 16);
-        if (sure || (tie && tie_at < want)) {
-            // the ties before it that stay, and those that are sure
-            const uint32_t at = taken + (before & 0xffffu) + (min(tie_at, want) - min(tied, want));
-            kept[at] = i;
-            if (out) out[at] = ld_after(weights + i);
+        const uint32_t before = cta_before(uint32_t(__popc(sure)) | uint32_t(__popc(tie)) << 16, sums, &all);
+        // the ties before it that stay, and those that are sure
+        uint32_t tie_at = tied + (before >> 16);
+        uint32_t at = taken + (before & 0xffffu) + (min(tie_at, want) - min(tied, want));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool ties_here = tie >> j & 1;
+            if ((sure >> j & 1) || (ties_here && tie_at < want)) kept[at++] = i + j;
+            tie_at += ties_here;
         }
         taken += (all & 0xffffu) + (min(tied + (all >> 16), want) - min(tied, want));
         tied += all >> 16;
@@ -203,83 +225,101 @@ struct CopyDiv {
     RowDiv heads, keep;
 };
 
-// VEC bytes at once: neighbouring lanes copy neighbouring vectors of a row of keys and of values.
+// VEC bytes at once.  A warp takes 32 rows: each lane finds the places of one (its position, then the pages, which the
+// next rows' are asked for ahead of) and copies its scales and its weight; then the lanes share the rows' codes,
+// neighbouring lanes neighbouring vectors, a few rows of each lane under way.
 template <int VEC>
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictArgs a, CopyDiv by, int row_bytes) {
+__global__ void __launch_bounds__(kCopyThreads, 3) evict_copy_kernel(const EvictArgs a, CopyDiv by, int row_bytes) {
     using R = std::conditional_t<VEC == 16, uint4, std::conditional_t<VEC == 8, uint2, uint8_t>>;
     pdl_next();
     const int lane = threadIdx.x & 31;
     const int vecs = row_bytes / VEC, scales = a.d / a.cache.group;
-    // lanes of a row: as many as it has vectors (a power of two, at most 32)
-    int lanes = 1;
-    while (lanes < vecs && lanes < 32) lanes *= 2;
-    const int at_once = 32 / lanes, mine = lane & (lanes - 1);
-    const int64_t rows = a.sequences * a.heads * a.keep, pages = a.cache.slots / a.cache.page.d;
-    const int64_t step = int64_t(gridDim.x) * (kCopyThreads / 32) * at_once;
-    int64_t r0 = (int64_t(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5)) * at_once + lane / lanes;
-    for (; r0 < rows; r0 += step * kCopyAhead) {
-        int64_t from_code[kCopyAhead], to_code[kCopyAhead], from_scale[kCopyAhead], to_scale[kCopyAhead];
-        int64_t j[kCopyAhead], s[kCopyAhead], i[kCopyAhead], from_page[kCopyAhead], to_page[kCopyAhead];
-        int head[kCopyAhead];
-#pragma unroll
-        for (int k = 0; k < kCopyAhead; ++k) {
-            const int64_t r = r0 + k * step;
-            j[k] = -1;
-            if (r >= rows) continue;
-            const int64_t in_seq = row_div(r, by.heads);
-            head[k] = int(r - in_seq * a.heads);
-            s[k] = row_div(in_seq, by.keep);
-            i[k] = in_seq - s[k] * a.keep;
-            j[k] = ld_after(a.kept + (s[k] * a.heads + head[k]) * a.keep + i[k]);
+    int lanes = 1, log = 0;  // of a row: as many as it has vectors (a power of two, at most 32)
+    while (lanes < vecs && lanes < 32) lanes *= 2, ++log;
+    const int mine = lane & (lanes - 1), row_of = lane >> log, at_once = 32 >> log;
+    const int64_t rows = a.sequences * a.heads * a.keep;
+    const uint64_t pages = uint64_t(a.cache.slots / a.cache.page.d);
+    const int64_t step = int64_t(gridDim.x) * kCopyThreads;
+    const CacheDev& c = a.cache;
+    int64_t s = 0, i = 0, j = -1, from_page = -1, to_page = -1;  // sequence, new position and old one (-1: none), pages
+    int head = 0;
+    float weight = 0.f;
+    auto position = [&](int64_t r) {
+        j = -1;
+        if (r >= rows) return;
+        const int64_t in_seq = row_div(r, by.heads);
+        head = int(r - in_seq * a.heads);
+        s = row_div(in_seq, by.keep);
+        i = in_seq - s * a.keep;
+        j = ld_after(a.kept + (s * a.heads + head) * a.keep + i);
+    };
+    auto look_up = [&]() {
+        if (j < 0) return;
+        from_page = ld_after(a.table + s * a.table_stride + row_div(j, c.page));
+        to_page = ld_after(a.new_table + s * a.new_stride + row_div(i, c.page));
+        if (a.new_weights) weight = ld_after(a.weights + s * a.weight_ts + head * a.weight_hs + j);
+    };
+    int64_t r = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x;
+    position(r);
+    look_up();
+    for (int64_t r0 = r - lane; r0 < rows; r0 += step) {
+        bool there = j >= 0;
+        if (there && a.new_weights) a.new_weights[s * a.new_ts + head * a.new_hs + i] = weight;
+        if (there && (uint64_t(from_page) >= pages || uint64_t(to_page) >= pages)) {
+            atomicOr(a.err, kErrCacheSlot);
+            there = false;
         }
-#pragma unroll
-        for (int k = 0; k < kCopyAhead; ++k) {
-            if (j[k] < 0) continue;
-            const int64_t from_entry = row_div(j[k], a.cache.page), to_entry = row_div(i[k], a.cache.page);
-            from_page[k] = ld_after(a.table + s[k] * a.table_stride + from_entry);
-            to_page[k] = ld_after(a.new_table + s[k] * a.new_stride + to_entry);
-            j[k] -= from_entry * a.cache.page.d;
-            i[k] -= to_entry * a.cache.page.d;
+        int64_t from = 0, to = 0, from_scale = 0, to_scale = 0;
+        if (there) {
+            const int64_t in_from = j - row_div(j, c.page) * c.page.d, in_to = i - row_div(i, c.page) * c.page.d;
+            from = from_page * c.page_stride + in_from * c.slot_stride + head * c.head_stride;
+            to = to_page * c.page_stride + in_to * c.slot_stride + head * c.head_stride;
+            from_scale = from_page * c.scale_page_stride + in_from * c.scale_slot_stride + head * c.scale_head_stride;
+            to_scale = to_page * c.scale_page_stride + in_to * c.scale_slot_stride + head * c.scale_head_stride;
         }
-#pragma unroll
-        for (int k = 0; k < kCopyAhead; ++k) {
-            if (j[k] < 0) continue;
-            if (from_page[k] < 0 || from_page[k] >= pages || to_page[k] < 0 || to_page[k] >= pages) {
-                atomicOr(a.err, kErrCacheSlot);
-                j[k] = -1;
-                continue;
+        const uint32_t all = __ballot_sync(0xffffffffu, there);
+        r += step;
+        position(r);
+        // this lane's row's scales: the first of both at once
+        if (there) {
+            const float k = ld_after(c.scales[0] + from_scale), v = ld_after(c.scales[1] + from_scale);
+            c.scales[0][to_scale] = k;
+            c.scales[1][to_scale] = v;
+            for (int g = 1; g < scales; ++g) {
+                const float k2 = ld_after(c.scales[0] + from_scale + g), v2 = ld_after(c.scales[1] + from_scale + g);
+                c.scales[0][to_scale + g] = k2;
+                c.scales[1][to_scale + g] = v2;
             }
-            const CacheDev& c = a.cache;
-            from_code[k] = from_page[k] * c.page_stride + j[k] * c.slot_stride + head[k] * c.head_stride;
-            to_code[k] = to_page[k] * c.page_stride + i[k] * c.slot_stride + head[k] * c.head_stride;
-            from_scale[k] = from_page[k] * c.scale_page_stride + j[k] * c.scale_slot_stride + head[k] * c.scale_head_stride;
-            to_scale[k] = to_page[k] * c.scale_page_stride + i[k] * c.scale_slot_stride + head[k] * c.scale_head_stride;
         }
-        for (int v = mine; v < vecs; v += lanes) {
+        for (int q0 = 0; q0 < lanes; q0 += kCopyAhead) {
             R x[kCopyAhead][2];
 #pragma unroll
             for (int k = 0; k < kCopyAhead; ++k) {
-                if (j[k] < 0) continue;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    x[k][t] = ld_after(reinterpret_cast<const R*>(a.cache.codes[t] + from_code[k]) + v);
+                const int row = (q0 + k) * at_once + row_of;
+                const int64_t at = __shfl_sync(0xffffffffu, from, row & 31);
+                if (q0 + k < lanes && (all >> row & 1) && mine < vecs) {
+                    x[k][0] = ld_after(reinterpret_cast<const R*>(c.codes[0] + at) + mine);
+                    x[k][1] = ld_after(reinterpret_cast<const R*>(c.codes[1] + at) + mine);
+                }
             }
 #pragma unroll
             for (int k = 0; k < kCopyAhead; ++k) {
-                if (j[k] < 0) continue;
+                const int row = (q0 + k) * at_once + row_of;
+                const int64_t at = __shfl_sync(0xffffffffu, to, row & 31);
+                const int64_t at_from = __shfl_sync(0xffffffffu, from, row & 31);
+                if (q0 + k < lanes && (all >> row & 1)) {
+                    if (mine < vecs) {
+                        reinterpret_cast<R*>(c.codes[0] + at)[mine] = x[k][0];
+                        reinterpret_cast<R*>(c.codes[1] + at)[mine] = x[k][1];
+                    }
+                    for (int v = mine + lanes; v < vecs; v += lanes)  // (rows of more than 32 vectors)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) reinterpret_cast<R*>(a.cache.codes[t] + to_code[k])[v] = x[k][t];
+                        for (int t = 0; t < 2; ++t)
+                            reinterpret_cast<R*>(c.codes[t] + at)[v] =
+                                ld_after(reinterpret_cast<const R*>(c.codes[t] + at_from) + v);
+                }
             }
-        }
-        for (int g = mine; g < 2 * scales; g += lanes) {
-            const int t = g >= scales, at = g - t * scales;
-            float x[kCopyAhead];
-#pragma unroll
-            for (int k = 0; k < kCopyAhead; ++k)
-                if (j[k] >= 0) x[k] = ld_after(a.cache.scales[t] + from_scale[k] + at);
-#pragma unroll
-            for (int k = 0; k < kCopyAhead; ++k)
-                if (j[k] >= 0) a.cache.scales[t][to_scale[k] + at] = x[k];
+            if (q0 == 0) look_up();
         }
     }
 }
@@ -290,7 +330,7 @@ nrm_status choose(EvictArgs& a, const DevInfo* dev, cudaStream_t s) {
     int ctas = 1;
     while (ctas < kEvictCluster && a.cap > int64_t(ctas) * kEvictPart && pairs * ctas * 2 <= 2 * int64_t(dev->sms)) ctas *= 2;
     if (pairs * ctas >= (int64_t(1) << 31)) return fail(NRM_ERR_UNSUPPORTED, "sequences*heads must be < 2^31");
-    const int64_t most = ((a.cap + ctas - 1) / ctas + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
+    const int64_t most = ((a.cap + ctas - 1) / ctas + kEvictTurn - 1) / kEvictTurn * kEvictTurn;
     int held = int(most <= kEvictHeld ? most : 0);
     const void* fn = reinterpret_cast<const void*>(&evict_choose_kernel);
     const size_t smem = size_t(held) * 4;
@@ -330,15 +370,12 @@ nrm_status kv_evict(const EvictArgs& args, cudaStream_t s) {
             reinterpret_cast<uintptr_t>(a.cache.codes[1]) % b == 0 && a.cache.page_stride % b == 0 &&
             a.cache.slot_stride % b == 0 && a.cache.head_stride % b == 0)
             vec = b;
-    int lanes = 1;
-    while (lanes < bytes / vec && lanes < 32) lanes *= 2;
-    const int64_t at_once = int64_t(kCopyThreads / lanes) * kCopyAhead;
-    const int64_t want = (rows + at_once - 1) / at_once;
+    const int64_t want = (rows + kCopyThreads - 1) / kCopyThreads;
     void* q[] = {&a, &by, &bytes};
     const void* fn = vec == 16  ? reinterpret_cast<const void*>(&evict_copy_kernel<16>)
                      : vec == 8 ? reinterpret_cast<const void*>(&evict_copy_kernel<8>)
                                 : reinterpret_cast<const void*>(&evict_copy_kernel<1>);
-    return launch_pdl(fn, dim3(unsigned(std::min<int64_t>(want, int64_t(dev->sms) * 64))), dim3(kCopyThreads), q, s);
+    return launch_pdl(fn, dim3(unsigned(std::min<int64_t>(want, int64_t(dev->sms) * 3))), dim3(kCopyThreads), q, s);
 }
 
 }  // namespace nrm
