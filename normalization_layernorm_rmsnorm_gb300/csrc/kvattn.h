@@ -49,6 +49,7 @@ struct AttnArgs {
     int snap;                 // pairs of at most so many tiles are not cut
     int q_vec, out_vec;       // queries and outputs are aligned to 16 bytes
     int scale_vec;            // a row's scales are whole aligned 16 bytes
+    int near;                 // rows of whole 16 bytes whose places are below 2^32 of them
     int64_t pages;
     unsigned int* err;
 };

@@ -160,6 +160,10 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
                     (cache->heads == 1 || cache->head_stride % b == 0))
                     vec = int(b);
         const int64_t es = int64_t(dsize(dt));
+        // (strides below 2^40 times counts whose extents were checked: no overflow)
+        const int64_t extent = (cache->pages - 1) * cache->page_stride + (cache->page_size - 1) * cache->slot_stride +
+                               (cache->heads - 1) * cache->head_stride;
+        a.near = vec == 16 && extent < (int64_t(1) << 36);
         auto whole = [&](const nrm_heads* v) {
             return aligned(v->data, 16) && (sequences == 1 || v->token_stride * es % 16 == 0) &&
                    (v->heads == 1 || v->head_stride * es % 16 == 0);

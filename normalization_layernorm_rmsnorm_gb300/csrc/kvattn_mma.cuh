@@ -34,6 +34,9 @@
 
 namespace nrm {
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
 // n bytes, and zeros for the rest.
 __device__ __forceinline__ void cp_async_8_or_0(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
@@ -96,21 +99,22 @@ __device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
 __device__ __forceinline__ uint32_t codes4(uint32_t v) { return v & 0x000f000fu; }
 __device__ __forceinline__ uint32_t codes4_next(uint32_t v) { return v & 0x00f000f0u; }
 
-// What a kernel is made for: the stored form, rows of UNITS units of 32 or 16 elements (every group is whole units;
-// EXACT: of no fewer), and eights of heads.  With the count known the products of a tile are one block of
+// What a kernel is made for: the stored form, rows of UNITS units of 128, 64, 32 or 16 elements (every group is whole
+// units; EXACT: of no fewer), and eights of heads.  With the count known the products of a tile are one block of
 // instructions, which the loops' ends would cut in pieces too short to fill the waits.
 template <int KIND_, int UNIT_, int UNITS_, int NT_, bool EXACT_ = true>
 struct AttnForm {
     static constexpr int KIND = KIND_, UNIT = UNIT_, UNITS = UNITS_, NT = NT_, DMAX = UNIT * UNITS;
     static constexpr bool EXACT = EXACT_;
-    static constexpr int STEPS = UNIT / 16, TILES = UNIT / 16;
-    static constexpr int KP = UNIT / 4, VP = UNIT / 8;  // elements of a lane's piece of a unit
+    // keys are read in units of 32 at most, of which a lane has KP elements; values in whole units, VP elements a lane
+    static constexpr int SUB = UNIT < 32 ? UNIT : 32, SUBS = UNIT / SUB, STEPS = SUB / 16, TILES = UNIT / 16;
+    static constexpr int KP = SUB / 4, VP = UNIT / 8;
     static constexpr int BITS = KIND == NRM_CACHE_INT4 ? 4 : 8;
     static constexpr int ROW = DMAX * BITS / 8;
     static constexpr int CHUNKS = ROW % 16 == 0 ? ROW / 16 : 0;  // 16-byte vectors of a row
     // rows in shared memory: an odd number of 32 bytes (a key's fragment of 8 bytes a lane, 4 rows at a time) or of 16
     // (else) apart, the fragments' reads meet no bank twice
-    static constexpr int K_UNIT = BITS == 8 && UNIT == 32 ? 32 : 16;
+    static constexpr int K_UNIT = BITS == 8 && SUB == 32 ? 32 : 16;
     static constexpr int K_PITCH = ((ROW + K_UNIT - 1) / K_UNIT | 1) * K_UNIT, V_PITCH = ((ROW + 15) / 16 | 1) * 16;
     static constexpr uint32_t V_AT = 32 * K_PITCH, S_AT = V_AT + 32 * V_PITCH;
     // the integers' codes are taken as they lie, plus BIAS, as fp16's smallest numbers: 2^-24 of the value
@@ -182,14 +186,22 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         constexpr int W = decltype(which)::value, PITCH = W ? F::V_PITCH : F::K_PITCH;
         const uint32_t to = ring + sm.codes + (W ? F::V_AT : 0);
         const uint8_t* codes = a.cache.codes[W];
-        if (F::EXACT && F::CHUNKS > 0 && a.vec == 16) {
-            // neighbouring lanes copy neighbouring vectors of a row
+        if (F::EXACT && F::CHUNKS > 0 && a.near) {
+            // places in 16 bytes; neighbouring lanes copy neighbouring vectors of a row
             constexpr int C = F::CHUNKS > 0 ? F::CHUNKS : 1;
+            auto from = [&](int r, int c) { return codes + uint64_t(in_ring<const uint32_t>(sm.places + r * 4)) * 16 + c * 16; };
+            if (m == 0xffffffffu) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
-                cp_async_16_or_0(to + r * PITCH + c * 16, codes + in_ring<const int64_t>(sm.places + r * 8) + c * 16,
-                                 int(m >> r << 4) & 16);
+                for (int i = 0; i < C; ++i) {
+                    const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
+                    cp_async_16(to + r * PITCH + c * 16, from(r, c));
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < C; ++i) {
+                    const int r = (i * 32 + lane) / C, c = (i * 32 + lane) % C;
+                    cp_async_16_or_0(to + r * PITCH + c * 16, from(r, c), int(m >> r << 4) & 16);
+                }
             }
         } else {
             const int chunks = a.row_bytes / a.vec, row_step = 32 / chunks, chunk_step = 32 - row_step * chunks;
@@ -219,7 +231,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             code = page * a.cache.page_stride + in_page * a.cache.slot_stride + p.head * a.cache.head_stride;
             scale = page * a.cache.scale_page_stride + in_page * a.cache.scale_slot_stride + p.head * a.cache.scale_head_stride;
         }
-        in_ring<int64_t>(sm.places + lane * 8) = code;
+        if (F::EXACT && F::CHUNKS > 0 && a.near) in_ring<uint32_t>(sm.places + lane * 4) = uint32_t(code >> 4);
+        else in_ring<int64_t>(sm.places + lane * 8) = code;
         __syncwarp();
         copy_rows(std::integral_constant<int, 0>{}, m);
         const uint32_t ks = ring + sm.scales + lane * groups * 4, vs = ks + 32 * groups * 4;
@@ -253,10 +266,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
     for (int nt = 0; nt < NT; ++nt) {
         const int h = nt * 8 + gid;
         const bits* row = static_cast<const bits*>(a.q.p) + p.s * a.q.ts + (p.q0 + h) * a.q.hs;
-        float x[F::UNITS][F::KP], off[F::UNITS], most = 0.f;
+        float x[F::DMAX / F::SUB][F::KP], off[F::UNITS], most = 0.f;
 #pragma unroll
-        for (int u = 0; u < F::UNITS; ++u) {
-            const int at = u * F::UNIT + tid * F::KP;
+        for (int u = 0; u < F::DMAX / F::SUB; ++u) {
+            const int at = u * F::SUB + tid * F::KP;
             const bool there = h < p.heads && (F::EXACT || u < units);
             if (there && a.q_vec) {
                 constexpr int B = F::KP * int(sizeof(T));  // 8, 16 or 32 bytes
@@ -310,8 +323,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 }
                 if constexpr (F::BIAS != 0) {
                     constexpr float of = -F::BIAS * 0x1p-24f;
-                    if (b == 0 && part == 0) off[u] = 0.f;
-                    off[u] = fmaf(F::BITS == 4 && b == 1 ? 16.f * of : of, r.x + r.y, off[u]);
+                    if (b == 0 && ks % (F::UNIT / 16) == 0) off[ks / (F::UNIT / 16)] = 0.f;
+                    off[ks / (F::UNIT / 16)] = fmaf(F::BITS == 4 && b == 1 ? 16.f * of : of, r.x + r.y, off[ks / (F::UNIT / 16)]);
                 }
             }
         }
@@ -393,49 +406,60 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             if (!F::EXACT && u >= units) break;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                uint32_t f[F::STEPS][4];
-                const uint32_t from = sm.codes + (16 * half + gid) * F::K_PITCH + tid * (F::KP * F::BITS / 8) + u * (F::UNIT * F::BITS / 8);
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t row = from + r * 8 * F::K_PITCH;
-                    if constexpr (F::BITS == 8 && F::STEPS == 2) {
-                        const uint2 w = in_ring<const uint2>(row);
-                        codes8<F::KIND>(w.x, f[0][r], f[0][2 + r]);
-                        codes8<F::KIND>(w.y, f[F::STEPS - 1][r], f[F::STEPS - 1][2 + r]);
-                    } else if constexpr (F::BITS == 8) {
-                        codes8<F::KIND>(lds<4>(row), f[0][r], f[0][2 + r]);
-                    } else if constexpr (F::STEPS == 2) {
-                        const uint32_t w = lds<4>(row) ^ 0x88888888u;  // elements (0, 4), (1, 5), (2, 6), (3, 7)
-                        f[0][r] = codes4(w);
-                        f[0][2 + r] = codes4_next(w);
-                        f[F::STEPS - 1][r] = codes4(w >> 8);
-                        f[F::STEPS - 1][2 + r] = codes4_next(w >> 8);
-                    } else {
-                        uint32_t w = lds<2>(row) ^ 0x8888u;  // elements (0, 2), (1, 3)
-                        w |= w << 8;
-                        f[0][r] = codes4(w);
-                        f[0][2 + r] = codes4_next(w);
-                    }
-                }
-                const uint32_t scales = sm.k_scales + (u * 32 + 16 * half + gid) * 4;
-                const float s0 = in_ring<const float>(scales), s1 = in_ring<const float>(scales + 32);
+                float c[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
                     if constexpr (F::BIAS != 0) {
                         const float2 less = in_ring<const float2>(sm.bias + ((u * NT + nt) * 8 + tid * 2) * 4);
-                        c[0] = c[2] = less.x;
-                        c[1] = c[3] = less.y;
+                        c[nt][0] = c[nt][2] = less.x;
+                        c[nt][1] = c[nt][3] = less.y;
+                    }
+                }
+#pragma unroll
+                for (int sub = 0; sub < F::SUBS; ++sub) {
+                    uint32_t f[F::STEPS][4];
+                    const uint32_t from = sm.codes + (16 * half + gid) * F::K_PITCH + tid * (F::KP * F::BITS / 8) +
+                                          (u * F::SUBS + sub) * (F::SUB * F::BITS / 8);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t row = from + r * 8 * F::K_PITCH;
+                        if constexpr (F::BITS == 8 && F::STEPS == 2) {
+                            const uint2 w = in_ring<const uint2>(row);
+                            codes8<F::KIND>(w.x, f[0][r], f[0][2 + r]);
+                            codes8<F::KIND>(w.y, f[F::STEPS - 1][r], f[F::STEPS - 1][2 + r]);
+                        } else if constexpr (F::BITS == 8) {
+                            codes8<F::KIND>(lds<4>(row), f[0][r], f[0][2 + r]);
+                        } else if constexpr (F::STEPS == 2) {
+                            const uint32_t w = lds<4>(row) ^ 0x88888888u;  // elements (0, 4), (1, 5), (2, 6), (3, 7)
+                            f[0][r] = codes4(w);
+                            f[0][2 + r] = codes4_next(w);
+                            f[F::STEPS - 1][r] = codes4(w >> 8);
+                            f[F::STEPS - 1][2 + r] = codes4_next(w >> 8);
+                        } else {
+                            uint32_t w = lds<2>(row) ^ 0x8888u;  // elements (0, 2), (1, 3)
+                            w |= w << 8;
+                            f[0][r] = codes4(w);
+                            f[0][2 + r] = codes4_next(w);
+                        }
                     }
 #pragma unroll
                     for (int st = 0; st < F::STEPS; ++st)
 #pragma unroll
-                        for (int t = 0; t < QT; ++t)
-                            mma16816(c, f[st], q[u * F::STEPS + st][nt][t][0], q[u * F::STEPS + st][nt][t][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int t = 0; t < QT; ++t) {
+                                const auto& qf = q[(u * F::SUBS + sub) * F::STEPS + st][nt][t];
+                                mma16816(c[nt], f[st], qf[0], qf[1]);
+                            }
+                }
+                const uint32_t scales = sm.k_scales + (u * 32 + 16 * half + gid) * 4;
+                const float s0 = in_ring<const float>(scales), s1 = in_ring<const float>(scales + 32);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        l[half][nt][i] = u == 0 ? c[i] * (i < 2 ? s0 : s1) : fmaf(c[i], i < 2 ? s0 : s1, l[half][nt][i]);
-                }
+                        l[half][nt][i] = u == 0 ? c[nt][i] * (i < 2 ? s0 : s1) : fmaf(c[nt][i], i < 2 ? s0 : s1, l[half][nt][i]);
             }
         }
         __syncwarp();
@@ -547,18 +571,38 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t row = from + r * 8 * F::V_PITCH;
-                    const uint32_t x = lds<F::VP * F::BITS / 8>(row), y = lds<F::VP * F::BITS / 8>(row + F::V_PITCH);
-                    if constexpr (F::BITS == 8) {
-                        codes8<F::KIND>(__byte_perm(x, y, 0x5140), f[0][2 * r], f[0][2 * r + 1]);
-                        if constexpr (F::TILES == 2)
-                            codes8<F::KIND>(__byte_perm(x, y, 0x7362), f[F::TILES - 1][2 * r], f[F::TILES - 1][2 * r + 1]);
+                    constexpr int B = F::VP * F::BITS / 8;  // bytes of the piece: 16 to 1
+                    uint32_t x[(B + 3) / 4], y[(B + 3) / 4];
+                    if constexpr (B == 16) {
+                        const uint4 v = in_ring<const uint4>(row), v2 = in_ring<const uint4>(row + F::V_PITCH);
+                        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                        y[0] = v2.x, y[1] = v2.y, y[2] = v2.z, y[3] = v2.w;
+                    } else if constexpr (B == 8) {
+                        const uint2 v = in_ring<const uint2>(row), v2 = in_ring<const uint2>(row + F::V_PITCH);
+                        x[0] = v.x, x[1] = v.y;
+                        y[0] = v2.x, y[1] = v2.y;
                     } else {
-                        const uint32_t v = __byte_perm(x, y, 0x5410) ^ (F::TILES == 2 ? 0x88888888u : 0x00880088u);
-                        f[0][2 * r] = codes4(v);
-                        f[0][2 * r + 1] = codes4_next(v);
-                        if constexpr (F::TILES == 2) {
-                            f[F::TILES - 1][2 * r] = codes4(v >> 8);
-                            f[F::TILES - 1][2 * r + 1] = codes4_next(v >> 8);
+                        x[0] = lds<B>(row);
+                        y[0] = lds<B>(row + F::V_PITCH);
+                    }
+                    if constexpr (F::BITS == 8) {
+#pragma unroll
+                        for (int w4 = 0; w4 < (B + 3) / 4; ++w4) {
+                            codes8<F::KIND>(__byte_perm(x[w4], y[w4], 0x5140), f[2 * w4][2 * r], f[2 * w4][2 * r + 1]);
+                            if constexpr (B >= 4)
+                                codes8<F::KIND>(__byte_perm(x[w4], y[w4], 0x7362), f[(2 * w4 + 1) % F::TILES][2 * r],
+                                                f[(2 * w4 + 1) % F::TILES][2 * r + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h2 = 0; h2 < (B + 1) / 2; ++h2) {  // two bytes of both rows: 4 elements
+                            const uint32_t v = __byte_perm(x[h2 / 2], y[h2 / 2], h2 % 2 ? 0x7632 : 0x5410) ^ (B == 1 ? 0x00880088u : 0x88888888u);
+                            f[(2 * h2) % F::TILES][2 * r] = codes4(v);
+                            f[(2 * h2) % F::TILES][2 * r + 1] = codes4_next(v);
+                            if constexpr (B > 1) {
+                                f[(2 * h2 + 1) % F::TILES][2 * r] = codes4(v >> 8);
+                                f[(2 * h2 + 1) % F::TILES][2 * r + 1] = codes4_next(v >> 8);
+                            }
                         }
                     }
                 }
@@ -613,24 +657,25 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                     v[2 * t] = acc[u][t][nt][i] * once * d0;
                     v[2 * t + 1] = acc[u][t][nt][2 + i] * next * d0;
                 }
-                if (!p.whole) {
-                    if constexpr (F::VP == 4) *reinterpret_cast<float4*>(part + at) = make_float4(v[0], v[1], v[F::VP - 2], v[F::VP - 1]);
-                    else *reinterpret_cast<float2*>(part + at) = make_float2(v[0], v[1]);
-                } else if (a.out_vec) {
-                    if constexpr (sizeof(T) == 4) {
-                        if constexpr (F::VP == 4)
-                            *reinterpret_cast<float4*>(row + at) = make_float4(v[0], v[1], v[F::VP - 2], v[F::VP - 1]);
-                        else *reinterpret_cast<float2*>(row + at) = make_float2(v[0], v[1]);
-                    } else {
-                        uint32_t w0 = pack2<T>(make_float2(v[0], v[1]));
-                        if constexpr (F::VP == 4)
-                            *reinterpret_cast<uint2*>(row + at) =
-                                make_uint2(w0, pack2<T>(make_float2(v[F::VP - 2], v[F::VP - 1])));
-                        else *reinterpret_cast<uint32_t*>(row + at) = w0;
-                    }
-                } else {
+                // in fours, or the last two
 #pragma unroll
-                    for (int k = 0; k < F::VP; ++k) row[at + k] = Io<T>::store(v[k]);
+                for (int k = 0; k < F::VP; k += 4) {
+                    constexpr bool FOUR = F::VP >= 4;
+                    const float v2 = FOUR ? v[(k + 2) % F::VP] : 0.f, v3 = FOUR ? v[(k + 3) % F::VP] : 0.f;
+                    if (!p.whole || (a.out_vec && sizeof(T) == 4)) {
+                        float* to = (p.whole ? reinterpret_cast<float*>(row) : part) + at + k;
+                        if constexpr (FOUR) *reinterpret_cast<float4*>(to) = make_float4(v[k], v[k + 1], v2, v3);
+                        else *reinterpret_cast<float2*>(to) = make_float2(v[k], v[k + 1]);
+                    } else if (a.out_vec) {
+                        if constexpr (sizeof(T) == 2) {
+                            const uint32_t w0 = pack2<T>(make_float2(v[k], v[k + 1]));
+                            if constexpr (FOUR) *reinterpret_cast<uint2*>(row + at + k) = make_uint2(w0, pack2<T>(make_float2(v2, v3)));
+                            else *reinterpret_cast<uint32_t*>(row + at + k) = w0;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = k; e < F::VP && e < k + 4; ++e) row[at + e] = Io<T>::store(v[e]);
+                    }
                 }
             }
             if (gid == 0) {
@@ -683,26 +728,36 @@ nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
 // One translation unit for each storage type and stored form.
 template <typename T, int KIND>
 nrm_status attn_mma(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
-    const bool wide = a.d % 32 == 0 && a.cache.group % 32 == 0;
     a.row_bytes = KIND == NRM_CACHE_INT4 ? a.d / 2 : a.d;
     const int nt = a.d <= 128 && a.shared > 8 ? 2 : 1;
     attn_chunks(a, 8 * nt);
     a.pages = a.cache.slots / a.cache.page.d;
-    // rows of the usual lengths have kernels of their own; of others, one for all
-    const int units = a.d / (wide ? 32 : 16);
-    switch (wide ? units : 100 + units) {
-    case 2: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 32, 2, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 32, 2, 1>>(a, dev, s);
-    case 3: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 32, 3, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 32, 3, 1>>(a, dev, s);
-    case 4: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 32, 4, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 32, 4, 1>>(a, dev, s);
-    case 5: return attn_mma_launch<T, AttnForm<KIND, 32, 5, 1>>(a, dev, s);
-    case 8: return attn_mma_launch<T, AttnForm<KIND, 32, 8, 1>>(a, dev, s);
-    case 104: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 16, 4, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 16, 4, 1>>(a, dev, s);
-    case 105: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 16, 5, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 16, 5, 1>>(a, dev, s);
-    case 106: return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, 16, 6, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, 16, 6, 1>>(a, dev, s);
-    case 110: return attn_mma_launch<T, AttnForm<KIND, 16, 10, 1>>(a, dev, s);
-    default: break;
-    }
+    // the usual rows and groups have kernels of their own: units as long as the groups allow
+    int unit = 16;
+    for (int u : {32, 64, 128})
+        if (a.d % u == 0 && a.cache.group % u == 0) unit = u;
+    if (unit == 64 && a.d % 64 == 0 && a.d / 64 != 1 && a.d / 64 != 2 && a.d / 64 != 4) unit = 32;
+#define NRM_ATTN_FORM(U, N) \
+    if (unit == U && a.d == U * N) return attn_mma_launch<T, AttnForm<KIND, U, N, 1>>(a, dev, s)
+#define NRM_ATTN_FORM2(U, N)                                                                        \
+    if (unit == U && a.d == U * N)                                                                  \
+    return nt == 2 ? attn_mma_launch<T, AttnForm<KIND, U, N, 2>>(a, dev, s) : attn_mma_launch<T, AttnForm<KIND, U, N, 1>>(a, dev, s)
+    NRM_ATTN_FORM2(128, 1);
+    NRM_ATTN_FORM2(64, 2);
+    NRM_ATTN_FORM2(32, 4);
+    NRM_ATTN_FORM2(64, 1);
     attn_chunks(a, 8);
+    NRM_ATTN_FORM(32, 2);
+    NRM_ATTN_FORM(16, 4);
+    NRM_ATTN_FORM(16, 5);
+    NRM_ATTN_FORM(32, 3);
+    NRM_ATTN_FORM(16, 6);
+    NRM_ATTN_FORM(32, 5);
+    NRM_ATTN_FORM(16, 10);
+    NRM_ATTN_FORM(128, 2);
+    NRM_ATTN_FORM(64, 4);
+#undef NRM_ATTN_FORM
+#undef NRM_ATTN_FORM2
     return attn_mma_launch<T, AttnForm<KIND, 16, 16, 1, false>>(a, dev, s);
 }
 
