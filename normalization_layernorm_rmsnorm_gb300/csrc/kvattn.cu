@@ -31,7 +31,8 @@ nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
         // a CTA for each head where there are too few pairs to fill the GPU
         const int pairs = a.sequences * a.hk * a.chunks;
         const bool few = pairs < dev->sms;
-        st = launch_pdl(reinterpret_cast<const void*>(&attn_join_kernel<T>),
+        st = launch_pdl(a.d <= 128 ? reinterpret_cast<const void*>(&attn_join_kernel<T, 1>)
+                                   : reinterpret_cast<const void*>(&attn_join_kernel<T, 2>),
                         dim3(unsigned(pairs), few ? unsigned(a.heads) : 1u), dim3(few ? 32 * kJoinWarps : 128), p, s);
         if (st != NRM_OK) return st;
     }

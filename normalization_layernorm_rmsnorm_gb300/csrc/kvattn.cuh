@@ -37,16 +37,19 @@ __device__ __forceinline__ float exp2_approx(float v) {
 // What a maximum is subtracted as: an empty one (all logits -infinity) as 0.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
-// The sequences' tiles, in shared memory.
+// The sequences' work, in shared memory, counted in tiles: a sequence's tiles and kAttnStart for its beginning (the
+// queries, the first copies' wait, the result), none for one without positions.
 struct AttnTable {
     int64_t n[kAttnSequences];        // positions
-    int pre[kAttnSequences + 1];      // tiles before each sequence
+    int pre[kAttnSequences + 1];      // work before each sequence
     int sums[32];
 };
-__device__ __forceinline__ int attn_tiles(const AttnArgs& a, int64_t n) {
+__device__ __forceinline__ int attn_work(const AttnArgs& a, int64_t n) {
     const int64_t seen = a.window > 0 && n > a.window ? a.window : n;
-    return int((seen + kAttnTile - 1) / kAttnTile);
+    return seen > 0 ? int((seen + kAttnTile - 1) / kAttnTile) + kAttnStart : 0;
 }
+// The tile that work `c` of a sequence (from its beginning) belongs to.
+__device__ __forceinline__ int attn_tile(int c) { return max(0, c - kAttnStart); }
 
 // All threads of the CTA; CTA 0 writes the tiles to the workspace, for the kernels that follow.
 __device__ __forceinline__ void attn_table(const AttnArgs& a, AttnTable& t) {
@@ -62,7 +65,7 @@ __device__ __forceinline__ void attn_table(const AttnArgs& a, AttnTable& t) {
                 n = n < 0 ? 0 : a.cap;
             }
             t.n[s] = n;
-            tiles = attn_tiles(a, n);
+            tiles = attn_work(a, n);
         }
         int run = tiles;
 #pragma unroll
@@ -87,7 +90,7 @@ __device__ __forceinline__ void attn_table(const AttnArgs& a, AttnTable& t) {
     }
 }
 
-// The shares of all sequences' tiles: the first `more` have one tile more.  Where there are more pairs than workers,
+// The shares of all sequences' work: the first `more` have one more.  Where there are more pairs than workers,
 // one share.
 struct AttnShares {
     int used, each, more;
@@ -98,13 +101,13 @@ struct AttnShares {
         more = total - each * used;
     }
     __device__ __forceinline__ int begin(int r) const { return r * each + min(r, more); }
-    // the share that holds tile t
+    // the share that holds work t
     __device__ __forceinline__ int owner(int t) const {
         const int longer = more * (each + 1);
         return t < longer ? t / (each + 1) : more + (t - longer) / each;
     }
 };
-// The sequence that tile t belongs to.
+// The sequence that work t belongs to.
 __device__ __forceinline__ int attn_sequence(const int* pre, int sequences, int t) {
     int lo = 0, hi = sequences - 1;  // the last s with pre[s] <= t
     while (lo < hi) {
@@ -144,20 +147,23 @@ __device__ __forceinline__ void attn_pieces(const AttnArgs& a, const AttnTable& 
     // (more pairs than workers: a worker takes several)
     for (int64_t w = int(blockIdx.x) * used_warps + warp; w < work; w += int64_t(gridDim.x) * used_warps) {
         const int r = int(w / pairs), pair = int(w - int64_t(r) * pairs);
-        // a share's end, moved to the beginning of the sequence that it would cut where that is short
-        auto edge = [&](int t, int& s) {
-            s = attn_sequence(table.pre, a.sequences, min(t, total - 1));
-            const int first = table.pre[s];
-            return t < total && table.pre[s + 1] - first <= a.snap ? first : t;
+        // a share's end: a tile of a sequence, moved to the first one of a sequence that is short
+        struct Edge {
+            int s, tile;
         };
-        int s, s_end;
-        int t = edge(shares.begin(r), s);
-        const int end = edge(shares.begin(r + 1), s_end);
+        auto edge = [&](int t) {
+            if (t >= total) return Edge{a.sequences, 0};
+            const int s = attn_sequence(table.pre, a.sequences, t), first = table.pre[s];
+            return Edge{s, table.pre[s + 1] - first <= a.snap + kAttnStart ? 0 : attn_tile(t - first)};
+        };
+        const Edge from = edge(shares.begin(r)), to = edge(shares.begin(r + 1));
         const int head = pair / a.chunks, chunk = pair - head * a.chunks;
-        while (t < end) {
-            while (table.pre[s + 1] <= t) ++s;  // (sequences without tiles are passed over)
-            const int first = table.pre[s], tiles = table.pre[s + 1] - first;
+        for (int s = from.s; s < a.sequences && s <= to.s; ++s) {
+            const int tiles = attn_tile(table.pre[s + 1] - table.pre[s]);
             AttnPiece p;
+            p.tile0 = s == from.s ? from.tile : 0;
+            p.tile1 = s == to.s ? to.tile : tiles;
+            if (p.tile0 >= p.tile1) continue;
             p.s = s;
             p.pair = pair;
             p.head = head;
@@ -165,12 +171,9 @@ __device__ __forceinline__ void attn_pieces(const AttnArgs& a, const AttnTable& 
             p.heads = min(a.heads, a.shared - chunk * a.heads);
             p.n = table.n[s];
             p.lo = a.window > 0 && p.n > a.window ? p.n - a.window : 0;
-            p.tile0 = t - first;
-            p.tile1 = min(tiles, p.tile0 + (end - t));
             p.whole = p.tile0 == 0 && p.tile1 == tiles;
             p.part = attn_part(a, r, pair, p.tile0 == 0);
             f(p);
-            t += p.tile1 - p.tile0;
         }
     }
 }
@@ -324,20 +327,20 @@ __global__ void __launch_bounds__(kAttnThreads) attn_scalar_kernel(const AttnArg
 // are few and so have many pieces, for each of its heads (blockIdx.y).  Its warps
 // share the heads, and the warps of a head its pieces.
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, int E>  // E: rows of up to E * 128
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnArgs a) {
     using bits = typename Io<T>::bits_t;
-    constexpr int E = kHeadMaxD / 128, AHEAD = 4;
-    __shared__ float4 joined[kJoinWarps][kHeadMaxD / 4];
-    __shared__ float sums[kJoinWarps];
+    constexpr int AHEAD = 8 / E;  // pieces of a warp under way
+    __shared__ float4 joined[kJoinWarps][E * 32];
+    __shared__ float sums[kJoinWarps], tops[kJoinWarps];
     const int warps = int(blockDim.x) >> 5;
     pdl_next();
     const int pairs = a.hk * a.chunks;
     const int s = int(blockIdx.x) / pairs, pair = int(blockIdx.x) - s * pairs;
-    const int before = ld_after(a.prefix + s), tiles = ld_after(a.prefix + s + 1) - before;
-    if (tiles <= a.snap) return;
+    const int before = ld_after(a.prefix + s), work = ld_after(a.prefix + s + 1) - before;
     const AttnShares shares(a, ld_after(a.prefix + a.sequences));
-    const int w0 = shares.owner(before), w1 = shares.owner(before + tiles - 1);
+    if (work <= a.snap + kAttnStart) return;
+    const int w0 = shares.owner(before + kAttnStart), w1 = shares.owner(before + work - 1);
     if (w0 == w1) return;  // written by that worker
     const int head = pair / a.chunks, chunk = pair - head * a.chunks;
     const int heads = min(a.heads, a.shared - chunk * a.heads), q0 = head * a.shared + chunk * a.heads;
@@ -348,61 +351,73 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const AttnAr
     for (int h0 = 0; h0 < mine; h0 += at_once) {
         const int h = gridDim.y > 1 ? int(blockIdx.y) : h0 + group;
         const bool there = group < at_once && h0 + group < mine && h < heads;
-        // the first worker's piece is the beginning of its last pair, the others' the end of their first
+        // the first worker's piece is the beginning of its last sequence, the others' the end of their first
         auto part = [&](int w) {
             return a.part + attn_part(a, w, pair, w == w0) + h * attn_part_row(a.d);
         };
-        float top = -INFINITY, sum = 0.f;
-        float4 acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (there) {
-            for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, ld_after(part(w) + a.d));
+            float top = -INFINITY, sum = 0.f;
+            float4 acc[E];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float base = finite_max(top);
+            for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int w = w0 + in_group; w <= w1; w += AHEAD * each) {
-                float f[AHEAD], l[AHEAD];
+                float m[AHEAD], l[AHEAD];
                 uint4 v[AHEAD][E];
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k) {
-                    const bool in = w + k * each <= w1;
-                    const float* from = part(in ? w + k * each : w);
-                    f[k] = in ? ld_after(from + a.d) : -INFINITY;
+                    m[k] = -INFINITY;
+                    l[k] = 0.f;
+                    if (w + k * each > w1) continue;
+                    const float* from = part(w + k * each);
+                    m[k] = ld_after(from + a.d);
                     l[k] = ld_after(from + a.d + 1);
 #pragma unroll
                     for (int e = 0; e < E; ++e)
                         if (lane * 4 + 128 * e < a.d) v[k][e] = ld_after(reinterpret_cast<const uint4*>(from) + lane + 32 * e);
                 }
+                float most = top;
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) most = fmaxf(most, m[k]);
+                const float base = finite_max(most), grow = exp2_approx(top - base);
+                top = most;
+                sum *= grow;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = make_float4(acc[e].x * grow, acc[e].y * grow, acc[e].z * grow, acc[e].w * grow);
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k) {
-                    if (w + k * each > w1) break;
-                    f[k] = exp2_approx(f[k] - base);
-                    sum = fmaf(l[k], f[k], sum);
+                    if (w + k * each > w1) continue;
+                    const float f = exp2_approx(m[k] - base);
+                    sum = fmaf(l[k], f, sum);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
                         if (lane * 4 + 128 * e >= a.d) break;
-                        acc[e].x = fmaf(__uint_as_float(v[k][e].x), f[k], acc[e].x);
-                        acc[e].y = fmaf(__uint_as_float(v[k][e].y), f[k], acc[e].y);
-                        acc[e].z = fmaf(__uint_as_float(v[k][e].z), f[k], acc[e].z);
-                        acc[e].w = fmaf(__uint_as_float(v[k][e].w), f[k], acc[e].w);
+                        acc[e].x = fmaf(__uint_as_float(v[k][e].x), f, acc[e].x);
+                        acc[e].y = fmaf(__uint_as_float(v[k][e].y), f, acc[e].y);
+                        acc[e].z = fmaf(__uint_as_float(v[k][e].z), f, acc[e].z);
+                        acc[e].w = fmaf(__uint_as_float(v[k][e].w), f, acc[e].w);
                     }
                 }
             }
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (lane * 4 + 128 * e < a.d) joined[warp][lane + 32 * e] = acc[e];
-            if (lane == 0) sums[warp] = sum;
+            if (lane == 0) {
+                sums[warp] = sum;
+                tops[warp] = top;
+            }
         }
         __syncthreads();
         if (there) {
-            float all = 0.f;
-            for (int k = 0; k < each; ++k) all += sums[group * each + k];
+            float top = -INFINITY, all = 0.f;
+            for (int k = 0; k < each; ++k) top = fmaxf(top, tops[group * each + k]);
+            const float base = finite_max(top);
+            for (int k = 0; k < each; ++k) all = fmaf(sums[group * each + k], exp2_approx(tops[group * each + k] - base), all);
             const float scale = all == 0.f ? 0.f : 1.f / all;
             bits* row = static_cast<bits*>(a.out.p) + s * a.out.ts + (q0 + h) * a.out.hs;
             for (int i = in_group * 32 + lane; i < a.d; i += each * 32) {
                 float v = 0.f;
-                for (int k = 0; k < each; ++k) v += reinterpret_cast<const float*>(joined[group * each + k])[i];
+                for (int k = 0; k < each; ++k)
+                    v = fmaf(reinterpret_cast<const float*>(joined[group * each + k])[i], exp2_approx(tops[group * each + k] - base), v);
                 row[i] = Io<T>::store(v * scale);
             }
             if (in_group == 0 && lane == 0) attn_write_lse(a, s, q0 + h, top, all);
@@ -431,9 +446,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_weights_kernel(const AttnAr
     int s = attn_sequence(pre, a.sequences, t / a.hk);
     while (t < end) {
         while (pre[s + 1] * a.hk <= t) ++s;
-        const int tiles = pre[s + 1] - pre[s], at = t - pre[s] * a.hk;
-        const int head = at / tiles;
-        const int tile0 = at - head * tiles, tile1 = min(tiles, tile0 + (end - t));
+        const int work = pre[s + 1] - pre[s], at = t - pre[s] * a.hk;
+        const int head = at / work, work0 = at - head * work, work1 = min(work, work0 + (end - t));
+        const int tile0 = attn_tile(work0), tile1 = attn_tile(work1);
         const int64_t n = max(int64_t(0), min(a.cap, ld_after(a.lengths + s)));
         const int64_t lo = a.window > 0 && n > a.window ? n - a.window : 0;
         const int64_t j1 = min(n, lo + int64_t(tile1) * kAttnTile);
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_weights_kernel(const AttnAr
             for (int k = 0; k < AHEAD; ++k)
                 if (j + 32 * k < j1) out[j + 32 * k] += sum[k];
         }
-        t += tile1 - tile0;
+        t += work1 - work0;
     }
 }
 

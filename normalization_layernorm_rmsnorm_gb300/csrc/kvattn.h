@@ -12,9 +12,10 @@ namespace nrm {
 // call with more is cut into launches.
 constexpr int kAttnSequences = 1024;
 constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
+constexpr int kAttnStart = 2;        // what a sequence costs a worker beside its tiles, in tiles
 constexpr int kAttnWarps = 16;       // warps of a CTA at most, each a worker of its own
 constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
-constexpr int64_t kAttnTiles = int64_t(1) << 31;  // of all pairs of a launch, fewer than this
+constexpr int64_t kAttnTiles = int64_t(1) << 31;  // the work of all pairs of a launch is below it
 
 // Pairs: a head of the cache with a chunk of the query heads that read it.
 struct AttnArgs {
@@ -69,7 +70,7 @@ inline int attn_most_tiles(const AttnArgs& a) {
 // would have taken 1, but nothing has to be joined.  (250 sequences of 60 positions: cut, the joining took as long as
 // the rest.)  Otherwise those of one tile, which cannot be cut.
 inline void attn_snap(AttnArgs& a) {
-    a.snap = 2 * int64_t(a.sequences) * a.hk * a.chunks >= a.workers ? 8 : 1;
+    a.snap = 4 * int64_t(a.sequences) * a.hk * a.chunks >= a.workers ? 8 : 1;
 }
 // Floats of one partial result: accumulator, maximum and sum of each head, in whole 16 bytes.
 __host__ __device__ inline int64_t attn_part_row(int d) { return (int64_t(d) + 2 + 3) / 4 * 4; }

@@ -117,7 +117,7 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
         NRM_TRY(check_stats({lse}, 4));
         if (sequences == 0) return NRM_OK;
         // the tiles of a launch are counted in 32 bits
-        const int64_t tiles = (a.cap / kAttnTile + 1) * attn_most_pairs(q->heads, cache->heads);
+        const int64_t tiles = (a.cap / kAttnTile + 1 + kAttnStart) * attn_most_pairs(q->heads, cache->heads);
         if (a.cap / kAttnTile >= kAttnTiles || tiles >= kAttnTiles)
             return fail(NRM_ERR_UNSUPPORTED, "positions*heads of a sequence must be < 2^36");
         const DevInfo* dev = dev_info();

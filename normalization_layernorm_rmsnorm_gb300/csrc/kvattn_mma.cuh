@@ -134,7 +134,7 @@ struct AttnSmem {
 constexpr uint32_t kAttnPlaces = 32 * 8;
 // Warps of a CTA, by the registers that a thread needs.
 template <typename T, typename F>
-constexpr int attn_warps = F::DMAX > 128 || F::NT > 1 ? 8 : sizeof(T) == 4 ? 12 : 16;
+constexpr int attn_warps = F::DMAX > 128 || F::NT > 1 ? 8 : sizeof(T) == 4 ? 12 : 12;
 template <typename T>
 constexpr int kAttnFactors = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;  // of p
 template <typename T, typename F>
