@@ -12,7 +12,7 @@ namespace nrm {
 // call with more is cut into launches.
 constexpr int kAttnSequences = 1024;
 constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
-constexpr int kAttnStart = 2;        // what a sequence costs a worker beside its tiles, in tiles
+constexpr int kAttnStart = 5;        // what a sequence costs a worker beside its tiles, in tiles
 constexpr int kAttnWarps = 16;       // warps of a CTA at most, each a worker of its own
 constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
 constexpr int64_t kAttnTiles = int64_t(1) << 31;  // the work of all pairs of a launch is below it
