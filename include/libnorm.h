@@ -672,7 +672,7 @@ NRM_API size_t nrm_kv_attention_workspace_bytes(int64_t sequences, int64_t heads
  * the positions that stay, capacity >= keep; what lies behind the last is left
  * as it was; may be NULL; not the memory of weights.
  * 1 <= keep < 2^31; 0 <= first, recent; first + recent <= keep; sequences of
- * fewer than 2^32 positions.
+ * at most 2^30 positions (the smaller of width*page_size and weights->capacity).
  */
 NRM_API nrm_status nrm_kv_cache_evict(const nrm_kv_cache *cache, const nrm_kv_pages *pages,
                               const nrm_kv_weights *weights, const int64_t *new_table,

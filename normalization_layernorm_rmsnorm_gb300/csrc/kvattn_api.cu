@@ -205,7 +205,7 @@ nrm_status nrm_kv_cache_evict(const nrm_kv_cache* cache, const nrm_kv_pages* pag
         NRM_TRY(check_weights("weights", weights, sequences, cache->heads));
         if (keep < 1 || first < 0 || recent < 0 || first > keep || recent > keep - first)
             return fail(NRM_ERR_INVALID_ARG, "keep must be >= 1, first and recent >= 0, and first + recent <= keep");
-        if (a.cap >= (int64_t(1) << 32)) return fail(NRM_ERR_UNSUPPORTED, "a sequence must have fewer than 2^32 positions");
+        if (a.cap > (int64_t(1) << 30)) return fail(NRM_ERR_UNSUPPORTED, "a sequence must have at most 2^30 positions");
         if (keep >= (int64_t(1) << 31)) return fail(NRM_ERR_UNSUPPORTED, "keep must be < 2^31");
         NRM_TRY(check_pages("new_table", new_table, new_width, new_stride, sequences, cache->page_size));
         if (sequences > 0 && new_width * cache->page_size < keep)

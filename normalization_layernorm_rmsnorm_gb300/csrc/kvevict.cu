@@ -89,32 +89,36 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         if (ctas > 1) cluster_sync_all();
         else __syncthreads();
     };
-    // this CTA's positions, whole turns of its threads
-    const int64_t each = ((n + ctas - 1) / ctas + kEvictTurn - 1) / kEvictTurn * kEvictTurn;
-    const int64_t first = min(n, part * each), last = min(n, first + each), lo = a.first, hi = n - a.recent;
-    const bool holds = last - first <= held;
+    // this CTA's positions, whole turns of its threads, and of them those between, [from, to)
+    const int each = (int(n) + ctas - 1) / ctas / kEvictTurn * kEvictTurn + kEvictTurn;
+    const int first = min(int(n), part * each), count = min(int(n) - first, each);
+    const int from = min(count, max(0, int(a.first) - first)), to = min(count, max(0, int(n - a.recent) - first));
+    const bool holds = count <= held;
+    weights += first;
     if (holds) {
-        const int count = int(last - first);
         constexpr int AHEAD = 16;
         for (int i = threadIdx.x; i < count; i += AHEAD * kEvictThreads) {
             float w[AHEAD];
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
-                if (i + k * kEvictThreads < count) w[k] = ld_after(weights + first + i + k * kEvictThreads);
+                if (i + k * kEvictThreads < count) w[k] = ld_after(weights + i + k * kEvictThreads);
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k)
                 if (i + k * kEvictThreads < count) keys[i + k * kEvictThreads] = weight_key(w[k]);
         }
     }
-    // four neighbouring positions, those below `last`
-    auto four = [&](int64_t i, uint32_t (&k)[4]) {
+    // four neighbouring positions, and which of them lie between (a bit each)
+    auto four = [&](int i, uint32_t (&k)[4]) -> uint32_t {
         if (holds) {
-            const uint4 v = *reinterpret_cast<const uint4*>(keys + (i - first));  // (what lies behind `last` is not used)
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + i);  // (what lies behind the last is not used)
             k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) k[j] = i + j < last ? weight_key(ld_after(weights + i + j)) : 0;
+            for (int j = 0; j < 4; ++j) k[j] = i + j < count ? weight_key(ld_after(weights + i + j)) : 0;
         }
+        if (i >= from && i + 4 <= to) return 15u;
+        const int lo = min(4, max(0, from - i)), hi = min(4, max(0, to - i));
+        return ((1u << hi) - 1) & ~((1u << lo) - 1);
     };
     // the border among the positions between: of those with its key, the first `want` stay
     uint32_t want = uint32_t(a.keep - a.first - a.recent), border = 0;
@@ -127,13 +131,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         uint32_t* mine = counts[round & 1];
         for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads) mine[i] = 0;
         __syncthreads();
-        const int64_t from = max(first, lo), to = min(last, hi);
-        for (int64_t i = first + 4 * int(threadIdx.x); i < to; i += kEvictTurn) {
+        for (int i = 4 * int(threadIdx.x); i < to; i += kEvictTurn) {
             uint32_t k[4];
-            four(i, k);
+            const uint32_t between = four(i, k);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (i + j >= from && i + j < to && (round == 0 || k[j] >> (shift + bits) == border >> (shift + bits)))
+                if ((between >> j & 1) && (round == 0 || k[j] >> (shift + bits) == border >> (shift + bits)))
                     atomicAdd(&mine[k[j] >> shift & ((1u << bits) - 1)], 1u);
         }
         cluster_sync();
@@ -164,22 +167,24 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         want = found[1];
         __syncthreads();
     }
-    // of four positions, which stay for sure and which lie on the border: a bit each, and their counts
-    auto stay = [&](int64_t i, uint32_t& sure, uint32_t& tie) {
+    // of four positions, which stay for sure and which lie on the border: a bit each
+    auto stay = [&](int i, uint32_t& sure, uint32_t& tie) {
         sure = tie = 0;
-        if (i >= last) return;
+        if (i >= count) return;
         uint32_t k[4];
-        four(i, k);
+        const uint32_t between = four(i, k), there = i + 4 <= count ? 15u : (1u << (count - i)) - 1;
+        if (any) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (i + j >= last) break;
-            const bool between = i + j >= lo && i + j < hi;
-            sure |= uint32_t(!between || (any && k[j] > border)) << j;
-            tie |= uint32_t(between && any && k[j] == border) << j;
+            for (int j = 0; j < 4; ++j) {
+                sure |= uint32_t(k[j] > border) << j;
+                tie |= uint32_t(k[j] == border) << j;
+            }
         }
+        sure = (sure & between) | (there & ~between);
+        tie &= between;
     };
     uint32_t above = 0, ties = 0, sure, tie;
-    for (int64_t i = first + 4 * int(threadIdx.x); i < last; i += kEvictTurn) {
+    for (int i = 4 * int(threadIdx.x); i < count; i += kEvictTurn) {
         stay(i, sure, tie);
         above += __popc(sure);
         ties += __popc(tie);
@@ -199,8 +204,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
     }
     taken += min(tied, want);  // of the ties before this CTA's, those that stay
     // in order: each turn takes the next positions, four to a thread
-    for (int64_t i0 = first; i0 < last; i0 += kEvictTurn) {
-        const int64_t i = i0 + 4 * int(threadIdx.x);
+    for (int i0 = 0; i0 < count; i0 += kEvictTurn) {
+        const int i = i0 + 4 * int(threadIdx.x);
         stay(i, sure, tie);
         // both counts in one sum: a turn has at most 2048 of each
         uint32_t all;
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool ties_here = tie >> j & 1;
-            if ((sure >> j & 1) || (ties_here && tie_at < want)) kept[at++] = i + j;
+            if ((sure >> j & 1) || (ties_here && tie_at < want)) kept[at++] = first + i + j;
             tie_at += ties_here;
         }
         taken += (all & 0xffffu) + (min(tied + (all >> 16), want) - min(tied, want));
@@ -330,7 +335,7 @@ nrm_status choose(EvictArgs& a, const DevInfo* dev, cudaStream_t s) {
     int ctas = 1;
     while (ctas < kEvictCluster && a.cap > int64_t(ctas) * kEvictPart && pairs * ctas * 2 <= 2 * int64_t(dev->sms)) ctas *= 2;
     if (pairs * ctas >= (int64_t(1) << 31)) return fail(NRM_ERR_UNSUPPORTED, "sequences*heads must be < 2^31");
-    const int64_t most = ((a.cap + ctas - 1) / ctas + kEvictTurn - 1) / kEvictTurn * kEvictTurn;
+    const int64_t most = (a.cap + ctas - 1) / ctas / kEvictTurn * kEvictTurn + kEvictTurn;
     int held = int(most <= kEvictHeld ? most : 0);
     const void* fn = reinterpret_cast<const void*>(&evict_choose_kernel);
     const size_t smem = size_t(held) * 4;
