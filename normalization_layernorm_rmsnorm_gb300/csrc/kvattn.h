@@ -8,12 +8,14 @@
 
 namespace nrm {
 
-// Sequences of one launch: their tile counts lie in a CTA's shared memory.  A
-// call with more is cut into launches.
+// Sequences of one launch: their work lies in a CTA's shared memory.  A call with
+// more is cut into launches.
 constexpr int kAttnSequences = 1024;
 constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
-constexpr int kAttnStart = 5;        // what a sequence costs a worker beside its tiles, in tiles
-constexpr int kAttnWarps = 16;       // warps of a CTA at most, each a worker of its own
+// What a sequence costs a worker beside its tiles, in tiles: its queries, the first copies' wait, its result.  (64
+// sequences of 1 to 2048 positions: without it 56 us, with 2 tiles 53, 4 to 7 48.)
+constexpr int kAttnStart = 5;
+constexpr int kAttnWarps = 12;       // warps of a CTA at most, each a worker of its own
 constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
 constexpr int64_t kAttnTiles = int64_t(1) << 31;  // the work of all pairs of a launch is below it
 
@@ -38,9 +40,9 @@ struct AttnArgs {
     float* weights;           // (nullable)
     int64_t weight_ts, weight_hs;
     // workspace
-    int* prefix;              // [sequences + 1] tiles before each sequence
+    int* prefix;              // [sequences + 1] work before each sequence
     float* lse2;              // [sequences, hq], base 2
-    float* part;              // [workers][2] partial results
+    float* part;              // [shares][pairs][2] partial results
     float* logits;            // [sequences, pairs, logit_stride, logit_heads], base 2 (with weights)
     int64_t logit_stride;
     int workers;
@@ -66,9 +68,9 @@ inline int attn_most_tiles(const AttnArgs& a) {
     const int64_t seen = a.window > 0 && a.window < a.cap ? a.window : a.cap;
     return int((seen + kAttnTile - 1) / kAttnTile);
 }
-// Where there are pairs for half of the workers, short ones are left whole: a worker then takes up to 8 tiles where it
-// would have taken 1, but nothing has to be joined.  (250 sequences of 60 positions: cut, the joining took as long as
-// the rest.)  Otherwise those of one tile, which cannot be cut.
+// Where there are pairs for a quarter of the workers, short ones are left whole: a worker then takes up to 8 tiles where it
+// would have taken 1, but nothing has to be joined.  (250 sequences of up to 120 positions, 4 heads of keys: 15.5 us, cut
+// 20.)  Otherwise those of one tile, which cannot be cut.
 inline void attn_snap(AttnArgs& a) {
     a.snap = 4 * int64_t(a.sequences) * a.hk * a.chunks >= a.workers ? 8 : 1;
 }

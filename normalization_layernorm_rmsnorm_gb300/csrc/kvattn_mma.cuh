@@ -132,9 +132,10 @@ struct AttnSmem {
     uint32_t bias;             // [units][heads]: what the codes' bias adds to a unit's products, negative
 };
 constexpr uint32_t kAttnPlaces = 32 * 8;
-// Warps of a CTA, by the registers that a thread needs.
-template <typename T, typename F>
-constexpr int attn_warps = F::DMAX > 128 || F::NT > 1 ? 8 : sizeof(T) == 4 ? 12 : 12;
+// Warps of a CTA, by the registers that a thread needs.  (12: 131072 positions in 4 bits take 58 us; 10: 64; 14, with
+// 144 registers: 64; 16, with 128: 66.)
+template <typename F>
+constexpr int kAttnFormWarps = F::DMAX > 128 || F::NT > 1 ? 8 : kAttnWarps;
 template <typename T>
 constexpr int kAttnFactors = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;  // of p
 template <typename T, typename F>
@@ -692,7 +693,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 }
 
 template <typename T, typename F>
-__global__ void __launch_bounds__(32 * attn_warps<T, F>, 1) attn_mma_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * kAttnFormWarps<F>, 1) attn_mma_kernel(const AttnArgs a) {
     __shared__ AttnTable table;
     pdl_next();
     attn_table(a, table);
@@ -714,8 +715,8 @@ nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const int groups = a.d / a.cache.group;
     const size_t warp = attn_warp_bytes<T, F>(groups);
     // as many workers to an SM as have room for their rings beside the table
-    const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 64;
-    const int warps = int(std::min<size_t>(attn_warps<T, F>, room / warp));
+    const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 256;
+    const int warps = int(std::min<size_t>(kAttnFormWarps<F>, room / warp));
     a.workers = dev->sms * warps;
     attn_snap(a);
     const size_t smem = warps * warp;

@@ -256,6 +256,20 @@ def test_gradients_against_differences():
             assert abs((up - down) / (2 * step) - float(g[i])) < 0.01 + 0.01 * abs(float(g[i])), (i, up, down, float(g[i]))
 
 
+@pytest.mark.parametrize("rows,cols,gates", [(1030, 4096, 1), (985, 768, 5), (1000, 1536, 500), (700, 512, 0), (1300, 96, 13), (3000, 4096, 3)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows(dtype, rows, cols, gates):
+    # every slot of the ring used many times over, chunks that begin inside a gate's rows, rows that do not fill a slot
+    Block(dtype, rows, cols, gates, alpha=0.5).check()
+
+
+@pytest.mark.parametrize("gates", [2, 64, 320, 640])
+def test_gates_of_few_rows(gates):
+    Block("bf16", 640, 256, gates).check()
+    Block("f32", 640, 256, gates, pre=False).check()
+    Block("f16", 640, 256, gates, post=False, stream=False).check()
+
+
 def test_captured_with_a_shared_workspace():
     blocks = [Block("bf16", 700, 512, g, seed=g) for g in (1, 7)]
     ws = torch.empty(max(nrm.block_norm_workspace(b.x, b.gate).numel() for b in blocks), dtype=torch.uint8, device="cuda")

@@ -354,6 +354,32 @@ def test_far_offsets(d):
     assert same(*outs)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int4"])
+def test_strides_beyond_32_bits_of_vectors(kind):
+    # a cache described as spanning more than 2^36 bytes, of which the sequence uses the first page
+    c = Case("bf16", [60], 8, 2, 128, kind, 32, 64)
+    want, _ = c.run()
+    far = c.cache._c
+    page = int(c.table[0, 0])
+    for name, step in (("k_codes", c.codes[0].stride(0)), ("v_codes", c.codes[1].stride(0)), ("k_scales", 4 * c.scales[0].stride(0)),
+                       ("v_scales", 4 * c.scales[1].stride(0))):
+        setattr(far, name, getattr(far, name) + page * step)
+    far.pages, far.page_stride = 2, 1 << 38
+    table = c.table.clone()
+    c.table = torch.zeros_like(table)
+    got, _ = c.run()
+    assert same(got, want)
+    nrm.nrm_sync_status()
+
+
+@pytest.mark.parametrize("d,group", [(256, 32), (256, 64), (192, 64), (192, 192), (224, 32), (160, 32), (144, 48), (112, 16), (64, 64), (32, 32)])
+@pytest.mark.parametrize("kind", ["e4m3", "int8", "int4"])
+def test_rows_and_groups_of_every_kernel(d, group, kind):
+    # whole and partial tiles, one and two eights of heads
+    Case("bf16", [33, 128, 5], 10, 1, d, kind, group, 16).check(weights=True)
+    Case("f32", [70], 3, 1, d, kind, group, 16).check()
+
+
 def test_captured_and_replayed():
     c = Case("bf16", [300, 41], 8, 2, 64, "int8", 64, 16)
     q, table, lengths = c.q.cuda(), c.table.cuda(), c.lengths.cuda()
