@@ -698,9 +698,9 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 // partial rows; where the gate's rows are many, and so each has few, a warp takes
 // a row of its own (`by_warp`).
 // ---------------------------------------------------------------------------
-template <typename T>
+template <typename T, int C>  // C: columns of a lane, 4 where rows of floats are whole vectors (a sum of 152 rows of 4096: 12 -> 7 us)
 __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const BlockArgs a, int by_chunk, int by_warp) {
-    __shared__ float part[kBlockSumWarps][2][33];
+    __shared__ float part[kBlockSumWarps][2][32 * C + 1];
     pdl_next();
     void* out;
     int64_t c0 = 0, c1 = a.chunks - 1, row = 0;
@@ -725,34 +725,61 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
         if (c0 == c1) return;  // written by that chunk
     }
     if (!out) return;
-    const int col = int(blockIdx.x) * 32 + lane;
-    // Neumaier's sum
-    float s = 0.f, e = 0.f;
-    auto add = [&](float v) {
+    const int col = (int(blockIdx.x) * 32 + lane) * C;
+    // Neumaier's sums
+    float s[C] = {}, e[C] = {};
+    auto add = [](float& s, float& e, float v) {
         const float t = s + v;
         e += fabsf(s) >= fabsf(v) ? (s - t) + v : (v - t) + s;
         s = t;
     };
     if (col < a.cols) {
-#pragma unroll 4
-        for (int64_t c = alone ? c0 : c0 + warp; c <= c1; c += alone ? 1 : kBlockSumWarps)
-            add(ld_after(part_row(a, kind == 2 && c == c0 ? 3 : kind, c) + col));
+        constexpr int AHEAD = 8;
+        const int64_t step = alone ? 1 : kBlockSumWarps;
+        for (int64_t c = alone ? c0 : c0 + warp; c <= c1; c += AHEAD * step) {
+            float v[AHEAD][C];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int64_t at = c + k * step;
+                if (at > c1) break;
+                const float* from = part_row(a, kind == 2 && at == c0 ? 3 : kind, at) + col;
+                if constexpr (C == 4) {
+                    const uint4 x = ld_after(reinterpret_cast<const uint4*>(from));
+                    v[k][0] = __uint_as_float(x.x), v[k][1] = __uint_as_float(x.y);
+                    v[k][2] = __uint_as_float(x.z), v[k][3] = __uint_as_float(x.w);
+                } else {
+                    v[k][0] = ld_after(from);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (c + k * step > c1) break;
+#pragma unroll
+                for (int i = 0; i < C; ++i) add(s[i], e[i], v[k][i]);
+            }
+        }
     }
     if (alone) {
-        if (col < a.cols) put<T>(out, row * a.cols + col, s + e);
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (col < a.cols) put<T>(out, row * a.cols + col + i, s[i] + e[i]);
         return;
     }
-    part[warp][0][lane] = s;
-    part[warp][1][lane] = e;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        part[warp][0][lane * C + i] = s[i];
+        part[warp][1][lane * C + i] = e[i];
+    }
     __syncthreads();
-    if (warp != 0 || col >= a.cols) return;
-    s = e = 0.f;
+    const int mine = int(blockIdx.x) * 32 * C + int(threadIdx.x);
+    if (threadIdx.x >= 32 * C || mine >= a.cols) return;
+    float all = 0.f, lost = 0.f;
 #pragma unroll 8
     for (int w = 0; w < kBlockSumWarps; ++w) {
-        add(part[w][0][lane]);
-        add(part[w][1][lane]);
+        add(all, lost, part[w][0][threadIdx.x]);
+        add(all, lost, part[w][1][threadIdx.x]);
     }
-    put<T>(out, row * a.cols + col, s + e);
+    put<T>(out, row * a.cols + mine, all + lost);
 }
 
 // ---------------------------------------------------------------------------
@@ -879,8 +906,10 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     int by_warp = gate_rows > 4;
     if (by_warp) gate_rows = (gate_rows + kBlockSumWarps - 1) / kBlockSumWarps;
     void* q[] = {&a, &by_chunk, &by_warp};
-    return launch_pdl(reinterpret_cast<const void*>(&block_sum_kernel<T>),
-                      dim3(unsigned((a.cols + 31) / 32), unsigned(2 + gate_rows)), dim3(kBlockSumWarps * 32), q, s);
+    const int columns = a.cols % 4 == 0 ? 128 : 32;
+    return launch_pdl(columns == 128 ? reinterpret_cast<const void*>(&block_sum_kernel<T, 4>)
+                                     : reinterpret_cast<const void*>(&block_sum_kernel<T, 1>),
+                      dim3(unsigned((a.cols + columns - 1) / columns), unsigned(2 + gate_rows)), dim3(kBlockSumWarps * 32), q, s);
 }
 
 }  // namespace nrm
