@@ -1,8 +1,10 @@
 /*
  * libnorm.h -- C ABI of libnorm: forward and backward passes of LayerNorm,
- * RMSNorm and BatchNorm (with fused residual add and activation), and the norms
- * and position rotation of attention heads with a quantised key/value cache, on
- * one NVIDIA GB300 GPU (sm_103a), computed by hand-written CUDA kernels.
+ * RMSNorm and BatchNorm (with fused residual add and activation), the norms and
+ * position rotation of attention heads with a quantised key/value cache, the
+ * attention over that cache and eviction from it, and the norms around a block
+ * of a residual stream, on one NVIDIA GB300 GPU (sm_103a), computed by
+ * hand-written CUDA kernels.
  *
  * Sources for what each call computes (web articles on the attorch
  * normalization kernels):
@@ -632,10 +634,13 @@ typedef struct nrm_kv_weights {
  * and positions outside the window are left as they were.
  * scale: finite.  workspace: nrm_kv_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, clobbered; calls that overlap on the GPU need separate ones.
- * The sums are float32 over products that are exact, or of factors with 22
- * bits, but for the p_j of bfloat16 outputs, rounded to 11 bits.
- * 16-byte aligned rows of codes, with d and group multiples of 16, take the
- * tensor cores; other layouts, 8-byte aligned ones apart, run element by element.
+ * The sums are float32.  Their products are exact, or of factors with 22 bits;
+ * but for bfloat16 outputs p_j, the value's scale and their product have 11 bits
+ * each.  What of a p_j times a value's scale is below 2^-38 of the largest p_j
+ * times the largest such scale of the sequence's head may be lost.
+ * d and group multiples of 16, with rows of codes of whole aligned 16-byte (or
+ * 8-byte) vectors, take matrix instructions; other layouts run element by
+ * element.
  */
 NRM_API nrm_status nrm_kv_cache_attention(const nrm_heads *q, const nrm_kv_cache *cache,
                                   const nrm_kv_pages *pages, const nrm_heads *out, float scale,
