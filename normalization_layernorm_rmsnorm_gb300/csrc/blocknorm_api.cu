@@ -160,7 +160,7 @@ nrm_status nrm_block_norm_bwd(const void* dh, const void* dy, const void* f, con
         a.alpha = alpha;
         a.post = post != 0;
         a.chunks = block_chunks(*dev, rows);
-        const bool vec = whole_vectors({dh, dy, f, y, gate, w_post, w_pre, dx, df}, cols, dt);
+        const bool vec = whole_vectors({dh, dy, f, y, gate, w_post, w_pre, dx, df, dgate}, cols, dt);
         return by_dtype(dt, [&](auto tag) {
             return block_norm_bwd<decltype(tag)>(a, vec, reinterpret_cast<cudaStream_t>(stream));
         });

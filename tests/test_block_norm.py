@@ -52,13 +52,16 @@ class Block:
         self.dh = new(rows, cols) if pre else None
         self.dy = new(rows, cols) if stream else None
 
-    def place(self, x):
-        b = torch.empty(x.numel() + self.offset, dtype=x.dtype, device="cuda")[self.offset:].view(x.shape)
+    grads_at = None  # elements into their buffers; None: as all else
+
+    def place(self, x, at=None):
+        at = self.offset if at is None else at
+        b = torch.empty(x.numel() + at, dtype=x.dtype, device="cuda")[at:].view(x.shape)
         b.copy_(x)
         return b
 
-    def like(self, x):
-        return None if x is None else self.place(torch.full(x.shape, 7.0, dtype=x.dtype))
+    def like(self, x, at=None):
+        return None if x is None else self.place(torch.full(x.shape, 7.0, dtype=x.dtype), at)
 
     def fwd(self, y=None, h=None, stats=True, stream=None):
         y = self.like(self.x) if y is None else y
@@ -71,7 +74,7 @@ class Block:
 
     def bwd(self, y, r1, r2, grads=True, ws=None, stream=None):
         dx, df = self.like(self.x), self.like(self.x)
-        dgate, dw1, dw2 = (self.like(t) if grads else None for t in (self.gate, self.w_post, self.w_pre))
+        dgate, dw1, dw2 = (self.like(t, self.grads_at) if grads else None for t in (self.gate, self.w_post, self.w_pre))
         if ws is None and grads:
             ws = nrm.block_norm_workspace(self.x, self.gate)
             ws.fill_(0xff)
@@ -319,3 +322,13 @@ def test_random_shapes(seed):
     rows = min(rows, max(1, (1 << 21) // cols) // max(1, gates) * max(1, gates)) or max(1, gates)
     Block(str(rng.choice(["bf16", "f16", "f32"])), rows, cols, gates, alpha=float(rng.choice([1.0, 0.5, -2.0])), post=bool(rng.random() < 0.8),
           pre=bool(rng.random() < 0.9), seed=seed, weights=bool(rng.random() < 0.9)).check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,gates", [(30, 3), (30, 30), (400, 1), (400, 2)])
+def test_unaligned_gradients_alone(dtype, rows, gates):
+    # all else is whole vectors
+    c = Block(dtype, rows, 512, gates)
+    c.grads_at = 1
+    c.check()
+    nrm.nrm_sync_status()
