@@ -636,8 +636,9 @@ typedef struct nrm_kv_weights {
  * 16-byte aligned, clobbered; calls that overlap on the GPU need separate ones.
  * The sums are float32.  Their products are exact, or of factors with 22 bits;
  * but for bfloat16 outputs p_j, the value's scale and their product have 11 bits
- * each.  What of a p_j times a value's scale is below 2^-38 of the largest p_j
- * times the largest such scale of the sequence's head may be lost.
+ * each.  What of a query is below 2^-35 of its head's largest element, or of a
+ * p_j times a value's scale below 2^-38 of the largest p_j times the largest such
+ * scale of the sequence's head, may be lost.
  * d and group multiples of 16, with rows of codes of whole aligned 16-byte (or
  * 8-byte) vectors, take matrix instructions; other layouts run element by
  * element.

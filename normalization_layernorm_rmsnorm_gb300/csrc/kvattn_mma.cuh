@@ -341,7 +341,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 
     // ---- the running softmax ----
     float acc[F::UNITS][F::TILES][NT][4], m[NT][2], sum[NT][2];
-    int top[F::UNITS];  // the values' largest scale so far is below 2^top
+    int top[F::UNITS];  // the values' largest scale so far (its size: one may be negative) is below 2^top
 #pragma unroll
     for (int u = 0; u < F::UNITS; ++u) {
         top[u] = -1000;
@@ -368,13 +368,13 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
                 mine_of[u] = in_ring<const float>(mine + of_unit[u]);
-                larger |= mine_of[u] >= (top[u] < -126 ? -1.f : __uint_as_float(uint32_t(127 + top[u]) << 23));
+                larger |= fabsf(mine_of[u]) >= (top[u] < -126 ? -1.f : __uint_as_float(uint32_t(127 + top[u]) << 23));
             }
             if (__any_sync(0xffffffffu, larger)) {
 #pragma unroll
                 for (int u = 0; u < F::UNITS; ++u) {
                     if (!F::EXACT && u >= units) break;
-                    const uint32_t b = __float_as_uint(mine_of[u]);
+                    const uint32_t b = __float_as_uint(mine_of[u]) & 0x7fffffffu;
                     const uint32_t most = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
                     const int now = min(127, max(max(top[u], -100), int(most >> 23) - 126));
                     const float raise = exp2f(float(max(top[u] - now, -126)));

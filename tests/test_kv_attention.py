@@ -268,6 +268,18 @@ def test_scales_of_values_over_the_whole_range():
 
 
 @pytest.mark.parametrize("d", [64, 40])
+@pytest.mark.parametrize("kind", ["e4m3", "int8", "int4"])
+def test_negative_scales(d, kind):
+    # a cache that something else has written may hold them
+    c = Case("f32", [90, 33, 1], 4, 2, d, kind, 8 if d == 40 else 16, 16)
+    for t in range(2):
+        c.scales[t][:, ::2] *= -3
+    c.check(weights=True)
+    c.scales[1].abs_().neg_()
+    c.check()
+
+
+@pytest.mark.parametrize("d", [64, 40])
 def test_lengths_and_pages_out_of_range_are_reported(d):
     c = Case("f32", [45, 60, 30], 4, 2, d, "int8", d, 16, width=4, poison=0.0)
     good, _ = c.run()
