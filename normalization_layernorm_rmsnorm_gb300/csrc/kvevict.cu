@@ -47,17 +47,14 @@ __device__ __forceinline__ uint32_t warp_before(uint32_t mine, uint32_t* all) {
     *all = __shfl_sync(0xffffffffu, run, 31);
     return run - mine;
 }
-// Sum of `mine` over the threads before this one; *all: over all of them.
-__device__ __forceinline__ uint32_t cta_before(uint32_t mine, uint32_t* sums, uint32_t* all) {
+// Sum of `mine` over the threads before this one.
+__device__ __forceinline__ uint32_t cta_before(uint32_t mine, uint32_t* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t in_warp;
     const uint32_t before = warp_before(mine, &in_warp);
-    __syncthreads();
     if (lane == 0) sums[warp] = in_warp;
     __syncthreads();
-    const uint32_t other = lane < kEvictWarps ? sums[lane] : 0;
-    const uint32_t warps = warp_before(other, all);
-    return __shfl_sync(0xffffffffu, warps, warp) + before;
+    return __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0) + before;
 }
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t a) {
     uint32_t v;
@@ -67,8 +64,10 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t a) {
 
 __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const EvictArgs a, int ctas, int held) {
     extern __shared__ __align__(16) uint32_t keys[];  // [held]
-    __shared__ __align__(16) uint32_t counts[2][kEvictBins];
+    __shared__ __align__(16) uint32_t counts[2][kEvictBins];      // this CTA's
+    __shared__ __align__(16) uint32_t slices[2][kEvictBins / 2];  // the cluster's, of this CTA's share of the digits
     __shared__ uint32_t sums[32], found[2], share[2];
+    static_assert(kEvictWarps <= 32 && kEvictBins == 4 * kEvictThreads, "four digits to a thread");
     pdl_next();
     const int64_t which = blockIdx.x / ctas, s = which / a.heads;
     const int part = int(blockIdx.x % ctas), head = int(which - s * a.heads);
@@ -95,65 +94,98 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
     const int from = min(count, max(0, int(a.first) - first)), to = min(count, max(0, int(n - a.recent) - first));
     const bool holds = count <= held;
     weights += first;
-    if (holds) {
-        constexpr int AHEAD = 16;
-        for (int i = threadIdx.x; i < count; i += AHEAD * kEvictThreads) {
-            float w[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (i + k * kEvictThreads < count) w[k] = ld_after(weights + i + k * kEvictThreads);
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (i + k * kEvictThreads < count) keys[i + k * kEvictThreads] = weight_key(w[k]);
-        }
-    }
-    // four neighbouring positions, and which of them lie between (a bit each)
-    auto four = [&](int i, uint32_t (&k)[4]) -> uint32_t {
-        if (holds) {
-            const uint4 v = *reinterpret_cast<const uint4*>(keys + i);  // (what lies behind the last is not used)
-            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) k[j] = i + j < count ? weight_key(ld_after(weights + i + j)) : 0;
-        }
+    uint32_t want = uint32_t(a.keep - a.first - a.recent), border = 0;
+    const bool any = want > 0;
+    // of four neighbouring positions, which lie between (a bit each)
+    auto lie_between = [&](int i) -> uint32_t {
         if (i >= from && i + 4 <= to) return 15u;
         const int lo = min(4, max(0, from - i)), hi = min(4, max(0, to - i));
         return ((1u << hi) - 1) & ~((1u << lo) - 1);
     };
-    // the border among the positions between: of those with its key, the first `want` stay
-    uint32_t want = uint32_t(a.keep - a.first - a.recent), border = 0;
-    const bool any = want > 0;
+    const bool vectors = reinterpret_cast<uintptr_t>(weights) % 16 == 0;
+    auto load = [&](int i, uint32_t (&k)[4]) {
+        if (vectors && i + 4 <= count) {
+            const uint4 v = ld_after(reinterpret_cast<const uint4*>(weights + i));
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[j] = i + j < count ? __float_as_uint(ld_after(weights + i + j)) : 0;
+        }
+    };
+    auto four = [&](int i, uint32_t (&k)[4]) {
+        if (holds) {
+            const uint4 v = *reinterpret_cast<const uint4*>(keys + i);  // (what lies behind the last is not used)
+            k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+        } else {
+            load(i, k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[j] = weight_key(__uint_as_float(k[j]));
+        }
+    };
+    auto clear = [&](int round) {
+        reinterpret_cast<uint4*>(counts[round & 1])[threadIdx.x] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint2*>(slices[round & 1])[threadIdx.x] = make_uint2(0, 0);
+        __syncthreads();
+    };
+    // The border among the positions between: of those with its key, the first `want` stay.
+    constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
+    clear(0);
+    if (holds) {  // the first digits are counted as the weights arrive
+        constexpr int AHEAD = 8;
+        for (int i0 = 4 * int(threadIdx.x); i0 < count; i0 += AHEAD * kEvictTurn) {
+            uint32_t k[AHEAD][4];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (i0 + u * kEvictTurn < count) load(i0 + u * kEvictTurn, k[u]);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = i0 + u * kEvictTurn;
+                if (i >= count) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k[u][j] = weight_key(__uint_as_float(k[u][j]));
+                *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[u][0], k[u][1], k[u][2], k[u][3]);
+                const uint32_t between = lie_between(i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (between >> j & 1) atomicAdd(&counts[0][k[u][j] >> kShift[0]], 1u);
+            }
+        }
+    }
 #pragma unroll
     for (int round = 0; round < 3; ++round) {
         if (!any) break;
-        constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
         const int shift = kShift[round], bits = kBits[round];
-        uint32_t* mine = counts[round & 1];
-        for (int i = threadIdx.x; i < kEvictBins; i += kEvictThreads) mine[i] = 0;
-        __syncthreads();
-        for (int i = 4 * int(threadIdx.x); i < to; i += kEvictTurn) {
-            uint32_t k[4];
-            const uint32_t between = four(i, k);
+        uint32_t *mine = counts[round & 1], *slice = slices[round & 1];
+        if (round > 0) clear(round);
+        if (round > 0 || !holds)
+            for (int i = 4 * int(threadIdx.x); i < to; i += kEvictTurn) {
+                uint32_t k[4];
+                four(i, k);
+                const uint32_t between = lie_between(i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if ((between >> j & 1) && (round == 0 || k[j] >> (shift + bits) == border >> (shift + bits)))
-                    atomicAdd(&mine[k[j] >> shift & ((1u << bits) - 1)], 1u);
-        }
+                for (int j = 0; j < 4; ++j)
+                    if ((between >> j & 1) && (round == 0 || k[j] >> (shift + bits) == border >> (shift + bits)))
+                        atomicAdd(&mine[k[j] >> shift & ((1u << bits) - 1)], 1u);
+            }
         cluster_sync();
-        // thread t has the digits 4 t to 4 t + 3 from the largest down (16 bytes of each CTA's counts)
-        uint32_t c[4] = {}, all;
-        const uint32_t* digits = &mine[kEvictBins - 4 - int(threadIdx.x) * 4];
-#pragma unroll 8
-        for (int r = 0; r < ctas; ++r) {
-            const float4 v = ctas == 1 ? *reinterpret_cast<const float4*>(digits) : ld_dsmem_f4(dsmem_addr(digits, uint32_t(r)));
-            c[0] += __float_as_uint(v.w);
-            c[1] += __float_as_uint(v.z);
-            c[2] += __float_as_uint(v.y);
-            c[3] += __float_as_uint(v.x);
+        // thread t has the digits 4 t to 4 t + 3 from the largest down
+        const int at = kEvictBins - 4 - int(threadIdx.x) * 4;
+        float4 v;
+        if (ctas == 1) {
+            v = *reinterpret_cast<const float4*>(mine + at);
+        } else {
+            // each CTA adds a share of the digits, 16 bytes of one CTA's to a thread; then all read the sums
+            const int of = kEvictBins / ctas, part4 = of / 4, r = int(threadIdx.x) / part4, i = (int(threadIdx.x) - r * part4) * 4;
+            const float4 theirs = ld_dsmem_f4(dsmem_addr(mine + part * of + i, uint32_t(r)));
+            atomicAdd(slice + i, __float_as_uint(theirs.x));
+            atomicAdd(slice + i + 1, __float_as_uint(theirs.y));
+            atomicAdd(slice + i + 2, __float_as_uint(theirs.z));
+            atomicAdd(slice + i + 3, __float_as_uint(theirs.w));
+            cluster_sync();
+            v = ld_dsmem_f4(dsmem_addr(slice + at % of, uint32_t(at / of)));
         }
-        const uint32_t sum = c[0] + c[1] + c[2] + c[3];
-        static_assert(kEvictBins == 4 * kEvictThreads, "four digits to a thread");
-        uint32_t before = cta_before(sum, sums, &all);
+        const uint32_t c[4] = {__float_as_uint(v.w), __float_as_uint(v.z), __float_as_uint(v.y), __float_as_uint(v.x)};
+        uint32_t before = cta_before(c[0] + c[1] + c[2] + c[3], sums);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (before < want && want <= before + c[j]) {
@@ -165,14 +197,14 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         __syncthreads();
         border |= found[0] << shift;
         want = found[1];
-        __syncthreads();
     }
     // of four positions, which stay for sure and which lie on the border: a bit each
     auto stay = [&](int i, uint32_t& sure, uint32_t& tie) {
         sure = tie = 0;
         if (i >= count) return;
         uint32_t k[4];
-        const uint32_t between = four(i, k), there = i + 4 <= count ? 15u : (1u << (count - i)) - 1;
+        four(i, k);
+        const uint32_t between = lie_between(i), there = i + 4 <= count ? 15u : (1u << (count - i)) - 1;
         if (any) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -183,34 +215,46 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         sure = (sure & between) | (there & ~between);
         tie &= between;
     };
+    // a warp takes a stretch of positions: how many of it stay, then, behind those of the warps before it, which
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int stretch = (count + kEvictTurn - 1) / kEvictTurn * 128, begin = warp * stretch, end = min(count, begin + stretch);
     uint32_t above = 0, ties = 0, sure, tie;
-    for (int i = 4 * int(threadIdx.x); i < count; i += kEvictTurn) {
+    for (int i = begin + 4 * lane; i < end; i += 128) {
         stay(i, sure, tie);
         above += __popc(sure);
         ties += __popc(tie);
     }
-    uint32_t all_above, all_ties;
-    cta_before(above, sums, &all_above);
-    cta_before(ties, sums, &all_ties);
-    if (threadIdx.x == 0) {
-        share[0] = all_above;
-        share[1] = all_ties;
+    above = __reduce_add_sync(0xffffffffu, above);
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    __shared__ uint32_t of_warp[2][kEvictWarps];
+    if (lane == 0) {
+        of_warp[0][warp] = above;
+        of_warp[1][warp] = ties;
     }
-    cluster_sync();
-    uint32_t taken = 0, tied = 0;
-    for (int r = 0; r < part; ++r) {
-        taken += ld_dsmem_u32(dsmem_addr(&share[0], uint32_t(r)));
-        tied += ld_dsmem_u32(dsmem_addr(&share[1], uint32_t(r)));
+    __syncthreads();
+    above = lane < kEvictWarps ? of_warp[0][lane] : 0;
+    ties = lane < kEvictWarps ? of_warp[1][lane] : 0;
+    if (warp == 0) {
+        const uint32_t all_above = __reduce_add_sync(0xffffffffu, above), all_ties = __reduce_add_sync(0xffffffffu, ties);
+        if (lane == 0) {
+            share[0] = all_above;
+            share[1] = all_ties;
+        }
     }
-    taken += min(tied, want);  // of the ties before this CTA's, those that stay
-    // in order: each turn takes the next positions, four to a thread
-    for (int i0 = 0; i0 < count; i0 += kEvictTurn) {
-        const int i = i0 + 4 * int(threadIdx.x);
+    uint32_t taken = __reduce_add_sync(0xffffffffu, lane < warp ? above : 0);
+    uint32_t tied = __reduce_add_sync(0xffffffffu, lane < warp ? ties : 0);
+    if (ctas > 1) {
+        cluster_sync_all();
+        taken += __reduce_add_sync(0xffffffffu, lane < part ? ld_dsmem_u32(dsmem_addr(&share[0], uint32_t(lane))) : 0);
+        tied += __reduce_add_sync(0xffffffffu, lane < part ? ld_dsmem_u32(dsmem_addr(&share[1], uint32_t(lane))) : 0);
+    }
+    taken += min(tied, want);  // of the ties before, those that stay
+    for (int i0 = begin; i0 < end; i0 += 128) {
+        const int i = i0 + 4 * lane;
         stay(i, sure, tie);
-        // both counts in one sum: a turn has at most 2048 of each
-        uint32_t all;
-        const uint32_t before = cta_before(uint32_t(__popc(sure)) | uint32_t(__popc(tie)) << 16, sums, &all);
-        // the ties before it that stay, and those that are sure
+        uint32_t all;  // both counts in one sum
+        const uint32_t before = warp_before(uint32_t(__popc(sure)) | uint32_t(__popc(tie)) << 16, &all);
+        // the ties before it, and those that stay
         uint32_t tie_at = tied + (before >> 16);
         uint32_t at = taken + (before & 0xffffu) + (min(tie_at, want) - min(tied, want));
 #pragma unroll
