@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
         else __syncthreads();
     };
     // this CTA's positions, whole turns of its threads, and of them those between, [from, to)
-    const int each = (int(n) + ctas - 1) / ctas / kEvictTurn * kEvictTurn + kEvictTurn;
+    const int each = int((n + ctas * kEvictTurn - 1) / (ctas * kEvictTurn)) * kEvictTurn;
     const int first = min(int(n), part * each), count = min(int(n) - first, each);
     const int from = min(count, max(0, int(a.first) - first)), to = min(count, max(0, int(n - a.recent) - first));
     const bool holds = count <= held;
@@ -379,7 +379,7 @@ nrm_status choose(EvictArgs& a, const DevInfo* dev, cudaStream_t s) {
     int ctas = 1;
     while (ctas < kEvictCluster && a.cap > int64_t(ctas) * kEvictPart && pairs * ctas * 2 <= 2 * int64_t(dev->sms)) ctas *= 2;
     if (pairs * ctas >= (int64_t(1) << 31)) return fail(NRM_ERR_UNSUPPORTED, "sequences*heads must be < 2^31");
-    const int64_t most = (a.cap + ctas - 1) / ctas / kEvictTurn * kEvictTurn + kEvictTurn;
+    const int64_t most = (a.cap + ctas * kEvictTurn - 1) / (ctas * kEvictTurn) * kEvictTurn;
     int held = int(most <= kEvictHeld ? most : 0);
     const void* fn = reinterpret_cast<const void*>(&evict_choose_kernel);
     const size_t smem = size_t(held) * 4;
