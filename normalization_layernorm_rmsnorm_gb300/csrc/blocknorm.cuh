@@ -311,7 +311,95 @@ __global__ void __launch_bounds__(MOST, CTAS) block_fwd_vec_kernel(const BlockAr
 }
 
 // ---------------------------------------------------------------------------
-// whole 16-byte vectors, backward: rows through a ring in shared memory
+// rows of any length and alignment, forward: the same, element by element
+// ---------------------------------------------------------------------------
+// Thread t has the elements t, t + THREADS, ... (a known number apart: an access is then one instruction); what hides
+// the loads' latency is the CTAs of an SM and the next row, which is asked for before the second norm.
+constexpr int kBlockElems = 8;  // of a thread
+template <typename T, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) block_fwd_elem_kernel(const BlockArgs a, int per) {
+    using bits = typename Io<T>::bits_t;
+    constexpr int E = kBlockElems, threads = THREADS, warps = THREADS / 32;
+    __shared__ float sums[2][2][32];
+    pdl_next();
+    const int t = threadIdx.x, lane = t & 31, left = a.cols - t;
+    const int64_t first = int64_t(blockIdx.x) * per, end = min(a.rows, first + per);
+    const float inv = 1.f / float(a.cols);
+    int phase = 0;
+    auto row_sum = [&](float v, int which) {
+        v = warp_sum(v);
+        if (warps == 1) return v;
+        if (lane == 0) sums[which][phase][t >> 5] = v;
+        __syncthreads();
+        return warp_sum(lane < warps ? sums[which][phase][lane] : 0.f);
+    };
+    auto there = [&](int e) { return left > e * threads; };
+    bits fr[E], xr[E];
+    auto load_row = [&](int64_t row) {
+        if (row >= end) return;
+        const bits *f = static_cast<const bits*>(a.f) + row * a.cols + t, *x = static_cast<const bits*>(a.x) + row * a.cols + t;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (there(e)) fr[e] = ld_after(f + e * threads);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (there(e)) xr[e] = ld_after(x + e * threads);
+    };
+    load_row(first);
+    float scale[E], w_pre[E];  // alpha * gate * w_post
+    auto load_scale = [&](int64_t gate_row) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = e * threads + t;
+            scale[e] = a.alpha;
+            if (!there(e)) continue;
+            if (a.gates) scale[e] *= element<T>(a.gate, gate_row * a.cols + i);
+            if (a.w_post) scale[e] *= element<T>(a.w_post, i);
+        }
+    };
+    int64_t gate_row = a.gates ? row_div(first, a.per_gate) : 0, gate_end = a.gates ? (gate_row + 1) * a.per_gate.d : end;
+    load_scale(gate_row);
+#pragma unroll
+    for (int e = 0; e < E; ++e) w_pre[e] = a.h && there(e) ? weight_at<T>(a.w_pre, e * threads + t) : 1.f;
+    for (int64_t r = first; r < end; ++r) {
+        if (r == gate_end) {
+            gate_end += a.per_gate.d;
+            load_scale(++gate_row);
+        }
+        float r1 = 1.f;
+        if (a.post) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (there(e)) s = fmaf(Io<T>::load(fr[e]), Io<T>::load(fr[e]), s);
+            r1 = rsqrtf(row_sum(s, 0) * inv + a.eps);
+            if (a.rstd_post && t == 0) a.rstd_post[r] = r1;
+        }
+        float s = 0.f, y[E];
+        bits* to = static_cast<bits*>(a.y) + r * a.cols + t;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (!there(e)) continue;
+            const bits b = Io<T>::store(fmaf(Io<T>::load(fr[e]) * r1, scale[e], Io<T>::load(xr[e])));
+            to[e * threads] = b;
+            y[e] = Io<T>::load(b);
+            s = fmaf(y[e], y[e], s);
+        }
+        load_row(r + 1);
+        if (a.h) {
+            const float r2 = rsqrtf(row_sum(s, 1) * inv + a.eps);
+            if (a.rstd_pre && t == 0) a.rstd_pre[r] = r2;
+            to = static_cast<bits*>(a.h) + r * a.cols + t;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (there(e)) to[e * threads] = Io<T>::store(y[e] * r2 * w_pre[e]);
+        }
+        phase ^= 1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// backward: rows through a ring in shared memory
 // ---------------------------------------------------------------------------
 // A CTA stays for its chunk of rows.  One bulk copy for each of dh, dy, f and y
 // brings the next rows into a slot of the ring (a few slots ahead: enough bytes in
@@ -322,6 +410,11 @@ __global__ void __launch_bounds__(MOST, CTAS) block_fwd_vec_kernel(const BlockAr
 // which needs the first); after the first the slot is free.  A slot does not
 // reach over the end of a gate's row; there the groups' sums of its gradient are
 // added, in their order.
+//
+// Rows of whole 16-byte vectors are taken so.  Of others (ELEMS, the threads of a
+// group) a thread takes 16 bytes' worth of elements, ELEMS apart, one by one; the copies are rounded
+// outwards to 16 bytes, which stays within the tensor, but for its last bytes,
+// which thread 0 brings itself.
 constexpr int kBlockConsumers = 512;
 constexpr int kBlockSlots = 8;                       // at most
 constexpr uint64_t kBlockWaitNs = 2000000000ull;     // bounded waits: 2 s
@@ -363,21 +456,34 @@ struct BlockAsk {
         : walk(a, by_gate), from{t0, t1, t2, t3} {}
     // false: the slot's last rows were not done with in time
     __device__ __forceinline__ bool next(const BlockArgs& a, const BlockRing& g, unsigned char* smem, uint64_t* full, uint64_t* empty,
-                                         int64_t row_bytes, uint64_t pol) {
+                                         int64_t row_bytes, uint64_t pol, bool elem) {
         if (!walk.next(a, g)) return true;
         if (round > 0 && !mbar_wait_bounded(&empty[slot], (round - 1) & 1u, kBlockWaitNs)) {
             walk.r = walk.end;  // no more copies
             walk.count = 0;
             return false;
         }
-        const uint32_t bytes = uint32_t(walk.count * row_bytes);
+        int64_t begin = walk.r * row_bytes, end = begin + walk.count * row_bytes;
         unsigned char* to = smem + g.ring_at + size_t(slot) * g.slot_bytes;
+        if (elem) {
+            const int64_t last = end;
+            begin &= ~int64_t(15);
+            end = min((end + 15) & ~int64_t(15), (a.rows * row_bytes) & ~int64_t(15));
+            if (end < last) {  // the tensors' last bytes
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (from[k])
+                        for (int64_t i = end; i < last; i += 2)
+                            *reinterpret_cast<uint16_t*>(to + k * g.tensor_bytes + (i - begin)) =
+                                ld_after(reinterpret_cast<const uint16_t*>(static_cast<const unsigned char*>(from[k]) + i));
+            }
+        }
+        const uint32_t bytes = uint32_t(end - begin);
         mbar_arrive_expect_tx(&full[slot], bytes * ((from[0] != nullptr) + (from[1] != nullptr) + (from[2] != nullptr) + (from[3] != nullptr)));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (from[k])
-                bulk_g2s(to + k * g.tensor_bytes, static_cast<const unsigned char*>(from[k]) + walk.r * row_bytes, bytes, &full[slot],
-                         pol);
+            if (from[k] && bytes)
+                bulk_g2s(to + k * g.tensor_bytes, static_cast<const unsigned char*>(from[k]) + begin, bytes, &full[slot], pol);
         ++asked;
         if (++slot == g.slots) {
             slot = 0;
@@ -409,15 +515,58 @@ __device__ __forceinline__ void group_sums(float (&v)[R], float* place, int grou
 }
 
 // FAST: everything is there, with one gate for many rows or none, and rows of whole vectors for every thread.
-template <typename T, int VPT, int ROWS, bool FAST>
+template <typename T, int VPT, int ROWS, bool FAST, int ELEMS = 0>
 __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(const BlockArgs a, const BlockRing g) {
+    using bits = typename Io<T>::bits_t;
     constexpr int VE = kVec<T>, H = VE / 2;
+    constexpr bool ELEM = ELEMS != 0;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(8) uint64_t full[kBlockSlots], empty[kBlockSlots];
     __shared__ float sums[2][2][ROWS * 16];
     __shared__ int s_bad;
-    const int group = int(threadIdx.x) / g.threads, t = int(threadIdx.x) - group * g.threads, warps = g.threads >> 5;
-    const int nvec = a.cols / VE;
+    const int threads = ELEM ? ELEMS : g.threads;  // of a group
+    const int group = int(threadIdx.x) / threads, t = int(threadIdx.x) - group * threads, warps = threads >> 5;
+    const int nvec = ELEM ? VPT * threads : a.cols / VE;  // vectors of a row, or threads' shares of one
+    // Shares of elements: share j of thread t has the elements t + (j*VE + e)*ELEMS.  From a row (0 behind its end), and
+    // into one.
+    auto gather = [&](auto&& load, int j, int t) {
+        const int left = a.cols - t;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                const int at = (j * VE + k) * ELEMS;
+                w[k] = left > at ? uint32_t(load(t + at)) : 0u;
+            } else {
+                const int at = (j * VE + 2 * k) * ELEMS, next = at + ELEMS;
+                const uint32_t lo = left > at ? uint32_t(load(t + at)) : 0u, hi = left > next ? uint32_t(load(t + next)) : 0u;
+                w[k] = __byte_perm(lo, hi, 0x5410);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    auto scatter = [&](bits* row, int j, int t, uint4 v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const int left = a.cols - t;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            const int at = (j * VE + e) * ELEMS;
+            if (left > at) row[t + at] = sizeof(T) == 4 ? bits(w[e % 4]) : bits(w[e / 2 % 4] >> (16 * (e & 1)));
+        }
+    };
+    // vector or share j of thread t of row r of a tensor
+    auto from_global = [&](const void* p, int64_t r, int j, int t) {
+        if constexpr (ELEM) {
+            const bits* row = static_cast<const bits*>(p) + r * a.cols;
+            return gather([&](int at) { return ld_after(row + at); }, j, t);
+        } else {
+            return ld_after(static_cast<const uint4*>(p) + r * nvec + (j * threads + t));
+        }
+    };
+    auto to_global = [&](void* p, int64_t r, int j, int t, uint4 v) {
+        if constexpr (ELEM) scatter(static_cast<bits*>(p) + r * a.cols, j, t, v);
+        else st_v4(static_cast<uint4*>(p) + r * nvec + (j * threads + t), v);
+    };
     if (threadIdx.x == 0) {
         s_bad = 0;
         for (int i = 0; i < g.slots; ++i) {
@@ -433,7 +582,8 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
         float2 one[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) one[h] = f2(1.f);
-        weights[i] = w ? ld_after(static_cast<const uint4*>(w) + (i < nvec ? i : i - nvec)) : pack2x<T>(one);
+        const int k = i < nvec ? i : i - nvec;
+        weights[i] = w ? from_global(w, 0, k / threads, k % threads) : pack2x<T>(one);
     }
     __syncthreads();
 
@@ -445,7 +595,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     bool bad = false;
     BlockAsk ask(a, by_gate, a.dh, a.dy, a.f, a.dh ? a.y : nullptr);
     if (threadIdx.x == 0)
-        for (int i = 0; i < g.slots; ++i) ask.next(a, g, smem, full, empty, row_bytes, pol);
+        for (int i = 0; i < g.slots; ++i) ask.next(a, g, smem, full, empty, row_bytes, pol, ELEM);
 
     // Over rows with one gate (and over all without), the sums of dgate and dw_post are this one's, times alpha*w_post
     // and alpha*gate: sum_unit = sum of dx*f*r1.
@@ -458,7 +608,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     auto load_scale = [&](int64_t gate_row, bool with_weight, float2 (&to)[VPT][H]) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = j * g.threads + t;
+            const int i = j * threads + t;
 #pragma unroll
             for (int h = 0; h < H; ++h) to[j][h] = f2(a.alpha);
             if (i >= nvec) break;
@@ -469,7 +619,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 for (int h = 0; h < H; ++h) to[j][h] = __fmul2_rn(to[j][h], v[h]);
             }
             if (a.gates && gate_row >= 0) {
-                unpack2<T>(ld_after(static_cast<const uint4*>(a.gate) + gate_row * nvec + i), v);
+                unpack2<T>(from_global(a.gate, gate_row, j, t), v);
 #pragma unroll
                 for (int h = 0; h < H; ++h) to[j][h] = __fmul2_rn(to[j][h], v[h]);
             }
@@ -497,26 +647,39 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
 #pragma unroll
             for (int h = 0; h < H; ++h) acc[j][h] = f2(0.f);
     };
-    // the groups' sums of a gradient, added in their order, to a partial row `out` or, whole, to `out_t`
-    auto flush = [&](float2 (&acc)[VPT][H], float* out, void* out_t) {
+    // the groups' sums of a gradient, added in their order, to a partial row `out` or, whole, to row `out_row` of `out_t`
+    auto put_sums = [&](const float2 (&v)[H], int j, int t, float* out, void* out_t, int64_t out_row) {
+        if (out_t) {
+            to_global(out_t, out_row, j, t, pack2x<T>(v));
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            if constexpr (ELEM) {
+                const int at = t + (j * VE + 2 * h) * ELEMS;
+                if (at < a.cols) out[at] = v[h].x;
+                if (at + ELEMS < a.cols) out[at + ELEMS] = v[h].y;
+            } else {
+                reinterpret_cast<float2*>(out)[(j * threads + t) * H + h] = v[h];
+            }
+        }
+    };
+    auto flush = [&](float2 (&acc)[VPT][H], float* out, void* out_t, int64_t out_row) {
         // (the ring may be in use: its own place, before the ring)
         float* place = reinterpret_cast<float*>(smem + 2 * size_t(nvec) * 16);
         if (g.groups == 1) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int i = j * g.threads + t;
+                const int i = j * threads + t;
                 if (i >= nvec) break;
-                if (out_t) st_v4(static_cast<uint4*>(out_t) + i, pack2x<T>(acc[j]));
-                else
-#pragma unroll
-                    for (int h = 0; h < H; ++h) reinterpret_cast<float2*>(out)[i * H + h] = acc[j][h];
+                put_sums(acc[j], j, t, out, out_t, out_row);
             }
         } else {
             for (int k = 0; k < g.groups; ++k) {
                 if (group == k) {
 #pragma unroll
                     for (int j = 0; j < VPT; ++j) {
-                        const int i = j * g.threads + t;
+                        const int i = j * threads + t;
                         if (i >= nvec) break;
 #pragma unroll
                         for (int h = 0; h < H; ++h) {
@@ -531,10 +694,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 float2 v[H];
 #pragma unroll
                 for (int h = 0; h < H; ++h) v[h] = reinterpret_cast<float2*>(place)[h * nvec + i];
-                if (out_t) st_v4(static_cast<uint4*>(out_t) + i, pack2x<T>(v));
-                else
-#pragma unroll
-                    for (int h = 0; h < H; ++h) reinterpret_cast<float2*>(out)[i * H + h] = v[h];
+                put_sums(v, i / threads, i % threads, out, out_t, out_row);
             }
             __syncthreads();
         }
@@ -559,10 +719,15 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
         if (mine > 0) {
             auto rows = [&](auto full_rows) {
             constexpr bool FULL = decltype(full_rows)::value;  // all ROWS of them
-            const uint4* const from =
-                reinterpret_cast<const uint4*>(smem + g.ring_at + size_t(slot) * g.slot_bytes + group * ROWS * row_bytes) + t;
-            const uint32_t step = g.tensor_bytes / 16;
-            const int64_t r = walk.r + group * ROWS, at = r * nvec + t;
+            const unsigned char* const from = smem + g.ring_at + size_t(slot) * g.slot_bytes +
+                                              (ELEM ? int(walk.r * row_bytes & 15) : 0) + group * ROWS * row_bytes;
+            const int64_t r = walk.r + group * ROWS;
+            // vector or share j of this thread of the group's row k of a tensor
+            auto in_slot = [&](int tensor, int k, int j) {
+                const unsigned char* row = from + tensor * g.tensor_bytes + k * row_bytes;
+                if constexpr (ELEM) return gather([&](int at) { return reinterpret_cast<const bits*>(row)[at]; }, j, t);
+                else return reinterpret_cast<const uint4*>(row)[j * threads + t];
+            };
             if (by_row) load_scale(r, true, scale);  // (one row at once)
             uint4 dyr[ROWS][VPT], fr[ROWS][VPT], yr[ROWS][VPT];
             float2 big[ROWS][VPT][H];  // dh*w_pre, then dx*scale
@@ -578,14 +743,14 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 float2 sum = f2(0.f);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
-                    const int i = j * g.threads;
+                    const int i = j * threads;
                     if ((!FAST && i + t >= nvec) || !(FULL || k < mine)) break;
-                    if (has_dy) dyr[k][j] = from[step + k * nvec + i];
-                    fr[k][j] = from[2 * step + k * nvec + i];
+                    if (has_dy) dyr[k][j] = in_slot(1, k, j);
+                    fr[k][j] = in_slot(2, k, j);
                     if (has_dh) {
-                        yr[k][j] = from[3 * step + k * nvec + i];
+                        yr[k][j] = in_slot(3, k, j);
                         float2 dh[H], y[H], w[H];
-                        unpack2<T>(from[k * nvec + i], dh);
+                        unpack2<T>(in_slot(0, k, j), dh);
                         unpack2<T>(yr[k][j], y);
                         unpack2<T>(weights[i + t], w);
 #pragma unroll
@@ -598,18 +763,18 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 }
                 s[k] = sum.x + sum.y;
             }
-            if (has_dh) group_sums<ROWS>(s, sums[0][phase], group, warps, g.threads);
-            else if (warps > 1) named_barrier(kBlockBar + group, g.threads);
+            if (has_dh) group_sums<ROWS>(s, sums[0][phase], group, warps, threads);
+            else if (warps > 1) named_barrier(kBlockBar + group, threads);
             else __syncwarp();
             if (t == 0) mbar_arrive(&empty[slot]);  // (every thread of the group has read its part)
-            if (threadIdx.x == 0 && begun && !ask.next(a, g, smem, full, empty, row_bytes, pol)) bad = true;
+            if (threadIdx.x == 0 && begun && !ask.next(a, g, smem, full, empty, row_bytes, pol, ELEM)) bad = true;
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
                 const float c2 = r2[k] * r2[k] * r2[k] * (s[k] * inv);
                 float2 sum = f2(0.f);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
-                    const int i = j * g.threads;
+                    const int i = j * threads;
                     if ((!FAST && i + t >= nvec) || !(FULL || k < mine)) break;
                     float2 d[H], f[H];
 #pragma unroll
@@ -623,7 +788,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                         for (int h = 0; h < H; ++h)
                             d[h] = __ffma2_rn(y[h], f2(-c2), __ffma2_rn(f2(r2[k]), big[k][j][h], d[h]));
                     }
-                    st_v4(static_cast<uint4*>(a.dx) + at + k * nvec + i, pack2x<T>(d));
+                    to_global(a.dx, r + k, j, t, pack2x<T>(d));
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         big[k][j][h] = __fmul2_rn(d[h], scale[j][h]);
@@ -638,16 +803,16 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 close_gate(r);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j)
-                    if (j * g.threads + t < nvec && a.dgate)
-                        st_v4(static_cast<uint4*>(a.dgate) + at + j * g.threads, pack2x<T>(sum_unit[j]));
+                    if (j * threads + t < nvec && a.dgate)
+                        to_global(a.dgate, r, j, t, pack2x<T>(sum_unit[j]));
             }
-            if (post) group_sums<ROWS>(s, sums[1][phase], group, warps, g.threads);
+            if (post) group_sums<ROWS>(s, sums[1][phase], group, warps, threads);
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
                 const float c1 = r1[k] * r1[k] * r1[k] * (s[k] * inv);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
-                    const int i = j * g.threads;
+                    const int i = j * threads;
                     if ((!FAST && i + t >= nvec) || !(FULL || k < mine)) break;
                     if (post) {
                         float2 f[H];
@@ -656,7 +821,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                         for (int h = 0; h < H; ++h)
                             big[k][j][h] = __ffma2_rn(f2(r1[k]), big[k][j][h], __fmul2_rn(f[h], f2(-c1)));
                     }
-                    st_v4(static_cast<uint4*>(a.df) + at + k * nvec + i, pack2x<T>(big[k][j]));
+                    to_global(a.df, r + k, j, t, pack2x<T>(big[k][j]));
                 }
             }
             };
@@ -670,8 +835,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             const bool begins = first == gate_row * a.per_gate.d, ends = walk.r + walk.count == walk.gate_end;
             close_gate(gate_row);
             if (a.dgate)
-                flush(sum_unit, part_row(a, begins ? 3 : 2, blockIdx.x),
-                      begins && ends ? static_cast<uint4*>(a.dgate) + gate_row * nvec : nullptr);
+                flush(sum_unit, part_row(a, begins ? 3 : 2, blockIdx.x), begins && ends ? a.dgate : nullptr, gate_row);
             else clear(sum_unit);
             first = walk.r + walk.count;
             ++gate_row;
@@ -679,8 +843,8 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
     }
     if (!by_gate && !by_row) close_gate(gate_row);
     __syncthreads();
-    if (a.dw_post) flush(sum_post, part_row(a, 0, blockIdx.x), nullptr);
-    if (a.dw_pre) flush(sum_pre, part_row(a, 1, blockIdx.x), nullptr);
+    if (a.dw_post) flush(sum_post, part_row(a, 0, blockIdx.x), nullptr, 0);
+    if (a.dw_pre) flush(sum_pre, part_row(a, 1, blockIdx.x), nullptr, 0);
     if (bad) s_bad = 1;
     __syncthreads();
     if (threadIdx.x == 0 && s_bad) {
@@ -785,14 +949,20 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-// The ring for `tensors` tensors, groups taking `rows` rows at once, behind `before` bytes; false: no room for two slots.
-inline bool block_ring(BlockArgs& a, BlockRing& g, const DevInfo* dev, int nvec, int vpt, int rows, int tensors, uint32_t before) {
+// The ring for four tensors, groups taking `rows` rows at once, behind the weights and the place where the groups' sums
+// are added; false: no room for two slots.
+template <typename T>
+bool block_ring(BlockArgs& a, BlockRing& g, const DevInfo* dev, int vpt, int rows, bool elem) {
+    const int nvec = (a.cols + kVec<T> - 1) / kVec<T>;
     g.threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
+    if (elem) g.threads = g.threads <= 32 ? 32 : g.threads <= 128 ? 128 : kBlockConsumers;
     g.groups = std::min(kBlockConsumers / g.threads, 14);  // (named barriers)
     g.rows = g.groups * rows;
-    g.tensor_bytes = uint32_t(g.rows) * uint32_t(nvec) * 16;
-    g.slot_bytes = uint32_t(tensors) * g.tensor_bytes;
-    g.ring_at = (before + 127) / 128 * 128;
+    g.tensor_bytes = uint32_t(g.rows) * uint32_t(a.cols) * uint32_t(sizeof(T));
+    if (elem) g.tensor_bytes = (g.tensor_bytes + 15) / 16 * 16 + 16;  // rounded outwards at both ends
+    g.slot_bytes = 4 * g.tensor_bytes;
+    const int shares = elem ? vpt * g.threads : nvec;
+    g.ring_at = (uint32_t(shares) * (32 + kVec<T> * 4) + 127) / 128 * 128;
     g.slots = std::min((dev->max_smem_optin - 2048 - int(g.ring_at)) / int(g.slot_bytes), kBlockSlots);
     return g.slots >= 2;
 }
@@ -805,18 +975,25 @@ inline nrm_status block_ring_launch(const void* fn, BlockArgs& a, BlockRing& g, 
     return launch_pdl(fn, dim3(unsigned(a.chunks)), dim3(unsigned(g.groups * g.threads)), p, s, smem);
 }
 
+// Rows to a CTA: about 16, such that the CTAs come to whole waves (a wave of 3.4 costs as much as one of 4).
+inline nrm_status block_fwd_launch(const void* fn, BlockArgs& a, const DevInfo* dev, int threads, cudaStream_t s) {
+    const int64_t resident = int64_t(dev->sms) * std::max(1, cached_occupancy(fn, threads, 0));
+    const int64_t waves = (a.rows + 16 * resident - 1) / (16 * resident);
+    int per = int((a.rows + waves * resident - 1) / (waves * resident));
+    void* p[] = {&a, &per};
+    return launch_pdl(fn, dim3(unsigned((a.rows + per - 1) / per)), dim3(unsigned(threads)), p, s);
+}
+template <typename T, int THREADS, int CTAS>
+nrm_status block_fwd_elem(BlockArgs& a, const DevInfo* dev, cudaStream_t s) {
+    return block_fwd_launch(reinterpret_cast<const void*>(&block_fwd_elem_kernel<T, THREADS, CTAS>), a, dev, THREADS, s);
+}
 template <typename T, int VPT, int DEPTH, int MOST, int CTAS>
 nrm_status block_fwd_vec(BlockArgs& a, const DevInfo* dev, cudaStream_t s) {
     const int nvec = a.cols / kVec<T>, block = ((nvec + VPT - 1) / VPT + 31) / 32 * 32;
     const void* fn = nvec == VPT * block && a.post && a.h
                          ? reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, DEPTH, MOST, CTAS, true>)
                          : reinterpret_cast<const void*>(&block_fwd_vec_kernel<T, VPT, DEPTH, MOST, CTAS, false>);
-    // rows to a CTA: about 16, such that the CTAs come to whole waves (a wave of 3.4 costs as much as one of 4)
-    const int64_t resident = int64_t(dev->sms) * std::max(1, cached_occupancy(fn, block, 0));
-    const int64_t waves = (a.rows + 16 * resident - 1) / (16 * resident);
-    int per = int((a.rows + waves * resident - 1) / (waves * resident));
-    void* p[] = {&a, &per};
-    return launch_pdl(fn, dim3(unsigned((a.rows + per - 1) / per)), dim3(unsigned(block)), p, s);
+    return block_fwd_launch(fn, a, dev, block, s);
 }
 
 template <typename T>
@@ -842,13 +1019,22 @@ nrm_status block_norm_fwd(const BlockArgs& args, bool vec, cudaStream_t s) {
         if (nvec <= 512) return block_fwd_vec<T, 2, 3, 256, 2>(a, dev, s);
         return nvec <= 1024 ? block_fwd_vec<T, 2, 2, 512, 1>(a, dev, s) : block_fwd_vec<T, 4, 1, 512, 1>(a, dev, s);
     }
+    if (a.cols <= 1024 * kBlockElems && a.rows < (int64_t(1) << 31)) {
+        const int threads = (a.cols + kBlockElems - 1) / kBlockElems;
+        return threads <= 32    ? block_fwd_elem<T, 32, 24>(a, dev, s)
+               : threads <= 64  ? block_fwd_elem<T, 64, 16>(a, dev, s)
+               : threads <= 128 ? block_fwd_elem<T, 128, 8>(a, dev, s)
+               : threads <= 256 ? block_fwd_elem<T, 256, 4>(a, dev, s)
+               : threads <= 512 ? block_fwd_elem<T, 512, 2>(a, dev, s)
+                                : block_fwd_elem<T, 1024, 1>(a, dev, s);
+    }
     void* p[] = {&a};
     return launch_pdl(reinterpret_cast<const void*>(&block_fwd_scalar_kernel<T>),
                       dim3(unsigned(std::min<int64_t>(a.rows, int64_t(dev->sms) * 64))), dim3(kBlockThreads), p, s);
 }
 
 template <typename T>
-nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
+nrm_status block_norm_bwd(const BlockArgs& args, bool vec, bool copies, cudaStream_t s) {
     BlockArgs a = args;
     const DevInfo* dev = dev_info();
     if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
@@ -866,27 +1052,30 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, cudaStream_t s) {
     void* p[] = {&a};
     nrm_status st;
     bool sums = a.dgate || a.dw_post || a.dw_pre;
-    const int nvec = a.cols / kVec<T>;
+    const int nvec = (a.cols + kVec<T> - 1) / kVec<T>;
     bool ringed = false;
-    if (vec && nvec <= 2 * kBlockConsumers) {
+    if ((vec || copies) && nvec <= 2 * kBlockConsumers) {
+        static_assert(kBlockConsumers == 512);
         BlockRing g{};
-        const bool by_row = a.gates > 0 && a.per_gate.d == 1;
+        const bool by_row = a.gates > 0 && a.per_gate.d == 1, elem = !vec;
         const int vpt = nvec > kBlockConsumers ? 2 : 1;
-        // the weights, and the place where the groups' sums are added
-        const uint32_t before = uint32_t(nvec) * 32 + uint32_t(a.cols) * 4;
         // two rows of a group at once, for their waits to overlap, where the registers allow
-        if (vpt == 1 && !by_row && block_ring(a, g, dev, nvec, 1, 2, 4, before)) {
-            ringed = true;
-            const bool fast = nvec == g.threads && a.dh && a.dy && a.post;
-            st = block_ring_launch(fast ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, true>)
-                                        : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false>),
-                                   a, g, dev, s);
-        } else if (block_ring(a, g, dev, nvec, vpt, 1, 4, before)) {
-            ringed = true;
-            st = block_ring_launch(vpt == 1 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false>)
-                                            : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false>),
-                                   a, g, dev, s);
-        }
+        const bool two = vpt == 1 && !by_row && block_ring<T>(a, g, dev, 1, 2, elem);
+        ringed = two || block_ring<T>(a, g, dev, vpt, 1, elem);
+        const bool fast = vec && nvec == g.threads && a.dh && a.dy && a.post;
+        const void* fn = two && fast ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, true>)
+                         : two       ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false>)
+                         : vpt == 1  ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false>)
+                                     : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false>);
+        if (elem)
+            fn = two && g.threads == 32    ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 32>)
+                 : two && g.threads == 128 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 128>)
+                 : two                     ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 512>)
+                 : g.threads == 32         ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 32>)
+                 : g.threads == 128        ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 128>)
+                 : vpt == 1                ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 512>)
+                                           : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false, 512>);
+        if (ringed) st = block_ring_launch(fn, a, g, dev, s);
         if (ringed) {
             if (by_row) a.dgate = nullptr;  // done with
             sums = a.dgate || a.dw_post || a.dw_pre;

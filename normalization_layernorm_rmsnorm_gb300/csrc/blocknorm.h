@@ -42,6 +42,7 @@ inline int block_max_chunks(const DevInfo& d) { return 2 * d.sms; }
 
 // `vec`: rows are whole 16-byte vectors at 16-byte aligned addresses.
 template <typename T> nrm_status block_norm_fwd(const BlockArgs& a, bool vec, cudaStream_t s);
-template <typename T> nrm_status block_norm_bwd(const BlockArgs& a, bool vec, cudaStream_t s);
+// `copies`: dh, dy, f and y are at 16-byte aligned addresses.
+template <typename T> nrm_status block_norm_bwd(const BlockArgs& a, bool vec, bool copies, cudaStream_t s);
 
 }  // namespace nrm

@@ -161,8 +161,9 @@ nrm_status nrm_block_norm_bwd(const void* dh, const void* dy, const void* f, con
         a.post = post != 0;
         a.chunks = block_chunks(*dev, rows);
         const bool vec = whole_vectors({dh, dy, f, y, gate, w_post, w_pre, dx, df, dgate}, cols, dt);
+        const bool copies = aligned(dh, 16) && aligned(dy, 16) && aligned(f, 16) && aligned(y, 16);
         return by_dtype(dt, [&](auto tag) {
-            return block_norm_bwd<decltype(tag)>(a, vec, reinterpret_cast<cudaStream_t>(stream));
+            return block_norm_bwd<decltype(tag)>(a, vec, copies, reinterpret_cast<cudaStream_t>(stream));
         });
     });
 }
