@@ -269,6 +269,62 @@ __global__ void __launch_bounds__(kEvictThreads) evict_choose_kernel(const Evict
     if (ctas > 1) cluster_sync_all();  // the others may still read this CTA's counts
 }
 
+// Few positions: a CTA for each head of each sequence counts for every position those that come before it in weight.
+// (180 sequences of 2 positions, 12 heads, with the copy and the read back: 30 us with the kernel above.)
+constexpr int kSmallThreads = 128, kSmallMost = 2 * kSmallThreads;
+__global__ void __launch_bounds__(kSmallThreads) evict_choose_small_kernel(const EvictArgs a) {
+    __shared__ __align__(16) uint32_t keys[kSmallMost];  // 0: not between, which no weight's is
+    __shared__ uint32_t of_warp[32];
+    pdl_next();
+    const int64_t which = blockIdx.x, s = which / a.heads;
+    const int head = int(which - s * a.heads), t = int(threadIdx.x), lane = t & 31, warp = t >> 5;
+    int64_t length = ld_after(a.lengths + s);
+    if (length < 0 || length > a.cap) {
+        if (t == 0) atomicOr(a.err, kErrCacheSlot);
+        length = length < 0 ? 0 : a.cap;
+    }
+    const int n = int(length);
+    if (head == 0 && t == 0) a.new_lengths[s] = n < a.keep ? n : a.keep;
+    int64_t* kept = a.kept + which * a.keep;
+    if (n <= a.keep) {
+        for (int64_t i = t; i < a.keep; i += kSmallThreads) kept[i] = i < n ? i : -1;
+        return;
+    }
+    const float* weights = a.weights + s * a.weight_ts + head * a.weight_hs;
+    const int from = int(a.first), to = n - int(a.recent);
+    if (t < 32) of_warp[t] = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = t + j * kSmallThreads;
+        keys[i] = i >= from && i < to ? weight_key(ld_after(weights + i)) : 0u;
+    }
+    __syncthreads();
+    // this thread's two neighbouring positions
+    const uint32_t want = uint32_t(a.keep - a.first - a.recent), mine[2] = {keys[2 * t], keys[2 * t + 1]};
+    uint32_t rank[2] = {};
+    for (int j = 0; j < to; j += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(keys + j);
+        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) rank[m] += k[u] > mine[m] || (k[u] == mine[m] && j + u < 2 * t + m);
+    }
+    uint32_t stays[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int i = 2 * t + m;
+        stays[m] = i < n && (i < from || i >= to || rank[m] < want);
+    }
+    uint32_t all;
+    uint32_t at = warp_before(stays[0] + stays[1], &all);
+    if (lane == 0) of_warp[warp] = all;
+    __syncthreads();
+    at += __reduce_add_sync(0xffffffffu, lane < warp ? of_warp[lane] : 0);
+    if (stays[0]) kept[at] = 2 * t;
+    if (stays[1]) kept[at + stays[0]] = 2 * t + 1;
+}
+
 // Which row a lane copies: row r of the shortened sequences, head innermost.
 struct CopyDiv {
     RowDiv heads, keep;
@@ -375,6 +431,10 @@ __global__ void __launch_bounds__(kCopyThreads, 3) evict_copy_kernel(const Evict
 
 nrm_status choose(EvictArgs& a, const DevInfo* dev, cudaStream_t s) {
     const int64_t pairs = a.sequences * a.heads;
+    if (a.cap <= kSmallMost && pairs < (int64_t(1) << 31)) {
+        void* p[] = {&a};
+        return launch_pdl(reinterpret_cast<const void*>(&evict_choose_small_kernel), dim3(unsigned(pairs)), dim3(kSmallThreads), p, s);
+    }
     // CTAs to a head: as its positions are worth, while the GPU has room
     int ctas = 1;
     while (ctas < kEvictCluster && a.cap > int64_t(ctas) * kEvictPart && pairs * ctas * 2 <= 2 * int64_t(dev->sms)) ctas *= 2;

@@ -75,6 +75,8 @@ class Evict:
     ([100], 40, 0, 0), ([100], 40, 4, 10), ([100], 40, 40, 0), ([100], 40, 0, 40), ([100], 40, 17, 23), ([100], 1, 0, 0),
     ([100], 1, 1, 0), ([100], 99, 0, 0), ([100], 100, 3, 3), ([0, 1, 39, 40, 41, 3000], 40, 2, 5), ([5000], 2500, 4, 100),
     ([1025, 1024, 2049], 1024, 0, 1), ([33], 32, 0, 0),
+    # on both sides of what a CTA ranks at once
+    ([256, 0, 255, 3], 128, 3, 60), ([257, 256, 2], 129, 3, 60), ([2, 1, 0], 1, 0, 0), ([256], 255, 0, 0), ([256], 1, 0, 0),
 ])
 def test_against_the_reference(lengths, keep, first, recent):
     Evict(lengths, keep, first=first, recent=recent).check()
