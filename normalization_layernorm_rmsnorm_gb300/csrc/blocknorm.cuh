@@ -424,6 +424,7 @@ struct BlockRing {
     int groups, threads;     // groups of threads to a CTA; threads of a group, whole warps
     int rows;                // of a slot: groups times the rows that a group takes at once
     int slots;
+    int places;              // for the groups' sums
     uint32_t tensor_bytes;   // of a tensor's rows in a slot
     uint32_t slot_bytes;
     uint32_t ring_at;        // after the weights
@@ -675,26 +676,30 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
                 put_sums(acc[j], j, t, out, out_t, out_row);
             }
         } else {
-            for (int k = 0; k < g.groups; ++k) {
-                if (group == k) {
+            // (more than one group: a thread has one vector or share)  In as many turns as the places need, the sum so far
+            // in the first.
+            float2* const all = reinterpret_cast<float2*>(place);
+            for (int k0 = 0; k0 < g.groups;) {
+                const int at = k0 > 0, n = min(g.groups - k0, g.places - at);
+                if (group >= k0 && group < k0 + n) {
 #pragma unroll
-                    for (int j = 0; j < VPT; ++j) {
-                        const int i = j * threads + t;
-                        if (i >= nvec) break;
-#pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            float2* p = reinterpret_cast<float2*>(place) + h * nvec + i;
-                            *p = k == 0 ? acc[j][h] : __fadd2_rn(*p, acc[j][h]);
-                        }
-                    }
+                    for (int h = 0; h < H; ++h) all[((at + group - k0) * H + h) * threads + t] = acc[0][h];
                 }
                 __syncthreads();
+                for (int i = int(threadIdx.x); i < H * threads; i += int(blockDim.x)) {
+                    float2 v = all[i];
+#pragma unroll 4
+                    for (int k = 1; k < at + n; ++k) v = __fadd2_rn(v, all[k * H * threads + i]);
+                    all[i] = v;
+                }
+                __syncthreads();
+                k0 += n;
             }
             for (int i = int(threadIdx.x); i < nvec; i += int(blockDim.x)) {
                 float2 v[H];
 #pragma unroll
-                for (int h = 0; h < H; ++h) v[h] = reinterpret_cast<float2*>(place)[h * nvec + i];
-                put_sums(v, i / threads, i % threads, out, out_t, out_row);
+                for (int h = 0; h < H; ++h) v[h] = all[h * threads + i];
+                put_sums(v, 0, i, out, out_t, out_row);
             }
             __syncthreads();
         }
@@ -952,7 +957,7 @@ __global__ void __launch_bounds__(kBlockSumWarps * 32) block_sum_kernel(const Bl
 // The ring for four tensors, groups taking `rows` rows at once, behind the weights and the place where the groups' sums
 // are added; false: no room for two slots.
 template <typename T>
-bool block_ring(BlockArgs& a, BlockRing& g, const DevInfo* dev, int vpt, int rows, bool elem) {
+bool block_ring(BlockArgs& a, BlockRing& g, const DevInfo* dev, int vpt, int rows, bool elem, int room) {
     const int nvec = (a.cols + kVec<T> - 1) / kVec<T>;
     g.threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
     if (elem) g.threads = g.threads <= 32 ? 32 : g.threads <= 128 ? 128 : kBlockConsumers;
@@ -961,13 +966,19 @@ bool block_ring(BlockArgs& a, BlockRing& g, const DevInfo* dev, int vpt, int row
     g.tensor_bytes = uint32_t(g.rows) * uint32_t(a.cols) * uint32_t(sizeof(T));
     if (elem) g.tensor_bytes = (g.tensor_bytes + 15) / 16 * 16 + 16;  // rounded outwards at both ends
     g.slot_bytes = 4 * g.tensor_bytes;
+    // the groups' sums at once, or of a few large ones three and then the others (5 groups of 96 threads: 79 us, all at
+    // once, which leaves the L1 cache less, 82; 14 of 32: 34, all at once 32)
+    g.places = g.groups > 7 ? g.groups : g.groups > 1 ? std::min(g.groups, 3) : 0;
     const int shares = elem ? vpt * g.threads : nvec;
-    g.ring_at = (uint32_t(shares) * (32 + kVec<T> * 4) + 127) / 128 * 128;
-    g.slots = std::min((dev->max_smem_optin - 2048 - int(g.ring_at)) / int(g.slot_bytes), kBlockSlots);
+    g.ring_at = (uint32_t(shares) * 32 + uint32_t(g.places * g.threads) * kVec<T> * 4 + 127) / 128 * 128;
+    const int least = int(g.ring_at + 2 * g.slot_bytes), most = dev->max_smem_optin - 2048;
+    g.slots = std::min((std::min(most, std::max(room, least)) - int(g.ring_at)) / int(g.slot_bytes), kBlockSlots);
     return g.slots >= 2;
 }
 inline nrm_status block_ring_launch(const void* fn, BlockArgs& a, BlockRing& g, const DevInfo* dev, cudaStream_t s) {
-    a.chunks = std::min<int64_t>(dev->sms, (a.rows + g.rows - 1) / g.rows);
+    // few rows are spread over the GPU, two to a CTA (390 rows of 80, each three with a gate of their own: 22 us; with all
+    // the rows of a slot to a CTA 83)
+    a.chunks = std::min<int64_t>(dev->sms, (a.rows + 1) / 2);
     const size_t smem = g.ring_at + size_t(g.slots) * g.slot_bytes;
     nrm_status st = prepare_kernel(fn, smem, false);
     if (st != NRM_OK) return st;
@@ -1060,21 +1071,32 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, bool copies, cudaStre
         const bool by_row = a.gates > 0 && a.per_gate.d == 1, elem = !vec;
         const int vpt = nvec > kBlockConsumers ? 2 : 1;
         // two rows of a group at once, for their waits to overlap, where the registers allow
-        const bool two = vpt == 1 && !by_row && block_ring<T>(a, g, dev, 1, 2, elem);
-        ringed = two || block_ring<T>(a, g, dev, vpt, 1, elem);
-        const bool fast = vec && nvec == g.threads && a.dh && a.dy && a.post;
-        const void* fn = two && fast ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, true>)
-                         : two       ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false>)
-                         : vpt == 1  ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false>)
-                                     : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false>);
-        if (elem)
-            fn = two && g.threads == 32    ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 32>)
-                 : two && g.threads == 128 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 128>)
-                 : two                     ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 512>)
-                 : g.threads == 32         ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 32>)
-                 : g.threads == 128        ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 128>)
-                 : vpt == 1                ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 512>)
-                                           : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false, 512>);
+        const bool all = vec && vpt == 1 && !by_row && nvec % 32 == 0 && a.dh && a.dy && a.post;
+        // Kernels with branches keep some of their state in local memory, whose cache is what shared memory leaves: theirs
+        // is bounded (16 bits, 8192 rows of 6144: 380 us without a bound, 350 with 195 KB, 289 with 163; float32, 17152 of
+        // 1878: 249 without, 226 with 195, 253 with 163).
+        const int room = all ? dev->max_smem_optin : (sizeof(T) == 2 ? 163 : 195) * 1024;
+        // Two rows of a group at once, for their waits to overlap, where the registers allow: in 16 bits only without
+        // branches or in groups of one warp (8192 rows of 4095: 243 us with, 203 without; 17168 of 192: 33 and 45).
+        const bool two = vpt == 1 && !by_row && (all || sizeof(T) == 4 || nvec <= 32) && block_ring<T>(a, g, dev, 1, 2, elem, room);
+        ringed = two || block_ring<T>(a, g, dev, vpt, 1, elem, room);
+        const void* fn;
+        if (elem) {
+            fn = two && g.threads == 32 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 32>)
+                 : g.threads == 32      ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 32>)
+                 : g.threads == 128     ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 128>)
+                 : vpt == 1             ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false, 512>)
+                                        : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false, 512>);
+            if constexpr (sizeof(T) == 4)
+                if (two && g.threads > 32)
+                    fn = g.threads == 128 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 128>)
+                                          : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false, 512>);
+        } else {
+            fn = two && all ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, true>)
+                 : two      ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 2, false>)
+                 : vpt == 1 ? reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 1, 1, false>)
+                            : reinterpret_cast<const void*>(&block_bwd_ring_kernel<T, 2, 1, false>);
+        }
         if (ringed) st = block_ring_launch(fn, a, g, dev, s);
         if (ringed) {
             if (by_row) a.dgate = nullptr;  // done with

@@ -332,3 +332,39 @@ def test_unaligned_gradients_alone(dtype, rows, gates):
     c.grads_at = 1
     c.check()
     nrm.nrm_sync_status()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,cols,gates", [
+    (61, 67, 0), (61, 67, 1), (60, 67, 60), (60, 250, 4), (40, 513, 2), (40, 1001, 40), (45, 1023, 3), (30, 2049, 1), (18, 4095, 2),
+    (18, 4097, 18), (10, 6001, 1), (10, 8191, 5), (6, 8193, 1), (300, 1001, 1), (3000, 131, 6), (390, 80, 130), (1, 1, 0), (1, 5, 1), (3, 2, 3),
+])
+def test_odd_rows_of_every_kernel(dtype, rows, cols, gates):
+    # rows that begin anywhere within 16 bytes, and tensors that end there
+    Block(dtype, rows, cols, gates).check()
+    nrm.nrm_sync_status()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_odd_rows_leave_what_lies_around_them(dtype):
+    # the copies are rounded outwards: neither inputs nor what lies before and behind the outputs may change, and
+    # what lies around the inputs may be anything
+    rows, cols = 29, 333
+    c = Block(dtype, rows, cols, 1)
+    y, _, r1, r2 = c.fwd()
+    want = c.bwd(y, r1, r2)
+
+    def inside(x, around):
+        b = torch.full((x.numel() + 32,), around, dtype=x.dtype, device="cuda")
+        b[16:16 + x.numel()].view(x.shape).copy_(x)
+        return b, b[16:16 + x.numel()].view(x.shape)
+
+    for name in ("x", "f", "dh", "dy"):
+        setattr(c, name, inside(getattr(c, name), float("nan"))[1])
+    y = inside(y, float("inf"))[1]
+    outs = [inside(t, 7.0) for t in want]
+    ws = nrm.block_norm_workspace(c.x, c.gate)
+    nrm.nrm_block_norm_bwd(c.dh, c.dy, c.f, y, c.gate, c.w_post, c.w_pre, r1, r2, *[v for _, v in outs], ws, c.alpha)
+    nrm.nrm_sync_status()
+    for (b, v), w in zip(outs, want):
+        assert same(v.contiguous(), w) and (b[:16] == 7).all() and (b[16 + w.numel():] == 7).all()
