@@ -426,7 +426,7 @@ constexpr int kBlockBar = 1;                         // the groups' named barrie
 struct BlockRing {
     int groups, threads;     // groups of threads to a CTA; threads of a group, whole warps
     int rows;                // of a slot: groups times the rows that a group takes at once
-    int slots;
+    int slots;               // two at least: rows are asked for a slot ahead of those that are worked on
     int places;              // for the groups' sums
     uint32_t tensor_bytes;   // of a tensor's rows in a slot
     uint32_t slot_bytes;
