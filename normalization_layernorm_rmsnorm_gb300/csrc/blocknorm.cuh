@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             }
             if (has_dh) group_sums<ROWS>(s, sums[0][phase], group, warps, threads);
             else if (warps > 1) named_barrier(kBlockBar + group, threads);
-            else __syncwarp();
+            if (warps == 1) __syncwarp();  // (a warp's sums are exchanges, which order no reads)
             if (t == 0) mbar_arrive(&empty[slot]);  // (every thread of the group has read its part)
             if (threadIdx.x == 0 && begun && !ask.next(a, g, smem, full, empty, row_bytes, pol, ELEM)) bad = true;
 #pragma unroll
