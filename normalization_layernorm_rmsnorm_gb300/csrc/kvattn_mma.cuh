@@ -503,7 +503,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
                 most = fmaxf(m[nt][i], most);
                 const float base = finite_max(most) - 8.f;  // p * 2^8, and so the sum
-                grow[nt][i] = exp2_approx(m[nt][i] - base - 8.f);
+                // from the maxima themselves: 1 where they are equal, whatever the 8 was rounded to
+                grow[nt][i] = exp2_approx(m[nt][i] - finite_max(most));
                 grows |= most > m[nt][i];
                 m[nt][i] = most;
                 float add = 0.f;
