@@ -634,14 +634,22 @@ typedef struct nrm_kv_weights {
  * and positions outside the window are left as they were.
  * scale: finite.  workspace: nrm_kv_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, clobbered; calls that overlap on the GPU need separate ones.
- * The sums are float32.  Their products are exact, or of factors with 22 bits;
- * but for bfloat16 outputs p_j, the value's scale and their product have 11 bits
- * each.  What of a query is below 2^-35 of its head's largest element, or of a
- * p_j times a value's scale below 2^-38 of the largest p_j times the largest such
- * scale of the sequence's head, may be lost.
- * d and group multiples of 16, with rows of codes of whole aligned 16-byte (or
- * 8-byte) vectors, take matrix instructions; other layouts run element by
- * element.
+ * Precision.  d and group multiples of 16, with rows of codes of whole aligned
+ * 16-byte (or 8-byte) vectors, take matrix instructions; other layouts run
+ * element by element, in float32 throughout.  With matrix instructions sums are
+ * float32, and their products have these factors:
+ *  - a code as it is;
+ *  - a query's element: exact in 16 bits, 22 bits in float32; either way what is
+ *    below 2^-39 of its head's largest element may be lost;
+ *  - p_j times its value's scale: a float32 product rounded to 22 bits, or, for
+ *    bfloat16 outputs, to 11; what is below 2^-50 (bfloat16: 2^-39) of the largest
+ *    p_j times the largest scale of that group of elements in the sequence may be
+ *    lost.  (The bound is the product's: small p_j alone, or small scales, keep
+ *    their bits.)
+ * Integers' codes are added with a bias of 128 (8 in 4 bits), which is taken off
+ * again, so roundings go by the codes plus that; and terms are cut off at 2^-15
+ * of a code's step times the largest query's element, or the largest p_j times
+ * scale, that they are added with.
  */
 NRM_API nrm_status nrm_kv_cache_attention(const nrm_heads *q, const nrm_kv_cache *cache,
                                   const nrm_kv_pages *pages, const nrm_heads *out, float scale,

@@ -3,21 +3,37 @@
 // Both products are m16n8k16 with fp16 factors and fp32 sums, the query heads of
 // a pair as the eight columns: logits = codes of 16 keys [16 x d] * queries [d x
 // 8], and out^T = codes of 16 values [d x 16] * weights [16 x 8].  A code is
-// exact in fp16 in every stored form (an integer is taken with a bias, which one more
-// product takes off again, as one of fp16's smallest numbers, so that it costs no
-// conversion); the keys' scales multiply the logits, the values' the weights.  Queries are scaled by a power of two to at most 2^15:
-// those of 16 bits then are exact, of float32 ones the rest is a second factor
-// (22 bits).  A weight is p*2^8 times its value's scale, the largest scale seen
-// brought below 2^6, all in fp16: 11 bits down to 2^-28 of the largest; where
-// the output has more (fp16, float32), p, the scale and their product each have a
-// second factor too.  The order of the d elements in a product is free, so a lane
-// takes its keys' elements as they lie in 8 (or 4) neighbours, and its values' in
-// 4 (or 2).
+// exact in fp16 in every stored form (an integer is taken with a bias, which one
+// more product takes off again, as one of fp16's smallest numbers, so that it costs
+// no conversion); the keys' scales multiply the logits, the values' the weights.
+// Queries are scaled by a power of two to at most 2^15: those of 16 bits then are
+// exact, of float32 ones the rest is a second factor (22 bits).
+//
+// An instruction lines its terms up by their factors' exponents and cuts them off
+// at 2^-25 of the largest (measured, term by term); fp16's smallest numbers go by
+// the exponent of 2^-14 that they are stored with.  A term with an integer's code
+// so ends at 2^-15 of a code's step times the other factor: for 8 bits 2^-22 of the
+// largest code, for the lower of two 4-bit codes 2^-18, for the upper, which is
+// taken 16 times as large, 2^-22.  (Shifting the lower up too would cost two
+// instructions for eight codes; the values themselves were rounded to half a step.)
+//
+// A weight is p times its value's scale, multiplied in float32 with the largest
+// scale seen brought below 2^15 and rounded to fp16: 11 bits down to 2^-28 of the
+// largest p times the largest scale, nothing below 2^-39.  (The bounds are the
+// product's alone: a p or a scale far below the largest keeps its bits as long as
+// the product does.)  bfloat16 outputs, whose significand has 8 bits, take that;
+// where the output has more (fp16, float32), what the rounding left off is a
+// second factor, 2^11 times as large, with a sum of its own in each tile: 22 bits
+// down to 2^-28, nothing below 2^-50.  (Two factors of one size end at one
+// place: below 2^-20 the second is 0.)
+//
+// The order of the d elements in a product is free, so a lane takes its keys'
+// elements as they lie in 8 (or 4) neighbours, and its values' in 4 (or 2).
 //
 // The columns' heads are the lanes' pairs in both results, so the running
 // maximum, the rescaling and the sum need nothing from other lanes but the
-// maximum over the positions; p changes from rows to columns by a transposing
-// exchange of 8x8 matrices.
+// maximum over the positions; weights change from rows to columns by a
+// transposing exchange of 8x8 matrices.
 //
 // Codes and scales are copied asynchronously into the warp's own ring in shared
 // memory, a tile of 32 positions at a time: its keys while the values before them are
@@ -122,13 +138,13 @@ struct AttnForm {
 };
 
 // A warp's shared memory: a tile's keys, values and scales of both, the places of a tile's rows, and its scales of each
-// unit, the values' in fp16.
+// unit.
 struct AttnSmem {
     uint32_t codes;            // keys, values
     uint32_t scales;           // [keys, values][32][groups]
     uint32_t places;           // [32] code offsets
     uint32_t k_scales;         // [units][32]
-    uint32_t v_scales;         // [factors][units][32]
+    uint32_t v_scales;         // [units][32], the largest brought below 2^15
     uint32_t bias;             // [units][heads]: what the codes' bias adds to a unit's products, negative
 };
 constexpr uint32_t kAttnPlaces = 32 * 8;
@@ -137,22 +153,10 @@ constexpr uint32_t kAttnPlaces = 32 * 8;
 template <typename F>
 constexpr int kAttnFormWarps = F::DMAX > 128 || F::NT > 1 ? 8 : kAttnWarps;
 template <typename T>
-constexpr int kAttnFactors = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;  // of p
-template <typename T, typename F>
+constexpr int kAttnFactors = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;  // of a weight
+template <typename F>
 __host__ __device__ constexpr uint32_t attn_warp_bytes(int groups) {
-    return F::S_AT + 2 * 32 * groups * 4 + kAttnPlaces + F::UNITS * 128 + kAttnFactors<T> * F::UNITS * 64 +
-           (F::BIAS ? F::UNITS * F::NT * 32 : 0);
-}
-
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
+    return F::S_AT + 2 * 32 * groups * 4 + kAttnPlaces + 2 * F::UNITS * 128 + (F::BIAS ? F::UNITS * F::NT * 32 : 0);
 }
 
 template <typename T, typename F>
@@ -359,7 +363,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         cp_async_wait<1>();  // the keys and the scales
         __syncwarp();
 
-        // the scales of this lane's position, of each unit, the values' in fp16; seldom one is larger than all before it
+        // the scales of this lane's position, of each unit; seldom a value's is larger than all before it
         {
             const uint32_t mine = sm.scales + (32 + lane) * groups * 4;
             float mine_of[F::UNITS];
@@ -376,7 +380,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                     if (!F::EXACT && u >= units) break;
                     const uint32_t b = __float_as_uint(mine_of[u]) & 0x7fffffffu;
                     const uint32_t most = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
-                    const int now = min(127, max(max(top[u], -100), int(most >> 23) - 126));
+                    const int now = max(max(top[u], -100), int(most >> 23) - 126);
                     const float raise = exp2f(float(max(top[u] - now, -126)));
                     top[u] = now;
 #pragma unroll
@@ -390,11 +394,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
-                const float s = mine_of[u] * __uint_as_float(uint32_t(127 + 6 - top[u]) << 23);
-                const __half hi = __float2half_rn(s);
-                in_ring<__half>(sm.v_scales + (u * 32 + lane) * 2) = hi;
-                if constexpr (WT == 2)
-                    in_ring<__half>(sm.v_scales + ((F::UNITS + u) * 32 + lane) * 2) = __float2half_rn(s - __half2float(hi));
+                in_ring<float>(sm.v_scales + (u * 32 + lane) * 4) = mine_of[u] * __uint_as_float(uint32_t(127 + 15 - top[u]) << 23);
                 in_ring<float>(sm.k_scales + (u * 32 + lane) * 4) = in_ring<const float>(mine - 32 * groups * 4 + of_unit[u]);
             }
             __syncwarp();
@@ -468,7 +468,6 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         cp_async_commit();
 
         float grow[NT][2];
-        uint32_t w[2][NT][WT][2];  // p as columns
         bool grows = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -502,9 +501,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 8));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 16));
                 most = fmaxf(m[nt][i], most);
-                const float base = finite_max(most) - 8.f;  // p * 2^8, and so the sum
-                // from the maxima themselves: 1 where they are equal, whatever the 8 was rounded to
-                grow[nt][i] = exp2_approx(m[nt][i] - finite_max(most));
+                const float base = finite_max(most);
+                grow[nt][i] = exp2_approx(m[nt][i] - base);  // (1 where they are equal: of both sums or neither)
                 grows |= most > m[nt][i];
                 m[nt][i] = most;
                 float add = 0.f;
@@ -516,18 +514,6 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 }
                 sum[nt][i] = fmaf(sum[nt][i], grow[nt][i], add);
             }
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float x = l[half][nt][2 * r], y = l[half][nt][2 * r + 1];
-                    const uint32_t hi = half2_bits(x, y);
-                    w[half][nt][0][r] = transpose8(hi);
-                    if constexpr (WT == 2) {
-                        const float2 f = half2_floats(hi);
-                        w[half][nt][WT - 1][r] = transpose8(half2_bits(x - f.x, y - f.y));
-                    }
-                }
         }
         if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
@@ -549,21 +535,19 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
-                // p times the scales of positions 2 tid and 2 tid + 1, and of 8 further
+                // the weights of positions gid and gid + 8, as columns those of 2 tid and 2 tid + 1, and of 8 further
                 uint32_t b[NT][WT][2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint32_t of = sm.v_scales + (u * 32 + 16 * half + 8 * r + 2 * tid) * 2;
-                    const uint32_t hi = in_ring<const uint32_t>(of);
+                    const float s = in_ring<const float>(sm.v_scales + (u * 32 + 16 * half + 8 * r + gid) * 4);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) b[nt][0][r] = mul_half2(w[half][nt][0][r], hi);
-                    if constexpr (WT == 2) {
-                        // what the product lost, and the products with the second factors
-                        const uint32_t lo = in_ring<const uint32_t>(of + F::UNITS * 64);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t lost = fma_half2(w[half][nt][0][r], hi, b[nt][0][r] ^ 0x80008000u);
-                            b[nt][WT - 1][r] = fma_half2(w[half][nt][0][r], lo, fma_half2(w[half][nt][WT - 1][r], hi, lost));
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float x = l[half][nt][2 * r] * s, y = l[half][nt][2 * r + 1] * s;
+                        const uint32_t hi = half2_bits(x, y);
+                        b[nt][0][r] = transpose8(hi);
+                        if constexpr (WT == 2) {
+                            const float2 f = half2_floats(hi);
+                            b[nt][WT - 1][r] = transpose8(half2_bits((x - f.x) * 0x1p11f, (y - f.y) * 0x1p11f));
                         }
                     }
                 }
@@ -614,12 +598,18 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < WT; ++k) {
-                            mma16816(acc[u][t][nt], f[t], b[nt][k][0], b[nt][k][1]);
+                            float second[4] = {};
+                            float(&to)[4] = k == 0 ? acc[u][t][nt] : second;
+                            mma16816(to, f[t], b[nt][k][0], b[nt][k][1]);
                             if constexpr (F::BIAS != 0) {
                                 // less the bias (0x8008: -8 * 2^-24)
                                 constexpr uint32_t once = F::BITS == 4 ? 0x80088008u : 0x80808080u, next = 0x80808080u;
                                 const uint32_t less[4] = {once, next, once, next};
-                                mma16816(acc[u][t][nt], less, b[nt][k][0], b[nt][k][1]);
+                                mma16816(to, less, b[nt][k][0], b[nt][k][1]);
+                            }
+                            if (k == 1) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) acc[u][t][nt][i] = fmaf(second[i], 0x1p-11f, acc[u][t][nt][i]);
                             }
                         }
             }
@@ -641,7 +631,6 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             s += __shfl_xor_sync(0xffffffffu, s, 4);
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
-            s *= 0x1p-8f;
             const int h = nt * 8 + tid * 2 + i;
             if (h >= p.heads) continue;
             const float scale = p.whole ? (s == 0.f ? 0.f : 1.f / s) : 1.f;
@@ -650,14 +639,14 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
-                const float d0 = __uint_as_float(uint32_t(127 + top[u]) << 23) * scale;
+                const float unit = __uint_as_float(uint32_t(127 + top[u] - 15) << 23);
                 const int at = u * F::UNIT + gid * F::VP;
                 float v[F::VP];
 #pragma unroll
                 for (int t = 0; t < F::TILES; ++t) {
-                    constexpr float once = F::BIAS ? 0x1p10f : 0x1p-14f, next = F::BITS == 4 ? 0x1p6f : once;
-                    v[2 * t] = acc[u][t][nt][i] * once * d0;
-                    v[2 * t + 1] = acc[u][t][nt][2 + i] * next * d0;
+                    constexpr float once = F::BIAS ? 0x1p24f : 1.f, next = F::BITS == 4 ? 0x1p20f : once;
+                    v[2 * t] = acc[u][t][nt][i] * (once * scale) * unit;
+                    v[2 * t + 1] = acc[u][t][nt][2 + i] * (next * scale) * unit;
                 }
                 // in fours, or the last two
 #pragma unroll
@@ -701,12 +690,12 @@ __global__ void __launch_bounds__(32 * kAttnFormWarps<F>, 1) attn_mma_kernel(con
     attn_empty<T>(a, table);
     const int groups = a.d / a.cache.group, warp = threadIdx.x >> 5;
     AttnSmem sm;
-    sm.codes = uint32_t(warp) * attn_warp_bytes<T, F>(groups);
+    sm.codes = uint32_t(warp) * attn_warp_bytes<F>(groups);
     sm.scales = sm.codes + F::S_AT;
     sm.places = sm.scales + 2 * 32 * groups * 4;
     sm.k_scales = sm.places + kAttnPlaces;
     sm.v_scales = sm.k_scales + F::UNITS * 128;
-    sm.bias = sm.v_scales + kAttnFactors<T> * F::UNITS * 64;
+    sm.bias = sm.v_scales + F::UNITS * 128;
     attn_pieces(a, table, [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
 }
 
@@ -714,7 +703,7 @@ template <typename T, typename F>
 nrm_status attn_mma_launch(AttnArgs& a, const DevInfo* dev, cudaStream_t s) {
     const void* fn = reinterpret_cast<const void*>(&attn_mma_kernel<T, F>);
     const int groups = a.d / a.cache.group;
-    const size_t warp = attn_warp_bytes<T, F>(groups);
+    const size_t warp = attn_warp_bytes<F>(groups);
     // as many workers to an SM as have room for their rings beside the table
     const size_t room = size_t(dev->max_smem_optin) - sizeof(AttnTable) - 256;
     const int warps = int(std::min<size_t>(kAttnFormWarps<F>, room / warp));
