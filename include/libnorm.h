@@ -632,7 +632,7 @@ typedef struct nrm_kv_weights {
  * that each position received is added to what it holds,
  *   weights[s, g, j] += sum over the heads h of g of p_j,
  * and positions outside the window are left as they were.
- * scale: finite.  workspace: nrm_kv_attention_workspace_bytes(...) bytes,
+ * scale: scale*log2(e) finite.  workspace: nrm_kv_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, clobbered; calls that overlap on the GPU need separate ones.
  * Precision.  d and group multiples of 16, with rows of codes of whole aligned
  * 16-byte (or 8-byte) vectors, take matrix instructions; other layouts run

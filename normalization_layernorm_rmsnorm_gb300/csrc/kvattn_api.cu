@@ -112,7 +112,8 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
             return fail(NRM_ERR_INVALID_ARG, "q has %lld heads, no multiple of the cache's %lld", (long long)q->heads,
                         (long long)cache->heads);
         if (weights) NRM_TRY(check_weights("weights", weights, sequences, cache->heads));
-        if (!std::isfinite(scale)) return fail(NRM_ERR_INVALID_ARG, "scale must be finite");
+        a.scale_log2 = float(double(scale) * 1.4426950408889634074);
+        if (!std::isfinite(a.scale_log2)) return fail(NRM_ERR_INVALID_ARG, "scale*log2(e) must be finite");
         if (window < 0) return fail(NRM_ERR_INVALID_ARG, "window must be >= 0");
         NRM_TRY(check_stats({lse}, 4));
         if (sequences == 0) return NRM_OK;
@@ -144,7 +145,6 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
         a.shared = a.hq / a.hk;
         a.d = int(cache->d);
         a.window = window;
-        a.scale_log2 = float(double(scale) * 1.4426950408889634074);
         if (weights) {
             a.weight_ts = weights->sequence_stride;
             a.weight_hs = weights->head_stride;

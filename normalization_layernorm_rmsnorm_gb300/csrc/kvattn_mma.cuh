@@ -302,10 +302,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         }
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^e > most (an infinity or a row of tiny numbers stays what it is, nearly)
-        const int e = max(-100, min(F::BIAS ? 118 : 127, int(__float_as_uint(most) >> 23) - 126));
+        // 2^e > most (an infinity stays one); float32's smallest number times `up` is 2^-23, which fp16 holds
+        const int e = max(-111, min(128, int(__float_as_uint(most) >> 23) - 126));
         const float up = __uint_as_float(uint32_t(127 + 15 - e) << 23);
-        const float down = __uint_as_float(uint32_t(127 + e) << 23) * (F::BIAS ? 0x1p9f : 0x1p-15f) * a.scale_log2;
+        const float down = __uint_as_float(uint32_t(127 - 15 + e) << 23) * a.scale_log2;
         factor[nt][0] = __shfl_sync(0xffffffffu, down, tid * 8);
         factor[nt][1] = __shfl_sync(0xffffffffu, down, tid * 8 + 4);
 #pragma unroll
@@ -363,18 +363,26 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         cp_async_wait<1>();  // the keys and the scales
         __syncwarp();
 
-        // the scales of this lane's position, of each unit; seldom a value's is larger than all before it
+        // the scales of this lane's position, of each unit; seldom a value's is larger than all before it, or a key's so
+        // large that its product with the codes' sum, which is below 2^32, might leave float32 although the logit does not
+        constexpr float kHuge = 0x1p90f, kLess = 0x1p-64f;
+        bool huge = false;
         {
             const uint32_t mine = sm.scales + (32 + lane) * groups * 4;
-            float mine_of[F::UNITS];
+            float mine_of[F::UNITS], k_of[F::UNITS], k_by = F::BIAS ? 0x1p24f : 1.f;
             bool larger = false;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
                 mine_of[u] = in_ring<const float>(mine + of_unit[u]);
+                k_of[u] = in_ring<const float>(mine - 32 * groups * 4 + of_unit[u]);
+                huge |= fabsf(k_of[u]) >= kHuge;
                 larger |= fabsf(mine_of[u]) >= (top[u] < -126 ? -1.f : __uint_as_float(uint32_t(127 + top[u]) << 23));
             }
+            larger |= huge;
             if (__any_sync(0xffffffffu, larger)) {
+                huge = __any_sync(0xffffffffu, huge);
+                if (huge) k_by *= kLess;
 #pragma unroll
                 for (int u = 0; u < F::UNITS; ++u) {
                     if (!F::EXACT && u >= units) break;
@@ -395,7 +403,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             for (int u = 0; u < F::UNITS; ++u) {
                 if (!F::EXACT && u >= units) break;
                 in_ring<float>(sm.v_scales + (u * 32 + lane) * 4) = mine_of[u] * __uint_as_float(uint32_t(127 + 15 - top[u]) << 23);
-                in_ring<float>(sm.k_scales + (u * 32 + lane) * 4) = in_ring<const float>(mine - 32 * groups * 4 + of_unit[u]);
+                in_ring<float>(sm.k_scales + (u * 32 + lane) * 4) = k_of[u] * k_by;
             }
             __syncwarp();
         }
@@ -475,6 +483,12 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) l[half][nt][i] *= factor[nt][i & 1];
+            if (huge) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) l[half][nt][i] *= 1.f / kLess;
+            }
             if (there != 0xffffffffu) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
