@@ -37,6 +37,10 @@ __device__ __forceinline__ float warps_sum(const float* sums, int warps) {
     return v;
 }
 
+// r^3 v.  One factor at a time: the mean of a gradient times a row is about 1/r, so that no step is far from the result,
+// while r^3 alone leaves float32 where a row and eps are tiny (r above 7e12).
+__device__ __forceinline__ float cubed(float r, float v) { return r * (r * (r * v)); }
+
 // Element i of a weight (1 where there is none).
 template <typename T>
 __device__ __forceinline__ float weight_at(const void* w, int64_t i) {
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(kBlockThreads) block_bwd_scalar_kernel(const B
             float s = 0.f;
             for (int i = threadIdx.x; i < a.cols; i += kBlockThreads)
                 s = fmaf(element<T>(a.dh, at + i) * weight_at<T>(a.w_pre, i), element<T>(a.y, at + i), s);
-            c2 = r2 * r2 * r2 * (cta_sum(s, sums) / cols);
+            c2 = cubed(r2, cta_sum(s, sums) / cols);
         }
         if (a.c2 && threadIdx.x == 0) a.c2[r] = c2;
         float s = 0.f;
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kBlockThreads) block_bwd_scalar_kernel(const B
             else put<T>(a.df, at + i, dn);
         }
         if (!a.post) continue;
-        const float c1 = r1 * r1 * r1 * (cta_sum(s, sums) / cols);
+        const float c1 = cubed(r1, cta_sum(s, sums) / cols);
         for (int i = threadIdx.x; i < a.cols; i += kBlockThreads) {
             const float d = grad_y<T>(a, at + i, i, r2, c2);
             const float dn = a.alpha * (a.gates ? element<T>(a.gate, gate_at + i) : 1.f) * d;
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             if (threadIdx.x == 0 && begun && !ask.next(a, g, smem, full, empty, row_bytes, pol, ELEM)) bad = true;
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
-                const float c2 = r2[k] * r2[k] * r2[k] * (s[k] * inv);
+                const float c2 = cubed(r2[k], s[k] * inv);
                 float2 sum = f2(0.f);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
@@ -817,7 +821,7 @@ __global__ void __launch_bounds__(kBlockConsumers, 1) block_bwd_ring_kernel(cons
             if (post) group_sums<ROWS>(s, sums[1][phase], group, warps, threads);
 #pragma unroll
             for (int k = 0; k < ROWS; ++k) {
-                const float c1 = r1[k] * r1[k] * r1[k] * (s[k] * inv);
+                const float c1 = cubed(r1[k], s[k] * inv);
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     const int i = j * threads;
