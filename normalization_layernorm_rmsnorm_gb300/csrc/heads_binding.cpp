@@ -526,6 +526,7 @@ struct Rows {
             raise(PyExc_ValueError, std::string(name) + " must be [gates, " + std::to_string(cols) + "], got " +
                                         shape_text(t->sizes()));
         *gates = t->numel() / cols;
+        if (*gates == 0 && rows > 0) raise(PyExc_ValueError, std::string(name) + " has no rows");
         return dense<false>(t, name, t->numel(), type);
     }
 };
