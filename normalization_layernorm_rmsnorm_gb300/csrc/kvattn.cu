@@ -10,7 +10,6 @@ nrm_status kv_attention(const AttnArgs& args, int vec, cudaStream_t s) {
     const DevInfo* dev = dev_info();
     if (!dev) return fail(NRM_ERR_CUDA, "no usable CUDA device");
     a.err = dev->err;
-    a.min_tiles = 1;
     void* p[] = {&a};
     nrm_status st;
     if (vec) {

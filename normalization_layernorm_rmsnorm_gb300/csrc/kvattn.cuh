@@ -95,8 +95,7 @@ __device__ __forceinline__ void attn_table(const AttnArgs& a, AttnTable& t) {
 struct AttnShares {
     int used, each, more;
     __device__ __forceinline__ AttnShares(const AttnArgs& a, int total) {
-        const int w = (total + a.min_tiles - 1) / a.min_tiles;
-        used = max(1, min(w, a.workers / (a.hk * a.chunks)));
+        used = max(1, min(total, a.workers / (a.hk * a.chunks)));
         each = total / used;
         more = total - each * used;
     }

@@ -46,7 +46,6 @@ struct AttnArgs {
     float* logits;            // [sequences, pairs, logit_stride, logit_heads], base 2 (with weights)
     int64_t logit_stride;
     int workers;
-    int min_tiles;            // of a worker that is used, but for the last
     // on matrix instructions
     int row_bytes, vec;       // of a row of codes, copied in vectors of 16 or 8 bytes
     int snap;                 // pairs of at most so many tiles are not cut
