@@ -117,6 +117,8 @@ nrm_status nrm_kv_cache_attention(const nrm_heads* q, const nrm_kv_cache* cache,
         if (window < 0) return fail(NRM_ERR_INVALID_ARG, "window must be >= 0");
         NRM_TRY(check_stats({lse}, 4));
         if (sequences == 0) return NRM_OK;
+        // positions are divided by the page's size too, and a sequence may have more of them than the cache has slots
+        a.cache.page = make_row_div(cache->page_size, std::max(a.cache.slots, a.cap));
         // the tiles of a launch are counted in 32 bits
         const int64_t tiles = (a.cap / kAttnTile + 1 + kAttnStart) * attn_most_pairs(q->heads, cache->heads);
         if (a.cap / kAttnTile >= kAttnTiles || tiles >= kAttnTiles)
