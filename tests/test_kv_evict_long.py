@@ -77,3 +77,27 @@ def test_the_sort_ranks_as_the_reference():
     w = g.choice([0.0, -0.0, 1.0, 2.0, np.nan, np.inf, -np.inf, -3.0], (2, 2, 60)).astype(np.float32)
     for got, want in zip(ranked(w, [60, 31], 30, 3, 4, 60), ref.evict(w, [60, 31], 30, 3, 4, 60)):
         assert np.array_equal(got, want)
+
+
+def test_captured_and_replayed_beside_another():
+    # two clusters' calls on streams of their own, captured into one graph; other lengths and weights at each replay
+    cases = [Evict([20000, 9000], 4000, 2, 16, "int8", 16, 16, 3, 50, seed=i) for i in range(2)]
+    for e in cases:
+        e.run()  # (the kernels are loaded)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        cases[0].run()
+        cases[1].run(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for n in ([20000, 9000], [8193, 20000], [4000, 4001], [0, 16385]):
+        for e in cases:
+            e.lengths.copy_(torch.tensor(n))
+            e.weights.copy_(torch.rand_like(e.weights))
+            e.kept.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for e in cases:
+            kept, new = ranked(e.weights.cpu().numpy(), n, 4000, 3, 50, e.cap)
+            assert np.array_equal(e.kept.cpu().numpy(), kept) and e.new_lengths.tolist() == new.tolist()
