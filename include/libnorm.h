@@ -626,14 +626,18 @@ typedef struct nrm_kv_weights {
  * 0), and k_j, v_j the values that nrm_kv_cache_read would give in float32:
  *   l_j = scale * sum_i q_i*k_ji;  lse = log sum_j exp l_j;
  *   p_j = exp(l_j - lse);          out_i = sum_j p_j*v_ji
- * Without a position (n == 0), out is 0 and lse -infinity.
+ * Without a position (n == 0, or none on a page of the cache), and where every
+ * logit is -infinity, out is 0 and lse -infinity.
  * q, out: [sequences, hq, d] views in dt (not in place).  lse: float32
  * [sequences, hq], dense; may be NULL.  weights: may be NULL, else the weight
  * that each position received is added to what it holds,
  *   weights[s, g, j] += sum over the heads h of g of p_j,
  * and positions outside the window are left as they were.
- * scale: scale*log2(e) finite.  workspace: nrm_kv_attention_workspace_bytes(...) bytes,
- * 16-byte aligned, clobbered; calls that overlap on the GPU need separate ones.
+ * scale: scale*log2(e) finite.  A sequence's positions (the smaller of
+ * width*page_size and the weights' capacity) times hk*ceil(hq/hk/4): below 2^36,
+ * else NRM_ERR_UNSUPPORTED.  workspace: nrm_kv_attention_workspace_bytes(...)
+ * bytes, 16-byte aligned, clobbered; calls that overlap on the GPU need separate
+ * ones.
  * Precision.  d and group multiples of 16, with rows of codes of whole aligned
  * 16-byte (or 8-byte) vectors, take matrix instructions; other layouts run
  * element by element, in float32 throughout.  With matrix instructions sums are

@@ -37,8 +37,8 @@ __device__ __forceinline__ float warps_sum(const float* sums, int warps) {
     return v;
 }
 
-// r^3 v.  One factor at a time: the mean of a gradient times a row is about 1/r, so that no step is far from the result,
-// while r^3 alone leaves float32 where a row and eps are tiny (r above 7e12).
+// r^3 v.  One factor at a time: the mean of a gradient times a row is about 1/r, so that no step is far from the
+// result, while r^3 alone leaves float32 where a row and eps are tiny (r above 7e12).
 __device__ __forceinline__ float cubed(float r, float v) { return r * (r * (r * v)); }
 
 // Element i of a weight (1 where there is none).
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kBlockThreads) block_cols_kernel(const BlockAr
 // kept as its rounded bits for the second norm.  A CTA takes `per` neighbouring
 // rows, one at a time, so that its columns of the weights and the gate stay in
 // registers, and asks for a row DEPTH rows before it is needed.  Bound by bytes
-// (16384 rows of 4096: 84 us, 0.94 of the copy rate).
+// (16384 rows of 4096: 85 us, 0.93 of the copy rate; as many bytes in float32,
+// 16384 rows of 2048: 83).
 // FAST: both norms, and rows of whole vectors for every thread: nothing then parts the loops' instructions.
 template <typename T, int VPT, int DEPTH, int MOST, int CTAS, bool FAST>
 __global__ void __launch_bounds__(MOST, CTAS) block_fwd_vec_kernel(const BlockArgs a, int per) {
@@ -1084,7 +1085,7 @@ nrm_status block_norm_bwd(const BlockArgs& args, bool vec, bool copies, cudaStre
         // 1878: 249 without, 226 with 195, 253 with 163).
         const int room = all ? dev->max_smem_optin : (sizeof(T) == 2 ? 163 : 195) * 1024;
         // Two rows of a group at once, for their waits to overlap, where the registers allow: in 16 bits only without
-        // branches or in groups of one warp (8192 rows of 4095: 243 us with, 203 without; 17168 of 192: 33 and 45).
+        // branches or in groups of one warp (8192 rows of 4095: 243 us with, 201 without; 17168 of 192: 34 and 45).
         const bool two = vpt == 1 && !by_row && (all || sizeof(T) == 4 || nvec <= 32) && block_ring<T>(a, g, dev, 1, 2, elem, room);
         ringed = two || block_ring<T>(a, g, dev, vpt, 1, elem, room);
         const void* fn;

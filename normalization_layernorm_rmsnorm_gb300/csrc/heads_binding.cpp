@@ -1,7 +1,8 @@
 // heads_binding.cpp -- argument marshalling of the operators on attention heads, on
-// the cached sequences and between the blocks of a residual stream, compiled: these calls take up to fifteen tensors with strides, and a served
-// model makes them for single tokens, where reading the tensors' shapes from
-// Python takes several times as long as the kernels.  Each function checks its
+// the cached sequences and between the blocks of a residual stream, compiled: these
+// calls take up to fifteen tensors with strides, and a served model makes them for
+// single tokens, where reading the tensors' shapes from Python takes several times
+// as long as the kernels.  Each function checks its
 // tensors (types, shapes, the current device), then calls the C entry point of
 // the same name on the current torch stream or the one given.  A status that is
 // not NRM_OK raises NrmError.

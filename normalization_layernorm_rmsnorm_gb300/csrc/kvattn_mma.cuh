@@ -149,7 +149,7 @@ struct AttnSmem {
 };
 constexpr uint32_t kAttnPlaces = 32 * 8;
 // Warps of a CTA, by the registers that a thread needs.  (12: 131072 positions in 4 bits take 58 us; 10: 64; 14, with
-// 144 registers: 64; 16, with 128: 66.)
+// 144 registers: 66; 16, with 128: 64.)
 template <typename F>
 constexpr int kAttnFormWarps = F::DMAX > 128 || F::NT > 1 ? 8 : kAttnWarps;
 template <typename T>
@@ -363,8 +363,9 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         cp_async_wait<1>();  // the keys and the scales
         __syncwarp();
 
-        // the scales of this lane's position, of each unit; seldom a value's is larger than all before it, or a key's so
-        // large that its product with the codes' sum, which is below 2^32, might leave float32 although the logit does not
+        // the scales of this lane's position, of each unit; seldom a value's is larger than all before it, or a key's
+        // so large that its product with the codes' sum, which is below 2^32, might leave float32 although the logit
+        // does not
         constexpr float kHuge = 0x1p90f, kLess = 0x1p-64f;
         bool huge = false;
         {

@@ -12,8 +12,9 @@
 // Bound by latency: three exchanges of the cluster, and a CTA's rounds over its part
 // (131072 positions to 65536, 8 heads: 22 us; 4096 to 1024: 7).
 //
-// Copying: bound by bytes (65536 rows of 8 heads of 128 bytes: 47 us, 0.87 of the copy rate).  The heads of a slot of the shortened sequence follow
-// one another, so that what is written lies together, and what is read nearly so.
+// Copying: bound by bytes (65536 rows of 8 heads of 128 bytes: 47 us, 0.87 of the
+// copy rate).  The heads of a slot of the shortened sequence follow one another, so
+// that what is written lies together, and what is read nearly so.
 #include "heads.cuh"
 #include "kvattn.h"
 
