@@ -650,10 +650,6 @@ typedef struct nrm_kv_weights {
  *    p_j times the largest scale of that group of elements in the sequence may be
  *    lost.  (The bound is the product's: small p_j alone, or small scales, keep
  *    their bits.)
- * Integers' codes are added with a bias of 128 (8 in 4 bits), which is taken off
- * again, so roundings go by the codes plus that; and terms are cut off at 2^-15
- * of a code's step times the largest query's element, or the largest p_j times
- * scale, that they are added with.
  */
 NRM_API nrm_status nrm_kv_cache_attention(const nrm_heads *q, const nrm_kv_cache *cache,
                                   const nrm_kv_pages *pages, const nrm_heads *out, float scale,

@@ -13,9 +13,9 @@ namespace nrm {
 constexpr int kAttnSequences = 1024;
 constexpr int kAttnTile = 32;        // positions of a tile: one to a lane
 // What a sequence costs a worker beside its tiles, in tiles: its queries, the first copies' wait, its result.  (0, 2, 5
-// and 7 tiles: 64 sequences of 1 to 2048 positions with weights 55.1, 52.4, 50.5, 48.5 us; 250 of up to 120 18.2, 15.8,
-// 15.3, 15.6; 16 of up to 16384 on one head of 256 40.0, 37.7, 37.7, 37.7; 9 in a window of 777 20.6, 18.9, 19.1, 19.0;
-// one of 131072, which has no beginning to even out, 56.7 and then 57.9.)
+// and 7 tiles: 64 sequences of 1 to 2048 positions with weights 55.3, 52.3, 50.5, 48.4 us; 250 of up to 120 17.2, 14.8,
+// 14.4, 14.7; 16 of up to 16384 on one head of 256 40.8, 39.4, 39.4, 39.4; 9 in a window of 777 20.5, 19.0, 19.1, 19.1;
+// one of 131072 in 4 bits 61.2, 60.6, 60.5, 60.5.)
 constexpr int kAttnStart = 5;
 constexpr int kAttnWarps = 12;       // warps of a CTA at most, each a worker of its own
 constexpr int kAttnHeads = 16;       // query heads that a worker takes, at most
@@ -70,8 +70,8 @@ inline int attn_most_tiles(const AttnArgs& a) {
     return int((seen + kAttnTile - 1) / kAttnTile);
 }
 // Where there are pairs for a quarter of the workers, short ones are left whole: a worker then takes up to 8 tiles where
-// it would have taken 1, but nothing has to be joined.  (250 sequences of up to 120 positions, 4 heads of keys: 15.3 us,
-// cut 20.4; 64 of 1 to 2048, 8 heads, of which an eighth are so short: 50.5, cut 47.7.)  Otherwise those of one tile,
+// it would have taken 1, but nothing has to be joined.  (250 sequences of up to 120 positions, 4 heads of keys: 14.4 us,
+// cut 19.4; 64 of 1 to 2048, 8 heads, of which an eighth are so short: 50.5, cut 47.8.)  Otherwise those of one tile,
 // which cannot be cut.
 inline void attn_snap(AttnArgs& a) {
     a.snap = 4 * int64_t(a.sequences) * a.hk * a.chunks >= a.workers ? 8 : 1;

@@ -3,19 +3,17 @@
 // Both products are m16n8k16 with fp16 factors and fp32 sums, the query heads of
 // a pair as the eight columns: logits = codes of 16 keys [16 x d] * queries [d x
 // 8], and out^T = codes of 16 values [d x 16] * weights [16 x 8].  A code is
-// exact in fp16 in every stored form (an integer is taken with a bias, which one
-// more product takes off again, as one of fp16's smallest numbers, so that it costs
-// no conversion); the keys' scales multiply the logits, the values' the weights.
-// Queries are scaled by a power of two to at most 2^15: those of 16 bits then are
-// exact, of float32 ones the rest is a second factor (22 bits).
+// exact in fp16 in every stored form; the keys' scales multiply the logits, the
+// values' the weights.  Queries are scaled by a power of two to at most 2^15: those
+// of 16 bits then are exact, of float32 ones the rest is a second factor (22 bits).
 //
-// An instruction lines its terms up by their factors' exponents and cuts them off
-// at 2^-25 of the largest (measured, term by term); fp16's smallest numbers go by
-// the exponent of 2^-14 that they are stored with.  A term with an integer's code
-// so ends at 2^-15 of a code's step times the other factor: for 8 bits 2^-22 of the
-// largest code, for the lower of two 4-bit codes 2^-18, for the upper, which is
-// taken 16 times as large, 2^-22.  (Shifting the lower up too would cost two
-// instructions for eight codes; the values themselves were rounded to half a step.)
+// (An integer could be taken as it lies, as one of fp16's smallest numbers, with a
+// bias that one more product takes off again, which saves its conversion: 131072
+// positions in 4 bits 58 us instead of 60.  But an instruction lines its terms up
+// by the exponents that their factors are stored with and cuts them off at 2^-25 of
+// the largest, and the smallest numbers are stored with 2^-14: terms then end at
+// 2^-15 of a code's step times the largest weight, so that where the position that
+// draws the weight has a code of 0, what the others give is off.)
 //
 // A weight is p times its value's scale, multiplied in float32 with the largest
 // scale seen brought below 2^15 and rounded to fp16: 11 bits down to 2^-28 of the
@@ -99,7 +97,15 @@ __device__ __forceinline__ uint32_t e4m3x2_halves(uint32_t v) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(v)));
     return h;
 }
-// Four 8-bit codes: bytes (0, 1) and (2, 3).  Integers: the byte plus 128, as fp16's smallest numbers (2^-24 of it).
+// Integers as fp16: behind the upper byte of 1024 a code (plus 2^7 or 2^3, so that it is not negative) adds its own
+// value, and a subtraction takes off what was added.
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+constexpr uint32_t kHalf1024 = 0x64006400u, kHalf1032 = 0x64086408u, kHalf1152 = 0x64806480u;  // twice each
+// Four 8-bit codes: bytes (0, 1) and (2, 3).
 template <int KIND>
 __device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
     if constexpr (KIND == NRM_CACHE_E4M3) {
@@ -107,13 +113,13 @@ __device__ __forceinline__ void codes8(uint32_t v, uint32_t& lo, uint32_t& hi) {
         hi = e4m3x2_halves(v >> 16);
     } else {
         v ^= 0x80808080u;
-        lo = __byte_perm(v, 0, 0x4140);
-        hi = __byte_perm(v, 0, 0x4342);
+        lo = sub_half2(__byte_perm(v, kHalf1024, 0x7170), kHalf1152);
+        hi = sub_half2(__byte_perm(v, kHalf1024, 0x7372), kHalf1152);
     }
 }
-// The 4-bit codes (plus 8) at the low ends of both halves, 2^-24 of them, and those above, 2^-20 of them.
-__device__ __forceinline__ uint32_t codes4(uint32_t v) { return v & 0x000f000fu; }
-__device__ __forceinline__ uint32_t codes4_next(uint32_t v) { return v & 0x00f000f0u; }
+// The 4-bit codes (plus 8) at the low ends of both halves, and those above, 16 times as large.
+__device__ __forceinline__ uint32_t codes4(uint32_t v) { return sub_half2((v & 0x000f000fu) | kHalf1024, kHalf1032); }
+__device__ __forceinline__ uint32_t codes4_next(uint32_t v) { return sub_half2((v & 0x00f000f0u) | kHalf1024, kHalf1152); }
 
 // What a kernel is made for: the stored form, rows of UNITS units of 128, 64, 32 or 16 elements (every group is whole
 // units; EXACT: of no fewer), and eights of heads.  With the count known the products of a tile are one block of
@@ -133,8 +139,6 @@ struct AttnForm {
     static constexpr int K_UNIT = BITS == 8 && SUB == 32 ? 32 : 16;
     static constexpr int K_PITCH = ((ROW + K_UNIT - 1) / K_UNIT | 1) * K_UNIT, V_PITCH = ((ROW + 15) / 16 | 1) * 16;
     static constexpr uint32_t V_AT = 32 * K_PITCH, S_AT = V_AT + 32 * V_PITCH;
-    // the integers' codes are taken as they lie, plus BIAS, as fp16's smallest numbers: 2^-24 of the value
-    static constexpr int BIAS = KIND == NRM_CACHE_INT4 ? 8 : KIND == NRM_CACHE_INT8 ? 128 : 0;
 };
 
 // A warp's shared memory: a tile's keys, values and scales of both, the places of a tile's rows, and its scales of each
@@ -145,18 +149,17 @@ struct AttnSmem {
     uint32_t places;           // [32] code offsets
     uint32_t k_scales;         // [units][32]
     uint32_t v_scales;         // [units][32], the largest brought below 2^15
-    uint32_t bias;             // [units][heads]: what the codes' bias adds to a unit's products, negative
 };
 constexpr uint32_t kAttnPlaces = 32 * 8;
-// Warps of a CTA, by the registers that a thread needs.  (12: 131072 positions in 4 bits take 58 us; 10: 64; 14, with
-// 144 registers: 66; 16, with 128: 64.)
+// Warps of a CTA, by the registers that a thread needs.  (12: 131072 positions in 4 bits take 60 us; 10: 68; 14, with
+// 144 registers: 70; 16, with 128: 66.)
 template <typename F>
 constexpr int kAttnFormWarps = F::DMAX > 128 || F::NT > 1 ? 8 : kAttnWarps;
 template <typename T>
 constexpr int kAttnFactors = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;  // of a weight
 template <typename F>
 __host__ __device__ constexpr uint32_t attn_warp_bytes(int groups) {
-    return F::S_AT + 2 * 32 * groups * 4 + kAttnPlaces + 2 * F::UNITS * 128 + (F::BIAS ? F::UNITS * F::NT * 32 : 0);
+    return F::S_AT + 2 * 32 * groups * 4 + kAttnPlaces + 2 * F::UNITS * 128;
 }
 
 template <typename T, typename F>
@@ -271,7 +274,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
     for (int nt = 0; nt < NT; ++nt) {
         const int h = nt * 8 + gid;
         const bits* row = static_cast<const bits*>(a.q.p) + p.s * a.q.ts + (p.q0 + h) * a.q.hs;
-        float x[F::DMAX / F::SUB][F::KP], off[F::UNITS], most = 0.f;
+        float x[F::DMAX / F::SUB][F::KP], most = 0.f;
 #pragma unroll
         for (int u = 0; u < F::DMAX / F::SUB; ++u) {
             const int at = u * F::SUB + tid * F::KP;
@@ -320,25 +323,10 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 const float by = F::BITS == 4 && b == 1 ? up * 0x1p-4f : up;
                 const float lo = x[u][i0] * by, hi = x[u][i1] * by;
                 q[ks][nt][0][b] = half2_bits(lo, hi);
-                float2 r = half2_floats(q[ks][nt][0][b]);
                 if constexpr (QT == 2) {
+                    const float2 r = half2_floats(q[ks][nt][0][b]);
                     q[ks][nt][QT - 1][b] = half2_bits(lo - r.x, hi - r.y);
-                    const float2 r2 = half2_floats(q[ks][nt][QT - 1][b]);
-                    r.x += r2.x, r.y += r2.y;
                 }
-                if constexpr (F::BIAS != 0) {
-                    constexpr float of = -F::BIAS * 0x1p-24f;
-                    if (b == 0 && ks % (F::UNIT / 16) == 0) off[ks / (F::UNIT / 16)] = 0.f;
-                    off[ks / (F::UNIT / 16)] = fmaf(F::BITS == 4 && b == 1 ? 16.f * of : of, r.x + r.y, off[ks / (F::UNIT / 16)]);
-                }
-            }
-        }
-        if constexpr (F::BIAS != 0) {
-#pragma unroll
-            for (int u = 0; u < F::UNITS; ++u) {
-                off[u] += __shfl_xor_sync(0xffffffffu, off[u], 1);
-                off[u] += __shfl_xor_sync(0xffffffffu, off[u], 2);
-                if (tid == 0) in_ring<float>(sm.bias + ((u * NT + nt) * 8 + gid) * 4) = off[u];
             }
         }
     }
@@ -370,7 +358,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
         bool huge = false;
         {
             const uint32_t mine = sm.scales + (32 + lane) * groups * 4;
-            float mine_of[F::UNITS], k_of[F::UNITS], k_by = F::BIAS ? 0x1p24f : 1.f;
+            float mine_of[F::UNITS], k_of[F::UNITS], k_by = 1.f;
             bool larger = false;
 #pragma unroll
             for (int u = 0; u < F::UNITS; ++u) {
@@ -383,7 +371,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             larger |= huge;
             if (__any_sync(0xffffffffu, larger)) {
                 huge = __any_sync(0xffffffffu, huge);
-                if (huge) k_by *= kLess;
+                if (huge) k_by = kLess;
 #pragma unroll
                 for (int u = 0; u < F::UNITS; ++u) {
                     if (!F::EXACT && u >= units) break;
@@ -418,14 +406,7 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
             for (int half = 0; half < 2; ++half) {
                 float c[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-                    if constexpr (F::BIAS != 0) {
-                        const float2 less = in_ring<const float2>(sm.bias + ((u * NT + nt) * 8 + tid * 2) * 4);
-                        c[nt][0] = c[nt][2] = less.x;
-                        c[nt][1] = c[nt][3] = less.y;
-                    }
-                }
+                for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
 #pragma unroll
                 for (int sub = 0; sub < F::SUBS; ++sub) {
                     uint32_t f[F::STEPS][4];
@@ -616,12 +597,6 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                             float second[4] = {};
                             float(&to)[4] = k == 0 ? acc[u][t][nt] : second;
                             mma16816(to, f[t], b[nt][k][0], b[nt][k][1]);
-                            if constexpr (F::BIAS != 0) {
-                                // less the bias (0x8008: -8 * 2^-24)
-                                constexpr uint32_t once = F::BITS == 4 ? 0x80088008u : 0x80808080u, next = 0x80808080u;
-                                const uint32_t less[4] = {once, next, once, next};
-                                mma16816(to, less, b[nt][k][0], b[nt][k][1]);
-                            }
                             if (k == 1) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) acc[u][t][nt][i] = fmaf(second[i], 0x1p-11f, acc[u][t][nt][i]);
@@ -659,9 +634,8 @@ __device__ __forceinline__ void attn_mma_piece(const AttnArgs& a, const AttnPiec
                 float v[F::VP];
 #pragma unroll
                 for (int t = 0; t < F::TILES; ++t) {
-                    constexpr float once = F::BIAS ? 0x1p24f : 1.f, next = F::BITS == 4 ? 0x1p20f : once;
-                    v[2 * t] = acc[u][t][nt][i] * (once * scale) * unit;
-                    v[2 * t + 1] = acc[u][t][nt][2 + i] * (next * scale) * unit;
+                    v[2 * t] = acc[u][t][nt][i] * scale * unit;
+                    v[2 * t + 1] = acc[u][t][nt][2 + i] * (F::BITS == 4 ? scale * 0x1p-4f : scale) * unit;
                 }
                 // in fours, or the last two
 #pragma unroll
@@ -710,7 +684,6 @@ __global__ void __launch_bounds__(32 * kAttnFormWarps<F>, 1) attn_mma_kernel(con
     sm.places = sm.scales + 2 * 32 * groups * 4;
     sm.k_scales = sm.places + kAttnPlaces;
     sm.v_scales = sm.k_scales + F::UNITS * 128;
-    sm.bias = sm.v_scales + F::UNITS * 128;
     attn_pieces(a, table, [&](const AttnPiece& p) { attn_mma_piece<T, F>(a, p, sm, groups); });
 }
 

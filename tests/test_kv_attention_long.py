@@ -4,21 +4,14 @@ little in each tile adds up, against the double-precision reference (oracle/serv
 Tolerances, derived before the first run.  u = 2^-24 is half a step of float32.
   * A logit l_j: float32 sums of d products in any order, 2u each, of factors with 22 bits for
     float32 queries (2^-21); scale, key's scale, and base 2 and back: 16 u (|l_j| + |lse|).
-    D_j = (2 (d + 16) u + 2^-21) S_j + 16 u (|l_j| + |lse|), S_j = scale sum |q| s (|code| + 2 b): the
-    products of integers' codes carry a bias b of 128 (8 in 4 bits) that is taken off again.  Where
-    queries are +-c, c of few bits, and the codes whole numbers, all sums are exact: the first part
-    is 0.
+    D_j = (2 (d + 16) u + 2^-21) S_j + 16 u (|l_j| + |lse|), S_j = scale sum |q k_j|.  Where queries are
+    +-c, c of few bits, and the codes whole numbers, all sums are exact: the first part is 0.
   * p_j = 2^(l_j - m): 2 D_j, the function's 2^-21 and the sum's (2 N + 64) u, N the tiles of a piece
     (a tile's positions are added in a few levels, the tiles in turn), for p_j and for the sum.
   * A weight: p_j times its value's scale, rounded to 22 bits (2^-22; bfloat16 11, 2^-11), of which
     what is below 2^-50 (bfloat16 2^-39) of the largest p_j times the largest scale may be lost.
-  * out: a tile's products reach a sum in up to 4 additions (8 with a bias: two halves, two factors), each
-    cut off at 4 u of what it holds: (16 N + 64) u, or (32 N + 64) u, of sum p s (|code| + 2 b).  Integers'
-    codes are fp16's smallest numbers, 2^-24 of the code, which an instruction lines up by the exponent of
-    2^-14 that they are stored with: it cuts its 17 terms off at 2^-25 of 2^-14 w, w the largest weight there,
-    which is 2^-15 of a code's step times w.  8 instructions a tile, and the tiles' largest weights are at
-    most their sum: 8 * 17 * 2^-15 sum p s (and for a logit 2 d/16 * 17 * 2^-15 scale max|q| s, unless its
-    terms are whole multiples of that).  Then half a step of the type.
+  * out: a tile's products reach a sum in up to 4 additions (two halves, two factors), each cut off at
+    4 u of what it holds: (16 N + 64) u of sum p |v|.  Then half a step of the type.
 """
 import numpy as np
 import pytest
@@ -29,7 +22,6 @@ from oracle import served as ref
 from test_heads import DT, TINY, U, f64, half_step
 
 pytestmark = pytest.mark.gpu
-BIAS = {"e4m3": 0, "int8": 128, "int4": 8}
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -49,15 +41,13 @@ def check_rows(dtype, kind, q, k, v, scale, out, lse, tiles, exact=()):
     """One sequence's heads on one head of the keys.  q, out [heads, d], lse [heads]; k, v: (codes, scales) of the
     positions; `exact`: positions whose logits' sums are exact."""
     (kc, ks), (vc, vs) = parts(*k, kind), parts(*v, kind)
-    b, d = BIAS[kind], q.shape[1]
+    d = q.shape[1]
     for h in range(q.shape[0]):
         l = scale * (kc * ks) @ q[h]
         want_lse = l.max() + np.log(np.exp(l - l.max()).sum())
         p = np.exp(l - want_lse)
-        S = scale * (np.abs(ks) * (np.abs(kc) + 2 * b)) @ np.abs(q[h])
+        S = scale * np.abs(kc * ks) @ np.abs(q[h])
         D = (2 * (d + 16) * U + 2.0 ** -21) * S
-        if b:
-            D = D + 2 * d / 16 * 17 * 2.0 ** -15 * scale * np.abs(q[h]).max() * np.abs(ks).max(-1)
         D[list(exact)] = 0
         D = D + 16 * U * (np.abs(l) + abs(want_lse))
         add = (2 * tiles + 64) * U
@@ -67,9 +57,7 @@ def check_rows(dtype, kind, q, k, v, scale, out, lse, tiles, exact=()):
         want = p @ (vc * vs)
         lim = (p * (rel + (2.0 ** -11 if bf16 else 2.0 ** -22))) @ np.abs(vc * vs)
         lim = lim + 2.0 ** (-39 if bf16 else -50) * p.max() * np.abs(vs).max(0) * np.abs(vc).sum(0)
-        lim = lim + ((32 if b else 16) * tiles + 64) * U * (p @ (np.abs(vs) * (np.abs(vc) + 2 * b)))
-        if b:
-            lim = lim + 8 * 17 * 2.0 ** -15 * (p @ np.abs(vs))
+        lim = lim + (16 * tiles + 64) * U * (p @ np.abs(vc * vs))
         lim = lim + half_step(dtype) * (np.abs(want) + lim) + TINY[dtype]
         off = np.abs(out[h] - want)
         assert (off <= lim).all(), (h, off.max(), np.abs(want).max(), (off / lim).max())
