@@ -15,7 +15,8 @@ from ._binding import (  # noqa: F401
     NRM_ERR_CUDA, NRM_ERR_INVALID_ARG, NRM_ERR_TIMEOUT, NRM_ERR_UNSUPPORTED, NRM_ERR_WORKSPACE, NRM_F16,
     NRM_F32, NRM_OK, NRM_OP_LAYERNORM_BWD, NRM_OP_LAYERNORM_CF_BWD, NRM_OP_QK_NORM_BWD, NRM_OP_RMSNORM_BWD,
     NRM_PAIRS_ADJACENT, NRM_PAIRS_HALF, NrmError, batchnorm_workspace, block_norm_workspace,
-    kv_attention_workspace, kv_cache, load, nrm_act_dropout_bwd, nrm_act_dropout_fwd, nrm_act_mask_words, nrm_batchnorm_bwd, nrm_batchnorm_fwd,
+    kv_attention_workspace, kv_cache, load, nrm_act_dropout_bwd, nrm_act_dropout_fwd, nrm_act_mask_words,
+    nrm_batchnorm_bwd, nrm_batchnorm_fwd,
     nrm_batchnorm_workspace_bytes, nrm_block_norm_bwd, nrm_block_norm_fwd,
     nrm_kv_cache_attention, nrm_kv_cache_evict, nrm_kv_cache_read, nrm_kv_cache_write, nrm_last_error_message,
     nrm_layernorm_bwd, nrm_layernorm_bwd_ex, nrm_layernorm_bwd_noalloc, nrm_layernorm_cf_bwd,
